@@ -53,8 +53,9 @@ typedef enum {
     KDA_ERR_DEVICE = 5,      /* the device flagged bad input (e.g. cu_seqlens) */
     KDA_ERR_TOO_LARGE = 6,   /* kda_prefill_noalloc: the sizes need more scratch than its
                                 static array holds */
-    KDA_ERR_RANGE = 7        /* a bf16 prefill state came out non-finite (inputs outside the
+    KDA_ERR_RANGE = 7,       /* a bf16 prefill state came out non-finite (inputs outside the
                                 range that kda_prefill states) */
+    KDA_ERR_NO_SPACE = 8     /* a cache call needed more pages than were free */
 } kda_status;
 
 typedef enum { KDA_BF16 = 0, KDA_F32 = 1 } kda_dtype;
@@ -334,9 +335,11 @@ int kda_layer_prologue_decode(const void *q_raw, const void *k_raw, const void *
 
 /*
  * Synchronises `stream`, then reads and clears the device status word of a
- * kda_prefill workspace. Returns KDA_OK, KDA_ERR_TIMEOUT, KDA_ERR_DEVICE
- * (malformed cu_seqlens were seen), KDA_ERR_RANGE (a final state of the bf16
- * path was not finite) or KDA_ERR_CUDA, the first that applies in this order.
+ * kda_prefill, kda_attn_* or kda_cache_* workspace. Returns KDA_OK,
+ * KDA_ERR_TIMEOUT, KDA_ERR_DEVICE (malformed cu_seqlens, lengths, rows or page
+ * numbers were seen), KDA_ERR_RANGE (a final state of the bf16 path was not
+ * finite), KDA_ERR_NO_SPACE or KDA_ERR_CUDA, the first that applies in this
+ * order.
  */
 int kda_workspace_status(void *workspace, void *stream);
 
@@ -388,6 +391,153 @@ int kda_prefill_noalloc(const void *q, const void *k, const void *v, const float
  * device before any stream capture.
  */
 int kda_noalloc_status(void *stream);
+
+/*
+ * Softmax attention, for the full-attention layers that stand between a model's
+ * KDA layers ("K3 vs DSV4 architecture divergence", KDA section: the layers
+ * alternate). Hq query heads share Hkv key/value heads, G = Hq / Hkv <= 64 each:
+ *
+ *     o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j),
+ *     lse_i = ln sum_j p_ij,
+ *
+ * over the keys j that row i sees; a row that sees none has o = 0 and
+ * lse = -inf. Logits, maxima and sums are fp32 (with bf16 I/O p is rounded to
+ * bf16 for the product with v, out to bf16 at the end). A sequence's keys only
+ * ever touch its own rows: whatever lies past a sequence's end (another
+ * sequence, the rest of a page, NaN) is not used. Inside a sequence a NaN in v
+ * reaches every row of the same key tile, as 0 * NaN does.
+ * scale: finite and > 0. D = 128.
+ *
+ * Workspace: device buffer, 256-byte aligned, of the size that the query gives
+ * (it holds the status word and the parts of rows that several SMs share). Its
+ * first 256 bytes must be zero before its first use; calls do not clear the
+ * status word, kda_workspace_status() reads and clears it. It must not be shared
+ * by calls in flight at the same time.
+ *
+ * kda_attn_prefill: causal attention over N packed sequences.
+ *   q    : io dtype [Tq_total, Hq, D], ldq elements from one token to the next
+ *   k, v : io dtype [Tk_total, Hkv, D], ldk and ldv likewise (so that q, k and v
+ *          may be views of one projection's rows)
+ *   out  : io dtype [Tq_total, Hq, D], contiguous   lse : fp32 [Tq_total, Hq] or NULL
+ *   cu_seqlens_q, cu_seqlens_k : DEVICE int32 [N + 1] offsets, each from 0, non-decreasing, to
+ *          at most the total (then Tq and Tk are the totals). cu_seqlens_k NULL with
+ *          cu_seqlens_q given: the keys have the same offsets (Tk = Tq). Both NULL:
+ *          equal lengths Tq and Tk (the totals are N Tq and N Tk).
+ *   Token i of a sequence with Lq tokens and Lk keys sees the keys j <= i + Lk - Lq:
+ *   Lk = Lq is a prompt, Lk > Lq tokens appended to a prefix whose keys come
+ *   first; with Lk < Lq the first Lq - Lk tokens see nothing.
+ *   Malformed offsets are flagged on the device (KDA_ERR_DEVICE from
+ *   kda_workspace_status) and the whole call is skipped.
+ * Pointers 16-byte aligned; ldq >= Hq D, ldk, ldv >= Hkv D, each a multiple of 16 bytes.
+ * Returns KDA_ERR_UNSUPPORTED for D != 128, G > 64 or an unknown io; N = 0 or no
+ * token is a no-op.
+ */
+size_t kda_attn_prefill_workspace_size(int32_t N, int32_t Tq_total, int32_t Tk_total, int32_t Hq,
+                                       int32_t Hkv, int32_t D, int32_t io);
+int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk,
+                     int64_t ldv, float scale, const int32_t *cu_seqlens_q,
+                     const int32_t *cu_seqlens_k, int32_t N, int32_t Tq, int32_t Tk, int32_t Hq,
+                     int32_t Hkv, int32_t D, int32_t io, void *out, float *lse, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * kda_attn_decode: attention of T new tokens (1..64) of each of B sequences over
+ * a paged cache and over one another: T = 1 is the plain decode step, T > 1 the
+ * drafted tokens of speculative decoding, as a chain or a tree.
+ *   q : io dtype [B, T, Hq, D], ldq elements from one token to the next (a
+ *       sequence's tokens are T ldq apart)
+ *   k_pages, v_pages : io dtype [num_pages, Hkv, page_size, D]; page_size 16, 32, 64,
+ *       128 or 256
+ *   block_table : DEVICE int32 [B, table_cols], row b's pages in order, table_ld
+ *       entries from one row to the next
+ *   seq_lens : DEVICE int32 [B], tokens of each sequence in the cache (0 is fine)
+ *   k_new, v_new : io dtype [B, T, Hkv, D] (ldk, ldv), the new tokens' own keys and
+ *       values, not (yet) in the cache; both NULL: the tokens see the cache alone
+ *   tree_mask : DEVICE uint64 [B, T] or NULL. Bit s of [b][t]: new token t sees new
+ *       token s (its ancestors in the tree and itself). NULL: the chain, s <= t.
+ *   out : io dtype [B, T, Hq, D], contiguous   lse : fp32 [B, T, Hq] or NULL
+ * Every token sees all seq_lens[b] cached ones. A length outside
+ * 0..table_cols page_size is flagged (KDA_ERR_DEVICE) and its sequence skipped
+ * (nothing written); a page number outside the pool is flagged and its keys read
+ * as zeros. kda_cache_append adds the accepted tokens to the cache.
+ * Workspace, alignment and errors as kda_attn_prefill; T > 64 or another page size
+ * is KDA_ERR_UNSUPPORTED. B = 0 or T = 0 is a no-op.
+ */
+size_t kda_attn_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                      int32_t page_size, int32_t table_cols, int32_t io);
+int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk,
+                    int64_t ldv, const void *k_pages, const void *v_pages, int32_t num_pages,
+                    int32_t page_size, const int32_t *block_table, int64_t table_ld,
+                    int32_t table_cols, const int32_t *seq_lens, const uint64_t *tree_mask,
+                    float scale, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                    int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
+ * The pages of a cache. block_table int32 [rows, table_cols] (table_ld entries
+ * from one row to the next): a row's pages in order, then -1; seq_lens int32
+ * [rows]; refs int32 [num_pages] (16-byte aligned): the table entries on each page,
+ * 0 = free. All three are DEVICE arrays that these calls update, for any number of
+ * layers' pools at once. Pages are chosen lowest number first, so results depend
+ * on the inputs alone. `workspace` (256-byte aligned, kda_cache_workspace_size
+ * bytes, its first 256 bytes zero before its first use) also takes the status:
+ * malformed rows, lengths or page numbers are skipped and flagged
+ * (KDA_ERR_DEVICE); a call that needs more pages than are free changes nothing
+ * and is flagged (KDA_ERR_NO_SPACE).
+ *
+ * kda_cache_alloc: gives every row the pages it lacks for want[row] tokens (DEVICE
+ *   int32 [rows]; a row never loses pages). seq_lens is not touched.
+ * kda_cache_fork: for i < n, row dst[i] (which must be empty, else it is flagged and
+ *   skipped) becomes a copy of row src[i]: full pages are shared (refs + 1); where
+ *   the length ends inside a page, dst gets a fresh page, and copies[i] = (shared
+ *   page, fresh page) has to be copied in every pool (kda_cache_copy); copies[i] =
+ *   (-1, -1) otherwise. src or dst < 0 skips the pair. No dst may be another
+ *   pair's src or dst.
+ * kda_cache_free: drops the pages of rows[i], i < n (distinct; < 0 is skipped): refs - 1,
+ *   entries -1, length 0.
+ * kda_cache_compact: with L live pages, the j-th live page numbered >= L moves to
+ *   the j-th free page below L; table entries are renamed, refs moved; copies
+ *   int32 [num_pages, 2] gets the (from, to) pairs, then (-1, -1); *count (DEVICE) their
+ *   number. Afterwards the live pages are 0 .. L - 1.
+ * kda_cache_copy: entry `to` = entry `from` for every pair, in each of n_pools pools
+ *   (HOST array of DEVICE pointers, 16-byte aligned) of num_entries entries of
+ *   entry_bytes (a multiple of 16). pairs: DEVICE int32 [n, 2]; those with a number
+ *   outside the pool are skipped; count: DEVICE, only the first *count pairs (NULL:
+ *   all n). No `to` may be another pair's `from` or `to`. Also copies entries of
+ *   a KDA state pool or convolution-state pool, which a forked sequence needs of
+ *   its own.
+ * kda_cache_append: writes rows k, v (io dtype, [.., Hkv, D], ldk / ldv elements from
+ *   one token to the next) to positions start[b], start[b] + 1, ... (DEVICE int32 [N])
+ *   of sequences b = 0 .. N - 1 (table rows), whose pages must be there:
+ *     cu_seqlens given (DEVICE int32 [N + 1]): packed rows, T = their total;
+ *     else [N, T] rows, of sequence b the first count[b] (DEVICE int32 [N], NULL: T)
+ *     in the order of index (DEVICE int32 [N, T], NULL: 0, 1, ..): the accepted
+ *     tokens of a draft.
+ *   Rows without a valid page are skipped and flagged (workspace may be NULL: then
+ *   not flagged). Positions must be distinct.
+ */
+size_t kda_cache_workspace_size(int32_t num_pages, int32_t rows);
+int kda_cache_alloc(int32_t *block_table, int64_t table_ld, int32_t rows, int32_t table_cols,
+                    const int32_t *want, int32_t *refs, int32_t num_pages, int32_t page_size,
+                    void *workspace, size_t workspace_bytes, void *stream);
+int kda_cache_fork(int32_t *block_table, int64_t table_ld, int32_t rows, int32_t table_cols,
+                   int32_t *seq_lens, int32_t *refs, int32_t num_pages, int32_t page_size,
+                   const int32_t *src, const int32_t *dst, int32_t n, int32_t *copies,
+                   void *workspace, size_t workspace_bytes, void *stream);
+int kda_cache_free(int32_t *block_table, int64_t table_ld, int32_t rows, int32_t table_cols,
+                   int32_t *seq_lens, int32_t *refs, int32_t num_pages, const int32_t *which,
+                   int32_t n, void *workspace, size_t workspace_bytes, void *stream);
+int kda_cache_compact(int32_t *block_table, int64_t table_ld, int32_t rows, int32_t table_cols,
+                      int32_t *refs, int32_t num_pages, int32_t *copies, int32_t *count,
+                      void *workspace, size_t workspace_bytes, void *stream);
+int kda_cache_copy(void *const *pools, int32_t n_pools, int64_t entry_bytes, int32_t num_entries,
+                   const int32_t *pairs, int32_t n, const int32_t *count, void *stream);
+int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv,
+                     const int32_t *cu_seqlens, int32_t N, int32_t T, const int32_t *index,
+                     const int32_t *count, const int32_t *start, const int32_t *block_table,
+                     int64_t table_ld, int32_t table_cols, int32_t num_pages, int32_t page_size,
+                     int32_t Hkv, int32_t D, int32_t io, void *k_pages, void *v_pages,
+                     void *workspace, void *stream);
 
 #ifdef __cplusplus
 }

@@ -25,6 +25,7 @@ KDA_ERR_TIMEOUT = 4
 KDA_ERR_DEVICE = 5
 KDA_ERR_TOO_LARGE = 6
 KDA_ERR_RANGE = 7
+KDA_ERR_NO_SPACE = 8
 KDA_BF16 = 0
 KDA_F32 = 1
 KDA_SCHEDULE_SPLIT = 0
@@ -36,7 +37,11 @@ EXPORTED = ("kda_status_string", "kda_abi_version", "kda_prefill_workspace_size"
             "kda_prefill_schedule", "kda_decode", "kda_prefill_ex", "kda_layer_prologue",
             "kda_layer_epilogue", "kda_prefill_set_schedule", "kda_prefill_noalloc",
             "kda_noalloc_status", "kda_layer_prologue_decode", "kda_prefill_workspace_size_ring",
-            "kda_prefill_workspace_size_min", "kda_prefill_plan")
+            "kda_prefill_workspace_size_min", "kda_prefill_plan", "kda_attn_prefill",
+            "kda_attn_prefill_workspace_size", "kda_attn_decode",
+            "kda_attn_decode_workspace_size", "kda_cache_workspace_size", "kda_cache_alloc",
+            "kda_cache_fork", "kda_cache_free", "kda_cache_compact", "kda_cache_copy",
+            "kda_cache_append")
 
 
 class PrefillPlanInfo(ctypes.Structure):
@@ -107,6 +112,32 @@ def load() -> ctypes.CDLL:
         lib.kda_prefill_noalloc.restype = ctypes.c_int
         lib.kda_noalloc_status.argtypes = [P]
         lib.kda_noalloc_status.restype = ctypes.c_int
+        I64 = ctypes.c_int64
+        lib.kda_attn_prefill_workspace_size.argtypes = [I32] * 7
+        lib.kda_attn_prefill_workspace_size.restype = SZ
+        lib.kda_attn_prefill.argtypes = [P, P, P, I64, I64, I64, F32, P, P] + [I32] * 7 + [P, P, P,
+                                                                                         SZ, P]
+        lib.kda_attn_prefill.restype = ctypes.c_int
+        lib.kda_attn_decode_workspace_size.argtypes = [I32] * 8
+        lib.kda_attn_decode_workspace_size.restype = SZ
+        lib.kda_attn_decode.argtypes = ([P, I64, P, P, I64, I64, P, P, I32, I32, P, I64, I32, P, P,
+                                         F32] + [I32] * 6 + [P, P, P, SZ, P])
+        lib.kda_attn_decode.restype = ctypes.c_int
+        lib.kda_cache_workspace_size.argtypes = [I32, I32]
+        lib.kda_cache_workspace_size.restype = SZ
+        lib.kda_cache_alloc.argtypes = [P, I64, I32, I32, P, P, I32, I32, P, SZ, P]
+        lib.kda_cache_alloc.restype = ctypes.c_int
+        lib.kda_cache_fork.argtypes = [P, I64, I32, I32, P, P, I32, I32, P, P, I32, P, P, SZ, P]
+        lib.kda_cache_fork.restype = ctypes.c_int
+        lib.kda_cache_free.argtypes = [P, I64, I32, I32, P, P, I32, P, I32, P, SZ, P]
+        lib.kda_cache_free.restype = ctypes.c_int
+        lib.kda_cache_compact.argtypes = [P, I64, I32, I32, P, I32, P, P, P, SZ, P]
+        lib.kda_cache_compact.restype = ctypes.c_int
+        lib.kda_cache_copy.argtypes = [P, I32, I64, I32, P, I32, P, P]
+        lib.kda_cache_copy.restype = ctypes.c_int
+        lib.kda_cache_append.argtypes = [P, P, I64, I64, P, I32, I32, P, P, P, P, I64, I32, I32,
+                                         I32, I32, I32, I32, P, P, P, P]
+        lib.kda_cache_append.restype = ctypes.c_int
         # test-only entry point (include/kda_testing.h)
         lib.kda_testing_prefill_chain_timeout.argtypes = [P, P, P, P, P, F32, P, P, I32, I32, I32,
                                                           I32, I32, I32, P, P, P, SZ, I32, P]
@@ -416,3 +447,339 @@ def kda_check_cu_seqlens(cu_host, T_total: int) -> int:
     import numpy as np
     a = np.ascontiguousarray(np.asarray(cu_host, dtype=np.int32))
     return int(load().kda_check_cu_seqlens(a.ctypes.data, a.shape[0] - 1, int(T_total)))
+
+
+# ---- softmax attention and the pages of its cache ---------------------------------
+def _rows_ld(t: torch.Tensor, name: str) -> int:
+    """Elements from one token row of [.., heads, D] to the next; the heads and
+    channels of a row must be contiguous, the tokens evenly spaced."""
+    H, D = t.shape[-2:]
+    if not t.is_cuda:
+        raise ValueError("KDA tensors must be CUDA tensors")
+    if D > 1 and t.stride(-1) != 1 or H > 1 and t.stride(-2) != D:
+        raise ValueError("%s: the [heads, D] rows must be contiguous" % name)
+    tokens = t.numel() // max(H * D, 1)
+    if tokens <= 1:
+        return H * D
+    if t.dim() == 3:
+        return t.stride(0)
+    B, T = t.shape[:2]
+    if T == 1:
+        return t.stride(0)
+    if B > 1 and t.stride(0) != T * t.stride(1):
+        raise ValueError("%s: the tokens must be evenly spaced" % name)
+    return t.stride(1)
+
+
+def _same(name, ref: torch.Tensor, *ts, dtype=None):
+    for t in ts:
+        if t is None:
+            continue
+        if t.dtype != (dtype or ref.dtype):
+            raise ValueError("%s must have dtype %s" % (name, dtype or ref.dtype))
+        if t.device != ref.device:
+            raise ValueError("KDA tensors must be on one device")
+
+
+def _table_args(block_table):
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_cuda:
+        raise ValueError("block_table must be a CUDA int32 [rows, cols] tensor")
+    rows, cols = block_table.shape
+    if cols > 1 and block_table.stride(1) != 1:
+        raise ValueError("the rows of block_table must be contiguous")
+    return rows, cols, block_table.stride(0) if rows > 1 else cols
+
+
+def _new_workspace(nbytes: int, device) -> torch.Tensor:
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    ws[:256].zero_()
+    return ws
+
+
+def kda_attn_prefill_workspace_size(N: int, Tq_total: int, Tk_total: int, Hq: int, Hkv: int, D: int,
+                                    io: int) -> int:
+    return int(load().kda_attn_prefill_workspace_size(N, Tq_total, Tk_total, Hq, Hkv, D, io))
+
+
+def kda_attn_decode_workspace_size(B: int, T: int, Hq: int, Hkv: int, D: int, page_size: int,
+                                   table_cols: int, io: int) -> int:
+    return int(load().kda_attn_decode_workspace_size(B, T, Hq, Hkv, D, page_size, table_cols, io))
+
+
+def kda_cache_workspace_size(num_pages: int, rows: int) -> int:
+    return int(load().kda_cache_workspace_size(num_pages, rows))
+
+
+def attn_prefill_workspace(q, k, cu_seqlens=None, N=1):
+    """A device workspace for kda_attn_prefill on q [T, Hq, D], k [Tk, Hkv, D]
+    (its status word zeroed)."""
+    N = cu_seqlens.numel() - 1 if cu_seqlens is not None else N
+    return _new_workspace(kda_attn_prefill_workspace_size(N, q.shape[0], k.shape[0], q.shape[1],
+                                                          k.shape[1], q.shape[2],
+                                                          _io_code(q.dtype)), q.device)
+
+
+def attn_decode_workspace(q, k_pages, block_table):
+    """A device workspace for kda_attn_decode on q [B, T, Hq, D] (its status word
+    zeroed)."""
+    B, T, Hq, D = q.shape
+    return _new_workspace(kda_attn_decode_workspace_size(B, T, Hq, k_pages.shape[1], D,
+                                                         k_pages.shape[2], block_table.shape[1],
+                                                         _io_code(q.dtype)), q.device)
+
+
+def cache_workspace(refs, rows=None):
+    """A device workspace for the kda_cache_* calls on a pool with these refs and a
+    block table of `rows` rows (default: at most as many as pages), its status
+    word zeroed."""
+    P = refs.numel()
+    return _new_workspace(kda_cache_workspace_size(P, P if rows is None else rows), refs.device)
+
+
+def kda_attn_prefill(q, k, v, scale, cu_seqlens=None, cu_seqlens_k=None, N=1, out=None, lse=None,
+                     output_lse=False, workspace=None, stream=None):
+    """Causal attention over packed sequences (C entry point ``kda_attn_prefill``).
+
+    q: [Tq_total, Hq, D]; k, v: [Tk_total, Hkv, D] (bf16 or fp32; tokens may be
+    strided, e.g. views of one projection's rows); cu_seqlens, cu_seqlens_k:
+    device int32 [N+1] offsets of the query and key tokens (cu_seqlens_k None:
+    the same), or None (N sequences of equal length). A sequence's last token
+    sees all of its keys. Returns (out [Tq_total, Hq, D], lse fp32 [Tq_total,
+    Hq] or None)."""
+    lib = load()
+    io = _io_code(q.dtype)
+    Tq, Hq, D = q.shape
+    Tk, Hkv, _ = k.shape
+    if v.shape != k.shape or k.shape[2] != D:
+        raise ValueError("k and v must have the shape [Tk_total, Hkv, D]")
+    ldq, ldk, ldv = _rows_ld(q, "q"), _rows_ld(k, "k"), _rows_ld(v, "v")
+    _same("k and v", q, k, v)
+    _check_cuda(cu_seqlens, cu_seqlens_k, out, lse, workspace)
+    _same("cu_seqlens", q, cu_seqlens, cu_seqlens_k, dtype=torch.int32)
+    if cu_seqlens is not None:
+        N = cu_seqlens.numel() - 1
+        if cu_seqlens_k is not None and cu_seqlens_k.numel() != N + 1:
+            raise ValueError("cu_seqlens_k must have as many offsets as cu_seqlens")
+        nq, nk = Tq, Tk
+    else:
+        if N < 1 or Tq % N or Tk % N:
+            raise ValueError("q and k must hold N sequences of equal length")
+        nq, nk = Tq // N, Tk // N
+    if out is None:
+        out = torch.empty((Tq, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if lse is None and output_lse:
+        lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+    elif lse is not None and lse.shape != (Tq, Hq):
+        raise ValueError("lse must have the shape [Tq_total, Hq]")
+    _same("out", q, out)
+    _same("lse", q, lse, dtype=torch.float32)
+    if workspace is None:
+        workspace = attn_prefill_workspace(q, k, cu_seqlens, N)
+    rc = lib.kda_attn_prefill(_ptr(q), _ptr(k), _ptr(v), ldq, ldk, ldv, float(scale),
+                              _ptr(cu_seqlens), _ptr(cu_seqlens_k), N, nq, nk, Hq, Hkv, D, io,
+                              _ptr(out), _ptr(lse), _ptr(workspace), workspace.numel(),
+                              _stream_ptr(stream))
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_attn_prefill")
+    return out, lse
+
+
+def kda_attn_decode(q, k_pages, v_pages, block_table, seq_lens, scale, k_new=None, v_new=None,
+                    tree_mask=None, out=None, lse=None, output_lse=False, workspace=None,
+                    stream=None):
+    """Attention of T new tokens per sequence over a paged cache and one another
+    (C entry point ``kda_attn_decode``).
+
+    q: [B, T, Hq, D], T <= 64; k_pages, v_pages: [P, Hkv, page, D]; block_table:
+    int32 [B, cols]; seq_lens: int32 [B] cached tokens; k_new, v_new:
+    [B, T, Hkv, D] of the new tokens themselves (or None); tree_mask: int64
+    [B, T], bit s = the token sees new token s (None: the chain, s <= t).
+    Returns (out [B, T, Hq, D], lse fp32 [B, T, Hq] or None)."""
+    lib = load()
+    io = _io_code(q.dtype)
+    B, T, Hq, D = q.shape
+    P, Hkv, page, Dk = k_pages.shape
+    if v_pages.shape != k_pages.shape or Dk != D:
+        raise ValueError("k_pages and v_pages must have the shape [P, Hkv, page, D]")
+    ldq = _rows_ld(q, "q")
+    ldk = ldv = 0
+    if k_new is not None and v_new is not None:
+        if k_new.shape != (B, T, Hkv, D) or v_new.shape != (B, T, Hkv, D):
+            raise ValueError("k_new and v_new must have the shape [B, T, Hkv, D]")
+        ldk, ldv = _rows_ld(k_new, "k_new"), _rows_ld(v_new, "v_new")
+    _same("keys and values", q, k_pages, v_pages, k_new, v_new)
+    _check_cuda(k_pages, v_pages, seq_lens, tree_mask, out, lse, workspace)
+    rows, cols, ld = _table_args(block_table)
+    if rows != B or seq_lens.shape != (B,):
+        raise ValueError("block_table and seq_lens must have a row for each sequence")
+    _same("seq_lens", q, block_table, seq_lens, dtype=torch.int32)
+    if tree_mask is not None and tree_mask.shape != (B, T):
+        raise ValueError("tree_mask must have the shape [B, T]")
+    _same("tree_mask", q, tree_mask, dtype=torch.int64)
+    if out is None:
+        out = torch.empty((B, T, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the shape of q")
+    if lse is None and output_lse:
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+    elif lse is not None and lse.shape != (B, T, Hq):
+        raise ValueError("lse must have the shape [B, T, Hq]")
+    _same("out", q, out)
+    _same("lse", q, lse, dtype=torch.float32)
+    if workspace is None:
+        workspace = attn_decode_workspace(q, k_pages, block_table)
+    rc = lib.kda_attn_decode(_ptr(q), ldq, _ptr(k_new), _ptr(v_new), ldk, ldv, _ptr(k_pages),
+                             _ptr(v_pages), P, page, _ptr(block_table), ld, cols, _ptr(seq_lens),
+                             _ptr(tree_mask), float(scale), B, T, Hq, Hkv, D, io, _ptr(out),
+                             _ptr(lse), _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_attn_decode")
+    return out, lse
+
+
+def _cache_ints(block_table, *ts):
+    _check_cuda(*ts)
+    _same("cache arrays", block_table, *ts, dtype=torch.int32)
+
+
+def kda_cache_alloc(block_table, want, refs, page_size, workspace=None, stream=None):
+    """Gives every row of block_table the pages it lacks for want[row] tokens (C
+    entry point ``kda_cache_alloc``); refs: int32 [P]. All device int32 arrays,
+    updated in place."""
+    rows, cols, ld = _table_args(block_table)
+    _cache_ints(block_table, want, refs)
+    if want.shape != (rows,):
+        raise ValueError("want must have an entry for each row")
+    if workspace is None:
+        workspace = cache_workspace(refs, rows)
+    rc = load().kda_cache_alloc(_ptr(block_table), ld, rows, cols, _ptr(want), _ptr(refs),
+                                refs.numel(), page_size, _ptr(workspace), workspace.numel(),
+                                _stream_ptr(stream))
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_cache_alloc")
+
+
+def kda_cache_fork(block_table, seq_lens, refs, src, dst, page_size, copies=None, workspace=None,
+                   stream=None):
+    """Row dst[i] becomes a copy of row src[i], sharing its full pages (C entry
+    point ``kda_cache_fork``). Returns copies int32 [n, 2]: the (from, to) pages
+    that ``kda_cache_copy`` has to copy in every pool, (-1, -1) for none."""
+    rows, cols, ld = _table_args(block_table)
+    n = src.numel()
+    if dst.numel() != n or seq_lens.shape != (rows,):
+        raise ValueError("src and dst must pair up, seq_lens must have an entry for each row")
+    if copies is None:
+        copies = torch.empty((n, 2), dtype=torch.int32, device=block_table.device)
+    elif copies.shape != (n, 2):
+        raise ValueError("copies must have the shape [n, 2]")
+    _cache_ints(block_table, seq_lens, refs, src, dst, copies)
+    if workspace is None:
+        workspace = cache_workspace(refs, rows)
+    rc = load().kda_cache_fork(_ptr(block_table), ld, rows, cols, _ptr(seq_lens), _ptr(refs),
+                               refs.numel(), page_size, _ptr(src), _ptr(dst), n, _ptr(copies),
+                               _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_cache_fork")
+    return copies
+
+
+def kda_cache_free(block_table, seq_lens, refs, rows, workspace=None, stream=None):
+    """Drops the pages of the given rows (device int32, distinct; < 0 is skipped;
+    C entry point ``kda_cache_free``)."""
+    n_rows, cols, ld = _table_args(block_table)
+    if seq_lens.shape != (n_rows,):
+        raise ValueError("seq_lens must have an entry for each row")
+    _cache_ints(block_table, seq_lens, refs, rows)
+    if workspace is None:
+        workspace = cache_workspace(refs, n_rows)
+    rc = load().kda_cache_free(_ptr(block_table), ld, n_rows, cols, _ptr(seq_lens), _ptr(refs),
+                               refs.numel(), _ptr(rows), rows.numel(), _ptr(workspace),
+                               workspace.numel(), _stream_ptr(stream))
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_cache_free")
+
+
+def kda_cache_compact(block_table, refs, copies=None, count=None, workspace=None, stream=None):
+    """Renames the live pages to 0 .. L - 1 (C entry point ``kda_cache_compact``).
+    Returns (copies int32 [P, 2], count int32 [1]): the (from, to) pages that
+    ``kda_cache_copy`` has to copy in every pool, and how many."""
+    rows, cols, ld = _table_args(block_table)
+    P = refs.numel()
+    if copies is None:
+        copies = torch.empty((P, 2), dtype=torch.int32, device=refs.device)
+    elif copies.shape != (P, 2):
+        raise ValueError("copies must have the shape [P, 2]")
+    if count is None:
+        count = torch.empty(1, dtype=torch.int32, device=refs.device)
+    _cache_ints(block_table, refs, copies, count)
+    if workspace is None:
+        workspace = cache_workspace(refs, rows)
+    rc = load().kda_cache_compact(_ptr(block_table), ld, rows, cols, _ptr(refs), P, _ptr(copies),
+                                  _ptr(count), _ptr(workspace), workspace.numel(),
+                                  _stream_ptr(stream))
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_cache_compact")
+    return copies, count
+
+
+def kda_cache_copy(pools, copies, count=None, stream=None):
+    """Entry copies[i][1] = entry copies[i][0] in each pool (C entry point
+    ``kda_cache_copy``): pools of equal shape [entries, ...], any dtype; copies
+    int32 [n, 2]; count: device int32 [1], only the first *count pairs."""
+    pools = list(pools)
+    if not pools:
+        return
+    _check_cuda(copies, count, *pools)
+    _same("copies", pools[0], copies, count, dtype=torch.int32)
+    if copies.dim() != 2 or copies.shape[1] != 2:
+        raise ValueError("copies must have the shape [n, 2]")
+    entries = pools[0].shape[0]
+    entry = pools[0].numel() // max(entries, 1) * pools[0].element_size()
+    for p in pools:
+        if p.shape[0] != entries or p.numel() * p.element_size() != entry * entries:
+            raise ValueError("the pools must have entries of one size")
+    ptrs = (ctypes.c_void_p * len(pools))(*[p.data_ptr() for p in pools])
+    rc = load().kda_cache_copy(ptrs, len(pools), entry, entries, _ptr(copies), copies.shape[0],
+                               _ptr(count), _stream_ptr(stream))
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_cache_copy")
+
+
+def kda_cache_append(k, v, k_pages, v_pages, block_table, start, cu_seqlens=None, index=None,
+                     count=None, workspace=None, stream=None):
+    """Writes key and value rows into the pages at positions start[b], start[b] + 1,
+    ... of each sequence (C entry point ``kda_cache_append``).
+
+    k, v: packed [T_total, Hkv, D] with cu_seqlens (device int32 [N+1]), or
+    [N, T, Hkv, D], of which sequence b appends the rows index[b, :count[b]]
+    (device int32; None: all, in order): the accepted tokens of a draft."""
+    lib = load()
+    io = _io_code(k.dtype)
+    P, Hkv, page, D = k_pages.shape
+    if v.shape != k.shape or v_pages.shape != k_pages.shape or k.shape[-2:] != (Hkv, D):
+        raise ValueError("k, v must be rows of [Hkv, D], the pools [P, Hkv, page, D]")
+    ldk, ldv = _rows_ld(k, "k"), _rows_ld(v, "v")
+    _same("rows and pages", k, v, k_pages, v_pages)
+    rows, cols, ld = _table_args(block_table)
+    _check_cuda(k_pages, v_pages, workspace)
+    _cache_ints(block_table, start, cu_seqlens, index, count)
+    if cu_seqlens is not None:
+        if k.dim() != 3:
+            raise ValueError("packed rows must be [T_total, Hkv, D]")
+        N, T = cu_seqlens.numel() - 1, k.shape[0]
+    else:
+        if k.dim() != 4:
+            raise ValueError("rows without cu_seqlens must be [N, T, Hkv, D]")
+        N, T = k.shape[:2]
+    if rows < N or start.shape != (N,):
+        raise ValueError("block_table and start must have a row for each sequence")
+    if index is not None and index.shape != (N, T) or count is not None and count.shape != (N,):
+        raise ValueError("index must have the shape [N, T], count [N]")
+    rc = lib.kda_cache_append(_ptr(k), _ptr(v), ldk, ldv, _ptr(cu_seqlens), N, T, _ptr(index),
+                              _ptr(count), _ptr(start), _ptr(block_table), ld, cols, P, page, Hkv,
+                              D, io, _ptr(k_pages), _ptr(v_pages), _ptr(workspace),
+                              _stream_ptr(stream))
+    if rc != KDA_OK:
+        raise KDAError(rc, "kda_cache_append")

@@ -105,6 +105,7 @@ const char *kda_status_string(int status) {
         case KDA_ERR_DEVICE: return "KDA_ERR_DEVICE";
         case KDA_ERR_TOO_LARGE: return "KDA_ERR_TOO_LARGE";
         case KDA_ERR_RANGE: return "KDA_ERR_RANGE";
+        case KDA_ERR_NO_SPACE: return "KDA_ERR_NO_SPACE";
         default: return "KDA_ERR_UNKNOWN";
     }
 }
@@ -423,6 +424,7 @@ int kda_workspace_status(void *workspace, void *stream) {
     if (word & kda::kStatusTimeout) return KDA_ERR_TIMEOUT;
     if (word & kda::kStatusBadSeqlens) return KDA_ERR_DEVICE;
     if (word & kda::kStatusRange) return KDA_ERR_RANGE;
+    if (word & kda::kStatusNoSpace) return KDA_ERR_NO_SPACE;
     return KDA_OK;
 }
 

@@ -1,0 +1,340 @@
+// Softmax attention: the arguments and the work split that the tensor-core
+// kernel (bf16, kda_attn_tc.cu), the CUDA-core kernel (fp32, kda_attn_f32.cu)
+// and the kernel that joins split rows (kda_attn_combine.cu) share.
+//
+// Work. An item is (sequence, kv head, row block): the rows of a block are
+// (token, query head of the group) pairs, token major, so that the G query
+// heads that share a kv head share every K and V tile that is loaded. A row
+// block is `streams` tiles of `tile_tokens` tokens (tile_tokens * G rows at
+// most per tile). An item's keys are cut into tiles of `kt` keys; with drafts,
+// the last tile holds the drafts alone.
+//
+// Split. All items, in order, form one line of weighted work (their visible
+// keys plus a fixed share for an item's start and end); CTA c takes the part
+// [U c / C, U (c + 1) / C) of it, cut at key tiles. So every CTA has the same
+// load whatever the lengths are, one long sequence spreads over all SMs, and a
+// CTA has at most two parts of items: its first (which starts inside an item)
+// and its last (which ends inside one). Those write (O, m, l) to the workspace
+// and the join kernel adds them up in CTA order; all others write their rows.
+#pragma once
+
+#include <stdint.h>
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace attn {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kPartRows = 256;  // rows of a part in the workspace
+constexpr int kMaxDrafts = 64;  // a row's draft mask has 64 bits
+
+// Workspace: status word and padding, the parts' headers, then per part slot
+// O (fp32, [32 channel quads][256 rows][4]) and m, l ([256] each).
+constexpr size_t kWsHeader = 256;
+struct PartHeader {
+    int32_t valid;      // this slot holds a part of an item
+    int32_t ends;       // the item's last part
+    int32_t token0;     // first token row of the item in q / out
+    int32_t tokens;     // valid tokens of the item
+    int32_t kvh;        // kv head
+    int32_t pad[3];
+};
+__host__ __device__ constexpr size_t part_stride() {
+    return (size_t)kPartRows * kD * 4 + (size_t)kPartRows * 8;
+}
+__host__ __device__ inline size_t headers_bytes(int ctas) {
+    return ((size_t)2 * ctas * sizeof(PartHeader) + 255) / 256 * 256;
+}
+__host__ __device__ inline size_t workspace_bytes(int ctas) {
+    return kWsHeader + headers_bytes(ctas) + (size_t)2 * ctas * part_stride();
+}
+
+// Arguments shared by the kernels (prefill: packed rows; decode: pages).
+struct Args {
+    // sizes
+    int N, Hq, Hkv, G;       // sequences, heads, Hq / Hkv
+    int T;                   // decode: new tokens per sequence; prefill: query rows of an equal-length sequence
+    int Tk;                  // prefill: keys of an equal-length sequence
+    int Tq_total, Tk_total;  // prefill: packed totals
+    int page, pages, table_cols;
+    long long table_ld;
+    int has_new;             // decode: k_new / v_new given
+    int tile_tokens;         // tokens of a row tile
+    int streams;             // row tiles of an item: 2, or 1 when both streams share one row tile
+    int kt;                  // keys of a key tile
+    int extra;               // an item's start and end, in keys
+    int min_part;            // keys of work below which no further CTA is used
+    float scale;
+    // device pointers
+    const int32_t *cu_q, *cu_k;      // prefill offsets (NULL: equal lengths)
+    const int32_t *table, *lens;     // decode
+    const unsigned long long *mask;  // decode, NULL: the chain
+    void *out;
+    float *lse;
+    unsigned char *ws;               // NULL: no part is ever split (one CTA)
+    int ctas;
+};
+
+__device__ __forceinline__ uint32_t *status_word(const Args &a) {
+    return reinterpret_cast<uint32_t *>(a.ws);
+}
+__device__ __forceinline__ PartHeader *part_header(const Args &a, int slot) {
+    return reinterpret_cast<PartHeader *>(a.ws + kWsHeader) + slot;
+}
+__device__ __forceinline__ float *part_o(const Args &a, int slot) {
+    return reinterpret_cast<float *>(a.ws + kWsHeader + headers_bytes(a.ctas) +
+                                     (size_t)slot * part_stride());
+}
+__device__ __forceinline__ float2 *part_ml(const Args &a, int slot) {
+    return reinterpret_cast<float2 *>(part_o(a, slot) + (size_t)kPartRows * kD);
+}
+
+// One sequence. ok = false: malformed lengths.
+struct Seq {
+    int q0, Lq;  // first query row, query tokens
+    int k0, Lk;  // prefill: first key row, keys; decode: Lk = cached tokens
+    int ni;      // items per kv head
+};
+template <bool PAGED>
+__device__ __forceinline__ bool load_seq(const Args &a, int n, Seq &s) {
+    const int block = a.tile_tokens * a.streams;
+    bool ok = true;
+    if (PAGED) {
+        s.q0 = n * a.T;
+        s.Lq = a.T;
+        s.k0 = 0;
+        s.Lk = a.lens[n];
+        ok = s.Lk >= 0 && (long long)s.Lk <= (long long)a.table_cols * a.page;
+    } else {
+        int q1, k1;
+        if (a.cu_q != nullptr) {
+            s.q0 = a.cu_q[n];
+            q1 = a.cu_q[n + 1];
+        } else {
+            s.q0 = n * a.T;
+            q1 = s.q0 + a.T;
+        }
+        if (a.cu_k != nullptr) {
+            s.k0 = a.cu_k[n];
+            k1 = a.cu_k[n + 1];
+        } else {
+            s.k0 = n * a.Tk;
+            k1 = s.k0 + a.Tk;
+        }
+        ok = s.q0 >= 0 && q1 >= s.q0 && q1 <= a.Tq_total && s.k0 >= 0 && k1 >= s.k0 &&
+             k1 <= a.Tk_total && (n != 0 || (s.q0 == 0 && s.k0 == 0));
+        s.Lq = q1 - s.q0;
+        s.Lk = k1 - s.k0;
+    }
+    if (!ok) s.Lq = 0;
+    s.ni = (s.Lq + block - 1) / block;
+    return ok;
+}
+// Keys that the last row of item i sees (prefill), or all keys (decode).
+template <bool PAGED>
+__device__ __forceinline__ int item_keys(const Args &a, const Seq &s, int i) {
+    if (PAGED) return s.Lk;
+    const long long last = (long long)(i + 1) * a.tile_tokens * a.streams;
+    const long long v = (last < s.Lq ? last : s.Lq) + (long long)s.Lk - s.Lq;
+    return v > 0 ? (int)v : 0;
+}
+template <bool PAGED>
+__device__ __forceinline__ int item_tiles(const Args &a, const Seq &s, int i) {
+    return (item_keys<PAGED>(a, s, i) + a.kt - 1) / a.kt + (PAGED ? a.has_new : 0);
+}
+// Weight of items 0 .. i - 1 of one kv head (arithmetic series of visible keys).
+template <bool PAGED>
+__device__ __forceinline__ long long items_weight(const Args &a, const Seq &s, int i) {
+    if (i <= 0) return 0;
+    if (PAGED)
+        return (long long)i * (a.extra + (long long)((s.Lk + a.kt - 1) / a.kt + a.has_new) * a.kt);
+    const long long block = a.tile_tokens * a.streams, d = (long long)s.Lk - s.Lq;
+    long long w = (long long)i * a.extra;
+    const int full = i < s.ni ? i : s.ni - 1;  // items whose last token is not the sequence's
+    long long first = d < 0 ? (-d) / block : 0;  // items that see nothing
+    if (first < full) {
+        const long long lo = d + (first + 1) * block, hi = d + (long long)full * block;
+        w += (lo + hi) * (full - first) / 2;
+    }
+    if (i >= s.ni) w += s.Lk;  // the last item's last row sees every key
+    return w;
+}
+template <bool PAGED>
+__device__ __forceinline__ long long seq_weight(const Args &a, const Seq &s) {
+    return s.ni == 0 ? 0 : items_weight<PAGED>(a, s, s.ni) * a.Hkv;
+}
+
+// A point on the line of work: before tile `tile` of item (n, h, i).
+struct Point {
+    int n, h, i, tile;
+};
+__device__ __forceinline__ bool same_item(const Point &x, const Point &y) {
+    return x.n == y.n && x.h == y.h && x.i == y.i;
+}
+
+// The point at distance x into sequence n (0 <= x < its weight).
+template <bool PAGED>
+__device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n, long long x) {
+    const long long per_head = items_weight<PAGED>(a, s, s.ni);
+    Point p;
+    p.n = n;
+    p.h = (int)(x / per_head);
+    x -= p.h * per_head;
+    int lo = 0, hi = s.ni - 1;  // the last item that starts at or before x
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (items_weight<PAGED>(a, s, mid) <= x) lo = mid;
+        else hi = mid - 1;
+    }
+    p.i = lo;
+    const long long y = x - items_weight<PAGED>(a, s, lo) - a.extra / 2;
+    const int nt = item_tiles<PAGED>(a, s, lo);
+    const long long t = y <= 0 ? 0 : (y + a.kt / 2) / a.kt;
+    p.tile = t < nt ? (int)t : nt;
+    return p;
+}
+
+// Finds, with one converged warp, the points at U c / C and U (c + 1) / C.
+// Returns false when there is nothing for this CTA: it has no part, or the
+// offsets are malformed (which sets the status bit; the whole call is then
+// skipped). A decode sequence with a malformed length is flagged and skipped
+// alone. `used` is the number of CTAs with a part.
+template <bool PAGED>
+__device__ __forceinline__ bool split_points(const Args &a, int c, Point &p0, Point &p1) {
+    const int lane = threadIdx.x & 31;
+    long long total = 0;
+    bool good = true;
+    for (int n0 = 0; n0 < a.N; n0 += 32) {
+        Seq s;
+        long long w = 0;
+        if (n0 + lane < a.N) {
+            good = load_seq<PAGED>(a, n0 + lane, s) && good;
+            w = seq_weight<PAGED>(a, s);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        total += w;
+    }
+    good = __all_sync(0xffffffffu, good);
+    if (!good) {
+        if (lane == 0 && a.ws != nullptr) atomicOr(status_word(a), kStatusBadSeqlens);
+        if (!PAGED) return false;
+    }
+    if (total == 0) return false;
+    long long ctas = total / a.min_part;
+    ctas = ctas < 1 ? 1 : (ctas < a.ctas ? ctas : a.ctas);
+    if (c >= ctas) return false;
+    const long long x0 = total / ctas * c + total % ctas * c / ctas;
+    const long long x1 = total / ctas * (c + 1) + total % ctas * (c + 1) / ctas;
+    p1.n = a.N;  // the end of the line
+    p1.h = p1.i = p1.tile = 0;
+    long long before = 0;
+    bool found0 = false, found1 = c + 1 == ctas;
+    for (int n0 = 0; n0 < a.N && !(found0 && found1); n0 += 32) {
+        Seq s;
+        long long w = 0;
+        if (n0 + lane < a.N) {
+            load_seq<PAGED>(a, n0 + lane, s);
+            w = seq_weight<PAGED>(a, s);
+        }
+        long long incl = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        const long long lo = before + incl - w;
+        for (int e = 0; e < 2; ++e) {
+            const long long x = e ? x1 : x0;
+            const bool here = (e ? !found1 : !found0) && w > 0 && x >= lo && x < lo + w;
+            const unsigned who = __ballot_sync(0xffffffffu, here);
+            if (who == 0) continue;
+            Point p = {0, 0, 0, 0};
+            if (here) p = point_in_seq<PAGED>(a, s, n0 + lane, x - lo);
+            const int src = __ffs(who) - 1;
+            p.n = __shfl_sync(0xffffffffu, p.n, src);
+            p.h = __shfl_sync(0xffffffffu, p.h, src);
+            p.i = __shfl_sync(0xffffffffu, p.i, src);
+            p.tile = __shfl_sync(0xffffffffu, p.tile, src);
+            if (e) {
+                p1 = p;
+                found1 = true;
+            } else {
+                p0 = p;
+                found0 = true;
+            }
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    return found0;
+}
+
+// A part of an item: the key tiles [ta, tb) of (n, h, i).
+struct Part {
+    int n, h, i;
+    int ta, tb, nt;   // tiles of this part, tiles of the item
+    int q0, tokens;   // first token row, valid tokens of the item
+    int first_tok;    // the item's first token within its sequence
+    int Lq, Lk, k0;
+    __device__ __forceinline__ bool whole() const { return ta == 0 && tb == nt; }
+};
+
+// Walks the parts of [at, end). Every role of a CTA walks them alike.
+template <bool PAGED>
+struct Walk {
+    Point at, end;
+    Seq s;
+    int seq_n;
+    __device__ __forceinline__ void init(const Point &p0, const Point &p1) {
+        at = p0;
+        end = p1;
+        seq_n = -1;
+    }
+    __device__ __forceinline__ bool next(const Args &a, Part &p) {
+        while (true) {
+            if (at.n >= a.N || (same_item(at, end) && at.tile >= end.tile)) return false;
+            if (seq_n != at.n) {
+                load_seq<PAGED>(a, at.n, s);
+                seq_n = at.n;
+            }
+            if (s.ni == 0) {
+                ++at.n;
+                at.h = at.i = at.tile = 0;
+                continue;
+            }
+            const int block = a.tile_tokens * a.streams;
+            p.n = at.n;
+            p.h = at.h;
+            p.i = at.i;
+            p.nt = item_tiles<PAGED>(a, s, at.i);
+            p.ta = at.tile;
+            p.tb = same_item(at, end) ? end.tile : p.nt;
+            p.first_tok = at.i * block;
+            p.q0 = s.q0 + p.first_tok;
+            p.tokens = min(block, s.Lq - p.first_tok);
+            p.Lq = s.Lq;
+            p.Lk = s.Lk;
+            p.k0 = s.k0;
+            if (same_item(at, end)) {
+                at.tile = end.tile;
+            } else {
+                at.tile = 0;
+                if (++at.i == s.ni) {
+                    at.i = 0;
+                    if (++at.h == a.Hkv) {
+                        at.h = 0;
+                        ++at.n;
+                    }
+                }
+            }
+            // a part without tiles is one only for rows that see nothing
+            if (p.tb > p.ta || p.nt == 0) return true;
+        }
+    }
+};
+// The workspace slot of CTA c's unfinished part.
+__device__ __forceinline__ int part_slot(int c, const Part &p) { return 2 * c + (p.ta == 0); }
+
+}  // namespace attn
+}  // namespace kda

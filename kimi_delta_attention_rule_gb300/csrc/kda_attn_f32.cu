@@ -1,0 +1,271 @@
+// Softmax attention in fp32 on CUDA cores (the formulas and the work split are
+// those of kda_attn.cuh): 128 threads hold 64 (token, head) rows; per tile of 64
+// keys a thread forms an 8 x 4 piece of S = Q K^T and an 8 x 8 piece of O += P V.
+// Bound by the FMA pipe: 12 shared loads of 16 bytes per 128 FMAs (S) and 16 per
+// 256 (O), two CTAs per SM so that one loads while the other multiplies.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_attn.cuh"
+#include "kda_common.cuh"
+
+namespace kda {
+namespace attn {
+
+constexpr int kF32Threads = 128;
+constexpr int kF32Tile = 64;          // rows, and keys
+constexpr int kPitch = kD + 4;        // floats per Q / K row: neighbouring rows on other banks
+constexpr int kPitchP = kF32Tile + 4;
+constexpr int kF32Smem = (2 * kF32Tile * kPitch + kF32Tile * kD) * 4;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+}
+
+struct F32Ptrs {
+    const float *q, *k, *v, *kn, *vn;  // decode: k, v = pages
+    long long ldq, ldk, ldv;           // decode: of kn, vn
+};
+
+template <bool PAGED>
+__global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const Args a, const F32Ptrs io) {
+    extern __shared__ __align__(16) float smf[];
+    float *const Qs = smf, *const Ks = smf + kF32Tile * kPitch, *const Vs = smf + 2 * kF32Tile * kPitch;
+    float *const Ps = Ks;  // P replaces K once S is formed
+    __shared__ Point pts[2];
+    __shared__ int any;
+    const int tid = threadIdx.x, cta = blockIdx.x;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (tid < 32) {
+        Point p0, p1;
+        const bool ok = split_points<PAGED>(a, cta, p0, p1);
+        if (tid == 0) {
+            pts[0] = p0;
+            pts[1] = p1;
+            any = ok;
+            part_header(a, 2 * cta)->valid = 0;
+            part_header(a, 2 * cta + 1)->valid = 0;
+        }
+    }
+    __syncthreads();
+    if (!any) return;
+    Walk<PAGED> walk;
+    walk.init(pts[0], pts[1]);
+    const int ty = tid >> 4, tx = tid & 15;  // rows 8 ty + i; keys tx + 16 e, channels 4 tx + 64 e
+    const float c = a.scale * kLog2e;
+    const int G = a.G;
+    Part p;
+    while (walk.next(a, p)) {
+        const int rows = p.tokens * G;
+        __syncthreads();  // the last part's reads are done
+        for (int x = tid; x < kF32Tile * 32; x += kF32Threads) {
+            const int r = x >> 5, ch = (x & 31) * 4, tok = r / G;
+            const bool ok = r < rows;
+            const float *src = io.q + (ok ? (long long)(p.q0 + tok) * io.ldq + (p.h * G + r - tok * G) * kD + ch : 0);
+            cp16(smem_u32(Qs + r * kPitch + ch), src, ok);
+        }
+        cp_commit();
+        float m[8], l[8];
+        float4 o[8][2];
+        long long seen[8];  // keys that the row sees (of the cache: all)
+        unsigned long long bits[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+            const int r = 8 * ty + i, t = p.first_tok + r / G;
+            seen[i] = PAGED ? p.Lk : (long long)p.Lk - p.Lq + t + 1;
+            bits[i] = 0;
+            if (PAGED && r < rows) {
+                bits[i] = a.mask != nullptr ? a.mask[(size_t)p.n * a.T + t]
+                                            : (t >= 63 ? ~0ull : (2ull << t) - 1);
+                if (a.T < 64) bits[i] &= (1ull << a.T) - 1;
+            }
+        }
+        for (int t = p.ta; t < p.tb; ++t) {
+            const bool drafts = PAGED && a.has_new && t == p.nt - 1;
+            // keys past the end load as zeros (0 times what is there could be NaN)
+            const int valid = drafts ? a.T : min(kF32Tile, p.Lk - t * kF32Tile);
+            __syncthreads();
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                for (int x = tid; x < kF32Tile * 32; x += kF32Threads) {
+                    const int r = x >> 5, ch = (x & 31) * 4;
+                    bool ok = r < valid;
+                    const float *src = io.q;
+                    if (ok) {
+                        if (!PAGED) {
+                            src = (kv ? io.v : io.k) +
+                                  (long long)(p.k0 + t * kF32Tile + r) * (kv ? io.ldv : io.ldk) + p.h * kD + ch;
+                        } else if (drafts) {
+                            src = (kv ? io.vn : io.kn) +
+                                  (long long)(p.n * a.T + r) * (kv ? io.ldv : io.ldk) + p.h * kD + ch;
+                        } else {
+                            const int pos = t * kF32Tile + r;
+                            const int pg = a.table[(size_t)p.n * a.table_ld + pos / a.page];
+                            if (pg < 0 || pg >= a.pages) {  // zeros instead
+                                atomicOr(status_word(a), kStatusBadSeqlens);
+                                ok = false;
+                            } else {
+                                src = (kv ? io.v : io.k) +
+                                      (((size_t)pg * a.Hkv + p.h) * a.page + pos % a.page) * kD + ch;
+                            }
+                        }
+                    }
+                    cp16(smem_u32(kv ? Vs + r * kD + ch : Ks + r * kPitch + ch), src, ok);
+                }
+                cp_commit();
+            }
+            cp_wait<1>();
+            __syncthreads();
+            float s[8][4] = {};
+#pragma unroll 4
+            for (int d = 0; d < kD; d += 4) {
+                float4 kk[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kk[e] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * e) * kPitch + d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 qq = *reinterpret_cast<const float4 *>(Qs + (8 * ty + i) * kPitch + d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        s[i][e] = fmaf(qq.x, kk[e].x, s[i][e]);
+                        s[i][e] = fmaf(qq.y, kk[e].y, s[i][e]);
+                        s[i][e] = fmaf(qq.z, kk[e].z, s[i][e]);
+                        s[i][e] = fmaf(qq.w, kk[e].w, s[i][e]);
+                    }
+                }
+            }
+            __syncthreads();  // K is read: P may replace it
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = tx + 16 * e;
+                    const bool see = drafts ? (bits[i] >> key & 1) != 0 : seen[i] > (long long)t * kF32Tile + key;
+                    if (!see) s[i][e] = -INFINITY;
+                    top = fmaxf(top, s[i][e]);
+                }
+#pragma unroll
+                for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const float up = fmaxf(m[i], top);
+                const float f = m[i] == -INFINITY ? 0.f : exp2f((m[i] - up) * c);
+                const float uc = up == -INFINITY ? 0.f : up * c;
+                m[i] = up;
+                float sum = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y = exp2f(fmaf(s[i][e], c, -uc));
+                    sum += y;
+                    Ps[(8 * ty + i) * kPitchP + tx + 16 * e] = y;
+                }
+                l[i] = l[i] * f + sum;  // this lane's keys; joined at the end
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    o[i][e].x *= f;
+                    o[i][e].y *= f;
+                    o[i][e].z *= f;
+                    o[i][e].w *= f;
+                }
+            }
+            cp_wait<0>();
+            __syncthreads();
+#pragma unroll 2
+            for (int key = 0; key < kF32Tile; key += 4) {
+                float4 vv[4][2];
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        vv[x][e] = *reinterpret_cast<const float4 *>(Vs + (key + x) * kD + 4 * tx + 64 * e);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 pp = *reinterpret_cast<const float4 *>(Ps + (8 * ty + i) * kPitchP + key);
+                    const float w[4] = {pp.x, pp.y, pp.z, pp.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            o[i][e].x = fmaf(w[x], vv[x][e].x, o[i][e].x);
+                            o[i][e].y = fmaf(w[x], vv[x][e].y, o[i][e].y);
+                            o[i][e].z = fmaf(w[x], vv[x][e].z, o[i][e].z);
+                            o[i][e].w = fmaf(w[x], vv[x][e].w, o[i][e].w);
+                        }
+                }
+            }
+        }
+        if (p.ta >= p.tb) cp_wait<0>();  // Q of a part without keys
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+            for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+            const int r = 8 * ty + i;
+            if (r >= rows) continue;
+            if (!p.whole()) {
+                const int slot = part_slot(cta, p);
+                float4 *o4 = reinterpret_cast<float4 *>(part_o(a, slot)) + r;
+                o4[(size_t)tx * kPartRows] = o[i][0];
+                o4[(size_t)(16 + tx) * kPartRows] = o[i][1];
+                if (tx == 0) part_ml(a, slot)[r] = make_float2(m[i], l[i]);
+                continue;
+            }
+            const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+            const int tok = r / G;
+            const size_t dst = (size_t)(p.q0 + tok) * a.Hq + p.h * G + r - tok * G;
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + dst * kD + 4 * tx + 64 * e) =
+                    make_float4(o[i][e].x * inv, o[i][e].y * inv, o[i][e].z * inv, o[i][e].w * inv);
+            if (tx == 0 && a.lse != nullptr) a.lse[dst] = l[i] == 0.f ? -INFINITY : m[i] * a.scale + logf(l[i]);
+        }
+        if (tid == 0 && !p.whole()) {
+            PartHeader *h = part_header(a, part_slot(cta, p));
+            h->ends = p.tb == p.nt;
+            h->token0 = p.q0;
+            h->tokens = p.tokens;
+            h->kvh = p.h;
+            h->valid = 1;
+        }
+    }
+}
+
+cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
+
+template <bool PAGED>
+static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
+    a.kt = kF32Tile;
+    a.streams = 1;
+    a.tile_tokens = PAGED && a.T * a.G < kF32Tile ? a.T : kF32Tile / a.G;
+    a.extra = 64;
+    a.min_part = 256;
+    cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF32Smem);
+    if (e != cudaSuccess) return e;
+    attn_f32_kernel<PAGED><<<a.ctas, kF32Threads, kF32Smem, stream>>>(a, io);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? launch_attn_combine(a, false, stream) : e;
+}
+
+cudaError_t launch_attn_prefill_f32(const Args &a, const void *q, const void *k, const void *v, long long ldq,
+                                    long long ldk, long long ldv, cudaStream_t stream) {
+    const F32Ptrs io = {static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(v),
+                        nullptr, nullptr, ldq, ldk, ldv};
+    return launch_f32<false>(a, io, stream);
+}
+cudaError_t launch_attn_decode_f32(const Args &a, const void *q, const void *kp, const void *vp, const void *kn,
+                                   const void *vn, long long ldq, long long ldk, long long ldv,
+                                   cudaStream_t stream) {
+    const F32Ptrs io = {static_cast<const float *>(q), static_cast<const float *>(kp), static_cast<const float *>(vp),
+                        static_cast<const float *>(kn), static_cast<const float *>(vn), ldq, ldk, ldv};
+    return launch_f32<true>(a, io, stream);
+}
+
+}  // namespace attn
+}  // namespace kda

@@ -1,0 +1,579 @@
+// The pages of a key/value cache: appending rows, and allocating, forking,
+// freeing, compacting and copying pages.
+//
+// A cache is a pool of pages [pages][Hkv][page][128] for K and one for V (of any
+// number of layers), a block table int32 [rows][cols] (row b: the pages of a
+// sequence in order, -1 past its end) and refs int32 [pages], the number of table
+// entries on each page (0: free). A page is chosen lowest number first, so that a
+// call's result is a function of its inputs.
+//
+// The calls that choose pages need, for every page, its rank among the free (or
+// live) ones: a prefix sum over refs. They run as one cluster of eight CTAs,
+// each with an eighth of refs, that exchange their counts through distributed
+// shared memory: one launch, no workspace for the sum, no spinning. Bound: the
+// latency of a handful of dependent loads and cluster barriers (refs itself, 4
+// bytes per page, is 0.3 us of one SM's bandwidth at 8,192 pages).
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_common.cuh"
+
+namespace kda {
+namespace cache {
+
+namespace cg = cooperative_groups;
+
+constexpr int kCtas = 8;  // the largest portable cluster
+constexpr int kThreads = 1024;
+constexpr int kMaxPools = 16;
+
+struct Table {
+    int32_t *entries;
+    int64_t ld;
+    int32_t rows, cols;
+    __device__ __forceinline__ int32_t *row(int r) const { return entries + (size_t)r * ld; }
+};
+
+// ---- append -----------------------------------------------------------------
+// kRows rows per block: kRows threads find where their row goes, then all copy
+// 16-byte pieces, K and V, four in flight per thread.
+constexpr int kAppendRows = 8;
+constexpr int kAppendThreads = 256;
+
+__global__ void __launch_bounds__(kAppendThreads)
+    append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, int64_t ldk, int64_t ldv,
+                  const int32_t *__restrict__ cu, int N, int T, int64_t rows, const int32_t *__restrict__ index,
+                  const int32_t *__restrict__ count, const int32_t *__restrict__ start, Table table, int pages,
+                  int page, int Hkv, int piece_bits, uint4 *__restrict__ kp, uint4 *__restrict__ vp,
+                  uint32_t *status) {
+    __shared__ int64_t src[kAppendRows], dst[kAppendRows];  // source row; first piece of (page, head 0, offset)
+    const int64_t r0 = (int64_t)blockIdx.x * kAppendRows;
+    if (threadIdx.x < kAppendRows) {
+        const int64_t r = r0 + threadIdx.x;
+        int64_t from = -1, to = -1;
+        if (r < rows) {
+            int n, i;
+            bool ok = true;
+            if (cu != nullptr) {
+                int lo = 0, hi = N - 1;  // the last sequence that starts at or before r
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (cu[mid] <= r) lo = mid;
+                    else hi = mid - 1;
+                }
+                n = lo;
+                i = (int)(r - cu[n]);
+                if (cu[0] != 0 || cu[n + 1] <= r) {  // offsets that do not cover this row
+                    ok = false;
+                    if (status) atomicOr(status, kStatusBadSeqlens);
+                }
+                from = r;
+            } else {
+                n = (int)(r / T);
+                i = (int)(r - (int64_t)n * T);
+                from = r;
+                if (count != nullptr) {
+                    const int have = count[n];
+                    if (have < 0 || have > T) {
+                        ok = false;
+                        if (status && i == 0) atomicOr(status, kStatusBadSeqlens);
+                    } else {
+                        ok = i < have;
+                    }
+                }
+                if (ok && index != nullptr) {
+                    const int x = index[r];
+                    if (x < 0 || x >= T) {
+                        ok = false;
+                        if (status) atomicOr(status, kStatusBadSeqlens);
+                    }
+                    from = (int64_t)n * T + x;
+                }
+            }
+            if (ok) {
+                const int64_t pos = (int64_t)start[n] + i, slot = pos / page;
+                const int pg = pos >= 0 && slot < table.cols ? table.row(n)[slot] : -1;
+                if (pg >= 0 && pg < pages) to = ((int64_t)pg * Hkv * page + pos % page) << piece_bits;
+                else if (status) atomicOr(status, kStatusBadSeqlens);
+            }
+        }
+        src[threadIdx.x] = from;
+        dst[threadIdx.x] = to;
+    }
+    __syncthreads();
+    const int per_row = Hkv << piece_bits;  // 16-byte pieces of a row
+    const int total = kAppendRows * per_row;
+    const int64_t head_step = (int64_t)page << piece_bits;
+    constexpr int kFlight = 4;
+    for (int x0 = threadIdx.x; x0 < 2 * total; x0 += kFlight * kAppendThreads) {
+        uint4 y[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            int x = x0 + f * kAppendThreads;
+            const bool is_v = x >= total;
+            x -= is_v ? total : 0;
+            if (x >= total) continue;
+            const int r = x / per_row, w = x - r * per_row;
+            if (dst[r] >= 0) y[f] = (is_v ? v : k)[src[r] * (is_v ? ldv : ldk) + w];
+        }
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            int x = x0 + f * kAppendThreads;
+            const bool is_v = x >= total;
+            x -= is_v ? total : 0;
+            if (x >= total) continue;
+            const int r = x / per_row, w = x - r * per_row, h = w >> piece_bits;
+            if (dst[r] >= 0)
+                (is_v ? vp : kp)[dst[r] + h * head_step + (w & ((1 << piece_bits) - 1))] = y[f];
+        }
+    }
+}
+
+// ---- copy ---------------------------------------------------------------------
+// A block takes 32 KB of one entry at a time: eight 16-byte pieces in flight per
+// thread before the first is stored.
+struct Pools {
+    uint4 *base[kMaxPools];
+};
+constexpr int kCopyThreads = 256, kCopyFlight = 8, kCopyChunk = kCopyThreads * kCopyFlight;
+
+__global__ void __launch_bounds__(kCopyThreads)
+    copy_kernel(const Pools pools, int n_pools, int64_t entry, int entries, const int2 *__restrict__ pairs, int n,
+                const int32_t *__restrict__ count) {
+    if (count != nullptr) {
+        const int have = *count;
+        n = have < 0 ? 0 : (have < n ? have : n);
+    }
+    const int64_t chunks = (entry + kCopyChunk - 1) / kCopyChunk, per_pair = chunks * n_pools;
+    for (int64_t w = blockIdx.x; w < per_pair * n; w += gridDim.x) {
+        const int j = (int)(w / per_pair);
+        const int2 p = pairs[j];
+        if (p.x < 0 || p.y < 0 || p.x >= entries || p.y >= entries || p.x == p.y) continue;
+        const int rest = (int)(w - j * per_pair), pool = (int)(rest / chunks);
+        const int64_t at = (rest - pool * chunks) * kCopyChunk + threadIdx.x;
+        const uint4 *src = pools.base[pool] + p.x * entry;
+        uint4 *dst = pools.base[pool] + p.y * entry;
+        uint4 y[kCopyFlight];
+#pragma unroll
+        for (int f = 0; f < kCopyFlight; ++f)
+            if (at + f * kCopyThreads < entry) y[f] = __ldcs(src + at + f * kCopyThreads);
+#pragma unroll
+        for (int f = 0; f < kCopyFlight; ++f)
+            if (at + f * kCopyThreads < entry) __stcs(dst + at + f * kCopyThreads, y[f]);
+    }
+}
+
+// ---- free -----------------------------------------------------------------------
+__global__ void __launch_bounds__(256)
+    free_kernel(Table table, int32_t *lens, int32_t *refs, int pages, const int32_t *__restrict__ rows,
+                uint32_t *status) {
+    const int r = rows[blockIdx.x];
+    if (r < 0 || r >= table.rows) {
+        if (r >= 0 && status && threadIdx.x == 0) atomicOr(status, kStatusBadSeqlens);
+        return;
+    }
+    int32_t *row = table.row(r);
+    for (int j = blockIdx.y * blockDim.x + threadIdx.x; j < table.cols; j += gridDim.y * blockDim.x) {
+        const int pg = row[j];
+        if (pg < 0) continue;
+        if (pg < pages) atomicSub(refs + pg, 1);
+        else if (status) atomicOr(status, kStatusBadSeqlens);
+        row[j] = -1;
+    }
+    if (blockIdx.y == 0 && threadIdx.x == 0) lens[r] = 0;
+}
+
+// ---- block and cluster sums -------------------------------------------------------
+// Exclusive prefix of x over the block; total gets the sum. Converged block.
+__device__ __forceinline__ int block_exclusive(int x, int *warp_sums, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();  // warp_sums is free
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    const int mine = warp_sums[lane];  // 32 warps
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    total = __shfl_sync(0xffffffffu, sum, 31);
+    const int before = __shfl_sync(0xffffffffu, sum - mine, warp);
+    return before + incl - x;
+}
+
+// The slice of refs of one CTA: a multiple of four pages, read as int4.
+struct Slice {
+    int lo, hi;
+};
+__device__ __forceinline__ Slice slice_of(int pages, int rank) {
+    const int per = ((pages + kCtas - 1) / kCtas + 3) & ~3;
+    Slice s;
+    s.lo = min(pages, rank * per);
+    s.hi = min(pages, s.lo + per);
+    return s;
+}
+// refs[p .. p + 3] as four live bits (pages past hi: neither live nor free)
+__device__ __forceinline__ void flags4(const int32_t *refs, int p, int hi, int &live, int &free) {
+    live = free = 0;
+    if (p + 4 <= hi) {
+        const int4 x = *reinterpret_cast<const int4 *>(refs + p);
+        live = (x.x > 0) | (x.y > 0) << 1 | (x.z > 0) << 2 | (x.w > 0) << 3;
+        free = 15 ^ live;
+        return;
+    }
+    for (int e = 0; e < 4 && p + e < hi; ++e) {
+        const int x = refs[p + e];
+        live |= (x > 0) << e;
+        free |= (x <= 0) << e;
+    }
+}
+
+struct Shared {
+    int warp_sums[32];
+    int mine;   // this CTA's count, read by the others
+    int mine2;
+};
+
+// Sum of a count over the CTAs before this one, and over all. `which` is a
+// member of Shared that holds this CTA's count.
+__device__ __forceinline__ void cluster_prefix(cg::cluster_group &cl, int *mine, int rank, int &before, int &total) {
+    cl.sync();
+    before = total = 0;
+#pragma unroll
+    for (int i = 0; i < kCtas; ++i) {
+        const int x = *cl.map_shared_rank(mine, i);
+        total += x;
+        before += i < rank ? x : 0;
+    }
+}
+
+// The free pages of rank < need, lowest first, into list; returns the number of
+// free pages. Ends with the cluster in step: list is complete for every CTA.
+__device__ __forceinline__ int list_free(cg::cluster_group &cl, Shared &sh, const int32_t *refs, int pages, int need,
+                                         int32_t *list) {
+    const int rank = (int)cl.block_rank();
+    const Slice s = slice_of(pages, rank);
+    int mine = 0;
+    for (int p = s.lo + 4 * (int)threadIdx.x; p < s.hi; p += 4 * kThreads) {
+        int live, fr;
+        flags4(refs, p, s.hi, live, fr);
+        mine += __popc(fr);
+    }
+    int total, before, all;
+    block_exclusive(mine, sh.warp_sums, total);
+    if (threadIdx.x == 0) sh.mine = total;
+    cluster_prefix(cl, &sh.mine, rank, before, all);
+    if (need <= all) {
+        int at = before;
+        for (int p0 = s.lo; p0 < s.hi && at < need; p0 += 4 * kThreads) {
+            const int p = p0 + 4 * (int)threadIdx.x;
+            int live = 0, fr = 0, round;
+            if (p < s.hi) flags4(refs, p, s.hi, live, fr);
+            int j = at + block_exclusive(__popc(fr), sh.warp_sums, round);
+            for (int e = 0; e < 4; ++e)
+                if (fr >> e & 1) {
+                    if (j < need) list[j] = p + e;
+                    ++j;
+                }
+            at += round;
+        }
+    }
+    cl.sync();
+    return all;
+}
+
+// ---- fork -------------------------------------------------------------------------
+// Each CTA ranks all forks that need a page (their lengths end inside one) and
+// lists its slice's free pages; then a warp per fork copies the table row.
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    fork_kernel(Table table, int32_t *lens, int32_t *refs, int pages, int page, const int32_t *__restrict__ src,
+                const int32_t *__restrict__ dst, int n, int2 *copies, int32_t *list, int32_t *ranks,
+                uint32_t *status) {
+    __shared__ Shared sh;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank();
+    // ranks[i]: -2 = not a fork, -1 = no partial page, else its rank among the fresh pages
+    int need = 0;
+    for (int i0 = 0; i0 < n; i0 += kThreads) {
+        const int i = i0 + (int)threadIdx.x;
+        int state = -2;
+        if (i < n) {
+            const int a = src[i], z = dst[i];
+            if (a >= 0 && z >= 0) {
+                bool ok = a < table.rows && z < table.rows && a != z;
+                if (ok) {
+                    const int len = lens[a];
+                    ok = len >= 0 && (long long)len <= (long long)table.cols * page && table.row(z)[0] < 0;
+                    state = len % page != 0;
+                }
+                if (!ok) {
+                    state = -2;
+                    if (rank == 0 && status) atomicOr(status, kStatusBadSeqlens);
+                }
+            }
+        }
+        int round;
+        const int j = need + block_exclusive(state == 1, sh.warp_sums, round);
+        if (rank == 0 && i < n) ranks[i] = state == 1 ? j : (state == 0 ? -1 : -2);
+        need += round;
+    }
+    const int have = list_free(cl, sh, refs, pages, need, list);
+    if (need > have && rank == 0 && threadIdx.x == 0 && status) atomicOr(status, kStatusNoSpace);
+    const int lane = threadIdx.x & 31;
+    for (int i = rank * (kThreads / 32) + (int)(threadIdx.x >> 5); i < n; i += kCtas * kThreads / 32) {
+        const int state = ranks[i];
+        int2 pair = make_int2(-1, -1);
+        if (state != -2 && need <= have) {
+            const int32_t *from = table.row(src[i]);
+            int32_t *to = table.row(dst[i]);
+            const int len = lens[src[i]], full = len / page;
+#pragma unroll 4
+            for (int j = lane; j < full; j += 32) {
+                const int pg = from[j];
+                to[j] = pg;
+                if (pg >= 0 && pg < pages) atomicAdd(refs + pg, 1);
+                else if (status) atomicOr(status, kStatusBadSeqlens);
+            }
+            if (state >= 0) {
+                pair = make_int2(from[full], list[state]);
+                if (lane == 0) {
+                    to[full] = pair.y;
+                    refs[pair.y] = 1;
+                }
+            }
+            if (lane == 0) lens[dst[i]] = len;
+        }
+        if (lane == 0) copies[i] = pair;
+    }
+    cl.sync();  // no CTA leaves while another may read its shared memory
+}
+
+// ---- alloc ------------------------------------------------------------------------
+// The entries in use of a row: the first -1, by a 32-way search of one warp.
+__device__ __forceinline__ int row_used(const int32_t *row, int cols) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = cols;  // the answer lies in [lo, hi]
+    while (hi > lo) {
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const bool used = at < hi && row[at] >= 0;
+        const unsigned b = __ballot_sync(0xffffffffu, used);
+        const int k = b == 0xffffffffu ? 32 : __ffs(~b) - 1;  // probes in use
+        if (k == 0) return lo;
+        const int last = lo + (k - 1) * step;  // in use; the next probe is not
+        hi = min(hi, last + step);
+        lo = last + 1;
+    }
+    return lo;
+}
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    alloc_kernel(Table table, const int32_t *__restrict__ want, int32_t *refs, int pages, int page, int32_t *list,
+                 int2 *rows_state, uint32_t *status) {
+    __shared__ Shared sh;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank(), lane = threadIdx.x & 31;
+    const int warp = rank * (kThreads / 32) + (int)(threadIdx.x >> 5), warps = kCtas * kThreads / 32;
+    for (int r = warp; r < table.rows; r += warps) {  // (pages in use, pages to add)
+        const int used = row_used(table.row(r), table.cols);
+        const long long w = want[r];
+        const bool ok = w >= 0 && w <= (long long)table.cols * page;
+        if (!ok && lane == 0 && status) atomicOr(status, kStatusBadSeqlens);
+        const int to = ok ? (int)((w + page - 1) / page) : 0;
+        if (lane == 0) rows_state[r] = make_int2(used, max(0, to - used));
+    }
+    cl.sync();
+    int need = 0;
+    for (int r0 = 0; r0 < table.rows; r0 += kThreads) {
+        const int r = r0 + (int)threadIdx.x;
+        int round;
+        block_exclusive(r < table.rows ? rows_state[r].y : 0, sh.warp_sums, round);
+        need += round;
+    }
+    const int have = list_free(cl, sh, refs, pages, need, list);
+    if (need > have) {
+        if (rank == 0 && threadIdx.x == 0 && status) atomicOr(status, kStatusNoSpace);
+    } else if (need > 0) {
+        int at = 0;
+        for (int r0 = 0; r0 < table.rows; r0 += kThreads) {
+            const int r = r0 + (int)threadIdx.x;
+            const int2 s = r < table.rows ? rows_state[r] : make_int2(0, 0);
+            int round;
+            const int j = at + block_exclusive(s.y, sh.warp_sums, round);
+            at += round;
+            if (threadIdx.x % kCtas != rank) continue;
+            int32_t *row = r < table.rows ? table.row(r) : nullptr;
+            for (int e = 0; e < s.y; ++e) {
+                const int pg = list[j + e];
+                row[s.x + e] = pg;
+                refs[pg] = 1;
+            }
+        }
+    }
+    cl.sync();
+}
+
+// ---- compact ----------------------------------------------------------------------
+// n = live pages. The j-th live page >= n moves to the j-th free page < n.
+__global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
+    compact_kernel(int32_t *refs, int pages, int2 *copies, int32_t *count, int32_t *name, int32_t *n_live) {
+    __shared__ Shared sh;
+    cg::cluster_group cl = cg::this_cluster();
+    const int rank = (int)cl.block_rank();
+    const Slice s = slice_of(pages, rank);
+    int mine = 0, total, before, n;
+    for (int p = s.lo + 4 * (int)threadIdx.x; p < s.hi; p += 4 * kThreads) {
+        int live, fr;
+        flags4(refs, p, s.hi, live, fr);
+        mine += __popc(live);
+    }
+    block_exclusive(mine, sh.warp_sums, total);
+    if (threadIdx.x == 0) sh.mine = total;
+    cluster_prefix(cl, &sh.mine, rank, before, n);
+    // holes below n (as many as live pages from n on), by slice
+    mine = 0;
+    for (int p = s.lo + 4 * (int)threadIdx.x; p < min(s.hi, n); p += 4 * kThreads) {
+        int live, fr;
+        flags4(refs, p, min(s.hi, n), live, fr);
+        mine += __popc(fr);
+    }
+    block_exclusive(mine, sh.warp_sums, total);
+    if (threadIdx.x == 0) sh.mine2 = total;
+    int holes_before, holes;
+    cluster_prefix(cl, &sh.mine2, rank, holes_before, holes);
+    // live pages before this slice that are >= n: all live before less those below n
+    const int low_before = min(s.lo, n) - holes_before;
+    int hole_at = holes_before, move_at = before - low_before;
+    for (int p0 = s.lo; p0 < s.hi; p0 += 4 * kThreads) {
+        const int p = p0 + 4 * (int)threadIdx.x;
+        int live = 0, fr = 0, round;
+        if (p < s.hi) flags4(refs, p, s.hi, live, fr);
+        const int low = p + 4 <= n ? 15 : (p >= n ? 0 : (1 << (n - p)) - 1);
+        const int hole = fr & low, mover = live & ~low;
+        int j = hole_at + block_exclusive(__popc(hole), sh.warp_sums, round);
+        hole_at += round;
+        for (int e = 0; e < 4; ++e)
+            if (hole >> e & 1) copies[j++].y = p + e;
+        j = move_at + block_exclusive(__popc(mover), sh.warp_sums, round);
+        move_at += round;
+        for (int e = 0; e < 4; ++e)
+            if (mover >> e & 1) copies[j++].x = p + e;
+            else if (p + e >= n && p + e < s.hi) name[p + e] = p + e;
+    }
+    cl.sync();
+    for (int j = rank * kThreads + (int)threadIdx.x; j < pages; j += kCtas * kThreads) {
+        if (j < holes) {
+            const int2 p = copies[j];
+            name[p.x] = p.y;
+            refs[p.y] = refs[p.x];
+            refs[p.x] = 0;
+        } else {
+            copies[j] = make_int2(-1, -1);
+        }
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+        *count = holes;
+        *n_live = n;
+    }
+    cl.sync();
+}
+// Table entries of the pages that moved (those from n_live on) get their new names.
+__global__ void __launch_bounds__(256)
+    rename_kernel(Table table, int pages, const int32_t *__restrict__ name, const int32_t *__restrict__ n_live,
+                  uint32_t *status) {
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    const int n = *n_live;
+    for (int r = blockIdx.x; r < table.rows; r += gridDim.x) {
+        int32_t *row = table.row(r);
+        for (int j = blockIdx.y * blockDim.x + threadIdx.x; j < table.cols; j += gridDim.y * blockDim.x) {
+            const int pg = row[j];
+            if (pg < n) continue;
+            if (pg < pages) row[j] = name[pg];
+            else if (status) atomicOr(status, kStatusBadSeqlens);
+        }
+    }
+}
+
+// ---- host -------------------------------------------------------------------------
+cudaError_t launch_append(const void *k, const void *v, int64_t ldk, int64_t ldv, const int32_t *cu, int N, int T,
+                          int64_t rows, const int32_t *index, const int32_t *count, const int32_t *start,
+                          const int32_t *table, int64_t table_ld, int cols, int pages, int page, int Hkv, int es,
+                          void *kp, void *vp, uint32_t *status, cudaStream_t stream) {
+    const int piece_bits = es == 2 ? 4 : 5;  // 16-byte pieces of a head's row: 16 or 32
+    const int64_t per = 16 / es;
+    const Table t = {const_cast<int32_t *>(table), table_ld, N, cols};
+    append_kernel<<<(unsigned)((rows + kAppendRows - 1) / kAppendRows), kAppendThreads, 0, stream>>>(
+        static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), ldk / per, ldv / per, cu, N, T, rows, index,
+        count, start, t, pages, page, Hkv, piece_bits, static_cast<uint4 *>(kp), static_cast<uint4 *>(vp), status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_copy(void *const *pools, int n_pools, int64_t entry_bytes, int entries, const int32_t *pairs, int n,
+                        const int32_t *count, int sms, cudaStream_t stream) {
+    for (int at = 0; at < n_pools; at += kMaxPools) {
+        Pools p = {};
+        const int here = n_pools - at < kMaxPools ? n_pools - at : kMaxPools;
+        for (int i = 0; i < here; ++i) p.base[i] = static_cast<uint4 *>(pools[at + i]);
+        const int64_t entry = entry_bytes / 16, work = (entry + kCopyChunk - 1) / kCopyChunk * here * n;
+        const int64_t most = (int64_t)sms * 8;
+        copy_kernel<<<(unsigned)(work < most ? work : most), kCopyThreads, 0, stream>>>(
+            p, here, entry, entries, reinterpret_cast<const int2 *>(pairs), n, count);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+static dim3 table_grid(int rows, int cols) {  // about one entry per thread, within reason
+    const int y = (cols + 255) / 256;
+    return dim3((unsigned)rows, (unsigned)(y < 64 ? y : 64));
+}
+
+cudaError_t launch_free(int32_t *table, int64_t ld, int rows, int cols, int32_t *lens, int32_t *refs, int pages,
+                        const int32_t *which, int n, uint32_t *status, cudaStream_t stream) {
+    free_kernel<<<table_grid(n, cols), 256, 0, stream>>>(Table{table, ld, rows, cols}, lens, refs, pages, which, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_fork(int32_t *table, int64_t ld, int rows, int cols, int32_t *lens, int32_t *refs, int pages, int page,
+                        const int32_t *src, const int32_t *dst, int n, int32_t *copies, int32_t *scratch,
+                        uint32_t *status, cudaStream_t stream) {
+    fork_kernel<<<kCtas, kThreads, 0, stream>>>(Table{table, ld, rows, cols}, lens, refs, pages, page, src, dst, n,
+                                                reinterpret_cast<int2 *>(copies), scratch, scratch + pages, status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_alloc(int32_t *table, int64_t ld, int rows, int cols, const int32_t *want, int32_t *refs, int pages,
+                         int page, int32_t *scratch, uint32_t *status, cudaStream_t stream) {
+    alloc_kernel<<<kCtas, kThreads, 0, stream>>>(Table{table, ld, rows, cols}, want, refs, pages, page,
+                                                 scratch + 2 * (int64_t)rows, reinterpret_cast<int2 *>(scratch), status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_compact(int32_t *table, int64_t ld, int rows, int cols, int32_t *refs, int pages, int32_t *copies,
+                           int32_t *count, int32_t *scratch, uint32_t *status, cudaStream_t stream) {
+    compact_kernel<<<kCtas, kThreads, 0, stream>>>(refs, pages, reinterpret_cast<int2 *>(copies), count, scratch + 4,
+                                                   scratch);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || rows == 0 || cols == 0) return e;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = table_grid(rows < 65535 ? rows : 65535, cols);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, rename_kernel, Table{table, ld, rows, cols}, pages,
+                              static_cast<const int32_t *>(scratch + 4), static_cast<const int32_t *>(scratch), status);
+}
+
+}  // namespace cache
+}  // namespace kda

@@ -17,6 +17,7 @@ constexpr float kGMax = 0.0f;
 constexpr uint32_t kStatusBadSeqlens = 1u;
 constexpr uint32_t kStatusTimeout = 2u;
 constexpr uint32_t kStatusRange = 4u;  // a result of the bf16 prefill is not finite
+constexpr uint32_t kStatusNoSpace = 8u;  // a cache call needed more pages than are free
 
 __device__ __forceinline__ float clamp_g(float g) { return fminf(fmaxf(g, kGMin), kGMax); }
 

@@ -87,6 +87,16 @@ __device__ __forceinline__ uint64_t smem_desc(uint32_t saddr, uint32_t lbo, uint
     return d;                // base offset 0, relative LBO, layout SWIZZLE_NONE
 }
 
+// Shared-memory matrix descriptor, 128-byte swizzle (what a tensor-map copy with
+// SWIZZLE_128B and 128-byte boxes writes): rows of 64 16-bit elements, groups of
+// eight rows (1024 bytes, 1024-byte aligned) SBO apart. K-major: the rows run
+// along M or N and one descriptor covers 64 elements of K (LBO unused; the next
+// 16 elements of K are 32 bytes on). MN-major: the rows run along K and LBO is
+// the distance between blocks of 64 M or N elements.
+__device__ __forceinline__ uint64_t smem_desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    return smem_desc(saddr, lbo, sbo) | (uint64_t)2 << 61;
+}
+
 // Instruction descriptor, kind::f16, fp32 accumulation.
 // ab_f16: 1 = fp16 operands, 0 = bf16 operands (A and B always share the type).
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, int ab_f16, int a_mn, int b_mn) {
