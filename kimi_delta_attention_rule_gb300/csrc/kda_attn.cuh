@@ -62,9 +62,9 @@ struct Args {
     int has_new;             // decode: k_new / v_new given
     int tile_tokens;         // tokens of a row tile
     int streams;             // row tiles of an item: 2, or 1 when both streams share one row tile
-    int kt;                  // keys of a key tile
     int extra;               // an item's start and end, in keys
     int min_part;            // keys of work below which no further CTA is used
+    int cut;                 // tiles that a part of an item has at least
     float scale;
     // device pointers
     const int32_t *cu_q, *cu_k;      // prefill offsets (NULL: equal lengths)
@@ -135,34 +135,33 @@ __device__ __forceinline__ bool load_seq(const Args &a, int n, Seq &s) {
 template <bool PAGED>
 __device__ __forceinline__ int item_keys(const Args &a, const Seq &s, int i) {
     if (PAGED) return s.Lk;
-    const long long last = (long long)(i + 1) * a.tile_tokens * a.streams;
-    const long long v = (last < s.Lq ? last : s.Lq) + (long long)s.Lk - s.Lq;
-    return v > 0 ? (int)v : 0;
+    const int left = (int)((unsigned)s.Lq - (unsigned)(i + 1) * (unsigned)(a.tile_tokens * a.streams));  // tokens after the item
+    const int v = left > 0 ? s.Lk - left : s.Lk;
+    return v > 0 ? v : 0;
 }
-template <bool PAGED>
+template <bool PAGED, int KT>
 __device__ __forceinline__ int item_tiles(const Args &a, const Seq &s, int i) {
-    return (item_keys<PAGED>(a, s, i) + a.kt - 1) / a.kt + (PAGED ? a.has_new : 0);
+    return (int)(((unsigned)item_keys<PAGED>(a, s, i) + KT - 1) / KT) + (PAGED ? a.has_new : 0);
 }
 // Weight of items 0 .. i - 1 of one kv head (arithmetic series of visible keys).
-template <bool PAGED>
+template <bool PAGED, int KT>
 __device__ __forceinline__ long long items_weight(const Args &a, const Seq &s, int i) {
     if (i <= 0) return 0;
-    if (PAGED)
-        return (long long)i * (a.extra + (long long)((s.Lk + a.kt - 1) / a.kt + a.has_new) * a.kt);
-    const long long block = a.tile_tokens * a.streams, d = (long long)s.Lk - s.Lq;
+    if (PAGED) return (long long)i * (a.extra + (long long)item_tiles<PAGED, KT>(a, s, 0) * KT);
+    const int block = a.tile_tokens * a.streams, d = s.Lk - s.Lq;
     long long w = (long long)i * a.extra;
     const int full = i < s.ni ? i : s.ni - 1;  // items whose last token is not the sequence's
-    long long first = d < 0 ? (-d) / block : 0;  // items that see nothing
+    const int first = d < 0 ? -d / block : 0;  // items that see nothing
     if (first < full) {
-        const long long lo = d + (first + 1) * block, hi = d + (long long)full * block;
-        w += (lo + hi) * (full - first) / 2;
+        const long long lo = (long long)(first + 1) * block, hi = (long long)full * block;
+        w += ((lo + hi + 2LL * d) * (full - first)) >> 1;
     }
     if (i >= s.ni) w += s.Lk;  // the last item's last row sees every key
     return w;
 }
-template <bool PAGED>
+template <bool PAGED, int KT>
 __device__ __forceinline__ long long seq_weight(const Args &a, const Seq &s) {
-    return s.ni == 0 ? 0 : items_weight<PAGED>(a, s, s.ni) * a.Hkv;
+    return s.ni == 0 ? 0 : items_weight<PAGED, KT>(a, s, s.ni) * a.Hkv;
 }
 
 // A point on the line of work: before tile `tile` of item (n, h, i).
@@ -173,25 +172,32 @@ __device__ __forceinline__ bool same_item(const Point &x, const Point &y) {
     return x.n == y.n && x.h == y.h && x.i == y.i;
 }
 
-// The point at distance x into sequence n (0 <= x < its weight).
-template <bool PAGED>
+// The point at distance x into sequence n (0 <= x < its weight); a converged
+// warp with the same arguments in all lanes.
+template <bool PAGED, int KT>
 __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n, long long x) {
-    const long long per_head = items_weight<PAGED>(a, s, s.ni);
+    const int lane = threadIdx.x & 31;
+    const long long per_head = items_weight<PAGED, KT>(a, s, s.ni);
     Point p;
     p.n = n;
-    p.h = (int)(x / per_head);
+    p.h = min(a.Hkv - 1, (int)((float)x / (float)per_head));
+    while (p.h > 0 && p.h * per_head > x) --p.h;  // (the quotient was rounded)
+    while (p.h + 1 < a.Hkv && (p.h + 1) * per_head <= x) ++p.h;
     x -= p.h * per_head;
-    int lo = 0, hi = s.ni - 1;  // the last item that starts at or before x
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (items_weight<PAGED>(a, s, mid) <= x) lo = mid;
-        else hi = mid - 1;
+    int lo = 0, count = s.ni;  // the last item that starts at or before x is in [lo, lo + count)
+    while (count > 1) {
+        const int step = (count + 31) / 32, at = lo + lane * step;
+        const bool before = lane * step < count && items_weight<PAGED, KT>(a, s, at) <= x;
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));  // (lane 0 always is)
+        count = min(step, count - k * step);
+        lo += k * step;
     }
     p.i = lo;
-    const long long y = x - items_weight<PAGED>(a, s, lo) - a.extra / 2;
-    const int nt = item_tiles<PAGED>(a, s, lo);
-    const long long t = y <= 0 ? 0 : (y + a.kt / 2) / a.kt;
-    p.tile = t < nt ? (int)t : nt;
+    const long long y = x - items_weight<PAGED, KT>(a, s, lo) - a.extra / 2;
+    const int nt = item_tiles<PAGED, KT>(a, s, lo);
+    const int t = y <= 0 ? 0 : (int)min((y + KT / 2) / KT, (long long)nt);
+    // short pieces are not worth their join: such a cut moves to the item's edge
+    p.tile = t < a.cut ? 0 : (t > nt - a.cut ? nt : t);
     return p;
 }
 
@@ -199,44 +205,46 @@ __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n
 // Returns false when there is nothing for this CTA: it has no part, or the
 // offsets are malformed (which sets the status bit; the whole call is then
 // skipped). A decode sequence with a malformed length is flagged and skipped
-// alone. `used` is the number of CTAs with a part.
-template <bool PAGED>
-__device__ __forceinline__ bool split_points(const Args &a, int c, Point &p0, Point &p1) {
+// alone. s0 gets the sequence of p0.
+template <bool PAGED, int KT>
+__device__ __forceinline__ bool split_points(const Args &a, int c, Point &p0, Point &p1, Seq &s0) {
     const int lane = threadIdx.x & 31;
-    long long total = 0;
+    long long total = 0, w = 0;
     bool good = true;
+    Seq s;
     for (int n0 = 0; n0 < a.N; n0 += 32) {
-        Seq s;
-        long long w = 0;
+        w = 0;
         if (n0 + lane < a.N) {
             good = load_seq<PAGED>(a, n0 + lane, s) && good;
-            w = seq_weight<PAGED>(a, s);
+            w = seq_weight<PAGED, KT>(a, s);
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
         total += w;
     }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
     good = __all_sync(0xffffffffu, good);
     if (!good) {
-        if (lane == 0 && a.ws != nullptr) atomicOr(status_word(a), kStatusBadSeqlens);
+        if (lane == 0) atomicOr(status_word(a), kStatusBadSeqlens);
         if (!PAGED) return false;
     }
     if (total == 0) return false;
-    long long ctas = total / a.min_part;
-    ctas = ctas < 1 ? 1 : (ctas < a.ctas ? ctas : a.ctas);
+    // (single precision: a cut may lie anywhere, but for all CTAs at the same place)
+    const float units = (float)total;
+    const int ctas = max(1, (int)fminf((float)a.ctas, units / (float)a.min_part));
     if (c >= ctas) return false;
-    const long long x0 = total / ctas * c + total % ctas * c / ctas;
-    const long long x1 = total / ctas * (c + 1) + total % ctas * (c + 1) / ctas;
+    const long long x0 = (long long)(units * ((float)c / (float)ctas));
+    const long long x1 = (long long)(units * ((float)(c + 1) / (float)ctas));
     p1.n = a.N;  // the end of the line
     p1.h = p1.i = p1.tile = 0;
     long long before = 0;
     bool found0 = false, found1 = c + 1 == ctas;
     for (int n0 = 0; n0 < a.N && !(found0 && found1); n0 += 32) {
-        Seq s;
-        long long w = 0;
-        if (n0 + lane < a.N) {
-            load_seq<PAGED>(a, n0 + lane, s);
-            w = seq_weight<PAGED>(a, s);
+        if (a.N > 32) {  // (else the loop above left them in place)
+            w = 0;
+            if (n0 + lane < a.N) {
+                load_seq<PAGED>(a, n0 + lane, s);
+                w = seq_weight<PAGED, KT>(a, s);
+            }
         }
         long long incl = w;
 #pragma unroll
@@ -245,23 +253,26 @@ __device__ __forceinline__ bool split_points(const Args &a, int c, Point &p0, Po
             if (lane >= o) incl += v;
         }
         const long long lo = before + incl - w;
+#pragma unroll 1
         for (int e = 0; e < 2; ++e) {
             const long long x = e ? x1 : x0;
             const bool here = (e ? !found1 : !found0) && w > 0 && x >= lo && x < lo + w;
             const unsigned who = __ballot_sync(0xffffffffu, here);
             if (who == 0) continue;
-            Point p = {0, 0, 0, 0};
-            if (here) p = point_in_seq<PAGED>(a, s, n0 + lane, x - lo);
             const int src = __ffs(who) - 1;
-            p.n = __shfl_sync(0xffffffffu, p.n, src);
-            p.h = __shfl_sync(0xffffffffu, p.h, src);
-            p.i = __shfl_sync(0xffffffffu, p.i, src);
-            p.tile = __shfl_sync(0xffffffffu, p.tile, src);
+            Seq t;
+            t.q0 = __shfl_sync(0xffffffffu, s.q0, src);
+            t.Lq = __shfl_sync(0xffffffffu, s.Lq, src);
+            t.k0 = __shfl_sync(0xffffffffu, s.k0, src);
+            t.Lk = __shfl_sync(0xffffffffu, s.Lk, src);
+            t.ni = __shfl_sync(0xffffffffu, s.ni, src);
+            const Point p = point_in_seq<PAGED, KT>(a, t, n0 + src, x - __shfl_sync(0xffffffffu, lo, src));
             if (e) {
                 p1 = p;
                 found1 = true;
             } else {
                 p0 = p;
+                s0 = t;
                 found0 = true;
             }
         }
@@ -281,15 +292,16 @@ struct Part {
 };
 
 // Walks the parts of [at, end). Every role of a CTA walks them alike.
-template <bool PAGED>
+template <bool PAGED, int KT>
 struct Walk {
     Point at, end;
     Seq s;
     int seq_n;
-    __device__ __forceinline__ void init(const Point &p0, const Point &p1) {
+    __device__ __forceinline__ void init(const Point &p0, const Point &p1, const Seq &s0) {
         at = p0;
         end = p1;
-        seq_n = -1;
+        s = s0;
+        seq_n = p0.n;
     }
     __device__ __forceinline__ bool next(const Args &a, Part &p) {
         while (true) {
@@ -307,7 +319,7 @@ struct Walk {
             p.n = at.n;
             p.h = at.h;
             p.i = at.i;
-            p.nt = item_tiles<PAGED>(a, s, at.i);
+            p.nt = item_tiles<PAGED, KT>(a, s, at.i);
             p.ta = at.tile;
             p.tb = same_item(at, end) ? end.tile : p.nt;
             p.first_tok = at.i * block;

@@ -70,7 +70,7 @@ int sm_count() {
 // CTAs of one attention call: all that fit on the device at once, fewer when
 // an upper bound of the work (in keys) cannot fill them.
 int attn_ctas(int32_t io, long long keys) {
-    const long long most = (io == KDA_F32 ? 2LL : 1LL) * sm_count(), part = io == KDA_F32 ? 256 : 768;
+    const long long most = (io == KDA_F32 ? 2LL : 1LL) * sm_count(), part = io == KDA_F32 ? 128 : 384;
     const long long n = keys / part;
     return (int)(n < 1 ? 1 : (n < most ? n : most));
 }

@@ -39,15 +39,18 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const Args a, 
     float *const Qs = smf, *const Ks = smf + kF32Tile * kPitch, *const Vs = smf + 2 * kF32Tile * kPitch;
     float *const Ps = Ks;  // P replaces K once S is formed
     __shared__ Point pts[2];
+    __shared__ Seq seq0;
     __shared__ int any;
     const int tid = threadIdx.x, cta = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (tid < 32) {
         Point p0, p1;
-        const bool ok = split_points<PAGED>(a, cta, p0, p1);
+        Seq s0;
+        const bool ok = split_points<PAGED, kF32Tile>(a, cta, p0, p1, s0);
         if (tid == 0) {
             pts[0] = p0;
             pts[1] = p1;
+            seq0 = s0;
             any = ok;
             part_header(a, 2 * cta)->valid = 0;
             part_header(a, 2 * cta + 1)->valid = 0;
@@ -55,8 +58,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const Args a, 
     }
     __syncthreads();
     if (!any) return;
-    Walk<PAGED> walk;
-    walk.init(pts[0], pts[1]);
+    Walk<PAGED, kF32Tile> walk;
+    walk.init(pts[0], pts[1], seq0);
     const int ty = tid >> 4, tx = tid & 15;  // rows 8 ty + i; keys tx + 16 e, channels 4 tx + 64 e
     const float c = a.scale * kLog2e;
     const int G = a.G;
@@ -241,11 +244,11 @@ cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
 
 template <bool PAGED>
 static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
-    a.kt = kF32Tile;
     a.streams = 1;
     a.tile_tokens = PAGED && a.T * a.G < kF32Tile ? a.T : kF32Tile / a.G;
     a.extra = 64;
-    a.min_part = 256;
+    a.min_part = 128;
+    a.cut = 3;
     cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF32Smem);
     if (e != cudaSuccess) return e;
     attn_f32_kernel<PAGED><<<a.ctas, kF32Threads, kF32Smem, stream>>>(a, io);

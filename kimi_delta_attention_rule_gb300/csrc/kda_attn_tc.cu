@@ -5,17 +5,23 @@
 //   m_i = max_j s_ij (kept in fp32, over the keys seen so far),
 //   l_i = sum_j e^{s_ij - m_i} (fp32)
 //
-// in one pass over the keys. A CTA (12 warps) holds two row tiles of 128
-// (token, head of the group) rows, one per softmax warpgroup: S = Q K^T and
-// O += P V run as M128 N128 tcgen05.mma with S, P and O in TMEM (S 2 x 128
-// columns, P over S, O 2 x 128); one thread of an MMA warp issues, a TMA warp
-// fills a ring of 128-key K and V tiles, and each softmax thread owns one row
-// (a TMEM lane), so no row statistic ever crosses threads. While one
-// warpgroup forms P from its S, the tensor core runs the other's products.
-// O is rescaled only when a row's maximum grows by more than 2^8, which P in
-// bf16 (rounded to nearest, relative step 2^-8) and l in fp32 hold without loss.
-// With at most 128 rows per kv head (decode) both warpgroups take the same row
-// tile and alternate key tiles; their results are joined at the end (DUAL).
+// in one pass over the keys. A CTA holds two row tiles of 128 (token, head of the
+// group) rows, its streams: S = Q K^T and O += P V run as M128 N128 tcgen05.mma
+// with S, P and O in TMEM (S 2 x 128 columns, P over S, O 2 x 128). Roles of the
+// 20 warps: 16 softmax warps, one thread that issues the products, a TMA warp that
+// fills a ring of 128-key K and V tiles, a scheduler that walks the CTA's parts
+// ahead of the others, a warp that zeroes V rows past a sequence's end. While one
+// stream forms P from its S, the tensor core runs the other's products.
+//
+// Each softmax thread owns one row (a TMEM lane), so no row statistic ever crosses
+// threads. Per stream S, P and the products form one serial chain, which is what
+// bounds the kernel: so P goes to the tensor core in two halves (the first half's
+// products run while the second half's exponentials do), and a part's first Q K^T
+// follows the last P V of the part before it, under that part's epilogue. O is
+// rescaled only when a row's maximum grows by more than 2^8, which P in bf16
+// (rounded to nearest, relative step 2^-8) and l in fp32 hold without loss.
+// With at most 128 rows per kv head (decode) both streams take the same row tile
+// and alternate key tiles; their results are joined at the end (DUAL).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -29,12 +35,15 @@
 namespace kda {
 namespace attn {
 
-constexpr int kThreads = 384;   // 2 softmax warpgroups, MMA warp, TMA warp, 2 idle
+constexpr int kSoftmaxWarps = 8;
+constexpr int kWarpMma = 8, kWarpTma = 9, kWarpSched = 10, kWarpFix = 11;
+constexpr int kThreads = 384;
 constexpr int kTile = 128;      // rows of a row tile, keys of a key tile
 constexpr uint32_t kTileBytes = 32768;  // 128 rows x 128 channels bf16, two 64-channel halves
 constexpr uint32_t kHalf = 16384;
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr float kRescale = 8.f;  // log2 growth of a maximum that rescales O
+constexpr int kJobRing = 8;  // more than the ring has slots: a job holds its slot until it is done
 
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: S/P of stream s at 128 s, O at 256 + 128 s
 
@@ -42,33 +51,53 @@ struct Maps {
     CUtensorMap q, k, v, kn, vn;
 };
 
-// Shared memory. Not DUAL: Q [2 buffers][2 tiles], ring of 3. DUAL: Q [2
-// buffers], 32 KB for the join of the two streams, ring of 4.
+// A part as the roles need it, in shared memory.
+constexpr int kDescs = 4;
+struct Desc {
+    int last;              // no further part
+    int n, h, q0, k0, Lk;
+    int first_tok;         // the item's first token within its sequence
+    int ta, nt;            // the part's first tile; tiles of the item
+    int whole, slot;       // the part is the item; its workspace slot
+    int writer;            // DUAL: the stream with the first tile, which joins and writes
+    int seen;              // prefill: keys that the item's first token sees; decode: cached keys
+    int q[2];              // running number of each stream's Q tile
+    int count[2];          // key tiles of each stream
+    int start[2];          // its first tile (DUAL: every second from there)
+    int tokens[2];         // valid tokens of its row tile
+};
+
+// Shared memory: Q tiles, (DUAL) 32 KB for the join of the two streams, the ring
+// of K and V tiles, barriers and descriptors.
 template <bool DUAL>
 struct Smem {
-    static constexpr int kRing = DUAL ? 4 : 3;
+    static constexpr int kQs = DUAL ? 2 : 3, kRing = 4;
     static constexpr uint32_t kQ = 0;
-    static constexpr uint32_t kJoin = 2 * kTileBytes;  // DUAL only
-    static constexpr uint32_t kKv = (DUAL ? 3 : 4) * kTileBytes;
+    static constexpr uint32_t kJoin = kQs * kTileBytes;  // DUAL only
+    static constexpr uint32_t kKv = 3 * kTileBytes;
     static constexpr uint32_t kBars = kKv + kRing * kTileBytes;
-    static constexpr uint32_t kBytes = kBars + 1024 + 1024;  // + barriers and descriptors, + alignment
+    static constexpr uint32_t kBytes = kBars + 1024;
 };
 
 struct Bars {  // shared-memory addresses
     uint32_t base;
     __device__ uint32_t qfull(int i) const { return base + 8 * i; }
-    __device__ uint32_t qempty(int i) const { return base + 16 + 8 * i; }
-    __device__ uint32_t sfull(int s) const { return base + 32 + 8 * s; }
-    __device__ uint32_t pready(int s) const { return base + 48 + 8 * s; }
-    __device__ uint32_t ofull(int s) const { return base + 64 + 8 * s; }
-    __device__ uint32_t tail() const { return base + 80; }
-    __device__ uint32_t kvfull(int i) const { return base + 96 + 8 * i; }
-    __device__ uint32_t kvempty(int i) const { return base + 128 + 8 * i; }
-    __device__ uint32_t tmem() const { return base + 160; }
-    __device__ uint32_t dfull(int i) const { return base + 168 + 8 * i; }
-    __device__ uint32_t dempty(int i) const { return base + 200 + 8 * i; }
-    static constexpr uint32_t kDesc = 256;  // kDescs descriptors
+    __device__ uint32_t qempty(int i) const { return base + 24 + 8 * i; }
+    __device__ uint32_t sfull(int s) const { return base + 48 + 8 * s; }
+    __device__ uint32_t pready(int s, int half) const { return base + 64 + 16 * half + 8 * s; }
+    __device__ uint32_t ofull(int s) const { return base + 96 + 8 * s; }
+    __device__ uint32_t kvfull(int i) const { return base + 112 + 8 * i; }
+    __device__ uint32_t kvempty(int i) const { return base + 144 + 8 * i; }
+    __device__ uint32_t vraw(int i) const { return base + 176 + 8 * i; }
+    __device__ uint32_t dfull(int i) const { return base + 208 + 8 * i; }
+    __device__ uint32_t dempty(int i) const { return base + 240 + 8 * i; }
+    __device__ uint32_t jfull(int i) const { return base + 272 + 8 * i; }
+    static constexpr uint32_t kTmem = 336;
+    static constexpr uint32_t kDead = 340;  // a role gave up
+    static constexpr uint32_t kJobs = 344;  // kJobRing times (slot, valid rows)
+    static constexpr uint32_t kDesc = 416;  // kDescs descriptors
 };
+static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= 1024, "barrier area");
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
@@ -84,6 +113,9 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *m, int c
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
         "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
+    asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -106,32 +138,33 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
     return d;
 }
+// A bounded wait. (The clock is read once in 4096 tries: a read takes as long as
+// much of what is waited for.)
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
+    if (tc::mbar_try_wait(bar, parity)) return true;
+    uint64_t t0 = 0;
+    for (uint32_t i = 1;; ++i) {
+        if (tc::mbar_try_wait(bar, parity)) return true;
+        if (i % 4096 != 0) continue;
+        const uint64_t now = tc::globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > kWaitNs) return false;
+    }
+}
 // a wait of a whole warp, which leaves it converged
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, kWaitNs));
+    return __all_sync(0xffffffffu, wait(bar, parity));
 }
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("barrier.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
-// A part as the roles need it, in shared memory. The scheduler warp walks the
-// CTA's parts ahead of the others (its dependent loads of lengths are off their
-// path, and their registers hold no walk) and puts them in a ring.
-constexpr int kDescs = 4;
-struct Desc {
-    int last;              // no further part
-    int n, h, q0, k0, Lk;
-    int first_tok;         // the item's first token within its sequence
-    int ta, step;          // stream s takes the tiles ta + s (step - 1), then every step-th
-    int nt;                // tiles of the item
-    int whole, ends, slot; // the part is the item; it is the item's last; its workspace slot
-    int part_tokens;
-    int count[2];          // tiles of each stream
-    int tokens[2];         // valid tokens of its row tile
-    int seen;              // prefill: keys that the item's first token sees; decode: cached keys
+// The scheduler's state over a CTA's parts: Q tiles and (DUAL) key tiles so far.
+struct Run {
+    int q, tiles;
 };
 template <bool PAGED, bool DUAL>
-__device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, Desc &d) {
+__device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, Run &run, Desc &d) {
     d.last = 0;
     d.n = p.n;
     d.h = p.h;
@@ -140,29 +173,40 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
     d.Lk = p.Lk;
     d.first_tok = p.first_tok;
     d.ta = p.ta;
-    d.step = DUAL ? 2 : 1;
     d.nt = p.nt;
     d.whole = p.whole();
-    d.ends = p.tb == p.nt;
     d.slot = part_slot(cta, p);
-    d.part_tokens = p.tokens;
+    d.writer = DUAL ? run.tiles & 1 : 0;
     d.seen = PAGED ? p.Lk : p.Lk - p.Lq + p.first_tok + 1;
-    for (int s = 0; s < 2; ++s) {
-        if (DUAL) {
+    if (DUAL) {  // tiles alternate between the streams, across parts too
+        const int tiles = p.tb - p.ta;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int second = s != d.writer;
             d.tokens[s] = p.tokens;
-            d.count[s] = (p.tb - p.ta - s + 1) / 2;
-            continue;
+            d.count[s] = (tiles + 1 - second) / 2;
+            d.start[s] = p.ta + second;
+            d.q[s] = run.q;
         }
-        const int left = p.tokens - s * a.tile_tokens;
-        const int tokens = left < 0 ? 0 : (left < a.tile_tokens ? left : a.tile_tokens);
-        int end = p.tb;
-        if (!PAGED) {  // the keys that the row tile's last token sees
-            const int seen = d.seen + s * a.tile_tokens + tokens - 1;
-            const int nt = seen <= 0 ? 0 : (seen + kTile - 1) / kTile;
-            end = end < nt ? end : nt;
+        run.tiles += tiles;
+        run.q += tiles > 0;
+    } else {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            const int left = p.tokens - s * a.tile_tokens;
+            const int tokens = left < 0 ? 0 : (left < a.tile_tokens ? left : a.tile_tokens);
+            int end = p.tb;
+            if (!PAGED) {  // the keys that the row tile's last token sees
+                const int seen = d.seen + s * a.tile_tokens + tokens - 1;
+                const int nt = seen <= 0 ? 0 : (int)(((unsigned)seen + kTile - 1) / kTile);
+                end = end < nt ? end : nt;
+            }
+            d.tokens[s] = tokens;
+            d.count[s] = tokens == 0 || end < p.ta ? 0 : end - p.ta;
+            d.start[s] = p.ta;
+            d.q[s] = run.q;
+            run.q += d.count[s] > 0;
         }
-        d.tokens[s] = tokens;
-        d.count[s] = tokens == 0 || end < p.ta ? 0 : end - p.ta;
     }
 }
 
@@ -170,65 +214,91 @@ template <bool PAGED, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const Args a, const __grid_constant__ Maps maps) {
     using L = Smem<DUAL>;
-    extern __shared__ unsigned char smem_raw[];
-    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    unsigned char *const sm = smem_raw + (base - smem_u32(smem_raw));
+    extern __shared__ __align__(1024) unsigned char sm[];
+    const uint32_t base = smem_u32(sm);
     const Bars bars{base + L::kBars};
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int cta = blockIdx.x;
+    if (base & 1023u) {  // (the swizzled tiles need it)
+        if (tid == 0) atomicOr(status_word(a), kStatusTimeout);
+        return;
+    }
 
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    if (warp == 9) {
+    if (warp == kWarpTma) {
         if (lane == 0) {
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < L::kQs; ++i) {
                 tc::mbar_init(bars.qfull(i), 1);
-                tc::mbar_init(bars.qempty(i), 8);
-                tc::mbar_init(bars.sfull(i), 1);
-                tc::mbar_init(bars.pready(i), 4);
-                tc::mbar_init(bars.ofull(i), 1);
+                tc::mbar_init(bars.qempty(i), 4);  // the softmax warps of one stream
             }
-            tc::mbar_init(bars.tail(), 1);
-            for (int i = 0; i < kDescs; ++i) {
-                tc::mbar_init(bars.dfull(i), 1);
-                tc::mbar_init(bars.dempty(i), 10);  // TMA, MMA, 8 softmax warps
+            for (int i = 0; i < 2; ++i) {
+                tc::mbar_init(bars.sfull(i), 1);
+                tc::mbar_init(bars.pready(i, 0), 4);
+                tc::mbar_init(bars.pready(i, 1), 4);
+                tc::mbar_init(bars.ofull(i), 1);
             }
             for (int i = 0; i < L::kRing; ++i) {
                 tc::mbar_init(bars.kvfull(i), 1);
                 tc::mbar_init(bars.kvempty(i), 1);
+                tc::mbar_init(bars.vraw(i), 1);
             }
+            for (int i = 0; i < kDescs; ++i) {
+                tc::mbar_init(bars.dfull(i), 1);
+                tc::mbar_init(bars.dempty(i), kSoftmaxWarps + 2);  // and TMA, MMA
+            }
+            for (int i = 0; i < kJobRing; ++i) tc::mbar_init(bars.jfull(i), 1);
+            *reinterpret_cast<int *>(sm + L::kBars + Bars::kDead) = 0;
             tc::fence_mbar_init();
         }
-    } else if (warp == 10) {
-        tc::tmem_alloc(bars.tmem(), 512);
+    } else if (warp == kWarpFix) {
+        tc::tmem_alloc(bars.base + Bars::kTmem, 512);
         tc::tmem_relinquish();
+    } else if (warp == kWarpMma) {
+        if (lane == 0) {
+            prefetch_map(&maps.q);
+            prefetch_map(&maps.k);
+            prefetch_map(&maps.v);
+            if (PAGED && a.has_new) {
+                prefetch_map(&maps.kn);
+                prefetch_map(&maps.vn);
+            }
+        }
     }
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    const uint32_t tm = *reinterpret_cast<uint32_t *>(sm + L::kBars + 160);
+    const uint32_t tm = *reinterpret_cast<uint32_t *>(sm + L::kBars + Bars::kTmem);
     const Desc *const descs = reinterpret_cast<const Desc *>(sm + L::kBars + Bars::kDesc);
+    volatile int *const dead = reinterpret_cast<volatile int *>(sm + L::kBars + Bars::kDead);
     bool alive = true;
     uint32_t nd = 0;  // descriptors taken
+    // a wait that may last for a whole part: limited too, and ends when another role gives up
+    auto long_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        for (int i = 0; i < 100; ++i) {
+            if (warp_wait(bar, parity)) return true;
+            if (*dead) return false;
+        }
+        return false;
+    };
     // the next descriptor (NULL: no further part, or a wait ran out)
     auto next_desc = [&]() -> const Desc * {
-        alive = tc::mbar_wait(bars.dfull(nd % kDescs), (nd / kDescs) & 1, kWaitNs);
+        alive = warp_wait(bars.dfull(nd % kDescs), (nd / kDescs) & 1);
         const Desc *d = descs + nd % kDescs;
         return alive && !d->last ? d : nullptr;
     };
-    auto free_desc = [&]() { mbar_arrive(bars.dempty(nd++ % kDescs)); };
 
-    if (warp < 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;\n");
-        // ---- softmax warpgroups: thread = row (TMEM lane) ------------------------
-        const int s = warp >> 2, r = tid & 127;
-        const uint32_t tl = tm + ((uint32_t)(32 * (warp & 3)) << 16);
+    if (warp < kSoftmaxWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
+        // ---- softmax warps: thread = row (TMEM lane) ---------------------------------
+        const int s = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
+        const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
         const uint32_t tS = tl + kColS + 128 * s, tO = tl + kColO + 128 * s;
         const int tok = r / a.G, g = r - tok * a.G;
         const float c = a.scale * kLog2e;
-        uint32_t ns = 0, no = 0, items = 0;
+        uint32_t ns = 0, no = 0;
         while (const Desc *d = next_desc()) {
-            const int steps = d->count[s], others = d->count[1 - s], tokens = d->tokens[s];
-            const bool row_ok = tok < tokens;
+            const int steps = d->count[s];
+            const bool row_ok = tok < d->tokens[s];
             const bool warp_ok = __any_sync(0xffffffffu, row_ok);
             float m = -INFINITY, l = 0.f;
             unsigned long long bits = 0;
@@ -241,9 +311,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // keys that the row tile's first row and this row see
             const int seen0 = d->seen + (PAGED ? 0 : s * a.tile_tokens);
             const int seen = PAGED ? seen0 : seen0 + tok;
-            const int last_tile = d->nt - 1, step = d->step;
-            int t = d->ta + s * (step - 1);
-            for (int j = 0; j < steps; ++j, t += step) {
+            const int draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
+            int t = d->start[s];
+            for (int j = 0; j < steps; ++j, t += DUAL ? 2 : 1) {
                 if (!warp_wait(bars.sfull(s), ns++ & 1)) {
                     alive = false;
                     break;
@@ -252,8 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp_ok) {
                     uint32_t x[8][16];
                     tc::tmem_ld_cols<8>(tS, x);
-                    const bool drafts = PAGED && a.has_new && t == last_tile;
-                    if (drafts) {
+                    if (PAGED && t == draft_tile) {
 #pragma unroll
                         for (int i = 0; i < kTile; ++i)
                             if (i >= kMaxDrafts || !((bits >> i) & 1)) x[i / 16][i % 16] = 0xff800000u;
@@ -274,22 +343,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j == 0) {
                         m = top;
                     } else {
-                        // -inf - -inf is NaN: not greater, no rescale
+                        // (-inf - -inf is NaN: not greater, no rescale)
                         const bool grow = (top - m) * c > kRescale;
                         if (__any_sync(0xffffffffu, grow)) {
                             const float up = fmaxf(m, top);
                             const float f = m == -INFINITY ? 0.f : ex2((m - up) * c);
                             m = up;
                             l *= f;
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q) {
+                                uint32_t o[1][16];
+                                tc::tmem_ld_cols<1>(tO + 16 * q, o);
 #pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                uint32_t o[2][16];
-                                tc::tmem_ld_cols<2>(tO + 32 * q, o);
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
-                                    o[i / 16][i % 16] = __float_as_uint(f * __uint_as_float(o[i / 16][i % 16]));
-                                tc::tmem_st16u(tO + 32 * q, o[0]);
-                                tc::tmem_st16u(tO + 32 * q + 16, o[1]);
+                                for (int i = 0; i < 16; ++i)
+                                    o[0][i] = __float_as_uint(f * __uint_as_float(o[0][i]));
+                                tc::tmem_st16u(tO + 16 * q, o[0]);
                             }
                         }
                     }
@@ -311,16 +379,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[i] = pack_bf16(y.x, y.y);
                         }
                         tc::tmem_st16u(tS + 16 * q, w);
+                        if (q == 1) {  // the first half's products may start
+                            tc::tmem_wait_st();
+                            tc::fence_before_sync();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bars.pready(s, 0));
+                        }
                     }
                     l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc::tmem_wait_st();
+                } else if (lane == 0) {
+                    mbar_arrive(bars.pready(s, 0));
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bars.pready(s));
+                if (lane == 0) mbar_arrive(bars.pready(s, 1));
             }
             if (!alive) break;
             // ---- the part's end ----
+            const int others = d->count[1 - s];
             if (steps > 0) {
                 if (!warp_wait(bars.ofull(s), no++ & 1)) {
                     alive = false;
@@ -328,49 +405,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc::fence_after_sync();
             }
-            const uint32_t qb = items & 1;
-            if (steps == 0 && others > 0 && !warp_wait(bars.qfull(qb), (items >> 1) & 1)) {
-                // (without this wait an idle stream would run ahead and release the
-                // buffer of the item after next in the other stream's stead)
-                alive = false;
-                break;
-            }
-            if (steps + others > 0) ++items;
-            float f = 1.f, f1 = 0.f;  // weights of this stream's and (DUAL) the other's O
-            if (DUAL && others > 0 && steps > 0) {
-                // join: stream 1 hands over (m, l), then O in two halves of 64 channels
-                float *box = reinterpret_cast<float *>(sm + L::kJoin);
-                if (s == 1) reinterpret_cast<float2 *>(box)[r] = make_float2(m, l);
-                named_bar(1, 256);
-                if (s == 0) {
-                    const float2 ml = reinterpret_cast<float2 *>(box)[r];
+            const bool joins = DUAL && steps > 0 && others > 0 && warp_ok;
+            if (joins) {
+                // the second stream hands over (m, l), then O in two parts of 64 channels;
+                // a barrier of the two warps of these 32 rows around each
+                float4 *const box = reinterpret_cast<float4 *>(sm + L::kJoin) + r;
+                const int join_bar = 1 + quad;
+                float f = 1.f, f1 = 0.f;
+                if (s != d->writer) *box = make_float4(m, l, 0.f, 0.f);
+                named_bar(join_bar, 64);
+                if (s == d->writer) {
+                    const float4 ml = *box;
                     const float up = fmaxf(m, ml.x);
                     f = m == -INFINITY ? 0.f : ex2((m - up) * c);
                     f1 = ml.x == -INFINITY ? 0.f : ex2((ml.x - up) * c);
                     m = up;
                     l = l * f + ml.y * f1;
                 }
-                named_bar(1, 256);
+                named_bar(join_bar, 64);
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (s == 1 && warp_ok) {
-                        uint32_t o[4][16];
-                        tc::tmem_ld_cols<4>(tO + 64 * h, o);
-                        float4 *b4 = reinterpret_cast<float4 *>(box) + r;
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t o[4][16];
+                    tc::tmem_ld_cols<4>(tO + 64 * p, o);
+                    if (s != d->writer) {
 #pragma unroll
                         for (int q = 0; q < 16; ++q)
-                            b4[128 * q] = make_float4(
+                            box[128 * q] = make_float4(
                                 __uint_as_float(o[q / 4][4 * (q % 4)]), __uint_as_float(o[q / 4][4 * (q % 4) + 1]),
                                 __uint_as_float(o[q / 4][4 * (q % 4) + 2]), __uint_as_float(o[q / 4][4 * (q % 4) + 3]));
                     }
-                    named_bar(1, 256);
-                    if (s == 0 && warp_ok) {
-                        uint32_t o[4][16];
-                        tc::tmem_ld_cols<4>(tO + 64 * h, o);
-                        const float4 *b4 = reinterpret_cast<const float4 *>(box) + r;
+                    named_bar(join_bar, 64);
+                    if (s == d->writer) {
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
-                            const float4 y = b4[128 * q];
+                            const float4 y = box[128 * q];
                             uint32_t *z = &o[q / 4][4 * (q % 4)];
                             z[0] = __float_as_uint(f * __uint_as_float(z[0]) + f1 * y.x);
                             z[1] = __float_as_uint(f * __uint_as_float(z[1]) + f1 * y.y);
@@ -378,334 +446,392 @@ __global__ void __launch_bounds__(kThreads, 1)
                             z[3] = __float_as_uint(f * __uint_as_float(z[3]) + f1 * y.w);
                         }
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) tc::tmem_st16u(tO + 64 * h + 16 * q, o[q]);
+                        for (int q = 0; q < 4; ++q) tc::tmem_st16u(tO + 64 * p + 16 * q, o[q]);
                         tc::tmem_wait_st();
                     }
-                    named_bar(1, 256);
+                    named_bar(join_bar, 64);
                 }
             }
-            const bool writes = warp_ok && (!DUAL || s == 0);
-            if (writes && !d->whole) {
-                const int slot = d->slot, row = DUAL ? r : 128 * s + r;
-                float4 *o4 = reinterpret_cast<float4 *>(part_o(a, slot)) + row;
-#pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t o[2][16];
-                    if (steps > 0) tc::tmem_ld_cols<2>(tO + 32 * q, o);
-                    if (row_ok) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                            if (steps > 0)
-                                y = make_float4(__uint_as_float(o[i / 4][4 * (i % 4)]),
-                                                __uint_as_float(o[i / 4][4 * (i % 4) + 1]),
-                                                __uint_as_float(o[i / 4][4 * (i % 4) + 2]),
-                                                __uint_as_float(o[i / 4][4 * (i % 4) + 3]));
-                            o4[(size_t)(8 * q + i) * kPartRows] = y;
-                        }
-                    }
-                }
-                if (row_ok) part_ml(a, slot)[row] = make_float2(m, l);
-            } else if (writes) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool writer = !DUAL || s == d->writer;
+            if (warp_ok && writer) {
                 const int q0 = d->q0 + (DUAL ? 0 : s * a.tile_tokens);
-                unsigned char *stage = sm + L::kQ + (DUAL ? qb : 2 * qb + s) * kTileBytes;
-                if (row_ok && a.lse != nullptr)
-                    a.lse[(size_t)(q0 + tok) * a.Hq + d->h * a.G + g] =
-                        l == 0.f ? -INFINITY : m * a.scale + logf(l);
-                if (steps == 0) {  // rows that see nothing
-                    if (row_ok) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                               ((size_t)(q0 + tok) * a.Hq + d->h * a.G + g) * kD);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
-                    }
-                } else {
+                const int row0 = d->h * a.G;
+                if (!d->whole) {
+                    const int row = DUAL ? r : 128 * s + r;
+                    float4 *o4 = reinterpret_cast<float4 *>(part_o(a, d->slot)) + row;
 #pragma unroll 1
                     for (int q = 0; q < 4; ++q) {
                         uint32_t o[2][16];
-                        tc::tmem_ld_cols<2>(tO + 32 * q, o);
+                        if (steps > 0) tc::tmem_ld_cols<2>(tO + 32 * q, o);
+                        if (row_ok) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                w[e] = pack_bf16(inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e]),
-                                                 inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e + 1]));
-                            const int ch = 4 * q + i;
-                            *reinterpret_cast<uint4 *>(stage + r * 256 + ((ch ^ (r & 15)) * 16)) =
-                                make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int i = 0; i < 8; ++i) {
+                                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                                if (steps > 0)
+                                    y = make_float4(__uint_as_float(o[i / 4][4 * (i % 4)]),
+                                                    __uint_as_float(o[i / 4][4 * (i % 4) + 1]),
+                                                    __uint_as_float(o[i / 4][4 * (i % 4) + 2]),
+                                                    __uint_as_float(o[i / 4][4 * (i % 4) + 3]));
+                                o4[(size_t)(8 * q + i) * kPartRows] = y;
+                            }
                         }
                     }
-                    __syncwarp();
-                    // 16 lanes write one row of 256 bytes
-                    const int rows = tokens * a.G;
-                    for (int i = lane >> 4; i < 32; i += 2) {
-                        const int row = 32 * (warp & 3) + i;
-                        if (row >= rows) break;
-                        const int ch = lane & 15, tk = row / a.G;
-                        const uint4 y = *reinterpret_cast<const uint4 *>(stage + row * 256 + ((ch ^ (row & 15)) * 16));
-                        reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                  ((size_t)(q0 + tk) * a.Hq + d->h * a.G + (row - tk * a.G)) * kD)[ch] = y;
+                    if (row_ok) part_ml(a, d->slot)[row] = make_float2(m, l);
+                } else {
+                    if (row_ok && a.lse != nullptr)
+                        a.lse[(size_t)(q0 + tok) * a.Hq + row0 + g] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+                    __nv_bfloat16 *const out = static_cast<__nv_bfloat16 *>(a.out);
+                    if (steps == 0) {  // rows that see nothing
+                        if (row_ok) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)(q0 + tok) * a.Hq + row0 + g) * kD);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+                        }
+                    } else {
+                        // through this stream's Q tile: its products are done
+                        unsigned char *stage = sm + L::kQ + d->q[s] % L::kQs * kTileBytes;
+                        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            uint32_t o[2][16];
+                            tc::tmem_ld_cols<2>(tO + 32 * q, o);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    w[e] = pack_bf16(inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e]),
+                                                     inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e + 1]));
+                                *reinterpret_cast<uint4 *>(stage + r * 256 + (((4 * q + i) ^ (r & 15)) * 16)) =
+                                    make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                        __syncwarp();
+                        // sixteen lanes write a row's 256 bytes
+                        const int rows = d->tokens[s] * a.G, ch = lane & 15;
+#pragma unroll 4
+                        for (int i = 0; i < 32; i += 2) {
+                            const int row = 32 * quad + i + (lane >> 4), tk = row / a.G;
+                            const uint4 y = *reinterpret_cast<const uint4 *>(stage + row * 256 + ((ch ^ (row & 15)) * 16));
+                            if (row < rows)
+                                reinterpret_cast<uint4 *>(out + ((size_t)(q0 + tk) * a.Hq + row0 + (row - tk * a.G)) * kD)[ch] = y;
+                        }
                     }
                 }
             }
             // O is read: the MMA warp's next P V waits for this warp's next P.
-            // The Q buffer (the staging's too) goes back to the TMA warp.
+            // The Q tile (the staging's too) goes back to the TMA warp.
             tc::fence_before_sync();
-            if (steps + others > 0) {
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.qempty(qb));
-            }
+            tc::fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
+            if (lane == 0) {
+                if (steps > 0 && writer) mbar_arrive(bars.qempty(d->q[s] % L::kQs));
+                mbar_arrive(bars.dempty(nd % kDescs));
+            }
             ++nd;
         }
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;\n");
-        if (warp == 10) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
+        if (warp == kWarpSched) {
             // ---- scheduler warp ---------------------------------------------------
             Point p0, p1;
-            const bool any = split_points<PAGED>(a, cta, p0, p1);
+            Seq s0;
+            const bool any = split_points<PAGED, kTile>(a, cta, p0, p1, s0);
             if (lane == 0) {
                 part_header(a, 2 * cta)->valid = 0;
                 part_header(a, 2 * cta + 1)->valid = 0;
-                Walk<PAGED> walk;
-                Part p;
-                if (any) walk.init(p0, p1);
-                bool more = true;
-                while (more && alive) {
-                    if (nd >= kDescs) alive = tc::mbar_wait(bars.dempty(nd % kDescs), (nd / kDescs - 1) & 1, kWaitNs);
-                    if (!alive) break;
+            }
+            Walk<PAGED, kTile> walk;
+            Part p;
+            if (any) walk.init(p0, p1, s0);
+            Run run = {0, 0};
+            bool more = true;
+            while (more) {
+                if (nd >= kDescs && !(alive = long_wait(bars.dempty(nd % kDescs), (nd / kDescs - 1) & 1))) break;
+                more = any && walk.next(a, p);
+                if (lane == 0) {
                     Desc *d = const_cast<Desc *>(descs) + nd % kDescs;
-                    more = any && walk.next(a, p);
                     if (more) {
-                        describe<PAGED, DUAL>(a, p, cta, *d);
-                        if (!d->whole) {
-                            PartHeader *h = part_header(a, d->slot);
-                            h->ends = d->ends;
-                            h->token0 = p.q0;
-                            h->tokens = p.tokens;
-                            h->kvh = p.h;
-                            h->valid = 1;
-                        }
+                        describe<PAGED, DUAL>(a, p, cta, run, *d);
                     } else {
                         d->last = 1;
                     }
-                    mbar_arrive(bars.dfull(nd++ % kDescs));
+                    mbar_arrive(bars.dfull(nd % kDescs));
+                    if (more && !p.whole()) {
+                        PartHeader *h = part_header(a, part_slot(cta, p));
+                        h->ends = p.tb == p.nt;
+                        h->token0 = p.q0;
+                        h->tokens = p.tokens;
+                        h->kvh = p.h;
+                        h->valid = 1;
+                    }
                 }
+                ++nd;
             }
-        } else if (warp == 9) {
+        } else if (warp == kWarpTma) {
             // ---- TMA warp ------------------------------------------------------
-            const int G = a.G;
-            uint32_t kv = 0, items = 0, tails = 0;
-            const uint32_t qbytes = (uint32_t)a.tile_tokens * G * 256u;
-            // one K (is_v = false) or V tile into the next ring slot
-            auto load = [&](const Desc &pt, int t, bool is_v) {
+            // K tile g, then V tile g - kLag: in the order in which the products take
+            // them, through the ends of parts.
+            constexpr int kLag = DUAL ? 2 : 1;
+            struct Load {
+                int n, h, k0, Lk, t, draft, pg;
+            };
+            uint32_t kv = 0, jobs = 0, g = 0;
+            const uint32_t qbytes = (uint32_t)(a.tile_tokens * a.G) * 256u;
+            const int rows = a.page < kTile ? a.page : kTile;  // decode: rows of one copy
+            // decode: the page of this lane's copy of tile t
+            auto page_of = [&](int n, int Lk, int t) -> int {
+                const int pos = t * kTile + lane * rows;
+                if (!PAGED || lane * rows >= kTile || pos >= Lk) return -1;
+                return __ldg(a.table + (size_t)n * a.table_ld + pos / a.page);
+            };
+            auto load = [&](const Load &x, bool is_v) {
                 const uint32_t slot = kv % L::kRing;
                 const uint32_t dst = base + L::kKv + slot * kTileBytes;
-                if (kv >= (uint32_t)L::kRing &&
-                    !warp_wait(bars.kvempty(slot), (kv / L::kRing - 1) & 1)) {
+                if (kv >= (uint32_t)L::kRing && !warp_wait(bars.kvempty(slot), (kv / L::kRing - 1) & 1)) {
                     alive = false;
                     return;
                 }
                 ++kv;
-                int valid;  // rows of this tile that are the sequence's own
-                bool drafts = false;
-                if (PAGED) {
-                    drafts = a.has_new && t == pt.nt - 1;
-                    valid = drafts ? a.T : pt.Lk - t * kTile;
-                } else {
-                    valid = pt.Lk - t * kTile;
-                }
-                valid = valid < kTile ? valid : kTile;
+                // rows of this tile that are the sequence's own
+                const int left = x.draft ? a.T : x.Lk - x.t * kTile, valid = left < kTile ? left : kTile;
                 // rows past the end hold other sequences' values or nothing at all:
                 // P is 0 there, but 0 times a NaN is not, so V gets zeros
                 const bool fix = is_v && valid < kTile;
-                const uint32_t bar = fix ? bars.tail() : bars.kvfull(slot);
+                const uint32_t bar = fix ? bars.vraw(slot) : bars.kvfull(slot);
                 if (!PAGED) {
                     if (lane == 0) {
                         const CUtensorMap *m = is_v ? &maps.v : &maps.k;
                         tc::mbar_arrive_expect_tx(bar, kTileBytes);
-                        tma_3d(dst, m, 0, pt.h, pt.k0 + t * kTile, bar);
-                        tma_3d(dst + kHalf, m, 64, pt.h, pt.k0 + t * kTile, bar);
+                        tma_3d(dst, m, 0, x.h, x.k0 + x.t * kTile, bar);
+                        tma_3d(dst + kHalf, m, 64, x.h, x.k0 + x.t * kTile, bar);
                     }
-                } else if (drafts) {
+                } else if (x.draft) {
                     if (lane == 0) {
                         const CUtensorMap *m = is_v ? &maps.vn : &maps.kn;
                         tc::mbar_arrive_expect_tx(bar, 64 * 256);
-                        tma_3d(dst, m, 0, pt.h, pt.n * a.T, bar);
-                        tma_3d(dst + kHalf, m, 64, pt.h, pt.n * a.T, bar);
+                        tma_3d(dst, m, 0, x.h, x.n * a.T, bar);
+                        tma_3d(dst + kHalf, m, 64, x.h, x.n * a.T, bar);
                     }
                 } else {
-                    const int rows = a.page < kTile ? a.page : kTile;  // rows of one copy
                     const int copies = (valid + rows - 1) / rows;
-                    if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)copies * rows * 256u);
+                    if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(copies * rows) * 256u);
                     __syncwarp();
                     if (lane < copies) {
                         const CUtensorMap *m = is_v ? &maps.v : &maps.k;
-                        const int pos = t * kTile + lane * rows;
-                        const int pg = a.table[(size_t)pt.n * a.table_ld + pos / a.page];
-                        int row;
-                        if (pg < 0 || pg >= a.pages) {  // zeros instead (past the pool's last row)
+                        int row = a.pages * a.Hkv * a.page;  // past the pool's last row: zeros
+                        if (x.pg >= 0 && x.pg < a.pages)
+                            row = (x.pg * a.Hkv + x.h) * a.page + (x.t * kTile + lane * rows) % a.page;
+                        else
                             atomicOr(status_word(a), kStatusBadSeqlens);
-                            row = a.pages * a.Hkv * a.page;
-                        } else {
-                            row = (pg * a.Hkv + pt.h) * a.page + pos % a.page;
-                        }
                         tma_2d(dst + lane * rows * 128, m, 0, row, bar);
                         tma_2d(dst + kHalf + lane * rows * 128, m, 64, row, bar);
                     }
                 }
-                if (fix) {
-                    __syncwarp();
-                    if (!warp_wait(bars.tail(), tails++ & 1)) {
-                        alive = false;
-                        return;
-                    }
-                    for (int r = valid + (lane >> 3); r < kTile; r += 4) {
-                        const uint32_t at = L::kKv + slot * kTileBytes + r * 128 + (lane & 7) * 16;
-                        *reinterpret_cast<uint4 *>(sm + at) = make_uint4(0, 0, 0, 0);
-                        *reinterpret_cast<uint4 *>(sm + at + kHalf) = make_uint4(0, 0, 0, 0);
-                    }
-                    tc::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.kvfull(slot));
+                if (fix && lane == 0) {  // the fixing warp waits for the copy and hands the slot on
+                    int2 *job = reinterpret_cast<int2 *>(sm + L::kBars + Bars::kJobs) + jobs % kJobRing;
+                    *job = make_int2((int)slot, valid);
+                    mbar_arrive(bars.jfull(jobs % kJobRing));
+                }
+                if (fix) ++jobs;
+                __syncwarp();
+            };
+            auto load_q = [&](int i, int tok, int h) {
+                const uint32_t slot = (uint32_t)i % L::kQs, use = (uint32_t)i / L::kQs;
+                if (use > 0 && !warp_wait(bars.qempty(slot), (use - 1) & 1)) {
+                    alive = false;
+                    return;
+                }
+                if (lane == 0) {
+                    const uint32_t dst = base + L::kQ + slot * kTileBytes, bar = bars.qfull(slot);
+                    tc::mbar_arrive_expect_tx(bar, qbytes);
+                    tma_3d(dst, &maps.q, 0, h * a.G, tok, bar);
+                    tma_3d(dst + kHalf, &maps.q, 64, h * a.G, tok, bar);
                 }
                 __syncwarp();
             };
+            Load x1, x2;  // the last two K tiles
+            x1.pg = x2.pg = -1;
             while (const Desc *d = next_desc()) {
-                const int n0 = d->count[0], n1 = d->count[1];
-                if (n0 + n1 > 0) {
-                    const uint32_t qb = items & 1;
-                    if (items >= 2 && !warp_wait(bars.qempty(qb), ((items >> 1) - 1) & 1)) {
-                        alive = false;
-                        break;
-                    }
-                    ++items;
-                    if (lane == 0) {
-                        const int tiles = DUAL ? 1 : (d->tokens[1] > 0 ? 2 : 1);
-                        tc::mbar_arrive_expect_tx(bars.qfull(qb), tiles * qbytes);
-                        for (int i = 0; i < tiles; ++i) {
-                            const uint32_t dst = base + L::kQ + (DUAL ? qb : 2 * qb + i) * kTileBytes;
-                            const int tok = d->q0 + i * a.tile_tokens;
-                            tma_3d(dst, &maps.q, 0, d->h * G, tok, bars.qfull(qb));
-                            tma_3d(dst + kHalf, &maps.q, 64, d->h * G, tok, bars.qfull(qb));
-                        }
-                    }
-                    __syncwarp();
-                    // In the order in which the MMA warp takes them: one K tile ahead of
-                    // the V tiles (DUAL: one of each stream).
-                    const int tiles = DUAL ? n0 + n1 : (n0 > n1 ? n0 : n1), ahead = DUAL ? 2 : 1;
-                    for (int j = 0; j < tiles + ahead && alive; ++j) {
-                        if (j >= ahead) load(*d, d->ta + j - ahead, true);
-                        if (alive && j < tiles) load(*d, d->ta + j, false);
-                    }
+                const int c0 = d->count[0], c1 = d->count[1];
+                const int tiles = DUAL ? c0 + c1 : (c0 > c1 ? c0 : c1);
+                Load x;
+                x.n = d->n;
+                x.h = d->h;
+                x.k0 = d->k0;
+                x.Lk = d->Lk;
+                const int ta = d->ta, draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
+                int next_pg = page_of(x.n, x.Lk, ta), next_pg2 = page_of(x.n, x.Lk, ta + 1);
+                for (int j = 0; j < tiles && alive; ++j, ++g) {
+                    x.t = ta + j;
+                    x.draft = PAGED && x.t == draft_tile;
+                    x.pg = next_pg;  // looked up two tiles ahead
+                    next_pg = next_pg2;
+                    next_pg2 = page_of(x.n, x.Lk, x.t + 2);
+                    if (g >= (uint32_t)kLag) load(DUAL ? x2 : x1, true);
+                    if (j == 0 && alive && (DUAL || c0 > 0)) load_q(d->q[0], d->q0, x.h);
+                    if (alive) load(x, false);
+                    if (!DUAL && j == 0 && alive && c1 > 0) load_q(d->q[1], d->q0 + a.tile_tokens, x.h);
+                    x2 = x1;
+                    x1 = x;
                 }
+                if (!alive) break;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
                 ++nd;
             }
-        } else if (warp == 8) {
-            // ---- MMA warp (one thread) -------------------------------------------
-            if (lane == 0) {
-                constexpr uint32_t kIdQK = tc::idesc_f16(128, 128, 0, 0, 0);
-                constexpr uint32_t kIdPV = tc::idesc_f16(128, 128, 0, 0, 1);
-                uint32_t kv = 0, items = 0, np[2] = {0, 0};
-                auto wait_kv = [&](uint32_t at) {
+            if (DUAL && alive && g >= 2) load(x2, true);
+            if (alive && g >= 1) load(x1, true);
+            if (lane == 0) {  // no further job
+                reinterpret_cast<int2 *>(sm + L::kBars + Bars::kJobs)[jobs % kJobRing] = make_int2(-1, 0);
+                mbar_arrive(bars.jfull(jobs % kJobRing));
+            }
+        } else if (warp == kWarpFix) {
+            // ---- fixing warp: zeros in the V rows past a sequence's end ----------------
+            uint32_t fixed = 0;
+            for (uint32_t jobs = 0;; ++jobs) {
+                if (!(alive = long_wait(bars.jfull(jobs % kJobRing), (jobs / kJobRing) & 1))) break;
+                const int2 job = reinterpret_cast<const int2 *>(sm + L::kBars + Bars::kJobs)[jobs % kJobRing];
+                const int slot = job.x;
+                if (slot < 0) break;
+                // the slot's V copies that end here: one phase of vraw each
+                if (!(alive = warp_wait(bars.vraw(slot), (fixed >> slot) & 1))) break;
+                fixed ^= 1u << slot;
+                for (int r = job.y + (lane >> 3); r < kTile; r += 4) {
+                    const uint32_t at = L::kKv + slot * kTileBytes + r * 128 + (lane & 7) * 16;
+                    *reinterpret_cast<uint4 *>(sm + at) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(sm + at + kHalf) = make_uint4(0, 0, 0, 0);
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.kvfull(slot));
+            }
+        } else {
+            // ---- MMA warp: the whole warp walks along, one lane issues --------------
+            constexpr uint32_t kIdQK = tc::idesc_f16(128, 128, 0, 0, 0);
+            constexpr uint32_t kIdPV = tc::idesc_f16(128, 128, 0, 0, 1);
+            const uint32_t lead = tc::elect_one();
+            const uint64_t q_desc = tc::smem_desc_sw128(base + L::kQ, 16, 1024);
+            const uint64_t k_desc = tc::smem_desc_sw128(base + L::kKv, 16, 1024);
+            const uint64_t v_desc = tc::smem_desc_sw128(base + L::kKv, kHalf, 1024);
+            uint32_t kv = 0, np0 = 0, np1 = 0;
+            auto wait_kv = [&](uint32_t at) {
+                if (alive) alive = warp_wait(bars.kvfull(at % L::kRing), (at / L::kRing) & 1);
+            };
+            auto free_kv = [&](uint32_t at) { tc::mma_commit_lead(lead, bars.kvempty(at % L::kRing)); };
+            // S_s = Q K^T with Q tile i; then the row tile's softmax may read it
+            auto qk = [&](int s, int i, bool first, uint32_t at) {
+                const uint32_t slot = (uint32_t)i % L::kQs;
+                if (first && alive) alive = warp_wait(bars.qfull(slot), ((uint32_t)i / L::kQs) & 1);
+                if (!alive) return;
+                const uint64_t qd = q_desc + slot * (kTileBytes >> 4);
+                const uint64_t kd = k_desc + (at % L::kRing) * (kTileBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+                    tc::mma_f16_lead(lead, tm + kColS + 128 * s, qd + off, kd + off, kIdQK, kk > 0);
+                }
+                tc::mma_commit_lead(lead, bars.sfull(s));
+            };
+            // O_s (+)= P V, each half of the keys once its P is there
+            auto pv = [&](int s, uint32_t at, bool first, bool last) {
+                const uint64_t vd = v_desc + (at % L::kRing) * (kTileBytes >> 4);
+                const uint32_t parity = (s ? np1++ : np0++) & 1;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (alive) alive = warp_wait(bars.pready(s, half), parity);
                     if (!alive) return;
-                    alive = tc::mbar_wait(bars.kvfull(at % L::kRing), (at / L::kRing) & 1, kWaitNs);
-                };
-                auto qk = [&](int s, uint32_t qb, uint32_t at) {
-                    const uint32_t qa = base + L::kQ + (DUAL ? qb : 2 * qb + s) * kTileBytes;
-                    const uint32_t ka = base + L::kKv + (at % L::kRing) * kTileBytes;
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-                        tc::mma_f16(tm + kColS + 128 * s, tc::smem_desc_sw128(qa + off, 16, 1024),
-                                    tc::smem_desc_sw128(ka + off, 16, 1024), kIdQK, kk > 0);
-                    }
-                    tc::mma_commit(bars.sfull(s));
-                };
-                auto pv = [&](int s, uint32_t at, bool first) {
-                    const uint32_t va = base + L::kKv + (at % L::kRing) * kTileBytes;
-                    for (int kk = 0; kk < 8; ++kk)
-                        tc::mma_f16_ta(tm + kColO + 128 * s, tm + kColS + 128 * s + 8 * kk,
-                                       tc::smem_desc_sw128(va + kk * 2048, kHalf, 1024), kIdPV,
-                                       !first || kk > 0);
-                };
-                auto free_kv = [&](uint32_t at) { tc::mma_commit(bars.kvempty(at % L::kRing)); };
-                auto wait_p = [&](int s) {
-                    if (!alive) return;
-                    alive = tc::mbar_wait(bars.pready(s), np[s]++ & 1, kWaitNs);
                     tc::fence_after_sync();
+#pragma unroll
+                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                        tc::mma_f16_ta_lead(lead, tm + kColO + 128 * s, tm + kColS + 128 * s + 8 * kk,
+                                            vd + ((kk * 2048) >> 4), kIdPV, !first || kk > 0);
+                }
+                if (last) tc::mma_commit_lead(lead, bars.ofull(s));
+            };
+            if (!DUAL) {
+                // step g: per stream, P V of step g - 1, then Q K^T of step g (of the next
+                // part when the last one is through: its S is there when its O is read)
+                int n0 = 0, n1 = 0, at_j = -1;  // of step g - 1
+                while (alive) {
+                    const Desc *d = next_desc();
+                    if (!alive) break;
+                    int c0 = 0, c1 = 0, q0 = 0, q1 = 0;
+                    if (d != nullptr) {
+                        c0 = d->count[0];
+                        c1 = d->count[1];
+                        q0 = d->q[0];
+                        q1 = d->q[1];
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
+                        ++nd;
+                        if (c0 + c1 == 0) continue;
+                    }
+                    const int n = d == nullptr ? 1 : (c0 > c1 ? c0 : c1);
+                    for (int j = 0; j < n && alive; ++j) {
+                        const uint32_t v = kv, k = kv + (at_j >= 0);
+                        kv = k + (d != nullptr);
+                        if (at_j >= 0) wait_kv(v);
+                        bool waited = false;
+#pragma unroll
+                        for (int s = 0; s < 2; ++s) {
+                            const int before = s ? n1 : n0, now = s ? c1 : c0;
+                            if (at_j >= 0 && at_j < before) pv(s, v, at_j == 0, at_j + 1 == before);
+                            if (j < now) {
+                                if (!waited) wait_kv(k);
+                                waited = true;
+                                qk(s, s ? q1 : q0, j == 0, k);
+                            }
+                        }
+                        if (!alive) break;
+                        if (at_j >= 0) free_kv(v);
+                        if (d != nullptr) free_kv(k);
+                        at_j = j;
+                        n0 = c0;
+                        n1 = c1;
+                    }
+                    if (d == nullptr) break;
+                }
+            } else {
+                // tile g is stream g % 2's: its P V of tile g - 2, then Q K^T of tile g
+                uint32_t g = 0;
+                bool first[2] = {true, true}, last[2] = {false, false};
+                auto finish = [&](int s) {
+                    const uint32_t v = kv++;
+                    wait_kv(v);
+                    pv(s, v, first[s], last[s]);
+                    if (alive) free_kv(v);
                 };
                 while (const Desc *d = next_desc()) {
-                    const int n0 = d->count[0], n1 = d->count[1];
-                    free_desc();
-                    if (n0 + n1 == 0) continue;
-                    const int n = n0 > n1 ? n0 : n1;
-                    const uint32_t qb = items & 1;
-                    alive = tc::mbar_wait(bars.qfull(qb), (items >> 1) & 1, kWaitNs);
-                    ++items;
-                    if (!DUAL) {
-                        wait_kv(kv);
-                        if (!alive) break;
-                        if (n0 > 0) qk(0, qb, kv);
-                        if (n1 > 0) qk(1, qb, kv);
-                        free_kv(kv++);
-                        for (int j = 0; j < n && alive; ++j) {
-                            const uint32_t v = kv++;
-                            const bool more = j + 1 < n;
-                            const uint32_t k = more ? kv++ : 0;
-                            wait_kv(v);
-                            for (int s = 0; s < 2; ++s) {
-                                const int ns = s ? n1 : n0;
-                                if (j < ns) {
-                                    wait_p(s);
-                                    if (!alive) break;
-                                    pv(s, v, j == 0);
-                                    if (j + 1 == ns) tc::mma_commit(bars.ofull(s));
-                                }
-                                if (j + 1 < ns) {
-                                    if (s == 0 || n0 <= j + 1) wait_kv(k);
-                                    if (!alive) break;
-                                    qk(s, qb, k);
-                                }
-                            }
-                            free_kv(v);
-                            if (more) free_kv(k);
-                        }
-                    } else {
-                        // tiles 0, 1, 2, .. go to streams 0, 1, 0, ..; K runs two tiles ahead of V
-                        const int tiles = n0 + n1;
-                        for (int j = 0; j < tiles + 2 && alive; ++j) {
-                            const int s = j & 1;
-                            if (j >= 2) {
-                                wait_kv(kv);
-                                wait_p(s);
-                                if (!alive) break;
-                                pv(s, kv, j < 4);
-                                if (j >= tiles) tc::mma_commit(bars.ofull(s));
-                                free_kv(kv++);
-                            }
-                            if (j < tiles) {
-                                wait_kv(kv);
-                                if (!alive) break;
-                                qk(s, qb, kv);
-                                free_kv(kv++);
-                            }
-                        }
+                    const int tiles = d->count[0] + d->count[1], q = d->q[0];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
+                    ++nd;
+                    for (int j = 0; j < tiles && alive; ++j, ++g) {
+                        const int s = g & 1;
+                        if (g >= 2) finish(s);
+                        const uint32_t k = kv++;
+                        wait_kv(k);
+                        qk(s, q, j < 2, k);
+                        if (alive) free_kv(k);
+                        first[s] = j < 2;
+                        last[s] = j + 2 >= tiles;
                     }
+                    if (!alive) break;
                 }
+                if (alive && g >= 2) finish(g & 1);
+                if (alive && g >= 1) finish((g + 1) & 1);
             }
         }
     }
     __syncwarp();
-    if (!alive && lane == 0) atomicOr(status_word(a), kStatusTimeout);
+    if (!alive && lane == 0) {
+        *dead = 1;
+        atomicOr(status_word(a), kStatusTimeout);
+    }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == 10) tc::tmem_dealloc(tm, 512);
+    if (warp == kWarpFix) tc::tmem_dealloc(tm, 512);
 }
 
 // ---- host -----------------------------------------------------------------
@@ -748,11 +874,11 @@ cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
 
 cudaError_t launch_attn_prefill_tc(Args a, const void *q, const void *k, const void *v, long long ldq,
                                    long long ldk, long long ldv, cudaStream_t stream) {
-    a.kt = kTile;
     a.tile_tokens = kTile / a.G;
     a.streams = 2;
     a.extra = 256;
-    a.min_part = 768;
+    a.min_part = 384;
+    a.cut = 4;
     Maps m{};
     if (!map3(&m.q, q, a.Hq, a.Tq_total, ldq, a.G, a.tile_tokens) ||
         !map3(&m.k, k, a.Hkv, a.Tk_total, ldk, 1, kTile) ||
@@ -766,11 +892,11 @@ cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const v
                                   const void *vn, long long ldq, long long ldk, long long ldv,
                                   cudaStream_t stream) {
     const bool dual = a.T * a.G <= kTile;
-    a.kt = kTile;
     a.streams = dual ? 1 : 2;
     a.tile_tokens = dual ? a.T : kTile / a.G;
     a.extra = 256;
-    a.min_part = 768;
+    a.min_part = 384;
+    a.cut = 4;
     const long long rows = (long long)a.pages * a.Hkv * a.page, toks = (long long)a.N * a.T;
     Maps m{};
     if (!map3(&m.q, q, a.Hq, toks, ldq, a.G, a.tile_tokens) ||
