@@ -157,13 +157,13 @@ def kda_status_string(code: int) -> str:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream_ptr(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream_ptr(stream) -> int:
+    if stream is None:  # (the raw handle: a torch.cuda.Stream object takes 3 us to make)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _io_code(dt: torch.dtype) -> int:
@@ -456,19 +456,17 @@ def _rows_ld(t: torch.Tensor, name: str) -> int:
     H, D = t.shape[-2:]
     if not t.is_cuda:
         raise ValueError("KDA tensors must be CUDA tensors")
-    if D > 1 and t.stride(-1) != 1 or H > 1 and t.stride(-2) != D:
+    st = t.stride()
+    if D > 1 and st[-1] != 1 or H > 1 and st[-2] != D:
         raise ValueError("%s: the [heads, D] rows must be contiguous" % name)
-    tokens = t.numel() // max(H * D, 1)
-    if tokens <= 1:
-        return H * D
     if t.dim() == 3:
-        return t.stride(0)
+        return st[0] if t.shape[0] > 1 else H * D
     B, T = t.shape[:2]
     if T == 1:
-        return t.stride(0)
-    if B > 1 and t.stride(0) != T * t.stride(1):
+        return st[0] if B > 1 else H * D
+    if B > 1 and st[0] != T * st[1]:
         raise ValueError("%s: the tokens must be evenly spaced" % name)
-    return t.stride(1)
+    return st[1]
 
 
 def _same(name, ref: torch.Tensor, *ts, dtype=None):

@@ -14,8 +14,11 @@
 // [U c / C, U (c + 1) / C) of it, cut at key tiles. So every CTA has the same
 // load whatever the lengths are, one long sequence spreads over all SMs, and a
 // CTA has at most two parts of items: its first (which starts inside an item)
-// and its last (which ends inside one). Those write (O, m, l) to the workspace
-// and the join kernel adds them up in CTA order; all others write their rows.
+// and its last (which ends inside one). Those write (O, m, l) to the workspace and
+// the join kernel adds them up in CTA order; all others write their rows. (A join by
+// the CTA that finishes an item last saves a launch, 4 us of host time, but one SM
+// waits for all the parts' loads: 5 to 20 us more on calls with many parts.) Few and
+// short items go to a CTA each (`direct`), without the search and without a join.
 #pragma once
 
 #include <stdint.h>
@@ -28,6 +31,8 @@ namespace attn {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPartRows = 256;  // rows of a part in the workspace
 constexpr int kMaxDrafts = 64;  // a row's draft mask has 64 bits
+// Keys of work (an item's start and end included) below which no further CTA is used.
+constexpr int kTcMinPart = 384, kF32MinPart = 128;
 
 // Workspace: status word and padding, the parts' headers, then per part slot
 // O (fp32, [32 channel quads][256 rows][4]) and m, l ([256] each).
@@ -65,6 +70,7 @@ struct Args {
     int extra;               // an item's start and end, in keys
     int min_part;            // keys of work below which no further CTA is used
     int cut;                 // tiles that a part of an item has at least
+    int direct;              // one CTA for each slot of an item, nothing is split
     float scale;
     // device pointers
     const int32_t *cu_q, *cu_k;      // prefill offsets (NULL: equal lengths)
@@ -72,8 +78,8 @@ struct Args {
     const unsigned long long *mask;  // decode, NULL: the chain
     void *out;
     float *lse;
-    unsigned char *ws;               // NULL: no part is ever split (one CTA)
-    int ctas;
+    unsigned char *ws;
+    int ctas, sms;           // CTAs that share the work; SMs of the device
 };
 
 __device__ __forceinline__ uint32_t *status_word(const Args &a) {
@@ -290,6 +296,67 @@ struct Part {
     int Lq, Lk, k0;
     __device__ __forceinline__ bool whole() const { return ta == 0 && tb == nt; }
 };
+template <bool PAGED, int KT>
+__device__ __forceinline__ void item_part(const Args &a, const Seq &s, Part &p) {
+    const int block = a.tile_tokens * a.streams;
+    p.nt = item_tiles<PAGED, KT>(a, s, p.i);
+    p.first_tok = p.i * block;
+    p.q0 = s.q0 + p.first_tok;
+    p.tokens = min(block, s.Lq - p.first_tok);
+    p.Lq = s.Lq;
+    p.Lk = s.Lk;
+    p.k0 = s.k0;
+}
+
+// `direct`: the item of slot x, whole. A head's slots: those of sequence n start at
+// (its first token) / block + n, which leaves each sequence at least as many slots
+// as it has items. A converged warp. False: an empty slot or malformed offsets.
+template <bool PAGED, int KT>
+__device__ __forceinline__ bool direct_part(const Args &a, int x, Part &p) {
+    const int lane = threadIdx.x & 31, block = a.tile_tokens * a.streams;
+    Seq s;
+    bool good = true;
+    if (PAGED) {
+        const int ni = (a.T + block - 1) / block;
+        p.i = x % ni;
+        p.h = x / ni % a.Hkv;
+        p.n = x / ni / a.Hkv;
+        good = load_seq<PAGED>(a, p.n, s);
+    } else {
+        const int slots = a.Tq_total / block + a.N;
+        p.h = x / slots;
+        const int slot = x - p.h * slots;
+        p.n = -1;
+        for (int n0 = 0; n0 < a.N; n0 += 32) {
+            Seq t;
+            bool here = false;
+            if (n0 + lane < a.N) {
+                good = load_seq<PAGED>(a, n0 + lane, t) && good;
+                here = t.q0 / block + n0 + lane <= slot;
+            }
+            const unsigned who = __ballot_sync(0xffffffffu, here);
+            if (who == 0) continue;
+            const int src = 31 - __clz(who);
+            p.n = n0 + src;
+            s.q0 = __shfl_sync(0xffffffffu, t.q0, src);
+            s.Lq = __shfl_sync(0xffffffffu, t.Lq, src);
+            s.k0 = __shfl_sync(0xffffffffu, t.k0, src);
+            s.Lk = __shfl_sync(0xffffffffu, t.Lk, src);
+            s.ni = __shfl_sync(0xffffffffu, t.ni, src);
+        }
+        good = __all_sync(0xffffffffu, good);
+        p.i = slot - (s.q0 / block + p.n);
+    }
+    if (!good) {
+        if (lane == 0) atomicOr(status_word(a), kStatusBadSeqlens);
+        return false;
+    }
+    if (p.n < 0 || p.i >= s.ni) return false;
+    item_part<PAGED, KT>(a, s, p);
+    p.ta = 0;
+    p.tb = p.nt;
+    return true;
+}
 
 // Walks the parts of [at, end). Every role of a CTA walks them alike.
 template <bool PAGED, int KT>
@@ -315,19 +382,12 @@ struct Walk {
                 at.h = at.i = at.tile = 0;
                 continue;
             }
-            const int block = a.tile_tokens * a.streams;
             p.n = at.n;
             p.h = at.h;
             p.i = at.i;
-            p.nt = item_tiles<PAGED, KT>(a, s, at.i);
+            item_part<PAGED, KT>(a, s, p);
             p.ta = at.tile;
             p.tb = same_item(at, end) ? end.tile : p.nt;
-            p.first_tok = at.i * block;
-            p.q0 = s.q0 + p.first_tok;
-            p.tokens = min(block, s.Lq - p.first_tok);
-            p.Lq = s.Lq;
-            p.Lk = s.Lk;
-            p.k0 = s.k0;
             if (same_item(at, end)) {
                 at.tile = end.tile;
             } else {
@@ -347,6 +407,7 @@ struct Walk {
 };
 // The workspace slot of CTA c's unfinished part.
 __device__ __forceinline__ int part_slot(int c, const Part &p) { return 2 * c + (p.ta == 0); }
+
 
 }  // namespace attn
 }  // namespace kda

@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include <nvtx3/nvToolsExt.h>
 
 #include "kda.h"
@@ -48,7 +50,7 @@ using kda::attn::Args;
 
 constexpr int kMaxGroup = 64;
 constexpr int kMaxTokens = kda::attn::kMaxDrafts;
-constexpr size_t kHeader = kda::attn::kWsHeader;
+constexpr size_t kHeader = 256;  // of a cache workspace: the status word
 
 struct Range {
     explicit Range(const char *name) { nvtxRangePushA(name); }
@@ -59,18 +61,21 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 int done(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
 
 int sm_count() {
+    static std::atomic<int> known[64];
     int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    const bool any = cudaGetDevice(&dev) == cudaSuccess;
+    if (any && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+    if (!any || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();  // no device: sizes for a full GB300
         return 152;
     }
+    if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
     return n;
 }
 // CTAs of one attention call: all that fit on the device at once, fewer when
 // an upper bound of the work (in keys) cannot fill them.
 int attn_ctas(int32_t io, long long keys) {
-    const long long most = (io == KDA_F32 ? 2LL : 1LL) * sm_count(), part = io == KDA_F32 ? 128 : 384;
+    const long long most = (io == KDA_F32 ? 2LL : 1LL) * sm_count(), part = io == KDA_F32 ? kda::attn::kF32MinPart : kda::attn::kTcMinPart;
     const long long n = keys / part;
     return (int)(n < 1 ? 1 : (n < most ? n : most));
 }
@@ -141,6 +146,7 @@ int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, i
     a.G = Hq / Hkv;
     a.T = Tq;
     a.Tk = Tk;
+    a.sms = sm_count();
     a.Tq_total = (int)tq;
     a.Tk_total = (int)tk;
     a.scale = scale;
@@ -196,6 +202,7 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
     a.G = Hq / Hkv;
     a.T = T;
     a.page = page_size;
+    a.sms = sm_count();
     a.pages = num_pages;
     a.table_cols = table_cols;
     a.table_ld = table_ld;

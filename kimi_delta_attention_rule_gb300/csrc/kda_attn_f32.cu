@@ -34,37 +34,46 @@ struct F32Ptrs {
 };
 
 template <bool PAGED>
-__global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const Args a, const F32Ptrs io) {
+__global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_constant__ Args a, const F32Ptrs io) {
     extern __shared__ __align__(16) float smf[];
     float *const Qs = smf, *const Ks = smf + kF32Tile * kPitch, *const Vs = smf + 2 * kF32Tile * kPitch;
     float *const Ps = Ks;  // P replaces K once S is formed
     __shared__ Point pts[2];
     __shared__ Seq seq0;
     __shared__ int any;
-    const int tid = threadIdx.x, cta = blockIdx.x;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    const int tid = threadIdx.x, cta = blockIdx.x;
+    __shared__ Part direct;
     if (tid < 32) {
         Point p0, p1;
         Seq s0;
-        const bool ok = split_points<PAGED, kF32Tile>(a, cta, p0, p1, s0);
+        Part p;
+        const bool ok = a.direct ? direct_part<PAGED, kF32Tile>(a, cta, p)
+                                 : split_points<PAGED, kF32Tile>(a, cta, p0, p1, s0);
         if (tid == 0) {
-            pts[0] = p0;
-            pts[1] = p1;
-            seq0 = s0;
+            if (a.direct) {
+                direct = p;
+            } else {
+                pts[0] = p0;
+                pts[1] = p1;
+                seq0 = s0;
+            }
+            if (!a.direct) {
+                part_header(a, 2 * cta)->valid = 0;
+                part_header(a, 2 * cta + 1)->valid = 0;
+            }
             any = ok;
-            part_header(a, 2 * cta)->valid = 0;
-            part_header(a, 2 * cta + 1)->valid = 0;
         }
     }
     __syncthreads();
     if (!any) return;
     Walk<PAGED, kF32Tile> walk;
-    walk.init(pts[0], pts[1], seq0);
+    if (!a.direct) walk.init(pts[0], pts[1], seq0);
     const int ty = tid >> 4, tx = tid & 15;  // rows 8 ty + i; keys tx + 16 e, channels 4 tx + 64 e
     const float c = a.scale * kLog2e;
     const int G = a.G;
-    Part p;
-    while (walk.next(a, p)) {
+    Part p = direct;
+    for (bool more = a.direct || walk.next(a, p); more; more = !a.direct && walk.next(a, p)) {
         const int rows = p.tokens * G;
         __syncthreads();  // the last part's reads are done
         for (int x = tid; x < kF32Tile * 32; x += kF32Threads) {
@@ -247,13 +256,17 @@ static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
     a.streams = 1;
     a.tile_tokens = PAGED && a.T * a.G < kF32Tile ? a.T : kF32Tile / a.G;
     a.extra = 64;
-    a.min_part = 128;
+    a.min_part = kF32MinPart;
     a.cut = 3;
+    const long long slots = PAGED ? (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens)
+                                  : ((long long)a.Tq_total / a.tile_tokens + a.N) * a.Hkv;
+    const long long keys = PAGED ? (long long)a.table_cols * a.page + kF32Tile : a.Tk;
+    a.direct = slots <= 2 * a.sms && keys <= (2 * a.cut - 1) * kF32Tile;
     cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF32Smem);
     if (e != cudaSuccess) return e;
-    attn_f32_kernel<PAGED><<<a.ctas, kF32Threads, kF32Smem, stream>>>(a, io);
+    attn_f32_kernel<PAGED><<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kF32Threads, kF32Smem, stream>>>(a, io);
     e = cudaGetLastError();
-    return e == cudaSuccess ? launch_attn_combine(a, false, stream) : e;
+    return e == cudaSuccess && !a.direct ? launch_attn_combine(a, false, stream) : e;
 }
 
 cudaError_t launch_attn_prefill_f32(const Args &a, const void *q, const void *k, const void *v, long long ldq,

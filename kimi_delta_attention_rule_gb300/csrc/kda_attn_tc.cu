@@ -27,6 +27,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "kda_attn.cuh"
 #include "kda_common.cuh"
 #include "kda_tcgen05.cuh"
@@ -38,6 +40,7 @@ namespace attn {
 constexpr int kSoftmaxWarps = 8;
 constexpr int kWarpMma = 8, kWarpTma = 9, kWarpSched = 10, kWarpFix = 11;
 constexpr int kThreads = 384;
+constexpr int kMinPart = kTcMinPart;
 constexpr int kTile = 128;      // rows of a row tile, keys of a key tile
 constexpr uint32_t kTileBytes = 32768;  // 128 rows x 128 channels bf16, two 64-channel halves
 constexpr uint32_t kHalf = 16384;
@@ -58,7 +61,7 @@ struct Desc {
     int n, h, q0, k0, Lk;
     int first_tok;         // the item's first token within its sequence
     int ta, nt;            // the part's first tile; tiles of the item
-    int whole, slot;       // the part is the item; its workspace slot
+    int whole, slot;       // the part is the item; else its workspace slot
     int writer;            // DUAL: the stream with the first tile, which joins and writes
     int seen;              // prefill: keys that the item's first token sees; decode: cached keys
     int q[2];              // running number of each stream's Q tile
@@ -212,7 +215,7 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
 
 template <bool PAGED, bool DUAL>
 __global__ void __launch_bounds__(kThreads, 1)
-    attn_tc_kernel(const Args a, const __grid_constant__ Maps maps) {
+    attn_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     using L = Smem<DUAL>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
@@ -224,7 +227,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (warp == kWarpTma) {
         if (lane == 0) {
             for (int i = 0; i < L::kQs; ++i) {
@@ -264,6 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -293,7 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
         const uint32_t tl = tm + ((uint32_t)(32 * quad) << 16);
         const uint32_t tS = tl + kColS + 128 * s, tO = tl + kColO + 128 * s;
-        const int tok = r / a.G, g = r - tok * a.G;
+        const uint32_t inv_g = (65536u + a.G - 1) / a.G;  // x / G = x inv_g >> 16, exact for x < 1024
+        const int tok = (int)(r * inv_g >> 16), g = r - tok * a.G;
         const float c = a.scale * kLog2e;
         uint32_t ns = 0, no = 0;
         while (const Desc *d = next_desc()) {
@@ -511,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int rows = d->tokens[s] * a.G, ch = lane & 15;
 #pragma unroll 4
                         for (int i = 0; i < 32; i += 2) {
-                            const int row = 32 * quad + i + (lane >> 4), tk = row / a.G;
+                            const int row = 32 * quad + i + (lane >> 4), tk = (int)(row * inv_g >> 16);
                             const uint4 y = *reinterpret_cast<const uint4 *>(stage + row * 256 + ((ch ^ (row & 15)) * 16));
                             if (row < rows)
                                 reinterpret_cast<uint4 *>(out + ((size_t)(q0 + tk) * a.Hq + row0 + (row - tk * a.G)) * kD)[ch] = y;
@@ -533,29 +537,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         if (warp == kWarpSched) {
-            // ---- scheduler warp ---------------------------------------------------
+            // ---- scheduler warp: walks the CTA's parts ahead of the others ------------
             Point p0, p1;
             Seq s0;
-            const bool any = split_points<PAGED, kTile>(a, cta, p0, p1, s0);
-            if (lane == 0) {
+            Part p;
+            bool more = a.direct ? direct_part<PAGED, kTile>(a, cta, p)
+                                 : split_points<PAGED, kTile>(a, cta, p0, p1, s0);
+            Walk<PAGED, kTile> walk;
+            if (more && !a.direct) {
+                walk.init(p0, p1, s0);
+                more = walk.next(a, p);
+            }
+            if (lane == 0 && !a.direct) {
                 part_header(a, 2 * cta)->valid = 0;
                 part_header(a, 2 * cta + 1)->valid = 0;
             }
-            Walk<PAGED, kTile> walk;
-            Part p;
-            if (any) walk.init(p0, p1, s0);
             Run run = {0, 0};
-            bool more = true;
-            while (more) {
+            while (true) {
                 if (nd >= kDescs && !(alive = long_wait(bars.dempty(nd % kDescs), (nd / kDescs - 1) & 1))) break;
-                more = any && walk.next(a, p);
                 if (lane == 0) {
                     Desc *d = const_cast<Desc *>(descs) + nd % kDescs;
-                    if (more) {
-                        describe<PAGED, DUAL>(a, p, cta, run, *d);
-                    } else {
-                        d->last = 1;
-                    }
+                    if (more) describe<PAGED, DUAL>(a, p, cta, run, *d);
+                    else d->last = 1;
                     mbar_arrive(bars.dfull(nd % kDescs));
                     if (more && !p.whole()) {
                         PartHeader *h = part_header(a, part_slot(cta, p));
@@ -567,6 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 ++nd;
+                if (!more) break;
+                more = !a.direct && walk.next(a, p);
             }
         } else if (warp == kWarpTma) {
             // ---- TMA warp ------------------------------------------------------
@@ -834,6 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpFix) tc::tmem_dealloc(tm, 512);
 }
 
+cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
+
 // ---- host -----------------------------------------------------------------
 namespace {
 // [rows][heads][128] bf16 with `ld` elements between rows; box = 64 channels x bh heads x br rows
@@ -860,43 +867,46 @@ bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 template <bool PAGED, bool DUAL>
-cudaError_t launch(const Args &a, const Maps &maps, cudaStream_t stream) {
+cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
+    a.streams = DUAL ? 1 : 2;
+    // An item's start and end cost about two key tiles; a join about four.
+    a.extra = 256;
+    a.min_part = kMinPart;
+    a.cut = 4;
+    a.direct = slots <= a.sms && keys <= (long long)(2 * a.cut - 1) * kTile;
     constexpr int bytes = Smem<DUAL>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<PAGED, DUAL>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    attn_tc_kernel<PAGED, DUAL><<<a.ctas, kThreads, bytes, stream>>>(a, maps);
-    return cudaGetLastError();
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(attn_tc_kernel<PAGED, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    attn_tc_kernel<PAGED, DUAL><<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kThreads, bytes, stream>>>(a, maps);
+    e = cudaGetLastError();
+    return e == cudaSuccess && !a.direct ? launch_attn_combine(a, true, stream) : e;
 }
 }  // namespace
-
-cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
 
 cudaError_t launch_attn_prefill_tc(Args a, const void *q, const void *k, const void *v, long long ldq,
                                    long long ldk, long long ldv, cudaStream_t stream) {
     a.tile_tokens = kTile / a.G;
-    a.streams = 2;
-    a.extra = 256;
-    a.min_part = 384;
-    a.cut = 4;
     Maps m{};
     if (!map3(&m.q, q, a.Hq, a.Tq_total, ldq, a.G, a.tile_tokens) ||
         !map3(&m.k, k, a.Hkv, a.Tk_total, ldk, 1, kTile) ||
         !map3(&m.v, v, a.Hkv, a.Tk_total, ldv, 1, kTile))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch<false, false>(a, m, stream);
-    return e == cudaSuccess ? launch_attn_combine(a, true, stream) : e;
+    const long long slots = ((long long)a.Tq_total / (2 * a.tile_tokens) + a.N) * a.Hkv;
+    return launch<false, false>(a, m, slots, a.Tk, stream);
 }
 
 cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const void *vp, const void *kn,
                                   const void *vn, long long ldq, long long ldk, long long ldv,
                                   cudaStream_t stream) {
     const bool dual = a.T * a.G <= kTile;
-    a.streams = dual ? 1 : 2;
     a.tile_tokens = dual ? a.T : kTile / a.G;
-    a.extra = 256;
-    a.min_part = 384;
-    a.cut = 4;
     const long long rows = (long long)a.pages * a.Hkv * a.page, toks = (long long)a.N * a.T;
     Maps m{};
     if (!map3(&m.q, q, a.Hq, toks, ldq, a.G, a.tile_tokens) ||
@@ -906,8 +916,10 @@ cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const v
     if (a.has_new && (!map3(&m.kn, kn, a.Hkv, toks, ldk, 1, kMaxDrafts) ||
                       !map3(&m.vn, vn, a.Hkv, toks, ldv, 1, kMaxDrafts)))
         return cudaErrorInvalidValue;
-    cudaError_t e = dual ? launch<true, true>(a, m, stream) : launch<true, false>(a, m, stream);
-    return e == cudaSuccess ? launch_attn_combine(a, true, stream) : e;
+    const int block = a.tile_tokens * (dual ? 1 : 2);
+    const long long slots = (long long)a.N * a.Hkv * ((a.T + block - 1) / block);
+    const long long keys = (long long)a.table_cols * a.page + kTile;
+    return dual ? launch<true, true>(a, m, slots, keys, stream) : launch<true, false>(a, m, slots, keys, stream);
 }
 
 }  // namespace attn
