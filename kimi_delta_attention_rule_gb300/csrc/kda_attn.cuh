@@ -71,6 +71,7 @@ struct Args {
     int min_part;            // keys of work below which no further CTA is used
     int cut;                 // tiles that a part of an item has at least
     int direct;              // one CTA for each slot of an item, nothing is split
+    float unit, inv_unit;    // keys per unit of weight, and its inverse
     float scale;
     // device pointers
     const int32_t *cu_q, *cu_k;      // prefill offsets (NULL: equal lengths)
@@ -81,6 +82,13 @@ struct Args {
     unsigned char *ws;
     int ctas, sms;           // CTAs that share the work; SMs of the device
 };
+
+// The unit of weight: `keys` is an upper bound of a call's work in keys.
+inline void set_unit(Args &a, double keys) {
+    a.unit = 1.f;
+    while (keys / a.unit > 1e9) a.unit *= 2.f;
+    a.inv_unit = 1.f / a.unit;
+}
 
 __device__ __forceinline__ uint32_t *status_word(const Args &a) {
     return reinterpret_cast<uint32_t *>(a.ws);
@@ -149,25 +157,25 @@ template <bool PAGED, int KT>
 __device__ __forceinline__ int item_tiles(const Args &a, const Seq &s, int i) {
     return (int)(((unsigned)item_keys<PAGED>(a, s, i) + KT - 1) / KT) + (PAGED ? a.has_new : 0);
 }
-// Weight of items 0 .. i - 1 of one kv head (arithmetic series of visible keys).
+// Weight of items 0 .. i - 1 of one kv head: an arithmetic series of visible keys and
+// `extra` keys per item, in units of a.unit keys, which the host chooses so that a
+// call's total stays below 2^30. Formed in fp32: every operation rounds
+// monotonically, so the weights rise with i, and all that follows is in whole units.
 template <bool PAGED, int KT>
-__device__ __forceinline__ long long items_weight(const Args &a, const Seq &s, int i) {
-    if (i <= 0) return 0;
-    if (PAGED) return (long long)i * (a.extra + (long long)item_tiles<PAGED, KT>(a, s, 0) * KT);
-    const int block = a.tile_tokens * a.streams, d = s.Lk - s.Lq;
-    long long w = (long long)i * a.extra;
-    const int full = i < s.ni ? i : s.ni - 1;  // items whose last token is not the sequence's
-    const int first = d < 0 ? -d / block : 0;  // items that see nothing
-    if (first < full) {
-        const long long lo = (long long)(first + 1) * block, hi = (long long)full * block;
-        w += ((lo + hi + 2LL * d) * (full - first)) >> 1;
+__device__ __forceinline__ uint32_t items_weight(const Args &a, const Seq &s, int i) {
+    float w;
+    if (PAGED) {
+        w = (float)i * (float)(a.extra + item_tiles<PAGED, KT>(a, s, 0) * KT);
+    } else {
+        const int d = s.Lk - s.Lq, full = i < s.ni ? i : s.ni - 1;  // items without the sequence's last token
+        const float block = (float)(a.tile_tokens * a.streams);
+        const float unseen = fmaxf(0.f, floorf((float)-d / block));  // items that see nothing
+        const float count = fmaxf(0.f, (float)full - unseen);
+        // the last rows of items `unseen` .. full - 1 see d + block (unseen + 1) .. keys
+        w = (float)i * (float)a.extra + count * fmaf(0.5f * block, (float)full + unseen + 1.f, (float)d);
+        if (i >= s.ni) w += (float)s.Lk;
     }
-    if (i >= s.ni) w += s.Lk;  // the last item's last row sees every key
-    return w;
-}
-template <bool PAGED, int KT>
-__device__ __forceinline__ long long seq_weight(const Args &a, const Seq &s) {
-    return s.ni == 0 ? 0 : items_weight<PAGED, KT>(a, s, s.ni) * a.Hkv;
+    return (uint32_t)(fmaxf(w, 0.f) * a.inv_unit);
 }
 
 // A point on the line of work: before tile `tile` of item (n, h, i).
@@ -178,113 +186,105 @@ __device__ __forceinline__ bool same_item(const Point &x, const Point &y) {
     return x.n == y.n && x.h == y.h && x.i == y.i;
 }
 
-// The point at distance x into sequence n (0 <= x < its weight); a converged
-// warp with the same arguments in all lanes.
+// The point at distance x into sequence n (x below its weight); a converged warp with
+// the same arguments in all lanes.
 template <bool PAGED, int KT>
-__device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n, long long x) {
+__device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n, uint32_t x) {
     const int lane = threadIdx.x & 31;
-    const long long per_head = items_weight<PAGED, KT>(a, s, s.ni);
+    const uint32_t per_head = items_weight<PAGED, KT>(a, s, s.ni);
     Point p;
     p.n = n;
-    p.h = min(a.Hkv - 1, (int)((float)x / (float)per_head));
-    while (p.h > 0 && p.h * per_head > x) --p.h;  // (the quotient was rounded)
-    while (p.h + 1 < a.Hkv && (p.h + 1) * per_head <= x) ++p.h;
-    x -= p.h * per_head;
+    p.h = (int)(x / per_head);
+    x -= (uint32_t)p.h * per_head;
     int lo = 0, count = s.ni;  // the last item that starts at or before x is in [lo, lo + count)
     while (count > 1) {
-        const int step = (count + 31) / 32, at = lo + lane * step;
+        const int step = (count + 31) >> 5, at = lo + lane * step;
         const bool before = lane * step < count && items_weight<PAGED, KT>(a, s, at) <= x;
         const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));  // (lane 0 always is)
         count = min(step, count - k * step);
         lo += k * step;
     }
     p.i = lo;
-    const long long y = x - items_weight<PAGED, KT>(a, s, lo) - a.extra / 2;
+    const float y = (float)(x - items_weight<PAGED, KT>(a, s, lo)) * a.unit - 0.5f * (float)a.extra;
     const int nt = item_tiles<PAGED, KT>(a, s, lo);
-    const int t = y <= 0 ? 0 : (int)min((y + KT / 2) / KT, (long long)nt);
+    const int t = (int)fminf(fmaxf(0.f, y * (1.f / KT) + 0.5f), (float)nt);
     // short pieces are not worth their join: such a cut moves to the item's edge
     p.tile = t < a.cut ? 0 : (t > nt - a.cut ? nt : t);
     return p;
 }
 
-// Finds, with one converged warp, the points at U c / C and U (c + 1) / C.
-// Returns false when there is nothing for this CTA: it has no part, or the
-// offsets are malformed (which sets the status bit; the whole call is then
-// skipped). A decode sequence with a malformed length is flagged and skipped
-// alone. s0 gets the sequence of p0.
+// Finds, with one converged warp, the point at U c / C (at the line's end: n = N).
+// Returns false when CTA c has no part, or the offsets are malformed (which sets the
+// status bit; the whole call is then skipped). A decode sequence with a malformed
+// length is flagged and skipped alone. s0 gets the point's sequence. (It runs once,
+// before everything else that a CTA does, from a cold instruction cache: short code
+// counts more than few operations.)
 template <bool PAGED, int KT>
-__device__ __forceinline__ bool split_points(const Args &a, int c, Point &p0, Point &p1, Seq &s0) {
+__device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq &s0) {
     const int lane = threadIdx.x & 31;
-    long long total = 0, w = 0;
-    bool good = true;
-    Seq s;
-    for (int n0 = 0; n0 < a.N; n0 += 32) {
-        w = 0;
-        if (n0 + lane < a.N) {
-            good = load_seq<PAGED>(a, n0 + lane, s) && good;
-            w = seq_weight<PAGED, KT>(a, s);
-        }
-        total += w;
-    }
+    constexpr int kFlight = PAGED ? 4 : 1;  // groups of 32 sequences whose loads are in flight together
+    uint32_t w[kFlight], total = 0;
+    auto weigh = [&](int n0) {
+        bool ok = true;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    good = __all_sync(0xffffffffu, good);
-    if (!good) {
+        for (int u = 0; u < kFlight; ++u) {
+            const int n = n0 + 32 * u + lane;
+            Seq s;
+            w[u] = 0;
+            if (n < a.N) {
+                ok = load_seq<PAGED>(a, n, s) && ok;
+                if (s.ni > 0) w[u] = items_weight<PAGED, KT>(a, s, s.ni) * (uint32_t)a.Hkv;
+            }
+        }
+        return ok;
+    };
+    bool good = true;
+#pragma unroll 1
+    for (int n0 = 0; n0 < a.N; n0 += 32 * kFlight) {
+        good = weigh(n0) && good;
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) total += w[u];
+    }
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (!__all_sync(0xffffffffu, good)) {
         if (lane == 0) atomicOr(status_word(a), kStatusBadSeqlens);
         if (!PAGED) return false;
     }
     if (total == 0) return false;
     // (single precision: a cut may lie anywhere, but for all CTAs at the same place)
     const float units = (float)total;
-    const int ctas = max(1, (int)fminf((float)a.ctas, units / (float)a.min_part));
-    if (c >= ctas) return false;
-    const long long x0 = (long long)(units * ((float)c / (float)ctas));
-    const long long x1 = (long long)(units * ((float)(c + 1) / (float)ctas));
-    p1.n = a.N;  // the end of the line
-    p1.h = p1.i = p1.tile = 0;
-    long long before = 0;
-    bool found0 = false, found1 = c + 1 == ctas;
-    for (int n0 = 0; n0 < a.N && !(found0 && found1); n0 += 32) {
-        if (a.N > 32) {  // (else the loop above left them in place)
-            w = 0;
-            if (n0 + lane < a.N) {
-                load_seq<PAGED>(a, n0 + lane, s);
-                w = seq_weight<PAGED, KT>(a, s);
-            }
-        }
-        long long incl = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        const long long lo = before + incl - w;
+    const int ctas = max(1, (int)fminf((float)a.ctas, units * a.unit / (float)a.min_part));
+    if (c > ctas) return false;
+    p0.n = a.N;
+    p0.h = p0.i = p0.tile = 0;
+    if (c == ctas) return true;
+    uint32_t x = (uint32_t)(units * ((float)c / (float)ctas));
 #pragma unroll 1
-        for (int e = 0; e < 2; ++e) {
-            const long long x = e ? x1 : x0;
-            const bool here = (e ? !found1 : !found0) && w > 0 && x >= lo && x < lo + w;
-            const unsigned who = __ballot_sync(0xffffffffu, here);
-            if (who == 0) continue;
-            const int src = __ffs(who) - 1;
-            Seq t;
-            t.q0 = __shfl_sync(0xffffffffu, s.q0, src);
-            t.Lq = __shfl_sync(0xffffffffu, s.Lq, src);
-            t.k0 = __shfl_sync(0xffffffffu, s.k0, src);
-            t.Lk = __shfl_sync(0xffffffffu, s.Lk, src);
-            t.ni = __shfl_sync(0xffffffffu, s.ni, src);
-            const Point p = point_in_seq<PAGED, KT>(a, t, n0 + src, x - __shfl_sync(0xffffffffu, lo, src));
-            if (e) {
-                p1 = p;
-                found1 = true;
-            } else {
-                p0 = p;
-                s0 = t;
-                found0 = true;
+    for (int n0 = 0; n0 < a.N; n0 += 32 * kFlight) {
+        if (a.N > 32 * kFlight) weigh(n0);  // (else the loop above left them in place)
+#pragma unroll
+        for (int u = 0; u < kFlight; ++u) {
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, w[u]);
+            if (x >= sum) {
+                x -= sum;
+                continue;
             }
+            uint32_t incl = w[u];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+            }
+            const int src = __ffs(__ballot_sync(0xffffffffu, x < incl)) - 1;
+            x -= __shfl_sync(0xffffffffu, incl - w[u], src);
+            p0.n = n0 + 32 * u + src;
+            n0 = a.N;  // found
+            break;
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
     }
-    return found0;
+    load_seq<PAGED>(a, p0.n, s0);
+    p0 = point_in_seq<PAGED, KT>(a, s0, p0.n, x);
+    return true;
 }
 
 // A part of an item: the key tiles [ta, tb) of (n, h, i).

@@ -44,25 +44,24 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     const int tid = threadIdx.x, cta = blockIdx.x;
     __shared__ Part direct;
-    if (tid < 32) {
-        Point p0, p1;
+    if (tid < 64) {  // one warp finds where this CTA's work starts, one where it ends
+        const int w = tid >> 5;
+        Point pt;
         Seq s0;
         Part p;
-        const bool ok = a.direct ? direct_part<PAGED, kF32Tile>(a, cta, p)
-                                 : split_points<PAGED, kF32Tile>(a, cta, p0, p1, s0);
-        if (tid == 0) {
-            if (a.direct) {
-                direct = p;
-            } else {
-                pts[0] = p0;
-                pts[1] = p1;
-                seq0 = s0;
-            }
-            if (!a.direct) {
+        bool ok = false;
+        if (!a.direct) ok = split_point<PAGED, kF32Tile>(a, cta + w, pt, s0) && (w != 0 || pt.n < a.N);
+        else if (w == 0) ok = direct_part<PAGED, kF32Tile>(a, cta, p);
+        if ((tid & 31) == 0) {
+            pts[w] = pt;
+            if (w == 0) {
+                if (a.direct) direct = p;
+                else seq0 = s0;
+                any = ok;
+            } else if (!a.direct) {
                 part_header(a, 2 * cta)->valid = 0;
                 part_header(a, 2 * cta + 1)->valid = 0;
             }
-            any = ok;
         }
     }
     __syncthreads();
@@ -261,6 +260,7 @@ static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
     const long long slots = PAGED ? (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens)
                                   : ((long long)a.Tq_total / a.tile_tokens + a.N) * a.Hkv;
     const long long keys = PAGED ? (long long)a.table_cols * a.page + kF32Tile : a.Tk;
+    set_unit(a, (double)slots * ((double)keys + a.extra + kF32Tile));
     a.direct = slots <= 2 * a.sms && keys <= (2 * a.cut - 1) * kF32Tile;
     cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF32Smem);
     if (e != cudaSuccess) return e;

@@ -79,7 +79,8 @@ struct Smem {
     static constexpr uint32_t kJoin = kQs * kTileBytes;  // DUAL only
     static constexpr uint32_t kKv = 3 * kTileBytes;
     static constexpr uint32_t kBars = kKv + kRing * kTileBytes;
-    static constexpr uint32_t kBytes = kBars + 1024;
+    static constexpr uint32_t kMl = kBars + 1024;  // DUAL: the second stream's m and l
+    static constexpr uint32_t kBytes = kMl + (DUAL ? 1024 : 0);
 };
 
 struct Bars {  // shared-memory addresses
@@ -98,24 +99,35 @@ struct Bars {  // shared-memory addresses
     static constexpr uint32_t kTmem = 336;
     static constexpr uint32_t kDead = 340;  // a role gave up
     static constexpr uint32_t kJobs = 344;  // kJobRing times (slot, valid rows)
-    static constexpr uint32_t kDesc = 416;  // kDescs descriptors
+    static constexpr uint32_t kEnd = 408;   // Point: the end of the CTA's work
+    static constexpr uint32_t kDesc = 432;  // kDescs descriptors
 };
 static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= 1024, "barrier area");
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
+// Tensor copies issued by a converged warp, of which the lane with `lead` set takes
+// part: its operands stay in uniform registers (a copy issued by a lane of its own
+// choice cost 100 cycles, which at 16-row pages bounded the loads).
+__device__ __forceinline__ void tma_2d(uint32_t lead, uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
-        "l"(m), "r"(c0), "r"(c1), "r"(bar)
+        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
+        " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
+        "l"(m), "r"(c0), "r"(c1), "r"(bar), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
+__device__ __forceinline__ void tma_3d(uint32_t lead, uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
-        "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        "{\n .reg .pred q;\n setp.ne.b32 q, %6, 0;\n"
+        " @q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
+        "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(lead)
         : "memory");
+}
+__device__ __forceinline__ void expect_tx(uint32_t lead, uint32_t bar, uint32_t bytes) {
+    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
+                 "r"(bytes), "r"(lead)
+                 : "memory");
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
@@ -153,6 +165,16 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
         if (t0 == 0) t0 = now;
         else if (now - t0 > kWaitNs) return false;
     }
+}
+// whether a phase is through, without waiting
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // a wait of a whole warp, which leaves it converged
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
@@ -227,7 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         return;
     }
 
-    if (warp == kWarpTma) {
+    Point p0;
+    Seq s0;
+    bool any = false;
+    if (warp == kWarpSched) {  // where this CTA's work starts; kWarpFix: where it ends
+        if (!a.direct) any = split_point<PAGED, kTile>(a, cta, p0, s0) && p0.n < a.N;
+    } else if (warp == kWarpTma) {
         if (lane == 0) {
             for (int i = 0; i < L::kQs; ++i) {
                 tc::mbar_init(bars.qfull(i), 1);
@@ -253,9 +280,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::fence_mbar_init();
         }
     } else if (warp == kWarpFix) {
+        if (!a.direct) {
+            split_point<PAGED, kTile>(a, cta + 1, p0, s0);
+            if (lane == 0) {
+                *reinterpret_cast<Point *>(sm + L::kBars + Bars::kEnd) = p0;
+                part_header(a, 2 * cta)->valid = 0;
+                part_header(a, 2 * cta + 1)->valid = 0;
+            }
+        }
+    } else if (warp == kWarpMma) {
         tc::tmem_alloc(bars.base + Bars::kTmem, 512);
         tc::tmem_relinquish();
-    } else if (warp == kWarpMma) {
         if (lane == 0) {
             prefetch_map(&maps.q);
             prefetch_map(&maps.k);
@@ -409,37 +444,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 tc::fence_after_sync();
             }
-            const bool joins = DUAL && steps > 0 && others > 0 && warp_ok;
-            if (joins) {
-                // the second stream hands over (m, l), then O in two parts of 64 channels;
-                // a barrier of the two warps of these 32 rows around each
+            const bool writer = !DUAL || s == d->writer, joins = DUAL && steps > 0 && others > 0;
+            if (warp_ok && (writer || joins)) {
+                // In two parts of 64 channels: O from TMEM; the second stream of a join
+                // hands it over in shared memory; the writer stores the sum, or stages it
+                // (as 128 bytes of a row in this stream's Q tile, whose products are done).
                 float4 *const box = reinterpret_cast<float4 *>(sm + L::kJoin) + r;
-                const int join_bar = 1 + quad;
+                float2 *const box_ml = reinterpret_cast<float2 *>(sm + L::kMl) + r;
+                const int join_bar = 1 + quad;  // the two warps of these 32 rows
+                const int q0 = d->q0 + (DUAL ? 0 : s * a.tile_tokens), row0 = d->h * a.G;
+                unsigned char *const stage = sm + L::kQ + d->q[s] % L::kQs * kTileBytes;
                 float f = 1.f, f1 = 0.f;
-                if (s != d->writer) *box = make_float4(m, l, 0.f, 0.f);
-                named_bar(join_bar, 64);
-                if (s == d->writer) {
-                    const float4 ml = *box;
-                    const float up = fmaxf(m, ml.x);
-                    f = m == -INFINITY ? 0.f : ex2((m - up) * c);
-                    f1 = ml.x == -INFINITY ? 0.f : ex2((ml.x - up) * c);
-                    m = up;
-                    l = l * f + ml.y * f1;
-                }
-                named_bar(join_bar, 64);
 #pragma unroll 1
                 for (int p = 0; p < 2; ++p) {
-                    uint32_t o[4][16];
-                    tc::tmem_ld_cols<4>(tO + 64 * p, o);
-                    if (s != d->writer) {
+                    uint32_t o[4][16] = {};
+                    if (steps > 0) tc::tmem_ld_cols<4>(tO + 64 * p, o);
+                    if (!writer) {
+                        if (p == 0) *box_ml = make_float2(m, l);
 #pragma unroll
                         for (int q = 0; q < 16; ++q)
                             box[128 * q] = make_float4(
                                 __uint_as_float(o[q / 4][4 * (q % 4)]), __uint_as_float(o[q / 4][4 * (q % 4) + 1]),
                                 __uint_as_float(o[q / 4][4 * (q % 4) + 2]), __uint_as_float(o[q / 4][4 * (q % 4) + 3]));
+                        named_bar(join_bar, 64);  // handed over
+                        named_bar(join_bar, 64);  // taken
+                        continue;
                     }
-                    named_bar(join_bar, 64);
-                    if (s == d->writer) {
+                    if (joins) {
+                        named_bar(join_bar, 64);
+                        if (p == 0) {
+                            const float2 ml = *box_ml;
+                            const float up = fmaxf(m, ml.x);
+                            f = m == -INFINITY ? 1.f : ex2((m - up) * c);  // (then O and l are 0, or NaN)
+                            f1 = ml.x == -INFINITY ? 1.f : ex2((ml.x - up) * c);
+                            m = up;
+                            l = l * f + ml.y * f1;
+                        }
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
                             const float4 y = box[128 * q];
@@ -449,73 +489,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                             z[2] = __float_as_uint(f * __uint_as_float(z[2]) + f1 * y.z);
                             z[3] = __float_as_uint(f * __uint_as_float(z[3]) + f1 * y.w);
                         }
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) tc::tmem_st16u(tO + 64 * p + 16 * q, o[q]);
-                        tc::tmem_wait_st();
+                        named_bar(join_bar, 64);
                     }
-                    named_bar(join_bar, 64);
-                }
-            }
-            const bool writer = !DUAL || s == d->writer;
-            if (warp_ok && writer) {
-                const int q0 = d->q0 + (DUAL ? 0 : s * a.tile_tokens);
-                const int row0 = d->h * a.G;
-                if (!d->whole) {
-                    const int row = DUAL ? r : 128 * s + r;
-                    float4 *o4 = reinterpret_cast<float4 *>(part_o(a, d->slot)) + row;
-#pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t o[2][16];
-                        if (steps > 0) tc::tmem_ld_cols<2>(tO + 32 * q, o);
+                    if (!d->whole) {
                         if (row_ok) {
+                            float4 *o4 = reinterpret_cast<float4 *>(part_o(a, d->slot)) + (DUAL ? r : 128 * s + r);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-                                if (steps > 0)
-                                    y = make_float4(__uint_as_float(o[i / 4][4 * (i % 4)]),
-                                                    __uint_as_float(o[i / 4][4 * (i % 4) + 1]),
-                                                    __uint_as_float(o[i / 4][4 * (i % 4) + 2]),
-                                                    __uint_as_float(o[i / 4][4 * (i % 4) + 3]));
-                                o4[(size_t)(8 * q + i) * kPartRows] = y;
-                            }
+                            for (int q = 0; q < 16; ++q)
+                                o4[(size_t)(16 * p + q) * kPartRows] = make_float4(
+                                    __uint_as_float(o[q / 4][4 * (q % 4)]), __uint_as_float(o[q / 4][4 * (q % 4) + 1]),
+                                    __uint_as_float(o[q / 4][4 * (q % 4) + 2]), __uint_as_float(o[q / 4][4 * (q % 4) + 3]));
                         }
+                        continue;
                     }
-                    if (row_ok) part_ml(a, d->slot)[row] = make_float2(m, l);
-                } else {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    if (steps == 0) {  // rows that see nothing (no Q tile is theirs): zeros
+                        if (row_ok) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
+                                                                   ((size_t)(q0 + tok) * a.Hq + row0 + g) * kD + 64 * p);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) dst[i] = make_uint4(0, 0, 0, 0);
+                        }
+                        continue;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16(inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e]),
+                                             inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e + 1]));
+                        *reinterpret_cast<uint4 *>(stage + r * 256 + (((8 * p + i) ^ (r & 15)) * 16)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                if (writer && !d->whole) {
+                    if (row_ok) part_ml(a, d->slot)[DUAL ? r : 128 * s + r] = make_float2(m, l);
+                } else if (writer) {
                     if (row_ok && a.lse != nullptr)
                         a.lse[(size_t)(q0 + tok) * a.Hq + row0 + g] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
-                    __nv_bfloat16 *const out = static_cast<__nv_bfloat16 *>(a.out);
-                    if (steps == 0) {  // rows that see nothing
-                        if (row_ok) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(out + ((size_t)(q0 + tok) * a.Hq + row0 + g) * kD);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) dst[i] = make_uint4(0, 0, 0, 0);
-                        }
-                    } else {
-                        // through this stream's Q tile: its products are done
-                        unsigned char *stage = sm + L::kQ + d->q[s] % L::kQs * kTileBytes;
-                        const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            uint32_t o[2][16];
-                            tc::tmem_ld_cols<2>(tO + 32 * q, o);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t w[4];
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    w[e] = pack_bf16(inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e]),
-                                                     inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e + 1]));
-                                *reinterpret_cast<uint4 *>(stage + r * 256 + (((4 * q + i) ^ (r & 15)) * 16)) =
-                                    make_uint4(w[0], w[1], w[2], w[3]);
-                            }
-                        }
+                    if (steps > 0) {
                         __syncwarp();
                         // sixteen lanes write a row's 256 bytes
                         const int rows = d->tokens[s] * a.G, ch = lane & 15;
+                        __nv_bfloat16 *const out = static_cast<__nv_bfloat16 *>(a.out);
 #pragma unroll 4
                         for (int i = 0; i < 32; i += 2) {
                             const int row = 32 * quad + i + (lane >> 4), tk = (int)(row * inv_g >> 16);
+                            if (32 * quad + i >= rows) break;
                             const uint4 y = *reinterpret_cast<const uint4 *>(stage + row * 256 + ((ch ^ (row & 15)) * 16));
                             if (row < rows)
                                 reinterpret_cast<uint4 *>(out + ((size_t)(q0 + tk) * a.Hq + row0 + (row - tk * a.G)) * kD)[ch] = y;
@@ -538,19 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         if (warp == kWarpSched) {
             // ---- scheduler warp: walks the CTA's parts ahead of the others ------------
-            Point p0, p1;
-            Seq s0;
             Part p;
-            bool more = a.direct ? direct_part<PAGED, kTile>(a, cta, p)
-                                 : split_points<PAGED, kTile>(a, cta, p0, p1, s0);
+            bool more = a.direct ? direct_part<PAGED, kTile>(a, cta, p) : any;
             Walk<PAGED, kTile> walk;
             if (more && !a.direct) {
-                walk.init(p0, p1, s0);
+                walk.init(p0, *reinterpret_cast<const Point *>(sm + L::kBars + Bars::kEnd), s0);
                 more = walk.next(a, p);
-            }
-            if (lane == 0 && !a.direct) {
-                part_header(a, 2 * cta)->valid = 0;
-                part_header(a, 2 * cta + 1)->valid = 0;
             }
             Run run = {0, 0};
             while (true) {
@@ -584,11 +598,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t kv = 0, jobs = 0, g = 0;
             const uint32_t qbytes = (uint32_t)(a.tile_tokens * a.G) * 256u;
             const int rows = a.page < kTile ? a.page : kTile;  // decode: rows of one copy
+            const int row_bits = 31 - __clz(rows), page_bits = 31 - __clz(a.page);
+            const uint32_t lead = tc::elect_one();
             // decode: the page of this lane's copy of tile t
             auto page_of = [&](int n, int Lk, int t) -> int {
-                const int pos = t * kTile + lane * rows;
-                if (!PAGED || lane * rows >= kTile || pos >= Lk) return -1;
-                return __ldg(a.table + (size_t)n * a.table_ld + pos / a.page);
+                const int pos = t * kTile + (lane << row_bits);
+                if (!PAGED || (lane << row_bits) >= kTile || pos >= Lk) return -1;
+                return __ldg(a.table + (size_t)n * a.table_ld + (pos >> page_bits));
             };
             auto load = [&](const Load &x, bool is_v) {
                 const uint32_t slot = kv % L::kRing;
@@ -604,33 +620,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P is 0 there, but 0 times a NaN is not, so V gets zeros
                 const bool fix = is_v && valid < kTile;
                 const uint32_t bar = fix ? bars.vraw(slot) : bars.kvfull(slot);
+                const CUtensorMap *m = is_v ? &maps.v : &maps.k;
                 if (!PAGED) {
-                    if (lane == 0) {
-                        const CUtensorMap *m = is_v ? &maps.v : &maps.k;
-                        tc::mbar_arrive_expect_tx(bar, kTileBytes);
-                        tma_3d(dst, m, 0, x.h, x.k0 + x.t * kTile, bar);
-                        tma_3d(dst + kHalf, m, 64, x.h, x.k0 + x.t * kTile, bar);
-                    }
+                    expect_tx(lead, bar, kTileBytes);
+                    tma_3d(lead, dst, m, 0, x.h, x.k0 + x.t * kTile, bar);
+                    tma_3d(lead, dst + kHalf, m, 64, x.h, x.k0 + x.t * kTile, bar);
                 } else if (x.draft) {
-                    if (lane == 0) {
-                        const CUtensorMap *m = is_v ? &maps.vn : &maps.kn;
-                        tc::mbar_arrive_expect_tx(bar, 64 * 256);
-                        tma_3d(dst, m, 0, x.h, x.n * a.T, bar);
-                        tma_3d(dst + kHalf, m, 64, x.h, x.n * a.T, bar);
-                    }
+                    const CUtensorMap *mn = is_v ? &maps.vn : &maps.kn;
+                    expect_tx(lead, bar, 64 * 256);
+                    tma_3d(lead, dst, mn, 0, x.h, x.n * a.T, bar);
+                    tma_3d(lead, dst + kHalf, mn, 64, x.h, x.n * a.T, bar);
                 } else {
-                    const int copies = (valid + rows - 1) / rows;
-                    if (lane == 0) tc::mbar_arrive_expect_tx(bar, (uint32_t)(copies * rows) * 256u);
-                    __syncwarp();
-                    if (lane < copies) {
-                        const CUtensorMap *m = is_v ? &maps.v : &maps.k;
-                        int row = a.pages * a.Hkv * a.page;  // past the pool's last row: zeros
-                        if (x.pg >= 0 && x.pg < a.pages)
-                            row = (x.pg * a.Hkv + x.h) * a.page + (x.t * kTile + lane * rows) % a.page;
-                        else
-                            atomicOr(status_word(a), kStatusBadSeqlens);
-                        tma_2d(dst + lane * rows * 128, m, 0, row, bar);
-                        tma_2d(dst + kHalf + lane * rows * 128, m, 64, row, bar);
+                    const int copies = (valid + rows - 1) >> row_bits;
+                    expect_tx(lead, bar, (uint32_t)(copies << row_bits) * 256u);
+                    int row = a.pages * a.Hkv * a.page;  // past the pool's last row: zeros
+                    if (x.pg >= 0 && x.pg < a.pages)
+                        row = (x.pg * a.Hkv + x.h) * a.page + ((x.t * kTile + (lane << row_bits)) & (a.page - 1));
+                    else if (lane < copies)
+                        atomicOr(status_word(a), kStatusBadSeqlens);
+                    for (int i = 0; i < copies; ++i) {
+                        const int ri = __shfl_sync(0xffffffffu, row, i);
+                        tma_2d(lead, dst + (i << (row_bits + 7)), m, 0, ri, bar);
+                        tma_2d(lead, dst + kHalf + (i << (row_bits + 7)), m, 64, ri, bar);
                     }
                 }
                 if (fix && lane == 0) {  // the fixing warp waits for the copy and hands the slot on
@@ -647,16 +658,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alive = false;
                     return;
                 }
-                if (lane == 0) {
-                    const uint32_t dst = base + L::kQ + slot * kTileBytes, bar = bars.qfull(slot);
-                    tc::mbar_arrive_expect_tx(bar, qbytes);
-                    tma_3d(dst, &maps.q, 0, h * a.G, tok, bar);
-                    tma_3d(dst + kHalf, &maps.q, 64, h * a.G, tok, bar);
-                }
+                const uint32_t dst = base + L::kQ + slot * kTileBytes, bar = bars.qfull(slot);
+                expect_tx(lead, bar, qbytes);
+                tma_3d(lead, dst, &maps.q, 0, h * a.G, tok, bar);
+                tma_3d(lead, dst + kHalf, &maps.q, 64, h * a.G, tok, bar);
                 __syncwarp();
             };
             Load x1, x2;  // the last two K tiles
             x1.pg = x2.pg = -1;
+            uint32_t peeked = 0;  // descriptors whose first pages are looked up
+            int peek_pg = -1, peek_pg2 = -1;
             while (const Desc *d = next_desc()) {
                 const int c0 = d->count[0], c1 = d->count[1];
                 const int tiles = DUAL ? c0 + c1 : (c0 > c1 ? c0 : c1);
@@ -666,13 +677,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 x.k0 = d->k0;
                 x.Lk = d->Lk;
                 const int ta = d->ta, draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
-                int next_pg = page_of(x.n, x.Lk, ta), next_pg2 = page_of(x.n, x.Lk, ta + 1);
+                int next_pg = peek_pg, next_pg2 = peek_pg2;
+                if (PAGED && peeked != nd + 1) {
+                    next_pg = page_of(x.n, x.Lk, ta);
+                    next_pg2 = page_of(x.n, x.Lk, ta + 1);
+                }
                 for (int j = 0; j < tiles && alive; ++j, ++g) {
                     x.t = ta + j;
                     x.draft = PAGED && x.t == draft_tile;
                     x.pg = next_pg;  // looked up two tiles ahead
                     next_pg = next_pg2;
                     next_pg2 = page_of(x.n, x.Lk, x.t + 2);
+                    if (PAGED && j == tiles - 1 &&
+                        __all_sync(0xffffffffu, mbar_test(bars.dfull((nd + 1) % kDescs), ((nd + 1) / kDescs) & 1))) {
+                        const Desc *e = descs + (nd + 1) % kDescs;
+                        if (!e->last) {
+                            peek_pg = page_of(e->n, e->Lk, e->ta);
+                            peek_pg2 = page_of(e->n, e->Lk, e->ta + 1);
+                            peeked = nd + 2;
+                        }
+                    }
                     if (g >= (uint32_t)kLag) load(DUAL ? x2 : x1, true);
                     if (j == 0 && alive && (DUAL || c0 > 0)) load_q(d->q[0], d->q0, x.h);
                     if (alive) load(x, false);
@@ -836,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc::fence_before_sync();
     __syncthreads();
-    if (warp == kWarpFix) tc::tmem_dealloc(tm, 512);
+    if (warp == kWarpMma) tc::tmem_dealloc(tm, 512);
 }
 
 cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
@@ -872,6 +896,8 @@ cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, c
     // An item's start and end cost about two key tiles; a join about four.
     a.extra = 256;
     a.min_part = kMinPart;
+    // every item's keys, its start and end and, at the most, its drafts' tile
+    set_unit(a, (double)slots * ((double)keys + a.extra + kTile));
     a.cut = 4;
     a.direct = slots <= a.sms && keys <= (long long)(2 * a.cut - 1) * kTile;
     constexpr int bytes = Smem<DUAL>::kBytes;
