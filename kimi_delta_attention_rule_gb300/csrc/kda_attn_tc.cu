@@ -51,7 +51,7 @@ constexpr int kJobRing = 8;  // more than the ring has slots: a job holds its sl
 constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: S/P of stream s at 128 s, O at 256 + 128 s
 
 struct Maps {
-    CUtensorMap q, k, v, kn, vn;
+    CUtensorMap q, k, v, kn, vn, out;
 };
 
 // A part as the roles need it, in shared memory.
@@ -70,14 +70,19 @@ struct Desc {
     int tokens[2];         // valid tokens of its row tile
 };
 
-// Shared memory: Q tiles, (DUAL) 32 KB for the join of the two streams, the ring
-// of K and V tiles, barriers and descriptors.
-template <bool DUAL>
+// Shared memory: Q tiles of RT rows, (DUAL) the box for the join of the two streams
+// (RT rows x 64 channels fp32), the ring of K and V tiles, barriers and descriptors.
+// With RT = 32 (a decode step's rows, as a rule) the ring has six tiles: 192 KB in
+// flight instead of 128 hide the latency of a chain of short sequences. The products
+// read 128 rows of Q all the same; what lies behind the tile gives rows of S and O
+// that nobody looks at.
+template <bool DUAL, int RT>
 struct Smem {
-    static constexpr int kQs = DUAL ? 2 : 3, kRing = 4;
+    static constexpr int kQs = DUAL ? 2 : 3, kRing = RT == 32 ? 6 : 4;
+    static constexpr uint32_t kQTile = RT * 256, kQHalf = RT * 128;
     static constexpr uint32_t kQ = 0;
-    static constexpr uint32_t kJoin = kQs * kTileBytes;  // DUAL only
-    static constexpr uint32_t kKv = 3 * kTileBytes;
+    static constexpr uint32_t kJoin = kQs * kQTile;  // DUAL only
+    static constexpr uint32_t kKv = 3 * kQTile;
     static constexpr uint32_t kBars = kKv + kRing * kTileBytes;
     static constexpr uint32_t kMl = kBars + 1024;  // DUAL: the second stream's m and l
     static constexpr uint32_t kBytes = kMl + (DUAL ? 1024 : 0);
@@ -91,16 +96,16 @@ struct Bars {  // shared-memory addresses
     __device__ uint32_t pready(int s, int half) const { return base + 64 + 16 * half + 8 * s; }
     __device__ uint32_t ofull(int s) const { return base + 96 + 8 * s; }
     __device__ uint32_t kvfull(int i) const { return base + 112 + 8 * i; }
-    __device__ uint32_t kvempty(int i) const { return base + 144 + 8 * i; }
-    __device__ uint32_t vraw(int i) const { return base + 176 + 8 * i; }
-    __device__ uint32_t dfull(int i) const { return base + 208 + 8 * i; }
-    __device__ uint32_t dempty(int i) const { return base + 240 + 8 * i; }
-    __device__ uint32_t jfull(int i) const { return base + 272 + 8 * i; }
-    static constexpr uint32_t kTmem = 336;
-    static constexpr uint32_t kDead = 340;  // a role gave up
-    static constexpr uint32_t kJobs = 344;  // kJobRing times (slot, valid rows)
-    static constexpr uint32_t kEnd = 408;   // Point: the end of the CTA's work
-    static constexpr uint32_t kDesc = 432;  // kDescs descriptors
+    __device__ uint32_t kvempty(int i) const { return base + 160 + 8 * i; }
+    __device__ uint32_t vraw(int i) const { return base + 208 + 8 * i; }
+    __device__ uint32_t dfull(int i) const { return base + 256 + 8 * i; }
+    __device__ uint32_t dempty(int i) const { return base + 288 + 8 * i; }
+    __device__ uint32_t jfull(int i) const { return base + 320 + 8 * i; }
+    static constexpr uint32_t kTmem = 384;
+    static constexpr uint32_t kDead = 388;  // a role gave up
+    static constexpr uint32_t kJobs = 392;  // kJobRing times (slot, valid rows)
+    static constexpr uint32_t kEnd = 456;   // Point: the end of the CTA's work
+    static constexpr uint32_t kDesc = 480;  // kDescs descriptors
 };
 static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= 1024, "barrier area");
 
@@ -136,6 +141,12 @@ __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
+}
+// shared memory (128-byte swizzle) to global; the issuing thread's bulk group
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int c0, int c1, int c2, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(m),
+                 "r"(src), "r"(c0), "r"(c1), "r"(c2)
+                 : "memory");
 }
 // two fp32 operations in one instruction
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -235,10 +246,10 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
     }
 }
 
-template <bool PAGED, bool DUAL>
+template <bool PAGED, bool DUAL, int RT>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
-    using L = Smem<DUAL>;
+    using L = Smem<DUAL, RT>;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     const Bars bars{base + L::kBars};
@@ -445,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after_sync();
             }
             const bool writer = !DUAL || s == d->writer, joins = DUAL && steps > 0 && others > 0;
-            if (warp_ok && (writer || joins)) {
+            if ((warp_ok || (!DUAL && d->whole && steps > 0)) && (writer || joins)) {
                 // In two parts of 64 channels: O from TMEM; the second stream of a join
                 // hands it over in shared memory; the writer stores the sum, or stages it
                 // (as 128 bytes of a row in this stream's Q tile, whose products are done).
@@ -453,7 +464,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float2 *const box_ml = reinterpret_cast<float2 *>(sm + L::kMl) + r;
                 const int join_bar = 1 + quad;  // the two warps of these 32 rows
                 const int q0 = d->q0 + (DUAL ? 0 : s * a.tile_tokens), row0 = d->h * a.G;
-                unsigned char *const stage = sm + L::kQ + d->q[s] % L::kQs * kTileBytes;
+                // A full row tile goes out by two tensor copies, in the layout of Q; the rows
+                // of a short one (next to them may lie another sequence's) by the warps.
+                const bool full = !DUAL && d->tokens[s] == a.tile_tokens;
+                unsigned char *const stage = sm + L::kQ + d->q[s] % L::kQs * L::kQTile;
                 float f = 1.f, f1 = 0.f;
 #pragma unroll 1
                 for (int p = 0; p < 2; ++p) {
@@ -463,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (p == 0) *box_ml = make_float2(m, l);
 #pragma unroll
                         for (int q = 0; q < 16; ++q)
-                            box[128 * q] = make_float4(
+                            box[RT * q] = make_float4(
                                 __uint_as_float(o[q / 4][4 * (q % 4)]), __uint_as_float(o[q / 4][4 * (q % 4) + 1]),
                                 __uint_as_float(o[q / 4][4 * (q % 4) + 2]), __uint_as_float(o[q / 4][4 * (q % 4) + 3]));
                         named_bar(join_bar, 64);  // handed over
@@ -482,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
-                            const float4 y = box[128 * q];
+                            const float4 y = box[RT * q];
                             uint32_t *z = &o[q / 4][4 * (q % 4)];
                             z[0] = __float_as_uint(f * __uint_as_float(z[0]) + f1 * y.x);
                             z[1] = __float_as_uint(f * __uint_as_float(z[1]) + f1 * y.y);
@@ -519,8 +533,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 4; ++e)
                             w[e] = pack_bf16(inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e]),
                                              inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e + 1]));
-                        *reinterpret_cast<uint4 *>(stage + r * 256 + (((8 * p + i) ^ (r & 15)) * 16)) =
-                            make_uint4(w[0], w[1], w[2], w[3]);
+                        const int at = full ? p * L::kQHalf + r * 128 + ((i ^ (r & 7)) * 16)
+                                            : r * 256 + (((8 * p + i) ^ (r & 15)) * 16);
+                        *reinterpret_cast<uint4 *>(stage + at) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 if (writer && !d->whole) {
@@ -528,7 +543,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (writer) {
                     if (row_ok && a.lse != nullptr)
                         a.lse[(size_t)(q0 + tok) * a.Hq + row0 + g] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
-                    if (steps > 0) {
+                    if (steps > 0 && full) {
+                        tc::fence_async_smem();
+                        named_bar(1 + s, 128);  // the stream's four warps have staged their rows
+                        if (quad == 0 && lane == 0) {
+                            const uint32_t src = base + L::kQ + d->q[s] % L::kQs * L::kQTile;
+                            tma_store_3d(&maps.out, 0, row0, q0, src);
+                            tma_store_3d(&maps.out, 64, row0, q0, src + L::kQHalf);
+                            tc::bulk_commit();
+                            tc::bulk_wait_read();  // then the tile may take the next Q
+                        }
+                    } else if (steps > 0) {
                         __syncwarp();
                         // sixteen lanes write a row's 256 bytes
                         const int rows = d->tokens[s] * a.G, ch = lane & 15;
@@ -555,6 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++nd;
         }
+        if (lane == 0) tc::bulk_wait_all();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
         if (warp == kWarpSched) {
@@ -658,10 +684,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alive = false;
                     return;
                 }
-                const uint32_t dst = base + L::kQ + slot * kTileBytes, bar = bars.qfull(slot);
+                const uint32_t dst = base + L::kQ + slot * L::kQTile, bar = bars.qfull(slot);
                 expect_tx(lead, bar, qbytes);
                 tma_3d(lead, dst, &maps.q, 0, h * a.G, tok, bar);
-                tma_3d(lead, dst + kHalf, &maps.q, 64, h * a.G, tok, bar);
+                tma_3d(lead, dst + L::kQHalf, &maps.q, 64, h * a.G, tok, bar);
                 __syncwarp();
             };
             Load x1, x2;  // the last two K tiles
@@ -753,12 +779,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t slot = (uint32_t)i % L::kQs;
                 if (first && alive) alive = warp_wait(bars.qfull(slot), ((uint32_t)i / L::kQs) & 1);
                 if (!alive) return;
-                const uint64_t qd = q_desc + slot * (kTileBytes >> 4);
+                const uint64_t qd = q_desc + slot * (L::kQTile >> 4);
                 const uint64_t kd = k_desc + (at % L::kRing) * (kTileBytes >> 4);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-                    tc::mma_f16_lead(lead, tm + kColS + 128 * s, qd + off, kd + off, kIdQK, kk > 0);
+                    const uint32_t k16 = (kk & 3) * 32, half = kk >> 2;
+                    tc::mma_f16_lead(lead, tm + kColS + 128 * s, qd + ((half * L::kQHalf + k16) >> 4),
+                                     kd + ((half * kHalf + k16) >> 4), kIdQK, kk > 0);
                 }
                 tc::mma_commit_lead(lead, bars.sfull(s));
             };
@@ -890,7 +917,7 @@ bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-template <bool PAGED, bool DUAL>
+template <bool PAGED, bool DUAL, int RT>
 cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
     a.streams = DUAL ? 1 : 2;
     // An item's start and end cost about two key tiles; a join about four.
@@ -900,17 +927,17 @@ cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, c
     set_unit(a, (double)slots * ((double)keys + a.extra + kTile));
     a.cut = 4;
     a.direct = slots <= a.sms && keys <= (long long)(2 * a.cut - 1) * kTile;
-    constexpr int bytes = Smem<DUAL>::kBytes;
+    constexpr int bytes = Smem<DUAL, RT>::kBytes;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        e = cudaFuncSetAttribute(attn_tc_kernel<PAGED, DUAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(attn_tc_kernel<PAGED, DUAL, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    attn_tc_kernel<PAGED, DUAL><<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kThreads, bytes, stream>>>(a, maps);
+    attn_tc_kernel<PAGED, DUAL, RT><<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kThreads, bytes, stream>>>(a, maps);
     e = cudaGetLastError();
     return e == cudaSuccess && !a.direct ? launch_attn_combine(a, true, stream) : e;
 }
@@ -922,10 +949,11 @@ cudaError_t launch_attn_prefill_tc(Args a, const void *q, const void *k, const v
     Maps m{};
     if (!map3(&m.q, q, a.Hq, a.Tq_total, ldq, a.G, a.tile_tokens) ||
         !map3(&m.k, k, a.Hkv, a.Tk_total, ldk, 1, kTile) ||
-        !map3(&m.v, v, a.Hkv, a.Tk_total, ldv, 1, kTile))
+        !map3(&m.v, v, a.Hkv, a.Tk_total, ldv, 1, kTile) ||
+        !map3(&m.out, a.out, a.Hq, a.Tq_total, (long long)a.Hq * kD, a.G, a.tile_tokens))
         return cudaErrorInvalidValue;
     const long long slots = ((long long)a.Tq_total / (2 * a.tile_tokens) + a.N) * a.Hkv;
-    return launch<false, false>(a, m, slots, a.Tk, stream);
+    return launch<false, false, 128>(a, m, slots, a.Tk, stream);
 }
 
 cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const void *vp, const void *kn,
@@ -939,13 +967,16 @@ cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const v
         !map2(&m.k, kp, rows, a.page < kTile ? a.page : kTile) ||
         !map2(&m.v, vp, rows, a.page < kTile ? a.page : kTile))
         return cudaErrorInvalidValue;
+    if (!dual && !map3(&m.out, a.out, a.Hq, toks, (long long)a.Hq * kD, a.G, a.tile_tokens)) return cudaErrorInvalidValue;
     if (a.has_new && (!map3(&m.kn, kn, a.Hkv, toks, ldk, 1, kMaxDrafts) ||
                       !map3(&m.vn, vn, a.Hkv, toks, ldv, 1, kMaxDrafts)))
         return cudaErrorInvalidValue;
     const int block = a.tile_tokens * (dual ? 1 : 2);
     const long long slots = (long long)a.N * a.Hkv * ((a.T + block - 1) / block);
     const long long keys = (long long)a.table_cols * a.page + kTile;
-    return dual ? launch<true, true>(a, m, slots, keys, stream) : launch<true, false>(a, m, slots, keys, stream);
+    if (!dual) return launch<true, false, 128>(a, m, slots, keys, stream);
+    if (a.T * a.G <= 32) return launch<true, true, 32>(a, m, slots, keys, stream);
+    return launch<true, true, 128>(a, m, slots, keys, stream);
 }
 
 }  // namespace attn
