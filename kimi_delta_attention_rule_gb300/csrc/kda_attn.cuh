@@ -220,7 +220,7 @@ __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n
 // before everything else that a CTA does, from a cold instruction cache: short code
 // counts more than few operations.)
 template <bool PAGED, int KT>
-__device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq &s0) {
+__device__ __noinline__ bool split_point(const Args &a, int c, Point &p0, Seq &s0) {
     const int lane = threadIdx.x & 31;
     constexpr int kFlight = PAGED ? 4 : 1;  // groups of 32 sequences whose loads are in flight together
     uint32_t w[kFlight], total = 0;

@@ -44,7 +44,7 @@ constexpr int kMinPart = kTcMinPart;
 constexpr int kTile = 128;      // rows of a row tile, keys of a key tile
 constexpr uint32_t kTileBytes = 32768;  // 128 rows x 128 channels bf16, two 64-channel halves
 constexpr uint32_t kHalf = 16384;
-constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr long long kWaitNs = 2000000000;
 constexpr float kRescale = 8.f;  // log2 growth of a maximum that rescales O
 constexpr int kJobRing = 8;  // more than the ring has slots: a job holds its slot until it is done
 
@@ -70,18 +70,21 @@ struct Desc {
     int tokens[2];         // valid tokens of its row tile
 };
 
-// Shared memory: Q tiles of RT rows, (DUAL) the box for the join of the two streams
-// (RT rows x 64 channels fp32), the ring of K and V tiles, barriers and descriptors.
+// Shared memory: two Q tiles of RT rows, 32 KB for the way out (DUAL: the box for the
+// join of the two streams, RT rows x 64 channels fp32, and the rows are staged in the
+// Q tile; else both streams stage there, and their Q tiles are free for the next part
+// once the last Q K^T is through), the ring of K and V tiles, barriers, descriptors.
 // With RT = 32 (a decode step's rows, as a rule) the ring has six tiles: 192 KB in
 // flight instead of 128 hide the latency of a chain of short sequences. The products
 // read 128 rows of Q all the same; what lies behind the tile gives rows of S and O
 // that nobody looks at.
 template <bool DUAL, int RT>
 struct Smem {
-    static constexpr int kQs = DUAL ? 2 : 3, kRing = RT == 32 ? 6 : 4;
+    static constexpr int kQs = 2, kRing = RT == 32 ? 6 : 4;
     static constexpr uint32_t kQTile = RT * 256, kQHalf = RT * 128;
     static constexpr uint32_t kQ = 0;
-    static constexpr uint32_t kJoin = kQs * kQTile;  // DUAL only
+    static constexpr uint32_t kJoin = kQs * kQTile;   // DUAL only
+    static constexpr uint32_t kStage = kQs * kQTile;  // not DUAL: 64 channels of each stream's row tile
     static constexpr uint32_t kKv = 3 * kQTile;
     static constexpr uint32_t kBars = kKv + kRing * kTileBytes;
     static constexpr uint32_t kMl = kBars + 1024;  // DUAL: the second stream's m and l
@@ -91,21 +94,21 @@ struct Smem {
 struct Bars {  // shared-memory addresses
     uint32_t base;
     __device__ uint32_t qfull(int i) const { return base + 8 * i; }
-    __device__ uint32_t qempty(int i) const { return base + 24 + 8 * i; }
-    __device__ uint32_t sfull(int s) const { return base + 48 + 8 * s; }
-    __device__ uint32_t pready(int s, int half) const { return base + 64 + 16 * half + 8 * s; }
-    __device__ uint32_t ofull(int s) const { return base + 96 + 8 * s; }
-    __device__ uint32_t kvfull(int i) const { return base + 112 + 8 * i; }
-    __device__ uint32_t kvempty(int i) const { return base + 160 + 8 * i; }
-    __device__ uint32_t vraw(int i) const { return base + 208 + 8 * i; }
-    __device__ uint32_t dfull(int i) const { return base + 256 + 8 * i; }
-    __device__ uint32_t dempty(int i) const { return base + 288 + 8 * i; }
-    __device__ uint32_t jfull(int i) const { return base + 320 + 8 * i; }
-    static constexpr uint32_t kTmem = 384;
-    static constexpr uint32_t kDead = 388;  // a role gave up
-    static constexpr uint32_t kJobs = 392;  // kJobRing times (slot, valid rows)
-    static constexpr uint32_t kEnd = 456;   // Point: the end of the CTA's work
-    static constexpr uint32_t kDesc = 480;  // kDescs descriptors
+    __device__ uint32_t qempty(int i) const { return base + 32 + 8 * i; }
+    __device__ uint32_t sfull(int s) const { return base + 64 + 8 * s; }
+    __device__ uint32_t pready(int s, int half) const { return base + 80 + 16 * half + 8 * s; }
+    __device__ uint32_t ofull(int s) const { return base + 112 + 8 * s; }
+    __device__ uint32_t kvfull(int i) const { return base + 128 + 8 * i; }
+    __device__ uint32_t kvempty(int i) const { return base + 176 + 8 * i; }
+    __device__ uint32_t vraw(int i) const { return base + 224 + 8 * i; }
+    __device__ uint32_t dfull(int i) const { return base + 272 + 8 * i; }
+    __device__ uint32_t dempty(int i) const { return base + 304 + 8 * i; }
+    __device__ uint32_t jfull(int i) const { return base + 336 + 8 * i; }
+    static constexpr uint32_t kTmem = 400;
+    static constexpr uint32_t kDead = 404;  // a role gave up
+    static constexpr uint32_t kJobs = 408;  // kJobRing times (slot, valid rows)
+    static constexpr uint32_t kEnd = 472;   // Point: the end of the CTA's work
+    static constexpr uint32_t kDesc = 496;  // kDescs descriptors
 };
 static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= 1024, "barrier area");
 
@@ -164,18 +167,26 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
     return d;
 }
-// A bounded wait. (The clock is read once in 4096 tries: a read takes as long as
-// much of what is waited for.)
+// A bounded wait: true once the phase is through, false after two seconds. (The
+// clock is read once in 1024 tries: a read takes as long as much of what is waited
+// for. Written out, since it stands in many places and all code here is fetched cold.)
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
-    if (tc::mbar_try_wait(bar, parity)) return true;
-    uint64_t t0 = 0;
-    for (uint32_t i = 1;; ++i) {
-        if (tc::mbar_try_wait(bar, parity)) return true;
-        if (i % 4096 != 0) continue;
-        const uint64_t now = tc::globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        else if (now - t0 > kWaitNs) return false;
-    }
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p, q;\n .reg .u32 n, r;\n .reg .u64 t0, t;\n"
+        " mov.u32 n, 0;\n mov.u64 t0, 0;\n"
+        "WAIT:\n"
+        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " @p bra DONE;\n"
+        " add.u32 n, n, 1;\n and.b32 r, n, 1023;\n setp.ne.u32 q, r, 0;\n @q bra WAIT;\n"
+        " mov.u64 t, %%globaltimer;\n"
+        " setp.eq.u64 q, t0, 0;\n @q mov.u64 t0, t;\n"
+        " sub.u64 t, t, t0;\n setp.lt.u64 q, t, %3;\n @q bra WAIT;\n"
+        "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "n"(kWaitNs)
+        : "memory");
+    return ok != 0;
 }
 // whether a phase is through, without waiting
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
@@ -269,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             for (int i = 0; i < L::kQs; ++i) {
                 tc::mbar_init(bars.qfull(i), 1);
-                tc::mbar_init(bars.qempty(i), 4);  // the softmax warps of one stream
+                tc::mbar_init(bars.qempty(i), DUAL ? 4 : 1);  // DUAL: the writer's warps; else the products
             }
             for (int i = 0; i < 2; ++i) {
                 tc::mbar_init(bars.sfull(i), 1);
@@ -372,15 +383,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (warp_ok) {
                     uint32_t x[8][16];
                     tc::tmem_ld_cols<8>(tS, x);
-                    if (PAGED && t == draft_tile) {
-#pragma unroll
-                        for (int i = 0; i < kTile; ++i)
-                            if (i >= kMaxDrafts || !((bits >> i) & 1)) x[i / 16][i % 16] = 0xff800000u;
-                    } else if (seen0 < (t + 1) * kTile) {
+                    const bool drafts = PAGED && t == draft_tile;
+                    if (drafts || seen0 < (t + 1) * kTile) {
+                        // the keys that this row sees, a bit each
                         const int lim = seen - t * kTile;
 #pragma unroll
-                        for (int i = 0; i < kTile; ++i)
-                            if (i >= lim) x[i / 16][i % 16] = 0xff800000u;
+                        for (int i = 0; i < 4; ++i) {
+                            uint32_t see = lim >= 32 * i + 32 ? ~0u : (lim <= 32 * i ? 0u : (1u << (lim & 31)) - 1);
+                            if (PAGED && drafts) see = i == 0 ? (uint32_t)bits : (i == 1 ? (uint32_t)(bits >> 32) : 0u);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!(see >> e & 1)) x[2 * i + e / 16][e % 16] = 0xff800000u;
+                        }
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -459,15 +473,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((warp_ok || (!DUAL && d->whole && steps > 0)) && (writer || joins)) {
                 // In two parts of 64 channels: O from TMEM; the second stream of a join
                 // hands it over in shared memory; the writer stores the sum, or stages it
-                // (as 128 bytes of a row in this stream's Q tile, whose products are done).
+                // for whole rows to leave together.
                 float4 *const box = reinterpret_cast<float4 *>(sm + L::kJoin) + r;
                 float2 *const box_ml = reinterpret_cast<float2 *>(sm + L::kMl) + r;
                 const int join_bar = 1 + quad;  // the two warps of these 32 rows
                 const int q0 = d->q0 + (DUAL ? 0 : s * a.tile_tokens), row0 = d->h * a.G;
-                // A full row tile goes out by two tensor copies, in the layout of Q; the rows
-                // of a short one (next to them may lie another sequence's) by the warps.
+                // A full row tile goes out by tensor copies, in the layout of Q; the rows of a
+                // short one (next to them may lie another sequence's) by the warps.
                 const bool full = !DUAL && d->tokens[s] == a.tile_tokens;
-                unsigned char *const stage = sm + L::kQ + d->q[s] % L::kQs * L::kQTile;
+                const uint32_t stage_at = DUAL ? L::kQ + d->q[s] % L::kQs * L::kQTile : L::kStage + s * kHalf;
+                unsigned char *const stage = sm + stage_at;
+                const bool leader = quad == 0 && lane == 0;
+                const int rows = d->tokens[s] * a.G;
+                __nv_bfloat16 *const out = static_cast<__nv_bfloat16 *>(a.out);
                 float f = 1.f, f1 = 0.f;
 #pragma unroll 1
                 for (int p = 0; p < 2; ++p) {
@@ -526,6 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         continue;
                     }
+                    if (!DUAL) {  // the stage is free when its last copy has read it
+                        if (leader) tc::bulk_wait_read();
+                        named_bar(1 + s, 128);
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         uint32_t w[4];
@@ -533,9 +555,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int e = 0; e < 4; ++e)
                             w[e] = pack_bf16(inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e]),
                                              inv * __uint_as_float(o[i / 2][8 * (i % 2) + 2 * e + 1]));
-                        const int at = full ? p * L::kQHalf + r * 128 + ((i ^ (r & 7)) * 16)
-                                            : r * 256 + (((8 * p + i) ^ (r & 15)) * 16);
+                        const int at = DUAL ? r * 256 + (((8 * p + i) ^ (r & 15)) * 16) : r * 128 + ((i ^ (r & 7)) * 16);
                         *reinterpret_cast<uint4 *>(stage + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (DUAL) continue;
+                    if (full) {
+                        tc::fence_async_smem();
+                        named_bar(1 + s, 128);  // the stream's four warps have staged their rows
+                        if (leader) {
+                            tma_store_3d(&maps.out, 64 * p, row0, q0, base + stage_at);
+                            tc::bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        const int ch = lane & 7;  // eight lanes write 128 bytes of a row
+#pragma unroll 4
+                        for (int i = 0; i < 32; i += 4) {
+                            const int row = 32 * quad + i + (lane >> 3), tk = (int)(row * inv_g >> 16);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(stage + row * 128 + ((ch ^ (row & 7)) * 16));
+                            if (row < rows)
+                                reinterpret_cast<uint4 *>(out + ((size_t)(q0 + tk) * a.Hq + row0 + (row - tk * a.G)) * kD + 64 * p)[ch] = y;
+                        }
                     }
                 }
                 if (writer && !d->whole) {
@@ -543,21 +583,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else if (writer) {
                     if (row_ok && a.lse != nullptr)
                         a.lse[(size_t)(q0 + tok) * a.Hq + row0 + g] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
-                    if (steps > 0 && full) {
-                        tc::fence_async_smem();
-                        named_bar(1 + s, 128);  // the stream's four warps have staged their rows
-                        if (quad == 0 && lane == 0) {
-                            const uint32_t src = base + L::kQ + d->q[s] % L::kQs * L::kQTile;
-                            tma_store_3d(&maps.out, 0, row0, q0, src);
-                            tma_store_3d(&maps.out, 64, row0, q0, src + L::kQHalf);
-                            tc::bulk_commit();
-                            tc::bulk_wait_read();  // then the tile may take the next Q
-                        }
-                    } else if (steps > 0) {
+                    if (DUAL && steps > 0) {
                         __syncwarp();
-                        // sixteen lanes write a row's 256 bytes
-                        const int rows = d->tokens[s] * a.G, ch = lane & 15;
-                        __nv_bfloat16 *const out = static_cast<__nv_bfloat16 *>(a.out);
+                        const int ch = lane & 15;  // sixteen lanes write a row's 256 bytes
 #pragma unroll 4
                         for (int i = 0; i < 32; i += 2) {
                             const int row = 32 * quad + i + (lane >> 4), tk = (int)(row * inv_g >> 16);
@@ -570,12 +598,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // O is read: the MMA warp's next P V waits for this warp's next P.
-            // The Q tile (the staging's too) goes back to the TMA warp.
+            // DUAL: the Q tile (the staging's too) goes back to the TMA warp.
             tc::fence_before_sync();
             tc::fence_async_smem();
             __syncwarp();
             if (lane == 0) {
-                if (steps > 0 && writer) mbar_arrive(bars.qempty(d->q[s] % L::kQs));
+                if (DUAL && steps > 0 && writer) mbar_arrive(bars.qempty(d->q[s] % L::kQs));
                 mbar_arrive(bars.dempty(nd % kDescs));
             }
             ++nd;
@@ -632,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!PAGED || (lane << row_bits) >= kTile || pos >= Lk) return -1;
                 return __ldg(a.table + (size_t)n * a.table_ld + (pos >> page_bits));
             };
-            auto load = [&](const Load &x, bool is_v) {
+            auto load = [&](const Load x, bool is_v) {
                 const uint32_t slot = kv % L::kRing;
                 const uint32_t dst = base + L::kKv + slot * kTileBytes;
                 if (kv >= (uint32_t)L::kRing && !warp_wait(bars.kvempty(slot), (kv / L::kRing - 1) & 1)) {
@@ -653,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tma_3d(lead, dst + kHalf, m, 64, x.h, x.k0 + x.t * kTile, bar);
                 } else if (x.draft) {
                     const CUtensorMap *mn = is_v ? &maps.vn : &maps.kn;
-                    expect_tx(lead, bar, 64 * 256);
+                    expect_tx(lead, bar, (uint32_t)((a.T + 7) & ~7) * 256u);
                     tma_3d(lead, dst, mn, 0, x.h, x.n * a.T, bar);
                     tma_3d(lead, dst + kHalf, mn, 64, x.h, x.n * a.T, bar);
                 } else {
@@ -690,31 +718,48 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_3d(lead, dst + L::kQHalf, &maps.q, 64, h * a.G, tok, bar);
                 __syncwarp();
             };
-            Load x1, x2;  // the last two K tiles
-            x1.pg = x2.pg = -1;
+            Load x = {}, x1 = {}, x2 = {};  // this K tile and the last two
             uint32_t peeked = 0;  // descriptors whose first pages are looked up
-            int peek_pg = -1, peek_pg2 = -1;
-            while (const Desc *d = next_desc()) {
-                const int c0 = d->count[0], c1 = d->count[1];
-                const int tiles = DUAL ? c0 + c1 : (c0 > c1 ? c0 : c1);
-                Load x;
-                x.n = d->n;
-                x.h = d->h;
-                x.k0 = d->k0;
-                x.Lk = d->Lk;
-                const int ta = d->ta, draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
-                int next_pg = peek_pg, next_pg2 = peek_pg2;
-                if (PAGED && peeked != nd + 1) {
-                    next_pg = page_of(x.n, x.Lk, ta);
-                    next_pg2 = page_of(x.n, x.Lk, ta + 1);
+            int peek_pg = -1, peek_pg2 = -1, next_pg = -1, next_pg2 = -1;
+            int left = 0, flush = kLag, draft_tile = -1, q_first = 0;
+            const Desc *d = nullptr;
+            bool more = true;
+            while (alive) {
+                while (left == 0 && more) {  // the next part
+                    d = next_desc();
+                    more = d != nullptr;
+                    if (!more) break;
+                    const int n0 = d->count[0], n1 = d->count[1];
+                    left = DUAL ? n0 + n1 : (n0 > n1 ? n0 : n1);
+                    if (left == 0) {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
+                        ++nd;
+                        continue;
+                    }
+                    x.n = d->n;
+                    x.h = d->h;
+                    x.k0 = d->k0;
+                    x.Lk = d->Lk;
+                    x.t = d->ta - 1;
+                    draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
+                    q_first = 1;
+                    next_pg = peek_pg;
+                    next_pg2 = peek_pg2;
+                    if (PAGED && peeked != nd + 1) {
+                        next_pg = page_of(x.n, x.Lk, d->ta);
+                        next_pg2 = page_of(x.n, x.Lk, d->ta + 1);
+                    }
                 }
-                for (int j = 0; j < tiles && alive; ++j, ++g) {
-                    x.t = ta + j;
+                if (!alive || (left == 0 && flush-- == 0)) break;
+                const bool has_k = left > 0;
+                if (has_k) {
+                    ++x.t;
                     x.draft = PAGED && x.t == draft_tile;
                     x.pg = next_pg;  // looked up two tiles ahead
                     next_pg = next_pg2;
                     next_pg2 = page_of(x.n, x.Lk, x.t + 2);
-                    if (PAGED && j == tiles - 1 &&
+                    if (PAGED && left == 1 &&
                         __all_sync(0xffffffffu, mbar_test(bars.dfull((nd + 1) % kDescs), ((nd + 1) / kDescs) & 1))) {
                         const Desc *e = descs + (nd + 1) % kDescs;
                         if (!e->last) {
@@ -723,20 +768,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                             peeked = nd + 2;
                         }
                     }
-                    if (g >= (uint32_t)kLag) load(DUAL ? x2 : x1, true);
-                    if (j == 0 && alive && (DUAL || c0 > 0)) load_q(d->q[0], d->q0, x.h);
-                    if (alive) load(x, false);
-                    if (!DUAL && j == 0 && alive && c1 > 0) load_q(d->q[1], d->q0 + a.tile_tokens, x.h);
-                    x2 = x1;
-                    x1 = x;
                 }
-                if (!alive) break;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
-                ++nd;
+                // V of kLag tiles ago, then this K tile, a part's Q tiles around its first
+#pragma unroll 1
+                for (int is_k = g < (uint32_t)kLag; is_k < 1 + has_k && alive; ++is_k) {
+                    if (is_k && q_first && (DUAL || d->count[0] > 0)) load_q(d->q[0], d->q0, x.h);
+                    if (alive) load(is_k ? x : (DUAL ? x2 : x1), !is_k);
+                }
+                if (!DUAL && q_first && alive && d->count[1] > 0) load_q(d->q[1], d->q0 + a.tile_tokens, x.h);
+                q_first = 0;
+                x2 = x1;
+                x1 = x;
+                ++g;
+                if (has_k && --left == 0) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
+                    ++nd;
+                }
             }
-            if (DUAL && alive && g >= 2) load(x2, true);
-            if (alive && g >= 1) load(x1, true);
             if (lane == 0) {  // no further job
                 reinterpret_cast<int2 *>(sm + L::kBars + Bars::kJobs)[jobs % kJobRing] = make_int2(-1, 0);
                 mbar_arrive(bars.jfull(jobs % kJobRing));
@@ -775,7 +824,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             auto free_kv = [&](uint32_t at) { tc::mma_commit_lead(lead, bars.kvempty(at % L::kRing)); };
             // S_s = Q K^T with Q tile i; then the row tile's softmax may read it
-            auto qk = [&](int s, int i, bool first, uint32_t at) {
+            auto qk = [&](int s, int i, bool first, bool last, uint32_t at) {
                 const uint32_t slot = (uint32_t)i % L::kQs;
                 if (first && alive) alive = warp_wait(bars.qfull(slot), ((uint32_t)i / L::kQs) & 1);
                 if (!alive) return;
@@ -788,6 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      kd + ((half * kHalf + k16) >> 4), kIdQK, kk > 0);
                 }
                 tc::mma_commit_lead(lead, bars.sfull(s));
+                if (!DUAL && last) tc::mma_commit_lead(lead, bars.qempty(slot));
             };
             // O_s (+)= P V, each half of the keys once its P is there
             auto pv = [&](int s, uint32_t at, bool first, bool last) {
@@ -829,14 +879,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         kv = k + (d != nullptr);
                         if (at_j >= 0) wait_kv(v);
                         bool waited = false;
-#pragma unroll
+#pragma unroll 1
                         for (int s = 0; s < 2; ++s) {
                             const int before = s ? n1 : n0, now = s ? c1 : c0;
                             if (at_j >= 0 && at_j < before) pv(s, v, at_j == 0, at_j + 1 == before);
                             if (j < now) {
                                 if (!waited) wait_kv(k);
                                 waited = true;
-                                qk(s, s ? q1 : q0, j == 0, k);
+                                qk(s, s ? q1 : q0, j == 0, j + 1 == now, k);
                             }
                         }
                         if (!alive) break;
@@ -850,33 +900,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 // tile g is stream g % 2's: its P V of tile g - 2, then Q K^T of tile g
-                uint32_t g = 0;
-                bool first[2] = {true, true}, last[2] = {false, false};
-                auto finish = [&](int s) {
-                    const uint32_t v = kv++;
-                    wait_kv(v);
-                    pv(s, v, first[s], last[s]);
-                    if (alive) free_kv(v);
-                };
-                while (const Desc *d = next_desc()) {
-                    const int tiles = d->count[0] + d->count[1], q = d->q[0];
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
-                    ++nd;
-                    for (int j = 0; j < tiles && alive; ++j, ++g) {
-                        const int s = g & 1;
-                        if (g >= 2) finish(s);
+                uint32_t g = 0, flags = 0;  // per stream: its last tile was its part's first, last
+                int left = 0, j = 0, q = 0, tiles = 0, flush = 2;
+                bool more = true;
+                while (alive) {
+                    while (left == 0 && more) {  // the next part
+                        const Desc *d = next_desc();
+                        more = d != nullptr;
+                        if (!more) break;
+                        tiles = left = d->count[0] + d->count[1];
+                        q = d->q[0];
+                        j = 0;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
+                        ++nd;
+                    }
+                    if (!alive || (left == 0 && flush-- == 0)) break;
+                    const int s = g & 1;
+                    if (g >= 2) {
+                        const uint32_t v = kv++;
+                        wait_kv(v);
+                        pv(s, v, flags >> (2 * s) & 1, flags >> (2 * s + 1) & 1);
+                        if (!alive) break;
+                        free_kv(v);
+                    }
+                    if (left > 0) {
                         const uint32_t k = kv++;
                         wait_kv(k);
-                        qk(s, q, j < 2, k);
-                        if (alive) free_kv(k);
-                        first[s] = j < 2;
-                        last[s] = j + 2 >= tiles;
+                        qk(s, q, j < 2, false, k);
+                        if (!alive) break;
+                        free_kv(k);
+                        flags = (flags & ~(3u << (2 * s))) | ((uint32_t)(j < 2) | (uint32_t)(j + 2 >= tiles) << 1) << (2 * s);
+                        --left;
+                        ++j;
                     }
-                    if (!alive) break;
+                    ++g;
                 }
-                if (alive && g >= 2) finish(g & 1);
-                if (alive && g >= 1) finish((g + 1) & 1);
             }
         }
     }
@@ -968,8 +1027,8 @@ cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const v
         !map2(&m.v, vp, rows, a.page < kTile ? a.page : kTile))
         return cudaErrorInvalidValue;
     if (!dual && !map3(&m.out, a.out, a.Hq, toks, (long long)a.Hq * kD, a.G, a.tile_tokens)) return cudaErrorInvalidValue;
-    if (a.has_new && (!map3(&m.kn, kn, a.Hkv, toks, ldk, 1, kMaxDrafts) ||
-                      !map3(&m.vn, vn, a.Hkv, toks, ldv, 1, kMaxDrafts)))
+    const int drafts = (a.T + 7) & ~7;  // whole groups of eight rows of the swizzle
+    if (a.has_new && (!map3(&m.kn, kn, a.Hkv, toks, ldk, 1, drafts) || !map3(&m.vn, vn, a.Hkv, toks, ldv, 1, drafts)))
         return cudaErrorInvalidValue;
     const int block = a.tile_tokens * (dual ? 1 : 2);
     const long long slots = (long long)a.N * a.Hkv * ((a.T + block - 1) / block);
