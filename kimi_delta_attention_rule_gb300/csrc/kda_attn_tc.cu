@@ -15,8 +15,8 @@
 //
 // Each softmax thread owns one row (a TMEM lane), so no row statistic ever crosses
 // threads. Per stream S, P and the products form one serial chain, which is what
-// bounds the kernel: so P goes to the tensor core in two halves (the first half's
-// products run while the second half's exponentials do), and a part's first Q K^T
+// bounds the kernel: so P goes to the tensor core in two parts (96 keys' products run
+// while the last 32 keys' exponentials do), and a part's first Q K^T
 // follows the last P V of the part before it, under that part's epilogue. O is
 // rescaled only when a row's maximum grows by more than 2^8, which P in bf16
 // (rounded to nearest, relative step 2^-8) and l in fp32 hold without loss.
@@ -407,8 +407,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (j == 0) {
                         m = top;
                     } else {
-                        // (-inf - -inf is NaN: not greater, no rescale)
-                        const bool grow = (top - m) * c > kRescale;
+                        // (-inf - -inf is NaN: not greater, no rescale. Rows past the tile's own
+                        // hold anything: they have no say, or the bits would depend on it.)
+                        const bool grow = row_ok && (top - m) * c > kRescale;
                         if (__any_sync(0xffffffffu, grow)) {
                             const float up = fmaxf(m, top);
                             const float f = m == -INFINITY ? 0.f : ex2((m - up) * c);
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             w[i] = pack_bf16(y.x, y.y);
                         }
                         tc::tmem_st16u(tS + 16 * q, w);
-                        if (q == 1) {  // the first half's products may start
+                        if (q == 2) {  // the products of the first 96 keys may start
                             tc::tmem_wait_st();
                             tc::fence_before_sync();
                             __syncwarp();
@@ -839,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mma_commit_lead(lead, bars.sfull(s));
                 if (!DUAL && last) tc::mma_commit_lead(lead, bars.qempty(slot));
             };
-            // O_s (+)= P V, each half of the keys once its P is there
+            // O_s (+)= P V, keys 0 .. 95 and 96 .. 127 once their P is there
             auto pv = [&](int s, uint32_t at, bool first, bool last) {
                 const uint64_t vd = v_desc + (at % L::kRing) * (kTileBytes >> 4);
                 const uint32_t parity = (s ? np1++ : np0++) & 1;
@@ -849,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!alive) return;
                     tc::fence_after_sync();
 #pragma unroll
-                    for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                    for (int kk = half ? 6 : 0; kk < (half ? 8 : 6); ++kk)
                         tc::mma_f16_ta_lead(lead, tm + kColO + 128 * s, tm + kColS + 128 * s + 8 * kk,
                                             vd + ((kk * 2048) >> 4), kIdPV, !first || kk > 0);
                 }
@@ -979,12 +980,15 @@ bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
 template <bool PAGED, bool DUAL, int RT>
 cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
     a.streams = DUAL ? 1 : 2;
-    // An item's start and end cost about two key tiles; a join about four.
-    a.extra = 256;
+    // An item's start and end cost about one and a half key tiles (of 64 .. 256 tried,
+    // 192 is best on ragged prompts and no worse for decode); pieces of fewer than three
+    // tiles do not pay for their join (2: 10 % slower on short prompts, 4: 5 to 10 % on
+    // short caches).
+    a.extra = 192;
     a.min_part = kMinPart;
     // every item's keys, its start and end and, at the most, its drafts' tile
     set_unit(a, (double)slots * ((double)keys + a.extra + kTile));
-    a.cut = 4;
+    a.cut = 3;
     a.direct = slots <= a.sms && keys <= (long long)(2 * a.cut - 1) * kTile;
     constexpr int bytes = Smem<DUAL, RT>::kBytes;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
