@@ -1,8 +1,9 @@
 // Softmax attention in fp32 on CUDA cores (the formulas and the work split are
-// those of kda_attn.cuh): 128 threads hold 64 (token, head) rows; per tile of 64
-// keys a thread forms an 8 x 4 piece of S = Q K^T and an 8 x 8 piece of O += P V.
-// Bound by the FMA pipe: 12 shared loads of 16 bytes per 128 FMAs (S) and 16 per
-// 256 (O), two CTAs per SM so that one loads while the other multiplies.
+// those of kda_attn.cuh): 128 threads hold 64 (token, head) rows, or 32 or 8 where a
+// kv head has no more (RPT = 8, 4 or 1 rows per thread); per tile of 64 keys a thread forms
+// an RPT x 4 piece of S = Q K^T and an RPT x 8 piece of O += P V. Bound by the FMA
+// pipe: with RPT = 8, 12 shared loads of 16 bytes per 128 FMAs (S) and 16 per 256 (O),
+// two CTAs per SM so that one loads while the other multiplies.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -13,10 +14,10 @@ namespace kda {
 namespace attn {
 
 constexpr int kF32Threads = 128;
-constexpr int kF32Tile = 64;          // rows, and keys
+constexpr int kF32Tile = 64;          // keys; rows: 8 RPT
 constexpr int kPitch = kD + 4;        // floats per Q / K row: neighbouring rows on other banks
 constexpr int kPitchP = kF32Tile + 4;
-constexpr int kF32Smem = (2 * kF32Tile * kPitch + kF32Tile * kD) * 4;
+constexpr int f32_smem(int rpt) { return ((8 * rpt + kF32Tile) * kPitch + kF32Tile * kD) * 4; }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
@@ -33,10 +34,11 @@ struct F32Ptrs {
     long long ldq, ldk, ldv;           // decode: of kn, vn
 };
 
-template <bool PAGED>
+template <bool PAGED, int RPT>
 __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_constant__ Args a, const F32Ptrs io) {
     extern __shared__ __align__(16) float smf[];
-    float *const Qs = smf, *const Ks = smf + kF32Tile * kPitch, *const Vs = smf + 2 * kF32Tile * kPitch;
+    constexpr int kRows = 8 * RPT;
+    float *const Qs = smf, *const Ks = smf + kRows * kPitch, *const Vs = Ks + kF32Tile * kPitch;
     float *const Ps = Ks;  // P replaces K once S is formed
     __shared__ Point pts[2];
     __shared__ Seq seq0;
@@ -68,30 +70,30 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
     if (!any) return;
     Walk<PAGED, kF32Tile> walk;
     if (!a.direct) walk.init(pts[0], pts[1], seq0);
-    const int ty = tid >> 4, tx = tid & 15;  // rows 8 ty + i; keys tx + 16 e, channels 4 tx + 64 e
+    const int ty = tid >> 4, tx = tid & 15, lane = tid & 31, warp = tid >> 5;  // rows RPT ty + i; keys tx + 16 e, channels 4 tx + 64 e
     const float c = a.scale * kLog2e;
-    const int G = a.G;
+    const int G = a.G, page_bits = PAGED ? 31 - __clz(a.page) : 0;
     Part p = direct;
     for (bool more = a.direct || walk.next(a, p); more; more = !a.direct && walk.next(a, p)) {
         const int rows = p.tokens * G;
         __syncthreads();  // the last part's reads are done
-        for (int x = tid; x < kF32Tile * 32; x += kF32Threads) {
+        for (int x = tid; x < kRows * 32; x += kF32Threads) {
             const int r = x >> 5, ch = (x & 31) * 4, tok = r / G;
             const bool ok = r < rows;
             const float *src = io.q + (ok ? (long long)(p.q0 + tok) * io.ldq + (p.h * G + r - tok * G) * kD + ch : 0);
             cp16(smem_u32(Qs + r * kPitch + ch), src, ok);
         }
         cp_commit();
-        float m[8], l[8];
-        float4 o[8][2];
-        long long seen[8];  // keys that the row sees (of the cache: all)
-        unsigned long long bits[8];
+        float m[RPT], l[RPT];
+        float4 o[RPT][2];
+        long long seen[RPT];  // keys that the row sees (of the cache: all)
+        unsigned long long bits[RPT];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < RPT; ++i) {
             m[i] = -INFINITY;
             l[i] = 0.f;
             o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int r = 8 * ty + i, t = p.first_tok + r / G;
+            const int r = RPT * ty + i, t = p.first_tok + r / G;
             seen[i] = PAGED ? p.Lk : (long long)p.Lk - p.Lq + t + 1;
             bits[i] = 0;
             if (PAGED && r < rows) {
@@ -105,46 +107,51 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             // keys past the end load as zeros (0 times what is there could be NaN)
             const int valid = drafts ? a.T : min(kF32Tile, p.Lk - t * kF32Tile);
             __syncthreads();
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                for (int x = tid; x < kF32Tile * 32; x += kF32Threads) {
-                    const int r = x >> 5, ch = (x & 31) * 4;
-                    bool ok = r < valid;
-                    const float *src = io.q;
-                    if (ok) {
-                        if (!PAGED) {
-                            src = (kv ? io.v : io.k) +
-                                  (long long)(p.k0 + t * kF32Tile + r) * (kv ? io.ldv : io.ldk) + p.h * kD + ch;
-                        } else if (drafts) {
-                            src = (kv ? io.vn : io.kn) +
-                                  (long long)(p.n * a.T + r) * (kv ? io.ldv : io.ldk) + p.h * kD + ch;
-                        } else {
-                            const int pos = t * kF32Tile + r;
-                            const int pg = a.table[(size_t)p.n * a.table_ld + pos / a.page];
-                            if (pg < 0 || pg >= a.pages) {  // zeros instead
-                                atomicOr(status_word(a), kStatusBadSeqlens);
-                                ok = false;
-                            } else {
-                                src = (kv ? io.v : io.k) +
-                                      (((size_t)pg * a.Hkv + p.h) * a.page + pos % a.page) * kD + ch;
-                            }
-                        }
-                    }
-                    cp16(smem_u32(kv ? Vs + r * kD + ch : Ks + r * kPitch + ch), src, ok);
-                }
-                cp_commit();
+            // A warp copies the rows warp, warp + 4, ..: lane i finds where row warp + 4 i is.
+            const int mine = warp + 4 * (lane & 15);
+            bool ok = mine < valid;
+            long long at = 0, at_v = 0;
+            if (!PAGED) {
+                at = (long long)(p.k0 + t * kF32Tile + mine) * io.ldk;
+                at_v = (long long)(p.k0 + t * kF32Tile + mine) * io.ldv;
+            } else if (drafts) {
+                at = (long long)(p.n * a.T + mine) * io.ldk;
+                at_v = (long long)(p.n * a.T + mine) * io.ldv;
+            } else if (ok) {
+                const int pos = t * kF32Tile + mine;
+                const int pg = a.table[(size_t)p.n * a.table_ld + (pos >> page_bits)];
+                ok = pg >= 0 && pg < a.pages;
+                if (!ok) atomicOr(status_word(a), kStatusBadSeqlens);  // zeros instead
+                else at = at_v = (((long long)pg * a.Hkv) * a.page + (pos & (a.page - 1))) * kD;
             }
+            const long long head = (PAGED && !drafts ? (long long)p.h * a.page : p.h) * kD;
+            const float *const ksrc = (drafts ? io.kn : io.k) + head, *const vsrc = (drafts ? io.vn : io.v) + head;
+            const unsigned rows_ok = __ballot_sync(0xffffffffu, ok);
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const bool in = rows_ok >> i & 1;
+                const long long off = __shfl_sync(0xffffffffu, at, i);
+                cp16(smem_u32(Ks + (warp + 4 * i) * kPitch + 4 * lane), in ? ksrc + off + 4 * lane : io.q, in);
+            }
+            cp_commit();
+#pragma unroll 4
+            for (int i = 0; i < 16; ++i) {
+                const bool in = rows_ok >> i & 1;
+                const long long off = __shfl_sync(0xffffffffu, at_v, i);
+                cp16(smem_u32(Vs + (warp + 4 * i) * kD + 4 * lane), in ? vsrc + off + 4 * lane : io.q, in);
+            }
+            cp_commit();
             cp_wait<1>();
             __syncthreads();
-            float s[8][4] = {};
+            float s[RPT][4] = {};
 #pragma unroll 4
             for (int d = 0; d < kD; d += 4) {
                 float4 kk[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) kk[e] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * e) * kPitch + d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 qq = *reinterpret_cast<const float4 *>(Qs + (8 * ty + i) * kPitch + d);
+                for (int i = 0; i < RPT; ++i) {
+                    const float4 qq = *reinterpret_cast<const float4 *>(Qs + (RPT * ty + i) * kPitch + d);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         s[i][e] = fmaf(qq.x, kk[e].x, s[i][e]);
@@ -156,7 +163,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             }
             __syncthreads();  // K is read: P may replace it
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < RPT; ++i) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -176,7 +183,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                 for (int e = 0; e < 4; ++e) {
                     const float y = exp2f(fmaf(s[i][e], c, -uc));
                     sum += y;
-                    Ps[(8 * ty + i) * kPitchP + tx + 16 * e] = y;
+                    Ps[(RPT * ty + i) * kPitchP + tx + 16 * e] = y;
                 }
                 l[i] = l[i] * f + sum;  // this lane's keys; joined at the end
 #pragma unroll
@@ -198,8 +205,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                     for (int e = 0; e < 2; ++e)
                         vv[x][e] = *reinterpret_cast<const float4 *>(Vs + (key + x) * kD + 4 * tx + 64 * e);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 pp = *reinterpret_cast<const float4 *>(Ps + (8 * ty + i) * kPitchP + key);
+                for (int i = 0; i < RPT; ++i) {
+                    const float4 pp = *reinterpret_cast<const float4 *>(Ps + (RPT * ty + i) * kPitchP + key);
                     const float w[4] = {pp.x, pp.y, pp.z, pp.w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x)
@@ -215,10 +222,10 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
         }
         if (p.ta >= p.tb) cp_wait<0>();  // Q of a part without keys
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < RPT; ++i) {
 #pragma unroll
             for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
-            const int r = 8 * ty + i;
+            const int r = RPT * ty + i;
             if (r >= rows) continue;
             if (!p.whole()) {
                 const int slot = part_slot(cta, p);
@@ -250,21 +257,24 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
 
 cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
 
-template <bool PAGED>
+template <bool PAGED, int RPT>
 static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
+    constexpr int rows = 8 * RPT;
     a.streams = 1;
-    a.tile_tokens = PAGED && a.T * a.G < kF32Tile ? a.T : kF32Tile / a.G;
+    a.tile_tokens = PAGED && a.T * a.G < rows ? a.T : rows / a.G;
     a.extra = 64;
     a.min_part = kF32MinPart;
-    a.cut = 3;
+    a.cut = 1;
     const long long slots = PAGED ? (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens)
                                   : ((long long)a.Tq_total / a.tile_tokens + a.N) * a.Hkv;
     const long long keys = PAGED ? (long long)a.table_cols * a.page + kF32Tile : a.Tk;
     set_unit(a, (double)slots * ((double)keys + a.extra + kF32Tile));
-    a.direct = slots <= 2 * a.sms && keys <= (2 * a.cut - 1) * kF32Tile;
-    cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kF32Smem);
+    a.direct = slots <= 2 * a.sms && keys <= 2 * kF32Tile;
+    cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         f32_smem(RPT));
     if (e != cudaSuccess) return e;
-    attn_f32_kernel<PAGED><<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kF32Threads, kF32Smem, stream>>>(a, io);
+    attn_f32_kernel<PAGED, RPT>
+        <<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kF32Threads, f32_smem(RPT), stream>>>(a, io);
     e = cudaGetLastError();
     return e == cudaSuccess && !a.direct ? launch_attn_combine(a, false, stream) : e;
 }
@@ -273,14 +283,17 @@ cudaError_t launch_attn_prefill_f32(const Args &a, const void *q, const void *k,
                                     long long ldk, long long ldv, cudaStream_t stream) {
     const F32Ptrs io = {static_cast<const float *>(q), static_cast<const float *>(k), static_cast<const float *>(v),
                         nullptr, nullptr, ldq, ldk, ldv};
-    return launch_f32<false>(a, io, stream);
+    return launch_f32<false, 8>(a, io, stream);
 }
 cudaError_t launch_attn_decode_f32(const Args &a, const void *q, const void *kp, const void *vp, const void *kn,
                                    const void *vn, long long ldq, long long ldk, long long ldv,
                                    cudaStream_t stream) {
     const F32Ptrs io = {static_cast<const float *>(q), static_cast<const float *>(kp), static_cast<const float *>(vp),
                         static_cast<const float *>(kn), static_cast<const float *>(vn), ldq, ldk, ldv};
-    return launch_f32<true>(a, io, stream);
+    const int rows = a.T * a.G;
+    return rows <= 8    ? launch_f32<true, 1>(a, io, stream)
+           : rows <= 32 ? launch_f32<true, 4>(a, io, stream)
+                        : launch_f32<true, 8>(a, io, stream);
 }
 
 }  // namespace attn
