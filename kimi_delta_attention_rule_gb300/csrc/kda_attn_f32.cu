@@ -143,7 +143,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             cp_commit();
             cp_wait<1>();
             __syncthreads();
-            float s[RPT][4] = {};
+            // (two terms of a dot product per instruction, as two sums: half the issue slots)
+            float2 s2[RPT][4] = {};
 #pragma unroll 4
             for (int d = 0; d < kD; d += 4) {
                 float4 kk[4];
@@ -154,13 +155,16 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                     const float4 qq = *reinterpret_cast<const float4 *>(Qs + (RPT * ty + i) * kPitch + d);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[i][e] = fmaf(qq.x, kk[e].x, s[i][e]);
-                        s[i][e] = fmaf(qq.y, kk[e].y, s[i][e]);
-                        s[i][e] = fmaf(qq.z, kk[e].z, s[i][e]);
-                        s[i][e] = fmaf(qq.w, kk[e].w, s[i][e]);
+                        s2[i][e] = fma2(make_float2(qq.x, qq.y), make_float2(kk[e].x, kk[e].y), s2[i][e]);
+                        s2[i][e] = fma2(make_float2(qq.z, qq.w), make_float2(kk[e].z, kk[e].w), s2[i][e]);
                     }
                 }
             }
+            float s[RPT][4];
+#pragma unroll
+            for (int i = 0; i < RPT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][e] = s2[i][e].x + s2[i][e].y;
             __syncthreads();  // K is read: P may replace it
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
@@ -209,14 +213,15 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                     const float4 pp = *reinterpret_cast<const float4 *>(Ps + (RPT * ty + i) * kPitchP + key);
                     const float w[4] = {pp.x, pp.y, pp.z, pp.w};
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
+                    for (int x = 0; x < 4; ++x) {
+                        const float2 w2 = make_float2(w[x], w[x]);
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            o[i][e].x = fmaf(w[x], vv[x][e].x, o[i][e].x);
-                            o[i][e].y = fmaf(w[x], vv[x][e].y, o[i][e].y);
-                            o[i][e].z = fmaf(w[x], vv[x][e].z, o[i][e].z);
-                            o[i][e].w = fmaf(w[x], vv[x][e].w, o[i][e].w);
+                            const float2 lo = fma2(w2, make_float2(vv[x][e].x, vv[x][e].y), make_float2(o[i][e].x, o[i][e].y));
+                            const float2 hi = fma2(w2, make_float2(vv[x][e].z, vv[x][e].w), make_float2(o[i][e].z, o[i][e].w));
+                            o[i][e] = make_float4(lo.x, lo.y, hi.x, hi.y);
                         }
+                    }
                 }
             }
         }

@@ -151,22 +151,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int c0, int c
                  "r"(src), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
-// two fp32 operations in one instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;\n"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
-          "l"(reinterpret_cast<uint64_t &>(c)));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("add.rn.f32x2 %0, %1, %2;\n"
-        : "=l"(reinterpret_cast<uint64_t &>(d))
-        : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
-    return d;
-}
 // A bounded wait: true once the phase is through, false after two seconds. (The
 // clock is read once in 1024 tries: a read takes as long as much of what is waited
 // for. Written out, since it stands in many places and all code here is fetched cold.)
