@@ -101,10 +101,12 @@ struct Args {
     int ctas, sms;           // CTAs that share the work; SMs of the device
 };
 
-// The unit of weight: `keys` is an upper bound of a call's work in keys.
+// The unit of weight: `keys` is an upper bound of a call's work in keys, of at most
+// kMaxItems items.
+constexpr long long kMaxItems = 1LL << 29;
 inline void set_unit(Args &a, double keys) {
     a.unit = 1.f;
-    while (keys / a.unit > 1e9) a.unit *= 2.f;
+    while (keys / a.unit > 5e8) a.unit *= 2.f;
     a.inv_unit = 1.f / a.unit;
 }
 
@@ -177,8 +179,9 @@ __device__ __forceinline__ int item_tiles(const Args &a, const Seq &s, int i) {
 }
 // Weight of items 0 .. i - 1 of one kv head: an arithmetic series of visible keys and
 // `extra` keys per item, in units of a.unit keys, which the host chooses so that a
-// call's total stays below 2^30. Formed in fp32: every operation rounds
-// monotonically, so the weights rise with i, and all that follows is in whole units.
+// call's total stays below 2^30, and one unit per item, so that no item weighs
+// nothing. Formed in fp32: every operation rounds monotonically, so the weights rise
+// with i, and all that follows is in whole units.
 template <bool PAGED, int KT>
 __device__ __forceinline__ uint32_t items_weight(const Args &a, const Seq &s, int i) {
     float w;
@@ -193,7 +196,7 @@ __device__ __forceinline__ uint32_t items_weight(const Args &a, const Seq &s, in
         w = (float)i * (float)a.extra + count * fmaf(0.5f * block, (float)full + unseen + 1.f, (float)d);
         if (i >= s.ni) w += (float)s.Lk;
     }
-    return (uint32_t)(fmaxf(w, 0.f) * a.inv_unit);
+    return (uint32_t)(fmaxf(w, 0.f) * a.inv_unit) + (uint32_t)i;
 }
 
 // A point on the line of work: before tile `tile` of item (n, h, i).
@@ -271,7 +274,9 @@ __device__ __noinline__ bool split_point(const Args &a, int c, Point &p0, Seq &s
     if (total == 0) return false;
     // (single precision: a cut may lie anywhere, but for all CTAs at the same place)
     const float units = (float)total;
-    const int ctas = max(1, (int)fminf((float)a.ctas, units * a.unit / (float)a.min_part));
+    // at least min_part keys and two units each: the cuts inside an item are at
+    // different tiles, and every CTA from an item's first to its last has a part of it
+    const int ctas = max(1, (int)fminf((float)a.ctas, fminf(units * a.unit / (float)a.min_part, 0.5f * units)));
     if (c > ctas) return false;
     p0.n = a.N;
     p0.h = p0.i = p0.tile = 0;

@@ -99,6 +99,10 @@ long long decode_keys(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t pag
     const long long keys = (long long)page * cols + 512;
     return items > cap ? cap * 1024 : items * (keys < cap ? keys : cap);
 }
+// Items of a call at the most (the fp32 kernel's, which are the smaller ones).
+long long prefill_items(int32_t N, long long Tq, int32_t Hq, int32_t Hkv) {
+    return (Tq / (64 / (Hq / Hkv)) + N) * Hkv;
+}
 bool ld_ok(int64_t ld, int32_t heads, int32_t io) {
     return ld >= (int64_t)heads * kda::kD && ld % (io == KDA_BF16 ? 8 : 4) == 0 && ld < (1LL << 36);
 }
@@ -128,7 +132,8 @@ int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, i
         cu_k = cu_q;
     }
     const long long tq = packed ? Tq : (long long)N * Tq, tk = packed ? Tk : (long long)N * Tk;
-    if (tq > 0x7fffffffLL || tk > 0x7fffffffLL || tq * Hq > (1LL << 40) || tk * Hkv > (1LL << 40))
+    if (tq > 0x7fffffffLL || tk > 0x7fffffffLL || tq * Hq > (1LL << 40) || tk * Hkv > (1LL << 40) ||
+        prefill_items(N, tq, Hq, Hkv) > kda::attn::kMaxItems)
         return KDA_ERR_INVALID_ARG;
     if (N == 0 || tq == 0) return KDA_OK;
     if (q == nullptr || out == nullptr || (tk > 0 && (k == nullptr || v == nullptr)) || workspace == nullptr)
@@ -181,7 +186,8 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
     if ((k_new == nullptr) != (v_new == nullptr) || (tree_mask != nullptr && k_new == nullptr))
         return KDA_ERR_INVALID_ARG;
     if ((long long)num_pages * Hkv * page_size > 0x7fffffffLL || (long long)B * T > 0x7fffffffLL ||
-        (long long)B * T * Hq > (1LL << 40) || (long long)table_cols * page_size > 0x7fffffffLL)
+        (long long)B * T * Hq > (1LL << 40) || (long long)table_cols * page_size > 0x7fffffffLL ||
+        (long long)B * T * Hkv > kda::attn::kMaxItems)
         return KDA_ERR_INVALID_ARG;
     if (B == 0 || T == 0) return KDA_OK;
     if (q == nullptr || out == nullptr || seq_lens == nullptr || workspace == nullptr ||

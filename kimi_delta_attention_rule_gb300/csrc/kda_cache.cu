@@ -36,97 +36,92 @@ struct Table {
 };
 
 // ---- append -----------------------------------------------------------------
-// kRows rows per block: kRows threads find where their row goes, then all copy
-// 16-byte pieces, K and V, four in flight per thread.
-constexpr int kAppendRows = 8;
-constexpr int kAppendThreads = 256;
+// A warp per row: it issues the loads of the row's first 2 KB (which need no look-up,
+// but for accepted drafts), then finds where the row goes, a chain of dependent loads
+// that those of other warps and its own data hide, then stores.
+constexpr int kAppendWarps = 8, kAppendFlight = 4;
 
-__global__ void __launch_bounds__(kAppendThreads)
+// The last sequence that starts at or before row r, by one converged warp.
+__device__ __forceinline__ int find_sequence(const int32_t *__restrict__ cu, int N, int64_t r) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, count = N;  // in [lo, lo + count)
+    while (count > 1) {
+        const int step = (count + 31) >> 5, at = lo + lane * step;
+        const bool before = lane == 0 || (lane * step < count && cu[at] <= r);
+        const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));
+        count = min(step, count - k * step);
+        lo += k * step;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(32 * kAppendWarps)
     append_kernel(const uint4 *__restrict__ k, const uint4 *__restrict__ v, int64_t ldk, int64_t ldv,
                   const int32_t *__restrict__ cu, int N, int T, int64_t rows, const int32_t *__restrict__ index,
                   const int32_t *__restrict__ count, const int32_t *__restrict__ start, Table table, int pages,
                   int page, int Hkv, int piece_bits, uint4 *__restrict__ kp, uint4 *__restrict__ vp,
                   uint32_t *status) {
-    __shared__ int64_t src[kAppendRows], dst[kAppendRows];  // source row; first piece of (page, head 0, offset)
-    const int64_t r0 = (int64_t)blockIdx.x * kAppendRows;
-    if (threadIdx.x < kAppendRows) {
-        const int64_t r = r0 + threadIdx.x;
-        int64_t from = -1, to = -1;
-        if (r < rows) {
-            int n, i;
-            bool ok = true;
-            if (cu != nullptr) {
-                int lo = 0, hi = N - 1;  // the last sequence that starts at or before r
-                while (lo < hi) {
-                    const int mid = (lo + hi + 1) >> 1;
-                    if (cu[mid] <= r) lo = mid;
-                    else hi = mid - 1;
-                }
-                n = lo;
-                i = (int)(r - cu[n]);
-                if (cu[0] != 0 || cu[n + 1] <= r) {  // offsets that do not cover this row
-                    ok = false;
-                    if (status) atomicOr(status, kStatusBadSeqlens);
-                }
-                from = r;
-            } else {
-                n = (int)(r / T);
-                i = (int)(r - (int64_t)n * T);
-                from = r;
-                if (count != nullptr) {
-                    const int have = count[n];
-                    if (have < 0 || have > T) {
-                        ok = false;
-                        if (status && i == 0) atomicOr(status, kStatusBadSeqlens);
-                    } else {
-                        ok = i < have;
-                    }
-                }
-                if (ok && index != nullptr) {
-                    const int x = index[r];
-                    if (x < 0 || x >= T) {
-                        ok = false;
-                        if (status) atomicOr(status, kStatusBadSeqlens);
-                    }
-                    from = (int64_t)n * T + x;
-                }
-            }
-            if (ok) {
-                const int64_t pos = (int64_t)start[n] + i, slot = pos / page;
-                const int pg = pos >= 0 && slot < table.cols ? table.row(n)[slot] : -1;
-                if (pg >= 0 && pg < pages) to = ((int64_t)pg * Hkv * page + pos % page) << piece_bits;
-                else if (status) atomicOr(status, kStatusBadSeqlens);
+    const int lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    // the sequence, the row's number in it, and the row to read
+    int n = 0, i = 0;
+    bool ok = true;
+    int64_t from = r;
+    if (cu == nullptr) {
+        n = (int)(r / T);
+        i = (int)(r - (int64_t)n * T);
+        int have = T;
+        if (count != nullptr) {
+            have = count[n];
+            if (have < 0 || have > T) {
+                if (status && i == 0 && lane == 0) atomicOr(status, kStatusBadSeqlens);
+                return;
             }
         }
-        src[threadIdx.x] = from;
-        dst[threadIdx.x] = to;
+        if (i >= have) return;
+        if (index != nullptr) {
+            const int x = index[r];
+            ok = x >= 0 && x < T;
+            if (ok) from = (int64_t)n * T + x;
+        }
     }
-    __syncthreads();
-    const int per_row = Hkv << piece_bits;  // 16-byte pieces of a row
-    const int total = kAppendRows * per_row;
+    const int per_row = Hkv << piece_bits, work = 2 * per_row;  // 16-byte pieces of a row, of K and V
+    auto piece = [&](int x) { return x < per_row ? k[from * ldk + x] : v[from * ldv + (x - per_row)]; };
+    uint4 y[kAppendFlight];
+#pragma unroll
+    for (int f = 0; f < kAppendFlight; ++f)
+        if (lane + 32 * f < work) y[f] = piece(lane + 32 * f);
+    if (cu != nullptr) {
+        n = find_sequence(cu, N, r);
+        i = (int)(r - cu[n]);
+        ok = cu[0] == 0 && cu[n + 1] > r;  // else the offsets do not cover this row
+    }
+    int64_t dst = -1;  // first piece of (page, head 0, offset)
+    if (ok) {
+        const int64_t pos = (int64_t)start[n] + i, slot = pos / page;
+        const int pg = pos >= 0 && slot < table.cols ? table.row(n)[slot] : -1;
+        if (pg >= 0 && pg < pages) dst = ((int64_t)pg * Hkv * page + pos % page) << piece_bits;
+    }
+    if (dst < 0) {
+        if (status && lane == 0) atomicOr(status, kStatusBadSeqlens);
+        return;
+    }
     const int64_t head_step = (int64_t)page << piece_bits;
-    constexpr int kFlight = 4;
-    for (int x0 = threadIdx.x; x0 < 2 * total; x0 += kFlight * kAppendThreads) {
-        uint4 y[kFlight];
+    auto store = [&](int x, uint4 z) {
+        const bool is_v = x >= per_row;
+        const int w = is_v ? x - per_row : x;
+        (is_v ? vp : kp)[dst + (w >> piece_bits) * head_step + (w & ((1 << piece_bits) - 1))] = z;
+    };
+    for (int x0 = lane; x0 < work; x0 += 32 * kAppendFlight) {
+        if (x0 != lane) {
 #pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-            int x = x0 + f * kAppendThreads;
-            const bool is_v = x >= total;
-            x -= is_v ? total : 0;
-            if (x >= total) continue;
-            const int r = x / per_row, w = x - r * per_row;
-            if (dst[r] >= 0) y[f] = (is_v ? v : k)[src[r] * (is_v ? ldv : ldk) + w];
+            for (int f = 0; f < kAppendFlight; ++f)
+                if (x0 + 32 * f < work) y[f] = piece(x0 + 32 * f);
         }
 #pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-            int x = x0 + f * kAppendThreads;
-            const bool is_v = x >= total;
-            x -= is_v ? total : 0;
-            if (x >= total) continue;
-            const int r = x / per_row, w = x - r * per_row, h = w >> piece_bits;
-            if (dst[r] >= 0)
-                (is_v ? vp : kp)[dst[r] + h * head_step + (w & ((1 << piece_bits) - 1))] = y[f];
-        }
+        for (int f = 0; f < kAppendFlight; ++f)
+            if (x0 + 32 * f < work) store(x0 + 32 * f, y[f]);
     }
 }
 
@@ -508,7 +503,7 @@ cudaError_t launch_append(const void *k, const void *v, int64_t ldk, int64_t ldv
     const int piece_bits = es == 2 ? 4 : 5;  // 16-byte pieces of a head's row: 16 or 32
     const int64_t per = 16 / es;
     const Table t = {const_cast<int32_t *>(table), table_ld, N, cols};
-    append_kernel<<<(unsigned)((rows + kAppendRows - 1) / kAppendRows), kAppendThreads, 0, stream>>>(
+    append_kernel<<<(unsigned)((rows + kAppendWarps - 1) / kAppendWarps), 32 * kAppendWarps, 0, stream>>>(
         static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), ldk / per, ldv / per, cu, N, T, rows, index,
         count, start, t, pages, page, Hkv, piece_bits, static_cast<uint4 *>(kp), static_cast<uint4 *>(vp), status);
     return cudaGetLastError();

@@ -89,6 +89,37 @@ def test_many_sequences(dt):
 
 
 @pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("N,hkv", [(3000, 2), (70000, 4)])
+def test_very_many_single_tokens(N, hkv, dt):
+    """A sequence of one token is its own v: lengths that add up to far less than the
+    bound that the work search counts in."""
+    G = 2
+    q, k, v = rows(15, N, G * hkv, dt), rows(16, N, hkv, dt), rows(17, N, hkv, dt)
+    cu = torch.arange(N + 1, dtype=torch.int32, device=DEV)
+    out, lse = kda.kda_attn_prefill(q, k, v, SCALE, cu_seqlens=cu, output_lse=True)
+    assert torch.equal(out, v.repeat_interleave(G, 1))
+    kk = k.repeat_interleave(G, 1).double()
+    x = SCALE * (q.double() * kk).sum(2)
+    tol = 136 * 2.0**-24 * 2 * SCALE * (q.double() * kk).abs().sum(2) + 2.0**-21 + 2.0**-22 * x.abs()
+    assert ((lse.double() - x).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_one_long_among_very_many_short(dt):
+    """40,000 sequences of nothing or one token around one of 5,000."""
+    lens = [i % 2 for i in range(20000)] + [5000] + [(i + 1) % 2 for i in range(20000)]
+    n = sum(lens)
+    q, k, v = rows(18, n, 2, dt), rows(19, n, 1, dt), rows(20, n, 1, dt)
+    cu = offsets(lens)
+    out, lse = kda.kda_attn_prefill(q, k, v, SCALE, cu_seqlens=cu, output_lse=True)
+    a = int(cu[20000])
+    check(q[a:a + 5000], k[a:a + 5000], v[a:a + 5000], [5000], [5000], out[a:a + 5000], lse[a:a + 5000])
+    short = torch.ones(n, dtype=torch.bool, device=DEV)
+    short[a:a + 5000] = False
+    assert torch.equal(out[short], v.repeat_interleave(2, 1)[short])
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
 def test_growing_maxima(dt):
     """Keys that grow along the sequence: the running maximum moves at every tile
     (by far more than 2^8 once), and logits reach several hundred."""
