@@ -47,13 +47,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
-constexpr int kPartRows = 256;  // rows of a part in the workspace
 constexpr int kMaxDrafts = 64;  // a row's draft mask has 64 bits
 // Keys of work (an item's start and end included) below which no further CTA is used.
 constexpr int kTcMinPart = 384, kF32MinPart = 128;
 
 // Workspace: status word and padding, the parts' headers, then per part slot
-// O (fp32, [32 channel quads][256 rows][4]) and m, l ([256] each).
+// O (fp32, [32 channel quads][part_rows][4]) and m, l ([part_rows] each).
 constexpr size_t kWsHeader = 256;
 struct PartHeader {
     int32_t valid;      // this slot holds a part of an item
@@ -63,14 +62,12 @@ struct PartHeader {
     int32_t kvh;        // kv head
     int32_t pad[3];
 };
-__host__ __device__ constexpr size_t part_stride() {
-    return (size_t)kPartRows * kD * 4 + (size_t)kPartRows * 8;
-}
+__host__ __device__ inline size_t part_stride(int part_rows) { return (size_t)part_rows * (kD * 4 + 8); }
 __host__ __device__ inline size_t headers_bytes(int ctas) {
     return ((size_t)2 * ctas * sizeof(PartHeader) + 255) / 256 * 256;
 }
-__host__ __device__ inline size_t workspace_bytes(int ctas) {
-    return kWsHeader + headers_bytes(ctas) + (size_t)2 * ctas * part_stride();
+__host__ __device__ inline size_t workspace_bytes(int ctas, int part_rows) {
+    return kWsHeader + headers_bytes(ctas) + (size_t)2 * ctas * part_stride(part_rows);
 }
 
 // Arguments shared by the kernels (prefill: packed rows; decode: pages).
@@ -99,6 +96,7 @@ struct Args {
     float *lse;
     unsigned char *ws;
     int ctas, sms;           // CTAs that share the work; SMs of the device
+    int part_rows;           // rows of a part in the workspace: those of an item at the most
 };
 
 // The unit of weight: `keys` is an upper bound of a call's work in keys, of at most
@@ -118,10 +116,10 @@ __device__ __forceinline__ PartHeader *part_header(const Args &a, int slot) {
 }
 __device__ __forceinline__ float *part_o(const Args &a, int slot) {
     return reinterpret_cast<float *>(a.ws + kWsHeader + headers_bytes(a.ctas) +
-                                     (size_t)slot * part_stride());
+                                     (size_t)slot * part_stride(a.part_rows));
 }
 __device__ __forceinline__ float2 *part_ml(const Args &a, int slot) {
-    return reinterpret_cast<float2 *>(part_o(a, slot) + (size_t)kPartRows * kD);
+    return reinterpret_cast<float2 *>(part_o(a, slot) + (size_t)a.part_rows * kD);
 }
 
 // One sequence. ok = false: malformed lengths.

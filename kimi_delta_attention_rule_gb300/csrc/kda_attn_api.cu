@@ -79,6 +79,9 @@ int attn_ctas(int32_t io, long long keys) {
     const long long n = keys / part;
     return (int)(n < 1 ? 1 : (n < most ? n : most));
 }
+// Rows of an item at the most: a row tile (fp32), or two of 128 rows, which a decode
+// of at most 128 rows per kv head does not need.
+int part_rows(int32_t io, int rows) { return io == KDA_F32 ? 64 : (rows <= 128 ? 128 : 256); }
 int check_heads(int32_t Hq, int32_t Hkv, int32_t D, int32_t io) {
     if (Hq <= 0 || Hkv <= 0 || D <= 0 || Hq % Hkv != 0) return KDA_ERR_INVALID_ARG;
     if (io != KDA_BF16 && io != KDA_F32) return KDA_ERR_UNSUPPORTED;
@@ -115,7 +118,8 @@ extern "C" {
 size_t kda_attn_prefill_workspace_size(int32_t N, int32_t Tq_total, int32_t Tk_total, int32_t Hq, int32_t Hkv,
                                        int32_t D, int32_t io) {
     if (N < 0 || Tq_total < 0 || Tk_total < 0 || check_heads(Hq, Hkv, D, io) != KDA_OK) return 0;
-    return kda::attn::workspace_bytes(attn_ctas(io, prefill_keys(N, Tq_total, Tk_total, Hq, Hkv, io)));
+    return kda::attn::workspace_bytes(attn_ctas(io, prefill_keys(N, Tq_total, Tk_total, Hq, Hkv, io)),
+                                     part_rows(io, 256));
 }
 
 int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
@@ -144,7 +148,8 @@ int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, i
     if (!ld_ok(ldq, Hq, io) || !ld_ok(ldk, Hkv, io) || !ld_ok(ldv, Hkv, io)) return KDA_ERR_INVALID_ARG;
     Args a = {};
     a.ctas = attn_ctas(io, prefill_keys(N, tq, tk, Hq, Hkv, io));
-    if (workspace_bytes < kda::attn::workspace_bytes(a.ctas)) return KDA_ERR_INVALID_ARG;
+    a.part_rows = part_rows(io, 256);
+    if (workspace_bytes < kda::attn::workspace_bytes(a.ctas, a.part_rows)) return KDA_ERR_INVALID_ARG;
     a.N = N;
     a.Hq = Hq;
     a.Hkv = Hkv;
@@ -170,7 +175,8 @@ size_t kda_attn_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t 
                                       int32_t table_cols, int32_t io) {
     if (B < 0 || T < 0 || T > kMaxTokens || table_cols < 0 || !page_ok(page_size) || check_heads(Hq, Hkv, D, io) != KDA_OK)
         return 0;
-    return kda::attn::workspace_bytes(attn_ctas(io, decode_keys(B, T, Hq, Hkv, page_size, table_cols, io)));
+    return kda::attn::workspace_bytes(attn_ctas(io, decode_keys(B, T, Hq, Hkv, page_size, table_cols, io)),
+                                     part_rows(io, T * (Hq / Hkv)));
 }
 
 int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk, int64_t ldv,
@@ -201,7 +207,8 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
         return KDA_ERR_INVALID_ARG;
     Args a = {};
     a.ctas = attn_ctas(io, decode_keys(B, T, Hq, Hkv, page_size, table_cols, io));
-    if (workspace_bytes < kda::attn::workspace_bytes(a.ctas)) return KDA_ERR_INVALID_ARG;
+    a.part_rows = part_rows(io, T * (Hq / Hkv));
+    if (workspace_bytes < kda::attn::workspace_bytes(a.ctas, a.part_rows)) return KDA_ERR_INVALID_ARG;
     a.N = B;
     a.Hq = Hq;
     a.Hkv = Hkv;

@@ -65,7 +65,7 @@ __device__ __forceinline__ void join_rows(const Args &a, const PartHeader &h, in
                     const float2 ml = part_ml(a, slot)[at];
                     y[f].m = ml.x;
                     y[f].l = ml.y;
-                    y[f].o = reinterpret_cast<const float4 *>(part_o(a, slot))[(size_t)q * kPartRows + at];
+                    y[f].o = reinterpret_cast<const float4 *>(part_o(a, slot))[(size_t)q * a.part_rows + at];
                 }
             }
 #pragma unroll

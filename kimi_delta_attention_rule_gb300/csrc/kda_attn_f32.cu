@@ -235,8 +235,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             if (!p.whole()) {
                 const int slot = part_slot(cta, p);
                 float4 *o4 = reinterpret_cast<float4 *>(part_o(a, slot)) + r;
-                o4[(size_t)tx * kPartRows] = o[i][0];
-                o4[(size_t)(16 + tx) * kPartRows] = o[i][1];
+                o4[(size_t)tx * a.part_rows] = o[i][0];
+                o4[(size_t)(16 + tx) * a.part_rows] = o[i][1];
                 if (tx == 0) part_ml(a, slot)[r] = make_float2(m[i], l[i]);
                 continue;
             }

@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float4 *o4 = reinterpret_cast<float4 *>(part_o(a, d->slot)) + (DUAL ? r : 128 * s + r);
 #pragma unroll
                             for (int q = 0; q < 16; ++q)
-                                o4[(size_t)(16 * p + q) * kPartRows] = make_float4(
+                                o4[(size_t)(16 * p + q) * a.part_rows] = make_float4(
                                     __uint_as_float(o[q / 4][4 * (q % 4)]), __uint_as_float(o[q / 4][4 * (q % 4) + 1]),
                                     __uint_as_float(o[q / 4][4 * (q % 4) + 2]), __uint_as_float(o[q / 4][4 * (q % 4) + 3]));
                         }
