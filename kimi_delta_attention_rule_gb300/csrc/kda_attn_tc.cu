@@ -186,12 +186,6 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity));
 }
-// the same, each lane with its own answer
-__device__ __forceinline__ bool warp_wait_here(uint32_t bar, uint32_t parity) {
-    const bool ok = wait(bar, parity);
-    __syncwarp();
-    return ok;
-}
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("barrier.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
@@ -809,60 +803,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t q_desc = tc::smem_desc_sw128(base + L::kQ, 16, 1024);
             const uint64_t k_desc = tc::smem_desc_sw128(base + L::kKv, 16, 1024);
             const uint64_t v_desc = tc::smem_desc_sw128(base + L::kKv, kHalf, 1024);
-            uint32_t kv = 0, np = 0;  // ring position; parity of each stream's P
-            auto wait_kv = [&](uint32_t at) { return warp_wait_here(bars.kvfull(at % L::kRing), (at / L::kRing) & 1); };
-            auto free_kv = [&](uint32_t at) { tc::mma_commit_lead(lead, bars.kvempty(at % L::kRing)); };
-            // One step of stream s: O_s (+)= P V, keys 0 .. 95 and 96 .. 127 once their P is
-            // there, then S_s = Q K^T with Q tile i, after which its softmax may read S.
-            // What the second product waits for, and its descriptors, come before the wait
-            // for the last of P: from there on, the softmax of this stream stands still.
-            struct Step {
-                bool pv, pv_first, pv_last, qk, qk_first, qk_last;
-                uint32_t v, k;  // ring positions of the V and K tiles
-                int q;          // number of the Q tile
+            uint32_t kv = 0, np0 = 0, np1 = 0;
+            auto wait_kv = [&](uint32_t at) {
+                if (alive) alive = warp_wait(bars.kvfull(at % L::kRing), (at / L::kRing) & 1);
             };
-            auto step = [&](int s, const Step &x) {
-                const uint32_t slot = (uint32_t)x.q % L::kQs, qfull = bars.qfull(slot), qparity = ((uint32_t)x.q / L::kQs) & 1;
-                const uint64_t vd = v_desc + (x.v % L::kRing) * (kTileBytes >> 4);
-                const uint64_t kd = k_desc + (x.k % L::kRing) * (kTileBytes >> 4);
+            auto free_kv = [&](uint32_t at) { tc::mma_commit_lead(lead, bars.kvempty(at % L::kRing)); };
+            // S_s = Q K^T with Q tile i; then the row tile's softmax may read it
+            auto qk = [&](int s, int i, bool first, bool last, uint32_t at) {
+                const uint32_t slot = (uint32_t)i % L::kQs;
+                if (first && alive) alive = warp_wait(bars.qfull(slot), ((uint32_t)i / L::kQs) & 1);
+                if (!alive) return;
                 const uint64_t qd = q_desc + slot * (L::kQTile >> 4);
-                const uint32_t so = tm + kColS + 128 * s, oo = tm + kColO + 128 * s;
-                const uint32_t parity = np >> s & 1;
-                bool ok = true;  // (one vote per step; products after a wait that ran out do no harm)
-                if (x.pv) {
-                    np ^= 1u << s;
-                    ok = wait_kv(x.v) && ok;
-                    ok = warp_wait_here(bars.pready(s, 0), parity) && ok;
+                const uint64_t kd = k_desc + (at % L::kRing) * (kTileBytes >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk) {
+                    const uint32_t k16 = (kk & 3) * 32, half = kk >> 2;
+                    tc::mma_f16_lead(lead, tm + kColS + 128 * s, qd + ((half * L::kQHalf + k16) >> 4),
+                                     kd + ((half * kHalf + k16) >> 4), kIdQK, kk > 0);
+                }
+                tc::mma_commit_lead(lead, bars.sfull(s));
+                if (!DUAL && last) tc::mma_commit_lead(lead, bars.qempty(slot));
+            };
+            // O_s (+)= P V, keys 0 .. 95 and 96 .. 127 once their P is there
+            auto pv = [&](int s, uint32_t at, bool first, bool last) {
+                const uint64_t vd = v_desc + (at % L::kRing) * (kTileBytes >> 4);
+                const uint32_t parity = (s ? np1++ : np0++) & 1;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (alive) alive = warp_wait(bars.pready(s, half), parity);
+                    if (!alive) return;
                     tc::fence_after_sync();
 #pragma unroll
-                    for (int kk = 0; kk < 6; ++kk)
-                        tc::mma_f16_ta_lead(lead, oo, so + 8 * kk, vd + ((kk * 2048) >> 4), kIdPV, !x.pv_first || kk > 0);
+                    for (int kk = half ? 6 : 0; kk < (half ? 8 : 6); ++kk)
+                        tc::mma_f16_ta_lead(lead, tm + kColO + 128 * s, tm + kColS + 128 * s + 8 * kk,
+                                            vd + ((kk * 2048) >> 4), kIdPV, !first || kk > 0);
                 }
-                if (x.qk) {
-                    ok = wait_kv(x.k) && ok;
-                    // (DUAL: the Q tile may wait for the end of the part whose P V this is)
-                    if (!DUAL && x.qk_first) ok = warp_wait_here(qfull, qparity) && ok;
-                }
-                if (x.pv) {
-                    ok = warp_wait_here(bars.pready(s, 1), parity) && ok;
-                    tc::fence_after_sync();
-#pragma unroll
-                    for (int kk = 6; kk < 8; ++kk)
-                        tc::mma_f16_ta_lead(lead, oo, so + 8 * kk, vd + ((kk * 2048) >> 4), kIdPV, 1);
-                    if (x.pv_last) tc::mma_commit_lead(lead, bars.ofull(s));
-                }
-                if (x.qk) {
-                    if (DUAL && x.qk_first) ok = warp_wait_here(qfull, qparity) && ok;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk) {
-                        const uint32_t k16 = (kk & 3) * 32, half = kk >> 2;
-                        tc::mma_f16_lead(lead, so, qd + ((half * L::kQHalf + k16) >> 4), kd + ((half * kHalf + k16) >> 4),
-                                         kIdQK, kk > 0);
-                    }
-                    tc::mma_commit_lead(lead, bars.sfull(s));
-                    if (!DUAL && x.qk_last) tc::mma_commit_lead(lead, bars.qempty(slot));
-                }
-                alive = __all_sync(0xffffffffu, ok);
+                if (last) tc::mma_commit_lead(lead, bars.ofull(s));
             };
             if (!DUAL) {
                 // step g: per stream, P V of step g - 1, then Q K^T of step g (of the next
@@ -886,20 +862,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < n && alive; ++j) {
                         const uint32_t v = kv, k = kv + (at_j >= 0);
                         kv = k + (d != nullptr);
+                        if (at_j >= 0) wait_kv(v);
+                        bool waited = false;
 #pragma unroll 1
                         for (int s = 0; s < 2; ++s) {
                             const int before = s ? n1 : n0, now = s ? c1 : c0;
-                            Step x;
-                            x.pv = at_j >= 0 && at_j < before;
-                            x.pv_first = at_j == 0;
-                            x.pv_last = at_j + 1 == before;
-                            x.qk = j < now;
-                            x.qk_first = j == 0;
-                            x.qk_last = j + 1 == now;
-                            x.v = v;
-                            x.k = k;
-                            x.q = s ? q1 : q0;
-                            if (alive) step(s, x);
+                            if (at_j >= 0 && at_j < before) pv(s, v, at_j == 0, at_j + 1 == before);
+                            if (j < now) {
+                                if (!waited) wait_kv(k);
+                                waited = true;
+                                qk(s, s ? q1 : q0, j == 0, j + 1 == now, k);
+                            }
                         }
                         if (!alive) break;
                         if (at_j >= 0) free_kv(v);
@@ -929,23 +902,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (!alive || (left == 0 && flush-- == 0)) break;
                     const int s = g & 1;
-                    Step x;
-                    x.pv = g >= 2;
-                    x.pv_first = flags >> (2 * s) & 1;
-                    x.pv_last = flags >> (2 * s + 1) & 1;
-                    x.qk = left > 0;
-                    x.qk_first = j < 2;
-                    x.qk_last = false;
-                    x.v = kv;
-                    kv += x.pv;
-                    x.k = kv;
-                    kv += x.qk;
-                    x.q = q;
-                    step(s, x);
-                    if (!alive) break;
-                    if (x.pv) free_kv(x.v);
-                    if (x.qk) {
-                        free_kv(x.k);
+                    if (g >= 2) {
+                        const uint32_t v = kv++;
+                        wait_kv(v);
+                        pv(s, v, flags >> (2 * s) & 1, flags >> (2 * s + 1) & 1);
+                        if (!alive) break;
+                        free_kv(v);
+                    }
+                    if (left > 0) {
+                        const uint32_t k = kv++;
+                        wait_kv(k);
+                        qk(s, q, j < 2, false, k);
+                        if (!alive) break;
+                        free_kv(k);
                         flags = (flags & ~(3u << (2 * s))) | ((uint32_t)(j < 2) | (uint32_t)(j + 2 >= tiles) << 1) << (2 * s);
                         --left;
                         ++j;
