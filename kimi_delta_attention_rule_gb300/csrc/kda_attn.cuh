@@ -19,6 +19,12 @@
 // the CTA that finishes an item last saves a launch, 4 us of host time, but one SM
 // waits for all the parts' loads: 5 to 20 us more on calls with many parts.) Few and
 // short items go to a CTA each (`direct`), without the search and without a join.
+//
+// Early parts. A CTA's first part is done long before its neighbour's last one, so
+// where it ends the item, the neighbour adds it to its own rows as it writes them
+// (`joins_early`, row tiles of 128): items of two parts, nearly all of them with long
+// prompts, then need no second pass. Nobody waits: a part that is not there yet is left to
+// the join kernel, which adds the last two parts first, so that the bits are the same.
 #pragma once
 
 #include <stdint.h>
@@ -47,16 +53,39 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return d;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+// The factors that bring two partial sums (of maxima m0 and m1) to their common maximum.
+// (-inf: no key seen; l and O are 0, or NaN)
+__device__ __forceinline__ float2 join_factors(float m0, float m1, float c) {
+    const float up = fmaxf(m0, m1);
+    return make_float2(m0 == -INFINITY ? 1.f : ex2((m0 - up) * c), m1 == -INFINITY ? 1.f : ex2((m1 - up) * c));
+}
+// x f + y g, rounded alike wherever two parts are joined
+__device__ __forceinline__ float join_sum(float x, float f, float y, float g) {
+    return __fmaf_rn(x, f, __fmul_rn(y, g));
+}
+
 constexpr int kMaxDrafts = 64;  // a row's draft mask has 64 bits
 // Keys of work (an item's start and end included) below which no further CTA is used.
 constexpr int kTcMinPart = 384, kF32MinPart = 128;
+constexpr int kMaxCtas = 512;  // CTAs of a call
 
-// Workspace: status word and padding, the parts' headers, then per part slot
-// O (fp32, [32 channel quads][part_rows][4]) and m, l ([part_rows] each).
+// Workspace: status word, the early parts' flags and padding (256 bytes), the parts'
+// headers, then per part slot O (fp32, [32 channel quads][part_rows][4]) and m, l
+// ([part_rows] each).
 constexpr size_t kWsHeader = 256;
+// Bit c: CTA c's first part ends its item and is written. All zero between calls: the
+// join kernel clears them.
+constexpr int kFlagsAt = 64, kFlagWords = kMaxCtas / 32;
+static_assert(kFlagsAt + 4 * kFlagWords <= (int)kWsHeader, "the flags");
+constexpr int kEnds = 1, kEndsJoined = 2;
 struct PartHeader {
     int32_t valid;      // this slot holds a part of an item
-    int32_t ends;       // the item's last part
+    int32_t ends;       // kEnds: the item's last part; kEndsJoined: with the last part added
     int32_t token0;     // first token row of the item in q / out
     int32_t tokens;     // valid tokens of the item
     int32_t kvh;        // kv head
@@ -110,6 +139,9 @@ inline void set_unit(Args &a, double keys) {
 
 __device__ __forceinline__ uint32_t *status_word(const Args &a) {
     return reinterpret_cast<uint32_t *>(a.ws);
+}
+__device__ __forceinline__ uint32_t *early_flag(const Args &a, int cta) {  // bit cta % 32 of it
+    return reinterpret_cast<uint32_t *>(a.ws + kFlagsAt) + (cta >> 5);
 }
 __device__ __forceinline__ PartHeader *part_header(const Args &a, int slot) {
     return reinterpret_cast<PartHeader *>(a.ws + kWsHeader) + slot;

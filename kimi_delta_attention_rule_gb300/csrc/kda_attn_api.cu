@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include <nvtx3/nvToolsExt.h>
@@ -50,6 +51,7 @@ using kda::attn::Args;
 
 constexpr int kMaxGroup = 64;
 constexpr int kMaxTokens = kda::attn::kMaxDrafts;
+constexpr long long kMaxKeys = 0x7fffff00LL - 512;  // (positions two key tiles past a sequence's end are formed)
 constexpr size_t kHeader = 256;  // of a cache workspace: the status word
 
 struct Range {
@@ -75,8 +77,8 @@ int sm_count() {
 // CTAs of one attention call: all that fit on the device at once, fewer when
 // an upper bound of the work (in keys) cannot fill them.
 int attn_ctas(int32_t io, long long keys) {
-    const long long most = (io == KDA_F32 ? 2LL : 1LL) * sm_count(), part = io == KDA_F32 ? kda::attn::kF32MinPart : kda::attn::kTcMinPart;
-    const long long n = keys / part;
+    const int most = std::min((io == KDA_F32 ? 2 : 1) * sm_count(), kda::attn::kMaxCtas);
+    const long long n = keys / (io == KDA_F32 ? kda::attn::kF32MinPart : kda::attn::kTcMinPart);
     return (int)(n < 1 ? 1 : (n < most ? n : most));
 }
 // Rows of an item at the most: a row tile (fp32), or two of 128 rows, which a decode
@@ -192,7 +194,7 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
     if ((k_new == nullptr) != (v_new == nullptr) || (tree_mask != nullptr && k_new == nullptr))
         return KDA_ERR_INVALID_ARG;
     if ((long long)num_pages * Hkv * page_size > 0x7fffffffLL || (long long)B * T > 0x7fffffffLL ||
-        (long long)B * T * Hq > (1LL << 40) || (long long)table_cols * page_size > 0x7fffffffLL ||
+        (long long)B * T * Hq > (1LL << 40) || (long long)table_cols * page_size > kMaxKeys ||
         (long long)B * T * Hkv > kda::attn::kMaxItems)
         return KDA_ERR_INVALID_ARG;
     if (B == 0 || T == 0) return KDA_OK;

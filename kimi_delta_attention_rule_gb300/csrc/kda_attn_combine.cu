@@ -1,10 +1,14 @@
 // Joins the parts of items that more than one CTA worked on: for each row, over
 // the parts in CTA order,
 //   M = max_p m_p,  L = sum_p l_p e^{c (m_p - M)},  O = sum_p O_p e^{c (m_p - M)} / L.
-// A block takes a share of the item that starts (unfinished) in CTA c = blockIdx.x;
-// thread = (row, four channels), rows fastest, as the parts are laid out; the loads
-// of four parts are in flight at a time. With many parts (few rows over a long
-// cache) eight lanes share a thread's work. The
+//
+// Every block looks through the parts' headers (one load per thread), which gives it
+// all split items and how many threads' worth of rows they have, and takes every
+// gridDim-th chunk of that: a call may have one split item of a hundred parts or a
+// hundred of two, and all SMs share either evenly. Thread = (row, four channels), eight rows
+// and four quads to a warp, so that reads are 128 bytes (the parts are laid out rows
+// fastest) and writes whole sectors; the loads of four parts are in flight at a time.
+// With many parts (few rows over a long cache) eight lanes share a thread's work. The
 // order of the sum is fixed, so a call gives the same bits every time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -16,7 +20,8 @@
 namespace kda {
 namespace attn {
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinBlocks = 3;  // per SM (2, 3, 4: 37.7, 37.2, 38.4 us for an fp32 tree of 11 drafts on 6 short caches)
 
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 y) {
     *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
@@ -29,115 +34,182 @@ struct Acc {
 };
 // x = x + y, both relative to their own maxima
 __device__ __forceinline__ void join(Acc &x, const Acc &y, float c) {
-    const float up = fmaxf(x.m, y.m);
-    // (-inf: no key seen; l and O are 0, or NaN)
-    const float f = x.m == -INFINITY ? 1.f : exp2f((x.m - up) * c), g = y.m == -INFINITY ? 1.f : exp2f((y.m - up) * c);
-    x.m = up;
-    x.l = x.l * f + y.l * g;
-    x.o.x = x.o.x * f + y.o.x * g;
-    x.o.y = x.o.y * f + y.o.y * g;
-    x.o.z = x.o.z * f + y.o.z * g;
-    x.o.w = x.o.w * f + y.o.w * g;
+    const float2 f = join_factors(x.m, y.m, c);
+    x.m = fmaxf(x.m, y.m);
+    x.l = join_sum(x.l, f.x, y.l, f.y);
+    x.o.x = join_sum(x.o.x, f.x, y.o.x, f.y);
+    x.o.y = join_sum(x.o.y, f.x, y.o.y, f.y);
+    x.o.z = join_sum(x.o.z, f.x, y.o.z, f.y);
+    x.o.w = join_sum(x.o.w, f.x, y.o.w, f.y);
 }
 
-// SUB neighbouring lanes share a (row, quad), each with every SUB-th part.
+// Eight lanes per (row, quad), each with every eighth part?
+__device__ __forceinline__ bool shared_work(int n, int rows) { return n > 8 && rows <= 32; }
+
+// Chunk `chunk` of an item of n terms, the last of which is two parts with `pair`:
+// kJoinThreads / SUB (row, quad) pairs. SUB neighbouring lanes share one, each with
+// every SUB-th term.
 template <typename IO, int SUB>
-__device__ __forceinline__ void join_rows(const Args &a, const PartHeader &h, int c0, int n, int tile_rows) {
+__device__ __forceinline__ void join_rows(const Args &a, const PartHeader &h, int c0, int n, bool pair, int tile_rows,
+                                          int chunk) {
     const float c = a.scale * kLog2e;
     const int first = h.tokens < a.tile_tokens ? h.tokens : a.tile_tokens;
     const int rows0 = first * a.G, rows = h.tokens * a.G;  // rows in the parts: stream s at tile_rows s
     const int sub = threadIdx.x % SUB;
-    const int groups = kJoinThreads / SUB * (int)gridDim.y;
-    for (int i0 = blockIdx.y * (kJoinThreads / SUB); i0 < rows * 32; i0 += groups) {
-        const int i = i0 + (int)threadIdx.x / SUB;
-        const bool in = i < rows * 32;
-        const int q = in ? i / rows : 0, row = in ? i - q * rows : 0;
-        const int at = row < rows0 ? row : tile_rows + row - rows0;
-        Acc x = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-        constexpr int kFlight = 4;  // parts whose loads are issued together
-        for (int k0 = sub; k0 < n; k0 += kFlight * SUB) {
-            Acc y[kFlight];
+    const int i = chunk * (kJoinThreads / SUB) + (int)threadIdx.x / SUB;
+    const int eights = (rows + 7) >> 3, block = i >> 5;
+    const int q = block / eights * 4 + (i >> 3 & 3), row = block % eights * 8 + (i & 7);
+    const bool in = q < 32 && row < rows;
+    const int at = row < rows0 ? row : tile_rows + row - rows0;
+    auto load = [&](int k) {
+        const int slot = k == 0 ? 2 * c0 + 1 : 2 * (c0 + k);
+        const float2 ml = part_ml(a, slot)[at];
+        return Acc{ml.x, ml.y, reinterpret_cast<const float4 *>(part_o(a, slot))[(size_t)q * a.part_rows + at]};
+    };
+    Acc x = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    constexpr int kFlight = 4;  // parts whose loads are issued together
+    for (int k0 = sub; k0 < n; k0 += kFlight * SUB) {
+        Acc y[kFlight];
 #pragma unroll
-            for (int f = 0; f < kFlight; ++f) {
-                const int k = k0 + f * SUB, slot = k == 0 ? 2 * c0 + 1 : 2 * (c0 + k);
-                y[f] = Acc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-                if (k < n) {
-                    const float2 ml = part_ml(a, slot)[at];
-                    y[f].m = ml.x;
-                    y[f].l = ml.y;
-                    y[f].o = reinterpret_cast<const float4 *>(part_o(a, slot))[(size_t)q * a.part_rows + at];
-                }
-            }
-#pragma unroll
-            for (int f = 0; f < kFlight; ++f) join(x, y[f], c);
+        for (int f = 0; f < kFlight; ++f) {
+            const int k = k0 + f * SUB;
+            y[f] = Acc{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+            if (in && k < n) y[f] = load(k);
         }
+        Acc z = {-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        const int f_last = pair && in && (n - 1 - k0) % SUB == 0 ? (n - 1 - k0) / SUB : -1;
+        if (f_last >= 0 && f_last < kFlight) z = load(n);
 #pragma unroll
-        for (int w = 1; w < SUB; w <<= 1) {
-            Acc y;
-            y.m = __shfl_xor_sync(0xffffffffu, x.m, w);
-            y.l = __shfl_xor_sync(0xffffffffu, x.l, w);
-            y.o.x = __shfl_xor_sync(0xffffffffu, x.o.x, w);
-            y.o.y = __shfl_xor_sync(0xffffffffu, x.o.y, w);
-            y.o.z = __shfl_xor_sync(0xffffffffu, x.o.z, w);
-            y.o.w = __shfl_xor_sync(0xffffffffu, x.o.w, w);
-            join(x, y, c);
+        for (int f = 0; f < kFlight; ++f) {
+            if (f == f_last) join(y[f], z, c);
+            join(x, y[f], c);
         }
-        if (!in || sub != 0) continue;
-        const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
-        const int tok = row / a.G, head = h.kvh * a.G + row - tok * a.G;
-        const size_t dst = (size_t)(h.token0 + tok) * a.Hq + head;
-        store4(static_cast<IO *>(a.out) + dst * kD + 4 * q,
-               make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
-        if (q == 0 && a.lse != nullptr) a.lse[dst] = x.l == 0.f ? -INFINITY : x.m * a.scale + logf(x.l);
     }
+#pragma unroll
+    for (int w = 1; w < SUB; w <<= 1) {
+        Acc y;
+        y.m = __shfl_xor_sync(0xffffffffu, x.m, w);
+        y.l = __shfl_xor_sync(0xffffffffu, x.l, w);
+        y.o.x = __shfl_xor_sync(0xffffffffu, x.o.x, w);
+        y.o.y = __shfl_xor_sync(0xffffffffu, x.o.y, w);
+        y.o.z = __shfl_xor_sync(0xffffffffu, x.o.z, w);
+        y.o.w = __shfl_xor_sync(0xffffffffu, x.o.w, w);
+        join(x, y, c);
+    }
+    if (!in || sub != 0) return;
+    const float inv = x.l == 0.f ? 0.f : 1.f / x.l;
+    const int tok = row / a.G, head = h.kvh * a.G + row - tok * a.G;
+    const size_t dst = (size_t)(h.token0 + tok) * a.Hq + head;
+    store4(static_cast<IO *>(a.out) + dst * kD + 4 * q, make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
+    if (q == 0 && a.lse != nullptr) a.lse[dst] = x.l == 0.f ? -INFINITY : x.m * a.scale + logf(x.l);
 }
 
 template <typename IO>
-__global__ void __launch_bounds__(kJoinThreads) attn_combine_kernel(const Args a, const int tile_rows) {
+__global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_combine_kernel(const Args a, const int tile_rows,
+                                                                     const bool joins_early) {
+    constexpr int kWords = kMaxCtas / 32;
+    __shared__ uint32_t ends[kWords];  // bit c: CTA c's first part is an item's last one, or it has none
+    __shared__ int sums[kJoinThreads / 32];
+    __shared__ int starts[kMaxCtas + 1];  // chunks of the items that start before CTA c
+    __shared__ int terms[kMaxCtas];       // of the item that starts in CTA c; bit 16: the last one is two parts
+    __shared__ uint32_t joined[kWords];   // bit c: CTA c's first part holds the item's last one too
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    const int c0 = blockIdx.x;
-    const PartHeader h = *part_header(a, 2 * c0 + 1);
-    if (!h.valid) return;
-    // the item's other parts are the first ones of the CTAs that follow: every
-    // warp looks at 32 of them at a time
-    const int lane = threadIdx.x & 31;
-    int n = 1;
-    while (true) {
-        const int k = c0 + n + lane;
-        int ends = 1;
-        if (k < a.ctas) {
-            const PartHeader *x = part_header(a, 2 * k);
-            ends = !x->valid || x->ends;
+    if (blockIdx.x == 0 && tid < kFlagWords) *early_flag(a, 32 * tid) = 0;
+    constexpr int kRounds = kMaxCtas / kJoinThreads;
+    int rows[kRounds];  // of the item that starts in CTA tid + kJoinThreads i, 0: none
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int c = tid + kJoinThreads * i;
+        int end = kEnds;
+        rows[i] = 0;
+        if (c < a.ctas) {
+            const PartHeader *x = part_header(a, 2 * c);
+            if (x[0].valid) end = x[0].ends;
+            if (x[1].valid) rows[i] = x[1].tokens * a.G;
         }
-        const unsigned who = __ballot_sync(0xffffffffu, ends);
-        if (who != 0) {
-            n += __ffs(who);
-            break;
+        const unsigned who = __ballot_sync(0xffffffffu, end != 0), both = __ballot_sync(0xffffffffu, end == kEndsJoined);
+        if (lane == 0) {
+            ends[c >> 5] = who;
+            joined[c >> 5] = both;
         }
-        n += 32;
     }
-    if (c0 + n > a.ctas) n = a.ctas - c0;
-    if (n <= 8 || h.tokens * a.G > 32) join_rows<IO, 1>(a, h, c0, n, tile_rows);
-    else join_rows<IO, 8>(a, h, c0, n, tile_rows);
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) any |= rows[i];
+    if (!__syncthreads_or(any)) return;
+    int total = 0;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int c = tid + kJoinThreads * i;
+        if (kJoinThreads * i >= a.ctas) {  // (nor do the rounds after this one have any)
+            starts[c] = total;
+            continue;
+        }
+        int n = 1, chunks = 0;
+        if (rows[i] > 0) {  // its other parts are the first ones of the CTAs that follow
+            int e = c + 1, w = e >> 5;
+            uint32_t bits = w < kWords ? ends[w] & (~0u << (e & 31)) : 0u;
+            while (bits == 0 && ++w < kWords) bits = ends[w];
+            e = bits != 0 ? 32 * w + __ffs(bits) - 1 : a.ctas - 1;
+            e = min(e, a.ctas - 1);
+            n = e - c + 1;
+            if (joins_early && !(joined[e >> 5] >> (e & 31) & 1) && n > 1) n = (n - 1) | 1 << 16;
+            const int pairs = ((rows[i] + 7) & ~7) * 32 * (shared_work(n & 0xffff, rows[i]) ? 8 : 1);
+            chunks = (pairs + kJoinThreads - 1) / kJoinThreads;
+        }
+        int incl = chunks;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) sums[warp] = incl;
+        __syncthreads();
+        int before = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w) {
+            before += w < warp ? sums[w] : 0;
+            all += sums[w];
+        }
+        terms[c] = n;
+        starts[c] = total + before + incl - chunks;
+        total += all;
+        __syncthreads();  // sums is free
+    }
+    if (tid == 0) starts[kMaxCtas] = total;
+    __syncthreads();
+    for (int chunk = blockIdx.x; chunk < total; chunk += gridDim.x) {
+        int lo = 0, hi = kMaxCtas;  // the last CTA whose chunks start at or before this one
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (starts[mid] <= chunk) lo = mid;
+            else hi = mid;
+        }
+        const PartHeader h = *part_header(a, 2 * lo + 1);
+        const int n = terms[lo] & 0xffff;
+        const bool pair = terms[lo] >> 16;
+        if (shared_work(n, h.tokens * a.G)) join_rows<IO, 8>(a, h, lo, n, pair, tile_rows, chunk - starts[lo]);
+        else join_rows<IO, 1>(a, h, lo, n, pair, tile_rows, chunk - starts[lo]);
+    }
 }
 
-cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream) {
+cudaError_t launch_attn_combine(const Args &a, bool bf16, bool joins_early, cudaStream_t stream) {
     if (a.ctas < 2) return cudaSuccess;
     // may start while the attention kernel still runs (it waits for its end)
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    // a thread per (row, quad) of an item where the rows are few, two items of a
-    // row's quads per thread at most where they are many
-    const int rows = a.tile_tokens * a.streams * a.G;
-    cfg.gridDim = dim3((unsigned)a.ctas, (unsigned)(rows <= 32 ? 8 : rows / 8 < 32 ? rows / 8 + 1 : 32));
+    // at most the chunks that a.ctas items of all the rows that a part holds have
+    const long long most = (long long)a.ctas * a.part_rows * 32 / kJoinThreads, blocks = (long long)kJoinBlocks * a.sms;
+    cfg.gridDim = dim3((unsigned)(most < blocks ? most : blocks));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<__nv_bfloat16>, a, 128)
-                : cudaLaunchKernelEx(&cfg, attn_combine_kernel<float>, a, 128);
+    return bf16 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<__nv_bfloat16>, a, 128, joins_early)
+                : cudaLaunchKernelEx(&cfg, attn_combine_kernel<float>, a, 128, joins_early);
 }
 
 }  // namespace attn

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
         }
         if (tid == 0 && !p.whole()) {
             PartHeader *h = part_header(a, part_slot(cta, p));
-            h->ends = p.tb == p.nt;
+            h->ends = p.tb == p.nt ? kEnds : 0;
             h->token0 = p.q0;
             h->tokens = p.tokens;
             h->kvh = p.h;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
     }
 }
 
-cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_attn_combine(const Args &a, bool bf16, bool joins_early, cudaStream_t stream);
 
 template <bool PAGED, int RPT>
 static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
@@ -281,7 +281,7 @@ static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
     attn_f32_kernel<PAGED, RPT>
         <<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kF32Threads, f32_smem(RPT), stream>>>(a, io);
     e = cudaGetLastError();
-    return e == cudaSuccess && !a.direct ? launch_attn_combine(a, false, stream) : e;
+    return e == cudaSuccess && !a.direct ? launch_attn_combine(a, false, false, stream) : e;
 }
 
 cudaError_t launch_attn_prefill_f32(const Args &a, const void *q, const void *k, const void *v, long long ldq,

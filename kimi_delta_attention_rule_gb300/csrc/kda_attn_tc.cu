@@ -62,6 +62,7 @@ struct Desc {
     int first_tok;         // the item's first token within its sequence
     int ta, nt;            // the part's first tile; tiles of the item
     int whole, slot;       // the part is the item; else its workspace slot
+    int open;              // the item goes on in the next CTA
     int writer;            // DUAL: the stream with the first tile, which joins and writes
     int seen;              // prefill: keys that the item's first token sees; decode: cached keys
     int q[2];              // running number of each stream's Q tile
@@ -108,6 +109,7 @@ struct Bars {  // shared-memory addresses
     static constexpr uint32_t kDead = 404;  // a role gave up
     static constexpr uint32_t kJobs = 408;  // kJobRing times (slot, valid rows)
     static constexpr uint32_t kEnd = 472;   // Point: the end of the CTA's work
+    static constexpr uint32_t kEarly = 488;  // the next CTA's early part is there
     static constexpr uint32_t kDesc = 496;  // kDescs descriptors
 };
 static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= 1024, "barrier area");
@@ -139,11 +141,6 @@ __device__ __forceinline__ void expect_tx(uint32_t lead, uint32_t bar, uint32_t 
 }
 __device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
-}
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
 }
 // shared memory (128-byte swizzle) to global; the issuing thread's bulk group
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int c0, int c1, int c2, uint32_t src) {
@@ -186,6 +183,13 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait(bar, parity));
 }
+// z = z f + y g
+__device__ __forceinline__ void join4(uint32_t *z, float f, float4 y, float g) {
+    z[0] = __float_as_uint(join_sum(__uint_as_float(z[0]), f, y.x, g));
+    z[1] = __float_as_uint(join_sum(__uint_as_float(z[1]), f, y.y, g));
+    z[2] = __float_as_uint(join_sum(__uint_as_float(z[2]), f, y.z, g));
+    z[3] = __float_as_uint(join_sum(__uint_as_float(z[3]), f, y.w, g));
+}
 __device__ __forceinline__ void named_bar(int id, int threads) {
     asm volatile("barrier.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
@@ -207,6 +211,7 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
     d.nt = p.nt;
     d.whole = p.whole();
     d.slot = part_slot(cta, p);
+    d.open = p.tb < p.nt;
     d.writer = DUAL ? run.tiles & 1 : 0;
     d.seen = PAGED ? p.Lk : p.Lk - p.Lq + p.first_tok + 1;
     if (DUAL) {  // tiles alternate between the streams, across parts too
@@ -314,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tm = *reinterpret_cast<uint32_t *>(sm + L::kBars + Bars::kTmem);
     const Desc *const descs = reinterpret_cast<const Desc *>(sm + L::kBars + Bars::kDesc);
     volatile int *const dead = reinterpret_cast<volatile int *>(sm + L::kBars + Bars::kDead);
+    volatile int *const early_there = reinterpret_cast<volatile int *>(sm + L::kBars + Bars::kEarly);
     bool alive = true;
     uint32_t nd = 0;  // descriptors taken
     // a wait that may last for a whole part: limited too, and ends when another role gives up
@@ -447,6 +453,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!alive) break;
             // ---- the part's end ----
             const int others = d->count[1 - s];
+            bool early = false;  // the next CTA has the item's last part ready
+            if (!DUAL && d->open) {
+                if (tid == 0) {
+                    uint32_t flags;
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];\n" : "=r"(flags) : "l"(early_flag(a, cta + 1)) : "memory");
+                    *early_there = flags >> ((cta + 1) & 31) & 1;
+                    if (*early_there) {
+                        PartHeader *const h = part_header(a, d->slot);
+                        if (d->ta == 0) h->valid = 0;
+                        else h->ends = kEndsJoined;
+                    }
+                }
+                named_bar(5, 32 * kSoftmaxWarps);
+                early = *early_there != 0;
+            }
+            const bool whole = d->whole || (early && d->ta == 0);
+            const float *const next_o = part_o(a, 2 * (cta + 1));
             if (steps > 0) {
                 if (!warp_wait(bars.ofull(s), no++ & 1)) {
                     alive = false;
@@ -455,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after_sync();
             }
             const bool writer = !DUAL || s == d->writer, joins = DUAL && steps > 0 && others > 0;
-            if ((warp_ok || (!DUAL && d->whole && steps > 0)) && (writer || joins)) {
+            if ((warp_ok || (!DUAL && whole && (steps > 0 || early))) && (writer || joins)) {
                 // In two parts of 64 channels: O from TMEM; the second stream of a join
                 // hands it over in shared memory; the writer stores the sum, or stages it
                 // for whole rows to leave together.
@@ -491,24 +514,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                         named_bar(join_bar, 64);
                         if (p == 0) {
                             const float2 ml = *box_ml;
-                            const float up = fmaxf(m, ml.x);
-                            f = m == -INFINITY ? 1.f : ex2((m - up) * c);  // (then O and l are 0, or NaN)
-                            f1 = ml.x == -INFINITY ? 1.f : ex2((ml.x - up) * c);
-                            m = up;
-                            l = l * f + ml.y * f1;
+                            const float2 fs = join_factors(m, ml.x, c);
+                            f = fs.x;
+                            f1 = fs.y;
+                            m = fmaxf(m, ml.x);
+                            l = join_sum(l, f, ml.y, f1);
                         }
 #pragma unroll
                         for (int q = 0; q < 16; ++q) {
                             const float4 y = box[RT * q];
                             uint32_t *z = &o[q / 4][4 * (q % 4)];
-                            z[0] = __float_as_uint(f * __uint_as_float(z[0]) + f1 * y.x);
-                            z[1] = __float_as_uint(f * __uint_as_float(z[1]) + f1 * y.y);
-                            z[2] = __float_as_uint(f * __uint_as_float(z[2]) + f1 * y.z);
-                            z[3] = __float_as_uint(f * __uint_as_float(z[3]) + f1 * y.w);
+                            join4(z, f, y, f1);
                         }
                         named_bar(join_bar, 64);
                     }
-                    if (!d->whole) {
+                    if (!DUAL && early && row_ok) {
+                        const float4 *const y4 = reinterpret_cast<const float4 *>(next_o) + 128 * s + r;
+                        if (p == 0) {
+                            const float2 ml = __ldcg(part_ml(a, 2 * (cta + 1)) + 128 * s + r);
+                            const float2 fs = join_factors(m, ml.x, c);
+                            f = fs.x;
+                            f1 = fs.y;
+                            m = fmaxf(m, ml.x);
+                            l = join_sum(l, f, ml.y, f1);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 16; ++q)
+                            join4(&o[q / 4][4 * (q % 4)], f, __ldcg(y4 + (size_t)(16 * p + q) * a.part_rows), f1);
+                    }
+                    if (!whole) {
                         if (row_ok) {
                             float4 *o4 = reinterpret_cast<float4 *>(part_o(a, d->slot)) + (DUAL ? r : 128 * s + r);
 #pragma unroll
@@ -520,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         continue;
                     }
                     const float inv = l == 0.f ? 0.f : 1.f / l;
-                    if (steps == 0) {  // rows that see nothing (no Q tile is theirs): zeros
+                    if (steps == 0 && !early) {  // rows that see nothing (no Q tile is theirs): zeros
                         if (row_ok) {
                             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
                                                                    ((size_t)(q0 + tok) * a.Hq + row0 + g) * kD + 64 * p);
@@ -563,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
-                if (writer && !d->whole) {
+                if (writer && !whole) {
                     if (row_ok) part_ml(a, d->slot)[DUAL ? r : 128 * s + r] = make_float2(m, l);
                 } else if (writer) {
                     if (row_ok && a.lse != nullptr)
@@ -606,25 +640,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                 more = walk.next(a, p);
             }
             Run run = {0, 0};
+            const bool tells = !DUAL && more && p.ta > 0 && p.tb == p.nt;  // the CTA before may take the first part
+            auto tell = [&]() {  // (its descriptor is back: all of it is written)
+                if (tells && lane == 0)
+                    asm volatile("red.release.gpu.global.or.b32 [%0], %1;\n" ::"l"(early_flag(a, cta)), "r"(1u << (cta & 31))
+                                 : "memory");
+            };
             while (true) {
                 if (nd >= kDescs && !(alive = long_wait(bars.dempty(nd % kDescs), (nd / kDescs - 1) & 1))) break;
+                if (nd == kDescs) tell();
                 if (lane == 0) {
                     Desc *d = const_cast<Desc *>(descs) + nd % kDescs;
-                    if (more) describe<PAGED, DUAL>(a, p, cta, run, *d);
-                    else d->last = 1;
-                    mbar_arrive(bars.dfull(nd % kDescs));
                     if (more && !p.whole()) {
                         PartHeader *h = part_header(a, part_slot(cta, p));
-                        h->ends = p.tb == p.nt;
+                        h->ends = p.tb == p.nt ? kEnds : 0;
                         h->token0 = p.q0;
                         h->tokens = p.tokens;
                         h->kvh = p.h;
                         h->valid = 1;
                     }
+                    if (more) describe<PAGED, DUAL>(a, p, cta, run, *d);
+                    else d->last = 1;
+                    mbar_arrive(bars.dfull(nd % kDescs));
                 }
                 ++nd;
                 if (!more) break;
                 more = !a.direct && walk.next(a, p);
+            }
+            if (tells && alive && nd <= kDescs) {
+                alive = long_wait(bars.dempty(0), 0);
+                if (alive) tell();
             }
         } else if (warp == kWarpTma) {
             // ---- TMA warp ------------------------------------------------------
@@ -934,7 +979,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kWarpMma) tc::tmem_dealloc(tm, 512);
 }
 
-cudaError_t launch_attn_combine(const Args &a, bool bf16, cudaStream_t stream);
+cudaError_t launch_attn_combine(const Args &a, bool bf16, bool joins_early, cudaStream_t stream);
 
 // ---- host -----------------------------------------------------------------
 namespace {
@@ -986,7 +1031,7 @@ cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, c
     }
     attn_tc_kernel<PAGED, DUAL, RT><<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kThreads, bytes, stream>>>(a, maps);
     e = cudaGetLastError();
-    return e == cudaSuccess && !a.direct ? launch_attn_combine(a, true, stream) : e;
+    return e == cudaSuccess && !a.direct ? launch_attn_combine(a, true, !DUAL, stream) : e;
 }
 }  // namespace
 
