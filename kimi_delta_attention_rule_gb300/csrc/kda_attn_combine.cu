@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_combine_kernel
     __shared__ int terms[kMaxCtas];       // of the item that starts in CTA c; bit 16: the last one is two parts
     __shared__ uint32_t joined[kWords];   // bit c: CTA c's first part holds the item's last one too
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    wait_before();
+    let_next_start();
     if (blockIdx.x == 0 && tid < kFlagWords) *early_flag(a, 32 * tid) = 0;
     constexpr int kRounds = kMaxCtas / kJoinThreads;
     int rows[kRounds];  // of the item that starts in CTA tid + kJoinThreads i, 0: none
@@ -196,20 +197,10 @@ __global__ void __launch_bounds__(kJoinThreads, kJoinBlocks) attn_combine_kernel
 
 cudaError_t launch_attn_combine(const Args &a, bool bf16, bool joins_early, cudaStream_t stream) {
     if (a.ctas < 2) return cudaSuccess;
-    // may start while the attention kernel still runs (it waits for its end)
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
     // at most the chunks that a.ctas items of all the rows that a part holds have
     const long long most = (long long)a.ctas * a.part_rows * 32 / kJoinThreads, blocks = (long long)kJoinBlocks * a.sms;
-    cfg.gridDim = dim3((unsigned)(most < blocks ? most : blocks));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<__nv_bfloat16>, a, 128, joins_early)
-                : cudaLaunchKernelEx(&cfg, attn_combine_kernel<float>, a, 128, joins_early);
+    return launch_early(bf16 ? attn_combine_kernel<__nv_bfloat16> : attn_combine_kernel<float>,
+                        dim3((unsigned)(most < blocks ? most : blocks)), kJoinThreads, 0, stream, a, 128, joins_early);
 }
 
 }  // namespace attn

@@ -43,7 +43,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
     __shared__ Point pts[2];
     __shared__ Seq seq0;
     __shared__ int any;
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    wait_before();
+    let_next_start();
     const int tid = threadIdx.x, cta = blockIdx.x;
     __shared__ Part direct;
     if (tid < 64) {  // one warp finds where this CTA's work starts, one where it ends
@@ -278,9 +279,8 @@ static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
     cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          f32_smem(RPT));
     if (e != cudaSuccess) return e;
-    attn_f32_kernel<PAGED, RPT>
-        <<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kF32Threads, f32_smem(RPT), stream>>>(a, io);
-    e = cudaGetLastError();
+    e = launch_early(attn_f32_kernel<PAGED, RPT>, dim3(a.direct ? (unsigned)slots : (unsigned)a.ctas), kF32Threads,
+                     f32_smem(RPT), stream, a, io);
     return e == cudaSuccess && !a.direct ? launch_attn_combine(a, false, false, stream) : e;
 }
 

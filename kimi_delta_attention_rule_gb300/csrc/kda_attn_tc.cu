@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Point p0;
     Seq s0;
     bool any = false;
+    if (warp == kWarpSched || warp == kWarpFix) wait_before();
     if (warp == kWarpSched) {  // where this CTA's work starts; kWarpFix: where it ends
         if (!a.direct) any = split_point<PAGED, kTile>(a, cta, p0, s0) && p0.n < a.N;
     } else if (warp == kWarpTma) {
@@ -312,7 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    wait_before();
+    let_next_start();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
@@ -1029,8 +1031,8 @@ cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, c
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    attn_tc_kernel<PAGED, DUAL, RT><<<a.direct ? (unsigned)slots : (unsigned)a.ctas, kThreads, bytes, stream>>>(a, maps);
-    e = cudaGetLastError();
+    e = launch_early(attn_tc_kernel<PAGED, DUAL, RT>, dim3(a.direct ? (unsigned)slots : (unsigned)a.ctas), kThreads,
+                     bytes, stream, a, maps);
     return e == cudaSuccess && !a.direct ? launch_attn_combine(a, true, !DUAL, stream) : e;
 }
 }  // namespace

@@ -61,6 +61,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps)
                   const int32_t *__restrict__ count, const int32_t *__restrict__ start, Table table, int pages,
                   int page, int Hkv, int piece_bits, uint4 *__restrict__ kp, uint4 *__restrict__ vp,
                   uint32_t *status) {
+    wait_before();
+    let_next_start();
     const int lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * kAppendWarps + (threadIdx.x >> 5);
     if (r >= rows) return;
@@ -136,6 +138,8 @@ constexpr int kCopyThreads = 256, kCopyFlight = 8, kCopyChunk = kCopyThreads * k
 __global__ void __launch_bounds__(kCopyThreads)
     copy_kernel(const Pools pools, int n_pools, int64_t entry, int entries, const int2 *__restrict__ pairs, int n,
                 const int32_t *__restrict__ count) {
+    wait_before();
+    let_next_start();
     if (count != nullptr) {
         const int have = *count;
         n = have < 0 ? 0 : (have < n ? have : n);
@@ -163,6 +167,8 @@ __global__ void __launch_bounds__(kCopyThreads)
 __global__ void __launch_bounds__(256)
     free_kernel(Table table, int32_t *lens, int32_t *refs, int pages, const int32_t *__restrict__ rows,
                 uint32_t *status) {
+    wait_before();
+    let_next_start();
     const int r = rows[blockIdx.x];
     if (r < 0 || r >= table.rows) {
         if (r >= 0 && status && threadIdx.x == 0) atomicOr(status, kStatusBadSeqlens);
@@ -294,6 +300,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
                 uint32_t *status) {
     __shared__ Shared sh;
     cg::cluster_group cl = cg::this_cluster();
+    wait_before();
+    let_next_start();
     const int rank = (int)cl.block_rank();
     // ranks[i]: -2 = not a fork, -1 = no partial page, else its rank among the fresh pages
     int need = 0;
@@ -373,6 +381,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
                  int2 *rows_state, uint32_t *status) {
     __shared__ Shared sh;
     cg::cluster_group cl = cg::this_cluster();
+    wait_before();
+    let_next_start();
     const int rank = (int)cl.block_rank(), lane = threadIdx.x & 31;
     const int warp = rank * (kThreads / 32) + (int)(threadIdx.x >> 5), warps = kCtas * kThreads / 32;
     for (int r = warp; r < table.rows; r += warps) {  // (pages in use, pages to add)
@@ -420,6 +430,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     compact_kernel(int32_t *refs, int pages, int2 *copies, int32_t *count, int32_t *name, int32_t *n_live) {
     __shared__ Shared sh;
     cg::cluster_group cl = cg::this_cluster();
+    wait_before();
+    let_next_start();
     const int rank = (int)cl.block_rank();
     const Slice s = slice_of(pages, rank);
     int mine = 0, total, before, n;
@@ -482,7 +494,8 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 __global__ void __launch_bounds__(256)
     rename_kernel(Table table, int pages, const int32_t *__restrict__ name, const int32_t *__restrict__ n_live,
                   uint32_t *status) {
-    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    wait_before();
+    let_next_start();
     const int n = *n_live;
     for (int r = blockIdx.x; r < table.rows; r += gridDim.x) {
         int32_t *row = table.row(r);
@@ -503,10 +516,10 @@ cudaError_t launch_append(const void *k, const void *v, int64_t ldk, int64_t ldv
     const int piece_bits = es == 2 ? 4 : 5;  // 16-byte pieces of a head's row: 16 or 32
     const int64_t per = 16 / es;
     const Table t = {const_cast<int32_t *>(table), table_ld, N, cols};
-    append_kernel<<<(unsigned)((rows + kAppendWarps - 1) / kAppendWarps), 32 * kAppendWarps, 0, stream>>>(
-        static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), ldk / per, ldv / per, cu, N, T, rows, index,
-        count, start, t, pages, page, Hkv, piece_bits, static_cast<uint4 *>(kp), static_cast<uint4 *>(vp), status);
-    return cudaGetLastError();
+    return launch_early(append_kernel, dim3((unsigned)((rows + kAppendWarps - 1) / kAppendWarps)), 32 * kAppendWarps, 0,
+                        stream, static_cast<const uint4 *>(k), static_cast<const uint4 *>(v), ldk / per, ldv / per, cu, N,
+                        T, rows, index, count, start, t, pages, page, Hkv, piece_bits, static_cast<uint4 *>(kp),
+                        static_cast<uint4 *>(vp), status);
 }
 
 cudaError_t launch_copy(void *const *pools, int n_pools, int64_t entry_bytes, int entries, const int32_t *pairs, int n,
@@ -517,9 +530,8 @@ cudaError_t launch_copy(void *const *pools, int n_pools, int64_t entry_bytes, in
         for (int i = 0; i < here; ++i) p.base[i] = static_cast<uint4 *>(pools[at + i]);
         const int64_t entry = entry_bytes / 16, work = (entry + kCopyChunk - 1) / kCopyChunk * here * n;
         const int64_t most = (int64_t)sms * 8;
-        copy_kernel<<<(unsigned)(work < most ? work : most), kCopyThreads, 0, stream>>>(
-            p, here, entry, entries, reinterpret_cast<const int2 *>(pairs), n, count);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_early(copy_kernel, dim3((unsigned)(work < most ? work : most)), kCopyThreads, 0, stream,
+                                           p, here, entry, entries, reinterpret_cast<const int2 *>(pairs), n, count);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -532,42 +544,31 @@ static dim3 table_grid(int rows, int cols) {  // about one entry per thread, wit
 
 cudaError_t launch_free(int32_t *table, int64_t ld, int rows, int cols, int32_t *lens, int32_t *refs, int pages,
                         const int32_t *which, int n, uint32_t *status, cudaStream_t stream) {
-    free_kernel<<<table_grid(n, cols), 256, 0, stream>>>(Table{table, ld, rows, cols}, lens, refs, pages, which, status);
-    return cudaGetLastError();
+    return launch_early(free_kernel, table_grid(n, cols), 256, 0, stream, Table{table, ld, rows, cols}, lens, refs, pages,
+                        which, status);
 }
 
 cudaError_t launch_fork(int32_t *table, int64_t ld, int rows, int cols, int32_t *lens, int32_t *refs, int pages, int page,
                         const int32_t *src, const int32_t *dst, int n, int32_t *copies, int32_t *scratch,
                         uint32_t *status, cudaStream_t stream) {
-    fork_kernel<<<kCtas, kThreads, 0, stream>>>(Table{table, ld, rows, cols}, lens, refs, pages, page, src, dst, n,
-                                                reinterpret_cast<int2 *>(copies), scratch, scratch + pages, status);
-    return cudaGetLastError();
+    return launch_early(fork_kernel, dim3(kCtas), kThreads, 0, stream, Table{table, ld, rows, cols}, lens, refs, pages, page,
+                        src, dst, n, reinterpret_cast<int2 *>(copies), scratch, scratch + pages, status);
 }
 
 cudaError_t launch_alloc(int32_t *table, int64_t ld, int rows, int cols, const int32_t *want, int32_t *refs, int pages,
                          int page, int32_t *scratch, uint32_t *status, cudaStream_t stream) {
-    alloc_kernel<<<kCtas, kThreads, 0, stream>>>(Table{table, ld, rows, cols}, want, refs, pages, page,
-                                                 scratch + 2 * (int64_t)rows, reinterpret_cast<int2 *>(scratch), status);
-    return cudaGetLastError();
+    return launch_early(alloc_kernel, dim3(kCtas), kThreads, 0, stream, Table{table, ld, rows, cols}, want, refs, pages,
+                        page, scratch + 2 * (int64_t)rows, reinterpret_cast<int2 *>(scratch), status);
 }
 
 cudaError_t launch_compact(int32_t *table, int64_t ld, int rows, int cols, int32_t *refs, int pages, int32_t *copies,
                            int32_t *count, int32_t *scratch, uint32_t *status, cudaStream_t stream) {
-    compact_kernel<<<kCtas, kThreads, 0, stream>>>(refs, pages, reinterpret_cast<int2 *>(copies), count, scratch + 4,
-                                                   scratch);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = launch_early(compact_kernel, dim3(kCtas), kThreads, 0, stream, refs, pages,
+                                 reinterpret_cast<int2 *>(copies), count, scratch + 4, scratch);
     if (e != cudaSuccess || rows == 0 || cols == 0) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = table_grid(rows < 65535 ? rows : 65535, cols);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rename_kernel, Table{table, ld, rows, cols}, pages,
-                              static_cast<const int32_t *>(scratch + 4), static_cast<const int32_t *>(scratch), status);
+    return launch_early(rename_kernel, table_grid(rows < 65535 ? rows : 65535, cols), 256, 0, stream,
+                        Table{table, ld, rows, cols}, pages, static_cast<const int32_t *>(scratch + 4),
+                        static_cast<const int32_t *>(scratch), status);
 }
 
 }  // namespace cache
