@@ -269,9 +269,10 @@ __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n
 // status bit; the whole call is then skipped). A decode sequence with a malformed
 // length is flagged and skipped alone. s0 gets the point's sequence. (It runs once,
 // before everything else that a CTA does, from a cold instruction cache: short code
-// counts more than few operations.)
+// counts more than few operations. A kernel calls it in one place, inlined, so that the
+// arguments are read from the constant bank.)
 template <bool PAGED, int KT>
-__device__ __noinline__ bool split_point(const Args &a, int c, Point &p0, Seq &s0) {
+__device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq &s0) {
     const int lane = threadIdx.x & 31;
     constexpr int kFlight = PAGED ? 4 : 1;  // groups of 32 sequences whose loads are in flight together
     uint32_t w[kFlight], total = 0;

@@ -263,9 +263,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     Point p0;
     Seq s0;
     bool any = false;
-    if (warp == kWarpSched || warp == kWarpFix) wait_before();
-    if (warp == kWarpSched) {  // where this CTA's work starts; kWarpFix: where it ends
-        if (!a.direct) any = split_point<PAGED, kTile>(a, cta, p0, s0) && p0.n < a.N;
+    if (warp == kWarpSched || warp == kWarpFix) {  // where this CTA's work starts; kWarpFix: where it ends
+        const int end = warp == kWarpFix;
+        wait_before();
+        if (!a.direct) {
+            any = split_point<PAGED, kTile>(a, cta + end, p0, s0) && p0.n < a.N;
+            if (end && lane == 0) {
+                *reinterpret_cast<Point *>(sm + L::kBars + Bars::kEnd) = p0;
+                part_header(a, 2 * cta)->valid = 0;
+                part_header(a, 2 * cta + 1)->valid = 0;
+            }
+        }
     } else if (warp == kWarpTma) {
         if (lane == 0) {
             for (int i = 0; i < L::kQs; ++i) {
@@ -290,15 +298,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kJobRing; ++i) tc::mbar_init(bars.jfull(i), 1);
             *reinterpret_cast<int *>(sm + L::kBars + Bars::kDead) = 0;
             tc::fence_mbar_init();
-        }
-    } else if (warp == kWarpFix) {
-        if (!a.direct) {
-            split_point<PAGED, kTile>(a, cta + 1, p0, s0);
-            if (lane == 0) {
-                *reinterpret_cast<Point *>(sm + L::kBars + Bars::kEnd) = p0;
-                part_header(a, 2 * cta)->valid = 0;
-                part_header(a, 2 * cta + 1)->valid = 0;
-            }
         }
     } else if (warp == kWarpMma) {
         tc::tmem_alloc(bars.base + Bars::kTmem, 512);
