@@ -111,7 +111,8 @@ struct Args {
     int has_new;             // decode: k_new / v_new given
     int tile_tokens;         // tokens of a row tile
     int streams;             // row tiles of an item: 2, or 1 when both streams share one row tile
-    int extra;               // an item's start and end, in keys
+    int extra;               // an item's start and end, in keys: decode: at least
+    int extra_short;         // extra_short less half of the item's own keys
     int min_part;            // keys of work below which no further CTA is used
     int cut;                 // tiles that a part of an item has at least
     int direct;              // one CTA for each slot of an item, nothing is split
@@ -207,8 +208,14 @@ template <bool PAGED, int KT>
 __device__ __forceinline__ int item_tiles(const Args &a, const Seq &s, int i) {
     return (int)(((unsigned)item_keys<PAGED>(a, s, i) + KT - 1) / KT) + (PAGED ? a.has_new : 0);
 }
+// An item's start and end, in keys. (Decode: an item of few tiles is a chain of
+// latencies, one of many is bound by its loads.)
+template <bool PAGED, int KT>
+__device__ __forceinline__ int item_extra(const Args &a, int nt) {
+    return PAGED ? max(a.extra, a.extra_short - nt * (KT / 2)) : a.extra;
+}
 // Weight of items 0 .. i - 1 of one kv head: an arithmetic series of visible keys and
-// `extra` keys per item, in units of a.unit keys, which the host chooses so that a
+// the items' starts and ends, in units of a.unit keys, which the host chooses so that a
 // call's total stays below 2^30, and one unit per item, so that no item weighs
 // nothing. Formed in fp32: every operation rounds monotonically, so the weights rise
 // with i, and all that follows is in whole units.
@@ -216,7 +223,8 @@ template <bool PAGED, int KT>
 __device__ __forceinline__ uint32_t items_weight(const Args &a, const Seq &s, int i) {
     float w;
     if (PAGED) {
-        w = (float)i * (float)(a.extra + item_tiles<PAGED, KT>(a, s, 0) * KT);
+        const int nt = item_tiles<PAGED, KT>(a, s, 0);
+        w = (float)i * (float)(item_extra<PAGED, KT>(a, nt) + nt * KT);
     } else {
         const int d = s.Lk - s.Lq, full = i < s.ni ? i : s.ni - 1;  // items without the sequence's last token
         const float block = (float)(a.tile_tokens * a.streams);
@@ -256,8 +264,8 @@ __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n
         lo += k * step;
     }
     p.i = lo;
-    const float y = (float)(x - items_weight<PAGED, KT>(a, s, lo)) * a.unit - 0.5f * (float)a.extra;
     const int nt = item_tiles<PAGED, KT>(a, s, lo);
+    const float y = (float)(x - items_weight<PAGED, KT>(a, s, lo)) * a.unit - 0.5f * (float)item_extra<PAGED, KT>(a, nt);
     const int t = (int)fminf(fmaxf(0.f, y * (1.f / KT) + 0.5f), (float)nt);
     // short pieces are not worth their join: such a cut moves to the item's edge
     p.tile = t < a.cut ? 0 : (t > nt - a.cut ? nt : t);

@@ -269,6 +269,7 @@ static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
     a.streams = 1;
     a.tile_tokens = PAGED && a.T * a.G < rows ? a.T : rows / a.G;
     a.extra = 64;
+    a.extra_short = 0;
     a.min_part = kF32MinPart;
     a.cut = 1;
     const long long slots = PAGED ? (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens)

@@ -358,7 +358,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = d->first_tok + (DUAL ? 0 : s * a.tile_tokens) + tok;
                 bits = a.mask != nullptr ? a.mask[(size_t)d->n * a.T + t]
                                          : (t >= 63 ? ~0ull : (2ull << t) - 1);
-                if (a.T < 64) bits &= (1ull << a.T) - 1;
             }
             // keys that the row tile's first row and this row see
             const int seen0 = d->seen + (PAGED ? 0 : s * a.tile_tokens);
@@ -377,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool drafts = PAGED && t == draft_tile;
                     if (drafts || seen0 < (t + 1) * kTile) {
                         // the keys that this row sees, a bit each
+                        if (PAGED && drafts && a.T < 64) bits &= (1ull << a.T) - 1;
                         const int lim = seen - t * kTile;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -1010,16 +1010,19 @@ bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
 template <bool PAGED, bool DUAL, int RT>
 cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
     a.streams = DUAL ? 1 : 2;
-    // An item's start and end cost about one and a half key tiles (of 64 .. 256 tried,
-    // 192 is best on ragged prompts and no worse for decode); pieces of fewer than three
-    // tiles do not pay for their join (2: 10 % slower on short prompts, 4: 5 to 10 % on
-    // short caches).
+    // An item's start and end cost about as much as 1.2 key tiles of 256 rows, and a tile that is
+    // cut short half of one (extra 192, 256, 320 on ragged prompts: 51.8, 53.0, 55.5 us); a
+    // decode's are hidden by the loads of long items, but not of short ones (192 alone,
+    // 320 alone, 192 and 512: 71.0, 66.8, 66.5 us for 128 sequences of 500 tokens, 254.0,
+    // 256.5, 254.1 for 3,125). Pieces of fewer than two tiles do not pay for their join (cut
+    // 1, 2, 3 on ragged prompts: 52.9, 51.8, 53.3 us).
     a.extra = 192;
+    a.extra_short = PAGED ? 512 : 0;
     a.min_part = kMinPart;
     // every item's keys, its start and end and, at the most, its drafts' tile
-    set_unit(a, (double)slots * ((double)keys + a.extra + kTile));
-    a.cut = 3;
-    a.direct = slots <= a.sms && keys <= (long long)(2 * a.cut - 1) * kTile;
+    set_unit(a, (double)slots * ((double)keys + 512 + kTile));
+    a.cut = 2;
+    a.direct = slots <= a.sms && keys <= 5 * kTile;
     constexpr int bytes = Smem<DUAL, RT>::kBytes;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;
