@@ -593,19 +593,24 @@ def kda_attn_prefill(q, k, v, scale, cu_seqlens=None, cu_seqlens_k=None, N=1, ou
         nq, nk = Tq // N, Tk // N
     if out is None:
         out = torch.empty((Tq, Hq, D), dtype=dt, device=q.device)
+        op = out.data_ptr()
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
+    else:
+        op = _take("out", out, dt, dev)
+    lp = None
     if lse is None:
         if output_lse:
             lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
+            lp = lse.data_ptr()
     elif lse.shape != (Tq, Hq):
         raise ValueError("lse must have the shape [Tq_total, Hq]")
+    else:
+        lp = _take("lse", lse, torch.float32, dev)
     if workspace is None:
         workspace = attn_prefill_workspace(q, k, cu_seqlens, N)
     rc = load().kda_attn_prefill(qp, kp, vp, ldq, ldk, ldv, scale, cup, cukp, N, nq, nk, Hq, Hkv,
-                                 D, io, _take("out", out, dt, dev),
-                                 _take("lse", lse, torch.float32, dev),
-                                 _take("workspace", workspace, torch.uint8, dev),
+                                 D, io, op, lp, _take("workspace", workspace, torch.uint8, dev),
                                  workspace.numel(), _stream_ptr(stream))
     if rc != KDA_OK:
         raise KDAError(rc, "kda_attn_prefill")
@@ -649,22 +654,27 @@ def kda_attn_decode(q, k_pages, v_pages, block_table, seq_lens, scale, k_new=Non
         raise ValueError("tree_mask must have the shape [B, T]")
     if out is None:
         out = torch.empty((B, T, Hq, D), dtype=dt, device=q.device)
+        op = out.data_ptr()
     elif out.shape != q.shape:
         raise ValueError("out must have the shape of q")
+    else:
+        op = _take("out", out, dt, dev)
+    lp = None
     if lse is None:
         if output_lse:
             lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
+            lp = lse.data_ptr()
     elif lse.shape != (B, T, Hq):
         raise ValueError("lse must have the shape [B, T, Hq]")
+    else:
+        lp = _take("lse", lse, torch.float32, dev)
     if workspace is None:
         workspace = attn_decode_workspace(q, k_pages, block_table)
     rc = load().kda_attn_decode(qp, ldq, knp, vnp, ldk, ldv, _take("k_pages", k_pages, dt, dev),
                                 _take("v_pages", v_pages, dt, dev), P, page, tp, ld, cols,
                                 _take("seq_lens", seq_lens, _I32, dev),
                                 _take("tree_mask", tree_mask, torch.int64, dev), scale, B, T, Hq,
-                                Hkv, D, io, _take("out", out, dt, dev),
-                                _take("lse", lse, torch.float32, dev),
-                                _take("workspace", workspace, torch.uint8, dev),
+                                Hkv, D, io, op, lp, _take("workspace", workspace, torch.uint8, dev),
                                 workspace.numel(), _stream_ptr(stream))
     if rc != KDA_OK:
         raise KDAError(rc, "kda_attn_decode")

@@ -1,9 +1,13 @@
 // Softmax attention in fp32 on CUDA cores (the formulas and the work split are
-// those of kda_attn.cuh): 128 threads hold 64 (token, head) rows, or 32 or 8 where a
-// kv head has no more (RPT = 8, 4 or 1 rows per thread); per tile of 64 keys a thread forms
-// an RPT x 4 piece of S = Q K^T and an RPT x 8 piece of O += P V. Bound by the FMA
-// pipe: with RPT = 8, 12 shared loads of 16 bytes per 128 FMAs (S) and 16 per 256 (O),
-// two CTAs per SM so that one loads while the other multiplies.
+// those of kda_attn.cuh): 128 threads hold 64 (token, head) rows, or 32, 24 or 8 where a
+// kv head has no more (RPT = 8, 4, 3 or 1 rows per thread); per tile of 64 keys a thread
+// forms an RPT x 4 piece of S = Q K^T and an RPT x 8 piece of O += P V, two products per
+// instruction. With RPT = 8 a step of four channels loads 192 bytes per thread for 128
+// FMAs, one of four keys 256 bytes for 256, so shared memory and the FMA pipe bound it
+// alike: 173 us for 5.7 GFLOP of causal attention over 2,011 tokens, 33 TFLOP/s of the
+// 75 that the FMA pipe has. With few rows it is the loads: 65 us for one token on 40,000 cached
+// ones (164 MB, 2.5 TB/s), in a chain of copies that come while the tile before is multiplied
+// (79 us when they did not). Two CTAs per SM.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -15,9 +19,10 @@ namespace attn {
 
 constexpr int kF32Threads = 128;
 constexpr int kF32Tile = 64;          // keys; rows: 8 RPT
-constexpr int kPitch = kD + 4;        // floats per Q / K row: neighbouring rows on other banks
-constexpr int kPitchP = kF32Tile + 4;
-constexpr int f32_smem(int rpt) { return ((8 * rpt + kF32Tile) * kPitch + kF32Tile * kD) * 4; }
+// Q, K, V and P. Rows that a warp reads together would lie on the same banks: the 16-byte
+// pieces of a K row stand in the order of (piece xor row % 8), of a Q row of (piece xor
+// its thread row % 8), the 16-key groups of a P row of (group xor thread row % 2).
+constexpr int f32_smem(int rpt) { return (8 * rpt * (kD + kF32Tile) + 2 * kF32Tile * kD) * 4; }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0)
@@ -38,8 +43,7 @@ template <bool PAGED, int RPT>
 __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_constant__ Args a, const F32Ptrs io) {
     extern __shared__ __align__(16) float smf[];
     constexpr int kRows = 8 * RPT;
-    float *const Qs = smf, *const Ks = smf + kRows * kPitch, *const Vs = Ks + kF32Tile * kPitch;
-    float *const Ps = Ks;  // P replaces K once S is formed
+    float *const Qs = smf, *const Ks = Qs + kRows * kD, *const Vs = Ks + kF32Tile * kD, *const Ps = Vs + kF32Tile * kD;
     __shared__ Point pts[2];
     __shared__ Seq seq0;
     __shared__ int any;
@@ -82,12 +86,12 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             const int r = x >> 5, ch = (x & 31) * 4, tok = r / G;
             const bool ok = r < rows;
             const float *src = io.q + (ok ? (long long)(p.q0 + tok) * io.ldq + (p.h * G + r - tok * G) * kD + ch : 0);
-            cp16(smem_u32(Qs + r * kPitch + ch), src, ok);
+            cp16(smem_u32(Qs + r * kD + (ch ^ (r / RPT % 8 * 4))), src, ok);
         }
         cp_commit();
         float m[RPT], l[RPT];
         float4 o[RPT][2];
-        long long seen[RPT];  // keys that the row sees (of the cache: all)
+        int seen[RPT];  // keys that the row sees (of the cache: all)
         unsigned long long bits[RPT];
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             l[i] = 0.f;
             o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
             const int r = RPT * ty + i, t = p.first_tok + r / G;
-            seen[i] = PAGED ? p.Lk : (long long)p.Lk - p.Lq + t + 1;
+            seen[i] = PAGED ? p.Lk : p.Lk - p.Lq + t + 1;
             bits[i] = 0;
             if (PAGED && r < rows) {
                 bits[i] = a.mask != nullptr ? a.mask[(size_t)p.n * a.T + t]
@@ -103,45 +107,58 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                 if (a.T < 64) bits[i] &= (1ull << a.T) - 1;
             }
         }
-        for (int t = p.ta; t < p.tb; ++t) {
-            const bool drafts = PAGED && a.has_new && t == p.nt - 1;
+        // A warp copies the rows warp, warp + 4, ..: lane i knows where row warp + 4 i is.
+        struct Where {
+            long long k, v;
+            unsigned rows_ok;
+            bool drafts;
+        };
+        const int mine = warp + 4 * (lane & 15);
+        auto locate = [&](int t) {
+            Where w = {0, 0, 0, PAGED && a.has_new && t == p.nt - 1};
             // keys past the end load as zeros (0 times what is there could be NaN)
-            const int valid = drafts ? a.T : min(kF32Tile, p.Lk - t * kF32Tile);
-            __syncthreads();
-            // A warp copies the rows warp, warp + 4, ..: lane i finds where row warp + 4 i is.
-            const int mine = warp + 4 * (lane & 15);
+            const int valid = w.drafts ? a.T : min(kF32Tile, p.Lk - t * kF32Tile);
             bool ok = mine < valid;
-            long long at = 0, at_v = 0;
             if (!PAGED) {
-                at = (long long)(p.k0 + t * kF32Tile + mine) * io.ldk;
-                at_v = (long long)(p.k0 + t * kF32Tile + mine) * io.ldv;
-            } else if (drafts) {
-                at = (long long)(p.n * a.T + mine) * io.ldk;
-                at_v = (long long)(p.n * a.T + mine) * io.ldv;
+                w.k = (long long)(p.k0 + t * kF32Tile + mine) * io.ldk;
+                w.v = (long long)(p.k0 + t * kF32Tile + mine) * io.ldv;
+            } else if (w.drafts) {
+                w.k = (long long)(p.n * a.T + mine) * io.ldk;
+                w.v = (long long)(p.n * a.T + mine) * io.ldv;
             } else if (ok) {
                 const int pos = t * kF32Tile + mine;
                 const int pg = a.table[(size_t)p.n * a.table_ld + (pos >> page_bits)];
                 ok = pg >= 0 && pg < a.pages;
                 if (!ok) atomicOr(status_word(a), kStatusBadSeqlens);  // zeros instead
-                else at = at_v = (((long long)pg * a.Hkv) * a.page + (pos & (a.page - 1))) * kD;
+                else w.k = w.v = (((long long)pg * a.Hkv) * a.page + (pos & (a.page - 1))) * kD;
             }
-            const long long head = (PAGED && !drafts ? (long long)p.h * a.page : p.h) * kD;
-            const float *const ksrc = (drafts ? io.kn : io.k) + head, *const vsrc = (drafts ? io.vn : io.v) + head;
-            const unsigned rows_ok = __ballot_sync(0xffffffffu, ok);
+            w.rows_ok = __ballot_sync(0xffffffffu, ok);
+            return w;
+        };
+        auto copy = [&](const Where &w, bool is_v) {
+            const long long head = (PAGED && !w.drafts ? (long long)p.h * a.page : p.h) * kD + 4 * lane;
+            const float *const src = (is_v ? (w.drafts ? io.vn : io.v) : (w.drafts ? io.kn : io.k)) + head;
+            float *const dst = is_v ? Vs : Ks;
 #pragma unroll 4
             for (int i = 0; i < 16; ++i) {
-                const bool in = rows_ok >> i & 1;
-                const long long off = __shfl_sync(0xffffffffu, at, i);
-                cp16(smem_u32(Ks + (warp + 4 * i) * kPitch + 4 * lane), in ? ksrc + off + 4 * lane : io.q, in);
+                const bool in = w.rows_ok >> i & 1;
+                const long long off = __shfl_sync(0xffffffffu, is_v ? w.v : w.k, i);
+                const int r = warp + 4 * i;
+                cp16(smem_u32(dst + r * kD + (is_v ? 4 * lane : 4 * (lane ^ (r & 7)))), in ? src + off : io.q, in);
             }
+        };
+        // K of the next tile comes while this one's P V is formed, its V during the next Q K^T.
+        Where next = {};
+        if (p.ta < p.tb) {
+            next = locate(p.ta);
+            copy(next, false);
             cp_commit();
-#pragma unroll 4
-            for (int i = 0; i < 16; ++i) {
-                const bool in = rows_ok >> i & 1;
-                const long long off = __shfl_sync(0xffffffffu, at_v, i);
-                cp16(smem_u32(Vs + (warp + 4 * i) * kD + 4 * lane), in ? vsrc + off + 4 * lane : io.q, in);
-            }
+            copy(next, true);
             cp_commit();
+        }
+        for (int t = p.ta; t < p.tb; ++t) {
+            const bool drafts = next.drafts;
+            if (t + 1 < p.tb) next = locate(t + 1);
             cp_wait<1>();
             __syncthreads();
             // (two terms of a dot product per instruction, as two sums: half the issue slots)
@@ -150,10 +167,10 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             for (int d = 0; d < kD; d += 4) {
                 float4 kk[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) kk[e] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * e) * kPitch + d);
+                for (int e = 0; e < 4; ++e) kk[e] = *reinterpret_cast<const float4 *>(Ks + (tx + 16 * e) * kD + (d ^ (tx % 8 * 4)));
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    const float4 qq = *reinterpret_cast<const float4 *>(Qs + (RPT * ty + i) * kPitch + d);
+                    const float4 qq = *reinterpret_cast<const float4 *>(Qs + (RPT * ty + i) * kD + (d ^ (ty % 8 * 4)));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         s2[i][e] = fma2(make_float2(qq.x, qq.y), make_float2(kk[e].x, kk[e].y), s2[i][e]);
@@ -166,14 +183,16 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             for (int i = 0; i < RPT; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[i][e] = s2[i][e].x + s2[i][e].y;
-            __syncthreads();  // K is read: P may replace it
+            __syncthreads();  // K is read
+            if (t + 1 < p.tb) copy(next, false);
+            cp_commit();
 #pragma unroll
             for (int i = 0; i < RPT; ++i) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = tx + 16 * e;
-                    const bool see = drafts ? (bits[i] >> key & 1) != 0 : seen[i] > (long long)t * kF32Tile + key;
+                    const bool see = drafts ? (bits[i] >> key & 1) != 0 : seen[i] > t * kF32Tile + key;
                     if (!see) s[i][e] = -INFINITY;
                     top = fmaxf(top, s[i][e]);
                 }
@@ -188,7 +207,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                 for (int e = 0; e < 4; ++e) {
                     const float y = exp2f(fmaf(s[i][e], c, -uc));
                     sum += y;
-                    Ps[(RPT * ty + i) * kPitchP + tx + 16 * e] = y;
+                    Ps[(RPT * ty + i) * kF32Tile + tx + 16 * (e ^ (ty & 1))] = y;
                 }
                 l[i] = l[i] * f + sum;  // this lane's keys; joined at the end
 #pragma unroll
@@ -199,7 +218,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                     o[i][e].w *= f;
                 }
             }
-            cp_wait<0>();
+            cp_wait<1>();
             __syncthreads();
 #pragma unroll 2
             for (int key = 0; key < kF32Tile; key += 4) {
@@ -211,7 +230,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                         vv[x][e] = *reinterpret_cast<const float4 *>(Vs + (key + x) * kD + 4 * tx + 64 * e);
 #pragma unroll
                 for (int i = 0; i < RPT; ++i) {
-                    const float4 pp = *reinterpret_cast<const float4 *>(Ps + (RPT * ty + i) * kPitchP + key);
+                    const float4 pp = *reinterpret_cast<const float4 *>(Ps + (RPT * ty + i) * kF32Tile + (key ^ (ty % 2 * 16)));
                     const float w[4] = {pp.x, pp.y, pp.z, pp.w};
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
@@ -225,6 +244,9 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                     }
                 }
             }
+            __syncthreads();  // V and P are read
+            if (t + 1 < p.tb) copy(next, true);
+            cp_commit();
         }
         if (p.ta >= p.tb) cp_wait<0>();  // Q of a part without keys
 #pragma unroll
@@ -297,7 +319,10 @@ cudaError_t launch_attn_decode_f32(const Args &a, const void *q, const void *kp,
     const F32Ptrs io = {static_cast<const float *>(q), static_cast<const float *>(kp), static_cast<const float *>(vp),
                         static_cast<const float *>(kn), static_cast<const float *>(vn), ldq, ldk, ldv};
     const int rows = a.T * a.G;
+    // (RPT 8 or 1 for one token per kv head on 40,000: 95, 65 us; 8, 4 or 3 for the 22 rows of a tree of
+    // 11 drafts on six caches of 1,500: 99, 36.0, 33.2 us)
     return rows <= 8    ? launch_f32<true, 1>(a, io, stream)
+           : rows <= 24 ? launch_f32<true, 3>(a, io, stream)
            : rows <= 32 ? launch_f32<true, 4>(a, io, stream)
                         : launch_f32<true, 8>(a, io, stream);
 }
