@@ -470,6 +470,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 early = *early_there != 0;
             }
             const bool whole = d->whole || (early && d->ta == 0);
+            // the stage is free when its last copy has read it (seen to before O is there)
+            const bool staged = !DUAL && whole && (steps > 0 || early), leader = quad == 0 && lane == 0;
+            if (staged) {
+                if (leader) tc::bulk_wait_read();
+                named_bar(1 + s, 128);
+            }
             const float *const next_o = part_o(a, 2 * (cta + 1));
             if (steps > 0) {
                 if (!warp_wait(bars.ofull(s), no++ & 1)) {
@@ -479,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::fence_after_sync();
             }
             const bool writer = !DUAL || s == d->writer, joins = DUAL && steps > 0 && others > 0;
-            if ((warp_ok || (!DUAL && whole && (steps > 0 || early))) && (writer || joins)) {
+            if ((warp_ok || staged) && (writer || joins)) {
                 // In two parts of 64 channels: O from TMEM; the second stream of a join
                 // hands it over in shared memory; the writer stores the sum, or stages it
                 // for whole rows to leave together.
@@ -492,12 +498,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool full = !DUAL && d->tokens[s] == a.tile_tokens;
                 const uint32_t stage_at = DUAL ? L::kQ + d->q[s] % L::kQs * L::kQTile : L::kStage + s * kHalf;
                 unsigned char *const stage = sm + stage_at;
-                const bool leader = quad == 0 && lane == 0;
                 const int rows = d->tokens[s] * a.G;
                 __nv_bfloat16 *const out = static_cast<__nv_bfloat16 *>(a.out);
+                auto write_lse = [&]() {
+                    if (whole && row_ok && a.lse != nullptr)
+                        a.lse[(size_t)(q0 + tok) * a.Hq + row0 + g] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+                };
                 float f = 1.f, f1 = 0.f;
 #pragma unroll 1
                 for (int p = 0; p < 2; ++p) {
+                    if (!DUAL && p == 1) write_lse();  // (while the first half's copy reads the stage)
                     uint32_t o[4][16] = {};
                     if (steps > 0) tc::tmem_ld_cols<4>(tO + 64 * p, o);
                     if (!writer) {
@@ -564,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         continue;
                     }
-                    if (!DUAL) {  // the stage is free when its last copy has read it
+                    if (!DUAL && p == 1) {
                         if (leader) tc::bulk_wait_read();
                         named_bar(1 + s, 128);
                     }
@@ -601,8 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (writer && !whole) {
                     if (row_ok) part_ml(a, d->slot)[DUAL ? r : 128 * s + r] = make_float2(m, l);
                 } else if (writer) {
-                    if (row_ok && a.lse != nullptr)
-                        a.lse[(size_t)(q0 + tok) * a.Hq + row0 + g] = l == 0.f ? -INFINITY : m * a.scale + logf(l);
+                    if (DUAL) write_lse();
                     if (DUAL && steps > 0) {
                         __syncwarp();
                         const int ch = lane & 15;  // sixteen lanes write a row's 256 bytes
