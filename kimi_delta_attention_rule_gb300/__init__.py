@@ -1,9 +1,10 @@
 """KDA (Kimi Delta Attention) operator for NVIDIA GB300, behind a C ABI.
 
 The compute runs in ``libkda.so`` (hand-written CUDA for sm_103a, declared
-in ``include/kda.h``). This package is a thin ctypes binding with the same
-entry-point names; PyTorch only supplies device memory and streams. There is
-no CPU fallback: if the library is missing, every call raises.
+in ``include/kda.h``). This package is a thin binding with the same entry-point
+names (ctypes; for the attention and cache calls, native: ``_kda_bind.so``);
+PyTorch only supplies device memory and streams. There is no CPU fallback: if
+the library is missing, every call raises.
 """
 from __future__ import annotations
 
@@ -452,64 +453,29 @@ def kda_check_cu_seqlens(cu_host, T_total: int) -> int:
 
 
 # ---- softmax attention and the pages of its cache ---------------------------------
-# The checks look at each tensor once and return what the C call needs of it: with
-# a launch of a few microseconds, what Python does per argument counts.
-_I32 = torch.int32
+# Their kernels take a few microseconds, so what a call does on the host counts: the
+# tensors are looked at, and what the caller left out is allocated, in native code
+# (csrc/kda_bind.cpp, built next to libkda.so).
+_BIND_ENTRIES = ("kda_attn_prefill_workspace_size", "kda_attn_prefill",
+                 "kda_attn_decode_workspace_size", "kda_attn_decode", "kda_cache_workspace_size",
+                 "kda_cache_alloc", "kda_cache_fork", "kda_cache_free", "kda_cache_compact",
+                 "kda_cache_copy", "kda_cache_append")
+_bind = None
 
 
-def _refuse(name, t, dtype, dev):
-    if not t.is_cuda:
-        raise ValueError("KDA tensors must be CUDA tensors")
-    if t.dtype is not dtype:
-        raise ValueError("%s must have dtype %s" % (name, dtype))
-    if t.get_device() != dev:
-        raise ValueError("KDA tensors must be on one device")
-    raise ValueError("%s must be contiguous" % name)
-
-
-def _take(name, t, dtype, dev):
-    """The address of a contiguous tensor (None: NULL)."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
-        _refuse(name, t, dtype, dev)
-    return t.data_ptr()
-
-
-def _take_rows(name, t, dtype, dev, H, D):
-    """(address, elements from one token row to the next) of [.., H, D]: the heads
-    and channels of a row must be contiguous, the tokens evenly spaced."""
-    if t.dtype is not dtype or t.get_device() != dev:
-        _refuse(name, t, dtype, dev)
-    shape, st = t.shape, t.stride()
-    if st[-1] != 1 and D > 1 or st[-2] != D and H > 1:
-        raise ValueError("%s: the [heads, D] rows must be contiguous" % name)
-    if len(st) == 3:
-        return t.data_ptr(), st[0] if shape[0] > 1 else H * D
-    B, T = shape[0], shape[1]
-    if T == 1:
-        return t.data_ptr(), st[0] if B > 1 else H * D
-    if B > 1 and st[0] != T * st[1]:
-        raise ValueError("%s: the tokens must be evenly spaced" % name)
-    return t.data_ptr(), st[1]
-
-
-def _take_table(t):
-    """(address, row stride, rows, cols, device) of a block table."""
-    if t.dtype is not _I32 or not t.is_cuda or t.dim() != 2:
-        raise ValueError("block_table must be a CUDA int32 [rows, cols] tensor")
-    rows, cols = t.shape
-    st = t.stride()
-    if cols > 1 and st[1] != 1:
-        raise ValueError("the rows of block_table must be contiguous")
-    return t.data_ptr(), st[0] if rows > 1 else cols, rows, cols, t.get_device()
-
-
-def _device_of(t):
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("KDA tensors must be CUDA tensors")
-    return dev
+def _native():
+    """The binding module of these entry points; raises if it is absent."""
+    global _bind
+    if _bind is None:
+        lib = load()
+        try:
+            from . import _kda_bind
+        except ImportError as e:
+            raise RuntimeError("_kda_bind.so is not built (%s); run __graft_entry__.build()" % e)
+        _kda_bind.init(tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+                             for n in _BIND_ENTRIES), KDAError)
+        _bind = _kda_bind
+    return _bind
 
 
 def _new_workspace(nbytes: int, device) -> torch.Tensor:
@@ -568,53 +534,8 @@ def kda_attn_prefill(q, k, v, scale, cu_seqlens=None, cu_seqlens_k=None, N=1, ou
     the same), or None (N sequences of equal length). A sequence's last token
     sees all of its keys. Returns (out [Tq_total, Hq, D], lse fp32 [Tq_total,
     Hq] or None)."""
-    dt, dev = q.dtype, _device_of(q)
-    io = _io_code(dt)
-    Tq, Hq, D = q.shape
-    Tk, Hkv, Dk = k.shape
-    if v.shape != k.shape or Dk != D:
-        raise ValueError("k and v must have the shape [Tk_total, Hkv, D]")
-    qp, ldq = _take_rows("q", q, dt, dev, Hq, D)
-    kp, ldk = _take_rows("k", k, dt, dev, Hkv, D)
-    vp, ldv = _take_rows("v", v, dt, dev, Hkv, D)
-    cup = cukp = None
-    if cu_seqlens is not None:
-        cup = _take("cu_seqlens", cu_seqlens, _I32, dev)
-        N, nq, nk = cu_seqlens.numel() - 1, Tq, Tk
-        if cu_seqlens_k is not None:
-            cukp = _take("cu_seqlens_k", cu_seqlens_k, _I32, dev)
-            if cu_seqlens_k.numel() != N + 1:
-                raise ValueError("cu_seqlens_k must have as many offsets as cu_seqlens")
-    else:
-        if cu_seqlens_k is not None:
-            raise ValueError("cu_seqlens_k needs cu_seqlens")
-        if N < 1 or Tq % N or Tk % N:
-            raise ValueError("q and k must hold N sequences of equal length")
-        nq, nk = Tq // N, Tk // N
-    if out is None:
-        out = torch.empty((Tq, Hq, D), dtype=dt, device=q.device)
-        op = out.data_ptr()
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    else:
-        op = _take("out", out, dt, dev)
-    lp = None
-    if lse is None:
-        if output_lse:
-            lse = torch.empty((Tq, Hq), dtype=torch.float32, device=q.device)
-            lp = lse.data_ptr()
-    elif lse.shape != (Tq, Hq):
-        raise ValueError("lse must have the shape [Tq_total, Hq]")
-    else:
-        lp = _take("lse", lse, torch.float32, dev)
-    if workspace is None:
-        workspace = attn_prefill_workspace(q, k, cu_seqlens, N)
-    rc = load().kda_attn_prefill(qp, kp, vp, ldq, ldk, ldv, scale, cup, cukp, N, nq, nk, Hq, Hkv,
-                                 D, io, op, lp, _take("workspace", workspace, torch.uint8, dev),
-                                 workspace.numel(), _stream_ptr(stream))
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_attn_prefill")
-    return out, lse
+    return (_bind or _native()).attn_prefill(q, k, v, scale, cu_seqlens, cu_seqlens_k, N, out, lse,
+                                             output_lse, workspace, stream)
 
 
 def kda_attn_decode(q, k_pages, v_pages, block_table, seq_lens, scale, k_new=None, v_new=None,
@@ -628,74 +549,16 @@ def kda_attn_decode(q, k_pages, v_pages, block_table, seq_lens, scale, k_new=Non
     [B, T, Hkv, D] of the new tokens themselves (or None); tree_mask: int64
     [B, T], bit s = the token sees new token s (None: the chain, s <= t).
     Returns (out [B, T, Hq, D], lse fp32 [B, T, Hq] or None)."""
-    dt, dev = q.dtype, _device_of(q)
-    io = _io_code(dt)
-    B, T, Hq, D = q.shape
-    P, Hkv, page, Dk = k_pages.shape
-    if v_pages.shape != k_pages.shape or Dk != D:
-        raise ValueError("k_pages and v_pages must have the shape [P, Hkv, page, D]")
-    qp, ldq = _take_rows("q", q, dt, dev, Hq, D)
-    knp = vnp = None
-    ldk = ldv = 0
-    if k_new is not None:
-        if k_new.shape != (B, T, Hkv, D):
-            raise ValueError("k_new must have the shape [B, T, Hkv, D]")
-        knp, ldk = _take_rows("k_new", k_new, dt, dev, Hkv, D)
-    if v_new is not None:
-        if v_new.shape != (B, T, Hkv, D):
-            raise ValueError("v_new must have the shape [B, T, Hkv, D]")
-        vnp, ldv = _take_rows("v_new", v_new, dt, dev, Hkv, D)
-    tp, ld, rows, cols, tdev = _take_table(block_table)
-    if tdev != dev:
-        raise ValueError("KDA tensors must be on one device")
-    if rows != B or seq_lens.shape != (B,):
-        raise ValueError("block_table and seq_lens must have a row for each sequence")
-    if tree_mask is not None and tree_mask.shape != (B, T):
-        raise ValueError("tree_mask must have the shape [B, T]")
-    if out is None:
-        out = torch.empty((B, T, Hq, D), dtype=dt, device=q.device)
-        op = out.data_ptr()
-    elif out.shape != q.shape:
-        raise ValueError("out must have the shape of q")
-    else:
-        op = _take("out", out, dt, dev)
-    lp = None
-    if lse is None:
-        if output_lse:
-            lse = torch.empty((B, T, Hq), dtype=torch.float32, device=q.device)
-            lp = lse.data_ptr()
-    elif lse.shape != (B, T, Hq):
-        raise ValueError("lse must have the shape [B, T, Hq]")
-    else:
-        lp = _take("lse", lse, torch.float32, dev)
-    if workspace is None:
-        workspace = attn_decode_workspace(q, k_pages, block_table)
-    rc = load().kda_attn_decode(qp, ldq, knp, vnp, ldk, ldv, _take("k_pages", k_pages, dt, dev),
-                                _take("v_pages", v_pages, dt, dev), P, page, tp, ld, cols,
-                                _take("seq_lens", seq_lens, _I32, dev),
-                                _take("tree_mask", tree_mask, torch.int64, dev), scale, B, T, Hq,
-                                Hkv, D, io, op, lp, _take("workspace", workspace, torch.uint8, dev),
-                                workspace.numel(), _stream_ptr(stream))
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_attn_decode")
-    return out, lse
+    return (_bind or _native()).attn_decode(q, k_pages, v_pages, block_table, seq_lens, scale, k_new,
+                                            v_new, tree_mask, out, lse, output_lse, workspace,
+                                            stream)
 
 
 def kda_cache_alloc(block_table, want, refs, page_size, workspace=None, stream=None):
     """Gives every row of block_table the pages it lacks for want[row] tokens (C
     entry point ``kda_cache_alloc``); refs: int32 [P]. All device int32 arrays,
     updated in place."""
-    tp, ld, rows, cols, dev = _take_table(block_table)
-    if want.shape != (rows,):
-        raise ValueError("want must have an entry for each row")
-    if workspace is None:
-        workspace = cache_workspace(refs, rows)
-    rc = load().kda_cache_alloc(tp, ld, rows, cols, _take("want", want, _I32, dev),
-                                _take("refs", refs, _I32, dev), refs.numel(), page_size,
-                                _take("workspace", workspace, torch.uint8, dev),
-                                workspace.numel(), _stream_ptr(stream))
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_cache_alloc")
+    (_bind or _native()).cache_alloc(block_table, want, refs, page_size, workspace, stream)
 
 
 def kda_cache_fork(block_table, seq_lens, refs, src, dst, page_size, copies=None, workspace=None,
@@ -703,90 +566,28 @@ def kda_cache_fork(block_table, seq_lens, refs, src, dst, page_size, copies=None
     """Row dst[i] becomes a copy of row src[i], sharing its full pages (C entry
     point ``kda_cache_fork``). Returns copies int32 [n, 2]: the (from, to) pages
     that ``kda_cache_copy`` has to copy in every pool, (-1, -1) for none."""
-    tp, ld, rows, cols, dev = _take_table(block_table)
-    n = src.numel()
-    if dst.numel() != n or seq_lens.shape != (rows,):
-        raise ValueError("src and dst must pair up, seq_lens must have an entry for each row")
-    if copies is None:
-        copies = torch.empty((n, 2), dtype=_I32, device=block_table.device)
-    elif copies.shape != (n, 2):
-        raise ValueError("copies must have the shape [n, 2]")
-    if workspace is None:
-        workspace = cache_workspace(refs, rows)
-    rc = load().kda_cache_fork(tp, ld, rows, cols, _take("seq_lens", seq_lens, _I32, dev),
-                               _take("refs", refs, _I32, dev), refs.numel(), page_size,
-                               _take("src", src, _I32, dev), _take("dst", dst, _I32, dev), n,
-                               _take("copies", copies, _I32, dev),
-                               _take("workspace", workspace, torch.uint8, dev),
-                               workspace.numel(), _stream_ptr(stream))
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_cache_fork")
-    return copies
+    return (_bind or _native()).cache_fork(block_table, seq_lens, refs, src, dst, page_size, copies,
+                                           workspace, stream)
 
 
 def kda_cache_free(block_table, seq_lens, refs, rows, workspace=None, stream=None):
     """Drops the pages of the given rows (device int32, distinct; < 0 is skipped;
     C entry point ``kda_cache_free``)."""
-    tp, ld, n_rows, cols, dev = _take_table(block_table)
-    if seq_lens.shape != (n_rows,):
-        raise ValueError("seq_lens must have an entry for each row")
-    if workspace is None:
-        workspace = cache_workspace(refs, n_rows)
-    rc = load().kda_cache_free(tp, ld, n_rows, cols, _take("seq_lens", seq_lens, _I32, dev),
-                               _take("refs", refs, _I32, dev), refs.numel(),
-                               _take("rows", rows, _I32, dev), rows.numel(),
-                               _take("workspace", workspace, torch.uint8, dev),
-                               workspace.numel(), _stream_ptr(stream))
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_cache_free")
+    (_bind or _native()).cache_free(block_table, seq_lens, refs, rows, workspace, stream)
 
 
 def kda_cache_compact(block_table, refs, copies=None, count=None, workspace=None, stream=None):
     """Renames the live pages to 0 .. L - 1 (C entry point ``kda_cache_compact``).
     Returns (copies int32 [P, 2], count int32 [1]): the (from, to) pages that
     ``kda_cache_copy`` has to copy in every pool, and how many."""
-    tp, ld, rows, cols, dev = _take_table(block_table)
-    P = refs.numel()
-    if copies is None:
-        copies = torch.empty((P, 2), dtype=_I32, device=refs.device)
-    elif copies.shape != (P, 2):
-        raise ValueError("copies must have the shape [P, 2]")
-    if count is None:
-        count = torch.empty(1, dtype=_I32, device=refs.device)
-    if workspace is None:
-        workspace = cache_workspace(refs, rows)
-    rc = load().kda_cache_compact(tp, ld, rows, cols, _take("refs", refs, _I32, dev), P,
-                                  _take("copies", copies, _I32, dev),
-                                  _take("count", count, _I32, dev),
-                                  _take("workspace", workspace, torch.uint8, dev),
-                                  workspace.numel(), _stream_ptr(stream))
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_cache_compact")
-    return copies, count
+    return (_bind or _native()).cache_compact(block_table, refs, copies, count, workspace, stream)
 
 
 def kda_cache_copy(pools, copies, count=None, stream=None):
     """Entry copies[i][1] = entry copies[i][0] in each pool (C entry point
     ``kda_cache_copy``): pools of equal shape [entries, ...], any dtype; copies
     int32 [n, 2]; count: device int32 [1], only the first *count pairs."""
-    n_pools = len(pools)
-    if n_pools == 0:
-        return
-    first = pools[0]
-    dev = _device_of(first)
-    if copies.dim() != 2 or copies.shape[1] != 2:
-        raise ValueError("copies must have the shape [n, 2]")
-    entries, nbytes = first.shape[0], first.nbytes
-    ptrs = (ctypes.c_void_p * n_pools)()
-    for i, p in enumerate(pools):
-        if p.shape[0] != entries or p.nbytes != nbytes:
-            raise ValueError("the pools must have entries of one size")
-        ptrs[i] = _take("pools", p, p.dtype, dev)
-    rc = load().kda_cache_copy(ptrs, n_pools, nbytes // max(entries, 1), entries,
-                               _take("copies", copies, _I32, dev), copies.shape[0],
-                               _take("count", count, _I32, dev), _stream_ptr(stream))
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_cache_copy")
+    (_bind or _native()).cache_copy(pools, copies, count, stream)
 
 
 def kda_cache_append(k, v, k_pages, v_pages, block_table, start, cu_seqlens=None, index=None,
@@ -797,35 +598,5 @@ def kda_cache_append(k, v, k_pages, v_pages, block_table, start, cu_seqlens=None
     k, v: packed [T_total, Hkv, D] with cu_seqlens (device int32 [N+1]), or
     [N, T, Hkv, D], of which sequence b appends the rows index[b, :count[b]]
     (device int32; None: all, in order): the accepted tokens of a draft."""
-    dt, dev = k.dtype, _device_of(k)
-    io = _io_code(dt)
-    P, Hkv, page, D = k_pages.shape
-    if v.shape != k.shape or v_pages.shape != k_pages.shape or k.shape[-2:] != (Hkv, D):
-        raise ValueError("k, v must be rows of [Hkv, D], the pools [P, Hkv, page, D]")
-    if cu_seqlens is not None:
-        if k.dim() != 3:
-            raise ValueError("packed rows must be [T_total, Hkv, D]")
-        N, T = cu_seqlens.numel() - 1, k.shape[0]
-    else:
-        if k.dim() != 4:
-            raise ValueError("rows without cu_seqlens must be [N, T, Hkv, D]")
-        N, T = k.shape[:2]
-    kp, ldk = _take_rows("k", k, dt, dev, Hkv, D)
-    vp, ldv = _take_rows("v", v, dt, dev, Hkv, D)
-    tp, ld, rows, cols, tdev = _take_table(block_table)
-    if tdev != dev:
-        raise ValueError("KDA tensors must be on one device")
-    if rows < N or start.shape != (N,):
-        raise ValueError("block_table and start must have a row for each sequence")
-    if index is not None and index.shape != (N, T) or count is not None and count.shape != (N,):
-        raise ValueError("index must have the shape [N, T], count [N]")
-    rc = load().kda_cache_append(kp, vp, ldk, ldv, _take("cu_seqlens", cu_seqlens, _I32, dev), N, T,
-                                 _take("index", index, _I32, dev),
-                                 _take("count", count, _I32, dev),
-                                 _take("start", start, _I32, dev), tp, ld, cols, P, page, Hkv, D,
-                                 io, _take("k_pages", k_pages, dt, dev),
-                                 _take("v_pages", v_pages, dt, dev),
-                                 _take("workspace", workspace, torch.uint8, dev),
-                                 _stream_ptr(stream))
-    if rc != KDA_OK:
-        raise KDAError(rc, "kda_cache_append")
+    (_bind or _native()).cache_append(k, v, k_pages, v_pages, block_table, start, cu_seqlens, index,
+                                      count, workspace, stream)

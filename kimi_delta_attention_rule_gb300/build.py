@@ -1,7 +1,9 @@
-"""Builds libkda.so (the CUDA kernels + C ABI) in-tree for sm_103a.
+"""Builds libkda.so (the CUDA kernels + C ABI) in-tree for sm_103a, and
+_kda_bind.so (the Python side of the attention and cache calls).
 
 Each translation unit is compiled in parallel with nvcc, then linked into
-one shared library next to this file. Re-running skips an up-to-date build.
+one shared library next to this file; the binding, which alone sees PyTorch's
+headers, is one file for the host compiler. Re-running skips an up-to-date build.
 """
 from __future__ import annotations
 
@@ -17,6 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libkda.so")
+BIND_SRC = os.path.join(CSRC, "kda_bind.cpp")
+BIND = os.path.join(PKG, "_kda_bind.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -46,8 +50,39 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _bind_up_to_date() -> bool:
+    if not os.path.exists(BIND):
+        return False
+    t = os.path.getmtime(BIND)
+    return all(os.path.getmtime(p) <= t for p in [BIND_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def build_bind(force: bool = False) -> str:
+    """The binding module, against the PyTorch that runs this."""
+    if not force and _bind_up_to_date():
+        return BIND
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    tmp = BIND + ".tmp%d" % os.getpid()
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + INCLUDE]
+    for d in inc:
+        cmd += ["-isystem", d]
+    cmd += [BIND_SRC, "-o", tmp, "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s failed on %s:\n%s\n%s" % (cmd[0], BIND_SRC, r.stdout, r.stderr))
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
+        build_bind()
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     cc = nvcc()
@@ -61,7 +96,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        bind = ex.submit(build_bind, force)
         results = list(ex.map(compile_one, _sources()))
+        bind.result()
     if verbose:
         for _, log in results:
             sys.stderr.write(log)
