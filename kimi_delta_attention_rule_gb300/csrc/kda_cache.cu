@@ -256,35 +256,57 @@ __device__ __forceinline__ void cluster_prefix(cg::cluster_group &cl, int *mine,
     }
 }
 
+// The free pages among the four of a thread's first look at its CTA's slice.
+struct First {
+    Slice s;
+    int p, free;
+};
+__device__ __forceinline__ First first_free(const int32_t *refs, int pages, int rank) {
+    First f;
+    int live;
+    f.s = slice_of(pages, rank);
+    f.p = f.s.lo + 4 * (int)threadIdx.x;
+    f.free = 0;
+    if (f.p < f.s.hi) flags4(refs, f.p, f.s.hi, live, f.free);
+    return f;
+}
 // The free pages of rank < need, lowest first, into list; returns the number of
-// free pages. Ends with the cluster in step: list is complete for every CTA.
-__device__ __forceinline__ int list_free(cg::cluster_group &cl, Shared &sh, const int32_t *refs, int pages, int need,
+// free pages. Ends with the cluster in step: list is complete for every CTA, and no
+// CTA reads another's shared memory any more.
+__device__ __forceinline__ int list_free(cg::cluster_group &cl, Shared &sh, const int32_t *refs, const First &f, int need,
                                          int32_t *list) {
     const int rank = (int)cl.block_rank();
-    const Slice s = slice_of(pages, rank);
-    int mine = 0;
-    for (int p = s.lo + 4 * (int)threadIdx.x; p < s.hi; p += 4 * kThreads) {
-        int live, fr;
+    const Slice s = f.s;
+    int mine = __popc(f.free), live, fr;
+    for (int p = f.p + 4 * kThreads; p < s.hi; p += 4 * kThreads) {
         flags4(refs, p, s.hi, live, fr);
         mine += __popc(fr);
     }
     int total, before, all;
-    block_exclusive(mine, sh.warp_sums, total);
+    const int ahead = block_exclusive(mine, sh.warp_sums, total);
     if (threadIdx.x == 0) sh.mine = total;
     cluster_prefix(cl, &sh.mine, rank, before, all);
     if (need <= all) {
-        int at = before;
-        for (int p0 = s.lo; p0 < s.hi && at < need; p0 += 4 * kThreads) {
-            const int p = p0 + 4 * (int)threadIdx.x;
-            int live = 0, fr = 0, round;
-            if (p < s.hi) flags4(refs, p, s.hi, live, fr);
-            int j = at + block_exclusive(__popc(fr), sh.warp_sums, round);
+        auto put = [&](int p, int free, int j) {
             for (int e = 0; e < 4; ++e)
-                if (fr >> e & 1) {
+                if (free >> e & 1) {
                     if (j < need) list[j] = p + e;
                     ++j;
                 }
-            at += round;
+        };
+        if (s.hi - s.lo <= 4 * kThreads) {  // one look has been all
+            put(f.p, f.free, before + ahead);
+        } else {
+            int at = before;
+            for (int p0 = s.lo; p0 < s.hi && at < need; p0 += 4 * kThreads) {
+                const int p = p0 + 4 * (int)threadIdx.x;
+                int round;
+                fr = 0;
+                if (p < s.hi) flags4(refs, p, s.hi, live, fr);
+                const int j = at + block_exclusive(__popc(fr), sh.warp_sums, round);
+                put(p, fr, j);
+                at += round;
+            }
         }
     }
     cl.sync();
@@ -293,27 +315,35 @@ __device__ __forceinline__ int list_free(cg::cluster_group &cl, Shared &sh, cons
 
 // ---- fork -------------------------------------------------------------------------
 // Each CTA ranks all forks that need a page (their lengths end inside one) and
-// lists its slice's free pages; then a warp per fork copies the table row.
+// lists its slice's free pages; then a warp per fork copies the table row. All that does
+// not depend on the list is read ahead of it: what bounds the call is the number of
+// dependent reads and barriers (61 forks, 8,192 pages: see the call's figures below).
+constexpr int kForksAhead = kThreads;  // whose (rank, src, dst, length) stay in shared memory
+constexpr int kEntriesAhead = 4;       // table entries per lane
+
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     fork_kernel(Table table, int32_t *lens, int32_t *refs, int pages, int page, const int32_t *__restrict__ src,
                 const int32_t *__restrict__ dst, int n, int2 *copies, int32_t *list, int32_t *ranks,
                 uint32_t *status) {
     __shared__ Shared sh;
+    __shared__ int4 forks[kForksAhead];
     cg::cluster_group cl = cg::this_cluster();
     wait_before();
     let_next_start();
     const int rank = (int)cl.block_rank();
-    // ranks[i]: -2 = not a fork, -1 = no partial page, else its rank among the fresh pages
+    const First first = first_free(refs, pages, rank);
+    // a fork's rank: -2 = not a fork, -1 = no partial page, else its rank among the fresh pages
     int need = 0;
     for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + (int)threadIdx.x;
-        int state = -2;
+        int state = -2, a = -1, z = -1, len = 0;
         if (i < n) {
-            const int a = src[i], z = dst[i];
+            a = src[i];
+            z = dst[i];
             if (a >= 0 && z >= 0) {
                 bool ok = a < table.rows && z < table.rows && a != z;
                 if (ok) {
-                    const int len = lens[a];
+                    len = lens[a];
                     ok = len >= 0 && (long long)len <= (long long)table.cols * page && table.row(z)[0] < 0;
                     state = len % page != 0;
                 }
@@ -325,38 +355,62 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         }
         int round;
         const int j = need + block_exclusive(state == 1, sh.warp_sums, round);
-        if (rank == 0 && i < n) ranks[i] = state == 1 ? j : (state == 0 ? -1 : -2);
+        state = state == 1 ? j : (state == 0 ? -1 : -2);
+        if (i < kForksAhead) forks[i] = make_int4(state, a, z, len);
+        else if (rank == 0 && i < n) ranks[i] = state;
         need += round;
     }
-    const int have = list_free(cl, sh, refs, pages, need, list);
-    if (need > have && rank == 0 && threadIdx.x == 0 && status) atomicOr(status, kStatusNoSpace);
-    const int lane = threadIdx.x & 31;
-    for (int i = rank * (kThreads / 32) + (int)(threadIdx.x >> 5); i < n; i += kCtas * kThreads / 32) {
+    __syncthreads();
+    const int lane = threadIdx.x & 31, first_fork = rank * (kThreads / 32) + (int)(threadIdx.x >> 5);
+    auto fork_of = [&](int i) {
+        if (i < kForksAhead) return forks[i];
         const int state = ranks[i];
+        return make_int4(state, src[i], dst[i], state != -2 ? lens[src[i]] : 0);
+    };
+    int4 f = make_int4(-2, -1, -1, 0);
+    int ahead[kEntriesAhead], partial = -1;
+    if (first_fork < n && first_fork < kForksAhead) f = forks[first_fork];
+    if (f.x != -2) {
+#pragma unroll
+        for (int e = 0; e < kEntriesAhead; ++e) {
+            const int j = lane + 32 * e;
+            if (j < f.w / page) ahead[e] = table.row(f.y)[j];
+        }
+        if (f.x >= 0) partial = table.row(f.y)[f.w / page];
+    }
+    const int have = list_free(cl, sh, refs, first, need, list);
+    if (need > have && rank == 0 && threadIdx.x == 0 && status) atomicOr(status, kStatusNoSpace);
+    for (int i = first_fork; i < n; i += kCtas * kThreads / 32) {
+        const bool read = i == first_fork && i < kForksAhead;
+        if (!read) f = fork_of(i);
         int2 pair = make_int2(-1, -1);
-        if (state != -2 && need <= have) {
-            const int32_t *from = table.row(src[i]);
-            int32_t *to = table.row(dst[i]);
-            const int len = lens[src[i]], full = len / page;
-#pragma unroll 4
-            for (int j = lane; j < full; j += 32) {
-                const int pg = from[j];
+        if (f.x != -2 && need <= have) {
+            const int32_t *from = table.row(f.y);
+            int32_t *to = table.row(f.z);
+            const int full = f.w / page;
+            auto share = [&](int j, int pg) {
                 to[j] = pg;
                 if (pg >= 0 && pg < pages) atomicAdd(refs + pg, 1);
                 else if (status) atomicOr(status, kStatusBadSeqlens);
+            };
+            if (read) {
+#pragma unroll
+                for (int e = 0; e < kEntriesAhead; ++e)
+                    if (lane + 32 * e < full) share(lane + 32 * e, ahead[e]);
             }
-            if (state >= 0) {
-                pair = make_int2(from[full], list[state]);
+#pragma unroll 4
+            for (int j = lane + (read ? 32 * kEntriesAhead : 0); j < full; j += 32) share(j, from[j]);
+            if (f.x >= 0) {
+                pair = make_int2(read ? partial : from[full], list[f.x]);
                 if (lane == 0) {
                     to[full] = pair.y;
                     refs[pair.y] = 1;
                 }
             }
-            if (lane == 0) lens[dst[i]] = len;
+            if (lane == 0) lens[f.z] = f.w;
         }
         if (lane == 0) copies[i] = pair;
     }
-    cl.sync();  // no CTA leaves while another may read its shared memory
 }
 
 // ---- alloc ------------------------------------------------------------------------
@@ -384,6 +438,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
     wait_before();
     let_next_start();
     const int rank = (int)cl.block_rank(), lane = threadIdx.x & 31;
+    const First first = first_free(refs, pages, rank);
     const int warp = rank * (kThreads / 32) + (int)(threadIdx.x >> 5), warps = kCtas * kThreads / 32;
     for (int r = warp; r < table.rows; r += warps) {  // (pages in use, pages to add)
         const int used = row_used(table.row(r), table.cols);
@@ -401,7 +456,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         block_exclusive(r < table.rows ? rows_state[r].y : 0, sh.warp_sums, round);
         need += round;
     }
-    const int have = list_free(cl, sh, refs, pages, need, list);
+    const int have = list_free(cl, sh, refs, first, need, list);
     if (need > have) {
         if (rank == 0 && threadIdx.x == 0 && status) atomicOr(status, kStatusNoSpace);
     } else if (need > 0) {
@@ -421,7 +476,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
             }
         }
     }
-    cl.sync();
 }
 
 // ---- compact ----------------------------------------------------------------------
@@ -488,7 +542,6 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         *count = holes;
         *n_live = n;
     }
-    cl.sync();
 }
 // Table entries of the pages that moved (those from n_live on) get their new names.
 __global__ void __launch_bounds__(256)
