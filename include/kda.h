@@ -459,7 +459,8 @@ int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, i
  * Every token sees all seq_lens[b] cached ones. A length outside
  * 0..table_cols page_size is flagged (KDA_ERR_DEVICE) and its sequence skipped
  * (nothing written); a page number outside the pool is flagged and its keys read
- * as zeros. kda_cache_append adds the accepted tokens to the cache.
+ * as zeros. table_cols page_size may be 2^31 - 1024 at most. kda_cache_append adds
+ * the accepted tokens to the cache.
  * Workspace, alignment and errors as kda_attn_prefill; T > 64 or another page size
  * is KDA_ERR_UNSUPPORTED. B = 0 or T = 0 is a no-op.
  */

@@ -51,7 +51,7 @@ using kda::attn::Args;
 
 constexpr int kMaxGroup = 64;
 constexpr int kMaxTokens = kda::attn::kMaxDrafts;
-constexpr long long kMaxKeys = 0x7fffff00LL - 512;  // (positions two key tiles past a sequence's end are formed)
+constexpr long long kMaxKeys = (1LL << 31) - 1024;  // (positions two key tiles past a sequence's end are formed)
 constexpr size_t kHeader = 256;  // of a cache workspace: the status word
 
 struct Range {

@@ -10,6 +10,11 @@
 // fastest) and writes whole sectors; the loads of four parts are in flight at a time.
 // With many parts (few rows over a long cache) eight lanes share a thread's work. The
 // order of the sum is fixed, so a call gives the same bits every time.
+//
+// Bound by the parts' way through L2 and a chain of latencies (the headers, the search, a
+// part): 7 us for 152 parts of 4 rows, 12 us for the 28 MB of a step of 64 drafts by eight
+// users (cold caches). A grid with a column of blocks per CTA, most of them empty, took 12 us
+// more for 24 items of 13 parts.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -43,7 +48,9 @@ __device__ __forceinline__ void join(Acc &x, const Acc &y, float c) {
     x.o.w = join_sum(x.o.w, f.x, y.o.w, f.y);
 }
 
-// Eight lanes per (row, quad), each with every eighth part?
+// Eight lanes per (row, quad), each with every eighth part? (One long sequence 51.5 us
+// instead of 55.2, fp32 65.0 instead of 77.2; from four parts on: no better, 34.9 instead
+// of 33.0 for an fp32 tree.)
 __device__ __forceinline__ bool shared_work(int n, int rows) { return n > 8 && rows <= 32; }
 
 // Chunk `chunk` of an item of n terms, the last of which is two parts with `pair`:
