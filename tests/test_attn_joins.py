@@ -127,3 +127,34 @@ def test_append_then_read(io):
                 seen = torch.ones(1, t + 1, dtype=torch.bool, device=DEV)
                 ref = attn_ref.attend(q[t, b, :, h], k[b, :t + 1, h // 4], v[b, :t + 1, h // 4], seen, SCALE)
                 attn_ref.check(outs[t][0][b, :, h], outs[t][1][b, :, h], ref)
+
+
+@pytest.mark.parametrize("name,build", CASES, ids=[c[0] for c in CASES])
+def test_captured_behind_copies_and_other_streams(name, build):
+    """A graph whose calls follow a copy, a kernel and two streams that join."""
+    call, ws, (q, *_) = build(BF)
+    ref, ref_lse = call()
+    torch.cuda.synchronize()
+    x, y, z = q.clone(), torch.empty_like(q), torch.empty_like(q)
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    outs = []
+    with torch.cuda.graph(g):
+        y.copy_(x)  # a copy node
+        outs.append(call(q=y))
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            z.copy_(x)
+            z.mul_(1.0)
+        y.mul_(1.0)
+        here.wait_stream(side)  # two nodes before the next call
+        outs.append(call(q=z))
+        outs.append(call(q=y))
+    for _ in range(3):
+        y.zero_()
+        z.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for out, lse in outs:
+            assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
+    assert kda.kda_workspace_status(ws) == kda.KDA_OK and not ws[:256].any()
