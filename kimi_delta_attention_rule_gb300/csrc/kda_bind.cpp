@@ -6,9 +6,14 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+
+#include <algorithm>
+#include <cstring>
+#include <string>
 
 #include "kda.h"
 
@@ -68,15 +73,25 @@ bool truth(PyObject *o) {
     if (x < 0) throw python_error();
     return x != 0;
 }
-void *stream_of(PyObject *o) {
-    if (o == Py_None) return c10::cuda::getCurrentCUDAStream().stream();
-    PyObject *h = PyObject_GetAttrString(o, "cuda_stream");
-    if (h == nullptr) throw python_error();
-    void *s = PyLong_AsVoidPtr(h);
-    Py_DECREF(h);
-    if (s == nullptr && PyErr_Occurred()) throw python_error();
-    return s;
-}
+// The device of a call's tensors and its stream (None: the device's current one), while
+// the call lasts: what it allocates belongs to that stream, as the kernels do.
+struct Place {
+    c10::cuda::CUDAGuard device;
+    c10::cuda::OptionalCUDAStreamGuard other;
+    void *stream;
+    Place(PyObject *o, int dev) : device(static_cast<c10::DeviceIndex>(dev)) {
+        if (o == Py_None) {
+            stream = c10::cuda::getCurrentCUDAStream().stream();
+            return;
+        }
+        PyObject *h = PyObject_GetAttrString(o, "cuda_stream");
+        if (h == nullptr) throw python_error();
+        stream = PyLong_AsVoidPtr(h);
+        Py_DECREF(h);
+        if (stream == nullptr && PyErr_Occurred()) throw python_error();
+        other.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(dev)));
+    }
+};
 
 int cuda_index(const at::Tensor &t) {
     TORCH_CHECK_VALUE(t.is_cuda(), "KDA tensors must be CUDA tensors");
@@ -223,6 +238,7 @@ PyObject *attn_prefill(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     ARGS(12)
     const at::Tensor &q = tensor("q", x[0]), &k = tensor("k", x[1]), &v = tensor("v", x[2]);
     const int dev = cuda_index(q);
+    const Place place(x[11], dev);
     const auto dt = q.scalar_type();
     const int32_t io = io_of(dt);
     if (io < 0) return bad_dtype(dt);
@@ -251,10 +267,9 @@ PyObject *attn_prefill(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     else lse.none();
     const Space ws = workspace(x[10], q, dev, [&] { return kda_c.attn_prefill_workspace_size(N, Tq, Tk, Hq, Hkv, D, io); });
     const float scale = f32(x[3]);
-    void *const st = stream_of(x[11]);
     const int rc = call([&] {
         return kda_c.attn_prefill(rq.p, rk.p, rv.p, rq.ld, rk.ld, rv.ld, scale, cu, cuk, N, nq, nk, Hq, Hkv, D, io, out.p,
-                                  static_cast<float *>(lse.p), ws.p, ws.bytes, st);
+                                  static_cast<float *>(lse.p), ws.p, ws.bytes, place.stream);
     });
     return rc == KDA_OK ? pair(out, lse) : fail(rc, "kda_attn_prefill");
     END_HANDLE_TH_ERRORS
@@ -267,6 +282,7 @@ PyObject *attn_decode(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     ARGS(14)
     const at::Tensor &q = tensor("q", x[0]), &kp = tensor("k_pages", x[1]), &vp = tensor("v_pages", x[2]);
     const int dev = cuda_index(q);
+    const Place place(x[13], dev);
     const auto dt = q.scalar_type();
     const int32_t io = io_of(dt);
     if (io < 0) return bad_dtype(dt);
@@ -297,11 +313,10 @@ PyObject *attn_decode(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
         return kda_c.attn_decode_workspace_size(B, T, Hq, Hkv, D, page, table.cols, io);
     });
     const float scale = f32(x[5]);
-    void *const st = stream_of(x[13]);
     const int rc = call([&] {
         return kda_c.attn_decode(rq.p, rq.ld, rk.p, rv.p, rk.ld, rv.ld, k_pages, v_pages, P, page, table.p, table.ld,
                                  table.cols, lens, mask, scale, B, T, Hq, Hkv, D, io, out.p, static_cast<float *>(lse.p),
-                                 ws.p, ws.bytes, st);
+                                 ws.p, ws.bytes, place.stream);
     });
     return rc == KDA_OK ? pair(out, lse) : fail(rc, "kda_attn_decode");
     END_HANDLE_TH_ERRORS
@@ -329,14 +344,14 @@ PyObject *cache_alloc(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     HANDLE_TH_ERRORS
     ARGS(6)
     const BlockTable b = take_table(x[0]);
+    const Place place(x[5], b.dev);
     TORCH_CHECK_VALUE(tensor("want", x[1]).sizes() == at::IntArrayRef({b.rows}), "want must have an entry for each row");
     const int32_t *want = take_as<int32_t>("want", x[1], at::kInt, b.dev);
     const Refs refs = take_refs(x[2], b.dev);
     const int32_t page = i32("page_size", x[3]);
     const Space ws = cache_space(x[4], x[0], b, refs);
-    void *const st = stream_of(x[5]);
     const int rc = call([&] {
-        return kda_c.cache_alloc(b.p, b.ld, b.rows, b.cols, want, refs.p, refs.pages, page, ws.p, ws.bytes, st);
+        return kda_c.cache_alloc(b.p, b.ld, b.rows, b.cols, want, refs.p, refs.pages, page, ws.p, ws.bytes, place.stream);
     });
     if (rc != KDA_OK) return fail(rc, "kda_cache_alloc");
     Py_RETURN_NONE;
@@ -348,6 +363,7 @@ PyObject *cache_fork(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     HANDLE_TH_ERRORS
     ARGS(9)
     const BlockTable b = take_table(x[0]);
+    const Place place(x[8], b.dev);
     int32_t *const lens = take_lens(x[1], b);
     const Refs refs = take_refs(x[2], b.dev);
     const int32_t n = i32("src", tensor("src", x[3]).numel()), page = i32("page_size", x[5]);
@@ -356,10 +372,9 @@ PyObject *cache_fork(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     Out copies;
     copies.take_or_make("copies", x[6], {n, 2}, at::kInt, THPVariable_Unpack(x[0]), b.dev);
     const Space ws = cache_space(x[7], x[0], b, refs);
-    void *const st = stream_of(x[8]);
     const int rc = call([&] {
         return kda_c.cache_fork(b.p, b.ld, b.rows, b.cols, lens, refs.p, refs.pages, page, src, dst, n,
-                                static_cast<int32_t *>(copies.p), ws.p, ws.bytes, st);
+                                static_cast<int32_t *>(copies.p), ws.p, ws.bytes, place.stream);
     });
     return rc == KDA_OK ? copies.give() : fail(rc, "kda_cache_fork");
     END_HANDLE_TH_ERRORS
@@ -370,14 +385,14 @@ PyObject *cache_free(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     HANDLE_TH_ERRORS
     ARGS(6)
     const BlockTable b = take_table(x[0]);
+    const Place place(x[5], b.dev);
     int32_t *const lens = take_lens(x[1], b);
     const Refs refs = take_refs(x[2], b.dev);
     const int32_t n = i32("rows", tensor("rows", x[3]).numel());
     const int32_t *rows = take_as<int32_t>("rows", x[3], at::kInt, b.dev);
     const Space ws = cache_space(x[4], x[0], b, refs);
-    void *const st = stream_of(x[5]);
     const int rc = call([&] {
-        return kda_c.cache_free(b.p, b.ld, b.rows, b.cols, lens, refs.p, refs.pages, rows, n, ws.p, ws.bytes, st);
+        return kda_c.cache_free(b.p, b.ld, b.rows, b.cols, lens, refs.p, refs.pages, rows, n, ws.p, ws.bytes, place.stream);
     });
     if (rc != KDA_OK) return fail(rc, "kda_cache_free");
     Py_RETURN_NONE;
@@ -389,6 +404,7 @@ PyObject *cache_compact(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     HANDLE_TH_ERRORS
     ARGS(6)
     const BlockTable b = take_table(x[0]);
+    const Place place(x[5], b.dev);
     const Refs refs = take_refs(x[1], b.dev);
     Out copies, count;
     copies.take_or_make("copies", x[2], {refs.pages, 2}, at::kInt, THPVariable_Unpack(x[0]), b.dev);
@@ -400,10 +416,9 @@ PyObject *cache_compact(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
         count.take_or_make("count", x[3], {1}, at::kInt, THPVariable_Unpack(x[0]), b.dev);
     }
     const Space ws = cache_space(x[4], x[0], b, refs);
-    void *const st = stream_of(x[5]);
     const int rc = call([&] {
         return kda_c.cache_compact(b.p, b.ld, b.rows, b.cols, refs.p, refs.pages, static_cast<int32_t *>(copies.p),
-                                   static_cast<int32_t *>(count.p), ws.p, ws.bytes, st);
+                                   static_cast<int32_t *>(count.p), ws.p, ws.bytes, place.stream);
     });
     return rc == KDA_OK ? pair(copies, count) : fail(rc, "kda_cache_compact");
     END_HANDLE_TH_ERRORS
@@ -422,6 +437,7 @@ PyObject *cache_copy(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     if (n_pools == 0) Py_RETURN_NONE;
     const at::Tensor &first = tensor("pools", PySequence_Fast_GET_ITEM(items.o, 0)), &copies = tensor("copies", x[1]);
     const int dev = cuda_index(first);
+    const Place place(x[3], dev);
     TORCH_CHECK_VALUE(copies.dim() == 2 && copies.size(1) == 2, "copies must have the shape [n, 2]");
     TORCH_CHECK_VALUE(first.dim() > 0, "the pools must have entries of one size");
     const int32_t entries = i32("pools", first.size(0)), n = i32("copies", copies.size(0));
@@ -435,9 +451,8 @@ PyObject *cache_copy(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     }
     const int32_t *pairs = static_cast<int32_t *>(take("copies", copies, at::kInt, dev));
     const int32_t *count = take_as<int32_t>("count", x[2], at::kInt, dev);
-    void *const st = stream_of(x[3]);
     const int rc = call([&] {
-        return kda_c.cache_copy(ptrs.data(), n_pools, bytes / std::max(entries, 1), entries, pairs, n, count, st);
+        return kda_c.cache_copy(ptrs.data(), n_pools, bytes / std::max(entries, 1), entries, pairs, n, count, place.stream);
     });
     if (rc != KDA_OK) return fail(rc, "kda_cache_copy");
     Py_RETURN_NONE;
@@ -451,6 +466,7 @@ PyObject *cache_append(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     const at::Tensor &k = tensor("k", x[0]), &v = tensor("v", x[1]), &kp = tensor("k_pages", x[2]),
                      &vp = tensor("v_pages", x[3]);
     const int dev = cuda_index(k);
+    const Place place(x[10], dev);
     const auto dt = k.scalar_type();
     const int32_t io = io_of(dt);
     if (io < 0) return bad_dtype(dt);
@@ -479,10 +495,10 @@ PyObject *cache_append(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     const int32_t *cu = take_as<int32_t>("cu_seqlens", x[6], at::kInt, dev), *index = take_as<int32_t>("index", x[7], at::kInt, dev),
                   *count = take_as<int32_t>("count", x[8], at::kInt, dev), *start = take_as<int32_t>("start", x[5], at::kInt, dev);
     void *const k_pages = take("k_pages", kp, dt, dev), *const v_pages = take("v_pages", vp, dt, dev);
-    void *const ws = take("workspace", x[9], at::kByte, dev), *const st = stream_of(x[10]);
+    void *const ws = take("workspace", x[9], at::kByte, dev);
     const int rc = call([&] {
         return kda_c.cache_append(rk.p, rv.p, rk.ld, rv.ld, cu, N, T, index, count, start, b.p, b.ld, b.cols, P, page, Hkv,
-                                  D, io, k_pages, v_pages, ws, st);
+                                  D, io, k_pages, v_pages, ws, place.stream);
     });
     if (rc != KDA_OK) return fail(rc, "kda_cache_append");
     Py_RETURN_NONE;

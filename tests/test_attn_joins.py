@@ -158,3 +158,31 @@ def test_captured_behind_copies_and_other_streams(name, build):
         for out, lse in outs:
             assert torch.equal(out, ref) and torch.equal(lse, ref_lse)
     assert kda.kda_workspace_status(ws) == kda.KDA_OK and not ws[:256].any()
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_what_a_call_allocates_belongs_to_its_stream(dt):
+    """On another stream than the current one, without a workspace or outputs of the
+    caller's: nothing of the call waits for, or shares memory with, the current stream."""
+    q, k, v = rows(41, 1200, 8, dt), rows(42, 1200, 2, dt), rows(43, 1200, 2, dt)
+    x = make([900, 40], 2, 8, 2, 32, dt, seed=44)
+    ref = kda.kda_attn_prefill(q, k, v, SCALE, output_lse=True)
+    ref2 = kda.kda_attn_decode(x["q"], x["kp"], x["vp"], x["table"], x["lens"], SCALE, k_new=x["kn"], v_new=x["vn"],
+                               output_lse=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        torch.cuda._sleep(20_000_000)  # the current stream is busy for some ten milliseconds
+        done = torch.cuda.Event()
+        done.record()
+        junk = torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device=DEV)  # freed at once, written late
+        del junk
+        got = kda.kda_attn_prefill(q, k, v, SCALE, output_lse=True, stream=side)
+        got2 = kda.kda_attn_decode(x["q"], x["kp"], x["vp"], x["table"], x["lens"], SCALE, k_new=x["kn"], v_new=x["vn"],
+                                   output_lse=True, stream=side)
+        side.synchronize()
+        assert not done.query()  # the side stream did not wait
+        with torch.cuda.stream(side):
+            for a, b in zip(got + got2, ref + ref2):
+                assert torch.equal(a, b)
+        torch.cuda.synchronize()
