@@ -117,6 +117,10 @@ struct Args {
     int cut;                 // tiles that a part of an item has at least
     int direct;              // one CTA for each slot of an item, nothing is split
     float unit, inv_unit;    // keys per unit of weight, and its inverse
+    int block;               // tokens of an item: tile_tokens * streams
+    uint32_t block_mul;      // x / block = x block_mul >> block_shift, for x < 2^31
+    int block_shift;
+    float inv_block, inv_min_part;
     float scale;
     // device pointers
     const int32_t *cu_q, *cu_k;      // prefill offsets (NULL: equal lengths)
@@ -136,6 +140,37 @@ inline void set_unit(Args &a, double keys) {
     a.unit = 1.f;
     while (keys / a.unit > 5e8) a.unit *= 2.f;
     a.inv_unit = 1.f / a.unit;
+}
+
+// What divides by tile_tokens * streams. The search for a CTA's work is a chain of
+// dependent operations ahead of everything else, so none of it is a division of a
+// hundred cycles. With s = floor(log2 block) and m = ceil(2^(32 + s) / block), the quotient of x is
+// exact if x (m block - 2^(32 + s)) < 2^(32 + s): the bracket is below block < 2^(s + 1), x below 2^31.
+inline void set_block(Args &a) {
+    a.block = a.tile_tokens * a.streams;
+    int s = 0;
+    while ((2 << s) <= a.block) ++s;
+    const bool power = (1 << s) == a.block;  // then block_mul would have 33 bits
+    a.block_shift = power ? 31 + s : 32 + s;
+    a.block_mul = (uint32_t)((((uint64_t)1 << a.block_shift) + a.block - 1) / a.block);
+    a.inv_block = 1.f / (float)a.block;
+    a.inv_min_part = 1.f / (float)a.min_part;
+}
+__device__ __forceinline__ int div_block(const Args &a, int x) {  // x >= 0
+    return (int)(((uint64_t)(uint32_t)x * a.block_mul) >> a.block_shift);
+}
+// x / d for x < 2^30 and a quotient below 2^20: the estimate is off by one at most.
+__device__ __forceinline__ uint32_t quick_div(uint32_t x, uint32_t d, uint32_t &rest) {
+    uint32_t q = (uint32_t)__fdividef((float)x, (float)d);
+    rest = x - q * d;
+    if ((int)rest < 0) {
+        --q;
+        rest += d;
+    } else if (rest >= d) {
+        ++q;
+        rest -= d;
+    }
+    return q;
 }
 
 __device__ __forceinline__ uint32_t *status_word(const Args &a) {
@@ -163,7 +198,6 @@ struct Seq {
 };
 template <bool PAGED>
 __device__ __forceinline__ bool load_seq(const Args &a, int n, Seq &s) {
-    const int block = a.tile_tokens * a.streams;
     bool ok = true;
     if (PAGED) {
         s.q0 = n * a.T;
@@ -193,14 +227,14 @@ __device__ __forceinline__ bool load_seq(const Args &a, int n, Seq &s) {
         s.Lk = k1 - s.k0;
     }
     if (!ok) s.Lq = 0;
-    s.ni = (s.Lq + block - 1) / block;
+    s.ni = div_block(a, s.Lq) + (s.Lq - div_block(a, s.Lq) * a.block > 0);
     return ok;
 }
 // Keys that the last row of item i sees (prefill), or all keys (decode).
 template <bool PAGED>
 __device__ __forceinline__ int item_keys(const Args &a, const Seq &s, int i) {
     if (PAGED) return s.Lk;
-    const int left = (int)((unsigned)s.Lq - (unsigned)(i + 1) * (unsigned)(a.tile_tokens * a.streams));  // tokens after the item
+    const int left = (int)((unsigned)s.Lq - (unsigned)(i + 1) * (unsigned)a.block);  // tokens after the item
     const int v = left > 0 ? s.Lk - left : s.Lk;
     return v > 0 ? v : 0;
 }
@@ -227,8 +261,8 @@ __device__ __forceinline__ uint32_t items_weight(const Args &a, const Seq &s, in
         w = (float)i * (float)(item_extra<PAGED, KT>(a, nt) + nt * KT);
     } else {
         const int d = s.Lk - s.Lq, full = i < s.ni ? i : s.ni - 1;  // items without the sequence's last token
-        const float block = (float)(a.tile_tokens * a.streams);
-        const float unseen = fmaxf(0.f, floorf((float)-d / block));  // items that see nothing
+        const float block = (float)a.block;
+        const float unseen = fmaxf(0.f, floorf((float)-d * a.inv_block));  // items that see nothing
         const float count = fmaxf(0.f, (float)full - unseen);
         // the last rows of items `unseen` .. full - 1 see d + block (unseen + 1) .. keys
         w = (float)i * (float)a.extra + count * fmaf(0.5f * block, (float)full + unseen + 1.f, (float)d);
@@ -253,8 +287,7 @@ __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n
     const uint32_t per_head = items_weight<PAGED, KT>(a, s, s.ni);
     Point p;
     p.n = n;
-    p.h = (int)(x / per_head);
-    x -= (uint32_t)p.h * per_head;
+    p.h = (int)quick_div(x, per_head, x);
     int lo = 0, count = s.ni;  // the last item that starts at or before x is in [lo, lo + count)
     while (count > 1) {
         const int step = (count + 31) >> 5, at = lo + lane * step;
@@ -315,12 +348,13 @@ __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq
     const float units = (float)total;
     // at least min_part keys and two units each: the cuts inside an item are at
     // different tiles, and every CTA from an item's first to its last has a part of it
-    const int ctas = max(1, (int)fminf((float)a.ctas, fminf(units * a.unit / (float)a.min_part, 0.5f * units)));
+    const int ctas = max(1, (int)fminf((float)a.ctas, fminf(units * a.unit * a.inv_min_part, 0.5f * units)));
     if (c > ctas) return false;
     p0.n = a.N;
     p0.h = p0.i = p0.tile = 0;
     if (c == ctas) return true;
-    uint32_t x = (uint32_t)(units * ((float)c / (float)ctas));
+    // (a product with one factor for all: rising with c)
+    uint32_t x = (uint32_t)(units * ((float)c * __fdividef(1.f, (float)ctas)));
 #pragma unroll 1
     for (int n0 = 0; n0 < a.N; n0 += 32 * kFlight) {
         if (a.N > 32 * kFlight) weigh(n0);  // (else the loop above left them in place)
@@ -360,11 +394,10 @@ struct Part {
 };
 template <bool PAGED, int KT>
 __device__ __forceinline__ void item_part(const Args &a, const Seq &s, Part &p) {
-    const int block = a.tile_tokens * a.streams;
     p.nt = item_tiles<PAGED, KT>(a, s, p.i);
-    p.first_tok = p.i * block;
+    p.first_tok = p.i * a.block;
     p.q0 = s.q0 + p.first_tok;
-    p.tokens = min(block, s.Lq - p.first_tok);
+    p.tokens = min(a.block, s.Lq - p.first_tok);
     p.Lq = s.Lq;
     p.Lk = s.Lk;
     p.k0 = s.k0;
@@ -375,26 +408,27 @@ __device__ __forceinline__ void item_part(const Args &a, const Seq &s, Part &p) 
 // as it has items. A converged warp. False: an empty slot or malformed offsets.
 template <bool PAGED, int KT>
 __device__ __forceinline__ bool direct_part(const Args &a, int x, Part &p) {
-    const int lane = threadIdx.x & 31, block = a.tile_tokens * a.streams;
+    const int lane = threadIdx.x & 31;
     Seq s;
     bool good = true;
     if (PAGED) {
-        const int ni = (a.T + block - 1) / block;
-        p.i = x % ni;
-        p.h = x / ni % a.Hkv;
-        p.n = x / ni / a.Hkv;
+        uint32_t i, h;
+        const uint32_t nh = quick_div((uint32_t)x, (uint32_t)(div_block(a, a.T - 1) + 1), i);
+        p.n = (int)quick_div(nh, (uint32_t)a.Hkv, h);
+        p.i = (int)i;
+        p.h = (int)h;
         good = load_seq<PAGED>(a, p.n, s);
     } else {
-        const int slots = a.Tq_total / block + a.N;
-        p.h = x / slots;
-        const int slot = x - p.h * slots;
+        uint32_t in_head;
+        p.h = (int)quick_div((uint32_t)x, (uint32_t)(div_block(a, a.Tq_total) + a.N), in_head);
+        const int slot = (int)in_head;
         p.n = -1;
         for (int n0 = 0; n0 < a.N; n0 += 32) {
             Seq t;
             bool here = false;
             if (n0 + lane < a.N) {
                 good = load_seq<PAGED>(a, n0 + lane, t) && good;
-                here = t.q0 / block + n0 + lane <= slot;
+                here = div_block(a, t.q0) + n0 + lane <= slot;
             }
             const unsigned who = __ballot_sync(0xffffffffu, here);
             if (who == 0) continue;
@@ -407,7 +441,7 @@ __device__ __forceinline__ bool direct_part(const Args &a, int x, Part &p) {
             s.ni = __shfl_sync(0xffffffffu, t.ni, src);
         }
         good = __all_sync(0xffffffffu, good);
-        p.i = slot - (s.q0 / block + p.n);
+        p.i = slot - (div_block(a, s.q0) + p.n);
     }
     if (!good) {
         if (lane == 0) atomicOr(status_word(a), kStatusBadSeqlens);

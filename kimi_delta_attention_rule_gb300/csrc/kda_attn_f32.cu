@@ -77,13 +77,14 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
     if (!a.direct) walk.init(pts[0], pts[1], seq0);
     const int ty = tid >> 4, tx = tid & 15, lane = tid & 31, warp = tid >> 5;  // rows RPT ty + i; keys tx + 16 e, channels 4 tx + 64 e
     const float c = a.scale * kLog2e;
+    const uint32_t inv_g = (65536u + a.G - 1) / a.G;  // r / G = r inv_g >> 16 for r < 1024
     const int G = a.G, page_bits = PAGED ? 31 - __clz(a.page) : 0;
     Part p = direct;
     for (bool more = a.direct || walk.next(a, p); more; more = !a.direct && walk.next(a, p)) {
         const int rows = p.tokens * G;
         __syncthreads();  // the last part's reads are done
         for (int x = tid; x < kRows * 32; x += kF32Threads) {
-            const int r = x >> 5, ch = (x & 31) * 4, tok = r / G;
+            const int r = x >> 5, ch = (x & 31) * 4, tok = (int)(r * inv_g >> 16);
             const bool ok = r < rows;
             const float *src = io.q + (ok ? (long long)(p.q0 + tok) * io.ldq + (p.h * G + r - tok * G) * kD + ch : 0);
             cp16(smem_u32(Qs + r * kD + (ch ^ (r / RPT % 8 * 4))), src, ok);
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             m[i] = -INFINITY;
             l[i] = 0.f;
             o[i][0] = o[i][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-            const int r = RPT * ty + i, t = p.first_tok + r / G;
+            const int r = RPT * ty + i, t = p.first_tok + (int)(r * inv_g >> 16);
             seen[i] = PAGED ? p.Lk : p.Lk - p.Lq + t + 1;
             bits[i] = 0;
             if (PAGED && r < rows) {
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                 continue;
             }
             const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
-            const int tok = r / G;
+            const int tok = (int)(r * inv_g >> 16);
             const size_t dst = (size_t)(p.q0 + tok) * a.Hq + p.h * G + r - tok * G;
 #pragma unroll
             for (int e = 0; e < 2; ++e)
@@ -293,6 +294,7 @@ static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
     a.extra = 64;  // (more of it, and cuts at two or three tiles: slower)
     a.extra_short = 0;
     a.min_part = kF32MinPart;
+    set_block(a);
     a.cut = 1;
     const long long slots = PAGED ? (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens)
                                   : ((long long)a.Tq_total / a.tile_tokens + a.N) * a.Hkv;

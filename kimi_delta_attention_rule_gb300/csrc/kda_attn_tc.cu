@@ -1040,6 +1040,7 @@ cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, c
     a.extra = 192;
     a.extra_short = PAGED ? 512 : 0;
     a.min_part = kMinPart;
+    set_block(a);
     // every item's keys, its start and end and, at the most, its drafts' tile
     set_unit(a, (double)slots * ((double)keys + 512 + kTile));
     a.cut = 2;
