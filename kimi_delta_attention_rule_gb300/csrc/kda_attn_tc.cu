@@ -673,17 +673,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (nd == kDescs) tell();
                 if (lane == 0) {
                     Desc *d = const_cast<Desc *>(descs) + nd % kDescs;
-                    if (more && !p.whole()) {
-                        PartHeader *h = part_header(a, part_slot(cta, p));
-                        h->ends = p.tb == p.nt ? kEnds : 0;
-                        h->token0 = p.q0;
-                        h->tokens = p.tokens;
-                        h->kvh = p.h;
-                        h->valid = 1;
+                    // The others wait for the descriptor: the header of a part comes after it,
+                    // but ahead of it where the softmax warps may change it at the part's end.
+                    const bool open = more && p.tb < p.nt;
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {
+                        if ((k == 0) != open) {
+                            if (more) describe<PAGED, DUAL>(a, p, cta, run, *d);
+                            else d->last = 1;
+                            mbar_arrive(bars.dfull(nd % kDescs));
+                        } else if (more && !p.whole()) {
+                            PartHeader *h = part_header(a, part_slot(cta, p));
+                            h->ends = open ? 0 : kEnds;
+                            h->token0 = p.q0;
+                            h->tokens = p.tokens;
+                            h->kvh = p.h;
+                            h->valid = 1;
+                        }
                     }
-                    if (more) describe<PAGED, DUAL>(a, p, cta, run, *d);
-                    else d->last = 1;
-                    mbar_arrive(bars.dfull(nd % kDescs));
                 }
                 ++nd;
                 if (!more) break;
