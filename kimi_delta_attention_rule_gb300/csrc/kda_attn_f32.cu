@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
     __shared__ Seq seq0;
     __shared__ int any;
     wait_before();
-    let_next_start();
+    if (a.direct) let_next_start();
     const int tid = threadIdx.x, cta = blockIdx.x;
     __shared__ Part direct;
     if (tid < 64) {  // one warp finds where this CTA's work starts, one where it ends

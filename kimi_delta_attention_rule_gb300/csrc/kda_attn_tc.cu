@@ -325,7 +325,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     wait_before();
-    let_next_start();
+    // (Blocks of the join kernel that wait on SMs whose work is done first cost the others 1 us of
+    // 51 for one long sequence; a direct call has none, and the next call may start.)
+    if (a.direct) let_next_start();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
