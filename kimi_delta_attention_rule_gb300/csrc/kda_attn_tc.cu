@@ -26,9 +26,9 @@
 // Measured (GB300; copy 6,782 GB/s, cuBLAS bf16 1,917 TFLOP/s): causal attention of 8,192
 // tokens, 32 heads on 8: 318 us, 1,729 TFLOP/s, the tensor pipe busy 73 % of the time and the
 // exponentials' 36 %; a step of two row tiles takes some 2,700 cycles, 2,048 of them products.
-// One token each of 128 sequences, 400,003 cached tokens: 255 us, 6.4 TB/s (loads). Of a
-// short call, 12,000 cycles pass before the first softmax: the search for the CTA's work,
-// the page's number, the first tile, each from a cold cache. Tried without gain: 16
+// One token each of 128 sequences, 400,003 cached tokens: 254 us, 6.5 TB/s (loads). Some
+// 11,000 cycles pass before the first softmax (5,500 of a direct call): the search for the
+// CTA's work, the page's number, the first tile, each from a cold cache. Tried without gain: 16
 // softmax warps of two threads a row (spills), halves of 64 keys with a maximum ahead of
 // the second (340 us instead of 328), a third of the exponentials as polynomials (344 to 357
 // instead of 335), more Q tiles and fewer K tiles in the ring (458 instead of 425 for a long prefix), one fused step of both
