@@ -279,12 +279,11 @@ __device__ __forceinline__ bool same_item(const Point &x, const Point &y) {
     return x.n == y.n && x.h == y.h && x.i == y.i;
 }
 
-// The point at distance x into sequence n (x below its weight); a converged warp with
-// the same arguments in all lanes.
+// The point at distance x into sequence n (of this weight per head, x below all heads');
+// a converged warp with the same arguments in all lanes.
 template <bool PAGED, int KT>
-__device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n, uint32_t x) {
+__device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n, uint32_t per_head, uint32_t x) {
     const int lane = threadIdx.x & 31;
-    const uint32_t per_head = items_weight<PAGED, KT>(a, s, s.ni);
     Point p;
     p.n = n;
     p.h = (int)quick_div(x, per_head, x);
@@ -316,7 +315,7 @@ template <bool PAGED, int KT>
 __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq &s0) {
     const int lane = threadIdx.x & 31;
     constexpr int kFlight = PAGED ? 4 : 1;  // groups of 32 sequences whose loads are in flight together
-    uint32_t w[kFlight], total = 0;
+    uint32_t w[kFlight], total = 0, per_head = 1;  // w: a head's
     auto weigh = [&](int n0) {
         bool ok = true;
 #pragma unroll
@@ -326,7 +325,7 @@ __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq
             w[u] = 0;
             if (n < a.N) {
                 ok = load_seq<PAGED>(a, n, s) && ok;
-                if (s.ni > 0) w[u] = items_weight<PAGED, KT>(a, s, s.ni) * (uint32_t)a.Hkv;
+                if (s.ni > 0) w[u] = items_weight<PAGED, KT>(a, s, s.ni);
             }
         }
         return ok;
@@ -338,7 +337,7 @@ __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) total += w[u];
     }
-    total = __reduce_add_sync(0xffffffffu, total);
+    total = __reduce_add_sync(0xffffffffu, total) * (uint32_t)a.Hkv;
     if (!__all_sync(0xffffffffu, good)) {
         if (lane == 0) atomicOr(status_word(a), kStatusBadSeqlens);
         if (!PAGED) return false;
@@ -360,26 +359,28 @@ __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq
         if (a.N > 32 * kFlight) weigh(n0);  // (else the loop above left them in place)
 #pragma unroll
         for (int u = 0; u < kFlight; ++u) {
-            const uint32_t sum = __reduce_add_sync(0xffffffffu, w[u]);
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, w[u]) * (uint32_t)a.Hkv;
             if (x >= sum) {
                 x -= sum;
                 continue;
             }
-            uint32_t incl = w[u];
+            const uint32_t mine = w[u] * (uint32_t)a.Hkv;
+            uint32_t incl = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
             const int src = __ffs(__ballot_sync(0xffffffffu, x < incl)) - 1;
-            x -= __shfl_sync(0xffffffffu, incl - w[u], src);
+            x -= __shfl_sync(0xffffffffu, incl - mine, src);
+            per_head = __shfl_sync(0xffffffffu, w[u], src);
             p0.n = n0 + 32 * u + src;
             n0 = a.N;  // found
             break;
         }
     }
     load_seq<PAGED>(a, p0.n, s0);
-    p0 = point_in_seq<PAGED, KT>(a, s0, p0.n, x);
+    p0 = point_in_seq<PAGED, KT>(a, s0, p0.n, per_head, x);
     return true;
 }
 
@@ -454,7 +455,7 @@ __device__ __forceinline__ bool direct_part(const Args &a, int x, Part &p) {
     return true;
 }
 
-// Walks the parts of [at, end). Every role of a CTA walks them alike.
+// Walks the parts of [at, end).
 template <bool PAGED, int KT>
 struct Walk {
     Point at, end;
