@@ -99,6 +99,7 @@ long long prefill_keys(int32_t N, long long Tq, long long Tk, int32_t Hq, int32_
     return items > cap ? cap * 1024 : items * (Tk < cap ? Tk + 512 : cap);
 }
 long long decode_keys(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t page, int32_t cols, int32_t io) {
+    if (T == 0) return 0;
     const long long g = Hq / Hkv, block = io == KDA_F32 ? 64 / g : (T * g <= 128 ? T : 2 * (128 / g));
     const long long items = (long long)B * Hkv * ((T + block - 1) / block), cap = 1LL << 20;
     const long long keys = (long long)page * cols + 512;
