@@ -132,7 +132,9 @@ Rows take_rows(const char *name, const at::Tensor &t, at::ScalarType dtype, int 
                       ": the [heads, D] rows must be contiguous");
     Rows r;
     r.p = t.data_ptr();
-    if (n == 3) {
+    if (t.numel() == 0) {  // no token: the strides say nothing
+        r.ld = H * D;
+    } else if (n == 3) {
         r.ld = size[0] > 1 ? st[0] : H * D;
     } else if (size[1] == 1) {
         r.ld = size[0] > 1 ? st[0] : H * D;

@@ -31,3 +31,24 @@ def test_workspace_of_a_batch_without_tokens():
     q = torch.empty(3, 0, 8, 128, dtype=torch.bfloat16)
     pages, table = torch.empty(4, 2, 16, 128, dtype=torch.bfloat16), torch.zeros(3, 5, dtype=torch.int32)
     assert kda.attn_decode_workspace(q, pages, table).numel() >= 256
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("B", [0, 1, 3])
+def test_calls_are_no_ops(B, dt):
+    """Empty q, k_new, v_new (and slices of a wider projection), with and without a workspace."""
+    dev = "cuda:0"
+    pages = torch.zeros(4, 2, 16, 128, dtype=dt, device=dev)
+    table, lens = torch.zeros(B, 5, dtype=torch.int32, device=dev), torch.ones(B, dtype=torch.int32, device=dev)
+    fused = torch.empty(B, 2, 12, 128, dtype=dt, device=dev)[:, :0]
+    for q, k, v in ((torch.empty(B, 0, 8, 128, dtype=dt, device=dev),) + (torch.empty(B, 0, 2, 128, dtype=dt, device=dev),) * 2,
+                    (fused[:, :, :8], fused[:, :, 8:10], fused[:, :, 10:])):
+        for ws in (None, kda.attn_decode_workspace(q, pages, table)):
+            for new in (dict(k_new=k, v_new=v), {}):
+                out, lse = kda.kda_attn_decode(q, pages, pages, table, lens, 0.1, output_lse=True, workspace=ws, **new)
+                assert out.shape == (B, 0, 8, 128) and lse.shape == (B, 0, 8)
+        kda.kda_cache_append(k, v, pages, pages, table, lens)
+        kda.kda_cache_append(k, v, pages, pages, table, lens, index=table[:, :0].contiguous(), count=torch.zeros_like(lens))
+    torch.cuda.synchronize()
+    assert not pages.any()
