@@ -230,7 +230,7 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
     a.out = out;
     a.lse = lse;
     a.ws = static_cast<unsigned char *>(workspace);
-    if (num_pages == 0) k_pages = v_pages = q;  // never read, but a tensor map needs an address
+    if (num_pages == 0) k_pages = v_pages = q;  // a tensor map needs an address; its only row is never read
     Range range("kda_attn_decode");
     return done((io == KDA_BF16 ? kda::attn::launch_attn_decode_tc(a, q, k_pages, v_pages, k_new, v_new, ldq, ldk, ldv, static_cast<cudaStream_t>(stream))
                                 : kda::attn::launch_attn_decode_f32(a, q, k_pages, v_pages, k_new, v_new, ldq, ldk, ldv, static_cast<cudaStream_t>(stream))));

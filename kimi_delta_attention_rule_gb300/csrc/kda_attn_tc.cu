@@ -748,7 +748,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     const int copies = (valid + rows - 1) >> row_bits;
                     expect_tx(lead, bar, (uint32_t)(copies << row_bits) * 256u);
-                    int row = a.pages * a.Hkv * a.page;  // past the pool's last row: zeros
+                    int row = max(a.pages * a.Hkv * a.page, 1);  // past the map's last row (an empty pool's has one): zeros
                     if (x.pg >= 0 && x.pg < a.pages)
                         row = (x.pg * a.Hkv + x.h) * a.page + ((x.t * kTile + (lane << row_bits)) & (a.page - 1));
                     else if (lane < copies)
