@@ -492,8 +492,9 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
  *   skipped) becomes a copy of row src[i]: full pages are shared (refs + 1); where
  *   the length ends inside a page, dst gets a fresh page, and copies[i] = (shared
  *   page, fresh page) has to be copied in every pool (kda_cache_copy); copies[i] =
- *   (-1, -1) otherwise. src or dst < 0 skips the pair. No dst may be another
- *   pair's src or dst.
+ *   (-1, -1) otherwise. A src whose length ends inside a page that is not in the
+ *   pool is flagged and its pair skipped: dst stays empty and takes no page. src or
+ *   dst < 0 skips the pair. No dst may be another pair's src or dst.
  * kda_cache_free: drops the pages of rows[i], i < n (distinct; < 0 is skipped): refs - 1,
  *   entries -1, length 0.
  * kda_cache_compact: with L live pages, the j-th live page numbered >= L moves to

@@ -322,7 +322,7 @@ __device__ __forceinline__ int list_free(cg::cluster_group &cl, Shared &sh, cons
 // not depend on the list is read ahead of it: what bounds the call is the number of
 // dependent reads and barriers (free, fork and copy of 61 forks, 8,192 pages: 15.8 us, of
 // 5 forks, 1,024 pages: 9.3; 17.3 and 11.1 when the rows were read after it).
-constexpr int kForksAhead = kThreads;  // whose (rank, src, dst, length) stay in shared memory
+constexpr int kForksAhead = kThreads;  // whose (rank, src, dst, length) and last page stay in shared memory
 constexpr int kEntriesAhead = 4;       // table entries per lane
 
 __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
@@ -331,25 +331,32 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
                 uint32_t *status) {
     __shared__ Shared sh;
     __shared__ int4 forks[kForksAhead];
+    __shared__ int tails[kForksAhead];  // the partly filled last page of the source
     cg::cluster_group cl = cg::this_cluster();
     wait_before();
     let_next_start();
     const int rank = (int)cl.block_rank();
     const First first = first_free(refs, pages, rank);
-    // a fork's rank: -2 = not a fork, -1 = no partial page, else its rank among the fresh pages
+    // a fork's rank: -2 = not a fork (or a malformed one: it takes no page), -1 = no partial
+    // page, else its rank among the fresh pages
     int need = 0;
     for (int i0 = 0; i0 < n; i0 += kThreads) {
         const int i = i0 + (int)threadIdx.x;
-        int state = -2, a = -1, z = -1, len = 0;
+        int state = -2, a = -1, z = -1, len = 0, tail = -1;
         if (i < n) {
             a = src[i];
             z = dst[i];
             if (a >= 0 && z >= 0) {
                 bool ok = a < table.rows && z < table.rows && a != z;
                 if (ok) {
+                    const int taken = table.row(z)[0];
                     len = lens[a];
-                    ok = len >= 0 && (long long)len <= (long long)table.cols * page && table.row(z)[0] < 0;
+                    ok = len >= 0 && (long long)len <= (long long)table.cols * page && taken < 0;
                     state = len % page != 0;
+                }
+                if (ok && state == 1) {  // a page to copy from
+                    tail = table.row(a)[len / page];
+                    ok = tail >= 0 && tail < pages;
                 }
                 if (!ok) {
                     state = -2;
@@ -360,8 +367,12 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
         int round;
         const int j = need + block_exclusive(state == 1, sh.warp_sums, round);
         state = state == 1 ? j : (state == 0 ? -1 : -2);
-        if (i < kForksAhead) forks[i] = make_int4(state, a, z, len);
-        else if (rank == 0 && i < n) ranks[i] = state;
+        if (i < kForksAhead) {
+            forks[i] = make_int4(state, a, z, len);
+            tails[i] = tail;
+        } else if (rank == 0 && i < n) {
+            ranks[i] = state;
+        }
         need += round;
     }
     __syncthreads();
@@ -380,7 +391,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
             const int j = lane + 32 * e;
             if (j < f.w / page) ahead[e] = table.row(f.y)[j];
         }
-        if (f.x >= 0) partial = table.row(f.y)[f.w / page];
+        partial = tails[first_fork];
     }
     const int have = list_free(cl, sh, refs, first, need, list);
     if (need > have && rank == 0 && threadIdx.x == 0 && status) atomicOr(status, kStatusNoSpace);
