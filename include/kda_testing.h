@@ -51,6 +51,35 @@ int kda_testing_prefill_plan(int32_t N, int32_t T, int32_t H, int32_t varlen, in
                              int32_t cooperative, int32_t schedule_override, int32_t kind,
                              size_t workspace_bytes, kda_prefill_plan_info *plan);
 
+/*
+ * kda_attn_prefill and kda_attn_decode (bf16 I/O only, arguments as there) in which, in
+ * every CTA, one warp gives up at one of its waits, as if its limit of 20
+ * milliseconds (two seconds in production) had run out: warp 0..7 of the softmax,
+ * 8 products, 9 copies, 10 scheduler, 11 zeros past a sequence's end; `at` counts that
+ * warp's waits from 0. What the others wait for then never comes, so every role gives up
+ * within its limits, the call records KDA_ERR_TIMEOUT in the workspace's status word
+ * and returns; the outputs are garbage. (A warp that has fewer waits than that never gives
+ * up: the call is then an ordinary one.) It shows that a role that stops ends in an
+ * error status and a usable context, never in a hang. KDA_ERR_INVALID_ARG for another io,
+ * warp or at.
+ */
+int kda_testing_attn_prefill_timeout(const void *q, const void *k, const void *v, int64_t ldq,
+                                     int64_t ldk, int64_t ldv, float scale,
+                                     const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k,
+                                     int32_t N, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv,
+                                     int32_t D, int32_t io, void *out, float *lse, void *workspace,
+                                     size_t workspace_bytes, int32_t warp, int32_t at,
+                                     void *stream);
+int kda_testing_attn_decode_timeout(const void *q, int64_t ldq, const void *k_new,
+                                    const void *v_new, int64_t ldk, int64_t ldv,
+                                    const void *k_pages, const void *v_pages, int32_t num_pages,
+                                    int32_t page_size, const int32_t *block_table,
+                                    int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
+                                    const uint64_t *tree_mask, float scale, int32_t B, int32_t T,
+                                    int32_t Hq, int32_t Hkv, int32_t D, int32_t io, void *out,
+                                    float *lse, void *workspace, size_t workspace_bytes,
+                                    int32_t warp, int32_t at, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -141,7 +141,13 @@ def load() -> ctypes.CDLL:
         lib.kda_cache_append.argtypes = [P, P, I64, I64, P, I32, I32, P, P, P, P, I64, I32, I32,
                                          I32, I32, I32, I32, P, P, P, P]
         lib.kda_cache_append.restype = ctypes.c_int
-        # test-only entry point (include/kda_testing.h)
+        # test-only entry points (include/kda_testing.h)
+        lib.kda_testing_attn_prefill_timeout.argtypes = (lib.kda_attn_prefill.argtypes[:-1] +
+                                                         [I32, I32, P])
+        lib.kda_testing_attn_prefill_timeout.restype = ctypes.c_int
+        lib.kda_testing_attn_decode_timeout.argtypes = (lib.kda_attn_decode.argtypes[:-1] +
+                                                        [I32, I32, P])
+        lib.kda_testing_attn_decode_timeout.restype = ctypes.c_int
         lib.kda_testing_prefill_chain_timeout.argtypes = [P, P, P, P, P, F32, P, P, I32, I32, I32,
                                                           I32, I32, I32, P, P, P, SZ, I32, P]
         lib.kda_testing_prefill_chain_timeout.restype = ctypes.c_int

@@ -131,6 +131,7 @@ struct Args {
     unsigned char *ws;
     int ctas, sms;           // CTAs that share the work; SMs of the device
     int part_rows;           // rows of a part in the workspace: those of an item at the most
+    int lose, lose_at;       // tests: 1 + the warp that gives up, and at which of its waits (0: none does)
 };
 
 // The unit of weight: `keys` is an upper bound of a call's work in keys, of at most

@@ -11,6 +11,7 @@
 
 #include "kda.h"
 #include "kda_attn.cuh"
+#include "kda_testing.h"
 
 namespace kda {
 namespace attn {
@@ -113,22 +114,16 @@ bool ld_ok(int64_t ld, int32_t heads, int32_t io) {
     return ld >= (int64_t)heads * kda::kD && ld % (io == KDA_BF16 ? 8 : 4) == 0 && ld < (1LL << 36);
 }
 bool scale_ok(float s) { return isfinite(s) && s > 0.f; }
+// A warp of the bf16 kernel that gives up at one of its waits (tests).
+struct Lose {
+    int32_t warp = -1, at = 0;
+    bool ok(int32_t io) const { return io == KDA_BF16 && warp >= 0 && warp < 12 && at >= 0; }
+};
 
-}  // namespace
-
-extern "C" {
-
-size_t kda_attn_prefill_workspace_size(int32_t N, int32_t Tq_total, int32_t Tk_total, int32_t Hq, int32_t Hkv,
-                                       int32_t D, int32_t io) {
-    if (N < 0 || Tq_total < 0 || Tk_total < 0 || check_heads(Hq, Hkv, D, io) != KDA_OK) return 0;
-    return kda::attn::workspace_bytes(attn_ctas(io, prefill_keys(N, Tq_total, Tk_total, Hq, Hkv, io)),
-                                     part_rows(io, 256));
-}
-
-int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
-                     const int32_t *cu_q, const int32_t *cu_k, int32_t N, int32_t Tq, int32_t Tk, int32_t Hq,
-                     int32_t Hkv, int32_t D, int32_t io, void *out, float *lse, void *workspace,
-                     size_t workspace_bytes, void *stream) {
+int prefill_impl(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
+                 const int32_t *cu_q, const int32_t *cu_k, int32_t N, int32_t Tq, int32_t Tk, int32_t Hq,
+                 int32_t Hkv, int32_t D, int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                 const Lose &lose, void *stream) {
     const int rc = check_heads(Hq, Hkv, D, io);
     if (rc != KDA_OK) return rc;
     if (N < 0 || Tq < 0 || Tk < 0 || !scale_ok(scale)) return KDA_ERR_INVALID_ARG;
@@ -168,25 +163,20 @@ int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, i
     a.out = out;
     a.lse = lse;
     a.ws = static_cast<unsigned char *>(workspace);
+    a.lose = lose.warp + 1;
+    a.lose_at = lose.at;
     if (tk == 0) k = v = q;  // never read, but a tensor map needs an address
     Range range("kda_attn_prefill");
     return done((io == KDA_BF16 ? kda::attn::launch_attn_prefill_tc(a, q, k, v, ldq, ldk, ldv, static_cast<cudaStream_t>(stream))
                                 : kda::attn::launch_attn_prefill_f32(a, q, k, v, ldq, ldk, ldv, static_cast<cudaStream_t>(stream))));
 }
 
-size_t kda_attn_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
-                                      int32_t table_cols, int32_t io) {
-    if (B < 0 || T < 0 || T > kMaxTokens || table_cols < 0 || !page_ok(page_size) || check_heads(Hq, Hkv, D, io) != KDA_OK)
-        return 0;
-    return kda::attn::workspace_bytes(attn_ctas(io, decode_keys(B, T, Hq, Hkv, page_size, table_cols, io)),
-                                     part_rows(io, T * (Hq / Hkv)));
-}
-
-int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk, int64_t ldv,
-                    const void *k_pages, const void *v_pages, int32_t num_pages, int32_t page_size,
-                    const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
-                    const uint64_t *tree_mask, float scale, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
-                    int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+int decode_impl(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk, int64_t ldv,
+                const void *k_pages, const void *v_pages, int32_t num_pages, int32_t page_size,
+                const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
+                const uint64_t *tree_mask, float scale, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes, const Lose &lose,
+                void *stream) {
     const int rc = check_heads(Hq, Hkv, D, io);
     if (rc != KDA_OK) return rc;
     if (B < 0 || T < 0 || num_pages < 0 || table_cols < 0 || table_ld < table_cols || !scale_ok(scale))
@@ -230,10 +220,72 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
     a.out = out;
     a.lse = lse;
     a.ws = static_cast<unsigned char *>(workspace);
+    a.lose = lose.warp + 1;
+    a.lose_at = lose.at;
     if (num_pages == 0) k_pages = v_pages = q;  // a tensor map needs an address; its only row is never read
     Range range("kda_attn_decode");
     return done((io == KDA_BF16 ? kda::attn::launch_attn_decode_tc(a, q, k_pages, v_pages, k_new, v_new, ldq, ldk, ldv, static_cast<cudaStream_t>(stream))
                                 : kda::attn::launch_attn_decode_f32(a, q, k_pages, v_pages, k_new, v_new, ldq, ldk, ldv, static_cast<cudaStream_t>(stream))));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t kda_attn_prefill_workspace_size(int32_t N, int32_t Tq_total, int32_t Tk_total, int32_t Hq, int32_t Hkv,
+                                       int32_t D, int32_t io) {
+    if (N < 0 || Tq_total < 0 || Tk_total < 0 || check_heads(Hq, Hkv, D, io) != KDA_OK) return 0;
+    return kda::attn::workspace_bytes(attn_ctas(io, prefill_keys(N, Tq_total, Tk_total, Hq, Hkv, io)),
+                                     part_rows(io, 256));
+}
+
+int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
+                     const int32_t *cu_q, const int32_t *cu_k, int32_t N, int32_t Tq, int32_t Tk, int32_t Hq,
+                     int32_t Hkv, int32_t D, int32_t io, void *out, float *lse, void *workspace,
+                     size_t workspace_bytes, void *stream) {
+    return prefill_impl(q, k, v, ldq, ldk, ldv, scale, cu_q, cu_k, N, Tq, Tk, Hq, Hkv, D, io, out, lse, workspace,
+                        workspace_bytes, Lose(), stream);
+}
+
+int kda_testing_attn_prefill_timeout(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv,
+                                     float scale, const int32_t *cu_q, const int32_t *cu_k, int32_t N, int32_t Tq,
+                                     int32_t Tk, int32_t Hq, int32_t Hkv, int32_t D, int32_t io, void *out, float *lse,
+                                     void *workspace, size_t workspace_bytes, int32_t warp, int32_t at, void *stream) {
+    const Lose lose = {warp, at};
+    if (!lose.ok(io)) return KDA_ERR_INVALID_ARG;
+    return prefill_impl(q, k, v, ldq, ldk, ldv, scale, cu_q, cu_k, N, Tq, Tk, Hq, Hkv, D, io, out, lse, workspace,
+                        workspace_bytes, lose, stream);
+}
+
+size_t kda_attn_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
+                                      int32_t table_cols, int32_t io) {
+    if (B < 0 || T < 0 || T > kMaxTokens || table_cols < 0 || !page_ok(page_size) || check_heads(Hq, Hkv, D, io) != KDA_OK)
+        return 0;
+    return kda::attn::workspace_bytes(attn_ctas(io, decode_keys(B, T, Hq, Hkv, page_size, table_cols, io)),
+                                     part_rows(io, T * (Hq / Hkv)));
+}
+
+int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk, int64_t ldv,
+                    const void *k_pages, const void *v_pages, int32_t num_pages, int32_t page_size,
+                    const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
+                    const uint64_t *tree_mask, float scale, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                    int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    return decode_impl(q, ldq, k_new, v_new, ldk, ldv, k_pages, v_pages, num_pages, page_size, block_table, table_ld,
+                       table_cols, seq_lens, tree_mask, scale, B, T, Hq, Hkv, D, io, out, lse, workspace,
+                       workspace_bytes, Lose(), stream);
+}
+
+int kda_testing_attn_decode_timeout(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk,
+                                    int64_t ldv, const void *k_pages, const void *v_pages, int32_t num_pages,
+                                    int32_t page_size, const int32_t *block_table, int64_t table_ld, int32_t table_cols,
+                                    const int32_t *seq_lens, const uint64_t *tree_mask, float scale, int32_t B, int32_t T,
+                                    int32_t Hq, int32_t Hkv, int32_t D, int32_t io, void *out, float *lse,
+                                    void *workspace, size_t workspace_bytes, int32_t warp, int32_t at, void *stream) {
+    const Lose lose = {warp, at};
+    if (!lose.ok(io)) return KDA_ERR_INVALID_ARG;
+    return decode_impl(q, ldq, k_new, v_new, ldk, ldv, k_pages, v_pages, num_pages, page_size, block_table, table_ld,
+                       table_cols, seq_lens, tree_mask, scale, B, T, Hq, Hkv, D, io, out, lse, workspace,
+                       workspace_bytes, lose, stream);
 }
 
 // Scratch of the calls that choose pages: the free pages' list and a state per

@@ -55,7 +55,7 @@ constexpr int kMinPart = kTcMinPart;
 constexpr int kTile = 128;      // rows of a row tile, keys of a key tile
 constexpr uint32_t kTileBytes = 32768;  // 128 rows x 128 channels bf16, two 64-channel halves
 constexpr uint32_t kHalf = 16384;
-constexpr long long kWaitNs = 2000000000;
+constexpr long long kWaitNs = 2000000000, kTestWaitNs = 20000000;
 constexpr float kRescale = 8.f;  // log2 growth of a maximum that rescales O
 constexpr int kJobRing = 8;  // more than the ring has slots: a job holds its slot until it is done
 
@@ -123,8 +123,17 @@ struct Bars {  // shared-memory addresses
     static constexpr uint32_t kEnd = 472;   // Point: the end of the CTA's work
     static constexpr uint32_t kEarly = 488;  // the next CTA's early part is there
     static constexpr uint32_t kDesc = 496;  // kDescs descriptors
+    // Between the roles' own warps, at a part's end. (As mbarriers: a named barrier waits
+    // without a limit for a warp that has given up.)
+    static constexpr uint32_t kPartEnd = 880;
+    __device__ uint32_t early() const { return base + kPartEnd; }          // kEarly is written
+    __device__ uint32_t drained() const { return base + kPartEnd + 8; }    // all products are through
+    __device__ uint32_t stage_free(int s) const { return base + kPartEnd + 16 + 8 * s; }  // twice a staged part
+    __device__ uint32_t staged(int s) const { return base + kPartEnd + 32 + 8 * s; }      // likewise
+    __device__ uint32_t handed(int quad) const { return base + kPartEnd + 48 + 8 * quad; }  // DUAL: twice a joined part
+    __device__ uint32_t taken(int quad) const { return base + kPartEnd + 80 + 8 * quad; }   // likewise
 };
-static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= 1024, "barrier area");
+static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= Bars::kPartEnd && Bars::kPartEnd + 112 <= 1024, "barrier area");
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
@@ -160,9 +169,10 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int c0, int c
                  "r"(src), "r"(c0), "r"(c1), "r"(c2)
                  : "memory");
 }
-// A bounded wait: true once the phase is through, false after two seconds. (The
-// clock is read once in 1024 tries: a read takes as long as much of what is waited
-// for. Written out, since it stands in many places and all code here is fetched cold.)
+// A bounded wait: true once the phase is through, false after `NS` nanoseconds (two
+// seconds). (The clock is read once in 1024 tries: a read takes as long as much of what is
+// waited for. Written out, since it stands in many places and all code here is fetched cold.)
+template <long long NS>
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -177,7 +187,7 @@ __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity) {
         " sub.u64 t, t, t0;\n setp.lt.u64 q, t, %3;\n @q bra WAIT;\n"
         "DONE:\n selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(bar), "r"(parity), "n"(kWaitNs)
+        : "r"(bar), "r"(parity), "n"(NS)
         : "memory");
     return ok != 0;
 }
@@ -192,8 +202,9 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return ok != 0;
 }
 // a wait of a whole warp, which leaves it converged
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait(bar, parity));
+template <long long NS>
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait<NS>(bar, parity));
 }
 // z = z f + y g
 __device__ __forceinline__ void join4(uint32_t *z, float f, float4 y, float g) {
@@ -201,9 +212,6 @@ __device__ __forceinline__ void join4(uint32_t *z, float f, float4 y, float g) {
     z[1] = __float_as_uint(join_sum(__uint_as_float(z[1]), f, y.y, g));
     z[2] = __float_as_uint(join_sum(__uint_as_float(z[2]), f, y.z, g));
     z[3] = __float_as_uint(join_sum(__uint_as_float(z[3]), f, y.w, g));
-}
-__device__ __forceinline__ void named_bar(int id, int threads) {
-    asm volatile("barrier.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
 // The scheduler's state over a CTA's parts: Q tiles and (DUAL) key tiles so far.
@@ -258,10 +266,15 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
     }
 }
 
-template <bool PAGED, bool DUAL, int RT>
+// Every wait has a limit. A role whose wait runs out goes to the kernel's end, the others
+// follow as theirs run out or they see kDead, and the status tells; the copies and products
+// in flight are waited for first. TEST (kda_testing_attn_*): waits of 20 ms, and warp
+// a.lose - 1 gives up at its wait number a.lose_at.
+template <bool PAGED, bool DUAL, int RT, bool TEST>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     using L = Smem<DUAL, RT>;
+    constexpr long long kLimit = TEST ? kTestWaitNs : kWaitNs;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     const Bars bars{base + L::kBars};
@@ -308,6 +321,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc::mbar_init(bars.dempty(i), kSoftmaxWarps + 2);  // and TMA, MMA
             }
             for (int i = 0; i < kJobRing; ++i) tc::mbar_init(bars.jfull(i), 1);
+            tc::mbar_init(bars.drained(), 1);
+            if (DUAL) {
+                for (int i = 0; i < 4; ++i) {
+                    tc::mbar_init(bars.handed(i), 1);
+                    tc::mbar_init(bars.taken(i), 1);
+                }
+            } else {
+                tc::mbar_init(bars.early(), 1);
+                for (int i = 0; i < 2; ++i) {
+                    tc::mbar_init(bars.stage_free(i), 1);
+                    tc::mbar_init(bars.staged(i), 4);
+                }
+            }
             *reinterpret_cast<int *>(sm + L::kBars + Bars::kDead) = 0;
             tc::fence_mbar_init();
         }
@@ -337,6 +363,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int *const early_there = reinterpret_cast<volatile int *>(sm + L::kBars + Bars::kEarly);
     bool alive = true;
     uint32_t nd = 0;  // descriptors taken
+    int waits = 0;
+    auto warp_wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        if constexpr (TEST) {
+            if (warp == a.lose - 1 && waits++ >= a.lose_at) return false;
+        }
+        return wait_warp<kLimit>(bar, parity);
+    };
     // a wait that may last for a whole part: limited too, and ends when another role gives up
     auto long_wait = [&](uint32_t bar, uint32_t parity) -> bool {
         for (int i = 0; i < 100; ++i) {
@@ -479,16 +512,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (d->ta == 0) h->valid = 0;
                         else h->ends = kEndsJoined;
                     }
+                    mbar_arrive(bars.early());
                 }
-                named_bar(5, 32 * kSoftmaxWarps);
+                if (!(alive = warp_wait(bars.early(), 0))) break;  // (the last part of a CTA)
                 early = *early_there != 0;
             }
             const bool whole = d->whole || (early && d->ta == 0);
             // the stage is free when its last copy has read it (seen to before O is there)
             const bool staged = !DUAL && whole && (steps > 0 || early), leader = quad == 0 && lane == 0;
             if (staged) {
-                if (leader) tc::bulk_wait_read();
-                named_bar(1 + s, 128);
+                if (leader) {
+                    tc::bulk_wait_read();
+                    mbar_arrive(bars.stage_free(s));
+                }
+                if (!(alive = warp_wait(bars.stage_free(s), 0))) break;
             }
             const float *const next_o = part_o(a, 2 * (cta + 1));
             if (steps > 0) {
@@ -505,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // for whole rows to leave together.
                 float4 *const box = reinterpret_cast<float4 *>(sm + L::kJoin) + r;
                 float2 *const box_ml = reinterpret_cast<float2 *>(sm + L::kMl) + r;
-                const int join_bar = 1 + quad;  // the two warps of these 32 rows
+                // (the arrivals name the two warps by tid: with `quad` there too, two registers spill)
                 const int q0 = d->q0 + (DUAL ? 0 : s * a.tile_tokens), row0 = d->h * a.G;
                 // A full row tile goes out by tensor copies, in the layout of Q; the rows of a
                 // short one (next to them may lie another sequence's) by the warps.
@@ -531,12 +568,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             box[RT * q] = make_float4(
                                 __uint_as_float(o[q / 4][4 * (q % 4)]), __uint_as_float(o[q / 4][4 * (q % 4) + 1]),
                                 __uint_as_float(o[q / 4][4 * (q % 4) + 2]), __uint_as_float(o[q / 4][4 * (q % 4) + 3]));
-                        named_bar(join_bar, 64);  // handed over
-                        named_bar(join_bar, 64);  // taken
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.handed(tid >> 5 & 3));  // to the writer's warp of these 32 rows
+                        if (!(alive = warp_wait(bars.taken(quad), p))) break;
                         continue;
                     }
                     if (joins) {
-                        named_bar(join_bar, 64);
+                        if (!(alive = warp_wait(bars.handed(quad), p))) break;
                         if (p == 0) {
                             const float2 ml = *box_ml;
                             const float2 fs = join_factors(m, ml.x, c);
@@ -551,7 +589,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t *z = &o[q / 4][4 * (q % 4)];
                             join4(z, f, y, f1);
                         }
-                        named_bar(join_bar, 64);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.taken(tid >> 5 & 3));
                     }
                     if (!DUAL && early && row_ok) {
                         const float4 *const y4 = reinterpret_cast<const float4 *>(next_o) + 128 * s + r;
@@ -589,8 +628,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         continue;
                     }
                     if (!DUAL && p == 1) {
-                        if (leader) tc::bulk_wait_read();
-                        named_bar(1 + s, 128);
+                        if (leader) {
+                            tc::bulk_wait_read();
+                            mbar_arrive(bars.stage_free(s));
+                        }
+                        if (!(alive = warp_wait(bars.stage_free(s), 1))) break;
                     }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -603,9 +645,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         *reinterpret_cast<uint4 *>(stage + at) = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     if (DUAL) continue;
+                    // The stream's four warps have staged their rows (short tile: and are done with
+                    // them): the leader waits for that before it frees the stage again.
+                    auto all_staged = [&]() -> bool {
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.staged(s));
+                        return quad != 0 || warp_wait(bars.staged(s), p);
+                    };
                     if (full) {
                         tc::fence_async_smem();
-                        named_bar(1 + s, 128);  // the stream's four warps have staged their rows
+                        if (!(alive = all_staged())) break;
                         if (leader) {
                             tma_store_3d(&maps.out, 64 * p, row0, q0, base + stage_at);
                             tc::bulk_commit();
@@ -620,8 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (row < rows)
                                 reinterpret_cast<uint4 *>(out + ((size_t)(q0 + tk) * a.Hq + row0 + (row - tk * a.G)) * kD + 64 * p)[ch] = y;
                         }
+                        if (!(alive = all_staged())) break;
                     }
                 }
+                if (!alive) break;
                 if (writer && !whole) {
                     if (row_ok) part_ml(a, d->slot)[DUAL ? r : 128 * s + r] = make_float2(m, l);
                 } else if (writer) {
@@ -711,6 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int n, h, k0, Lk, t, draft, pg;
             };
             uint32_t kv = 0, jobs = 0, g = 0;
+            uint32_t sent = 0;  // bit i: slot i's last copy goes to the fixing warp; 8 + i: their number's parity; 16 + i: Q tile i's
             const uint32_t qbytes = (uint32_t)(a.tile_tokens * a.G) * 256u;
             const int rows = a.page < kTile ? a.page : kTile;  // decode: rows of one copy
             const int row_bits = 31 - __clz(rows), page_bits = 31 - __clz(a.page);
@@ -735,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P is 0 there, but 0 times a NaN is not, so V gets zeros
                 const bool fix = is_v && valid < kTile;
                 const uint32_t bar = fix ? bars.vraw(slot) : bars.kvfull(slot);
+                sent = fix ? (sent | 1u << slot) ^ (256u << slot) : sent & ~(1u << slot);
                 const CUtensorMap *m = is_v ? &maps.v : &maps.k;
                 if (!PAGED) {
                     expect_tx(lead, bar, kTileBytes);
@@ -773,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alive = false;
                     return;
                 }
+                sent ^= 65536u << slot;
                 const uint32_t dst = base + L::kQ + slot * L::kQTile, bar = bars.qfull(slot);
                 expect_tx(lead, bar, qbytes);
                 tma_3d(lead, dst, &maps.q, 0, h * a.G, tok, bar);
@@ -851,6 +905,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 reinterpret_cast<int2 *>(sm + L::kBars + Bars::kJobs)[jobs % kJobRing] = make_int2(-1, 0);
                 mbar_arrive(bars.jfull(jobs % kJobRing));
             }
+            // The last copy into each slot has landed before the CTA ends, whoever takes it or not.
+            // (Of n copies the last one's parity is n - 1's; of none it is that of no wait.)
+            bool landed = true;
+#pragma unroll 1
+            for (uint32_t i = 0; i < (uint32_t)L::kRing; ++i)
+                landed = wait_warp<kLimit>(sent >> i & 1 ? bars.vraw(i) : bars.kvfull(i),
+                                           (sent >> i & 1 ? ~sent >> (8 + i) : (kv + L::kRing - 1 - i) / L::kRing - 1) & 1) && landed;
+#pragma unroll 1
+            for (uint32_t i = 0; i < (uint32_t)L::kQs; ++i)
+                landed = wait_warp<kLimit>(bars.qfull(i), ~sent >> (16 + i) & 1) && landed;
+            alive = alive && landed;
         } else if (warp == kWarpFix) {
             // ---- fixing warp: zeros in the V rows past a sequence's end ----------------
             uint32_t fixed = 0;
@@ -998,6 +1063,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ++g;
                 }
             }
+            tc::mma_commit_lead(lead, bars.drained());  // no product outlives the CTA, or its TMEM
+            alive = wait_warp<kLimit>(bars.drained(), 0) && alive;
         }
     }
     __syncwarp();
@@ -1037,8 +1104,8 @@ bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-template <bool PAGED, bool DUAL, int RT>
-cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
+template <bool PAGED, bool DUAL, int RT, bool TEST>
+cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
     a.streams = DUAL ? 1 : 2;
     // An item's start and end cost about as much as 1.2 key tiles of 256 rows, and a tile that is
     // cut short half of one (extra 192, 256, 320 on ragged prompts: 51.8, 53.0, 55.5 us); a
@@ -1061,13 +1128,18 @@ cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, c
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        e = cudaFuncSetAttribute(attn_tc_kernel<PAGED, DUAL, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(attn_tc_kernel<PAGED, DUAL, RT, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    e = launch_early(attn_tc_kernel<PAGED, DUAL, RT>, dim3(a.direct ? (unsigned)slots : (unsigned)a.ctas), kThreads,
+    e = launch_early(attn_tc_kernel<PAGED, DUAL, RT, TEST>, dim3(a.direct ? (unsigned)slots : (unsigned)a.ctas), kThreads,
                      bytes, stream, a, maps);
     return e == cudaSuccess && !a.direct ? launch_attn_combine(a, true, !DUAL, stream) : e;
+}
+template <bool PAGED, bool DUAL, int RT>
+cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
+    return a.lose > 0 ? launch_form<PAGED, DUAL, RT, true>(a, maps, slots, keys, stream)
+                      : launch_form<PAGED, DUAL, RT, false>(a, maps, slots, keys, stream);
 }
 }  // namespace
 
