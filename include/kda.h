@@ -479,8 +479,8 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
  * from one row to the next): a row's pages in order, then -1; seq_lens int32
  * [rows]; refs int32 [num_pages] (16-byte aligned): the table entries on each page,
  * 0 = free. All three are DEVICE arrays that these calls update, for any number of
- * layers' pools at once. Pages are chosen lowest number first, so results depend
- * on the inputs alone. `workspace` (256-byte aligned, kda_cache_workspace_size
+ * layers' pools at once. num_pages and rows * table_cols are at most 2^31 - 2^16. Pages
+ * are chosen lowest number first, so results depend on the inputs alone. `workspace` (256-byte aligned, kda_cache_workspace_size
  * bytes, its first 256 bytes zero before its first use) also takes the status:
  * malformed rows, lengths or page numbers are skipped and flagged
  * (KDA_ERR_DEVICE); a call that needs more pages than are free changes nothing

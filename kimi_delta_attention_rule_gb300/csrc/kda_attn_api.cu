@@ -54,6 +54,9 @@ constexpr int kMaxGroup = 64;
 constexpr int kMaxTokens = kda::attn::kMaxDrafts;
 constexpr long long kMaxKeys = (1LL << 31) - 1024;  // (positions two key tiles past a sequence's end are formed)
 constexpr size_t kHeader = 256;  // of a cache workspace: the status word
+// Pages, and entries of a block table: their kernels step past the last one by less than 2^16
+// and add up the pages that all rows lack, in 32 bits.
+constexpr long long kMaxPages = (1LL << 31) - (1LL << 16);
 
 struct Range {
     explicit Range(const char *name) { nvtxRangePushA(name); }
@@ -299,6 +302,7 @@ size_t kda_cache_workspace_size(int32_t num_pages, int32_t rows) {
 static int check_cache(const int32_t *table, int64_t ld, int32_t rows, int32_t cols, const int32_t *refs,
                        int32_t num_pages, const void *ws, size_t ws_bytes) {
     if (rows < 0 || cols < 0 || ld < cols || num_pages < 0) return KDA_ERR_INVALID_ARG;
+    if (num_pages > kMaxPages || (long long)rows * cols > kMaxPages) return KDA_ERR_INVALID_ARG;
     if ((rows > 0 && cols > 0 && table == nullptr) || (num_pages > 0 && refs == nullptr) || ws == nullptr)
         return KDA_ERR_INVALID_ARG;
     if (!aligned(table, 4) || !aligned(refs, 16) || !aligned(ws, 256) ||
