@@ -4,6 +4,8 @@ _kda_bind.so (the Python side of the attention and cache calls).
 Each translation unit is compiled in parallel with nvcc, then linked into
 one shared library next to this file; the binding, which alone sees PyTorch's
 headers, is one file for the host compiler. Re-running skips an up-to-date build.
+Without Python's or PyTorch's headers the library is built all the same, with a
+warning; the Python calls that need the binding then raise.
 """
 from __future__ import annotations
 
@@ -12,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -80,9 +83,17 @@ def build_bind(force: bool = False) -> str:
     return BIND
 
 
+def _try_bind(force: bool = False) -> None:
+    try:
+        build_bind(force)
+    except Exception as e:
+        warnings.warn("the Python binding of the attention and cache calls is not built: %s" % e)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    """The library (raises if it cannot be built) and, where it can be built, the binding."""
     if not force and up_to_date():
-        build_bind()
+        _try_bind()
         return LIB
     os.makedirs(OBJDIR, exist_ok=True)
     cc = nvcc()
@@ -96,7 +107,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj, r.stderr
 
     with ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
-        bind = ex.submit(build_bind, force)
+        bind = ex.submit(_try_bind, force)
         results = list(ex.map(compile_one, _sources()))
         bind.result()
     if verbose:
