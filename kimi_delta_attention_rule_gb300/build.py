@@ -53,17 +53,40 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
+def _bind_stamp() -> str:
+    return os.path.join(OBJDIR, "bind.txt")
+
+
+def _bind_against() -> str:
+    """What the binding's binary interface goes by; kept beside the objects."""
+    import torch
+    return "python %s\ntorch %s %s\ncompiler %s\n" % (sys.version, torch.__version__, os.path.dirname(torch.__file__),
+                                                     os.environ.get("CXX", "g++"))
+
+
 def _bind_up_to_date() -> bool:
-    if not os.path.exists(BIND):
+    if not os.path.exists(BIND) or not os.path.exists(_bind_stamp()):
         return False
     t = os.path.getmtime(BIND)
-    return all(os.path.getmtime(p) <= t for p in [BIND_SRC] + glob.glob(os.path.join(INCLUDE, "*.h")))
+    if any(os.path.getmtime(p) > t for p in [BIND_SRC] + glob.glob(os.path.join(INCLUDE, "*.h"))):
+        return False
+    with open(_bind_stamp()) as f:
+        return f.read() == _bind_against()
 
 
 def build_bind(force: bool = False) -> str:
     """The binding module, against the PyTorch that runs this."""
     if not force and _bind_up_to_date():
         return BIND
+    try:
+        return _compile_bind()
+    except Exception:
+        if os.path.exists(BIND):  # a stale one: none is better
+            os.remove(BIND)
+        raise
+
+
+def _compile_bind() -> str:
     import sysconfig
 
     import torch
@@ -79,6 +102,9 @@ def build_bind(force: bool = False) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("%s failed on %s:\n%s\n%s" % (cmd[0], BIND_SRC, r.stdout, r.stderr))
+    os.makedirs(OBJDIR, exist_ok=True)
+    with open(_bind_stamp(), "w") as f:
+        f.write(_bind_against())
     os.replace(tmp, BIND)
     return BIND
 

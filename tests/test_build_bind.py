@@ -50,3 +50,34 @@ def test_both_are_built_once(tree):
     times = [os.stat(p).st_mtime_ns for p in (kbuild.LIB, kbuild.BIND)]
     kbuild.build()
     assert times == [os.stat(p).st_mtime_ns for p in (kbuild.LIB, kbuild.BIND)]
+
+
+def test_another_pytorch_or_python_builds_the_binding_anew(tree, monkeypatch):
+    import torch
+    kbuild.build()
+    first = os.stat(kbuild.BIND).st_mtime_ns
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    kbuild.build()
+    second = os.stat(kbuild.BIND).st_mtime_ns
+    assert second != first
+    kbuild.build()
+    assert os.stat(kbuild.BIND).st_mtime_ns == second
+    monkeypatch.setattr("sys.version", "3.99 (another)")
+    kbuild.build()
+    assert os.stat(kbuild.BIND).st_mtime_ns != second
+
+
+def test_a_binding_of_unknown_origin_is_built_anew(tree):
+    kbuild.build()
+    first = os.stat(kbuild.BIND).st_mtime_ns
+    (tree / "_build" / "bind.txt").unlink()
+    kbuild.build()
+    assert os.stat(kbuild.BIND).st_mtime_ns != first
+
+
+def test_a_stale_binding_does_not_outlive_a_failed_build(tree):
+    kbuild.build()
+    (tree / "csrc" / "bind.cpp").write_text("#error changed\n")
+    with pytest.warns(UserWarning, match="changed"):
+        kbuild.build()
+    assert not os.path.exists(kbuild.BIND)
