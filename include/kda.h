@@ -404,8 +404,9 @@ int kda_noalloc_status(void *stream);
  * lse = -inf. Logits, maxima and sums are fp32 (with bf16 I/O p is rounded to
  * bf16 for the product with v, out to bf16 at the end). A sequence's keys only
  * ever touch its own rows: whatever lies past a sequence's end (another
- * sequence, the rest of a page, NaN) is not used. Inside a sequence a NaN in v
- * reaches every row of the same key tile, as 0 * NaN does.
+ * sequence, the rest of a page, NaN) is not used. Inside a sequence a NaN or an infinity
+ * in v also reaches, in its channel, rows that do not see it but share its key tile (128 keys,
+ * fp32 64; a call's drafts are a tile), as 0 * NaN and 0 * infinity do.
  * scale: finite and > 0. D = 128.
  *
  * Workspace: device buffer, 256-byte aligned, of the size that the query gives
