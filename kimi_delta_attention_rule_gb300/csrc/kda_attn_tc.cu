@@ -123,17 +123,16 @@ struct Bars {  // shared-memory addresses
     static constexpr uint32_t kEnd = 472;   // Point: the end of the CTA's work
     static constexpr uint32_t kEarly = 488;  // the next CTA's early part is there
     static constexpr uint32_t kDesc = 496;  // kDescs descriptors
-    // Between the roles' own warps, at a part's end. (As mbarriers: a named barrier waits
-    // without a limit for a warp that has given up.)
+    // Between the softmax warps, at a part's end. (As mbarriers: a named barrier waits
+    // without a limit for a warp that has given up. But see hand_over.)
     static constexpr uint32_t kPartEnd = 880;
     __device__ uint32_t early() const { return base + kPartEnd; }          // kEarly is written
     __device__ uint32_t drained() const { return base + kPartEnd + 8; }    // all products are through
     __device__ uint32_t stage_free(int s) const { return base + kPartEnd + 16 + 8 * s; }  // twice a staged part
     __device__ uint32_t staged(int s) const { return base + kPartEnd + 32 + 8 * s; }      // likewise
-    __device__ uint32_t handed(int quad) const { return base + kPartEnd + 48 + 8 * quad; }  // DUAL: twice a joined part
-    __device__ uint32_t taken(int quad) const { return base + kPartEnd + 80 + 8 * quad; }   // likewise
+    static constexpr uint32_t kGone = 928;  // DUAL, four quads: a warp of these rows has given up
 };
-static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= Bars::kPartEnd && Bars::kPartEnd + 112 <= 1024, "barrier area");
+static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= Bars::kPartEnd && Bars::kGone + 16 <= 1024, "barrier area");
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
@@ -205,6 +204,16 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
 template <long long NS>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     return __all_sync(0xffffffffu, wait<NS>(bar, parity));
+}
+// DUAL: the two warps of the same 32 rows meet, four times a joined part. (A named barrier:
+// with mbarriers here 128 sequences of 500 tokens take 72.5 us instead of 69.6.) Such a barrier
+// waits for both, so it must not wait for a warp that is gone: a warp gives up only ahead of
+// a part's first meeting, and as it leaves it says so in kGone and arrives (hand_over_gone)
+// for that one. Its partner, should it come there, looks at kGone after the first meeting of a
+// part, and leaves too.
+__device__ __forceinline__ void hand_over(int quad) { asm volatile("barrier.sync %0, 64;\n" ::"r"(1 + quad) : "memory"); }
+__device__ __forceinline__ void hand_over_gone(int quad) {
+    asm volatile("barrier.arrive %0, 64;\n" ::"r"(1 + quad) : "memory");
 }
 // z = z f + y g
 __device__ __forceinline__ void join4(uint32_t *z, float f, float4 y, float g) {
@@ -323,10 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < kJobRing; ++i) tc::mbar_init(bars.jfull(i), 1);
             tc::mbar_init(bars.drained(), 1);
             if (DUAL) {
-                for (int i = 0; i < 4; ++i) {
-                    tc::mbar_init(bars.handed(i), 1);
-                    tc::mbar_init(bars.taken(i), 1);
-                }
+                *reinterpret_cast<int4 *>(sm + L::kBars + Bars::kGone) = make_int4(0, 0, 0, 0);
             } else {
                 tc::mbar_init(bars.early(), 1);
                 for (int i = 0; i < 2; ++i) {
@@ -394,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t inv_g = (65536u + a.G - 1) / a.G;  // x / G = x inv_g >> 16, exact for x < 1024
         const int tok = (int)(r * inv_g >> 16), g = r - tok * a.G;
         const float c = a.scale * kLog2e;
+        volatile int *const gone = reinterpret_cast<volatile int *>(sm + L::kBars + Bars::kGone);
         uint32_t ns = 0, no = 0;
         while (const Desc *d = next_desc()) {
             const int steps = d->count[s];
@@ -542,7 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // for whole rows to leave together.
                 float4 *const box = reinterpret_cast<float4 *>(sm + L::kJoin) + r;
                 float2 *const box_ml = reinterpret_cast<float2 *>(sm + L::kMl) + r;
-                // (the arrivals name the two warps by tid: with `quad` there too, two registers spill)
                 const int q0 = d->q0 + (DUAL ? 0 : s * a.tile_tokens), row0 = d->h * a.G;
                 // A full row tile goes out by tensor copies, in the layout of Q; the rows of a
                 // short one (next to them may lie another sequence's) by the warps.
@@ -568,13 +574,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                             box[RT * q] = make_float4(
                                 __uint_as_float(o[q / 4][4 * (q % 4)]), __uint_as_float(o[q / 4][4 * (q % 4) + 1]),
                                 __uint_as_float(o[q / 4][4 * (q % 4) + 2]), __uint_as_float(o[q / 4][4 * (q % 4) + 3]));
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bars.handed(tid >> 5 & 3));  // to the writer's warp of these 32 rows
-                        if (!(alive = warp_wait(bars.taken(quad), p))) break;
+                        hand_over(quad);  // handed over
+                        if (p == 0 && gone[quad] != 0) {
+                            alive = false;
+                            break;
+                        }
+                        hand_over(quad);  // taken
                         continue;
                     }
                     if (joins) {
-                        if (!(alive = warp_wait(bars.handed(quad), p))) break;
+                        hand_over(quad);
+                        if (p == 0 && gone[quad] != 0) {
+                            alive = false;
+                            break;
+                        }
                         if (p == 0) {
                             const float2 ml = *box_ml;
                             const float2 fs = join_factors(m, ml.x, c);
@@ -589,8 +602,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             uint32_t *z = &o[q / 4][4 * (q % 4)];
                             join4(z, f, y, f1);
                         }
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bars.taken(tid >> 5 & 3));
+                        hand_over(quad);
                     }
                     if (!DUAL && early && row_ok) {
                         const float4 *const y4 = reinterpret_cast<const float4 *>(next_o) + 128 * s + r;
@@ -702,6 +714,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             ++nd;
         }
+        if (DUAL && !alive && __all_sync(0xffffffffu, gone[quad] == 0)) {
+            if (lane == 0) gone[quad] = 1;
+            __syncwarp();
+            hand_over_gone(quad);
+        }
         if (lane == 0) tc::bulk_wait_all();
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n");
@@ -762,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int n, h, k0, Lk, t, draft, pg;
             };
             uint32_t kv = 0, jobs = 0, g = 0;
-            uint32_t sent = 0;  // bit i: slot i's last copy goes to the fixing warp; 8 + i: their number's parity; 16 + i: Q tile i's
+            uint32_t sent = 0;  // bit i: the parity of Q slot i's copies
             const uint32_t qbytes = (uint32_t)(a.tile_tokens * a.G) * 256u;
             const int rows = a.page < kTile ? a.page : kTile;  // decode: rows of one copy
             const int row_bits = 31 - __clz(rows), page_bits = 31 - __clz(a.page);
@@ -787,7 +804,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P is 0 there, but 0 times a NaN is not, so V gets zeros
                 const bool fix = is_v && valid < kTile;
                 const uint32_t bar = fix ? bars.vraw(slot) : bars.kvfull(slot);
-                sent = fix ? (sent | 1u << slot) ^ (256u << slot) : sent & ~(1u << slot);
                 const CUtensorMap *m = is_v ? &maps.v : &maps.k;
                 if (!PAGED) {
                     expect_tx(lead, bar, kTileBytes);
@@ -826,7 +842,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     alive = false;
                     return;
                 }
-                sent ^= 65536u << slot;
+                sent ^= 1u << slot;
                 const uint32_t dst = base + L::kQ + slot * L::kQTile, bar = bars.qfull(slot);
                 expect_tx(lead, bar, qbytes);
                 tma_3d(lead, dst, &maps.q, 0, h * a.G, tok, bar);
@@ -906,15 +922,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(bars.jfull(jobs % kJobRing));
             }
             // The last copy into each slot has landed before the CTA ends, whoever takes it or not.
-            // (Of n copies the last one's parity is n - 1's; of none it is that of no wait.)
+            // (Of n copies the last one's parity is n - 1's; of none it is that of no wait. A copy that
+            // the fixing warp would have handed on has landed when the limit is over.)
             bool landed = true;
 #pragma unroll 1
             for (uint32_t i = 0; i < (uint32_t)L::kRing; ++i)
-                landed = wait_warp<kLimit>(sent >> i & 1 ? bars.vraw(i) : bars.kvfull(i),
-                                           (sent >> i & 1 ? ~sent >> (8 + i) : (kv + L::kRing - 1 - i) / L::kRing - 1) & 1) && landed;
+                landed = wait_warp<kLimit>(bars.kvfull(i), ((kv + L::kRing - 1 - i) / L::kRing - 1) & 1) && landed;
 #pragma unroll 1
             for (uint32_t i = 0; i < (uint32_t)L::kQs; ++i)
-                landed = wait_warp<kLimit>(bars.qfull(i), ~sent >> (16 + i) & 1) && landed;
+                landed = wait_warp<kLimit>(bars.qfull(i), ~sent >> i & 1) && landed;
             alive = alive && landed;
         } else if (warp == kWarpFix) {
             // ---- fixing warp: zeros in the V rows past a sequence's end ----------------

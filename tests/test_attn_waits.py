@@ -16,14 +16,24 @@ SOURCE = os.path.join(kbuild.CSRC, "kda_attn_tc.cu")
 
 def test_no_role_waits_without_a_limit():
     """Roles meet at mbarriers, through the one bounded wait; a named barrier would wait
-    forever for a warp that has given up. The whole CTA meets where every path arrives: after the
-    set-up and at the end."""
+    forever for a warp that has given up. The one that there is, between the two warps of a join's
+    rows, has an arrival for a warp that leaves, and after a part's first meeting its partner looks
+    whether it has. The whole CTA meets where every path arrives: after the set-up and at the end."""
     code = re.sub(r"//[^\n]*", "", open(SOURCE).read())
-    assert not re.findall(r"\bbar(?:rier)?\.(?:cta\.)?(?:sync|red|arrive)\b", code)
+    named = re.findall(r"\bbar(?:rier)?\.(?:cta\.)?(?:sync|red|arrive)\b[^;]*", code)
+    assert named == ["barrier.sync %0, 64", "barrier.arrive %0, 64"]
     assert len(re.findall(r"try_wait", code)) == 1
     body = code[code.index("attn_tc_kernel(const"):]
-    assert len(re.findall(r"__syncthreads\(\)", body)) == 2
-    assert "bar.sync" not in body and "cooperative_groups" not in code
+    assert len(re.findall(r"__syncthreads\(\)", body)) == 2 and "cooperative_groups" not in code
+    part = body[body.index("hand_over(quad);"):]
+    meetings = [m.end() for m in re.finditer(r"hand_over\(quad\);", part)]
+    assert len(meetings) == 4  # either warp: twice a half of the row
+    for first in (meetings[0], meetings[2]):
+        assert re.match(r"\s*if \(p == 0 && gone\[quad\] != 0\) \{\s*alive = false;\s*break;", part[first:])
+    left = part.index("if (DUAL && !alive && __all_sync(0xffffffffu, gone[quad] == 0))")
+    assert meetings[3] < left < part.index("hand_over_gone(quad);")
+    # nothing that can give up stands between a part's first and last meeting
+    assert "warp_wait" not in part[:meetings[1]] and "warp_wait" not in part[meetings[1]:meetings[3]]
 
 
 FAKE = ctypes.c_void_p(0x100000)
