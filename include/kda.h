@@ -395,7 +395,8 @@ int kda_noalloc_status(void *stream);
 /*
  * Softmax attention, for the full-attention layers that stand between a model's
  * KDA layers ("K3 vs DSV4 architecture divergence", KDA section: the layers
- * alternate). Hq query heads share Hkv key/value heads, G = Hq / Hkv <= 64 each:
+ * alternate; there with gated MLA, whose cache of one latent row per token these
+ * calls do not read: they take K and V heads of 128 channels). Hq query heads share Hkv key/value heads, G = Hq / Hkv <= 64 each:
  *
  *     o_i = sum_j p_ij v_j / sum_j p_ij,   p_ij = exp(scale q_i . k_j),
  *     lse_i = ln sum_j p_ij,

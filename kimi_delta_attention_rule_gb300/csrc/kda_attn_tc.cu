@@ -18,15 +18,17 @@
 // bounds the kernel: so P goes to the tensor core in two parts (96 keys' products run
 // while the last 32 keys' exponentials do), and a part's first Q K^T
 // follows the last P V of the part before it, under that part's epilogue. O is
-// rescaled only when a row's maximum grows by more than 2^8, which P in bf16
-// (rounded to nearest, relative step 2^-8) and l in fp32 hold without loss.
+// rescaled only when a row's maximum grows by more than 2^8: P is then 2^8 at most, far
+// inside the range of bf16 (to which it is rounded, 2^-8 of it at most, for the product),
+// and l sums the unrounded terms in fp32.
 // With at most 128 rows per kv head (decode) both streams take the same row tile
 // and alternate key tiles; their results are joined at the end (DUAL).
 //
 // Measured (GB300; copy 6,782 GB/s, cuBLAS bf16 1,917 TFLOP/s): causal attention of 8,192
-// tokens, 32 heads on 8: 318 us, 1,729 TFLOP/s, the tensor pipe busy 73 % of the time and the
-// exponentials' 36 %; a step of two row tiles takes some 2,700 cycles, 2,048 of them products.
-// One token each of 128 sequences, 400,003 cached tokens: 254 us, 6.5 TB/s (loads). Some
+// tokens, 32 heads on 8: 320 us, 1,718 TFLOP/s in a short run in a graph, 355 us in calls back to
+// back (at the power cap); the tensor pipe is busy 74 % of the time and the
+// exponentials' 37 %; a step of two row tiles takes some 2,700 cycles, 2,048 of them products.
+// One token each of 128 sequences, 400,003 cached tokens: 251 us, 6.5 TB/s (loads). Some
 // 11,000 cycles pass before the first softmax (5,500 of a direct call): the search for the
 // CTA's work, the page's number, the first tile, each from a cold cache. Tried without gain: 16
 // softmax warps of two threads a row (spills), halves of 64 keys with a maximum ahead of
@@ -88,7 +90,7 @@ struct Desc {
 // once the last Q K^T is through), the ring of K and V tiles, barriers, descriptors.
 // With RT = 32 (a decode step's rows, as a rule) the ring has six tiles: 192 KB in
 // flight instead of 128 hide the latency of a chain of short sequences (128 of 500 tokens:
-// 66.6 us instead of 72.6; of 3,125: 255 instead of 250). The products
+// 66.6 us instead of 72.6 when it was taken; of 3,125: 255 instead of 250). The products
 // read 128 rows of Q all the same; what lies behind the tile gives rows of S and O
 // that nobody looks at.
 template <bool DUAL, int RT>
@@ -1176,7 +1178,7 @@ cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const v
                                   const void *vn, long long ldq, long long ldk, long long ldv,
                                   cudaStream_t stream) {
     // (one row tile for both streams instead of a second, empty one: 128 sequences of 500
-    // tokens 66.6 us instead of 79.3, one of 65,531 51.5 instead of 52.3)
+    // tokens, when it was taken, 66.6 us instead of 79.3, one of 65,531 51.5 instead of 52.3)
     const bool dual = a.T * a.G <= kTile;
     a.tile_tokens = dual ? a.T : kTile / a.G;
     const long long rows = (long long)a.pages * a.Hkv * a.page, toks = (long long)a.N * a.T;
