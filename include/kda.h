@@ -477,6 +477,37 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
                     void *stream);
 
 /*
+ * kda_attn_prefill and kda_attn_decode through a sliding window, for layers that bound
+ * their context: a token looks at the last `window` (>= 1) of the keys that it sees in the
+ * plain calls, and at the first `sinks` (>= 0) of them, which stay visible.
+ *   prefill: token i (which sees the keys j <= p, p = i + Lk - Lq) looks at those with j > p - window or
+ *            j < sinks.
+ *   decode:  a token that sees n >= 1 of the new ones (itself counted, whether or not its mask has
+ *            its own bit) looks at those and, of the cache, at the positions >= seq_lens[b] - (window - n) and
+ *            < sinks. With k_new, window >= T (a window never ends among the drafts, else
+ *            KDA_ERR_INVALID_ARG); without it n = 0. Pages of which no token of the call sees a key are not read, and
+ *            their table entries may hold anything: they can have been given back.
+ * Other keys between the two stretches are not used, but as in the plain calls a NaN or an infinity in v
+ * reaches rows whose own keys share its key tile. All else (arguments, workspace, its size,
+ * alignment, errors) is as in the plain calls; with a window past the longest sequence the
+ * result is theirs. Work and reads grow with the window, not with the context.
+ */
+int kda_attn_prefill_window(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk,
+                            int64_t ldv, float scale, int32_t window, int32_t sinks,
+                            const int32_t *cu_seqlens_q, const int32_t *cu_seqlens_k, int32_t N,
+                            int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv, int32_t D, int32_t io,
+                            void *out, float *lse, void *workspace, size_t workspace_bytes,
+                            void *stream);
+int kda_attn_decode_window(const void *q, int64_t ldq, const void *k_new, const void *v_new,
+                           int64_t ldk, int64_t ldv, const void *k_pages, const void *v_pages,
+                           int32_t num_pages, int32_t page_size, const int32_t *block_table,
+                           int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
+                           const uint64_t *tree_mask, float scale, int32_t window, int32_t sinks,
+                           int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t io,
+                           void *out, float *lse, void *workspace, size_t workspace_bytes,
+                           void *stream);
+
+/*
  * The pages of a cache. block_table int32 [rows, table_cols] (table_ld entries
  * from one row to the next): a row's pages in order, then -1; seq_lens int32
  * [rows]; refs int32 [num_pages] (16-byte aligned): the table entries on each page,

@@ -42,7 +42,7 @@ EXPORTED = ("kda_status_string", "kda_abi_version", "kda_prefill_workspace_size"
             "kda_attn_prefill_workspace_size", "kda_attn_decode",
             "kda_attn_decode_workspace_size", "kda_cache_workspace_size", "kda_cache_alloc",
             "kda_cache_fork", "kda_cache_free", "kda_cache_compact", "kda_cache_copy",
-            "kda_cache_append")
+            "kda_cache_append", "kda_attn_prefill_window", "kda_attn_decode_window")
 
 
 class PrefillPlanInfo(ctypes.Structure):
@@ -126,6 +126,12 @@ def load() -> ctypes.CDLL:
         lib.kda_attn_decode.argtypes = ([P, I64, P, P, I64, I64, P, P, I32, I32, P, I64, I32, P, P,
                                          F32] + [I32] * 6 + [P, P, P, SZ, P])
         lib.kda_attn_decode.restype = ctypes.c_int
+        lib.kda_attn_prefill_window.argtypes = ([P, P, P, I64, I64, I64, F32, I32, I32, P, P] + [I32] * 7 +
+                                                [P, P, P, SZ, P])
+        lib.kda_attn_prefill_window.restype = ctypes.c_int
+        lib.kda_attn_decode_window.argtypes = ([P, I64, P, P, I64, I64, P, P, I32, I32, P, I64, I32, P, P,
+                                                F32, I32, I32] + [I32] * 6 + [P, P, P, SZ, P])
+        lib.kda_attn_decode_window.restype = ctypes.c_int
         lib.kda_cache_workspace_size.argtypes = [I32, I32]
         lib.kda_cache_workspace_size.restype = SZ
         lib.kda_cache_alloc.argtypes = [P, I64, I32, I32, P, P, I32, I32, P, SZ, P]
@@ -465,7 +471,7 @@ def kda_check_cu_seqlens(cu_host, T_total: int) -> int:
 _BIND_ENTRIES = ("kda_attn_prefill_workspace_size", "kda_attn_prefill",
                  "kda_attn_decode_workspace_size", "kda_attn_decode", "kda_cache_workspace_size",
                  "kda_cache_alloc", "kda_cache_fork", "kda_cache_free", "kda_cache_compact",
-                 "kda_cache_copy", "kda_cache_append")
+                 "kda_cache_copy", "kda_cache_append", "kda_attn_prefill_window", "kda_attn_decode_window")
 _bind = None
 
 
@@ -558,6 +564,28 @@ def kda_attn_decode(q, k_pages, v_pages, block_table, seq_lens, scale, k_new=Non
     return (_bind or _native()).attn_decode(q, k_pages, v_pages, block_table, seq_lens, scale, k_new,
                                             v_new, tree_mask, out, lse, output_lse, workspace,
                                             stream)
+
+
+def kda_attn_prefill_window(q, k, v, scale, window, sinks=0, cu_seqlens=None, cu_seqlens_k=None, N=1,
+                            out=None, lse=None, output_lse=False, workspace=None, stream=None):
+    """kda_attn_prefill through a sliding window (C entry point
+    ``kda_attn_prefill_window``): a token looks at the last `window` keys of those it
+    sees, and at its sequence's first `sinks`. All else as kda_attn_prefill (its
+    workspace too)."""
+    return (_bind or _native()).attn_prefill_window(q, k, v, scale, cu_seqlens, cu_seqlens_k, N, out, lse,
+                                                    output_lse, workspace, stream, window, sinks)
+
+
+def kda_attn_decode_window(q, k_pages, v_pages, block_table, seq_lens, scale, window, sinks=0, k_new=None,
+                           v_new=None, tree_mask=None, out=None, lse=None, output_lse=False,
+                           workspace=None, stream=None):
+    """kda_attn_decode through a sliding window (C entry point
+    ``kda_attn_decode_window``): a token that sees n of the new ones looks at those, at
+    the last window - n cached tokens and at the first `sinks`; window >= T. Pages that
+    no token looks at are not read. All else as kda_attn_decode (its workspace too)."""
+    return (_bind or _native()).attn_decode_window(q, k_pages, v_pages, block_table, seq_lens, scale, k_new,
+                                                   v_new, tree_mask, out, lse, output_lse, workspace,
+                                                   stream, window, sinks)
 
 
 def kda_cache_alloc(block_table, want, refs, page_size, workspace=None, stream=None):

@@ -9,6 +9,11 @@
 // most per tile). An item's keys are cut into tiles of `kt` keys; with drafts,
 // the last tile holds the drafts alone.
 //
+// Window (WIN). A row that sees the keys below `seen` looks only at those from
+// seen - window on and at the first `sinks`. An item's tiles are then those of the sinks
+// and those from its first row's window on; the ones between are left out, and all
+// below counts tiles without them (`Span` knows which tile of the sequence each one is).
+//
 // Split. All items, in order, form one line of weighted work (their visible
 // keys plus a fixed share for an item's start and end); CTA c takes the part
 // [U c / C, U (c + 1) / C) of it, cut at key tiles. So every CTA has the same
@@ -122,6 +127,7 @@ struct Args {
     int block_shift;
     float inv_block, inv_min_part;
     float scale;
+    int window, sinks;       // WIN; window = 0: none
     // device pointers
     const int32_t *cu_q, *cu_k;      // prefill offsets (NULL: equal lengths)
     const int32_t *table, *lens;     // decode
@@ -141,6 +147,12 @@ inline void set_unit(Args &a, double keys) {
     a.unit = 1.f;
     while (keys / a.unit > 5e8) a.unit *= 2.f;
     a.inv_unit = 1.f / a.unit;
+}
+
+// An upper bound of an item's keys through a window of tiles of kt keys (`keys`: without it).
+inline long long window_keys(const Args &a, long long keys, int kt) {
+    const long long most = (long long)a.window + a.sinks + a.block + 3 * kt;
+    return keys < most ? keys : most;
 }
 
 // What divides by tile_tokens * streams. The search for a CTA's work is a chain of
@@ -243,6 +255,28 @@ template <bool PAGED, int KT>
 __device__ __forceinline__ int item_tiles(const Args &a, const Seq &s, int i) {
     return (int)(((unsigned)item_keys<PAGED>(a, s, i) + KT - 1) / KT) + (PAGED ? a.has_new : 0);
 }
+// Which tiles of its sequence an item has: the first `sinks` of them, none of the next
+// `skip`, the others; nt in all (with the drafts').
+struct Span {
+    int sinks, skip, nt;
+    __device__ __forceinline__ int tile(int t) const { return t < sinks ? t : t + skip; }
+};
+// The first key that a row's window holds if the row sees `seen` keys.
+__device__ __forceinline__ int window_start(const Args &a, int seen) { return seen > a.window ? seen - a.window : 0; }
+template <bool PAGED, int KT, bool WIN>
+__device__ __forceinline__ Span item_span(const Args &a, const Seq &s, int i) {
+    Span r = {0, 0, item_tiles<PAGED, KT>(a, s, i)};
+    if (WIN) {  // (decode: the first of a chain, or any of a tree, may see one new token, itself)
+        const int lo = window_start(a, PAGED ? s.Lk + a.has_new : s.Lk - s.Lq + i * a.block + 1) / KT;
+        const int sinks = (int)(((unsigned)a.sinks + KT - 1) / KT);
+        if (sinks < lo) {
+            r.sinks = sinks;
+            r.skip = lo - sinks;
+            r.nt -= r.skip;
+        }
+    }
+    return r;
+}
 // An item's start and end, in keys. (Decode: an item of few tiles is a chain of
 // latencies, one of many is bound by its loads.)
 template <bool PAGED, int KT>
@@ -254,20 +288,27 @@ __device__ __forceinline__ int item_extra(const Args &a, int nt) {
 // call's total stays below 2^30, and one unit per item, so that no item weighs
 // nothing. Formed in fp32: every operation rounds monotonically, so the weights rise
 // with i, and all that follows is in whole units.
-template <bool PAGED, int KT>
+// A window bounds the items' keys by those of a whole window, its block and the sinks.
+template <bool PAGED, int KT, bool WIN>
 __device__ __forceinline__ uint32_t items_weight(const Args &a, const Seq &s, int i) {
     float w;
     if (PAGED) {
-        const int nt = item_tiles<PAGED, KT>(a, s, 0);
+        const int nt = item_span<PAGED, KT, WIN>(a, s, 0).nt;
         w = (float)i * (float)(item_extra<PAGED, KT>(a, nt) + nt * KT);
     } else {
         const int d = s.Lk - s.Lq, full = i < s.ni ? i : s.ni - 1;  // items without the sequence's last token
         const float block = (float)a.block;
         const float unseen = fmaxf(0.f, floorf((float)-d * a.inv_block));  // items that see nothing
-        const float count = fmaxf(0.f, (float)full - unseen);
-        // the last rows of items `unseen` .. full - 1 see d + block (unseen + 1) .. keys
-        w = (float)i * (float)a.extra + count * fmaf(0.5f * block, (float)full + unseen + 1.f, (float)d);
-        if (i >= s.ni) w += (float)s.Lk;
+        float last = (float)full, most = 0.f;
+        if (WIN) {  // items from `last` on have `most` keys
+            most = (float)a.window + block + (float)(((unsigned)a.sinks + KT - 1) / KT * KT);
+            last = fminf(last, fmaxf(unseen, floorf((most - (float)d) * a.inv_block)));
+        }
+        const float count = fmaxf(0.f, last - unseen);
+        // the last rows of items `unseen` .. last - 1 see d + block (unseen + 1) .. keys
+        w = (float)i * (float)a.extra + count * fmaf(0.5f * block, last + unseen + 1.f, (float)d);
+        if (WIN) w += ((float)full - last) * most;
+        if (i >= s.ni) w += WIN ? fminf((float)s.Lk, most) : (float)s.Lk;
     }
     return (uint32_t)(fmaxf(w, 0.f) * a.inv_unit) + (uint32_t)i;
 }
@@ -282,7 +323,7 @@ __device__ __forceinline__ bool same_item(const Point &x, const Point &y) {
 
 // The point at distance x into sequence n (of this weight per head, x below all heads');
 // a converged warp with the same arguments in all lanes.
-template <bool PAGED, int KT>
+template <bool PAGED, int KT, bool WIN>
 __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n, uint32_t per_head, uint32_t x) {
     const int lane = threadIdx.x & 31;
     Point p;
@@ -291,14 +332,14 @@ __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n
     int lo = 0, count = s.ni;  // the last item that starts at or before x is in [lo, lo + count)
     while (count > 1) {
         const int step = (count + 31) >> 5, at = lo + lane * step;
-        const bool before = lane * step < count && items_weight<PAGED, KT>(a, s, at) <= x;
+        const bool before = lane * step < count && items_weight<PAGED, KT, WIN>(a, s, at) <= x;
         const int k = 31 - __clz(__ballot_sync(0xffffffffu, before));  // (lane 0 always is)
         count = min(step, count - k * step);
         lo += k * step;
     }
     p.i = lo;
-    const int nt = item_tiles<PAGED, KT>(a, s, lo);
-    const float y = (float)(x - items_weight<PAGED, KT>(a, s, lo)) * a.unit - 0.5f * (float)item_extra<PAGED, KT>(a, nt);
+    const int nt = item_span<PAGED, KT, WIN>(a, s, lo).nt;
+    const float y = (float)(x - items_weight<PAGED, KT, WIN>(a, s, lo)) * a.unit - 0.5f * (float)item_extra<PAGED, KT>(a, nt);
     const int t = (int)fminf(fmaxf(0.f, y * (1.f / KT) + 0.5f), (float)nt);
     // short pieces are not worth their join: such a cut moves to the item's edge
     p.tile = t < a.cut ? 0 : (t > nt - a.cut ? nt : t);
@@ -312,7 +353,7 @@ __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n
 // before everything else that a CTA does, from a cold instruction cache: short code
 // counts more than few operations. A kernel calls it in one place, inlined, so that the
 // arguments are read from the constant bank.)
-template <bool PAGED, int KT>
+template <bool PAGED, int KT, bool WIN>
 __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq &s0) {
     const int lane = threadIdx.x & 31;
     constexpr int kFlight = PAGED ? 4 : 1;  // groups of 32 sequences whose loads are in flight together
@@ -326,7 +367,7 @@ __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq
             w[u] = 0;
             if (n < a.N) {
                 ok = load_seq<PAGED>(a, n, s) && ok;
-                if (s.ni > 0) w[u] = items_weight<PAGED, KT>(a, s, s.ni);
+                if (s.ni > 0) w[u] = items_weight<PAGED, KT, WIN>(a, s, s.ni);
             }
         }
         return ok;
@@ -381,7 +422,7 @@ __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq
         }
     }
     load_seq<PAGED>(a, p0.n, s0);
-    p0 = point_in_seq<PAGED, KT>(a, s0, p0.n, per_head, x);
+    p0 = point_in_seq<PAGED, KT, WIN>(a, s0, p0.n, per_head, x);
     return true;
 }
 
@@ -389,14 +430,18 @@ __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq
 struct Part {
     int n, h, i;
     int ta, tb, nt;   // tiles of this part, tiles of the item
+    int sinks, skip;  // WIN: of the item's Span
     int q0, tokens;   // first token row, valid tokens of the item
     int first_tok;    // the item's first token within its sequence
     int Lq, Lk, k0;
     __device__ __forceinline__ bool whole() const { return ta == 0 && tb == nt; }
 };
-template <bool PAGED, int KT>
+template <bool PAGED, int KT, bool WIN>
 __device__ __forceinline__ void item_part(const Args &a, const Seq &s, Part &p) {
-    p.nt = item_tiles<PAGED, KT>(a, s, p.i);
+    const Span span = item_span<PAGED, KT, WIN>(a, s, p.i);
+    p.nt = span.nt;
+    p.sinks = span.sinks;
+    p.skip = span.skip;
     p.first_tok = p.i * a.block;
     p.q0 = s.q0 + p.first_tok;
     p.tokens = min(a.block, s.Lq - p.first_tok);
@@ -408,7 +453,7 @@ __device__ __forceinline__ void item_part(const Args &a, const Seq &s, Part &p) 
 // `direct`: the item of slot x, whole. A head's slots: those of sequence n start at
 // (its first token) / block + n, which leaves each sequence at least as many slots
 // as it has items. A converged warp. False: an empty slot or malformed offsets.
-template <bool PAGED, int KT>
+template <bool PAGED, int KT, bool WIN>
 __device__ __forceinline__ bool direct_part(const Args &a, int x, Part &p) {
     const int lane = threadIdx.x & 31;
     Seq s;
@@ -450,14 +495,14 @@ __device__ __forceinline__ bool direct_part(const Args &a, int x, Part &p) {
         return false;
     }
     if (p.n < 0 || p.i >= s.ni) return false;
-    item_part<PAGED, KT>(a, s, p);
+    item_part<PAGED, KT, WIN>(a, s, p);
     p.ta = 0;
     p.tb = p.nt;
     return true;
 }
 
 // Walks the parts of [at, end).
-template <bool PAGED, int KT>
+template <bool PAGED, int KT, bool WIN>
 struct Walk {
     Point at, end;
     Seq s;
@@ -483,7 +528,7 @@ struct Walk {
             p.n = at.n;
             p.h = at.h;
             p.i = at.i;
-            item_part<PAGED, KT>(a, s, p);
+            item_part<PAGED, KT, WIN>(a, s, p);
             p.ta = at.tile;
             p.tb = same_item(at, end) ? end.tile : p.nt;
             if (same_item(at, end)) {

@@ -117,6 +117,11 @@ bool ld_ok(int64_t ld, int32_t heads, int32_t io) {
     return ld >= (int64_t)heads * kda::kD && ld % (io == KDA_BF16 ? 8 : 4) == 0 && ld < (1LL << 36);
 }
 bool scale_ok(float s) { return isfinite(s) && s > 0.f; }
+// What a row sees of the keys before it: all of them, or a window's and the first `sinks`.
+struct Window {
+    int32_t keys = 0, sinks = 0;  // keys = 0: all
+    bool ok() const { return keys >= 1 && sinks >= 0; }
+};
 // A warp of the bf16 kernel that gives up at one of its waits (tests).
 struct Lose {
     int32_t warp = -1, at = 0;
@@ -126,7 +131,7 @@ struct Lose {
 int prefill_impl(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
                  const int32_t *cu_q, const int32_t *cu_k, int32_t N, int32_t Tq, int32_t Tk, int32_t Hq,
                  int32_t Hkv, int32_t D, int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes,
-                 const Lose &lose, void *stream) {
+                 const Window &window, const Lose &lose, void *stream) {
     const int rc = check_heads(Hq, Hkv, D, io);
     if (rc != KDA_OK) return rc;
     if (N < 0 || Tq < 0 || Tk < 0 || !scale_ok(scale)) return KDA_ERR_INVALID_ARG;
@@ -161,6 +166,8 @@ int prefill_impl(const void *q, const void *k, const void *v, int64_t ldq, int64
     a.Tq_total = (int)tq;
     a.Tk_total = (int)tk;
     a.scale = scale;
+    a.window = window.keys;
+    a.sinks = window.sinks;
     a.cu_q = cu_q;
     a.cu_k = cu_k;
     a.out = out;
@@ -178,8 +185,8 @@ int decode_impl(const void *q, int64_t ldq, const void *k_new, const void *v_new
                 const void *k_pages, const void *v_pages, int32_t num_pages, int32_t page_size,
                 const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
                 const uint64_t *tree_mask, float scale, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
-                int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes, const Lose &lose,
-                void *stream) {
+                int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes, const Window &window,
+                const Lose &lose, void *stream) {
     const int rc = check_heads(Hq, Hkv, D, io);
     if (rc != KDA_OK) return rc;
     if (B < 0 || T < 0 || num_pages < 0 || table_cols < 0 || table_ld < table_cols || !scale_ok(scale))
@@ -217,6 +224,8 @@ int decode_impl(const void *q, int64_t ldq, const void *k_new, const void *v_new
     a.table_ld = table_ld;
     a.has_new = k_new != nullptr;
     a.scale = scale;
+    a.window = window.keys;
+    a.sinks = window.sinks;
     a.table = block_table;
     a.lens = seq_lens;
     a.mask = reinterpret_cast<const unsigned long long *>(tree_mask);
@@ -247,7 +256,17 @@ int kda_attn_prefill(const void *q, const void *k, const void *v, int64_t ldq, i
                      int32_t Hkv, int32_t D, int32_t io, void *out, float *lse, void *workspace,
                      size_t workspace_bytes, void *stream) {
     return prefill_impl(q, k, v, ldq, ldk, ldv, scale, cu_q, cu_k, N, Tq, Tk, Hq, Hkv, D, io, out, lse, workspace,
-                        workspace_bytes, Lose(), stream);
+                        workspace_bytes, Window(), Lose(), stream);
+}
+
+int kda_attn_prefill_window(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv,
+                            float scale, int32_t window, int32_t sinks, const int32_t *cu_q, const int32_t *cu_k, int32_t N,
+                            int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv, int32_t D, int32_t io, void *out, float *lse,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    const Window w = {window, sinks};
+    if (!w.ok()) return KDA_ERR_INVALID_ARG;
+    return prefill_impl(q, k, v, ldq, ldk, ldv, scale, cu_q, cu_k, N, Tq, Tk, Hq, Hkv, D, io, out, lse, workspace,
+                        workspace_bytes, w, Lose(), stream);
 }
 
 int kda_testing_attn_prefill_timeout(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv,
@@ -257,7 +276,7 @@ int kda_testing_attn_prefill_timeout(const void *q, const void *k, const void *v
     const Lose lose = {warp, at};
     if (!lose.ok(io)) return KDA_ERR_INVALID_ARG;
     return prefill_impl(q, k, v, ldq, ldk, ldv, scale, cu_q, cu_k, N, Tq, Tk, Hq, Hkv, D, io, out, lse, workspace,
-                        workspace_bytes, lose, stream);
+                        workspace_bytes, Window(), lose, stream);
 }
 
 size_t kda_attn_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
@@ -275,7 +294,20 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
                     int32_t io, void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
     return decode_impl(q, ldq, k_new, v_new, ldk, ldv, k_pages, v_pages, num_pages, page_size, block_table, table_ld,
                        table_cols, seq_lens, tree_mask, scale, B, T, Hq, Hkv, D, io, out, lse, workspace,
-                       workspace_bytes, Lose(), stream);
+                       workspace_bytes, Window(), Lose(), stream);
+}
+
+int kda_attn_decode_window(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk, int64_t ldv,
+                           const void *k_pages, const void *v_pages, int32_t num_pages, int32_t page_size,
+                           const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
+                           const uint64_t *tree_mask, float scale, int32_t window, int32_t sinks, int32_t B, int32_t T,
+                           int32_t Hq, int32_t Hkv, int32_t D, int32_t io, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+    const Window w = {window, sinks};
+    if (!w.ok() || (k_new != nullptr && window < T)) return KDA_ERR_INVALID_ARG;
+    return decode_impl(q, ldq, k_new, v_new, ldk, ldv, k_pages, v_pages, num_pages, page_size, block_table, table_ld,
+                       table_cols, seq_lens, tree_mask, scale, B, T, Hq, Hkv, D, io, out, lse, workspace,
+                       workspace_bytes, w, Lose(), stream);
 }
 
 int kda_testing_attn_decode_timeout(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk,
@@ -288,7 +320,7 @@ int kda_testing_attn_decode_timeout(const void *q, int64_t ldq, const void *k_ne
     if (!lose.ok(io)) return KDA_ERR_INVALID_ARG;
     return decode_impl(q, ldq, k_new, v_new, ldk, ldv, k_pages, v_pages, num_pages, page_size, block_table, table_ld,
                        table_cols, seq_lens, tree_mask, scale, B, T, Hq, Hkv, D, io, out, lse, workspace,
-                       workspace_bytes, lose, stream);
+                       workspace_bytes, Window(), lose, stream);
 }
 
 // Scratch of the calls that choose pages: the free pages' list and a state per

@@ -39,7 +39,7 @@ struct F32Ptrs {
     long long ldq, ldk, ldv;           // decode: of kn, vn
 };
 
-template <bool PAGED, int RPT>
+template <bool PAGED, int RPT, bool WIN>
 __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_constant__ Args a, const F32Ptrs io) {
     extern __shared__ __align__(16) float smf[];
     constexpr int kRows = 8 * RPT;
@@ -57,8 +57,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
         Seq s0;
         Part p;
         bool ok = false;
-        if (!a.direct) ok = split_point<PAGED, kF32Tile>(a, cta + w, pt, s0) && (w != 0 || pt.n < a.N);
-        else if (w == 0) ok = direct_part<PAGED, kF32Tile>(a, cta, p);
+        if (!a.direct) ok = split_point<PAGED, kF32Tile, WIN>(a, cta + w, pt, s0) && (w != 0 || pt.n < a.N);
+        else if (w == 0) ok = direct_part<PAGED, kF32Tile, WIN>(a, cta, p);
         if ((tid & 31) == 0) {
             pts[w] = pt;
             if (w == 0) {
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
     }
     __syncthreads();
     if (!any) return;
-    Walk<PAGED, kF32Tile> walk;
+    Walk<PAGED, kF32Tile, WIN> walk;
     if (!a.direct) walk.init(pts[0], pts[1], seq0);
     const int ty = tid >> 4, tx = tid & 15, lane = tid & 31, warp = tid >> 5;  // rows RPT ty + i; keys tx + 16 e, channels 4 tx + 64 e
     const float c = a.scale * kLog2e;
@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
         float4 o[RPT][2];
         int seen[RPT];  // keys that the row sees (of the cache: all)
         unsigned long long bits[RPT];
+        int from[RPT];  // WIN: the first key of the row's window
 #pragma unroll
         for (int i = 0; i < RPT; ++i) {
             m[i] = -INFINITY;
@@ -107,7 +108,11 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
                                             : (t >= 63 ? ~0ull : (2ull << t) - 1);
                 if (a.T < 64) bits[i] &= (1ull << a.T) - 1;
             }
+            if (WIN) from[i] = window_start(a, PAGED && a.has_new ? p.Lk + max(1, __popcll(bits[i])) : seen[i]);
         }
+        const Span span = {p.sinks, p.skip, p.nt};
+        // the first key of all rows' windows: those before it, the sinks apart, are not read
+        const int first = WIN ? window_start(a, PAGED ? p.Lk + a.has_new : p.Lk - p.Lq + p.first_tok + 1) : 0;
         // A warp copies the rows warp, warp + 4, ..: lane i knows where row warp + 4 i is.
         struct Where {
             long long k, v;
@@ -115,11 +120,13 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             bool drafts;
         };
         const int mine = warp + 4 * (lane & 15);
-        auto locate = [&](int t) {
-            Where w = {0, 0, 0, PAGED && a.has_new && t == p.nt - 1};
+        auto locate = [&](int vt) {
+            Where w = {0, 0, 0, PAGED && a.has_new && vt == p.nt - 1};
+            const int t = WIN ? span.tile(vt) : vt;
             // keys past the end load as zeros (0 times what is there could be NaN)
             const int valid = w.drafts ? a.T : min(kF32Tile, p.Lk - t * kF32Tile);
             bool ok = mine < valid;
+            if (WIN && !w.drafts) ok = ok && (t * kF32Tile + mine >= first || t * kF32Tile + mine < a.sinks);
             if (!PAGED) {
                 w.k = (long long)(p.k0 + t * kF32Tile + mine) * io.ldk;
                 w.v = (long long)(p.k0 + t * kF32Tile + mine) * io.ldv;
@@ -193,7 +200,9 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = tx + 16 * e;
-                    const bool see = drafts ? (bits[i] >> key & 1) != 0 : seen[i] > t * kF32Tile + key;
+                    const int pos = (WIN ? span.tile(t) : t) * kF32Tile + key;
+                    bool see = drafts ? (bits[i] >> key & 1) != 0 : seen[i] > pos;
+                    if (WIN && !drafts) see = see && (pos >= from[i] || pos < a.sinks);
                     if (!see) s[i][e] = -INFINITY;
                     top = fmaxf(top, s[i][e]);
                 }
@@ -286,8 +295,8 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
 
 cudaError_t launch_attn_combine(const Args &a, bool bf16, bool joins_early, cudaStream_t stream);
 
-template <bool PAGED, int RPT>
-static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
+template <bool PAGED, int RPT, bool WIN>
+static cudaError_t launch_form(Args a, const F32Ptrs &io, cudaStream_t stream) {
     constexpr int rows = 8 * RPT;
     a.streams = 1;
     a.tile_tokens = PAGED && a.T * a.G < rows ? a.T : rows / a.G;
@@ -298,16 +307,22 @@ static cudaError_t launch_f32(Args a, const F32Ptrs &io, cudaStream_t stream) {
     a.cut = 1;
     const long long slots = PAGED ? (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens)
                                   : ((long long)a.Tq_total / a.tile_tokens + a.N) * a.Hkv;
-    const long long keys = PAGED ? (long long)a.table_cols * a.page + kF32Tile : a.Tk;
+    long long keys = PAGED ? (long long)a.table_cols * a.page + kF32Tile : a.Tk;
+    if (WIN) keys = window_keys(a, keys, kF32Tile);
     set_unit(a, (double)slots * ((double)keys + a.extra + kF32Tile));
     // (a CTA each for four prompts of 25 tokens: 14.3 us instead of 35.6)
     a.direct = slots <= 2 * a.sms && keys <= 2 * kF32Tile;
-    cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED, RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED, RPT, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          f32_smem(RPT));
     if (e != cudaSuccess) return e;
-    e = launch_early(attn_f32_kernel<PAGED, RPT>, dim3(a.direct ? (unsigned)slots : (unsigned)a.ctas), kF32Threads,
+    e = launch_early(attn_f32_kernel<PAGED, RPT, WIN>, dim3(a.direct ? (unsigned)slots : (unsigned)a.ctas), kF32Threads,
                      f32_smem(RPT), stream, a, io);
     return e == cudaSuccess && !a.direct ? launch_attn_combine(a, false, false, stream) : e;
+}
+
+template <bool PAGED, int RPT>
+static cudaError_t launch_f32(const Args &a, const F32Ptrs &io, cudaStream_t stream) {
+    return a.window > 0 ? launch_form<PAGED, RPT, true>(a, io, stream) : launch_form<PAGED, RPT, false>(a, io, stream);
 }
 
 cudaError_t launch_attn_prefill_f32(const Args &a, const void *q, const void *k, const void *v, long long ldq,

@@ -82,6 +82,7 @@ struct Desc {
     int count[2];          // key tiles of each stream
     int start[2];          // its first tile (DUAL: every second from there)
     int tokens[2];         // valid tokens of its row tile
+    int sinks, skip;       // WIN: the item's Span
 };
 
 // Shared memory: two Q tiles of RT rows, 32 KB for the way out (DUAL: the box for the
@@ -229,7 +230,7 @@ __device__ __forceinline__ void join4(uint32_t *z, float f, float4 y, float g) {
 struct Run {
     int q, tiles;
 };
-template <bool PAGED, bool DUAL>
+template <bool PAGED, bool DUAL, bool WIN>
 __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, Run &run, Desc &d) {
     d.last = 0;
     d.n = p.n;
@@ -245,6 +246,10 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
     d.open = p.tb < p.nt;
     d.writer = DUAL ? run.tiles & 1 : 0;
     d.seen = PAGED ? p.Lk : p.Lk - p.Lq + p.first_tok + 1;
+    if (WIN) {
+        d.sinks = p.sinks;
+        d.skip = p.skip;
+    }
     if (DUAL) {  // tiles alternate between the streams, across parts too
         const int tiles = p.tb - p.ta;
 #pragma unroll
@@ -265,7 +270,8 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
             int end = p.tb;
             if (!PAGED) {  // the keys that the row tile's last token sees
                 const int seen = d.seen + s * a.tile_tokens + tokens - 1;
-                const int nt = seen <= 0 ? 0 : (int)(((unsigned)seen + kTile - 1) / kTile);
+                int nt = seen <= 0 ? 0 : (int)(((unsigned)seen + kTile - 1) / kTile);
+                if (WIN) nt = nt > p.sinks + p.skip ? nt - p.skip : min(nt, p.sinks);
                 end = end < nt ? end : nt;
             }
             d.tokens[s] = tokens;
@@ -281,7 +287,7 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
 // follow as theirs run out or they see kDead, and the status tells; the copies and products
 // in flight are waited for first. TEST (kda_testing_attn_*): waits of 20 ms, and warp
 // a.lose - 1 gives up at its wait number a.lose_at.
-template <bool PAGED, bool DUAL, int RT, bool TEST>
+template <bool PAGED, bool DUAL, int RT, bool WIN, bool TEST>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     using L = Smem<DUAL, RT>;
@@ -303,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int end = warp == kWarpFix;
         wait_before();
         if (!a.direct) {
-            any = split_point<PAGED, kTile>(a, cta + end, p0, s0) && p0.n < a.N;
+            any = split_point<PAGED, kTile, WIN>(a, cta + end, p0, s0) && p0.n < a.N;
             if (end && lane == 0) {
                 *reinterpret_cast<Point *>(sm + L::kBars + Bars::kEnd) = p0;
                 part_header(a, 2 * cta)->valid = 0;
@@ -414,11 +420,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = d->first_tok + (DUAL ? 0 : s * a.tile_tokens) + tok;
                 bits = a.mask != nullptr ? a.mask[(size_t)d->n * a.T + t]
                                          : (t >= 63 ? ~0ull : (2ull << t) - 1);
+                if (WIN && a.T < 64) bits &= (1ull << a.T) - 1;
             }
             // keys that the row tile's first row and this row see
             const int seen0 = d->seen + (PAGED ? 0 : s * a.tile_tokens);
             const int seen = PAGED ? seen0 : seen0 + tok;
             const int draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
+            // WIN: where this row's window starts, and where the last one of the row tile does (decode: at most)
+            const Span span = {WIN ? d->sinks : 0, WIN ? d->skip : 0, 0};
+            const int from = WIN ? window_start(a, PAGED && a.has_new ? seen + max(1, __popcll(bits)) : seen) : 0;
+            const int from_last = WIN ? window_start(a, seen0 + (PAGED ? a.has_new * a.T : d->tokens[s] - 1)) : 0;
             int t = d->start[s];
             for (int j = 0; j < steps; ++j, t += DUAL ? 2 : 1) {
                 if (!warp_wait(bars.sfull(s), ns++ & 1)) {
@@ -430,13 +441,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t x[8][16];
                     tc::tmem_ld_cols<8>(tS, x);
                     const bool drafts = PAGED && t == draft_tile;
-                    if (drafts || seen0 < (t + 1) * kTile) {
+                    const int t0 = (WIN ? span.tile(t) : t) * kTile;  // the tile's first key
+                    if (drafts || seen0 < t0 + kTile || (WIN && from_last > t0 && a.sinks - kTile < t0)) {
                         // the keys that this row sees, a bit each
                         if (PAGED && drafts && a.T < 64) bits &= (1ull << a.T) - 1;
-                        const int lim = seen - t * kTile;
+                        const int lim = seen - t0;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            uint32_t see = lim >= 32 * i + 32 ? ~0u : (lim <= 32 * i ? 0u : (1u << (lim & 31)) - 1);
+                            auto below = [&](int n) { return n >= 32 * i + 32 ? ~0u : (n <= 32 * i ? 0u : (1u << (n & 31)) - 1); };
+                            uint32_t see = below(lim);
+                            if (WIN) see &= ~below(from - t0) | below(a.sinks - t0);
                             if (PAGED && drafts) see = i == 0 ? (uint32_t)bits : (i == 1 ? (uint32_t)(bits >> 32) : 0u);
 #pragma unroll
                             for (int e = 0; e < 32; ++e)
@@ -727,8 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kWarpSched) {
             // ---- scheduler warp: walks the CTA's parts ahead of the others ------------
             Part p;
-            bool more = a.direct ? direct_part<PAGED, kTile>(a, cta, p) : any;
-            Walk<PAGED, kTile> walk;
+            bool more = a.direct ? direct_part<PAGED, kTile, WIN>(a, cta, p) : any;
+            Walk<PAGED, kTile, WIN> walk;
             if (more && !a.direct) {
                 walk.init(p0, *reinterpret_cast<const Point *>(sm + L::kBars + Bars::kEnd), s0);
                 more = walk.next(a, p);
@@ -751,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int k = 0; k < 2; ++k) {
                         if ((k == 0) != open) {
-                            if (more) describe<PAGED, DUAL>(a, p, cta, run, *d);
+                            if (more) describe<PAGED, DUAL, WIN>(a, p, cta, run, *d);
                             else d->last = 1;
                             mbar_arrive(bars.dfull(nd % kDescs));
                         } else if (more && !p.whole()) {
@@ -779,6 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr int kLag = DUAL ? 2 : 1;
             struct Load {
                 int n, h, k0, Lk, t, draft, pg;
+                Span span;
             };
             uint32_t kv = 0, jobs = 0, g = 0;
             uint32_t sent = 0;  // bit i: the parity of Q slot i's copies
@@ -787,9 +802,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row_bits = 31 - __clz(rows), page_bits = 31 - __clz(a.page);
             const uint32_t lead = tc::elect_one();
             // decode: the page of this lane's copy of tile t
-            auto page_of = [&](int n, int Lk, int t) -> int {
-                const int pos = t * kTile + (lane << row_bits);
+            // (kNoPage: WIN: one that no row sees, of which nothing is read, its number neither)
+            constexpr int kNoPage = -2;
+            auto page_of = [&](const Span &span, int n, int Lk, int t) -> int {
+                const int pos = (WIN ? span.tile(t) : t) * kTile + (lane << row_bits);
                 if (!PAGED || (lane << row_bits) >= kTile || pos >= Lk) return -1;
+                if (WIN && pos >= a.sinks && pos + rows <= window_start(a, Lk + a.has_new)) return kNoPage;
                 return __ldg(a.table + (size_t)n * a.table_ld + (pos >> page_bits));
             };
             auto load = [&](const Load x, bool is_v) {
@@ -801,7 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++kv;
                 // rows of this tile that are the sequence's own
-                const int left = x.draft ? a.T : x.Lk - x.t * kTile, valid = left < kTile ? left : kTile;
+                const int t0 = (WIN ? x.span.tile(x.t) : x.t) * kTile;
+                const int left = x.draft ? a.T : x.Lk - t0, valid = left < kTile ? left : kTile;
                 // rows past the end hold other sequences' values or nothing at all:
                 // P is 0 there, but 0 times a NaN is not, so V gets zeros
                 const bool fix = is_v && valid < kTile;
@@ -809,8 +828,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const CUtensorMap *m = is_v ? &maps.v : &maps.k;
                 if (!PAGED) {
                     expect_tx(lead, bar, kTileBytes);
-                    tma_3d(lead, dst, m, 0, x.h, x.k0 + x.t * kTile, bar);
-                    tma_3d(lead, dst + kHalf, m, 64, x.h, x.k0 + x.t * kTile, bar);
+                    tma_3d(lead, dst, m, 0, x.h, x.k0 + t0, bar);
+                    tma_3d(lead, dst + kHalf, m, 64, x.h, x.k0 + t0, bar);
                 } else if (x.draft) {
                     const CUtensorMap *mn = is_v ? &maps.vn : &maps.kn;
                     expect_tx(lead, bar, (uint32_t)((a.T + 7) & ~7) * 256u);
@@ -821,8 +840,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     expect_tx(lead, bar, (uint32_t)(copies << row_bits) * 256u);
                     int row = max(a.pages * a.Hkv * a.page, 1);  // past the map's last row (an empty pool's has one): zeros
                     if (x.pg >= 0 && x.pg < a.pages)
-                        row = (x.pg * a.Hkv + x.h) * a.page + ((x.t * kTile + (lane << row_bits)) & (a.page - 1));
-                    else if (lane < copies)
+                        row = (x.pg * a.Hkv + x.h) * a.page + ((t0 + (lane << row_bits)) & (a.page - 1));
+                    else if (lane < copies && !(WIN && x.pg == kNoPage))
                         atomicOr(status_word(a), kStatusBadSeqlens);
                     for (int i = 0; i < copies; ++i) {
                         const int ri = __shfl_sync(0xffffffffu, row, i);
@@ -875,13 +894,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x.k0 = d->k0;
                     x.Lk = d->Lk;
                     x.t = d->ta - 1;
+                    if (WIN) x.span = {d->sinks, d->skip, 0};
                     draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
                     q_first = 1;
                     next_pg = peek_pg;
                     next_pg2 = peek_pg2;
                     if (PAGED && peeked != nd + 1) {
-                        next_pg = page_of(x.n, x.Lk, d->ta);
-                        next_pg2 = page_of(x.n, x.Lk, d->ta + 1);
+                        next_pg = page_of(x.span, x.n, x.Lk, d->ta);
+                        next_pg2 = page_of(x.span, x.n, x.Lk, d->ta + 1);
                     }
                 }
                 if (!alive || (left == 0 && flush-- == 0)) break;
@@ -891,13 +911,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x.draft = PAGED && x.t == draft_tile;
                     x.pg = next_pg;  // looked up two tiles ahead
                     next_pg = next_pg2;
-                    next_pg2 = page_of(x.n, x.Lk, x.t + 2);
+                    next_pg2 = page_of(x.span, x.n, x.Lk, x.t + 2);
                     if (PAGED && left == 1 &&
                         __all_sync(0xffffffffu, mbar_test(bars.dfull((nd + 1) % kDescs), ((nd + 1) / kDescs) & 1))) {
                         const Desc *e = descs + (nd + 1) % kDescs;
                         if (!e->last) {
-                            peek_pg = page_of(e->n, e->Lk, e->ta);
-                            peek_pg2 = page_of(e->n, e->Lk, e->ta + 1);
+                            const Span span = {WIN ? e->sinks : 0, WIN ? e->skip : 0, 0};
+                            peek_pg = page_of(span, e->n, e->Lk, e->ta);
+                            peek_pg2 = page_of(span, e->n, e->Lk, e->ta + 1);
                             peeked = nd + 2;
                         }
                     }
@@ -1122,7 +1143,7 @@ bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-template <bool PAGED, bool DUAL, int RT, bool TEST>
+template <bool PAGED, bool DUAL, int RT, bool WIN, bool TEST>
 cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
     a.streams = DUAL ? 1 : 2;
     // An item's start and end cost about as much as 1.2 key tiles of 256 rows, and a tile that is
@@ -1135,6 +1156,7 @@ cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long ke
     a.extra_short = PAGED ? 512 : 0;
     a.min_part = kMinPart;
     set_block(a);
+    if (WIN) keys = window_keys(a, keys, kTile);
     // every item's keys, its start and end and, at the most, its drafts' tile
     set_unit(a, (double)slots * ((double)keys + 512 + kTile));
     a.cut = 2;
@@ -1146,18 +1168,19 @@ cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long ke
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        e = cudaFuncSetAttribute(attn_tc_kernel<PAGED, DUAL, RT, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(attn_tc_kernel<PAGED, DUAL, RT, WIN, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    e = launch_early(attn_tc_kernel<PAGED, DUAL, RT, TEST>, dim3(a.direct ? (unsigned)slots : (unsigned)a.ctas), kThreads,
+    e = launch_early(attn_tc_kernel<PAGED, DUAL, RT, WIN, TEST>, dim3(a.direct ? (unsigned)slots : (unsigned)a.ctas), kThreads,
                      bytes, stream, a, maps);
     return e == cudaSuccess && !a.direct ? launch_attn_combine(a, true, !DUAL, stream) : e;
 }
 template <bool PAGED, bool DUAL, int RT>
 cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
-    return a.lose > 0 ? launch_form<PAGED, DUAL, RT, true>(a, maps, slots, keys, stream)
-                      : launch_form<PAGED, DUAL, RT, false>(a, maps, slots, keys, stream);
+    if (a.window > 0) return launch_form<PAGED, DUAL, RT, true, false>(a, maps, slots, keys, stream);
+    return a.lose > 0 ? launch_form<PAGED, DUAL, RT, false, true>(a, maps, slots, keys, stream)
+                      : launch_form<PAGED, DUAL, RT, false, false>(a, maps, slots, keys, stream);
 }
 }  // namespace
 

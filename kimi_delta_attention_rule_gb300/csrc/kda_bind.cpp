@@ -31,6 +31,8 @@ struct Entry {
     decltype(&kda_cache_compact) cache_compact;
     decltype(&kda_cache_copy) cache_copy;
     decltype(&kda_cache_append) cache_append;
+    decltype(&kda_attn_prefill_window) attn_prefill_window;
+    decltype(&kda_attn_decode_window) attn_decode_window;
 } kda_c;
 PyObject *error_class = nullptr;  // KDAError(code, what)
 
@@ -234,10 +236,8 @@ PyObject *pair(Out &a, Out &b) {
         return nullptr; \
     }
 
-// (q, k, v, scale, cu_seqlens, cu_seqlens_k, N, out, lse, output_lse, workspace, stream)
-PyObject *attn_prefill(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
-    HANDLE_TH_ERRORS
-    ARGS(12)
+// x: (q, k, v, scale, cu_seqlens, cu_seqlens_k, N, out, lse, output_lse, workspace, stream[, window, sinks])
+PyObject *prefill_call(PyObject *const *x, bool windowed) {
     const at::Tensor &q = tensor("q", x[0]), &k = tensor("k", x[1]), &v = tensor("v", x[2]);
     const int dev = cuda_index(q);
     const Place place(x[11], dev);
@@ -269,19 +269,32 @@ PyObject *attn_prefill(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     else lse.none();
     const Space ws = workspace(x[10], q, dev, [&] { return kda_c.attn_prefill_workspace_size(N, Tq, Tk, Hq, Hkv, D, io); });
     const float scale = f32(x[3]);
+    const int32_t window = windowed ? i32("window", x[12]) : 0, sinks = windowed ? i32("sinks", x[13]) : 0;
+    float *const l = static_cast<float *>(lse.p);
     const int rc = call([&] {
-        return kda_c.attn_prefill(rq.p, rk.p, rv.p, rq.ld, rk.ld, rv.ld, scale, cu, cuk, N, nq, nk, Hq, Hkv, D, io, out.p,
-                                  static_cast<float *>(lse.p), ws.p, ws.bytes, place.stream);
+        return windowed ? kda_c.attn_prefill_window(rq.p, rk.p, rv.p, rq.ld, rk.ld, rv.ld, scale, window, sinks, cu, cuk, N, nq,
+                                                    nk, Hq, Hkv, D, io, out.p, l, ws.p, ws.bytes, place.stream)
+                        : kda_c.attn_prefill(rq.p, rk.p, rv.p, rq.ld, rk.ld, rv.ld, scale, cu, cuk, N, nq, nk, Hq, Hkv, D, io,
+                                             out.p, l, ws.p, ws.bytes, place.stream);
     });
-    return rc == KDA_OK ? pair(out, lse) : fail(rc, "kda_attn_prefill");
+    return rc == KDA_OK ? pair(out, lse) : fail(rc, windowed ? "kda_attn_prefill_window" : "kda_attn_prefill");
+}
+PyObject *attn_prefill(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    ARGS(12)
+    return prefill_call(x, false);
+    END_HANDLE_TH_ERRORS
+}
+PyObject *attn_prefill_window(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    ARGS(14)
+    return prefill_call(x, true);
     END_HANDLE_TH_ERRORS
 }
 
-// (q, k_pages, v_pages, block_table, seq_lens, scale, k_new, v_new, tree_mask, out, lse, output_lse, workspace,
-// stream)
-PyObject *attn_decode(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
-    HANDLE_TH_ERRORS
-    ARGS(14)
+// x: (q, k_pages, v_pages, block_table, seq_lens, scale, k_new, v_new, tree_mask, out, lse, output_lse, workspace,
+// stream[, window, sinks])
+PyObject *decode_call(PyObject *const *x, bool windowed) {
     const at::Tensor &q = tensor("q", x[0]), &kp = tensor("k_pages", x[1]), &vp = tensor("v_pages", x[2]);
     const int dev = cuda_index(q);
     const Place place(x[13], dev);
@@ -315,12 +328,28 @@ PyObject *attn_decode(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
         return kda_c.attn_decode_workspace_size(B, T, Hq, Hkv, D, page, table.cols, io);
     });
     const float scale = f32(x[5]);
+    const int32_t window = windowed ? i32("window", x[14]) : 0, sinks = windowed ? i32("sinks", x[15]) : 0;
+    float *const l = static_cast<float *>(lse.p);
     const int rc = call([&] {
-        return kda_c.attn_decode(rq.p, rq.ld, rk.p, rv.p, rk.ld, rv.ld, k_pages, v_pages, P, page, table.p, table.ld,
-                                 table.cols, lens, mask, scale, B, T, Hq, Hkv, D, io, out.p, static_cast<float *>(lse.p),
-                                 ws.p, ws.bytes, place.stream);
+        return windowed ? kda_c.attn_decode_window(rq.p, rq.ld, rk.p, rv.p, rk.ld, rv.ld, k_pages, v_pages, P, page, table.p,
+                                                   table.ld, table.cols, lens, mask, scale, window, sinks, B, T, Hq, Hkv, D,
+                                                   io, out.p, l, ws.p, ws.bytes, place.stream)
+                        : kda_c.attn_decode(rq.p, rq.ld, rk.p, rv.p, rk.ld, rv.ld, k_pages, v_pages, P, page, table.p,
+                                            table.ld, table.cols, lens, mask, scale, B, T, Hq, Hkv, D, io, out.p, l, ws.p,
+                                            ws.bytes, place.stream);
     });
-    return rc == KDA_OK ? pair(out, lse) : fail(rc, "kda_attn_decode");
+    return rc == KDA_OK ? pair(out, lse) : fail(rc, windowed ? "kda_attn_decode_window" : "kda_attn_decode");
+}
+PyObject *attn_decode(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    ARGS(14)
+    return decode_call(x, false);
+    END_HANDLE_TH_ERRORS
+}
+PyObject *attn_decode_window(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    ARGS(16)
+    return decode_call(x, true);
     END_HANDLE_TH_ERRORS
 }
 
@@ -532,6 +561,7 @@ PyObject *init(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {METHOD(init),       METHOD(attn_prefill),  METHOD(attn_decode), METHOD(cache_alloc), METHOD(cache_fork),
                          METHOD(cache_free), METHOD(cache_compact), METHOD(cache_copy),  METHOD(cache_append),
+                         METHOD(attn_prefill_window), METHOD(attn_decode_window),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
