@@ -574,6 +574,70 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv,
                      int32_t Hkv, int32_t D, int32_t io, void *k_pages, void *v_pages,
                      void *workspace, void *stream);
 
+/*
+ * Cutting a cache down by the attention that its tokens get, for contexts that outgrow their
+ * budget: the weights are added up step by step, and now and then the tokens with the least
+ * leave. Every kv head has weights and a choice of its own (a page holds each head's rows
+ * apart); lengths, pages and budgets are the sequence's.
+ *
+ * kda_attn_weights: adds to weights[b][h][j], for every cached token j of sequence b, the
+ *   attention that it gets from the sequence's last tokens through the query heads of kv head h:
+ *       sum over tokens i < count[b] and heads g of exp(scale q_ig . k_j - lse_ig),
+ *       j <= seq_lens[b] - count[b] + i.
+ *   The tokens are those of which the last count[b] (DEVICE int32 [B], NULL: T) cached ones are
+ *   the keys, q and lse rows index[b][0 .. count[b] - 1] (DEVICE int32 [B, T], NULL: 0, 1, ..): the
+ *   step's tokens once kda_cache_append has taken the accepted ones (the same index and
+ *   count), or a prompt's last T.
+ *   q : io dtype [B, T, Hq, D] as in kda_attn_decode, T <= 64   lse : fp32 [B, T, Hq], from the
+ *       attention call of these rows; a row of lse = -inf gives nothing
+ *   weights : fp32 [B, Hkv, cap], cap >= every seq_lens[b]; past seq_lens[b] not touched
+ *   k_pages, block_table, seq_lens, scale and alignment as in kda_attn_decode. Logits, exponentials
+ *   and sums are fp32. No two rows may share weights; pages may be shared. A malformed length or
+ *   count is flagged and its sequence skipped, a malformed index flagged and its row skipped, a
+ *   page number outside the pool flagged and its keys read as zeros (workspace: 256-byte aligned, its
+ *   first 256 bytes zero before its first use; NULL: not flagged).
+ *
+ * kda_cache_evict: of the seq_lens[b] tokens of row b, keep[b] (DEVICE int32 [rows]; < 0 skips the
+ *   row) stay, or all if there are no more: per kv head the first `sinks`, the last `recent`
+ *   (as many as fit; the first ones first) and of the others those of the largest weights
+ *   (of equal ones the earlier; a NaN counts as the largest). They keep their order: slot i
+ *   takes the token of slot kept[b][h][i], in k_pages, v_pages and weights.
+ *     dst_table NULL: in place. Rows whose tokens all stay are left alone.
+ *     else DEVICE int32 [rows, dst_cols]: the slots are those of its pages, which must be none
+ *     of block_table's, with room for the staying tokens (kda_cache_alloc on dst_table); the
+ *     old pages are only read (they may be shared), kda_cache_free gives them back.
+ *   weights : fp32 [rows, Hkv, cap]   weights_out : the same, may be weights itself: the
+ *       staying ones, then zeros up to seq_lens[b]; what is past that is not touched
+ *   kept : int32 [rows, Hkv, cap]: written for the staying slots
+ *   refs : DEVICE int32 [num_pages] or NULL: if given, a row is flagged and skipped where a page
+ *       that it writes to has not exactly one reference (in place, rows that shared pages
+ *       with a fork would overwrite its tokens)
+ *   seq_lens and the tables are not changed, for any number of layers to be cut alike:
+ *   afterwards kda_cache_trim. Malformed lengths or page numbers are flagged, their rows skipped.
+ *   rows * Hkv is at most 2^25. workspace: kda_cache_evict_workspace_size bytes, as for the other calls.
+ *
+ * kda_cache_trim: each row keeps the pages of its first want[row] tokens (DEVICE int32 [rows]; < 0
+ *   skips the row) and drops the others (refs - 1, entries -1); its length is want[row] at most.
+ *   Workspace as for kda_cache_alloc.
+ */
+int kda_attn_weights(const void *q, int64_t ldq, const void *k_pages, int32_t num_pages,
+                     int32_t page_size, const int32_t *block_table, int64_t table_ld,
+                     int32_t table_cols, const int32_t *seq_lens, const float *lse,
+                     const int32_t *index, const int32_t *count, float scale, int32_t B, int32_t T,
+                     int32_t Hq, int32_t Hkv, int32_t D, int32_t io, float *weights, int32_t cap,
+                     void *workspace, void *stream);
+size_t kda_cache_evict_workspace_size(int32_t rows);
+int kda_cache_evict(void *k_pages, void *v_pages, int32_t num_pages, int32_t page_size,
+                    int32_t *block_table, int64_t table_ld, int32_t rows, int32_t table_cols,
+                    int32_t *dst_table, int64_t dst_ld, int32_t dst_cols, const int32_t *refs,
+                    const int32_t *seq_lens, const int32_t *keep, int32_t sinks, int32_t recent,
+                    int32_t Hkv, int32_t D, int32_t io, const float *weights, float *weights_out,
+                    int32_t *kept, int32_t cap, void *workspace, size_t workspace_bytes,
+                    void *stream);
+int kda_cache_trim(int32_t *block_table, int64_t table_ld, int32_t rows, int32_t table_cols,
+                   int32_t *seq_lens, int32_t *refs, int32_t num_pages, int32_t page_size,
+                   const int32_t *want, void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

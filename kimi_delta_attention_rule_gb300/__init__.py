@@ -42,7 +42,8 @@ EXPORTED = ("kda_status_string", "kda_abi_version", "kda_prefill_workspace_size"
             "kda_attn_prefill_workspace_size", "kda_attn_decode",
             "kda_attn_decode_workspace_size", "kda_cache_workspace_size", "kda_cache_alloc",
             "kda_cache_fork", "kda_cache_free", "kda_cache_compact", "kda_cache_copy",
-            "kda_cache_append", "kda_attn_prefill_window", "kda_attn_decode_window")
+            "kda_cache_append", "kda_attn_prefill_window", "kda_attn_decode_window",
+            "kda_attn_weights", "kda_cache_evict_workspace_size", "kda_cache_evict", "kda_cache_trim")
 
 
 class PrefillPlanInfo(ctypes.Structure):
@@ -147,6 +148,16 @@ def load() -> ctypes.CDLL:
         lib.kda_cache_append.argtypes = [P, P, I64, I64, P, I32, I32, P, P, P, P, I64, I32, I32,
                                          I32, I32, I32, I32, P, P, P, P]
         lib.kda_cache_append.restype = ctypes.c_int
+        lib.kda_attn_weights.argtypes = ([P, I64, P, I32, I32, P, I64, I32, P, P, P, P, F32] + [I32] * 6 +
+                                         [P, I32, P, P])
+        lib.kda_attn_weights.restype = ctypes.c_int
+        lib.kda_cache_evict_workspace_size.argtypes = [I32]
+        lib.kda_cache_evict_workspace_size.restype = SZ
+        lib.kda_cache_evict.argtypes = ([P, P, I32, I32, P, I64, I32, I32, P, I64, I32, P, P, P] + [I32] * 5 +
+                                        [P, P, P, I32, P, SZ, P])
+        lib.kda_cache_evict.restype = ctypes.c_int
+        lib.kda_cache_trim.argtypes = [P, I64, I32, I32, P, P, I32, I32, P, P, SZ, P]
+        lib.kda_cache_trim.restype = ctypes.c_int
         # test-only entry points (include/kda_testing.h)
         lib.kda_testing_attn_prefill_timeout.argtypes = (lib.kda_attn_prefill.argtypes[:-1] +
                                                          [I32, I32, P])
@@ -471,7 +482,8 @@ def kda_check_cu_seqlens(cu_host, T_total: int) -> int:
 _BIND_ENTRIES = ("kda_attn_prefill_workspace_size", "kda_attn_prefill",
                  "kda_attn_decode_workspace_size", "kda_attn_decode", "kda_cache_workspace_size",
                  "kda_cache_alloc", "kda_cache_fork", "kda_cache_free", "kda_cache_compact",
-                 "kda_cache_copy", "kda_cache_append", "kda_attn_prefill_window", "kda_attn_decode_window")
+                 "kda_cache_copy", "kda_cache_append", "kda_attn_prefill_window", "kda_attn_decode_window",
+                 "kda_attn_weights", "kda_cache_evict_workspace_size", "kda_cache_evict", "kda_cache_trim")
 _bind = None
 
 
@@ -534,6 +546,16 @@ def cache_workspace(refs, rows=None):
     word zeroed."""
     P = refs.numel()
     return _new_workspace(kda_cache_workspace_size(P, P if rows is None else rows), refs.device)
+
+
+def kda_cache_evict_workspace_size(rows: int) -> int:
+    return int(load().kda_cache_evict_workspace_size(rows))
+
+
+def evict_workspace(weights):
+    """A device workspace for kda_cache_evict on these weights [rows, Hkv, cap] (its status
+    word zeroed)."""
+    return _new_workspace(kda_cache_evict_workspace_size(weights.shape[0]), weights.device)
 
 
 def kda_attn_prefill(q, k, v, scale, cu_seqlens=None, cu_seqlens_k=None, N=1, out=None, lse=None,
@@ -634,3 +656,36 @@ def kda_cache_append(k, v, k_pages, v_pages, block_table, start, cu_seqlens=None
     (device int32; None: all, in order): the accepted tokens of a draft."""
     (_bind or _native()).cache_append(k, v, k_pages, v_pages, block_table, start, cu_seqlens, index,
                                       count, workspace, stream)
+
+
+def kda_attn_weights(q, k_pages, block_table, seq_lens, lse, scale, weights=None, index=None, count=None,
+                     workspace=None, stream=None):
+    """Adds up the attention weight that cached tokens get from their sequence's last ones
+    (C entry point ``kda_attn_weights``).
+
+    q: [B, T, Hq, D], T <= 64, and lse fp32 [B, T, Hq], of an attention call; k_pages: [P, Hkv,
+    page, D], in which the keys of these tokens are already the last ones; of sequence b's
+    rows those of index[b, :count[b]] count (device int32; None: all, in order), as in
+    kda_cache_append; weights: fp32 [B, Hkv, cap], added to (None: zeros, cap = cols * page).
+    Returns weights."""
+    return (_bind or _native()).attn_weights(q, k_pages, block_table, seq_lens, lse, scale, weights, index,
+                                             count, workspace, stream)
+
+
+def kda_cache_evict(k_pages, v_pages, weights, block_table, seq_lens, keep, sinks=0, recent=0, dst_table=None,
+                    refs=None, weights_out=None, kept=None, workspace=None, stream=None):
+    """Keeps keep[row] tokens of each row (device int32; < 0 skips it), per kv head the first
+    `sinks`, the last `recent` and those of the largest weights between, and moves them, in
+    order, to the row's first slots (C entry point ``kda_cache_evict``): in place, or to
+    the pages of dst_table. weights: fp32 [rows, Hkv, cap], moved along (to weights_out; None:
+    in place). refs: rows whose pages others share are flagged and skipped. block_table and
+    seq_lens stay: kda_cache_trim(block_table, seq_lens, refs, keep, page) follows once all layers are
+    cut. Returns kept int32 [rows, Hkv, cap]: the old slot of each new one (-1 past the end)."""
+    return (_bind or _native()).cache_evict(k_pages, v_pages, weights, block_table, seq_lens, keep, sinks, recent,
+                                            dst_table, refs, weights_out, kept, workspace, stream)
+
+
+def kda_cache_trim(block_table, seq_lens, refs, want, page_size, workspace=None, stream=None):
+    """Every row keeps the pages of its first want[row] tokens (device int32; < 0 skips it) and
+    drops the others; seq_lens is want at most (C entry point ``kda_cache_trim``)."""
+    (_bind or _native()).cache_trim(block_table, seq_lens, refs, want, page_size, workspace, stream)

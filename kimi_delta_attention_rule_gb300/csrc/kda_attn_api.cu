@@ -11,6 +11,7 @@
 
 #include "kda.h"
 #include "kda_attn.cuh"
+#include "kda_attn_weights.cuh"
 #include "kda_testing.h"
 
 namespace kda {
@@ -26,7 +27,16 @@ cudaError_t launch_attn_decode_f32(const Args &a, const void *q, const void *kp,
                                    const void *vn, long long ldq, long long ldk, long long ldv,
                                    cudaStream_t stream);
 }  // namespace attn
+namespace weights {
+cudaError_t launch_weights(const Args &a, bool bf16, int sms, cudaStream_t stream);
+}  // namespace weights
 namespace cache {
+cudaError_t launch_evict(void *kp, void *vp, int pages, int page, int32_t *table, int64_t ld, int rows, int cols,
+                         int32_t *dst, int64_t dst_ld, int dst_cols, const int32_t *refs, const int32_t *lens,
+                         const int32_t *keep, int sinks, int recent, int Hkv, int es, const float *w, float *w_out,
+                         int32_t *kept, int cap, int32_t *state, uint32_t *status, int sms, cudaStream_t stream);
+cudaError_t launch_trim(int32_t *table, int64_t ld, int rows, int cols, int32_t *lens, int32_t *refs, int pages, int page,
+                        const int32_t *want, uint32_t *status, cudaStream_t stream);
 cudaError_t launch_append(const void *k, const void *v, int64_t ldk, int64_t ldv, const int32_t *cu, int N, int T,
                           int64_t rows, const int32_t *index, const int32_t *count, const int32_t *start,
                           const int32_t *table, int64_t table_ld, int cols, int pages, int page, int Hkv, int es,
@@ -435,6 +445,100 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv, con
     return done(kda::cache::launch_append(k, v, ldk, ldv, cu, N, T, rows, index, count, start, table, table_ld, cols,
                                           num_pages, page_size, Hkv, io == KDA_BF16 ? 2 : 4, k_pages, v_pages,
                                           status_of(workspace), static_cast<cudaStream_t>(stream)));
+}
+
+int kda_attn_weights(const void *q, int64_t ldq, const void *k_pages, int32_t num_pages, int32_t page_size,
+                     const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
+                     const float *lse, const int32_t *index, const int32_t *count, float scale, int32_t B, int32_t T,
+                     int32_t Hq, int32_t Hkv, int32_t D, int32_t io, float *weights, int32_t cap, void *workspace,
+                     void *stream) {
+    const int rc = check_heads(Hq, Hkv, D, io);
+    if (rc != KDA_OK) return rc;
+    if (B < 0 || T < 0 || num_pages < 0 || table_cols < 0 || table_ld < table_cols || cap < 0 || !scale_ok(scale))
+        return KDA_ERR_INVALID_ARG;
+    if (T > kMaxTokens || !page_ok(page_size)) return KDA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * Hkv * page_size > 0x7fffffffLL || (long long)B * T > 0x7fffffffLL ||
+        (long long)B * T * Hq > (1LL << 40) || (long long)table_cols * page_size > kMaxKeys || cap > kMaxKeys ||
+        (long long)B * Hkv > kda::attn::kMaxItems)
+        return KDA_ERR_INVALID_ARG;
+    if (B == 0 || T == 0 || cap == 0 || table_cols == 0 || num_pages == 0) return KDA_OK;  // no cached token
+    if (q == nullptr || k_pages == nullptr || block_table == nullptr || seq_lens == nullptr || lse == nullptr ||
+        weights == nullptr)
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
+        !aligned(index, 4) || !aligned(count, 4) || !aligned(weights, 4) || !aligned(workspace, 256))
+        return KDA_ERR_INVALID_ARG;
+    if (!ld_ok(ldq, Hq, io)) return KDA_ERR_INVALID_ARG;
+    kda::weights::Args a = {};
+    a.q = q;
+    a.ldq = ldq;
+    a.kp = k_pages;
+    a.lse = lse;
+    a.w = weights;
+    a.index = index;
+    a.count = count;
+    a.table = block_table;
+    a.lens = seq_lens;
+    a.table_ld = table_ld;
+    a.B = B;
+    a.T = T;
+    a.G = Hq / Hkv;
+    a.Hkv = Hkv;
+    a.cap = cap;
+    a.page = page_size;
+    a.pages = num_pages;
+    a.cols = table_cols;
+    a.t1 = T;
+    a.scale = scale;
+    a.status = status_of(workspace);
+    Range range("kda_attn_weights");
+    return done(kda::weights::launch_weights(a, io == KDA_BF16, sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+size_t kda_cache_evict_workspace_size(int32_t rows) {
+    return rows < 0 ? 0 : (kHeader + (size_t)rows * 4 + 255) / 256 * 256;
+}
+
+int kda_cache_evict(void *k_pages, void *v_pages, int32_t num_pages, int32_t page_size, int32_t *block_table,
+                    int64_t table_ld, int32_t rows, int32_t table_cols, int32_t *dst_table, int64_t dst_ld,
+                    int32_t dst_cols, const int32_t *refs, const int32_t *seq_lens, const int32_t *keep, int32_t sinks,
+                    int32_t recent, int32_t Hkv, int32_t D, int32_t io, const float *weights, float *weights_out,
+                    int32_t *kept, int32_t cap, void *ws, size_t ws_bytes, void *stream) {
+    const int rc = check_heads(Hkv, Hkv, D, io);
+    if (rc != KDA_OK) return rc;
+    if (num_pages < 0 || rows < 0 || table_cols < 0 || table_ld < table_cols || sinks < 0 || recent < 0 || cap < 0)
+        return KDA_ERR_INVALID_ARG;
+    if (!page_ok(page_size)) return KDA_ERR_UNSUPPORTED;
+    if (dst_table != nullptr && (dst_cols < 0 || dst_ld < dst_cols)) return KDA_ERR_INVALID_ARG;
+    if ((long long)num_pages * Hkv * page_size > 0x7fffffffLL || num_pages > kMaxPages ||
+        (long long)rows * table_cols > kMaxPages || (long long)rows * dst_cols > kMaxPages ||
+        (long long)table_cols * page_size > kMaxKeys || cap > kMaxKeys || (long long)rows * Hkv > (1LL << 25))
+        return KDA_ERR_INVALID_ARG;
+    if (rows == 0 || cap == 0 || table_cols == 0 || num_pages == 0) return KDA_OK;  // no cached token
+    if (k_pages == nullptr || v_pages == nullptr || block_table == nullptr || seq_lens == nullptr || keep == nullptr ||
+        weights == nullptr || weights_out == nullptr || kept == nullptr || ws == nullptr)
+        return KDA_ERR_INVALID_ARG;
+    if (!aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(block_table, 4) || !aligned(dst_table, 4) ||
+        !aligned(refs, 4) || !aligned(seq_lens, 4) || !aligned(keep, 4) || !aligned(weights, 4) ||
+        !aligned(weights_out, 4) || !aligned(kept, 4) || !aligned(ws, 256) || ws_bytes < kda_cache_evict_workspace_size(rows))
+        return KDA_ERR_INVALID_ARG;
+    Range range("kda_cache_evict");
+    return done(kda::cache::launch_evict(k_pages, v_pages, num_pages, page_size, block_table, table_ld, rows, table_cols,
+                                         dst_table, dst_ld, dst_cols, refs, seq_lens, keep, sinks, recent, Hkv,
+                                         io == KDA_BF16 ? 2 : 4, weights, weights_out, kept, cap, scratch_of(ws),
+                                         status_of(ws), sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+int kda_cache_trim(int32_t *table, int64_t ld, int32_t rows, int32_t cols, int32_t *seq_lens, int32_t *refs,
+                   int32_t num_pages, int32_t page_size, const int32_t *want, void *ws, size_t ws_bytes, void *stream) {
+    const int rc = check_cache(table, ld, rows, cols, refs, num_pages, ws, ws_bytes);
+    if (rc != KDA_OK) return rc;
+    if (page_size <= 0) return KDA_ERR_INVALID_ARG;
+    if (rows == 0 || cols == 0) return KDA_OK;
+    if (seq_lens == nullptr || want == nullptr || !aligned(seq_lens, 4) || !aligned(want, 4)) return KDA_ERR_INVALID_ARG;
+    Range range("kda_cache_trim");
+    return done(kda::cache::launch_trim(table, ld, rows, cols, seq_lens, refs, num_pages, page_size, want, status_of(ws),
+                                        static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

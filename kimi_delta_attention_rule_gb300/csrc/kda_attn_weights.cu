@@ -1,0 +1,130 @@
+// Attention weights on CUDA cores (the formula and the work split are those of
+// kda_attn_weights.cuh): 128 threads take tiles of 64 keys; a thread forms a 4 x 4 piece
+// of S = K Q^T for 32 rows at a time, its exponentials, and their sum over its rows; the
+// eight threads of a key add up in shared memory in a fixed order. Several CTAs per SM hide
+// one another's loads.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_attn_weights.cuh"
+#include "kda_common.cuh"
+
+namespace kda {
+namespace weights {
+
+constexpr int kThreads = 128, kKeys = 64, kRows = 32;
+// Rows of K and Q are read by neighbouring threads: the 16-byte pieces of a row stand in the order
+// of (piece xor row % 8).
+constexpr int kSmem = (kKeys + kRows) * kD * 4 + 8 * kKeys * 4 + kRows * 8;
+
+__device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
+    const uint2 x = *reinterpret_cast<const uint2 *>(p);
+    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x.x)),
+                 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x.y));
+    return make_float4(lo.x, lo.y, hi.x, hi.y);
+}
+
+template <typename IO>
+__global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_constant__ Args a) {
+    extern __shared__ __align__(16) float sm[];
+    float *const Ks = sm, *const Qs = Ks + kKeys * kD, *const sums = Qs + kRows * kD, *const minus_lse = sums + 8 * kKeys;
+    int *const seen = reinterpret_cast<int *>(minus_lse + kRows);  // keys that a row sees
+    wait_before();
+    let_next_start();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tx = tid & 15, ty = tid >> 4;
+    const IO *const q = static_cast<const IO *>(a.q), *const kp = static_cast<const IO *>(a.kp);
+    const int Hq = a.Hkv * a.G, page_bits = 31 - __clz(a.page);
+    Walk<kKeys> walk;
+    walk.init(a, blockIdx.x, gridDim.x);
+    Part p;
+    while (walk.next(a, p)) {
+        const int rows = p.s.tokens * a.G;
+        for (int t = p.ta; t < p.tb; ++t) {
+            __syncthreads();  // the last tile is through
+            for (int r = warp; r < kKeys; r += kThreads / 32) {
+                const int pos = t * kKeys + r;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (pos < p.s.len) {
+                    const int pg = a.table[(size_t)p.b * a.table_ld + (pos >> page_bits)];
+                    if (pg >= 0 && pg < a.pages)
+                        x = load4(kp + (((size_t)pg * a.Hkv + p.h) * a.page + (pos & (a.page - 1))) * kD + 4 * lane);
+                    else if (lane == 0)
+                        flag(a);
+                }
+                *reinterpret_cast<float4 *>(Ks + r * kD + 4 * (lane ^ (r & 7))) = x;
+            }
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};  // keys tx + 16 e
+            for (int r0 = 0; r0 < rows; r0 += kRows) {
+                if (r0 > 0) __syncthreads();  // the last rows are read
+                if (rows > kRows || t == p.ta) {
+                    for (int r = warp; r < kRows; r += kThreads / 32) {
+                        const int i = (r0 + r) / a.G, g = r0 + r - i * a.G;
+                        int tok = r0 + r < rows ? token_of(a, p.b, a.t0 + i) : -1;
+                        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                        float l = -INFINITY;
+                        if (tok >= 0) {
+                            x = load4(q + ((size_t)p.b * a.T + tok) * a.ldq + (size_t)(p.h * a.G + g) * kD + 4 * lane);
+                            l = a.lse[((size_t)p.b * a.T + tok) * Hq + p.h * a.G + g];
+                        }
+                        *reinterpret_cast<float4 *>(Qs + r * kD + 4 * (lane ^ (r & 7))) = x;
+                        if (lane == 0) {
+                            minus_lse[r] = -l;
+                            seen[r] = l == -INFINITY ? 0 : p.s.len - p.s.count + a.t0 + i + 1;
+                        }
+                    }
+                }
+                __syncthreads();
+                float s[4][4] = {};
+#pragma unroll 4
+                for (int d = 0; d < kD; d += 4) {
+                    float4 kk[4], qq[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) kk[e] = load4(Ks + (tx + 16 * e) * kD + (d ^ ((tx & 7) * 4)));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qq[i] = load4(Qs + (ty + 8 * i) * kD + (d ^ (ty * 4)));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            s[e][i] = fmaf(kk[e].x, qq[i].x, s[e][i]);
+                            s[e][i] = fmaf(kk[e].y, qq[i].y, s[e][i]);
+                            s[e][i] = fmaf(kk[e].z, qq[i].z, s[e][i]);
+                            s[e][i] = fmaf(kk[e].w, qq[i].w, s[e][i]);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = ty + 8 * i;
+                    const float l = minus_lse[r];
+                    const int n = seen[r];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (t * kKeys + tx + 16 * e < n) sum[e] += expf(fmaf(s[e][i], a.scale, l));
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sums[ty * kKeys + tx + 16 * e] = sum[e];
+            __syncthreads();
+            const int pos = t * kKeys + tid;
+            if (tid < kKeys && pos < p.s.len) {
+                float y = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y += sums[i * kKeys + tid];
+                a.w[((size_t)p.b * a.Hkv + p.h) * a.cap + pos] += y;
+            }
+        }
+    }
+}
+
+cudaError_t launch_weights(const Args &a, bool bf16, int sms, cudaStream_t stream) {
+    const auto kernel = bf16 ? weights_kernel<__nv_bfloat16> : weights_kernel<float>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    const long long tiles = (long long)a.B * a.Hkv * (((long long)a.cols * a.page + kKeys - 1) / kKeys), most = 4LL * sms;
+    return launch_early(kernel, dim3((unsigned)(tiles < most ? tiles : most)), kThreads, kSmem, stream, a);
+}
+
+}  // namespace weights
+}  // namespace kda

@@ -33,6 +33,10 @@ struct Entry {
     decltype(&kda_cache_append) cache_append;
     decltype(&kda_attn_prefill_window) attn_prefill_window;
     decltype(&kda_attn_decode_window) attn_decode_window;
+    decltype(&kda_attn_weights) attn_weights;
+    decltype(&kda_cache_evict_workspace_size) cache_evict_workspace_size;
+    decltype(&kda_cache_evict) cache_evict;
+    decltype(&kda_cache_trim) cache_trim;
 } kda_c;
 PyObject *error_class = nullptr;  // KDAError(code, what)
 
@@ -152,15 +156,15 @@ struct BlockTable {
     int32_t rows, cols;
     int dev;
 };
-BlockTable take_table(PyObject *o) {
-    const at::Tensor &t = tensor("block_table", o);
-    TORCH_CHECK_VALUE(t.scalar_type() == at::kInt && t.is_cuda() && t.dim() == 2,
-                      "block_table must be a CUDA int32 [rows, cols] tensor");
-    TORCH_CHECK_VALUE(t.size(1) <= 1 || t.stride(1) == 1, "the rows of block_table must be contiguous");
+BlockTable take_table(PyObject *o, const char *name = "block_table") {
+    const at::Tensor &t = tensor(name, o);
+    TORCH_CHECK_VALUE(t.scalar_type() == at::kInt && t.is_cuda() && t.dim() == 2, name,
+                      " must be a CUDA int32 [rows, cols] tensor");
+    TORCH_CHECK_VALUE(t.size(1) <= 1 || t.stride(1) == 1, "the rows of ", name, " must be contiguous");
     BlockTable b;
     b.p = static_cast<int32_t *>(t.data_ptr());
-    b.rows = i32("block_table", t.size(0));
-    b.cols = i32("block_table", t.size(1));
+    b.rows = i32(name, t.size(0));
+    b.cols = i32(name, t.size(1));
     b.ld = b.rows > 1 ? t.stride(0) : b.cols;
     b.dev = static_cast<int>(t.get_device());
     return b;
@@ -536,6 +540,136 @@ PyObject *cache_append(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     END_HANDLE_TH_ERRORS
 }
 
+// The weights of a cache's tokens, [rows, Hkv, cap].
+int32_t weights_cap(const char *name, PyObject *o, int64_t rows, int64_t Hkv) {
+    const at::Tensor &t = tensor(name, o);
+    TORCH_CHECK_VALUE(t.dim() == 3 && t.size(0) == rows && t.size(1) == Hkv, name, " must have the shape [rows, Hkv, cap]");
+    return i32(name, t.size(2));
+}
+
+// (q, k_pages, block_table, seq_lens, lse, scale, weights, index, count, workspace, stream)
+PyObject *attn_weights(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    ARGS(11)
+    const at::Tensor &q = tensor("q", x[0]), &kp = tensor("k_pages", x[1]);
+    const int dev = cuda_index(q);
+    const Place place(x[10], dev);
+    const auto dt = q.scalar_type();
+    const int32_t io = io_of(dt);
+    if (io < 0) return bad_dtype(dt);
+    TORCH_CHECK_VALUE(q.dim() == 4 && kp.dim() == 4 && kp.size(3) == q.size(3),
+                      "q must have the shape [B, T, Hq, D], k_pages [P, Hkv, page, D]");
+    const int32_t B = i32("q", q.size(0)), T = i32("q", q.size(1)), Hq = i32("q", q.size(2)), D = i32("q", q.size(3));
+    const int32_t P = i32("k_pages", kp.size(0)), Hkv = i32("k_pages", kp.size(1)), page = i32("k_pages", kp.size(2));
+    const Rows rq = take_rows("q", q, dt, dev);
+    const BlockTable table = take_table(x[2]);
+    TORCH_CHECK_VALUE(table.dev == dev, "KDA tensors must be on one device");
+    TORCH_CHECK_VALUE(table.rows == B && tensor("seq_lens", x[3]).sizes() == at::IntArrayRef({B}),
+                      "block_table and seq_lens must have a row for each sequence");
+    check_shape("lse", x[4], {B, T, Hq});
+    check_shape("index", x[7], {B, T});
+    check_shape("count", x[8], {B});
+    const int32_t *lens = take_as<int32_t>("seq_lens", x[3], at::kInt, dev);
+    const float *lse = static_cast<float *>(take("lse", tensor("lse", x[4]), at::kFloat, dev));
+    const int32_t *index = take_as<int32_t>("index", x[7], at::kInt, dev), *count = take_as<int32_t>("count", x[8], at::kInt, dev);
+    const void *k_pages = take("k_pages", kp, dt, dev);
+    Out weights;
+    int32_t cap;
+    if (x[6] == Py_None) {
+        cap = i32("block_table", static_cast<int64_t>(table.cols) * page);
+        at::Tensor t = at::zeros({B, Hkv, cap}, at::TensorOptions().dtype(at::kFloat).device(q.device()));
+        weights.p = t.data_ptr();
+        weights.obj = THPVariable_Wrap(std::move(t));
+    } else {
+        cap = weights_cap("weights", x[6], B, Hkv);
+        weights.p = take("weights", x[6], at::kFloat, dev);
+        weights.obj = Py_NewRef(x[6]);
+    }
+    void *const ws = take("workspace", x[9], at::kByte, dev);
+    const float scale = f32(x[5]);
+    const int rc = call([&] {
+        return kda_c.attn_weights(rq.p, rq.ld, k_pages, P, page, table.p, table.ld, table.cols, lens, lse, index, count, scale, B,
+                                  T, Hq, Hkv, D, io, static_cast<float *>(weights.p), cap, ws, place.stream);
+    });
+    return rc == KDA_OK ? weights.give() : fail(rc, "kda_attn_weights");
+    END_HANDLE_TH_ERRORS
+}
+
+// (k_pages, v_pages, weights, block_table, seq_lens, keep, sinks, recent, dst_table, refs, weights_out, kept, workspace,
+// stream)
+PyObject *cache_evict(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    ARGS(14)
+    const at::Tensor &kp = tensor("k_pages", x[0]), &vp = tensor("v_pages", x[1]);
+    const int dev = cuda_index(kp);
+    const Place place(x[13], dev);
+    const auto dt = kp.scalar_type();
+    const int32_t io = io_of(dt);
+    if (io < 0) return bad_dtype(dt);
+    TORCH_CHECK_VALUE(kp.dim() == 4 && vp.sizes() == kp.sizes(), "k_pages and v_pages must have the shape [P, Hkv, page, D]");
+    const int32_t P = i32("k_pages", kp.size(0)), Hkv = i32("k_pages", kp.size(1)), page = i32("k_pages", kp.size(2)),
+                  D = i32("k_pages", kp.size(3));
+    void *const k_pages = take("k_pages", kp, dt, dev), *const v_pages = take("v_pages", vp, dt, dev);
+    const BlockTable b = take_table(x[3]);
+    TORCH_CHECK_VALUE(b.dev == dev, "KDA tensors must be on one device");
+    BlockTable dst = {nullptr, 0, b.rows, 0, dev};
+    if (x[8] != Py_None) {
+        dst = take_table(x[8], "dst_table");
+        TORCH_CHECK_VALUE(dst.dev == dev, "KDA tensors must be on one device");
+        TORCH_CHECK_VALUE(dst.rows == b.rows, "dst_table must have as many rows as block_table");
+        TORCH_CHECK_VALUE(dst.p != nullptr || b.rows == 0, "dst_table has no column");
+    }
+    const int32_t *const lens = take_lens(x[4], b);
+    TORCH_CHECK_VALUE(tensor("keep", x[5]).sizes() == at::IntArrayRef({b.rows}), "keep must have an entry for each row");
+    const int32_t *keep = take_as<int32_t>("keep", x[5], at::kInt, dev);
+    const int32_t sinks = i32("sinks", x[6]), recent = i32("recent", x[7]);
+    const int32_t cap = weights_cap("weights", x[2], b.rows, Hkv);
+    const float *w = take_as<float>("weights", x[2], at::kFloat, dev);
+    check_shape("weights_out", x[10], {b.rows, Hkv, cap});
+    float *w_out = x[10] == Py_None ? const_cast<float *>(w) : take_as<float>("weights_out", x[10], at::kFloat, dev);
+    const int32_t *refs = nullptr;
+    if (x[9] != Py_None) {
+        TORCH_CHECK_VALUE(tensor("refs", x[9]).numel() == P, "refs must have an entry for each page");
+        refs = take_as<int32_t>("refs", x[9], at::kInt, dev);
+    }
+    Out kept;
+    if (x[11] == Py_None) {
+        at::Tensor t = at::full({b.rows, Hkv, cap}, -1, at::TensorOptions().dtype(at::kInt).device(kp.device()));
+        kept.p = t.data_ptr();
+        kept.obj = THPVariable_Wrap(std::move(t));
+    } else {
+        kept.take_or_make("kept", x[11], {b.rows, Hkv, cap}, at::kInt, kp, dev);
+    }
+    const Space ws = workspace(x[12], kp, dev, [&] { return kda_c.cache_evict_workspace_size(b.rows); });
+    const int rc = call([&] {
+        return kda_c.cache_evict(k_pages, v_pages, P, page, b.p, b.ld, b.rows, b.cols, dst.p, dst.ld, dst.cols, refs, lens, keep,
+                                 sinks, recent, Hkv, D, io, w, w_out, static_cast<int32_t *>(kept.p), cap, ws.p, ws.bytes,
+                                 place.stream);
+    });
+    return rc == KDA_OK ? kept.give() : fail(rc, "kda_cache_evict");
+    END_HANDLE_TH_ERRORS
+}
+
+// (block_table, seq_lens, refs, want, page_size, workspace, stream)
+PyObject *cache_trim(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
+    HANDLE_TH_ERRORS
+    ARGS(7)
+    const BlockTable b = take_table(x[0]);
+    const Place place(x[6], b.dev);
+    int32_t *const lens = take_lens(x[1], b);
+    const Refs refs = take_refs(x[2], b.dev);
+    TORCH_CHECK_VALUE(tensor("want", x[3]).sizes() == at::IntArrayRef({b.rows}), "want must have an entry for each row");
+    const int32_t *want = take_as<int32_t>("want", x[3], at::kInt, b.dev);
+    const int32_t page = i32("page_size", x[4]);
+    const Space ws = cache_space(x[5], x[0], b, refs);
+    const int rc = call([&] {
+        return kda_c.cache_trim(b.p, b.ld, b.rows, b.cols, lens, refs.p, refs.pages, page, want, ws.p, ws.bytes, place.stream);
+    });
+    if (rc != KDA_OK) return fail(rc, "kda_cache_trim");
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
 // (addresses of the C functions in the order of Entry, KDAError)
 PyObject *init(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     constexpr Py_ssize_t n = sizeof(Entry) / sizeof(void *);
@@ -561,7 +695,8 @@ PyObject *init(PyObject *, PyObject *const *x, Py_ssize_t nargs) {
     { #name, reinterpret_cast<PyCFunction>(reinterpret_cast<void *>(name)), METH_FASTCALL, nullptr }
 PyMethodDef methods[] = {METHOD(init),       METHOD(attn_prefill),  METHOD(attn_decode), METHOD(cache_alloc), METHOD(cache_fork),
                          METHOD(cache_free), METHOD(cache_compact), METHOD(cache_copy),  METHOD(cache_append),
-                         METHOD(attn_prefill_window), METHOD(attn_decode_window),
+                         METHOD(attn_prefill_window), METHOD(attn_decode_window), METHOD(attn_weights),
+                         METHOD(cache_evict), METHOD(cache_trim),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kda_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

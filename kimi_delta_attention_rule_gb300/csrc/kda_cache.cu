@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kda_cache.cuh"
 #include "kda_common.cuh"
 
 namespace kda {
@@ -25,15 +26,7 @@ namespace cache {
 namespace cg = cooperative_groups;
 
 constexpr int kCtas = 8;  // the largest portable cluster
-constexpr int kThreads = 1024;
 constexpr int kMaxPools = 16;
-
-struct Table {
-    int32_t *entries;
-    int64_t ld;
-    int32_t rows, cols;
-    __device__ __forceinline__ int32_t *row(int r) const { return entries + (size_t)r * ld; }
-};
 
 // ---- append -----------------------------------------------------------------
 // A warp per row: it issues the loads of the row's first 2 KB (which need no look-up,
@@ -188,31 +181,7 @@ __global__ void __launch_bounds__(256)
     if (blockIdx.y == 0 && threadIdx.x == 0) lens[r] = 0;
 }
 
-// ---- block and cluster sums -------------------------------------------------------
-// Exclusive prefix of x over the block; total gets the sum. Converged block.
-__device__ __forceinline__ int block_exclusive(int x, int *warp_sums, int &total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int incl = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += y;
-    }
-    __syncthreads();  // warp_sums is free
-    if (lane == 31) warp_sums[warp] = incl;
-    __syncthreads();
-    const int mine = warp_sums[lane];  // 32 warps
-    int sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += y;
-    }
-    total = __shfl_sync(0xffffffffu, sum, 31);
-    const int before = __shfl_sync(0xffffffffu, sum - mine, warp);
-    return before + incl - x;
-}
-
+// ---- cluster sums ------------------------------------------------------------
 // The slice of refs of one CTA: a multiple of four pages, read as int4.
 struct Slice {
     int lo, hi;

@@ -1,0 +1,43 @@
+// What the kernels on a cache's pages share: the block table and sums over a block.
+#pragma once
+
+#include <stdint.h>
+
+namespace kda {
+namespace cache {
+
+constexpr int kThreads = 1024;  // of a block of block_exclusive
+
+struct Table {
+    int32_t *entries;
+    int64_t ld;
+    int32_t rows, cols;
+    __device__ __forceinline__ int32_t *row(int r) const { return entries + (size_t)r * ld; }
+};
+
+// Exclusive prefix of x over the block; total gets the sum. Converged block.
+__device__ __forceinline__ int block_exclusive(int x, int *warp_sums, int &total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+    }
+    __syncthreads();  // warp_sums is free
+    if (lane == 31) warp_sums[warp] = incl;
+    __syncthreads();
+    const int mine = warp_sums[lane];  // 32 warps
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    total = __shfl_sync(0xffffffffu, sum, 31);
+    const int before = __shfl_sync(0xffffffffu, sum - mine, warp);
+    return before + incl - x;
+}
+
+}  // namespace cache
+}  // namespace kda

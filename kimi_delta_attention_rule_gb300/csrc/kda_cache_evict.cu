@@ -1,0 +1,390 @@
+// Cutting a cache down: per sequence and kv head, the `keep` tokens that stay are the first
+// `sinks`, the last `recent` and, of those between, the ones of the largest accumulated
+// weight (ties: the earlier); they move to the slots 0 .. keep - 1, in their order.
+//
+// Choosing (select_kernel): one block per (sequence, head) finds the weight of rank
+// `heavy` by four passes over eight bits each of the weights' ordered patterns, then goes once
+// through the slots and writes the staying ones with their rank, a prefix sum over the block.
+//
+// Moving (move_kernel): a chunk is 2,048 pieces of 16 bytes, eight per thread, whose loads
+// are in flight together, and those of the next chunk before this one's are stored. To
+// other pages, a CTA takes a part of the line of all sequences' slots. In place, slot i
+// takes that of kept[i] >= i, so whoever writes slot i must know that all that lies there
+// is read: a CTA takes the slots of one (sequence, head, K or V) in order, of which it may store a
+// chunk as soon as its own loads of it are through, since later chunks read later slots; with few
+// sequences CTAs share a row's bytes, not its slots, and nobody waits for another CTA.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "kda_cache.cuh"
+#include "kda_common.cuh"
+
+namespace kda {
+namespace cache {
+
+struct EvictArgs {
+    Table src, dst;
+    const int32_t *lens, *keep;
+    const int32_t *refs;  // or NULL
+    int sinks, recent;
+    int Hkv, cap, page, page_bits, pages;
+    const float *w;       // [rows, Hkv, cap]
+    float *w_out;
+    int32_t *kept;
+    int32_t *state;       // [rows]: slots that move, 0: none
+    int in_place;
+    uint32_t *status;
+};
+
+// ---- the slots that stay ---------------------------------------------------------
+// Patterns that order as the weights do: NaN above all, -0 as 0.
+__device__ __forceinline__ uint32_t ordered(float x) {
+    if (x != x) return 0xffffffffu;
+    const uint32_t u = x == 0.f ? 0u : __float_as_uint(x);
+    return u >> 31 ? ~u : u | 0x80000000u;
+}
+
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictArgs a) {
+    __shared__ int warp_sums[32];
+    __shared__ int hist[kThreads / 32][256];
+    __shared__ int found[2];  // the digit, and how many above it there are
+    wait_before();
+    let_next_start();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
+    const int len = a.lens[b], budget = a.keep[b];
+    if (budget < 0) {
+        if (h == 0 && tid == 0) a.state[b] = 0;
+        return;
+    }
+    const int n = min(len, budget);
+    const bool moves = !a.in_place || len > budget;
+    bool bad = len < 0 || len > a.cap || (long long)len > (long long)a.src.cols * a.page ||
+               (long long)n > (long long)a.dst.cols * a.page;
+    if (!bad) {
+        const int32_t *const from = a.src.row(b), *const to = a.dst.row(b);
+        for (int j = tid; j < (int)(((unsigned)len + a.page - 1) >> a.page_bits); j += kThreads)
+            bad = bad || from[j] < 0 || from[j] >= a.pages;
+        for (int j = tid; j < (int)(((unsigned)n + a.page - 1) >> a.page_bits); j += kThreads) {
+            const int pg = to[j];
+            bad = bad || pg < 0 || pg >= a.pages;
+            if (!bad && moves && a.refs != nullptr) bad = a.refs[pg] != 1;  // others read what is there
+        }
+    }
+    if (__syncthreads_or(bad)) {
+        if (tid == 0 && h == 0) {
+            a.state[b] = 0;
+            atomicOr(a.status, kStatusBadSeqlens);
+        }
+        return;
+    }
+    if (h == 0 && tid == 0) a.state[b] = moves ? n : 0;
+    const float *const w = a.w + (size_t)blockIdx.x * a.cap;
+    float *const w_out = a.w_out + (size_t)blockIdx.x * a.cap;
+    int32_t *const kept = a.kept + (size_t)blockIdx.x * a.cap;
+    if (len <= budget) {
+        for (int i = tid; i < len; i += kThreads) {
+            kept[i] = i;
+            if (w_out != w) w_out[i] = w[i];
+        }
+        return;
+    }
+    const int sinks = min(a.sinks, n), recent = min(a.recent, n - sinks), end = len - recent;
+    int need = n - sinks - recent;  // of [sinks, end)
+    uint32_t top = 0xffffffffu;     // what is above it stays, and the first `need` equal ones
+    if (need > 0) {
+        top = 0;
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            for (int i = tid; i < 32 * 256; i += kThreads) (&hist[0][0])[i] = 0;
+            __syncthreads();
+            const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
+#pragma unroll 4
+            for (int i = sinks + tid; i < end; i += kThreads) {
+                const uint32_t key = ordered(w[i]);
+                if ((key & mask) == top) atomicAdd(&hist[warp][key >> shift & 255], 1);
+            }
+            __syncthreads();
+            if (tid < 256) {
+                int sum = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) sum += hist[i][tid];
+                hist[0][tid] = sum;
+            }
+            __syncthreads();
+            if (warp == 0) {  // lane l has the digits 255 - 8 l .. 248 - 8 l
+                int mine = 0, c[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mine += c[e] = hist[0][255 - 8 * lane - e];
+                int incl = mine;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += y;
+                }
+                int above = incl - mine;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (above < need && above + c[e] >= need) {
+                        found[0] = 255 - 8 * lane - e;
+                        found[1] = above;
+                    }
+                    above += c[e];
+                }
+            }
+            __syncthreads();
+            top |= (uint32_t)found[0] << shift;
+            need -= found[1];
+        }
+    }
+    // Weights in place: a round writes no slot past those that it or earlier ones have read.
+    int above = 0, equal = 0;
+    for (int i0 = 0; i0 < len; i0 += 4 * kThreads) {
+        float x[4];
+        int mine = 0;  // staying ones, and equal ones in the upper half
+        uint32_t stays = 0, ties = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + 4 * tid + e;
+            if (i >= len) continue;
+            x[e] = w[i];
+            const uint32_t key = ordered(x[e]);
+            const bool safe = i < sinks || i >= end;
+            if (safe || key > top) {
+                stays |= 1u << e;
+                ++mine;
+            } else if (key == top) {
+                ties |= 1u << e;
+                mine += 1 << 16;
+            }
+        }
+        int total;
+        const int before = block_exclusive(mine, warp_sums, total);
+        int s = above + (before & 0xffff), t = equal + (before >> 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool tie = ties >> e & 1;
+            if ((stays >> e & 1) || (tie && t < need)) {
+                const int to = s + min(t, need);
+                kept[to] = i0 + 4 * tid + e;
+                w_out[to] = x[e];
+            }
+            s += stays >> e & 1;
+            t += tie;
+        }
+        above += total & 0xffff;
+        equal += total >> 16;
+    }
+    __syncthreads();
+    for (int i = n + tid; i < len; i += kThreads) w_out[i] = 0.f;
+}
+
+// ---- the rows that move ------------------------------------------------------------
+constexpr int kMoveThreads = 256, kFlight = 8, kChunk = kMoveThreads * kFlight;
+constexpr int kMoveRows = kChunk / 4;  // rows of a chunk at the most: four pieces of each
+
+struct MoveArgs {
+    uint4 *kp, *vp;
+    int rows;        // of the table
+    int row_bits;    // pieces of a row: 16 or 32
+    int piece_bits;  // pieces of a slot in a chunk: in place those of a CTA's slice, else those of K and V
+    int parts;       // in place: CTAs of a (sequence, head)
+};
+
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ EvictArgs a, const MoveArgs m) {
+    __shared__ int2 where[3][kMoveRows];  // (from, to) rows of the pools, (-1, ..): none
+    wait_before();
+    let_next_start();
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int per_chunk = kChunk >> m.piece_bits;  // slots
+    // The chunks of this CTA: (b, h, chunk), `left` of them.
+    int b, h = 0, chunk = 0, n = 0;
+    long long left;
+    auto chunks = [&](int slots) { return (int)(((unsigned)slots + per_chunk - 1) / (unsigned)per_chunk); };
+    if (IN_PLACE) {
+        const int bh = blockIdx.x / m.parts;
+        b = bh / a.Hkv;
+        h = bh - b * a.Hkv;
+        n = a.state[b];
+        left = chunks(n);
+    } else {
+        long long total = 0;
+        for (int i = lane; i < m.rows; i += 32) total += chunks(a.state[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        total *= a.Hkv;
+        long long x = total * blockIdx.x / gridDim.x;
+        left = total * (blockIdx.x + 1LL) / gridDim.x - x;
+        if (left == 0) return;
+        for (b = 0; b < m.rows; b += 32) {
+            const int mine_n = b + lane < m.rows ? a.state[b + lane] : 0;
+            const long long mine = (long long)chunks(mine_n) * a.Hkv;
+            long long incl = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const long long sum = __shfl_sync(0xffffffffu, incl, 31);
+            if (x >= sum) {
+                x -= sum;
+                continue;
+            }
+            const int at = __ffs(__ballot_sync(0xffffffffu, x < incl)) - 1;
+            x -= __shfl_sync(0xffffffffu, incl - mine, at);
+            n = __shfl_sync(0xffffffffu, mine_n, at);
+            b += at;
+            h = (int)(x / chunks(n));
+            chunk = (int)(x - (long long)h * chunks(n));
+            break;
+        }
+    }
+    if (left == 0) return;
+    const int32_t *kept = a.kept + ((size_t)b * a.Hkv + h) * a.cap;
+    // Where the next chunk's rows are and go, and on to the one after it. (Behind the last: none.)
+    auto look = [&](int2 *to) {
+        const bool any = left > 0;
+        for (int r = tid; r < per_chunk; r += kMoveThreads) {
+            const int i = chunk * per_chunk + r;
+            int2 p = make_int2(-1, -1);
+            if (any && i < n) {
+                const int j = kept[i], mask = a.page - 1;
+                p.x = (a.src.row(b)[j >> a.page_bits] * a.Hkv + h) * a.page + (j & mask);
+                p.y = (a.dst.row(b)[i >> a.page_bits] * a.Hkv + h) * a.page + (i & mask);
+                if (p.x == p.y) p.x = -1;
+            }
+            to[r] = p;
+        }
+        if (!any) return;
+        --left;
+        ++chunk;
+        if (!IN_PLACE && left > 0 && chunk == chunks(n)) {
+            chunk = 0;
+            if (++h == a.Hkv) {
+                h = 0;
+                do n = ++b < m.rows ? a.state[b] : 0;
+                while (n == 0 && b < m.rows);
+            }
+            kept = a.kept + ((size_t)b * a.Hkv + h) * a.cap;
+        }
+    };
+    const int part = IN_PLACE ? blockIdx.x % m.parts : 0;
+    // piece x of a slot: of K or V, and which of its row
+    auto piece = [&](int x, int row, bool &is_v) -> size_t {
+        const int at = IN_PLACE ? (part << m.piece_bits) + x : x;
+        is_v = at >> m.row_bits;
+        return ((size_t)row << m.row_bits) + (at & ((1 << m.row_bits) - 1));
+    };
+    auto load = [&](const int2 *rows, uint4 *y) {
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int x = f * kMoveThreads + tid, from = rows[x >> m.piece_bits].x;
+            bool is_v;
+            const size_t at = piece(x & ((1 << m.piece_bits) - 1), from, is_v);
+            if (from >= 0) y[f] = (is_v ? m.vp : m.kp)[at];
+        }
+    };
+    auto store = [&](const int2 *rows, const uint4 *y) {
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int x = f * kMoveThreads + tid;
+            const int2 p = rows[x >> m.piece_bits];
+            bool is_v;
+            const size_t at = piece(x & ((1 << m.piece_bits) - 1), p.y, is_v);
+            if (p.x >= 0) (is_v ? m.vp : m.kp)[at] = y[f];
+        }
+    };
+    uint4 y[2][kFlight];
+    long long todo = left;
+    look(where[0]);
+    look(where[1]);
+    __syncthreads();
+    load(where[0], y[0]);
+    __syncthreads();
+    int at = 0;  // todo chunks from this buffer on
+    for (; todo > 0; todo -= 2) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int next = at == 2 ? 0 : at + 1, after = next == 2 ? 0 : next + 1;
+            load(where[next], y[1 - half]);
+            look(where[after]);
+            // this chunk's loads of all threads are through (the barrier before), and so
+            // are those of every slot that it writes
+            if (half == 0 || todo > 1) store(where[at], y[half]);
+            __syncthreads();
+            at = next;
+        }
+    }
+}
+
+// ---- pages behind the end ------------------------------------------------------------
+__global__ void __launch_bounds__(256)
+    trim_kernel(Table table, int32_t *lens, int32_t *refs, int pages, int page, const int32_t *__restrict__ want,
+                uint32_t *status) {
+    wait_before();
+    let_next_start();
+    for (int r = blockIdx.x; r < table.rows; r += gridDim.x) {
+        const int n = want[r];
+        if (n < 0) continue;
+        int32_t *row = table.row(r);
+        const int first = (int)(((unsigned)n + page - 1) / (unsigned)page);
+        for (int j = first + blockIdx.y * blockDim.x + threadIdx.x; j < table.cols; j += gridDim.y * blockDim.x) {
+            const int pg = row[j];
+            if (pg < 0) continue;
+            if (pg < pages) atomicSub(refs + pg, 1);
+            else if (status) atomicOr(status, kStatusBadSeqlens);
+            row[j] = -1;
+        }
+        if (blockIdx.y == 0 && threadIdx.x == 0 && lens[r] > n) lens[r] = n;
+    }
+}
+
+// ---- host ------------------------------------------------------------------------------
+cudaError_t launch_evict(void *kp, void *vp, int pages, int page, int32_t *table, int64_t ld, int rows, int cols,
+                         int32_t *dst, int64_t dst_ld, int dst_cols, const int32_t *refs, const int32_t *lens,
+                         const int32_t *keep, int sinks, int recent, int Hkv, int es, const float *w, float *w_out,
+                         int32_t *kept, int cap, int32_t *state, uint32_t *status, int sms, cudaStream_t stream) {
+    EvictArgs a = {};
+    a.src = Table{table, ld, rows, cols};
+    a.in_place = dst == nullptr;
+    a.dst = a.in_place ? a.src : Table{dst, dst_ld, rows, dst_cols};
+    a.lens = lens;
+    a.keep = keep;
+    a.refs = refs;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.Hkv = Hkv;
+    a.cap = cap;
+    a.page = page;
+    a.pages = pages;
+    while ((1 << a.page_bits) < page) ++a.page_bits;
+    a.w = w;
+    a.w_out = w_out;
+    a.kept = kept;
+    a.state = state;
+    a.status = status;
+    const long long heads = (long long)rows * Hkv;
+    cudaError_t e = launch_early(select_kernel, dim3((unsigned)heads), kThreads, 0, stream, a);
+    if (e != cudaSuccess) return e;
+    MoveArgs m = {static_cast<uint4 *>(kp), static_cast<uint4 *>(vp), rows, es == 2 ? 4 : 5, 0, 1};
+    m.piece_bits = m.row_bits;
+    if (a.in_place) {
+        // Slices of a row down to 64 bytes, until two CTAs per SM have work.
+        while (m.piece_bits > 2 && (heads * 2 << (m.row_bits - m.piece_bits)) < 2LL * sms) --m.piece_bits;
+        m.parts = 2 << (m.row_bits - m.piece_bits);
+        return launch_early(move_kernel<true>, dim3((unsigned)(heads * m.parts)), kMoveThreads, 0, stream, a, m);
+    }
+    m.piece_bits = m.row_bits + 1;
+    const long long per = kChunk >> m.piece_bits, most = heads * (((long long)cap + per - 1) / per), ctas = 4LL * sms;
+    return launch_early(move_kernel<false>, dim3((unsigned)(most < ctas ? most : ctas)), kMoveThreads, 0, stream, a, m);
+}
+
+cudaError_t launch_trim(int32_t *table, int64_t ld, int rows, int cols, int32_t *lens, int32_t *refs, int pages, int page,
+                        const int32_t *want, uint32_t *status, cudaStream_t stream) {
+    const int y = (cols + 255) / 256;
+    return launch_early(trim_kernel, dim3((unsigned)(rows < 65535 ? rows : 65535), (unsigned)(y < 64 ? y : 64)), 256, 0,
+                        stream, Table{table, ld, rows, cols}, lens, refs, pages, page, want, status);
+}
+
+}  // namespace cache
+}  // namespace kda
