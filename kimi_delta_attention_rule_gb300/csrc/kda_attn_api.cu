@@ -28,7 +28,8 @@ cudaError_t launch_attn_decode_f32(const Args &a, const void *q, const void *kp,
                                    cudaStream_t stream);
 }  // namespace attn
 namespace weights {
-cudaError_t launch_weights(const Args &a, bool bf16, int sms, cudaStream_t stream);
+cudaError_t launch_weights_tc(Args a, int sms, cudaStream_t stream);
+cudaError_t launch_weights_f32(const Args &a, int sms, cudaStream_t stream);
 }  // namespace weights
 namespace cache {
 cudaError_t launch_evict(void *kp, void *vp, int pages, int page, int32_t *table, int64_t ld, int rows, int cols,
@@ -492,7 +493,8 @@ int kda_attn_weights(const void *q, int64_t ldq, const void *k_pages, int32_t nu
     a.scale = scale;
     a.status = status_of(workspace);
     Range range("kda_attn_weights");
-    return done(kda::weights::launch_weights(a, io == KDA_BF16, sm_count(), static_cast<cudaStream_t>(stream)));
+    return done(io == KDA_BF16 ? kda::weights::launch_weights_tc(a, sm_count(), static_cast<cudaStream_t>(stream))
+                              : kda::weights::launch_weights_f32(a, sm_count(), static_cast<cudaStream_t>(stream)));
 }
 
 size_t kda_cache_evict_workspace_size(int32_t rows) {

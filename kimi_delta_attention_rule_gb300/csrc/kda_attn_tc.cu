@@ -46,6 +46,7 @@
 #include "kda_common.cuh"
 #include "kda_tcgen05.cuh"
 #include "kda_tensormap.cuh"
+#include "kda_tma.cuh"
 
 namespace kda {
 namespace attn {
@@ -137,34 +138,6 @@ struct Bars {  // shared-memory addresses
 };
 static_assert(Bars::kDesc + kDescs * sizeof(Desc) <= Bars::kPartEnd && Bars::kGone + 16 <= 1024, "barrier area");
 
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
-}
-// Tensor copies issued by a converged warp, of which the lane with `lead` set takes
-// part: its operands stay in uniform registers (a copy issued by a lane of its own
-// choice cost 100 cycles, which at 16-row pages bounded the loads).
-__device__ __forceinline__ void tma_2d(uint32_t lead, uint32_t dst, const CUtensorMap *m, int c0, int c1, uint32_t bar) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %5, 0;\n"
-        " @q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}\n" ::"r"(dst),
-        "l"(m), "r"(c0), "r"(c1), "r"(bar), "r"(lead)
-        : "memory");
-}
-__device__ __forceinline__ void tma_3d(uint32_t lead, uint32_t dst, const CUtensorMap *m, int c0, int c1, int c2, uint32_t bar) {
-    asm volatile(
-        "{\n .reg .pred q;\n setp.ne.b32 q, %6, 0;\n"
-        " @q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}\n" ::"r"(dst),
-        "l"(m), "r"(c0), "r"(c1), "r"(c2), "r"(bar), "r"(lead)
-        : "memory");
-}
-__device__ __forceinline__ void expect_tx(uint32_t lead, uint32_t bar, uint32_t bytes) {
-    asm volatile("{\n .reg .pred q;\n setp.ne.b32 q, %2, 0;\n @q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}\n" ::"r"(bar),
-                 "r"(bytes), "r"(lead)
-                 : "memory");
-}
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *m) {
-    asm volatile("prefetch.tensormap [%0];\n" ::"l"(m) : "memory");
-}
 // shared memory (128-byte swizzle) to global; the issuing thread's bulk group
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap *m, int c0, int c1, int c2, uint32_t src) {
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(m),
@@ -1129,17 +1102,6 @@ bool map3(CUtensorMap *m, const void *p, int heads, long long rows, long long ld
     const cuuint32_t box[3] = {64u, (cuuint32_t)bh, (cuuint32_t)br};
     const cuuint32_t es[3] = {1u, 1u, 1u};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
-    const EncodeTiledFn fn = encode_tiled();
-    if (fn == nullptr) return false;
-    const cuuint64_t dims[2] = {128, (cuuint64_t)(rows > 0 ? rows : 1)};
-    const cuuint64_t strides[1] = {256};
-    const cuuint32_t box[2] = {64u, (cuuint32_t)br};
-    const cuuint32_t es[2] = {1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, es,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -1,9 +1,8 @@
-// Attention weights on CUDA cores (the formula and the work split are those of
+// Attention weights in fp32 on CUDA cores (the formula and the work split are those of
 // kda_attn_weights.cuh): 128 threads take tiles of 64 keys; a thread forms a 4 x 4 piece
 // of S = K Q^T for 32 rows at a time, its exponentials, and their sum over its rows; the
 // eight threads of a key add up in shared memory in a fixed order. Several CTAs per SM hide
 // one another's loads.
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -19,14 +18,7 @@ constexpr int kThreads = 128, kKeys = 64, kRows = 32;
 constexpr int kSmem = (kKeys + kRows) * kD * 4 + 8 * kKeys * 4 + kRows * 8;
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
-__device__ __forceinline__ float4 load4(const __nv_bfloat16 *p) {
-    const uint2 x = *reinterpret_cast<const uint2 *>(p);
-    const float2 lo = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x.x)),
-                 hi = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&x.y));
-    return make_float4(lo.x, lo.y, hi.x, hi.y);
-}
 
-template <typename IO>
 __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(16) float sm[];
     float *const Ks = sm, *const Qs = Ks + kKeys * kD, *const sums = Qs + kRows * kD, *const minus_lse = sums + 8 * kKeys;
@@ -34,7 +26,7 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_const
     wait_before();
     let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tx = tid & 15, ty = tid >> 4;
-    const IO *const q = static_cast<const IO *>(a.q), *const kp = static_cast<const IO *>(a.kp);
+    const float *const q = static_cast<const float *>(a.q), *const kp = static_cast<const float *>(a.kp);
     const int Hq = a.Hkv * a.G, page_bits = 31 - __clz(a.page);
     Walk<kKeys> walk;
     walk.init(a, blockIdx.x, gridDim.x);
@@ -118,12 +110,11 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_const
     }
 }
 
-cudaError_t launch_weights(const Args &a, bool bf16, int sms, cudaStream_t stream) {
-    const auto kernel = bf16 ? weights_kernel<__nv_bfloat16> : weights_kernel<float>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+cudaError_t launch_weights_f32(const Args &a, int sms, cudaStream_t stream) {
+    cudaError_t e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)a.B * a.Hkv * (((long long)a.cols * a.page + kKeys - 1) / kKeys), most = 4LL * sms;
-    return launch_early(kernel, dim3((unsigned)(tiles < most ? tiles : most)), kThreads, kSmem, stream, a);
+    return launch_early(weights_kernel, dim3((unsigned)(tiles < most ? tiles : most)), kThreads, kSmem, stream, a);
 }
 
 }  // namespace weights

@@ -25,5 +25,18 @@ inline EncodeTiledFn encode_tiled() {
     return fn;
 }
 
+// [rows][128] bf16, 256 bytes from row to row; box = 64 channels x br rows
+inline bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {128, (cuuint64_t)(rows > 0 ? rows : 1)};
+    const cuuint64_t strides[1] = {256};
+    const cuuint32_t box[2] = {64u, (cuuint32_t)br};
+    const cuuint32_t es[2] = {1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace attn
 }  // namespace kda
