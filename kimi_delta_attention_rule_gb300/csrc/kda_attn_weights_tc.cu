@@ -6,9 +6,9 @@
 // thread, and nothing crosses threads; a row's -lse is the same word for all of them. A CTA
 // (one per SM) streams K tiles through a ring by TMA; the rows' Q lies in shared memory
 // for as long as the CTA stays with a (sequence, head), and the next one's is copied meanwhile.
-// Roles of the 11 warps: 8 for the exponentials (two groups of four, which take the tiles in
-// turn, each with its own 256 columns of TMEM), one issues the products, one fills the ring, one
-// walks the CTA's parts ahead of the others and copies Q and lse.
+// Roles of the 14 warps: 8 for the exponentials (two groups of four, which take the tiles in
+// turn, each with its own 256 columns of TMEM), one issues the products, one fills the ring, four
+// copy Q and lse, of which the first walks the CTA's parts ahead of the others.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -31,7 +31,7 @@ using attn::ex2;
 using attn::fma2;
 using attn::mbar_arrive;
 
-constexpr int kExpWarps = 8, kWarpMma = 8, kWarpTma = 9, kWarpSched = 10, kTcThreads = 352;
+constexpr int kExpWarps = 8, kWarpMma = 8, kWarpTma = 9, kWarpRows = 10, kRowWarps = 4, kTcThreads = 448;
 constexpr int kTile = 128, kMaxRows = 256;
 constexpr uint32_t kTileBytes = 32768, kHalf = 16384;
 constexpr int kDescs = 4, kMaxRing = 6;
@@ -50,7 +50,8 @@ struct Desc {
     int last;      // no further part
     int b, h, len;
     int ta, tb;
-    int rows;
+    int seen;      // keys that its first row sees
+    int tokens;
 };
 
 // Shared memory: two Q tiles of `nq` rows (in halves of 64 channels), the ring of K tiles, then:
@@ -58,7 +59,7 @@ struct Shared {
     float minus_lse[kDescs][kMaxRows];
     int seen[kDescs][kMaxRows];  // keys that a row sees; 0: it gives nothing
     Desc desc[kDescs];
-    int least[kDescs];  // keys that all rows see (0: some give nothing)
+    int4 least[kDescs];  // keys that all rows of each of the four warps see (0: some give nothing)
     uint64_t qfull[2], qempty[2], sfull[2], sempty[2];
     uint64_t kfull[kMaxRing], kempty[kMaxRing];
     uint64_t dfull[kDescs], rfull[kDescs], dempty[kDescs];
@@ -137,7 +138,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto bar = [](const uint64_t &x) { return smem_u32(&x); };
     if (warp == kWarpTma && lane == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(bar(sh.qfull[i]), 1);
+            tc::mbar_init(bar(sh.qfull[i]), kRowWarps);
             tc::mbar_init(bar(sh.qempty[i]), 1);
             tc::mbar_init(bar(sh.sfull[i]), 1);
             tc::mbar_init(bar(sh.sempty[i]), 4);
@@ -148,8 +149,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int i = 0; i < kDescs; ++i) {
             tc::mbar_init(bar(sh.dfull[i]), 1);
-            tc::mbar_init(bar(sh.rfull[i]), 1);
-            tc::mbar_init(bar(sh.dempty[i]), kExpWarps + 2);  // and TMA, MMA
+            tc::mbar_init(bar(sh.rfull[i]), kRowWarps);
+            tc::mbar_init(bar(sh.dempty[i]), kExpWarps + 2 + kRowWarps - 1);  // and TMA, MMA
         }
         tc::mbar_init(bar(sh.drained), 1);
         sh.dead = 0;
@@ -196,10 +197,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const uint32_t slot = nd % kDescs;
             const float *const minus_lse = sh.minus_lse[slot];
             const int *const seen = sh.seen[slot];
-            const int ta = d->ta, tb = d->tb, len = d->len, rows = d->rows;
+            const int ta = d->ta, tb = d->tb, len = d->len, rows = d->tokens * a.G;
             float *const w = a.w + ((size_t)d->b * a.Hkv + d->h) * a.cap;
             if (!(alive = wait_warp(bar(sh.rfull[slot]), (nd / kDescs) & 1))) break;
-            const int least = sh.least[slot];
+            const int4 four = sh.least[slot];
+            const int least = min(min(four.x, four.y), min(four.z, four.w));
             for (int t = ta + (int)((tiles ^ group) & 1); t < tb; t += 2) {
                 const int pos = t * kTile + r;
                 const bool ok = pos < len;
@@ -213,11 +215,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc::tmem_ld_cols<1>(tS, x);
                     sum = exp_sum<16, true>(x, minus_lse, seen, 0, pos, a.scale, sum);
                 } else {
-                    for (int c = 0; c < shape.nq; c += 32) {
-                        uint32_t x[2][16];
-                        tc::tmem_ld_cols<2>(tS + c, x);
-                        if (masked || c + 32 > rows) sum = exp_sum<32, true>(x, minus_lse, seen, c, pos, a.scale, sum);
-                        else sum = exp_sum<32, false>(x, minus_lse, seen, c, pos, a.scale, sum);
+                    uint32_t x[2][2][16];  // the next columns come while these are summed
+                    auto fetch = [&](int c, uint32_t y[2][16]) {
+                        tc::tmem_ld16_raw(tS + c, y[0]);
+                        tc::tmem_ld16_raw(tS + c + 16, y[1]);
+                    };
+                    fetch(0, x[0]);
+                    for (int c0 = 0; c0 < shape.nq; c0 += 64) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int c = c0 + 32 * e;
+                            if (c >= shape.nq) break;
+                            tc::tmem_wait_ld();
+                            tc::reg_fence16(x[e][0]);
+                            tc::reg_fence16(x[e][1]);
+                            if (c + 32 < shape.nq) fetch(c + 32, x[1 - e]);
+                            if (masked || c + 32 > rows) sum = exp_sum<32, true>(x[e], minus_lse, seen, c, pos, a.scale, sum);
+                            else sum = exp_sum<32, false>(x[e], minus_lse, seen, c, pos, a.scale, sum);
+                        }
                     }
                 }
                 tc::fence_before_sync();
@@ -229,75 +244,93 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tiles += tb - ta;
             done_desc();
         }
-    } else if (warp == kWarpSched) {
-        // ---- the CTA's parts, their Q and lse ----------------------------------------------
+    } else if (warp >= kWarpRows) {
+        // ---- the CTA's parts (the first of the warps), their Q and lse -----------------------
+        const int wr = warp - kWarpRows;
         Walk<kTile> walk;
-        walk.init(a, blockIdx.x, gridDim.x);
+        if (wr == 0) walk.init(a, blockIdx.x, gridDim.x);
         const __nv_bfloat16 *const q = static_cast<const __nv_bfloat16 *>(a.q);
         const uint32_t inv_g = (65536u + a.G - 1) / a.G;  // r / G = r inv_g >> 16 for r < 1024
         const int Hq = a.Hkv * a.G;
-        Part p;
         while (true) {
-            const bool more = walk.next(a, p);
             const uint32_t slot = nd % kDescs, tile = nd & 1;
-            if (nd >= kDescs && !(alive = long_wait(bar(sh.dempty[slot]), (nd / kDescs - 1) & 1))) break;
-            Desc *const d = &sh.desc[slot];
-            const int rows = more ? p.s.tokens * a.G : 0;
-            const int seen0 = more ? p.s.len - p.s.count + a.t0 + 1 : 0;  // of the first token
-            if (lane == 0) {
-                d->last = !more;
-                if (more) {
-                    d->b = p.b;
-                    d->h = p.h;
-                    d->len = p.s.len;
-                    d->ta = p.ta;
-                    d->tb = p.tb;
-                    d->rows = rows;
+            if (wr == 0) {
+                Part p;
+                const bool more = walk.next(a, p);
+                if (nd >= kDescs && !(alive = long_wait(bar(sh.dempty[slot]), (nd / kDescs - 1) & 1))) break;
+                if (lane == 0) {
+                    Desc *const d = &sh.desc[slot];
+                    d->last = !more;
+                    if (more) {
+                        d->b = p.b;
+                        d->h = p.h;
+                        d->len = p.s.len;
+                        d->ta = p.ta;
+                        d->tb = p.tb;
+                        d->seen = p.s.len - p.s.count + a.t0 + 1;
+                        d->tokens = p.s.tokens;
+                    }
+                    mbar_arrive(bar(sh.dfull[slot]));
                 }
-                mbar_arrive(bar(sh.dfull[slot]));
+                __syncwarp();
             }
-            if (!more) break;
+            const Desc *const d = next_desc();
+            if (d == nullptr) break;
+            const int b = d->b, tokens = d->tokens, rows = tokens * a.G, seen0 = d->seen, head = d->h * a.G;
+            const size_t token0 = (size_t)b * a.T;
             // the tokens' numbers in q, two to a lane
             int tok[2] = {a.t0 + lane, a.t0 + lane + 32};
             if (a.index != nullptr) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
-                    if (lane + 32 * e < p.s.tokens) tok[e] = token_of(a, p.b, a.t0 + lane + 32 * e);
+                    if (lane + 32 * e < tokens) tok[e] = token_of(a, b, a.t0 + lane + 32 * e);
             }
-            if (nd >= 2 && !(alive = long_wait(bar(sh.qempty[tile]), (nd / 2 - 1) & 1))) break;
             auto token = [&](int i) {
                 const int lo = __shfl_sync(0xffffffffu, tok[0], i & 31), hi = __shfl_sync(0xffffffffu, tok[1], i & 31);
                 return i < 32 ? lo : hi;
             };
+            if (nd >= 2 && !(alive = long_wait(bar(sh.qempty[tile]), (nd / 2 - 1) & 1))) break;
             const uint32_t dst = base + tile * shape.q_tile();
-            for (int r0 = 0; r0 < rows; r0 += 2) {  // two rows at a time, 16 pieces each
-                const int row = r0 + (lane >> 4), i = (int)(row * inv_g >> 16), c = lane & 15;
+            const int c = lane & 15;  // a row's 16 pieces, two rows at a time
+#pragma unroll 4
+            for (int r0 = 2 * wr; r0 < rows; r0 += 2 * kRowWarps) {
+                const int row = r0 + (lane >> 4), i = (int)(row * inv_g >> 16);
                 const int tk = token(min(i, 63));
                 if (row < rows && tk >= 0)
                     cp16(dst + (c >> 3) * (uint32_t)shape.nq * 128 + row * 128 + (((c & 7) ^ (row & 7)) * 16),
-                         q + ((size_t)p.b * a.T + tk) * a.ldq + (size_t)(p.h * a.G + row - i * a.G) * kD + 8 * c);
+                         q + (token0 + tk) * a.ldq + (size_t)(head + row - i * a.G) * kD + 8 * c);
             }
             asm volatile("cp.async.commit_group;\n" ::: "memory");
+            constexpr int kEach = kMaxRows / (32 * kRowWarps);  // rows of lse of a lane
+            float l[kEach];
+            int sees[kEach];
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int row = 32 * (wr + kRowWarps * k) + lane, i = (int)(row * inv_g >> 16), tk = token(min(i, 63));
+                l[k] = -INFINITY;
+                sees[k] = seen0 + i;
+                if (row < rows && tk >= 0) l[k] = a.lse[(token0 + tk) * Hq + head + row - i * a.G];
+            }
             bool nothing = false;
-            for (int row0 = 0; row0 < shape.nq; row0 += 32) {
-                const int row = row0 + lane, i = (int)(row * inv_g >> 16), tk = token(min(i, 63));
-                float l = -INFINITY;
-                if (row < rows && tk >= 0) l = a.lse[((size_t)p.b * a.T + tk) * Hq + p.h * a.G + row - i * a.G];
-                if (row < shape.nq) {
-                    const bool none = l == -INFINITY;
-                    sh.minus_lse[slot][row] = none ? 0.f : -l;
-                    sh.seen[slot][row] = none ? 0 : seen0 + i;
-                    nothing = nothing || (none && row < rows);
-                }
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int row = 32 * (wr + kRowWarps * k) + lane;
+                const bool none = l[k] == -INFINITY;
+                sh.minus_lse[slot][row] = none ? 0.f : -l[k];
+                sh.seen[slot][row] = none ? 0 : sees[k];
+                nothing = nothing || (none && row < rows);
             }
             nothing = __any_sync(0xffffffffu, nothing);
-            if (lane == 0) sh.least[slot] = nothing ? 0 : seen0;
+            if (lane == 0) (&sh.least[slot].x)[wr] = nothing ? 0 : seen0;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(sh.rfull[slot]));
             asm volatile("cp.async.wait_group 0;\n" ::: "memory");
             tc::fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(sh.qfull[tile]));
+            if (lane == 0) {
+                mbar_arrive(bar(sh.qfull[tile]));
+                if (wr != 0) mbar_arrive(bar(sh.dempty[slot]));
+            }
             ++nd;
         }
     } else if (warp == kWarpTma) {
