@@ -591,7 +591,7 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv,
  *   q : io dtype [B, T, Hq, D] as in kda_attn_decode, T <= 64   lse : fp32 [B, T, Hq], from the
  *       attention call of these rows; a row of lse = -inf gives nothing
  *   weights : fp32 [B, Hkv, cap], cap >= every seq_lens[b]; past seq_lens[b] not touched
- *   k_pages, block_table, seq_lens, scale and alignment as in kda_attn_decode. Logits, exponentials
+ *   k_pages, block_table, seq_lens, scale (at least 1e-30) and alignment as in kda_attn_decode. Logits, exponentials
  *   and sums are fp32. No two rows may share weights; pages may be shared. A malformed length or
  *   count is flagged and its sequence skipped, a malformed index flagged and its row skipped, a
  *   page number outside the pool flagged and its keys read as zeros (workspace: 256-byte aligned, its

@@ -455,7 +455,8 @@ int kda_attn_weights(const void *q, int64_t ldq, const void *k_pages, int32_t nu
                      void *stream) {
     const int rc = check_heads(Hq, Hkv, D, io);
     if (rc != KDA_OK) return rc;
-    if (B < 0 || T < 0 || num_pages < 0 || table_cols < 0 || table_ld < table_cols || cap < 0 || !scale_ok(scale))
+    if (B < 0 || T < 0 || num_pages < 0 || table_cols < 0 || table_ld < table_cols || cap < 0 || !scale_ok(scale) ||
+        scale < 1e-30f)  // (lse / scale is formed)
         return KDA_ERR_INVALID_ARG;
     if (T > kMaxTokens || !page_ok(page_size)) return KDA_ERR_UNSUPPORTED;
     if ((long long)num_pages * Hkv * page_size > 0x7fffffffLL || (long long)B * T > 0x7fffffffLL ||

@@ -1,14 +1,22 @@
 // Attention weights in bf16 on the tensor cores (the formula and the work split are those of
 // kda_attn_weights.cuh).
 //
-// A tile is S = K Q^T of 128 keys and up to 256 (token, head) rows: the keys are the
+// A tile is S = K Q^T of 128 keys and up to 512 (token, head) rows: the keys are the
 // product's M, so that a key is a TMEM lane, its exponentials and their sum belong to one
-// thread, and nothing crosses threads; a row's -lse is the same word for all of them. A CTA
+// thread, and nothing crosses threads. The rows' lse goes through the product too, as 16
+// further channels: keys have ones there, rows the three bf16 parts of -lse / scale (24 bits), so that
+// S leaves the tensor core as q.k - lse / scale in fp32 and costs a thread one product, one
+// exponential and one sum per element. A CTA
 // (one per SM) streams K tiles through a ring by TMA; the rows' Q lies in shared memory
 // for as long as the CTA stays with a (sequence, head), and the next one's is copied meanwhile.
-// Roles of the 14 warps: 8 for the exponentials (two groups of four, which take the tiles in
-// turn, each with its own 256 columns of TMEM), one issues the products, one fills the ring, four
-// copy Q and lse, of which the first walks the CTA's parts ahead of the others.
+// Roles of the 22 warps: 16 for the exponentials (four groups of four, each with 128 columns
+// of TMEM), one issues the products, one fills the ring, four copy Q and lse, of which the
+// first walks the CTA's parts ahead of the others.
+//
+// Up to 128 rows the groups take the tiles in turn. Up to 256 (PARTS = 2) a product is two groups
+// wide, so that K is read once for both, and up to 512 (PARTS = 4) a tile is two products for all four
+// groups; the groups of a tile hand their sums to its first one. With 512 rows the Q tile
+// takes the room of two, and a CTA waits for the next part's rows.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,11 +36,11 @@ namespace weights {
 
 using attn::add2;
 using attn::ex2;
-using attn::fma2;
 using attn::mbar_arrive;
 
-constexpr int kExpWarps = 8, kWarpMma = 8, kWarpTma = 9, kWarpRows = 10, kRowWarps = 4, kTcThreads = 448;
-constexpr int kTile = 128, kMaxRows = 256;
+constexpr int kGroups = 4, kExpWarps = 4 * kGroups, kWarpMma = 16, kWarpTma = 17, kWarpRows = 18, kRowWarps = 4;
+constexpr int kTcThreads = 32 * (kWarpRows + kRowWarps);
+constexpr int kTile = 128, kMaxRows = 512;
 constexpr uint32_t kTileBytes = 32768, kHalf = 16384;
 constexpr int kDescs = 4, kMaxRing = 6;
 constexpr uint64_t kWaitNs = 2000000000;
@@ -54,26 +62,35 @@ struct Desc {
     int tokens;
 };
 
-// Shared memory: two Q tiles of `nq` rows (in halves of 64 channels), the ring of K tiles, then:
+// Shared memory: two Q tiles (PARTS = 4: one) of `nq` rows (in halves of 64 channels), the ring of K tiles, the further
+// channels of the rows of each Q tile and of the keys (8 x 8 blocks of 128 bytes, two to eight
+// rows), then:
 struct Shared {
-    float minus_lse[kDescs][kMaxRows];
     int seen[kDescs][kMaxRows];  // keys that a row sees; 0: it gives nothing
     Desc desc[kDescs];
     int4 least[kDescs];  // keys that all rows of each of the four warps see (0: some give nothing)
-    uint64_t qfull[2], qempty[2], sfull[2], sempty[2];
+    uint64_t qfull[2], qempty[2];
+    uint64_t sfull[kGroups], sempty[kGroups];  // of a group's S, or of two groups'
     uint64_t kfull[kMaxRing], kempty[kMaxRing];
     uint64_t dfull[kDescs], rfull[kDescs], dempty[kDescs];
     uint64_t drained;
+    uint64_t pfull[kGroups][4], pempty[kGroups][4];  // the sums of a warp that hands them over
+    float sums[kGroups][kTile];
     uint32_t tmem;
     int dead;
 };
 constexpr int kSmemMost = 232448;
 struct Shape {
-    int nq;    // rows of a Q tile: 16, or a multiple of 32
+    int ns;    // rows of a group: 16, or a multiple of 32 up to 128
+    int nq;    // rows of a Q tile: PARTS ns
+    int tiles;  // Q tiles
     int ring;  // K tiles
     __host__ __device__ uint32_t q_tile() const { return (uint32_t)nq * 256; }
-    __host__ __device__ uint32_t ring_at() const { return 2 * q_tile(); }
-    __host__ __device__ uint32_t shared_at() const { return ring_at() + ring * kTileBytes; }
+    __host__ __device__ uint32_t ring_at() const { return tiles * q_tile(); }
+    __host__ __device__ uint32_t q_more_at() const { return ring_at() + ring * kTileBytes; }
+    __host__ __device__ uint32_t q_more() const { return (uint32_t)nq * 32; }
+    __host__ __device__ uint32_t k_more_at() const { return q_more_at() + tiles * q_more(); }
+    __host__ __device__ uint32_t shared_at() const { return k_more_at() + kTile * 32; }
     __host__ __device__ uint32_t bytes() const { return shared_at() + (uint32_t)sizeof(Shared); }
 };
 
@@ -94,26 +111,26 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
 }
 
-// The sum of exp(scale s - lse) over N columns of S from column c on.
+// Byte of (row, channel) of the further channels.
+__device__ __forceinline__ uint32_t more_at(int row, int ch) { return tc::kmajor_off(row, ch, 128, 256); }
+
+// The sum of 2^(c s) over N columns of S from column `at` on.
 template <int N, bool MASKED>
-__device__ __forceinline__ float2 exp_sum(uint32_t x[N / 16][16], const float *minus_lse, const int *seen, int c, int pos,
-                                          float scale, float2 sum) {
-    const float2 scale2 = make_float2(scale, scale), log2e = make_float2(attn::kLog2e, attn::kLog2e);
+__device__ __forceinline__ float2 exp_sum(uint32_t x[N / 16][16], const int *seen, int at, int pos, float c, float2 sum) {
+    const float2 c2 = make_float2(c, c);
 #pragma unroll
     for (int i = 0; i < N; i += 4) {
-        const float4 l = *reinterpret_cast<const float4 *>(minus_lse + c + i);
         float y[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(x[(i + e) / 16][(i + e) % 16]);
         if (MASKED) {
-            const int4 n = *reinterpret_cast<const int4 *>(seen + c + i);
+            const int4 n = *reinterpret_cast<const int4 *>(seen + at + i);
             y[0] = pos < n.x ? y[0] : -INFINITY;
             y[1] = pos < n.y ? y[1] : -INFINITY;
             y[2] = pos < n.z ? y[2] : -INFINITY;
             y[3] = pos < n.w ? y[3] : -INFINITY;
         }
-        float2 u = mul2(fma2(make_float2(y[0], y[1]), scale2, make_float2(l.x, l.y)), log2e);
-        float2 v = mul2(fma2(make_float2(y[2], y[3]), scale2, make_float2(l.z, l.w)), log2e);
+        float2 u = mul2(make_float2(y[0], y[1]), c2), v = mul2(make_float2(y[2], y[3]), c2);
         u.x = ex2(u.x);
         u.y = ex2(u.y);
         v.x = ex2(v.x);
@@ -123,10 +140,11 @@ __device__ __forceinline__ float2 exp_sum(uint32_t x[N / 16][16], const float *m
     return sum;
 }
 
-// SMALL: nq = 16.
-template <bool SMALL>
+// PARTS groups share a tile; SMALL: 16 rows at the most.
+template <int PARTS, bool SMALL>
 __global__ void __launch_bounds__(kTcThreads, 1)
     weights_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map, const Shape shape) {
+    constexpr int kQTiles = PARTS == 4 ? 1 : 2;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     Shared &sh = *reinterpret_cast<Shared *>(sm + shape.shared_at());
@@ -140,8 +158,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         for (int i = 0; i < 2; ++i) {
             tc::mbar_init(bar(sh.qfull[i]), kRowWarps);
             tc::mbar_init(bar(sh.qempty[i]), 1);
-            tc::mbar_init(bar(sh.sfull[i]), 1);
-            tc::mbar_init(bar(sh.sempty[i]), 4);
         }
         for (int i = 0; i < kMaxRing; ++i) {
             tc::mbar_init(bar(sh.kfull[i]), 1);
@@ -153,12 +169,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc::mbar_init(bar(sh.dempty[i]), kExpWarps + 2 + kRowWarps - 1);  // and TMA, MMA
         }
         tc::mbar_init(bar(sh.drained), 1);
+        for (int i = 0; i < 4; ++i) {
+            tc::mbar_init(bar(sh.sfull[i]), 1);
+            tc::mbar_init(bar(sh.sempty[i]), PARTS == 1 ? 4 : 8);
+            for (int j = 0; j < 4; ++j) {
+                tc::mbar_init(bar(sh.pfull[i][j]), 1);
+                tc::mbar_init(bar(sh.pempty[i][j]), 1);
+            }
+        }
         sh.dead = 0;
         tc::fence_mbar_init();
         attn::prefetch_map(&map);
     } else if (warp == kWarpMma) {
         tc::tmem_alloc(smem_u32(&sh.tmem), 512);
         tc::tmem_relinquish();
+    }
+    if (tid < kTile) {  // the keys' further channels: 1, 1, 1, 0, ..
+        uint4 *const to = reinterpret_cast<uint4 *>(sm + shape.k_more_at() + more_at(tid, 0));
+        to[0] = make_uint4(pack_bf16(1.f, 1.f), pack_bf16(1.f, 0.f), 0u, 0u);
+        to[8] = make_uint4(0u, 0u, 0u, 0u);
+        tc::fence_async_smem();
     }
     tc::fence_before_sync();
     __syncthreads();
@@ -190,55 +220,62 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp < kExpWarps) {
         // ---- exponentials: thread = key -------------------------------------------------
-        const int group = warp >> 2, r = 32 * (warp & 3) + lane;
-        const uint32_t tS = tm + ((uint32_t)(32 * (warp & 3)) << 16) + 256 * group;
+        const int group = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
+        const int part = group % PARTS, lead = group - part;  // which rows of a tile; the group that writes
+        const int buffer = PARTS == 1 ? group : group >> 1;
+        const uint32_t tS = tm + ((uint32_t)(32 * quad) << 16) + (PARTS == 1 ? 128 * group : 256 * buffer + (group & 1) * shape.ns);
+        const float c = a.scale * attn::kLog2e;
+        constexpr int kTurns = kGroups / PARTS;  // every so many tiles are this group's
         uint32_t tiles = 0, mine = 0;  // of the CTA, of this group
         while (const Desc *d = next_desc()) {
             const uint32_t slot = nd % kDescs;
-            const float *const minus_lse = sh.minus_lse[slot];
-            const int *const seen = sh.seen[slot];
-            const int ta = d->ta, tb = d->tb, len = d->len, rows = d->tokens * a.G;
+            const int *const seen = sh.seen[slot] + part * shape.ns;
+            const int ta = d->ta, tb = d->tb, len = d->len, rows = d->tokens * a.G - part * shape.ns;
             float *const w = a.w + ((size_t)d->b * a.Hkv + d->h) * a.cap;
             if (!(alive = wait_warp(bar(sh.rfull[slot]), (nd / kDescs) & 1))) break;
             const int4 four = sh.least[slot];
             const int least = min(min(four.x, four.y), min(four.z, four.w));
-            for (int t = ta + (int)((tiles ^ group) & 1); t < tb; t += 2) {
+            for (int t = ta + (int)((group / PARTS - tiles) % kTurns); t < tb; t += kTurns, ++mine) {
                 const int pos = t * kTile + r;
-                const bool ok = pos < len;
+                const bool ok = pos < len && part == 0;
                 const float before = ok ? w[pos] : 0.f;
-                if (!(alive = wait_warp(bar(sh.sfull[group]), mine++ & 1))) break;
-                tc::fence_after_sync();
                 const bool masked = least < (t + 1) * kTile;
                 float2 sum = make_float2(0.f, 0.f);
+                if (!(alive = wait_warp(bar(sh.sfull[buffer]), mine & 1))) break;
+                tc::fence_after_sync();
                 if (SMALL) {
                     uint32_t x[1][16];
                     tc::tmem_ld_cols<1>(tS, x);
-                    sum = exp_sum<16, true>(x, minus_lse, seen, 0, pos, a.scale, sum);
+                    sum = exp_sum<16, true>(x, seen, 0, pos, c, sum);
                 } else {
-                    uint32_t x[2][2][16];  // the next columns come while these are summed
-                    auto fetch = [&](int c, uint32_t y[2][16]) {
-                        tc::tmem_ld16_raw(tS + c, y[0]);
-                        tc::tmem_ld16_raw(tS + c + 16, y[1]);
-                    };
-                    fetch(0, x[0]);
-                    for (int c0 = 0; c0 < shape.nq; c0 += 64) {
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int c = c0 + 32 * e;
-                            if (c >= shape.nq) break;
-                            tc::tmem_wait_ld();
-                            tc::reg_fence16(x[e][0]);
-                            tc::reg_fence16(x[e][1]);
-                            if (c + 32 < shape.nq) fetch(c + 32, x[1 - e]);
-                            if (masked || c + 32 > rows) sum = exp_sum<32, true>(x[e], minus_lse, seen, c, pos, a.scale, sum);
-                            else sum = exp_sum<32, false>(x[e], minus_lse, seen, c, pos, a.scale, sum);
-                        }
+                    for (int at = 0; at < shape.ns; at += 32) {
+                        uint32_t x[2][16];
+                        tc::tmem_ld_cols<2>(tS + at, x);
+                        if (masked || at + 32 > rows) sum = exp_sum<32, true>(x, seen, at, pos, c, sum);
+                        else sum = exp_sum<32, false>(x, seen, at, pos, c, sum);
                     }
                 }
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.sempty[group]));
-                if (ok) w[pos] = before + (sum.x + sum.y);
+                if (lane == 0) mbar_arrive(bar(sh.sempty[buffer]));
+                float total = sum.x + sum.y;
+                if (part > 0) {
+                    if (mine > 0 && !(alive = wait_warp(bar(sh.pempty[group][quad]), (mine - 1) & 1))) break;
+                    sh.sums[group][r] = total;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(sh.pfull[group][quad]));
+                    continue;
+                }
+#pragma unroll
+                for (int e = 1; e < PARTS; ++e) {
+                    if (alive) alive = wait_warp(bar(sh.pfull[lead + e][quad]), mine & 1);
+                    if (!alive) break;
+                    total += sh.sums[lead + e][r];
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(sh.pempty[lead + e][quad]));
+                }
+                if (!alive) break;
+                if (ok) w[pos] = before + total;
             }
             if (!alive) break;
             tiles += tb - ta;
@@ -253,7 +290,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t inv_g = (65536u + a.G - 1) / a.G;  // r / G = r inv_g >> 16 for r < 1024
         const int Hq = a.Hkv * a.G;
         while (true) {
-            const uint32_t slot = nd % kDescs, tile = nd & 1;
+            const uint32_t slot = nd % kDescs, tile = nd % kQTiles;
             if (wr == 0) {
                 Part p;
                 const bool more = walk.next(a, p);
@@ -289,7 +326,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const int lo = __shfl_sync(0xffffffffu, tok[0], i & 31), hi = __shfl_sync(0xffffffffu, tok[1], i & 31);
                 return i < 32 ? lo : hi;
             };
-            if (nd >= 2 && !(alive = long_wait(bar(sh.qempty[tile]), (nd / 2 - 1) & 1))) break;
+            if (nd >= kQTiles && !(alive = long_wait(bar(sh.qempty[tile]), (nd / kQTiles - 1) & 1))) break;
             const uint32_t dst = base + tile * shape.q_tile();
             const int c = lane & 15;  // a row's 16 pieces, two rows at a time
 #pragma unroll 4
@@ -301,7 +338,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                          q + (token0 + tk) * a.ldq + (size_t)(head + row - i * a.G) * kD + 8 * c);
             }
             asm volatile("cp.async.commit_group;\n" ::: "memory");
-            constexpr int kEach = kMaxRows / (32 * kRowWarps);  // rows of lse of a lane
+            constexpr int kEach = PARTS;  // rows of lse of a lane
             float l[kEach];
             int sees[kEach];
 #pragma unroll
@@ -316,7 +353,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int k = 0; k < kEach; ++k) {
                 const int row = 32 * (wr + kRowWarps * k) + lane;
                 const bool none = l[k] == -INFINITY;
-                sh.minus_lse[slot][row] = none ? 0.f : -l[k];
+                if (row < shape.nq) {
+                    // (finite, since what is infinite times the keys' zeros is NaN: 2^(c x) is 0 or infinite far before)
+                    float x = none ? 0.f : -l[k] / a.scale;
+                    if (!(x != x)) x = fminf(fmaxf(x, -3e38f), 3e38f);
+                    const float hi = __bfloat162float(__float2bfloat16_rn(x)), mid = __bfloat162float(__float2bfloat16_rn(x - hi));
+                    unsigned char *const to = sm + shape.q_more_at() + tile * shape.q_more() + more_at(row, 0);
+                    *reinterpret_cast<uint4 *>(to) = make_uint4(pack_bf16(hi, mid), pack_bf16(x - hi - mid, 0.f), 0u, 0u);
+                    *reinterpret_cast<uint4 *>(to + 128) = make_uint4(0u, 0u, 0u, 0u);
+                }
                 sh.seen[slot][row] = none ? 0 : sees[k];
                 nothing = nothing || (none && row < rows);
             }
@@ -379,29 +424,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             alive = wait_warp(bar(sh.kfull[i]), ((kv + shape.ring - 1 - i) / shape.ring - 1) & 1) && alive;
     } else {
         // ---- products ------------------------------------------------------------------------
-        const uint32_t lead = tc::elect_one(), idesc = tc::idesc_f16(kTile, shape.nq, 0, 0, 0);
+        const uint64_t k_more = tc::smem_desc(base + shape.k_more_at(), 128, 256), q_more = tc::smem_desc(base + shape.q_more_at(), 128, 256);
+        const uint32_t lead = tc::elect_one(), idesc = tc::idesc_f16(kTile, (PARTS == 1 ? 1 : 2) * shape.ns, 0, 0, 0);
         const uint64_t q_desc = tc::smem_desc_sw128(base, 16, 1024), k_desc = tc::smem_desc_sw128(base + shape.ring_at(), 16, 1024);
         uint32_t kv = 0;
         while (const Desc *d = next_desc()) {
             const int n = d->tb - d->ta;
-            const uint32_t tile = nd & 1;
-            if (!(alive = wait_warp(bar(sh.qfull[tile]), (nd >> 1) & 1))) break;
-            const uint64_t qd = q_desc + tile * (shape.q_tile() >> 4);
+            const uint32_t tile = nd % kQTiles;
+            if (!(alive = wait_warp(bar(sh.qfull[tile]), (nd / kQTiles) & 1))) break;
             for (int t = 0; t < n; ++t) {
-                const uint32_t slot = kv % shape.ring, s = kv & 1;
+                const uint32_t slot = kv % shape.ring;
                 if (!(alive = wait_warp(bar(sh.kfull[slot]), (kv / shape.ring) & 1))) break;
-                if (kv >= 2 && !(alive = wait_warp(bar(sh.sempty[s]), ((kv >> 1) - 1) & 1))) break;
-                ++kv;
-                tc::fence_after_sync();
                 const uint64_t kd = k_desc + slot * (kTileBytes >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 8; ++kk) {
-                    const uint32_t k16 = (kk & 3) * 32, half = kk >> 2;
-                    tc::mma_f16_lead(lead, tm + 256 * s, kd + ((half * kHalf + k16) >> 4),
-                                     qd + ((half * (uint32_t)shape.nq * 128 + k16) >> 4), idesc, kk > 0);
+                for (int e = 0; e < (PARTS == 4 ? 2 : 1); ++e) {
+                    const uint32_t s = PARTS == 1 ? kv & 3 : (PARTS == 2 ? kv & 1 : e);
+                    const uint32_t used = PARTS == 1 ? kv >> 2 : (PARTS == 2 ? kv >> 1 : kv);  // times that this S has been
+                    if (alive && used > 0) alive = wait_warp(bar(sh.sempty[s]), (used - 1) & 1);
+                    if (!alive) break;
+                    tc::fence_after_sync();
+                    const uint32_t tS = tm + (PARTS == 1 ? 128 : 256) * s, row = e * 2 * shape.ns;
+                    const uint64_t qd = q_desc + ((tile * shape.q_tile() + row * 128) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk) {
+                        const uint32_t k16 = (kk & 3) * 32, half = kk >> 2;
+                        tc::mma_f16_lead(lead, tS, kd + ((half * kHalf + k16) >> 4),
+                                         qd + ((half * (uint32_t)shape.nq * 128 + k16) >> 4), idesc, kk > 0);
+                    }
+                    tc::mma_f16_lead(lead, tS, k_more, q_more + ((tile * shape.q_more() + row * 32) >> 4), idesc, 1);
+                    tc::mma_commit_lead(lead, bar(sh.sfull[s]));
                 }
+                if (!alive) break;
+                ++kv;
                 tc::mma_commit_lead(lead, bar(sh.kempty[slot]));
-                tc::mma_commit_lead(lead, bar(sh.sfull[s]));
             }
             if (!alive) break;
             tc::mma_commit_lead(lead, bar(sh.qempty[tile]));
@@ -420,26 +475,25 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == kWarpMma) tc::tmem_dealloc(tm, 512);
 }
 
-template <bool SMALL>
+template <int PARTS, bool SMALL>
 static cudaError_t launch_form(const Args &a, const CUtensorMap &map, const Shape &shape, unsigned ctas, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        e = cudaFuncSetAttribute(weights_tc_kernel<SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+        e = cudaFuncSetAttribute(weights_tc_kernel<PARTS, SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    return launch_early(weights_tc_kernel<SMALL>, dim3(ctas), kTcThreads, shape.bytes(), stream, a, map, shape);
+    return launch_early(weights_tc_kernel<PARTS, SMALL>, dim3(ctas), kTcThreads, shape.bytes(), stream, a, map, shape);
 }
 
 cudaError_t launch_weights_tc(Args a, int sms, cudaStream_t stream) {
     CUtensorMap map;
     if (!attn::map2(&map, a.kp, (long long)a.pages * a.Hkv * a.page, a.page < kTile ? a.page : kTile))
         return cudaErrorInvalidValue;
-    // tokens of a launch: as many as have 256 rows (a second launch reads K again, mostly from L2, and
-    // with so many rows the exponentials take as long as a tile's way from HBM), evenly shared
+    // tokens of a launch: as many as have 512 rows, evenly shared
     const int most = kMaxRows / a.G, T = a.T, launches = (T + most - 1) / most, per = (T + launches - 1) / launches;
     const long long tiles = (long long)a.B * a.Hkv * (((long long)a.cols * a.page + kTile - 1) / kTile);
     for (int t0 = 0; t0 < T; t0 += per) {
@@ -447,12 +501,18 @@ cudaError_t launch_weights_tc(Args a, int sms, cudaStream_t stream) {
         a.t1 = t0 + per < T ? t0 + per : T;
         Shape shape;
         const int rows = (a.t1 - a.t0) * a.G;
-        shape.nq = rows <= 16 ? 16 : (rows + 31) / 32 * 32;
-        shape.ring = ((int)kSmemMost - (int)sizeof(Shared) - (int)shape.ring_at()) / (int)kTileBytes;
+        const int parts = rows <= 128 ? 1 : (rows <= 256 ? 2 : 4);
+        shape.ns = rows <= 16 ? 16 : ((rows + parts - 1) / parts + 31) / 32 * 32;
+        shape.nq = parts * shape.ns;
+        shape.tiles = parts == 4 ? 1 : 2;
+        shape.ring = 0;
+        shape.ring = (kSmemMost - (int)shape.bytes()) / (int)kTileBytes;
         if (shape.ring > kMaxRing) shape.ring = kMaxRing;
         const unsigned ctas = (unsigned)(tiles < sms ? tiles : sms);
-        const cudaError_t e = shape.nq == 16 ? launch_form<true>(a, map, shape, ctas, stream)
-                                             : launch_form<false>(a, map, shape, ctas, stream);
+        const cudaError_t e = rows <= 16   ? launch_form<1, true>(a, map, shape, ctas, stream)
+                              : parts == 1 ? launch_form<1, false>(a, map, shape, ctas, stream)
+                              : parts == 2 ? launch_form<2, false>(a, map, shape, ctas, stream)
+                                           : launch_form<4, false>(a, map, shape, ctas, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -30,7 +30,7 @@ def test_refusals():
         return lib.kda_attn_weights(*a.values(), None)
     for kw in (dict(D=64), dict(io=2), dict(T=65), dict(page=8), dict(page=48), dict(Hq=130, ldq=130 * 128)):
         assert f(**kw) == UNSUPPORTED, kw
-    for kw in (dict(Hq=9), dict(B=-1), dict(T=-1), dict(P=-1), dict(ld=3), dict(cap=-1), dict(scale=0.0), dict(scale=math.nan),
+    for kw in (dict(Hq=9), dict(B=-1), dict(T=-1), dict(P=-1), dict(ld=3), dict(cap=-1), dict(scale=0.0), dict(scale=1e-31), dict(scale=math.nan),
                dict(q=None), dict(kp=None), dict(table=None), dict(lens=None), dict(lse=None), dict(w=None), dict(q=ODD), dict(kp=ODD),
                dict(ws=ODD), dict(ldq=1000), dict(ldq=1028), dict(P=1 << 27), dict(cols=1 << 24, ld=1 << 24, page=256),
                dict(w=ctypes.c_void_p(0x100002)), dict(B=1 << 20, T=64, Hq=8, Hkv=2, ldq=1 << 40)):
