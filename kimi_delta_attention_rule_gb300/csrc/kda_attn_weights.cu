@@ -1,8 +1,8 @@
 // Attention weights in fp32 on CUDA cores (the formula and the work split are those of
-// kda_attn_weights.cuh): 128 threads take tiles of 64 keys; a thread forms a 4 x 4 piece
-// of S = K Q^T for 32 rows at a time, its exponentials, and their sum over its rows; the
-// eight threads of a key add up in shared memory in a fixed order. Several CTAs per SM hide
-// one another's loads.
+// kda_attn_weights.cuh): 128 threads take tiles of 64 keys; a thread forms a 4 x RPT piece
+// of S = K Q^T for 8 RPT rows at a time (RPT = 1 where there are no more than eight, else 4), its
+// exponentials, and their sum over its rows; the eight threads of a key add up in shared memory in a
+// fixed order. Several CTAs per SM hide one another's loads.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -12,15 +12,22 @@
 namespace kda {
 namespace weights {
 
-constexpr int kThreads = 128, kKeys = 64, kRows = 32;
+constexpr int kThreads = 128, kKeys = 64;
 // Rows of K and Q are read by neighbouring threads: the 16-byte pieces of a row stand in the order
 // of (piece xor row % 8).
-constexpr int kSmem = (kKeys + kRows) * kD * 4 + 8 * kKeys * 4 + kRows * 8;
+constexpr int smem_of(int rows) { return (kKeys + rows) * kD * 4 + 8 * kKeys * 4 + rows * 8; }
 
 __device__ __forceinline__ float4 load4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
+__device__ __forceinline__ void cp16(float *dst, const float *src, bool ok) {  // (not ok: zeros)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(dst)), "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+template <int RPT>
 __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(16) float sm[];
+    constexpr int kRows = 8 * RPT;
     float *const Ks = sm, *const Qs = Ks + kKeys * kD, *const sums = Qs + kRows * kD, *const minus_lse = sums + 8 * kKeys;
     int *const seen = reinterpret_cast<int *>(minus_lse + kRows);  // keys that a row sees
     wait_before();
@@ -35,17 +42,23 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_const
         const int rows = p.s.tokens * a.G;
         for (int t = p.ta; t < p.tb; ++t) {
             __syncthreads();  // the last tile is through
-            for (int r = warp; r < kKeys; r += kThreads / 32) {
-                const int pos = t * kKeys + r;
-                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (pos < p.s.len) {
+            {  // a warp copies the rows warp, warp + 4, ..: lane i knows where row warp + 4 i is
+                const int pos = t * kKeys + warp + 4 * (lane & 15);
+                bool in = pos < p.s.len;
+                long long off = 0;
+                if (in) {
                     const int pg = a.table[(size_t)p.b * a.table_ld + (pos >> page_bits)];
-                    if (pg >= 0 && pg < a.pages)
-                        x = load4(kp + (((size_t)pg * a.Hkv + p.h) * a.page + (pos & (a.page - 1))) * kD + 4 * lane);
-                    else if (lane == 0)
-                        flag(a);
+                    in = pg >= 0 && pg < a.pages;
+                    if (in) off = (((long long)pg * a.Hkv + p.h) * a.page + (pos & (a.page - 1))) * kD;
+                    else flag(a);  // zeros instead
                 }
-                *reinterpret_cast<float4 *>(Ks + r * kD + 4 * (lane ^ (r & 7))) = x;
+                const unsigned rows_ok = __ballot_sync(0xffffffffu, in);
+#pragma unroll 4
+                for (int i = 0; i < kKeys / 4; ++i) {
+                    const int r = warp + 4 * i;
+                    cp16(Ks + r * kD + 4 * (lane ^ (r & 7)), kp + __shfl_sync(0xffffffffu, off, i) + 4 * lane, rows_ok >> i & 1);
+                }
+                asm volatile("cp.async.commit_group;\n" ::: "memory");
             }
             float sum[4] = {0.f, 0.f, 0.f, 0.f};  // keys tx + 16 e
             for (int r0 = 0; r0 < rows; r0 += kRows) {
@@ -67,19 +80,20 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_const
                         }
                     }
                 }
+                asm volatile("cp.async.wait_group 0;\n" ::: "memory");
                 __syncthreads();
-                float s[4][4] = {};
+                float s[4][RPT] = {};
 #pragma unroll 4
                 for (int d = 0; d < kD; d += 4) {
-                    float4 kk[4], qq[4];
+                    float4 kk[4], qq[RPT];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) kk[e] = load4(Ks + (tx + 16 * e) * kD + (d ^ ((tx & 7) * 4)));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) qq[i] = load4(Qs + (ty + 8 * i) * kD + (d ^ (ty * 4)));
+                    for (int i = 0; i < RPT; ++i) qq[i] = load4(Qs + (ty + 8 * i) * kD + (d ^ (ty * 4)));
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < RPT; ++i) {
                             s[e][i] = fmaf(kk[e].x, qq[i].x, s[e][i]);
                             s[e][i] = fmaf(kk[e].y, qq[i].y, s[e][i]);
                             s[e][i] = fmaf(kk[e].z, qq[i].z, s[e][i]);
@@ -87,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_const
                         }
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < RPT; ++i) {
                     const int r = ty + 8 * i;
                     const float l = minus_lse[r];
                     const int n = seen[r];
@@ -110,11 +124,17 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_const
     }
 }
 
-cudaError_t launch_weights_f32(const Args &a, int sms, cudaStream_t stream) {
-    cudaError_t e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+template <int RPT>
+static cudaError_t launch_form(const Args &a, int sms, cudaStream_t stream) {
+    constexpr int bytes = smem_of(8 * RPT);
+    const cudaError_t e = cudaFuncSetAttribute(weights_kernel<RPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const long long tiles = (long long)a.B * a.Hkv * (((long long)a.cols * a.page + kKeys - 1) / kKeys), most = 4LL * sms;
-    return launch_early(weights_kernel, dim3((unsigned)(tiles < most ? tiles : most)), kThreads, kSmem, stream, a);
+    return launch_early(weights_kernel<RPT>, dim3((unsigned)(tiles < most ? tiles : most)), kThreads, bytes, stream, a);
+}
+
+cudaError_t launch_weights_f32(const Args &a, int sms, cudaStream_t stream) {
+    return a.T * a.G <= 8 ? launch_form<1>(a, sms, stream) : launch_form<4>(a, sms, stream);
 }
 
 }  // namespace weights
