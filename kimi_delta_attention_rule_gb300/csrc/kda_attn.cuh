@@ -10,9 +10,10 @@
 // the last tile holds the drafts alone.
 //
 // Window (WIN). A row that sees the keys below `seen` looks only at those from
-// seen - window on and at the first `sinks`. An item's tiles are then those of the sinks
-// and those from its first row's window on; the ones between are left out, and all
-// below counts tiles without them (`Span` knows which tile of the sequence each one is).
+// seen - window on and at the first `sinks`. An item's keys are then the sinks and, right
+// behind them, those from its first row's window on, and all below counts keys and tiles
+// in that order, without the ones between (Span): a tile of sinks alone for every item would
+// cost as much as one of 128 keys.
 //
 // Split. All items, in order, form one line of weighted work (their visible
 // keys plus a fixed share for an item's start and end); CTA c takes the part
@@ -128,6 +129,8 @@ struct Args {
     float inv_block, inv_min_part;
     float scale;
     int window, sinks;       // WIN; window = 0: none
+    int sink_rows;           // `sinks`, and the multiple (a power of two) of key rows at
+    int grain;               // which an item's window starts, as copies need them
     // device pointers
     const int32_t *cu_q, *cu_k;      // prefill offsets (NULL: equal lengths)
     const int32_t *table, *lens;     // decode
@@ -149,9 +152,13 @@ inline void set_unit(Args &a, double keys) {
     a.inv_unit = 1.f / a.unit;
 }
 
-// An upper bound of an item's keys through a window of tiles of kt keys (`keys`: without it).
-inline long long window_keys(const Args &a, long long keys, int kt) {
-    const long long most = (long long)a.window + a.sinks + a.block + 3 * kt;
+// Sets the copies' grains, and gives an upper bound of an item's keys through its window
+// (`keys`: without it).
+inline long long set_window(Args &a, long long keys, int sink_grain, int grain) {
+    const long long rows = ((long long)a.sinks + sink_grain - 1) & -(long long)sink_grain;
+    a.sink_rows = (int)(rows < 0x7fffff00 ? rows : 0x7fffff00);  // (which no sequence is as long as)
+    a.grain = grain;
+    const long long most = (long long)a.window + rows + a.block + grain + 2 * 128;
     return keys < most ? keys : most;
 }
 
@@ -251,31 +258,29 @@ __device__ __forceinline__ int item_keys(const Args &a, const Seq &s, int i) {
     const int v = left > 0 ? s.Lk - left : s.Lk;
     return v > 0 ? v : 0;
 }
-template <bool PAGED, int KT>
-__device__ __forceinline__ int item_tiles(const Args &a, const Seq &s, int i) {
-    return (int)(((unsigned)item_keys<PAGED>(a, s, i) + KT - 1) / KT) + (PAGED ? a.has_new : 0);
-}
-// Which tiles of its sequence an item has: the first `sinks` of them, none of the next
-// `skip`, the others; nt in all (with the drafts').
+// An item's keys: the first `sinks` ones, then those from sinks + shift on.
 struct Span {
-    int sinks, skip, nt;
-    __device__ __forceinline__ int tile(int t) const { return t < sinks ? t : t + skip; }
+    int sinks, shift;
+    __device__ __forceinline__ int key(int v) const { return v < sinks ? v : v + shift; }
 };
 // The first key that a row's window holds if the row sees `seen` keys.
 __device__ __forceinline__ int window_start(const Args &a, int seen) { return seen > a.window ? seen - a.window : 0; }
-template <bool PAGED, int KT, bool WIN>
+template <bool PAGED, bool WIN>
 __device__ __forceinline__ Span item_span(const Args &a, const Seq &s, int i) {
-    Span r = {0, 0, item_tiles<PAGED, KT>(a, s, i)};
+    Span r = {0, 0};
     if (WIN) {  // (decode: the first of a chain, or any of a tree, may see one new token, itself)
-        const int lo = window_start(a, PAGED ? s.Lk + a.has_new : s.Lk - s.Lq + i * a.block + 1) / KT;
-        const int sinks = (int)(((unsigned)a.sinks + KT - 1) / KT);
-        if (sinks < lo) {
-            r.sinks = sinks;
-            r.skip = lo - sinks;
-            r.nt -= r.skip;
+        const int lo = window_start(a, PAGED ? s.Lk + a.has_new : s.Lk - s.Lq + i * a.block + 1) & -a.grain;
+        if (a.sink_rows < lo) {
+            r.sinks = a.sink_rows;
+            r.shift = lo - a.sink_rows;
         }
     }
     return r;
+}
+template <bool PAGED, int KT, bool WIN>
+__device__ __forceinline__ int item_tiles(const Args &a, const Seq &s, int i) {
+    return (int)(((unsigned)(item_keys<PAGED>(a, s, i) - item_span<PAGED, WIN>(a, s, i).shift) + KT - 1) / KT) +
+           (PAGED ? a.has_new : 0);
 }
 // An item's start and end, in keys. (Decode: an item of few tiles is a chain of
 // latencies, one of many is bound by its loads.)
@@ -293,7 +298,7 @@ template <bool PAGED, int KT, bool WIN>
 __device__ __forceinline__ uint32_t items_weight(const Args &a, const Seq &s, int i) {
     float w;
     if (PAGED) {
-        const int nt = item_span<PAGED, KT, WIN>(a, s, 0).nt;
+        const int nt = item_tiles<PAGED, KT, WIN>(a, s, 0);
         w = (float)i * (float)(item_extra<PAGED, KT>(a, nt) + nt * KT);
     } else {
         const int d = s.Lk - s.Lq, full = i < s.ni ? i : s.ni - 1;  // items without the sequence's last token
@@ -301,7 +306,7 @@ __device__ __forceinline__ uint32_t items_weight(const Args &a, const Seq &s, in
         const float unseen = fmaxf(0.f, floorf((float)-d * a.inv_block));  // items that see nothing
         float last = (float)full, most = 0.f;
         if (WIN) {  // items from `last` on have `most` keys
-            most = (float)a.window + block + (float)(((unsigned)a.sinks + KT - 1) / KT * KT);
+            most = (float)a.window + block + (float)a.sink_rows;
             last = fminf(last, fmaxf(unseen, floorf((most - (float)d) * a.inv_block)));
         }
         const float count = fmaxf(0.f, last - unseen);
@@ -338,7 +343,7 @@ __device__ __forceinline__ Point point_in_seq(const Args &a, const Seq &s, int n
         lo += k * step;
     }
     p.i = lo;
-    const int nt = item_span<PAGED, KT, WIN>(a, s, lo).nt;
+    const int nt = item_tiles<PAGED, KT, WIN>(a, s, lo);
     const float y = (float)(x - items_weight<PAGED, KT, WIN>(a, s, lo)) * a.unit - 0.5f * (float)item_extra<PAGED, KT>(a, nt);
     const int t = (int)fminf(fmaxf(0.f, y * (1.f / KT) + 0.5f), (float)nt);
     // short pieces are not worth their join: such a cut moves to the item's edge
@@ -430,7 +435,7 @@ __device__ __forceinline__ bool split_point(const Args &a, int c, Point &p0, Seq
 struct Part {
     int n, h, i;
     int ta, tb, nt;   // tiles of this part, tiles of the item
-    int sinks, skip;  // WIN: of the item's Span
+    Span span;
     int q0, tokens;   // first token row, valid tokens of the item
     int first_tok;    // the item's first token within its sequence
     int Lq, Lk, k0;
@@ -438,10 +443,8 @@ struct Part {
 };
 template <bool PAGED, int KT, bool WIN>
 __device__ __forceinline__ void item_part(const Args &a, const Seq &s, Part &p) {
-    const Span span = item_span<PAGED, KT, WIN>(a, s, p.i);
-    p.nt = span.nt;
-    p.sinks = span.sinks;
-    p.skip = span.skip;
+    p.span = item_span<PAGED, WIN>(a, s, p.i);
+    p.nt = item_tiles<PAGED, KT, WIN>(a, s, p.i);
     p.first_tok = p.i * a.block;
     p.q0 = s.q0 + p.first_tok;
     p.tokens = min(a.block, s.Lq - p.first_tok);

@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             }
             if (WIN) from[i] = window_start(a, PAGED && a.has_new ? p.Lk + max(1, __popcll(bits[i])) : seen[i]);
         }
-        const Span span = {p.sinks, p.skip, p.nt};
         // the first key of all rows' windows: those before it, the sinks apart, are not read
         const int first = WIN ? window_start(a, PAGED ? p.Lk + a.has_new : p.Lk - p.Lq + p.first_tok + 1) : 0;
         // A warp copies the rows warp, warp + 4, ..: lane i knows where row warp + 4 i is.
@@ -120,21 +119,19 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             bool drafts;
         };
         const int mine = warp + 4 * (lane & 15);
-        auto locate = [&](int vt) {
-            Where w = {0, 0, 0, PAGED && a.has_new && vt == p.nt - 1};
-            const int t = WIN ? span.tile(vt) : vt;
+        auto locate = [&](int t) {
+            Where w = {0, 0, 0, PAGED && a.has_new && t == p.nt - 1};
+            const int pos = WIN ? p.span.key(t * kF32Tile + mine) : t * kF32Tile + mine;  // of this lane's row
             // keys past the end load as zeros (0 times what is there could be NaN)
-            const int valid = w.drafts ? a.T : min(kF32Tile, p.Lk - t * kF32Tile);
-            bool ok = mine < valid;
-            if (WIN && !w.drafts) ok = ok && (t * kF32Tile + mine >= first || t * kF32Tile + mine < a.sinks);
+            bool ok = w.drafts ? mine < a.T : pos < p.Lk;
+            if (WIN && !w.drafts) ok = ok && (pos >= first || pos < a.sinks);
             if (!PAGED) {
-                w.k = (long long)(p.k0 + t * kF32Tile + mine) * io.ldk;
-                w.v = (long long)(p.k0 + t * kF32Tile + mine) * io.ldv;
+                w.k = (long long)(p.k0 + pos) * io.ldk;
+                w.v = (long long)(p.k0 + pos) * io.ldv;
             } else if (w.drafts) {
                 w.k = (long long)(p.n * a.T + mine) * io.ldk;
                 w.v = (long long)(p.n * a.T + mine) * io.ldv;
             } else if (ok) {
-                const int pos = t * kF32Tile + mine;
                 const int pg = a.table[(size_t)p.n * a.table_ld + (pos >> page_bits)];
                 ok = pg >= 0 && pg < a.pages;
                 if (!ok) atomicOr(status_word(a), kStatusBadSeqlens);  // zeros instead
@@ -200,7 +197,7 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int key = tx + 16 * e;
-                    const int pos = (WIN ? span.tile(t) : t) * kF32Tile + key;
+                    const int pos = WIN ? p.span.key(t * kF32Tile + key) : t * kF32Tile + key;
                     bool see = drafts ? (bits[i] >> key & 1) != 0 : seen[i] > pos;
                     if (WIN && !drafts) see = see && (pos >= from[i] || pos < a.sinks);
                     if (!see) s[i][e] = -INFINITY;
@@ -308,7 +305,7 @@ static cudaError_t launch_form(Args a, const F32Ptrs &io, cudaStream_t stream) {
     const long long slots = PAGED ? (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens)
                                   : ((long long)a.Tq_total / a.tile_tokens + a.N) * a.Hkv;
     long long keys = PAGED ? (long long)a.table_cols * a.page + kF32Tile : a.Tk;
-    if (WIN) keys = window_keys(a, keys, kF32Tile);
+    if (WIN) keys = set_window(a, keys, 1, 1);
     set_unit(a, (double)slots * ((double)keys + a.extra + kF32Tile));
     // (a CTA each for four prompts of 25 tokens: 14.3 us instead of 35.6)
     a.direct = slots <= 2 * a.sms && keys <= 2 * kF32Tile;

@@ -66,6 +66,7 @@ constexpr uint32_t kColS = 0, kColO = 256;  // TMEM columns: S/P of stream s at 
 
 struct Maps {
     CUtensorMap q, k, v, kn, vn, out;
+    CUtensorMap k16, v16;  // prefill through a window: 16 rows at a time, for tiles of sinks and others
 };
 
 // A part as the roles need it, in shared memory.
@@ -83,7 +84,7 @@ struct Desc {
     int count[2];          // key tiles of each stream
     int start[2];          // its first tile (DUAL: every second from there)
     int tokens[2];         // valid tokens of its row tile
-    int sinks, skip;       // WIN: the item's Span
+    Span span;             // WIN
 };
 
 // Shared memory: two Q tiles of RT rows, 32 KB for the way out (DUAL: the box for the
@@ -219,10 +220,7 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
     d.open = p.tb < p.nt;
     d.writer = DUAL ? run.tiles & 1 : 0;
     d.seen = PAGED ? p.Lk : p.Lk - p.Lq + p.first_tok + 1;
-    if (WIN) {
-        d.sinks = p.sinks;
-        d.skip = p.skip;
-    }
+    if (WIN) d.span = p.span;
     if (DUAL) {  // tiles alternate between the streams, across parts too
         const int tiles = p.tb - p.ta;
 #pragma unroll
@@ -243,8 +241,7 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
             int end = p.tb;
             if (!PAGED) {  // the keys that the row tile's last token sees
                 const int seen = d.seen + s * a.tile_tokens + tokens - 1;
-                int nt = seen <= 0 ? 0 : (int)(((unsigned)seen + kTile - 1) / kTile);
-                if (WIN) nt = nt > p.sinks + p.skip ? nt - p.skip : min(nt, p.sinks);
+                const int nt = seen <= 0 ? 0 : (int)(((unsigned)(WIN ? seen - p.span.shift : seen) + kTile - 1) / kTile);
                 end = end < nt ? end : nt;
             }
             d.tokens[s] = tokens;
@@ -399,10 +396,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int seen0 = d->seen + (PAGED ? 0 : s * a.tile_tokens);
             const int seen = PAGED ? seen0 : seen0 + tok;
             const int draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
-            // WIN: where this row's window starts, and where the last one of the row tile does (decode: at most)
-            const Span span = {WIN ? d->sinks : 0, WIN ? d->skip : 0, 0};
-            const int from = WIN ? window_start(a, PAGED && a.has_new ? seen + max(1, __popcll(bits)) : seen) : 0;
-            const int from_last = WIN ? window_start(a, seen0 + (PAGED ? a.has_new * a.T : d->tokens[s] - 1)) : 0;
+            // WIN: where this row's window starts, and where the last one of the row tile does (decode: at
+            // most), among the item's keys; so are `seen` and `seen0` from there on
+            const int shift = WIN ? d->span.shift : 0;
+            const int from = WIN ? window_start(a, PAGED && a.has_new ? seen + max(1, __popcll(bits)) : seen) - shift : 0;
+            const int from_last = WIN ? window_start(a, seen0 + (PAGED ? a.has_new * a.T : d->tokens[s] - 1)) - shift : 0;
             int t = d->start[s];
             for (int j = 0; j < steps; ++j, t += DUAL ? 2 : 1) {
                 if (!warp_wait(bars.sfull(s), ns++ & 1)) {
@@ -414,11 +412,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t x[8][16];
                     tc::tmem_ld_cols<8>(tS, x);
                     const bool drafts = PAGED && t == draft_tile;
-                    const int t0 = (WIN ? span.tile(t) : t) * kTile;  // the tile's first key
-                    if (drafts || seen0 < t0 + kTile || (WIN && from_last > t0 && a.sinks - kTile < t0)) {
+                    const int t0 = t * kTile;  // the tile's first key
+                    if (drafts || seen0 - shift < t0 + kTile || (WIN && from_last > t0 && a.sinks - kTile < t0)) {
                         // the keys that this row sees, a bit each
                         if (PAGED && drafts && a.T < 64) bits &= (1ull << a.T) - 1;
-                        const int lim = seen - t0;
+                        const int lim = seen - shift - t0;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             auto below = [&](int n) { return n >= 32 * i + 32 ? ~0u : (n <= 32 * i ? 0u : (1u << (n & 31)) - 1); };
@@ -775,12 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int row_bits = 31 - __clz(rows), page_bits = 31 - __clz(a.page);
             const uint32_t lead = tc::elect_one();
             // decode: the page of this lane's copy of tile t
-            // (kNoPage: WIN: one that no row sees, of which nothing is read, its number neither)
-            constexpr int kNoPage = -2;
             auto page_of = [&](const Span &span, int n, int Lk, int t) -> int {
-                const int pos = (WIN ? span.tile(t) : t) * kTile + (lane << row_bits);
+                const int v = t * kTile + (lane << row_bits), pos = WIN ? span.key(v) : v;
                 if (!PAGED || (lane << row_bits) >= kTile || pos >= Lk) return -1;
-                if (WIN && pos >= a.sinks && pos + rows <= window_start(a, Lk + a.has_new)) return kNoPage;
                 return __ldg(a.table + (size_t)n * a.table_ld + (pos >> page_bits));
             };
             auto load = [&](const Load x, bool is_v) {
@@ -792,17 +787,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++kv;
                 // rows of this tile that are the sequence's own
-                const int t0 = (WIN ? x.span.tile(x.t) : x.t) * kTile;
-                const int left = x.draft ? a.T : x.Lk - t0, valid = left < kTile ? left : kTile;
+                const int t0 = x.t * kTile, first = WIN && t0 >= x.span.sinks ? t0 + x.span.shift : t0;  // the tile's first key
+                const int left = x.draft ? a.T : x.Lk - (WIN ? x.span.shift : 0) - t0, valid = left < kTile ? left : kTile;
                 // rows past the end hold other sequences' values or nothing at all:
                 // P is 0 there, but 0 times a NaN is not, so V gets zeros
                 const bool fix = is_v && valid < kTile;
                 const uint32_t bar = fix ? bars.vraw(slot) : bars.kvfull(slot);
                 const CUtensorMap *m = is_v ? &maps.v : &maps.k;
-                if (!PAGED) {
+                if (!PAGED && WIN && t0 < x.span.sinks && t0 + kTile > x.span.sinks) {  // sinks, then others
+                    const CUtensorMap *m16 = is_v ? &maps.v16 : &maps.k16;
                     expect_tx(lead, bar, kTileBytes);
-                    tma_3d(lead, dst, m, 0, x.h, x.k0 + t0, bar);
-                    tma_3d(lead, dst + kHalf, m, 64, x.h, x.k0 + t0, bar);
+#pragma unroll 1
+                    for (int i = 0; i < kTile; i += 16) {
+                        const int row = x.k0 + x.span.key(t0 + i);
+                        tma_3d(lead, dst + i * 128, m16, 0, x.h, row, bar);
+                        tma_3d(lead, dst + kHalf + i * 128, m16, 64, x.h, row, bar);
+                    }
+                } else if (!PAGED) {
+                    expect_tx(lead, bar, kTileBytes);
+                    tma_3d(lead, dst, m, 0, x.h, x.k0 + first, bar);
+                    tma_3d(lead, dst + kHalf, m, 64, x.h, x.k0 + first, bar);
                 } else if (x.draft) {
                     const CUtensorMap *mn = is_v ? &maps.vn : &maps.kn;
                     expect_tx(lead, bar, (uint32_t)((a.T + 7) & ~7) * 256u);
@@ -813,8 +817,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     expect_tx(lead, bar, (uint32_t)(copies << row_bits) * 256u);
                     int row = max(a.pages * a.Hkv * a.page, 1);  // past the map's last row (an empty pool's has one): zeros
                     if (x.pg >= 0 && x.pg < a.pages)
-                        row = (x.pg * a.Hkv + x.h) * a.page + ((t0 + (lane << row_bits)) & (a.page - 1));
-                    else if (lane < copies && !(WIN && x.pg == kNoPage))
+                        row = (x.pg * a.Hkv + x.h) * a.page + ((WIN ? x.span.key(t0 + (lane << row_bits)) : t0 + (lane << row_bits)) & (a.page - 1));
+                    else if (lane < copies)
                         atomicOr(status_word(a), kStatusBadSeqlens);
                     for (int i = 0; i < copies; ++i) {
                         const int ri = __shfl_sync(0xffffffffu, row, i);
@@ -867,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x.k0 = d->k0;
                     x.Lk = d->Lk;
                     x.t = d->ta - 1;
-                    if (WIN) x.span = {d->sinks, d->skip, 0};
+                    if (WIN) x.span = d->span;
                     draft_tile = PAGED && a.has_new ? d->nt - 1 : -1;
                     q_first = 1;
                     next_pg = peek_pg;
@@ -889,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __all_sync(0xffffffffu, mbar_test(bars.dfull((nd + 1) % kDescs), ((nd + 1) / kDescs) & 1))) {
                         const Desc *e = descs + (nd + 1) % kDescs;
                         if (!e->last) {
-                            const Span span = {WIN ? e->sinks : 0, WIN ? e->skip : 0, 0};
+                            const Span span = WIN ? e->span : Span{0, 0};
                             peek_pg = page_of(span, e->n, e->Lk, e->ta);
                             peek_pg2 = page_of(span, e->n, e->Lk, e->ta + 1);
                             peeked = nd + 2;
@@ -1118,7 +1122,9 @@ cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long ke
     a.extra_short = PAGED ? 512 : 0;
     a.min_part = kMinPart;
     set_block(a);
-    if (WIN) keys = window_keys(a, keys, kTile);
+    // Where a tile's rows come from other places than one stretch, they come 16 rows (prefill) or a
+    // page's at a time.
+    if (WIN) keys = PAGED ? set_window(a, keys, a.page < kTile ? a.page : kTile, a.page < kTile ? a.page : kTile) : set_window(a, keys, 16, 1);
     // every item's keys, its start and end and, at the most, its drafts' tile
     set_unit(a, (double)slots * ((double)keys + 512 + kTile));
     a.cut = 2;
@@ -1154,6 +1160,8 @@ cudaError_t launch_attn_prefill_tc(Args a, const void *q, const void *k, const v
         !map3(&m.k, k, a.Hkv, a.Tk_total, ldk, 1, kTile) ||
         !map3(&m.v, v, a.Hkv, a.Tk_total, ldv, 1, kTile) ||
         !map3(&m.out, a.out, a.Hq, a.Tq_total, (long long)a.Hq * kD, a.G, a.tile_tokens))
+        return cudaErrorInvalidValue;
+    if (a.window > 0 && (!map3(&m.k16, k, a.Hkv, a.Tk_total, ldk, 1, 16) || !map3(&m.v16, v, a.Hkv, a.Tk_total, ldv, 1, 16)))
         return cudaErrorInvalidValue;
     const long long slots = ((long long)a.Tq_total / (2 * a.tile_tokens) + a.N) * a.Hkv;
     return launch<false, false, 128>(a, m, slots, a.Tk, stream);
