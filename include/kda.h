@@ -614,7 +614,7 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv,
  *       with a fork would overwrite its tokens)
  *   seq_lens and the tables are not changed, for any number of layers to be cut alike:
  *   afterwards kda_cache_trim. Malformed lengths or page numbers are flagged, their rows skipped.
- *   rows * Hkv is at most 2^25. workspace: kda_cache_evict_workspace_size bytes, as for the other calls.
+ *   rows * Hkv is at most 2^25, cap 2^31 - 2^13. workspace: kda_cache_evict_workspace_size bytes, as for the other calls.
  *
  * kda_cache_trim: each row keeps the pages of its first want[row] tokens (DEVICE int32 [rows]; < 0
  *   skips the row) and drops the others (refs - 1, entries -1); its length is want[row] at most.

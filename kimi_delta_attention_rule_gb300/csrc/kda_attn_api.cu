@@ -64,6 +64,7 @@ using kda::attn::Args;
 constexpr int kMaxGroup = 64;
 constexpr int kMaxTokens = kda::attn::kMaxDrafts;
 constexpr long long kMaxKeys = (1LL << 31) - 1024;  // (positions two key tiles past a sequence's end are formed)
+constexpr int32_t kMaxCap = INT32_MAX - 8191;  // weights of a row in an eviction (a round of slots past the end is formed)
 constexpr size_t kHeader = 256;  // of a cache workspace: the status word
 // Pages, and entries of a block table: their kernels step past the last one by less than 2^16
 // and add up the pages that all rows lack, in 32 bits.
@@ -515,7 +516,7 @@ int kda_cache_evict(void *k_pages, void *v_pages, int32_t num_pages, int32_t pag
     if (dst_table != nullptr && (dst_cols < 0 || dst_ld < dst_cols)) return KDA_ERR_INVALID_ARG;
     if ((long long)num_pages * Hkv * page_size > 0x7fffffffLL || num_pages > kMaxPages ||
         (long long)rows * table_cols > kMaxPages || (long long)rows * dst_cols > kMaxPages ||
-        (long long)table_cols * page_size > kMaxKeys || cap > kMaxKeys || (long long)rows * Hkv > (1LL << 25))
+        (long long)table_cols * page_size > kMaxKeys || cap > kMaxCap || (long long)rows * Hkv > (1LL << 25))
         return KDA_ERR_INVALID_ARG;
     if (rows == 0 || cap == 0 || table_cols == 0 || num_pages == 0) return KDA_OK;  // no cached token
     if (k_pages == nullptr || v_pages == nullptr || block_table == nullptr || seq_lens == nullptr || keep == nullptr ||

@@ -1130,6 +1130,16 @@ cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long ke
     a.cut = 2;
     // (a CTA each for four short prompts: 9.1 us instead of 14.4)
     a.direct = slots <= a.sms && keys <= 5 * kTile;
+    if (WIN && slots <= a.sms) {
+        // A CTA each takes as long as its tiles; shared evenly, fewer of them, but a search ahead and the
+        // parts' way out and back in, which cost as much as some tiles more (of one row tile 6, of two 11, of
+        // prompts, whose parts mostly have no second pass, 4). Direct and split, us: one token, 64 items
+        // of 9 tiles 14.7, 16.7, of 17 21.5, 20.0; 64 drafts, 64 items of 17 tiles 31.2, 35.3, of 33
+        // 52.0, 44.5; prompts, 128 items of 18 tiles 32.9, 38.4, of 34 53.3, 50.5.
+        constexpr int kTiles = PAGED ? (DUAL ? 6 : 11) : 4;
+        const long long own = (long long)a.window + a.sink_rows + (PAGED ? kTile : a.block), longest = keys < own ? keys : own;
+        a.direct = longest * (a.sms - slots) <= (long long)kTiles * kTile * a.sms;
+    }
     constexpr int bytes = Smem<DUAL, RT>::kBytes;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;

@@ -6,7 +6,7 @@
 namespace kda {
 namespace cache {
 
-constexpr int kThreads = 1024;  // of a block of block_exclusive
+constexpr int kThreads = 1024;  // of a block of the calls that choose pages
 
 struct Table {
     int32_t *entries;
@@ -15,7 +15,8 @@ struct Table {
     __device__ __forceinline__ int32_t *row(int r) const { return entries + (size_t)r * ld; }
 };
 
-// Exclusive prefix of x over the block; total gets the sum. Converged block.
+// Exclusive prefix of x over a block of WARPS warps; total gets the sum. Converged block.
+template <int WARPS = kThreads / 32>
 __device__ __forceinline__ int block_exclusive(int x, int *warp_sums, int &total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int incl = x;
@@ -27,7 +28,7 @@ __device__ __forceinline__ int block_exclusive(int x, int *warp_sums, int &total
     __syncthreads();  // warp_sums is free
     if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
-    const int mine = warp_sums[lane];  // 32 warps
+    const int mine = lane < WARPS ? warp_sums[lane] : 0;
     int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {

@@ -3,8 +3,12 @@
 // weight (ties: the earlier); they move to the slots 0 .. keep - 1, in their order.
 //
 // Choosing (select_kernel): one block per (sequence, head) finds the weight of rank
-// `heavy` by four passes over eight bits each of the weights' ordered patterns, then goes once
-// through the slots and writes the staying ones with their rank, a prefix sum over the block.
+// `heavy` by three passes over 11, 11 and 10 bits of the weights' ordered patterns, counted in one
+// histogram in shared memory, then goes once through the slots, four in a row to a thread, and writes
+// the staying ones by their rank, a prefix sum over the block. The first kCache patterns stay in shared
+// memory. The longest row bounds it: 1,024 threads a block (512, two blocks to an SM: XX us instead of
+// YY for 32 sequences of 250,007 tokens, 30,515 in the longest), patterns formed once and counted four at a time.
+// The next kernel starts when it is through: blocks that wait for it on SMs with room cost the moves 27 us.
 //
 // Moving (move_kernel): a chunk is 2,048 pieces of 16 bytes, eight per thread, whose loads
 // are in flight together, and those of the next chunk before this one's are stored. To
@@ -15,6 +19,8 @@
 // sequences CTAs share a row's bytes, not its slots, and nobody waits for another CTA.
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <atomic>
 
 #include "kda_cache.cuh"
 #include "kda_common.cuh"
@@ -38,18 +44,27 @@ struct EvictArgs {
 
 // ---- the slots that stay ---------------------------------------------------------
 // Patterns that order as the weights do: NaN above all, -0 as 0.
-__device__ __forceinline__ uint32_t ordered(float x) {
+__device__ __forceinline__ uint32_t ordered(uint32_t bits) {
+    const float x = __uint_as_float(bits);
     if (x != x) return 0xffffffffu;
     const uint32_t u = x == 0.f ? 0u : __float_as_uint(x);
     return u >> 31 ? ~u : u | 0x80000000u;
 }
+// Whether a pattern tells its weight, and which.
+__device__ __forceinline__ bool tells(uint32_t key) { return key != 0xffffffffu && key != 0x80000000u; }
+__device__ __forceinline__ float weight_of(uint32_t key) { return __uint_as_float(key >> 31 ? key & 0x7fffffffu : ~key); }
 
-__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ EvictArgs a) {
-    __shared__ int warp_sums[32];
-    __shared__ int hist[kThreads / 32][256];
+constexpr int kSelThreads = 1024, kSelWarps = 32;
+constexpr int kCache = 49152;
+constexpr int kBins = 2048, kBinsEach = kBins / kSelThreads;
+constexpr int kRound = 4 * kSelThreads;  // slots of a round of the last pass
+
+__global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_constant__ EvictArgs a) {
+    extern __shared__ __align__(16) uint32_t patterns[];
+    __shared__ int warp_sums[2][32];
+    __shared__ int hist[kBins];
     __shared__ int found[2];  // the digit, and how many above it there are
     wait_before();
-    let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
     const int len = a.lens[b], budget = a.keep[b];
@@ -61,16 +76,28 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     const bool moves = !a.in_place || len > budget;
     bool bad = len < 0 || len > a.cap || (long long)len > (long long)a.src.cols * a.page ||
                (long long)n > (long long)a.dst.cols * a.page;
+    const float *const w = a.w + (size_t)blockIdx.x * a.cap;
+    const int cached = min(len, kCache);
+    if (!bad && len > budget) {  // (on their way while the pages are looked at)
+        const int whole = (reinterpret_cast<uintptr_t>(w) & 15) == 0 ? cached & ~3 : 0;
+        for (int i = 4 * tid; i < whole; i += 4 * kSelThreads)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(patterns + i)), "l"(w + i) : "memory");
+        for (int i = whole + tid; i < cached; i += kSelThreads)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n" ::"r"(smem_u32(patterns + i)), "l"(w + i) : "memory");
+    }
     if (!bad) {
         const int32_t *const from = a.src.row(b), *const to = a.dst.row(b);
-        for (int j = tid; j < (int)(((unsigned)len + a.page - 1) >> a.page_bits); j += kThreads)
+        for (int j = tid; j < (int)(((unsigned)len + a.page - 1) >> a.page_bits); j += kSelThreads)
             bad = bad || from[j] < 0 || from[j] >= a.pages;
-        for (int j = tid; j < (int)(((unsigned)n + a.page - 1) >> a.page_bits); j += kThreads) {
+        for (int j = tid; j < (int)(((unsigned)n + a.page - 1) >> a.page_bits); j += kSelThreads) {
             const int pg = to[j];
             bad = bad || pg < 0 || pg >= a.pages;
             if (!bad && moves && a.refs != nullptr) bad = a.refs[pg] != 1;  // others read what is there
         }
     }
+    const int sinks = min(a.sinks, n), recent = min(a.recent, n - sinks), end = len - recent;
+    int need = n - sinks - recent;  // of [sinks, end)
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
     if (__syncthreads_or(bad)) {
         if (tid == 0 && h == 0) {
             a.state[b] = 0;
@@ -79,57 +106,61 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
         return;
     }
     if (h == 0 && tid == 0) a.state[b] = moves ? n : 0;
-    const float *const w = a.w + (size_t)blockIdx.x * a.cap;
     float *const w_out = a.w_out + (size_t)blockIdx.x * a.cap;
     int32_t *const kept = a.kept + (size_t)blockIdx.x * a.cap;
     if (len <= budget) {
-        for (int i = tid; i < len; i += kThreads) {
+        for (int i = tid; i < len; i += kSelThreads) {
             kept[i] = i;
             if (w_out != w) w_out[i] = w[i];
         }
         return;
     }
-    const int sinks = min(a.sinks, n), recent = min(a.recent, n - sinks), end = len - recent;
-    int need = n - sinks - recent;  // of [sinks, end)
-    uint32_t top = 0xffffffffu;     // what is above it stays, and the first `need` equal ones
-    if (need > 0) {
+    uint32_t top = 0xffffffffu;  // what is above it stays, and the first `need` equal ones
+    const bool ranked = need > 0;  // else the weights do not count, and their patterns are not formed
+    if (ranked) {
         top = 0;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 32 * 256; i += kThreads) (&hist[0][0])[i] = 0;
+        for (int shift = 21; shift >= 0; shift = shift == 21 ? 10 : shift - 10) {  // 21, 10, 0
+#pragma unroll
+            for (int e = 0; e < kBinsEach; ++e) hist[tid + kSelThreads * e] = 0;
             __syncthreads();
-            const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
+            const uint32_t mask = shift == 21 ? 0u : (shift == 10 ? ~0u << 21 : ~0u << 10), digits = shift == 0 ? 1023 : 2047;
+            auto count = [&](uint32_t key) {
+                if ((key & mask) == top) atomicAdd(&hist[key >> shift & digits], 1);
+            };
+#pragma unroll 2
+            for (int i = 4 * tid; i < cached; i += 4 * kSelThreads) {
+                uint4 x = *reinterpret_cast<const uint4 *>(patterns + i);  // (behind `cached`: anything)
+                if (shift == 21) {
+                    x = make_uint4(ordered(x.x), ordered(x.y), ordered(x.z), ordered(x.w));
+                    *reinterpret_cast<uint4 *>(patterns + i) = x;
+                }
+                if (i >= sinks && i + 4 <= min(end, cached)) {
+                    count(x.x);
+                    count(x.y);
+                    count(x.z);
+                    count(x.w);
+                } else {
+                    const int last = min(end, cached);
+                    if (i >= sinks && i < last) count(x.x);
+                    if (i + 1 >= sinks && i + 1 < last) count(x.y);
+                    if (i + 2 >= sinks && i + 2 < last) count(x.z);
+                    if (i + 3 >= sinks && i + 3 < last) count(x.w);
+                }
+            }
 #pragma unroll 4
-            for (int i = sinks + tid; i < end; i += kThreads) {
-                const uint32_t key = ordered(w[i]);
-                if ((key & mask) == top) atomicAdd(&hist[warp][key >> shift & 255], 1);
-            }
+            for (int i = max(sinks, kCache) + tid; i < end; i += kSelThreads) count(ordered(__float_as_uint(w[i])));
             __syncthreads();
-            if (tid < 256) {
-                int sum = 0;
+            int mine = 0, c[kBinsEach], total;  // the digits from the top
 #pragma unroll
-                for (int i = 0; i < 32; ++i) sum += hist[i][tid];
-                hist[0][tid] = sum;
-            }
-            __syncthreads();
-            if (warp == 0) {  // lane l has the digits 255 - 8 l .. 248 - 8 l
-                int mine = 0, c[8];
+            for (int e = 0; e < kBinsEach; ++e) mine += c[e] = hist[kBins - 1 - kBinsEach * tid - e];
+            int above = block_exclusive<kSelWarps>(mine, warp_sums[0], total);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mine += c[e] = hist[0][255 - 8 * lane - e];
-                int incl = mine;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += y;
+            for (int e = 0; e < kBinsEach; ++e) {
+                if (above < need && above + c[e] >= need) {
+                    found[0] = kBins - 1 - kBinsEach * tid - e;
+                    found[1] = above;
                 }
-                int above = incl - mine;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (above < need && above + c[e] >= need) {
-                        found[0] = 255 - 8 * lane - e;
-                        found[1] = above;
-                    }
-                    above += c[e];
-                }
+                above += c[e];
             }
             __syncthreads();
             top |= (uint32_t)found[0] << shift;
@@ -138,44 +169,73 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     }
     // Weights in place: a round writes no slot past those that it or earlier ones have read.
     int above = 0, equal = 0;
-    for (int i0 = 0; i0 < len; i0 += 4 * kThreads) {
-        float x[4];
-        int mine = 0;  // staying ones, and equal ones in the upper half
+    for (int i0 = 0, round = 0; i0 < len; i0 += kRound, ++round) {
+        const int at = i0 + 4 * tid;
+        uint32_t key[4] = {0, 0, 0, 0};
+        if (at < cached) *reinterpret_cast<uint4 *>(key) = *reinterpret_cast<const uint4 *>(patterns + at);
         uint32_t stays = 0, ties = 0;
+        float x[4];
+        // Most warps: no end of anything, no equal one, every staying weight told by its pattern.
+        bool plain = ranked && at >= sinks && at + 4 <= end && at + 4 <= cached;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const int i = i0 + 4 * tid + e;
-            if (i >= len) continue;
-            x[e] = w[i];
-            const uint32_t key = ordered(x[e]);
-            const bool safe = i < sinks || i >= end;
-            if (safe || key > top) {
-                stays |= 1u << e;
-                ++mine;
-            } else if (key == top) {
-                ties |= 1u << e;
-                mine += 1 << 16;
+            stays |= (uint32_t)(key[e] > top) << e;
+            plain = plain && key[e] != top && !(key[e] > top && !tells(key[e]));
+            x[e] = weight_of(key[e]);
+        }
+        if (!__all_sync(0xffffffffu, plain)) {
+            stays = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = at + e;
+                if (i >= len) continue;
+                if (ranked && i >= cached) key[e] = ordered(__float_as_uint(w[i]));
+                const bool stay = i < sinks || i >= end || (ranked && key[e] > top), tie = ranked && !stay && key[e] == top;
+                stays |= (uint32_t)stay << e;
+                ties |= (uint32_t)tie << e;
+                if (stay || tie) x[e] = w[i];
             }
         }
-        int total;
-        const int before = block_exclusive(mine, warp_sums, total);
-        int s = above + (before & 0xffff), t = equal + (before >> 16);
+        // staying ones ahead of this thread's, and equal ones in the upper half
+        int mine = __popc(stays) + (__popc(ties) << 16), incl = mine;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool tie = ties >> e & 1;
-            if ((stays >> e & 1) || (tie && t < need)) {
-                const int to = s + min(t, need);
-                kept[to] = i0 + 4 * tid + e;
-                w_out[to] = x[e];
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) warp_sums[round & 1][warp] = incl;
+        __syncthreads();  // (so that all of this round's weights are read; the other sums are the last round's)
+        const int theirs = warp_sums[round & 1][lane];
+        const int before = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0) + incl - mine;
+        const int total = __reduce_add_sync(0xffffffffu, theirs);
+        int s = above + (before & 0xffff), t = equal + (before >> 16);
+        if (ties == 0) {
+            s += min(t, need);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (stays >> e & 1) {
+                    kept[s] = at + e;
+                    w_out[s++] = x[e];
+                }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool tie = ties >> e & 1;
+                if ((stays >> e & 1) || (tie && t < need)) {
+                    const int to = s + min(t, need);
+                    kept[to] = at + e;
+                    w_out[to] = x[e];
+                }
+                s += stays >> e & 1;
+                t += tie;
             }
-            s += stays >> e & 1;
-            t += tie;
         }
         above += total & 0xffff;
         equal += total >> 16;
     }
+    let_next_start();
     __syncthreads();
-    for (int i = n + tid; i < len; i += kThreads) w_out[i] = 0.f;
+    for (int i = n + tid; i < len; i += kSelThreads) w_out[i] = 0.f;
 }
 
 // ---- the rows that move ------------------------------------------------------------
@@ -364,7 +424,18 @@ cudaError_t launch_evict(void *kp, void *vp, int pages, int page, int32_t *table
     a.state = state;
     a.status = status;
     const long long heads = (long long)rows * Hkv;
-    cudaError_t e = launch_early(select_kernel, dim3((unsigned)heads), kThreads, 0, stream, a);
+    // (shared memory for the longest possible row; past kCache weights the others are read from L2)
+    const int cached = cap < kCache ? (cap + 3) & ~3 : kCache;
+    static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCache * 4);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    e = launch_early(select_kernel, dim3((unsigned)heads), kSelThreads, (size_t)cached * 4, stream, a);
     if (e != cudaSuccess) return e;
     MoveArgs m = {static_cast<uint4 *>(kp), static_cast<uint4 *>(vp), rows, es == 2 ? 4 : 5, 0, 1};
     m.piece_bits = m.row_bits;
