@@ -1109,6 +1109,18 @@ bool map3(CUtensorMap *m, const void *p, int heads, long long rows, long long ld
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// Through a window: whether each item goes to a CTA of its own. That takes as long as its tiles; shared
+// evenly there are fewer to each, but a search ahead and the parts' way out and back in, which cost
+// as much as some tiles more (of one row tile 7, of two 11, of prompts, whose parts mostly have
+// no second pass, 4). Direct and split, us: one token, 64 items of 9 tiles 14.7, 16.7, of 17
+// 21.5, 20.0; 64 drafts, 64 items of 17 tiles 31.2, 35.3, of 33 52.0, 44.5; prompts, 128
+// items of 18 tiles 32.9, 38.4, of 34 53.3, 50.5.
+template <bool PAGED, bool DUAL>
+bool window_direct(const Args &a, long long slots, long long keys) {
+    constexpr int kTiles = PAGED ? (DUAL ? 7 : 11) : 4;
+    const long long own = (long long)a.window + a.sinks + (PAGED ? kTile : a.block), longest = keys < own ? keys : own;
+    return slots <= a.sms && longest * (a.sms - slots) <= (long long)kTiles * kTile * a.sms;
+}
 template <bool PAGED, bool DUAL, int RT, bool WIN, bool TEST>
 cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
     a.streams = DUAL ? 1 : 2;
@@ -1130,16 +1142,7 @@ cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long ke
     a.cut = 2;
     // (a CTA each for four short prompts: 9.1 us instead of 14.4)
     a.direct = slots <= a.sms && keys <= 5 * kTile;
-    if (WIN && slots <= a.sms) {
-        // A CTA each takes as long as its tiles; shared evenly, fewer of them, but a search ahead and the
-        // parts' way out and back in, which cost as much as some tiles more (of one row tile 6, of two 11, of
-        // prompts, whose parts mostly have no second pass, 4). Direct and split, us: one token, 64 items
-        // of 9 tiles 14.7, 16.7, of 17 21.5, 20.0; 64 drafts, 64 items of 17 tiles 31.2, 35.3, of 33
-        // 52.0, 44.5; prompts, 128 items of 18 tiles 32.9, 38.4, of 34 53.3, 50.5.
-        constexpr int kTiles = PAGED ? (DUAL ? 6 : 11) : 4;
-        const long long own = (long long)a.window + a.sink_rows + (PAGED ? kTile : a.block), longest = keys < own ? keys : own;
-        a.direct = longest * (a.sms - slots) <= (long long)kTiles * kTile * a.sms;
-    }
+    if (WIN) a.direct = window_direct<PAGED, DUAL>(a, slots, keys);
     constexpr int bytes = Smem<DUAL, RT>::kBytes;
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;
@@ -1182,8 +1185,13 @@ cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const v
                                   cudaStream_t stream) {
     // (one row tile for both streams instead of a second, empty one: 128 sequences of 500
     // tokens, when it was taken, 66.6 us instead of 79.3, one of 65,531 51.5 instead of 52.3)
-    const bool dual = a.T * a.G <= kTile;
+    bool dual = a.T * a.G <= kTile;
     a.tile_tokens = dual ? a.T : kTile / a.G;
+    const long long keys = (long long)a.table_cols * a.page + kTile;
+    // Through a window also where every row tile can be an item with a CTA of its own: 27 us instead of 33 for 64
+    // drafts of 8 users, 128 items of 17 tiles.
+    if (!dual && a.window > 0)
+        dual = window_direct<true, true>(a, (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens), keys);
     const long long rows = (long long)a.pages * a.Hkv * a.page, toks = (long long)a.N * a.T;
     Maps m{};
     if (!map3(&m.q, q, a.Hq, toks, ldq, a.G, a.tile_tokens) ||
@@ -1196,7 +1204,6 @@ cudaError_t launch_attn_decode_tc(Args a, const void *q, const void *kp, const v
         return cudaErrorInvalidValue;
     const int block = a.tile_tokens * (dual ? 1 : 2);
     const long long slots = (long long)a.N * a.Hkv * ((a.T + block - 1) / block);
-    const long long keys = (long long)a.table_cols * a.page + kTile;
     if (!dual) return launch<true, false, 128>(a, m, slots, keys, stream);
     if (a.T * a.G <= 32) return launch<true, true, 32>(a, m, slots, keys, stream);
     return launch<true, true, 128>(a, m, slots, keys, stream);

@@ -183,6 +183,17 @@ def test_trees(T, hq, hkv, window, dt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("B,window", [(1, 64), (38, 64), (39, 400), (60, 64), (60, 900), (80, 64), (80, 300)])
+def test_many_trees(B, window):
+    """Row tiles that are items of their own, pairs of them on a CTA each, and items that CTAs share."""
+    g = torch.Generator().manual_seed(B)
+    x = make(torch.randint(0, 1200, (B,), generator=g).tolist(), 64, 8, 1, 32, BF, seed=29)
+    mask = tree_masks(B, 64, B)
+    out, lse = decode(x, window, 3, mask)
+    check_decode(x, out, lse, window, 3, mask)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_masks_without_the_token_itself(dt):
     x = make([7, 200, 500], 6, 4, 2, 32, dt, seed=23)
