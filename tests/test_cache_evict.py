@@ -190,11 +190,12 @@ def test_long_rows(lens, keep, dt, how):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("how", [in_place, elsewhere])
-def test_many_rows(how):
+@pytest.mark.parametrize("rows,most", [(90, 120), (90, 400), (25, 2600)])
+def test_many_rows(rows, most, how):
     g = torch.Generator().manual_seed(6)
-    lens = torch.randint(0, 400, (90,), generator=g).tolist()
-    keep = torch.randint(-1, 300, (90,), generator=g).tolist()
-    how(Cache(lens, 16, 8, BF, seed=6, spare=1500), keep, 4, 10)
+    lens = torch.randint(0, most, (rows,), generator=g).tolist()
+    keep = torch.randint(-1, most * 3 // 4, (rows,), generator=g).tolist()
+    how(Cache(lens, 16, 8, BF, seed=6, spare=3000), keep, 4, 10)
 
 
 @pytest.mark.gpu
