@@ -1097,18 +1097,6 @@ cudaError_t launch_attn_combine(const Args &a, bool bf16, bool joins_early, cuda
 
 // ---- host -----------------------------------------------------------------
 namespace {
-// [rows][heads][128] bf16 with `ld` elements between rows; box = 64 channels x bh heads x br rows
-bool map3(CUtensorMap *m, const void *p, int heads, long long rows, long long ld, int bh, int br) {
-    const EncodeTiledFn fn = encode_tiled();
-    if (fn == nullptr) return false;
-    const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
-    const cuuint64_t strides[2] = {256, (cuuint64_t)ld * 2};
-    const cuuint32_t box[3] = {64u, (cuuint32_t)bh, (cuuint32_t)br};
-    const cuuint32_t es[3] = {1u, 1u, 1u};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 // Through a window: whether each item goes to a CTA of its own. That takes as long as its tiles; shared
 // evenly there are fewer to each, but a search ahead and the parts' way out and back in, which cost
 // as much as some tiles more (of one row tile 7, of two 11, of prompts, whose parts mostly have

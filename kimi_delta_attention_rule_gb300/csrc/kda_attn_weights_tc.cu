@@ -85,6 +85,7 @@ struct Shape {
     int nq;    // rows of a Q tile: PARTS ns
     int tiles;  // Q tiles
     int ring;  // K tiles
+    int box, boxes;  // Q by tensor copies: tokens of one, how many; box = 0: by the warps' own
     __host__ __device__ uint32_t q_tile() const { return (uint32_t)nq * 256; }
     __host__ __device__ uint32_t ring_at() const { return tiles * q_tile(); }
     __host__ __device__ uint32_t q_more_at() const { return ring_at() + ring * kTileBytes; }
@@ -143,7 +144,8 @@ __device__ __forceinline__ float2 exp_sum(uint32_t x[N / 16][16], const int *see
 // PARTS groups share a tile; SMALL: 16 rows at the most.
 template <int PARTS, bool SMALL>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    weights_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map, const Shape shape) {
+    weights_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map,
+                      const Shape shape) {
     constexpr int kQTiles = PARTS == 4 ? 1 : 2;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto bar = [](const uint64_t &x) { return smem_u32(&x); };
     if (warp == kWarpTma && lane == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(bar(sh.qfull[i]), kRowWarps);
+            tc::mbar_init(bar(sh.qfull[i]), kRowWarps + (shape.box > 0));  // the rows' warps, and the copies
             tc::mbar_init(bar(sh.qempty[i]), 1);
         }
         for (int i = 0; i < kMaxRing; ++i) {
@@ -180,6 +182,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sh.dead = 0;
         tc::fence_mbar_init();
         attn::prefetch_map(&map);
+        attn::prefetch_map(&q_map);
     } else if (warp == kWarpMma) {
         tc::tmem_alloc(smem_u32(&sh.tmem), 512);
         tc::tmem_relinquish();
@@ -328,9 +331,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             };
             if (nd >= kQTiles && !(alive = long_wait(bar(sh.qempty[tile]), (nd / kQTiles - 1) & 1))) break;
             const uint32_t dst = base + tile * shape.q_tile();
+            const bool copies = shape.box > 0;
+            if (copies && wr == 0) {  // (tokens past the part's own come along, whose columns nobody looks at)
+                const uint32_t lead = tc::elect_one(), full = bar(sh.qfull[tile]), bytes = (uint32_t)(shape.box * a.G) * 128u;
+                attn::expect_tx(lead, full, 2 * shape.boxes * bytes);
+                for (int i = 0; i < shape.boxes; ++i) {
+                    const int token = b * a.T + a.t0 + i * shape.box;
+                    attn::tma_3d(lead, dst + i * bytes, &q_map, 0, head, token, full);
+                    attn::tma_3d(lead, dst + (uint32_t)shape.nq * 128 + i * bytes, &q_map, 64, head, token, full);
+                }
+                __syncwarp();
+            }
             const int c = lane & 15;  // a row's 16 pieces, two rows at a time
 #pragma unroll 4
-            for (int r0 = 2 * wr; r0 < rows; r0 += 2 * kRowWarps) {
+            for (int r0 = copies ? rows : 2 * wr; r0 < rows; r0 += 2 * kRowWarps) {
                 const int row = r0 + (lane >> 4), i = (int)(row * inv_g >> 16);
                 const int tk = token(min(i, 63));
                 if (row < rows && tk >= 0)
@@ -378,6 +392,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             ++nd;
         }
+        // (as the ring's copies below)
+        if (wr == 0 && shape.box > 0)
+            for (uint32_t i = 0; i < kQTiles; ++i)
+                alive = wait_warp(bar(sh.qfull[i]), ((nd + kQTiles - 1 - i) / kQTiles - 1) & 1) && alive;
     } else if (warp == kWarpTma) {
         // ---- K tiles -------------------------------------------------------------------------
         // A copy is at most a page's rows of a tile; a lane each looks up the pages of the next 32
@@ -476,7 +494,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 template <int PARTS, bool SMALL>
-static cudaError_t launch_form(const Args &a, const CUtensorMap &map, const Shape &shape, unsigned ctas, cudaStream_t stream) {
+static cudaError_t launch_form(const Args &a, const CUtensorMap &map, const CUtensorMap &q_map, const Shape &shape, unsigned ctas, cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -486,7 +504,7 @@ static cudaError_t launch_form(const Args &a, const CUtensorMap &map, const Shap
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    return launch_early(weights_tc_kernel<PARTS, SMALL>, dim3(ctas), kTcThreads, shape.bytes(), stream, a, map, shape);
+    return launch_early(weights_tc_kernel<PARTS, SMALL>, dim3(ctas), kTcThreads, shape.bytes(), stream, a, map, q_map, shape);
 }
 
 cudaError_t launch_weights_tc(Args a, int sms, cudaStream_t stream) {
@@ -505,14 +523,23 @@ cudaError_t launch_weights_tc(Args a, int sms, cudaStream_t stream) {
         shape.ns = rows <= 16 ? 16 : ((rows + parts - 1) / parts + 31) / 32 * 32;
         shape.nq = parts * shape.ns;
         shape.tiles = parts == 4 ? 1 : 2;
+        // Tokens in a row come by one tensor copy of each half of the channels, or two past 256 rows, the first
+        // of which ends at a multiple of eight rows, where the swizzle starts over, if that leaves room.
+        shape.boxes = rows <= 256 ? 1 : 2;
+        shape.box = (a.t1 - a.t0 + shape.boxes - 1) / shape.boxes;
+        while (shape.boxes > 1 && shape.box * a.G % 8 != 0) ++shape.box;
+        if (a.index != nullptr || shape.boxes * shape.box * a.G > shape.nq) shape.box = 0;
+        CUtensorMap q_map = {};
+        if (shape.box > 0 && !attn::map3(&q_map, a.q, a.Hkv * a.G, (long long)a.B * T, a.ldq, a.G, shape.box))
+            return cudaErrorInvalidValue;
         shape.ring = 0;
         shape.ring = (kSmemMost - (int)shape.bytes()) / (int)kTileBytes;
         if (shape.ring > kMaxRing) shape.ring = kMaxRing;
         const unsigned ctas = (unsigned)(tiles < sms ? tiles : sms);
-        const cudaError_t e = rows <= 16   ? launch_form<1, true>(a, map, shape, ctas, stream)
-                              : parts == 1 ? launch_form<1, false>(a, map, shape, ctas, stream)
-                              : parts == 2 ? launch_form<2, false>(a, map, shape, ctas, stream)
-                                           : launch_form<4, false>(a, map, shape, ctas, stream);
+        const cudaError_t e = rows <= 16   ? launch_form<1, true>(a, map, q_map, shape, ctas, stream)
+                              : parts == 1 ? launch_form<1, false>(a, map, q_map, shape, ctas, stream)
+                              : parts == 2 ? launch_form<2, false>(a, map, q_map, shape, ctas, stream)
+                                           : launch_form<4, false>(a, map, q_map, shape, ctas, stream);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

@@ -25,6 +25,18 @@ inline EncodeTiledFn encode_tiled() {
     return fn;
 }
 
+// [rows][heads][128] bf16 with `ld` elements between rows; box = 64 channels x bh heads x br rows
+inline bool map3(CUtensorMap *m, const void *p, int heads, long long rows, long long ld, int bh, int br) {
+    const EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {128, (cuuint64_t)heads, (cuuint64_t)(rows > 0 ? rows : 1)};
+    const cuuint64_t strides[2] = {256, (cuuint64_t)ld * 2};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)bh, (cuuint32_t)br};
+    const cuuint32_t es[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(p), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 // [rows][128] bf16, 256 bytes from row to row; box = 64 channels x br rows
 inline bool map2(CUtensorMap *m, const void *p, long long rows, int br) {
     const EncodeTiledFn fn = encode_tiled();
