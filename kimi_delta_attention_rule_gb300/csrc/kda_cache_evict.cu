@@ -6,9 +6,10 @@
 // `heavy` by three passes over 11, 11 and 10 bits of the weights' ordered patterns, counted in one
 // histogram in shared memory, then goes once through the slots, four in a row to a thread, and writes
 // the staying ones by their rank, a prefix sum over the block. The first kCache patterns stay in shared
-// memory. The longest row bounds it: 1,024 threads a block (512, two blocks to an SM: XX us instead of
-// YY for 32 sequences of 250,007 tokens, 30,515 in the longest), patterns formed once and counted four at a time.
-// The next kernel starts when it is through: blocks that wait for it on SMs with room cost the moves 27 us.
+// memory. The longest row bounds it, 22 us for 30,515 tokens of which 4,096 stay (3 to load, 8 for the passes, 9
+// for the last one): so 1,024 threads a block, patterns formed once and counted four at a time.
+// The moves' launch comes when all blocks have chosen: blocks that wait for it on SMs with room made a
+// call 27 us longer.
 //
 // Moving (move_kernel): a chunk is 2,048 pieces of 16 bytes, eight per thread, whose loads
 // are in flight together, and those of the next chunk before this one's are stored. To
@@ -17,7 +18,7 @@
 // is read: a CTA takes the slots of one (sequence, head, K or V) in order, of which it may store a
 // chunk as soon as its own loads of it are through, since later chunks read later slots; with few
 // sequences CTAs share a row's bytes, not its slots, and nobody waits for another CTA. Short rows
-// are moved by the block that has chosen them, in one launch (FUSED).
+// are moved by the block that has chosen them, in one launch (FUSED). Bound by HBM: 952 MB in 147 us, 6.5 TB/s.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -40,6 +41,7 @@ struct EvictArgs {
     int32_t *kept;
     int32_t *state;       // [rows]: slots that move, 0: none
     int in_place;
+    int ranked;           // at most kRanked rows, the longest first
     uint32_t *status;
     uint4 *kp, *vp;
     int row_bits;         // 16-byte pieces of a row: 16 or 32
@@ -62,6 +64,7 @@ __device__ __forceinline__ float weight_of(uint32_t key) { return __uint_as_floa
 
 constexpr int kSelThreads = 1024, kSelWarps = 32;
 constexpr int kCache = 49152;
+constexpr int kRanked = 128;  // rows that are ranked at the most
 constexpr int kBins = 2048, kBinsEach = kBins / kSelThreads;
 constexpr int kRound = 4 * kSelThreads;  // slots of a round of the last pass
 
@@ -101,7 +104,22 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
     __shared__ int found[2];  // the digit, and how many above it there are
     wait_before();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int b = blockIdx.x / a.Hkv, h = blockIdx.x - b * a.Hkv;
+    // Where not all blocks start at once, long rows first: the last ones to start are then the shortest (25.7 us
+    // instead of 35.0 for 32 sequences of 966 to 30,515 tokens on 8 heads). Each thread ranks a row.
+    __shared__ int lens[kRanked], row_of_rank;
+    int b = blockIdx.x / a.Hkv;
+    const int h = blockIdx.x - b * a.Hkv;
+    if (a.ranked) {
+        if (tid < a.src.rows) lens[tid] = a.lens[tid];
+        __syncthreads();
+        if (tid < a.src.rows) {
+            int rank = 0;
+            for (int i = 0; i < a.src.rows; ++i) rank += lens[i] > lens[tid] || (lens[i] == lens[tid] && i < tid);
+            if (rank == b) row_of_rank = tid;
+        }
+        __syncthreads();
+        b = row_of_rank;
+    }
     const int len = a.lens[b], budget = a.keep[b];
     if (budget < 0) {
         if (!FUSED && h == 0 && tid == 0) a.state[b] = 0;
@@ -111,7 +129,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
     const bool moves = !a.in_place || len > budget;
     bool bad = len < 0 || len > a.cap || (long long)len > (long long)a.src.cols * a.page ||
                (long long)n > (long long)a.dst.cols * a.page;
-    const float *const w = a.w + (size_t)blockIdx.x * a.cap;
+    const size_t first = ((size_t)b * a.Hkv + h) * a.cap;
+    const float *const w = a.w + first;
     const int cached = min(len, kCache);
     if (!bad && len > budget) {  // (on their way while the pages are looked at)
         const int whole = (reinterpret_cast<uintptr_t>(w) & 15) == 0 ? cached & ~3 : 0;
@@ -141,8 +160,8 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
         return;
     }
     if (!FUSED && h == 0 && tid == 0) a.state[b] = moves ? n : 0;
-    float *const w_out = a.w_out + (size_t)blockIdx.x * a.cap;
-    int32_t *const kept = a.kept + (size_t)blockIdx.x * a.cap;
+    float *const w_out = a.w_out + first;
+    int32_t *const kept = a.kept + first;
     if (len <= budget) {
         for (int i = tid; i < len; i += kSelThreads) {
             kept[i] = i;
@@ -457,6 +476,7 @@ cudaError_t launch_evict(void *kp, void *vp, int pages, int page, int32_t *table
     a.state = state;
     a.status = status;
     const long long heads = (long long)rows * Hkv;
+    a.ranked = rows <= kRanked && heads > sms;
     a.kp = static_cast<uint4 *>(kp);
     a.vp = static_cast<uint4 *>(vp);
     a.row_bits = es == 2 ? 4 : 5;
