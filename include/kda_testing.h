@@ -80,6 +80,20 @@ int kda_testing_attn_decode_timeout(const void *q, int64_t ldq, const void *k_ne
                                     float *lse, void *workspace, size_t workspace_bytes,
                                     int32_t warp, int32_t at, void *stream);
 
+/*
+ * kda_attn_weights likewise (bf16 I/O only, arguments as there): warp 0..15 of the
+ * exponentials, 16 products, 17 copies of keys, 18..21 rows, of which 18 walks the parts. The weights
+ * are garbage afterwards.
+ */
+int kda_testing_attn_weights_timeout(const void *q, int64_t ldq, const void *k_pages,
+                                     int32_t num_pages, int32_t page_size,
+                                     const int32_t *block_table, int64_t table_ld,
+                                     int32_t table_cols, const int32_t *seq_lens, const float *lse,
+                                     const int32_t *index, const int32_t *count, float scale,
+                                     int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int32_t io, float *weights, int32_t cap, void *workspace,
+                                     int32_t warp, int32_t at, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -165,6 +165,8 @@ def load() -> ctypes.CDLL:
         lib.kda_testing_attn_decode_timeout.argtypes = (lib.kda_attn_decode.argtypes[:-1] +
                                                         [I32, I32, P])
         lib.kda_testing_attn_decode_timeout.restype = ctypes.c_int
+        lib.kda_testing_attn_weights_timeout.argtypes = lib.kda_attn_weights.argtypes[:-1] + [I32, I32, P]
+        lib.kda_testing_attn_weights_timeout.restype = ctypes.c_int
         lib.kda_testing_prefill_chain_timeout.argtypes = [P, P, P, P, P, F32, P, P, I32, I32, I32,
                                                           I32, I32, I32, P, P, P, SZ, I32, P]
         lib.kda_testing_prefill_chain_timeout.restype = ctypes.c_int

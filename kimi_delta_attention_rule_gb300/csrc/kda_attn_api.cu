@@ -137,7 +137,7 @@ struct Window {
 // A warp of the bf16 kernel that gives up at one of its waits (tests).
 struct Lose {
     int32_t warp = -1, at = 0;
-    bool ok(int32_t io) const { return io == KDA_BF16 && warp >= 0 && warp < 12 && at >= 0; }
+    bool ok(int32_t io, int32_t warps = 12) const { return io == KDA_BF16 && warp >= 0 && warp < warps && at >= 0; }
 };
 
 int prefill_impl(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv, float scale,
@@ -449,11 +449,11 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv, con
                                           status_of(workspace), static_cast<cudaStream_t>(stream)));
 }
 
-int kda_attn_weights(const void *q, int64_t ldq, const void *k_pages, int32_t num_pages, int32_t page_size,
-                     const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
-                     const float *lse, const int32_t *index, const int32_t *count, float scale, int32_t B, int32_t T,
-                     int32_t Hq, int32_t Hkv, int32_t D, int32_t io, float *weights, int32_t cap, void *workspace,
-                     void *stream) {
+static int weights_impl(const void *q, int64_t ldq, const void *k_pages, int32_t num_pages, int32_t page_size,
+                        const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
+                        const float *lse, const int32_t *index, const int32_t *count, float scale, int32_t B, int32_t T,
+                        int32_t Hq, int32_t Hkv, int32_t D, int32_t io, float *weights, int32_t cap, void *workspace,
+                        const Lose &lose, void *stream) {
     const int rc = check_heads(Hq, Hkv, D, io);
     if (rc != KDA_OK) return rc;
     if (B < 0 || T < 0 || num_pages < 0 || table_cols < 0 || table_ld < table_cols || cap < 0 || !scale_ok(scale) ||
@@ -494,9 +494,31 @@ int kda_attn_weights(const void *q, int64_t ldq, const void *k_pages, int32_t nu
     a.t1 = T;
     a.scale = scale;
     a.status = status_of(workspace);
+    a.lose = lose.warp + 1;
+    a.lose_at = lose.at;
     Range range("kda_attn_weights");
     return done(io == KDA_BF16 ? kda::weights::launch_weights_tc(a, sm_count(), static_cast<cudaStream_t>(stream))
                               : kda::weights::launch_weights_f32(a, sm_count(), static_cast<cudaStream_t>(stream)));
+}
+
+int kda_attn_weights(const void *q, int64_t ldq, const void *k_pages, int32_t num_pages, int32_t page_size,
+                     const int32_t *block_table, int64_t table_ld, int32_t table_cols, const int32_t *seq_lens,
+                     const float *lse, const int32_t *index, const int32_t *count, float scale, int32_t B, int32_t T,
+                     int32_t Hq, int32_t Hkv, int32_t D, int32_t io, float *weights, int32_t cap, void *workspace,
+                     void *stream) {
+    return weights_impl(q, ldq, k_pages, num_pages, page_size, block_table, table_ld, table_cols, seq_lens, lse, index,
+                        count, scale, B, T, Hq, Hkv, D, io, weights, cap, workspace, Lose(), stream);
+}
+
+int kda_testing_attn_weights_timeout(const void *q, int64_t ldq, const void *k_pages, int32_t num_pages,
+                                     int32_t page_size, const int32_t *block_table, int64_t table_ld, int32_t table_cols,
+                                     const int32_t *seq_lens, const float *lse, const int32_t *index, const int32_t *count,
+                                     float scale, int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t io,
+                                     float *weights, int32_t cap, void *workspace, int32_t warp, int32_t at, void *stream) {
+    const Lose lose = {warp, at};
+    if (!lose.ok(io, 22)) return KDA_ERR_INVALID_ARG;
+    return weights_impl(q, ldq, k_pages, num_pages, page_size, block_table, table_ld, table_cols, seq_lens, lse, index,
+                        count, scale, B, T, Hq, Hkv, D, io, weights, cap, workspace, lose, stream);
 }
 
 size_t kda_cache_evict_workspace_size(int32_t rows) {

@@ -33,6 +33,7 @@ struct Args {
     int t0, t1;          // the accepted tokens of this launch
     float scale;
     uint32_t *status;    // or NULL
+    int lose, lose_at;   // tests: 1 + the warp that gives up, and at which of its waits (0: none does)
 };
 
 __device__ __forceinline__ void flag(const Args &a) {

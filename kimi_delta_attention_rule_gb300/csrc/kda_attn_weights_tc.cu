@@ -43,7 +43,7 @@ constexpr int kTcThreads = 32 * (kWarpRows + kRowWarps);
 constexpr int kTile = 128, kMaxRows = 512;
 constexpr uint32_t kTileBytes = 32768, kHalf = 16384;
 constexpr int kDescs = 4, kMaxRing = 6;
-constexpr uint64_t kWaitNs = 2000000000;
+constexpr uint64_t kWaitNs = 2000000000, kTestWaitNs = 20000000;
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
     float2 d;
@@ -95,7 +95,8 @@ struct Shape {
     __host__ __device__ uint32_t bytes() const { return shared_at() + (uint32_t)sizeof(Shared); }
 };
 
-// A wait with a limit, of a whole warp.
+// A wait of a whole warp, at most LIMIT nanoseconds.
+template <uint64_t LIMIT>
 __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
     bool ok = false;
     uint64_t t0 = 0;
@@ -104,7 +105,7 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity) {
         if ((n & 1023) != 0) continue;
         const uint64_t t = tc::globaltimer_ns();
         if (t0 == 0) t0 = t;
-        else if (t - t0 > kWaitNs) break;
+        else if (t - t0 > LIMIT) break;
     }
     return __all_sync(0xffffffffu, ok);
 }
@@ -141,12 +142,16 @@ __device__ __forceinline__ float2 exp_sum(uint32_t x[N / 16][16], const int *see
     return sum;
 }
 
-// PARTS groups share a tile; SMALL: 16 rows at the most.
-template <int PARTS, bool SMALL>
+// PARTS groups share a tile; SMALL: 16 rows at the most. Every wait has a limit: a role whose wait
+// runs out goes to the kernel's end, the others follow as theirs run out or they see `dead`, and the
+// status tells; the copies and products in flight are waited for first. TEST
+// (kda_testing_attn_weights_timeout): waits of 20 ms, and warp a.lose - 1 gives up at its wait number a.lose_at.
+template <int PARTS, bool SMALL, bool TEST>
 __global__ void __launch_bounds__(kTcThreads, 1)
     weights_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ CUtensorMap map, const __grid_constant__ CUtensorMap q_map,
                       const Shape shape) {
     constexpr int kQTiles = PARTS == 4 ? 1 : 2;
+    constexpr uint64_t kLimit = TEST ? kTestWaitNs : kWaitNs;
     extern __shared__ __align__(1024) unsigned char sm[];
     const uint32_t base = smem_u32(sm);
     Shared &sh = *reinterpret_cast<Shared *>(sm + shape.shared_at());
@@ -202,10 +207,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     let_next_start();
     bool alive = true;
     uint32_t nd = 0;  // descriptors taken
+    int waits = 0;
+    auto warp_wait = [&](uint32_t at, uint32_t parity) -> bool {
+        if constexpr (TEST) {
+            if (warp == a.lose - 1 && waits++ >= a.lose_at) return false;
+        }
+        return wait_warp<kLimit>(at, parity);
+    };
     // a wait that may last as long as a part does: it ends when another role gives up
     auto long_wait = [&](uint32_t at, uint32_t parity) -> bool {
         for (int i = 0; i < 100; ++i) {
-            if (wait_warp(at, parity)) return true;
+            if (warp_wait(at, parity)) return true;
             if (*dead) return false;
         }
         return false;
@@ -235,7 +247,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int *const seen = sh.seen[slot] + part * shape.ns;
             const int ta = d->ta, tb = d->tb, len = d->len, rows = d->tokens * a.G - part * shape.ns;
             float *const w = a.w + ((size_t)d->b * a.Hkv + d->h) * a.cap;
-            if (!(alive = wait_warp(bar(sh.rfull[slot]), (nd / kDescs) & 1))) break;
+            if (!(alive = warp_wait(bar(sh.rfull[slot]), (nd / kDescs) & 1))) break;
             const int4 four = sh.least[slot];
             const int least = min(min(four.x, four.y), min(four.z, four.w));
             for (int t = ta + (int)((group / PARTS - tiles) % kTurns); t < tb; t += kTurns, ++mine) {
@@ -244,7 +256,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float before = ok ? w[pos] : 0.f;
                 const bool masked = least < (t + 1) * kTile;
                 float2 sum = make_float2(0.f, 0.f);
-                if (!(alive = wait_warp(bar(sh.sfull[buffer]), mine & 1))) break;
+                if (!(alive = warp_wait(bar(sh.sfull[buffer]), mine & 1))) break;
                 tc::fence_after_sync();
                 if (SMALL) {
                     uint32_t x[1][16];
@@ -263,7 +275,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 0) mbar_arrive(bar(sh.sempty[buffer]));
                 float total = sum.x + sum.y;
                 if (part > 0) {
-                    if (mine > 0 && !(alive = wait_warp(bar(sh.pempty[group][quad]), (mine - 1) & 1))) break;
+                    if (mine > 0 && !(alive = warp_wait(bar(sh.pempty[group][quad]), (mine - 1) & 1))) break;
                     sh.sums[group][r] = total;
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(sh.pfull[group][quad]));
@@ -271,7 +283,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 }
 #pragma unroll
                 for (int e = 1; e < PARTS; ++e) {
-                    if (alive) alive = wait_warp(bar(sh.pfull[lead + e][quad]), mine & 1);
+                    if (alive) alive = warp_wait(bar(sh.pfull[lead + e][quad]), mine & 1);
                     if (!alive) break;
                     total += sh.sums[lead + e][r];
                     __syncwarp();
@@ -395,7 +407,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // (as the ring's copies below)
         if (wr == 0 && shape.box > 0)
             for (uint32_t i = 0; i < kQTiles; ++i)
-                alive = wait_warp(bar(sh.qfull[i]), ((nd + kQTiles - 1 - i) / kQTiles - 1) & 1) && alive;
+                alive = wait_warp<kLimit>(bar(sh.qfull[i]), ((nd + kQTiles - 1 - i) / kQTiles - 1) & 1) && alive;
     } else if (warp == kWarpTma) {
         // ---- K tiles -------------------------------------------------------------------------
         // A copy is at most a page's rows of a tile; a lane each looks up the pages of the next 32
@@ -421,7 +433,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 else if (pos < len && pos < tb * kTile) flag(a);
                 for (int t = t0; t < tb && t < t0 + tiles_ahead; ++t) {
                     const uint32_t slot = kv % shape.ring;
-                    if (kv >= (uint32_t)shape.ring && !(alive = wait_warp(bar(sh.kempty[slot]), (kv / shape.ring - 1) & 1))) break;
+                    if (kv >= (uint32_t)shape.ring && !(alive = warp_wait(bar(sh.kempty[slot]), (kv / shape.ring - 1) & 1))) break;
                     ++kv;
                     const int copies = (min(len - t * kTile, kTile) + rows - 1) >> row_bits;
                     const uint32_t full = bar(sh.kfull[slot]), dst = base + shape.ring_at() + slot * kTileBytes;
@@ -439,7 +451,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         // the last copy into each slot has landed before the CTA ends, whoever takes it or not
         for (uint32_t i = 0; i < (uint32_t)shape.ring; ++i)
-            alive = wait_warp(bar(sh.kfull[i]), ((kv + shape.ring - 1 - i) / shape.ring - 1) & 1) && alive;
+            alive = wait_warp<kLimit>(bar(sh.kfull[i]), ((kv + shape.ring - 1 - i) / shape.ring - 1) & 1) && alive;
     } else {
         // ---- products ------------------------------------------------------------------------
         const uint64_t k_more = tc::smem_desc(base + shape.k_more_at(), 128, 256), q_more = tc::smem_desc(base + shape.q_more_at(), 128, 256);
@@ -449,16 +461,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         while (const Desc *d = next_desc()) {
             const int n = d->tb - d->ta;
             const uint32_t tile = nd % kQTiles;
-            if (!(alive = wait_warp(bar(sh.qfull[tile]), (nd / kQTiles) & 1))) break;
+            if (!(alive = warp_wait(bar(sh.qfull[tile]), (nd / kQTiles) & 1))) break;
             for (int t = 0; t < n; ++t) {
                 const uint32_t slot = kv % shape.ring;
-                if (!(alive = wait_warp(bar(sh.kfull[slot]), (kv / shape.ring) & 1))) break;
+                if (!(alive = warp_wait(bar(sh.kfull[slot]), (kv / shape.ring) & 1))) break;
                 const uint64_t kd = k_desc + slot * (kTileBytes >> 4);
 #pragma unroll
                 for (int e = 0; e < (PARTS == 4 ? 2 : 1); ++e) {
                     const uint32_t s = PARTS == 1 ? kv & 3 : (PARTS == 2 ? kv & 1 : e);
                     const uint32_t used = PARTS == 1 ? kv >> 2 : (PARTS == 2 ? kv >> 1 : kv);  // times that this S has been
-                    if (alive && used > 0) alive = wait_warp(bar(sh.sempty[s]), (used - 1) & 1);
+                    if (alive && used > 0) alive = warp_wait(bar(sh.sempty[s]), (used - 1) & 1);
                     if (!alive) break;
                     tc::fence_after_sync();
                     const uint32_t tS = tm + (PARTS == 1 ? 128 : 256) * s, row = e * 2 * shape.ns;
@@ -481,7 +493,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             done_desc();
         }
         tc::mma_commit_lead(lead, bar(sh.drained));  // no product outlives the CTA, or its TMEM
-        alive = wait_warp(bar(sh.drained), 0) && alive;
+        alive = wait_warp<kLimit>(bar(sh.drained), 0) && alive;
     }
     __syncwarp();
     if (!alive && lane == 0) {
@@ -493,18 +505,26 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (warp == kWarpMma) tc::tmem_dealloc(tm, 512);
 }
 
-template <int PARTS, bool SMALL>
-static cudaError_t launch_form(const Args &a, const CUtensorMap &map, const CUtensorMap &q_map, const Shape &shape, unsigned ctas, cudaStream_t stream) {
+template <int PARTS, bool SMALL, bool TEST>
+static cudaError_t launch_kernel(const Args &a, const CUtensorMap &map, const CUtensorMap &q_map, const Shape &shape, unsigned ctas,
+                                 cudaStream_t stream) {
     static std::atomic<uint64_t> ready{0};  // devices whose limit is raised
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        e = cudaFuncSetAttribute(weights_tc_kernel<PARTS, SMALL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
+        e = cudaFuncSetAttribute(weights_tc_kernel<PARTS, SMALL, TEST>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    return launch_early(weights_tc_kernel<PARTS, SMALL>, dim3(ctas), kTcThreads, shape.bytes(), stream, a, map, q_map, shape);
+    return launch_early(weights_tc_kernel<PARTS, SMALL, TEST>, dim3(ctas), kTcThreads, shape.bytes(), stream, a, map, q_map, shape);
+}
+
+template <int PARTS, bool SMALL>
+static cudaError_t launch_form(const Args &a, const CUtensorMap &map, const CUtensorMap &q_map, const Shape &shape, unsigned ctas,
+                               cudaStream_t stream) {
+    return a.lose > 0 ? launch_kernel<PARTS, SMALL, true>(a, map, q_map, shape, ctas, stream)
+                      : launch_kernel<PARTS, SMALL, false>(a, map, q_map, shape, ctas, stream);
 }
 
 cudaError_t launch_weights_tc(Args a, int sms, cudaStream_t stream) {
