@@ -602,7 +602,7 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv,
  *   (as many as fit; the first ones first) and of the others those of the largest weights
  *   (of equal ones the earlier; a NaN counts as the largest). They keep their order: slot i
  *   takes the token of slot kept[b][h][i], in k_pages, v_pages and weights.
- *     dst_table NULL: in place. Rows whose tokens all stay are left alone.
+ *     dst_table NULL or block_table itself: in place. Rows whose tokens all stay are left alone.
  *     else DEVICE int32 [rows, dst_cols]: the slots are those of its pages, which must be none
  *     of block_table's, with room for the staying tokens (kda_cache_alloc on dst_table); the
  *     old pages are only read (they may be shared), kda_cache_free gives them back.

@@ -535,6 +535,10 @@ int kda_cache_evict(void *k_pages, void *v_pages, int32_t num_pages, int32_t pag
     if (num_pages < 0 || rows < 0 || table_cols < 0 || table_ld < table_cols || sinks < 0 || recent < 0 || cap < 0)
         return KDA_ERR_INVALID_ARG;
     if (!page_ok(page_size)) return KDA_ERR_UNSUPPORTED;
+    if (dst_table != nullptr && dst_table == block_table) {  // in place, said otherwise
+        if (dst_ld != table_ld || dst_cols != table_cols) return KDA_ERR_INVALID_ARG;
+        dst_table = nullptr;
+    }
     if (dst_table != nullptr && (dst_cols < 0 || dst_ld < dst_cols)) return KDA_ERR_INVALID_ARG;
     if ((long long)num_pages * Hkv * page_size > 0x7fffffffLL || num_pages > kMaxPages ||
         (long long)rows * table_cols > kMaxPages || (long long)rows * dst_cols > kMaxPages ||

@@ -30,7 +30,8 @@ def test_refusals():
     for kw in (dict(D=64), dict(io=5), dict(page=8), dict(page=40)):
         assert f(**kw) == UNSUPPORTED, kw
     for kw in (dict(Hkv=0), dict(P=-1), dict(rows=-1), dict(cols=-1), dict(ld=4), dict(sinks=-1), dict(recent=-1), dict(cap=-1),
-               dict(dst=FAKE, dcols=3, dld=2), dict(dst=FAKE, dcols=-1), dict(kp=None), dict(vp=None), dict(t=None), dict(lens=None),
+               dict(dst=ctypes.c_void_p(0x200000), dcols=3, dld=2), dict(dst=ctypes.c_void_p(0x200000), dcols=-1),
+               dict(dst=FAKE, dcols=3, dld=5), dict(dst=FAKE, dcols=5, dld=6), dict(kp=None), dict(vp=None), dict(t=None), dict(lens=None),
                dict(keep=None), dict(w=None), dict(wo=None), dict(kept=None), dict(ws=None), dict(kp=ODD), dict(vp=ODD), dict(ws=ODD),
                dict(nbytes=need - 1), dict(w=ctypes.c_void_p(0x100002)), dict(P=1 << 27), dict(rows=1 << 25), dict(cols=1 << 24, ld=1 << 24, page=256)):
         assert f(**kw) == INVALID, kw
@@ -204,6 +205,13 @@ def test_weights_past_the_length_are_left_alone():
     tail = c.w[..., 100:].clone()
     in_place(c, [40], 1, 1)
     assert torch.equal(c.w[..., 100:], tail) and (c.w[..., 40:100] == 0).all()
+
+
+@pytest.mark.gpu
+def test_the_same_table_is_in_place():
+    for lens in ([500, 60], [9000]):
+        c = Cache(lens, 16, 2, BF, seed=15)
+        in_place(c, [40] * len(lens), 3, 20, dst_table=c.table)
 
 
 @pytest.mark.gpu
