@@ -29,7 +29,7 @@ cudaError_t launch_attn_decode_f32(const Args &a, const void *q, const void *kp,
 }  // namespace attn
 namespace weights {
 cudaError_t launch_weights_tc(Args a, int sms, cudaStream_t stream);
-cudaError_t launch_weights_f32(const Args &a, int sms, cudaStream_t stream);
+cudaError_t launch_weights_f32(Args a, int sms, cudaStream_t stream);
 }  // namespace weights
 namespace cache {
 cudaError_t launch_evict(void *kp, void *vp, int pages, int page, int32_t *table, int64_t ld, int rows, int cols,
