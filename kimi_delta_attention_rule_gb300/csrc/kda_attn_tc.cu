@@ -28,7 +28,9 @@
 // tokens, 32 heads on 8: 320 us, 1,718 TFLOP/s in a short run in a graph, 355 us in calls back to
 // back (at the power cap); the tensor pipe is busy 74 % of the time and the
 // exponentials' 37 %; a step of two row tiles takes some 2,700 cycles, 2,048 of them products.
-// One token each of 128 sequences, 400,003 cached tokens: 251 us, 6.5 TB/s (loads). Some
+// One token each of 128 sequences, 400,003 cached tokens: 251 us, 6.5 TB/s (loads).
+// Through a window (instances of their own): 15,001 tokens behind 1,383, window 4,096: 570 us in a graph, 1.66
+// PFLOP/s of visible keys; 128 sequences, window 1,024: 96.5 us, 5.4 TB/s, as caches of that length. Some
 // 11,000 cycles pass before the first softmax (5,500 of a direct call): the search for the
 // CTA's work, the page's number, the first tile, each from a cold cache. Tried without gain: 16
 // softmax warps of two threads a row (spills), halves of 64 keys with a maximum ahead of

@@ -17,6 +17,13 @@
 // wide, so that K is read once for both, and up to 512 (PARTS = 4) a tile is two products for all four
 // groups; the groups of a tile hand their sums to its first one. With 512 rows the Q tile
 // takes the room of two, and a CTA waits for the next part's rows.
+//
+// Measured (GB300; copy 6,790 GB/s): one token of 32 heads on 8 over 65,531 cached ones 26.8 us (5.1 TB/s with 5 us
+// of start), four drafts of 128 sequences on 400,003 134 us (6.3 TB/s): bound by HBM. 64 tokens of 8
+// prompts, 512 rows per kv head, 40,009 cached: 26 us, 1.73 us a tile and SM where its products alone take
+// 1.24 and its exponentials 1.0, which alternate on the two halves of TMEM. Tried on those 512 rows: two groups of
+// warps that take 128 columns into registers at once 2.2 us, products of 128 rows instead of 256 2.0 (their own
+// time 1.49), -lse from shared memory with a product and a sum more per element 2.2, two launches of 256 rows 2.2.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
