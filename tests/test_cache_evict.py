@@ -191,6 +191,15 @@ def test_long_rows(lens, keep, dt, how):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("how", [in_place, elsewhere])
+@pytest.mark.parametrize("fill", [lambda w: None, ties, odd_values])
+@pytest.mark.parametrize("length,keep", [(30001, 9001), (49149, 40001), (49152, 127), (49153, 49100), (60001, 20011)])
+def test_rows_about_what_a_block_holds(length, keep, fill, how):
+    """49,152 weights lie in shared memory, the rest is read again; equal ones across all of it."""
+    how(Cache([length, 4099], 256, 1, BF, seed=length % 91, spare=260, weights=fill), [keep, keep], 5, 33)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("how", [in_place, elsewhere])
 @pytest.mark.parametrize("rows,most", [(90, 120), (90, 400), (25, 2600)])
 def test_many_rows(rows, most, how):
     g = torch.Generator().manual_seed(6)
