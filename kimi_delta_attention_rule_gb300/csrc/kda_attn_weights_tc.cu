@@ -14,15 +14,17 @@
 // first walks the CTA's parts ahead of the others.
 //
 // Up to 128 rows the groups take the tiles in turn. Up to 256 (PARTS = 2) a product is two groups
-// wide, so that K is read once for both, and up to 512 (PARTS = 4) a tile is two products for all four
-// groups; the groups of a tile hand their sums to its first one. With 512 rows the Q tile
+// wide, so that K is read once for both, and up to 512 (PARTS = 4) a tile is two products, of each of which all four
+// groups take a quarter (a half each of one of them: 1.73 us a tile instead of 1.62, since two warps a scheduler
+// hide less); the groups of a tile hand their sums to its first one. With 512 rows the Q tile
 // takes the room of two, and a CTA waits for the next part's rows.
 //
 // Measured (GB300; copy 6,790 GB/s): one token of 32 heads on 8 over 65,531 cached ones 26.8 us (5.1 TB/s with 5 us
 // of start), four drafts of 128 sequences on 400,003 134 us (6.3 TB/s): bound by HBM. 64 tokens of 8
-// prompts, 512 rows per kv head, 40,009 cached: 26 us, 1.73 us a tile and SM where its products alone take
-// 1.24 and its exponentials 1.0, which alternate on the two halves of TMEM. Tried on those 512 rows: two groups of
-// warps that take 128 columns into registers at once 2.2 us, products of 128 rows instead of 256 2.0 (their own
+// prompts, 512 rows per kv head, 40,009 cached: 24 us, 1.62 us a tile and SM where its products alone take
+// 1.24 and its exponentials with one of nine products 1.49 (1.0 of the exponentials' pipe). Tried on those 512 rows: two groups of
+// warps that take 128 columns into registers at once 2.2 us, four that take their 64 at once 1.7, the next 16
+// columns while these are summed 1.83, products of 128 rows instead of 256 2.0 (their own
 // time 1.49), -lse from shared memory with a product and a sum more per element 2.2, two launches of 256 rows 2.2.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc::mbar_init(bar(sh.drained), 1);
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(bar(sh.sfull[i]), 1);
-            tc::mbar_init(bar(sh.sempty[i]), PARTS == 1 ? 4 : 8);
+            tc::mbar_init(bar(sh.sempty[i]), 4 * PARTS);
             for (int j = 0; j < 4; ++j) {
                 tc::mbar_init(bar(sh.pfull[i][j]), 1);
                 tc::mbar_init(bar(sh.pempty[i][j]), 1);
@@ -244,15 +246,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- exponentials: thread = key -------------------------------------------------
         const int group = warp >> 2, quad = warp & 3, r = 32 * quad + lane;
         const int part = group % PARTS, lead = group - part;  // which rows of a tile; the group that writes
-        const int buffer = PARTS == 1 ? group : group >> 1;
-        const uint32_t tS = tm + ((uint32_t)(32 * quad) << 16) + (PARTS == 1 ? 128 * group : 256 * buffer + (group & 1) * shape.ns);
+        const int buffer = PARTS == 1 ? group : (PARTS == 2 ? group >> 1 : 0);
+        const int cols = PARTS == 4 ? shape.ns / 2 : shape.ns;  // of this group in a product
+        const uint32_t tS = tm + ((uint32_t)(32 * quad) << 16) + (PARTS == 1 ? 128 : 256) * buffer + part * cols;
         const float c = a.scale * attn::kLog2e;
         constexpr int kTurns = kGroups / PARTS;  // every so many tiles are this group's
         uint32_t tiles = 0, mine = 0;  // of the CTA, of this group
         while (const Desc *d = next_desc()) {
             const uint32_t slot = nd % kDescs;
-            const int *const seen = sh.seen[slot] + part * shape.ns;
-            const int ta = d->ta, tb = d->tb, len = d->len, rows = d->tokens * a.G - part * shape.ns;
+            const int *const seen = sh.seen[slot] + part * cols;
+            const int ta = d->ta, tb = d->tb, len = d->len, rows = d->tokens * a.G - part * cols;
             float *const w = a.w + ((size_t)d->b * a.Hkv + d->h) * a.cap;
             if (!(alive = warp_wait(bar(sh.rfull[slot]), (nd / kDescs) & 1))) break;
             const int4 four = sh.least[slot];
@@ -263,23 +266,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 const float before = ok ? w[pos] : 0.f;
                 const bool masked = least < (t + 1) * kTile;
                 float2 sum = make_float2(0.f, 0.f);
-                if (!(alive = warp_wait(bar(sh.sfull[buffer]), mine & 1))) break;
-                tc::fence_after_sync();
-                if (SMALL) {
-                    uint32_t x[1][16];
-                    tc::tmem_ld_cols<1>(tS, x);
-                    sum = exp_sum<16, true>(x, seen, 0, pos, c, sum);
-                } else {
-                    for (int at = 0; at < shape.ns; at += 32) {
-                        uint32_t x[2][16];
-                        tc::tmem_ld_cols<2>(tS + at, x);
-                        if (masked || at + 32 > rows) sum = exp_sum<32, true>(x, seen, at, pos, c, sum);
-                        else sum = exp_sum<32, false>(x, seen, at, pos, c, sum);
+#pragma unroll 1
+                for (int e = 0; e < (PARTS == 4 ? 2 : 1); ++e) {  // products of a tile
+                    if (!(alive = warp_wait(bar(sh.sfull[buffer + e]), mine & 1))) break;
+                    tc::fence_after_sync();
+                    if (SMALL) {
+                        uint32_t x[1][16];
+                        tc::tmem_ld_cols<1>(tS, x);
+                        sum = exp_sum<16, true>(x, seen, 0, pos, c, sum);
+                    } else {
+                        const int row0 = 2 * shape.ns * e;
+                        int at = 0;
+                        for (; at + 32 <= cols; at += 32) {
+                            uint32_t x[2][16];
+                            tc::tmem_ld_cols<2>(tS + 256 * e + at, x);
+                            if (masked || row0 + at + 32 > rows) sum = exp_sum<32, true>(x, seen, row0 + at, pos, c, sum);
+                            else sum = exp_sum<32, false>(x, seen, row0 + at, pos, c, sum);
+                        }
+                        if (PARTS == 4 && at < cols) {  // 48 columns
+                            uint32_t x[1][16];
+                            tc::tmem_ld_cols<1>(tS + 256 * e + at, x);
+                            sum = exp_sum<16, true>(x, seen, row0 + at, pos, c, sum);
+                        }
                     }
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(sh.sempty[buffer + e]));
                 }
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(sh.sempty[buffer]));
+                if (!alive) break;
                 float total = sum.x + sum.y;
                 if (part > 0) {
                     if (mine > 0 && !(alive = warp_wait(bar(sh.pempty[group][quad]), (mine - 1) & 1))) break;
