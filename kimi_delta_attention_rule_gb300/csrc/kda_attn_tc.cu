@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int lim = seen - shift - t0;
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            auto below = [&](int n) { return n >= 32 * i + 32 ? ~0u : (n <= 32 * i ? 0u : (1u << (n & 31)) - 1); };
+                            auto below = [&](int n) { return __funnelshift_lc(~0u, 0u, (uint32_t)max(n - 32 * i, 0)); };  // (by 32 at most)
                             uint32_t see = below(lim);
                             if (WIN) see &= ~below(from - t0) | below(a.sinks - t0);
                             if (PAGED && drafts) see = i == 0 ? (uint32_t)bits : (i == 1 ? (uint32_t)(bits >> 32) : 0u);
