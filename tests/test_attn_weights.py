@@ -242,6 +242,17 @@ def test_one_long_sequence():
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,hq,hkv", [(64, 32, 4), (40, 32, 4), (64, 24, 4), (43, 32, 4), (32, 32, 4), (60, 4, 4)])
+def test_many_rows_of_long_sequences(T, hq, hkv, dt):
+    """A CTA goes from one sequence's rows to the next one's."""
+    x = make([5000, 129, 1, 4001, 63, 6100, 2500, 3333], T, hq, hkv, 32, dt, seed=51)
+    *r, st = run(x)
+    assert st == OK
+    check(x, *r)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
 def test_same_bits_captured_and_on_another_stream(dt):
     x = make([1000, 40, 333], 12, 8, 2, 16, dt, seed=49)
     ref = reference(x)
