@@ -490,7 +490,7 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
  * Other keys between the two stretches are not used, but as in the plain calls a NaN or an infinity in v
  * reaches rows whose own keys share its key tile. All else (arguments, workspace, its size,
  * alignment, errors) is as in the plain calls; with a window past the longest sequence the
- * result is theirs. Work and reads grow with the window, not with the context.
+ * result is theirs, up to rounding. Work and reads grow with the window, not with the context.
  */
 int kda_attn_prefill_window(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk,
                             int64_t ldv, float scale, int32_t window, int32_t sinks,

@@ -313,6 +313,20 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
 
 cudaError_t launch_attn_combine(const Args &a, bool bf16, bool joins_early, cudaStream_t stream);
 
+// Through a window: whether each item goes to a CTA of its own, as many as there are. That leaves SMs idle in
+// the last wave for as long as its items take; shared evenly the work costs a search and a join, as much as some
+// more keys (144 for 64 rows, for fewer rows 256). Direct and split, us: 2,011 tokens of three prompts, 12
+// heads on 4, window 64: 48, 57, 128: 70, 74, 200: 95, 91; 7 prompts of 50 tokens 14, 27; 4 drafts of 16 sequences,
+// 32 heads on 8, window 128: 19, 25, 400: 37, 39; 11 of 6 sequences, 12 on 4, window 64: 24.1, 24.6, 128: 34, 29. (Items of more than 8 tiles differ too much; a prompt's CTA looks at all sequences; the
+// division of slots is exact below 2^20.)
+template <bool PAGED, int RPT>
+static bool window_direct(const Args &a, long long slots, long long keys) {
+    const long long room = 2LL * a.sms, waves = (slots + room - 1) / room;
+    const long long own = (long long)a.window + a.sinks + (PAGED ? kF32Tile : a.block), longest = keys < own ? keys : own;
+    return slots < (1 << 20) && (PAGED || a.N <= 256) && longest <= 8 * kF32Tile &&
+           longest * (waves * room - slots) <= (RPT < 8 ? 256 : 144) * room;
+}
+
 template <bool PAGED, int RPT, bool WIN>
 static cudaError_t launch_form(Args a, const F32Ptrs &io, cudaStream_t stream) {
     constexpr int rows = 8 * RPT;
@@ -326,10 +340,11 @@ static cudaError_t launch_form(Args a, const F32Ptrs &io, cudaStream_t stream) {
     const long long slots = PAGED ? (long long)a.N * a.Hkv * ((a.T + a.tile_tokens - 1) / a.tile_tokens)
                                   : ((long long)a.Tq_total / a.tile_tokens + a.N) * a.Hkv;
     long long keys = PAGED ? (long long)a.table_cols * a.page + kF32Tile : a.Tk;
+    const bool own = WIN && window_direct<PAGED, RPT>(a, slots, keys);
     if (WIN) keys = set_window(a, keys, 1, 1);
     set_unit(a, (double)slots * ((double)keys + a.extra + kF32Tile));
     // (a CTA each for four prompts of 25 tokens: 14.3 us instead of 35.6)
-    a.direct = slots <= 2 * a.sms && keys <= 2 * kF32Tile;
+    a.direct = own || (slots <= 2 * a.sms && keys <= 2 * kF32Tile);
     cudaError_t e = cudaFuncSetAttribute(attn_f32_kernel<PAGED, RPT, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          f32_smem(RPT));
     if (e != cudaSuccess) return e;

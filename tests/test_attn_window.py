@@ -108,6 +108,16 @@ def test_long_prompt_on_many_sms(window):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("window", [30, 64, 150])
+def test_many_short_prompts(window, dt):
+    """More items than SMs have room for at a time, of a few tiles each."""
+    g = torch.Generator().manual_seed(window)
+    lens = torch.randint(0, 90, (60,), generator=g).tolist()
+    run_prefill(lens, lens, 12, 4, dt, window, 3, seed=window)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
 def test_window_past_the_end_is_the_plain_call(dt):
     lens = [3, 700, 129]
     q, k, v, out, lse = run_prefill(lens, lens, 4, 2, dt, 700, 0, seed=9)
@@ -238,6 +248,17 @@ def test_a_batch_over_many_sms():
     x = make(lens, 1, 8, 2, 16, BF, seed=26)
     out, lse = decode(x, 700, 4)
     check_decode(x, out, lse, 700, 4)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("B,T,hq,window", [(90, 5, 8, 40), (90, 18, 16, 64), (100, 1, 4, 150), (50, 40, 12, 200)])
+def test_many_short_items(B, T, hq, window, dt):
+    g = torch.Generator().manual_seed(B + T)
+    x = make(torch.randint(0, 400, (B,), generator=g).tolist(), T, hq, 4, 32, dt, seed=31)
+    mask = tree_masks(B, T, B)
+    out, lse = decode(x, window, 3, mask)
+    check_decode(x, out, lse, window, 3, mask)
 
 
 @pytest.mark.gpu
