@@ -10,8 +10,10 @@
 // With more rows (weights_kernel) a thread of 128 forms a 4 x 4 piece of S = K Q^T for 32 rows at a time, two
 // products per instruction, its exponentials, and their sum over its rows; the eight threads of a key add up
 // in shared memory in a fixed order. Up to 64 rows stay in shared memory while the CTA stays with a (sequence,
-// head), more of them take further launches: K, mostly from L2, costs less than rows that are loaded for every
-// tile (128 rows on 65,531 tokens 481 us instead of 562, 0.48 of the FMA pipe). Several CTAs per SM hide one another's loads.
+// head). More of them are loaded in turn for every tile where a CTA has few (185 rows, one tile: 55 us, in four
+// launches 76; 512 rows, three tiles: 358, 379), or take further launches where it has many: K, mostly from L2, then
+// costs less than the rows (116 rows, five tiles: 183 in one, 166 in two; 128 rows on 65,531 tokens 481 us instead
+// of 562, 0.48 of the FMA pipe). Several CTAs per SM hide one another's loads.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -37,6 +39,7 @@ __device__ __forceinline__ void cp16(float *dst, const float *src, bool ok) {  /
 __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_constant__ Args a) {
     extern __shared__ __align__(16) float sm[];
     const int held = (a.t1 - a.t0) * a.G > kRows ? kMostRows : kRows;  // rows that there is room for
+    const int most = held / a.G;                                     // tokens
     float *const Ks = sm, *const Qs = Ks + kKeys * kD, *const sums = Qs + held * kD, *const minus_lse = sums + 8 * kKeys;
     int *const seen = reinterpret_cast<int *>(minus_lse + held);  // keys that a row sees
     wait_before();
@@ -48,23 +51,29 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_const
     walk.init(a, blockIdx.x, gridDim.x);
     Part p;
     while (walk.next(a, p)) {
-        const int rows = p.s.tokens * a.G, padded = (rows + kRows - 1) & ~(kRows - 1);
-        __syncthreads();  // the last part is through
+        // rows of the tokens from `first` on, as many as there is room for
+        auto load_rows = [&](int first) {
+            const int rows = min(p.s.tokens - first, most) * a.G, padded = (rows + kRows - 1) & ~(kRows - 1);
 #pragma unroll 4
-        for (int r = warp; r < padded; r += kThreads / 32) {
-            const int i = r / a.G, g = r - i * a.G, tok = r < rows ? token_of(a, p.b, a.t0 + i) : -1;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            float l = -INFINITY;
-            if (tok >= 0) {
-                x = load4(q + ((size_t)p.b * a.T + tok) * a.ldq + (size_t)(p.h * a.G + g) * kD + 4 * lane);
-                l = a.lse[((size_t)p.b * a.T + tok) * Hq + p.h * a.G + g];
+            for (int r = warp; r < padded; r += kThreads / 32) {
+                const int i = r / a.G, g = r - i * a.G, tok = r < rows ? token_of(a, p.b, a.t0 + first + i) : -1;
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                float l = -INFINITY;
+                if (tok >= 0) {
+                    x = load4(q + ((size_t)p.b * a.T + tok) * a.ldq + (size_t)(p.h * a.G + g) * kD + 4 * lane);
+                    l = a.lse[((size_t)p.b * a.T + tok) * Hq + p.h * a.G + g];
+                }
+                *reinterpret_cast<float4 *>(Qs + r * kD + 4 * (lane ^ (r & 7))) = x;
+                if (lane == 0) {
+                    minus_lse[r] = -l;
+                    seen[r] = l == -INFINITY ? 0 : p.s.len - p.s.count + a.t0 + first + i + 1;
+                }
             }
-            *reinterpret_cast<float4 *>(Qs + r * kD + 4 * (lane ^ (r & 7))) = x;
-            if (lane == 0) {
-                minus_lse[r] = -l;
-                seen[r] = l == -INFINITY ? 0 : p.s.len - p.s.count + a.t0 + i + 1;
-            }
-        }
+            return padded;
+        };
+        __syncthreads();  // the last part is through
+        int padded = load_rows(0);
+        const bool stay = p.s.tokens <= most;
         for (int t = p.ta; t < p.tb; ++t) {
             if (t > p.ta) __syncthreads();  // the last tile is through
             {  // a warp copies the rows warp, warp + 4, ..: lane i knows where row warp + 4 i is
@@ -86,9 +95,18 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const __grid_const
                 asm volatile("cp.async.commit_group;\n" ::: "memory");
             }
             float sum[4] = {0.f, 0.f, 0.f, 0.f};  // keys tx + 16 e
+            if (!stay && t > p.ta) padded = load_rows(0);
             asm volatile("cp.async.wait_group 0;\n" ::: "memory");
             __syncthreads();
-            for (int r0 = 0; r0 < padded; r0 += kRows) {
+            for (int first = 0, r0 = 0;; r0 += kRows) {
+                if (r0 >= padded) {  // on to the next rows
+                    first += most;
+                    if (first >= p.s.tokens) break;
+                    __syncthreads();
+                    padded = load_rows(first);
+                    __syncthreads();
+                    r0 = 0;
+                }
                 float2 s2[4][kRpt] = {};
 #pragma unroll 4
                 for (int d = 0; d < kD; d += 4) {
@@ -229,9 +247,11 @@ cudaError_t launch_weights_f32(Args a, int sms, cudaStream_t stream) {
     if (a.T * a.G <= 8) return a.T * a.G <= 4 ? launch_few<4>(a, sms, stream) : launch_few<8>(a, sms, stream);
     const cudaError_t e = cudaFuncSetAttribute(weights_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(kMostRows));
     if (e != cudaSuccess) return e;
-    // tokens of a launch: as many as have kMostRows rows, evenly shared
-    const int most = kMostRows / a.G, T = a.T, launches = (T + most - 1) / most, per = (T + launches - 1) / launches;
-    const long long tiles = tiles_of(a), ctas = (per * a.G > kRows ? 3LL : 4LL) * sms;
+    // One launch where a CTA has four tiles at the most, else tokens of as many rows as stay in shared memory to each.
+    const int most = kMostRows / a.G, T = a.T;
+    const long long tiles = tiles_of(a);
+    const int launches = tiles <= 12LL * sms ? 1 : (T + most - 1) / most, per = (T + launches - 1) / launches;
+    const long long ctas = (per * a.G > kRows ? 3LL : 4LL) * sms;
     for (int t0 = 0; t0 < T; t0 += per) {
         a.t0 = t0;
         a.t1 = t0 + per < T ? t0 + per : T;
