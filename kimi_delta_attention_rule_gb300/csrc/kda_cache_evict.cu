@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
             need -= found[1];
         }
     }
-    // Weights in place: a round writes no slot past those that it or earlier ones have read.
+    // Weights in place: a step writes no slot past those that it or earlier ones have read.
     int above = 0, equal = 0;
     for (int i0 = 0, round = 0; i0 < len; i0 += kRound, ++round) {
         const int at = i0 + 4 * tid;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) select_kernel(const __grid_con
             if (lane >= o) incl += y;
         }
         if (lane == 31) warp_sums[round & 1][warp] = incl;
-        __syncthreads();  // (so that all of this round's weights are read; the other sums are the last round's)
+        __syncthreads();  // (so that all of this step's weights are read; the other sums are the last one's)
         const int theirs = warp_sums[round & 1][lane];
         const int before = __reduce_add_sync(0xffffffffu, lane < warp ? theirs : 0) + incl - mine;
         const int total = __reduce_add_sync(0xffffffffu, theirs);
