@@ -105,12 +105,14 @@ __global__ void __launch_bounds__(kF32Threads, 2) attn_f32_kernel(const __grid_c
             const int r = RPT * ty + i, t = p.first_tok + (int)(r * inv_g >> 16);
             seen[i] = PAGED ? p.Lk : p.Lk - p.Lq + t + 1;
             bits[i] = 0;
+            int fresh = 1;  // WIN: the new tokens that it sees, itself counted in any case
             if (PAGED && r < rows) {
                 bits[i] = a.mask != nullptr ? a.mask[(size_t)p.n * a.T + t]
                                             : (t >= 63 ? ~0ull : (2ull << t) - 1);
                 if (a.T < 64) bits[i] &= (1ull << a.T) - 1;
+                if (WIN) fresh = __popcll(bits[i] | 1ull << t);
             }
-            if (WIN) from[i] = window_start(a, PAGED && a.has_new ? p.Lk + max(1, __popcll(bits[i])) : seen[i]);
+            if (WIN) from[i] = window_start(a, PAGED && a.has_new ? p.Lk + fresh : seen[i]);
         }
         // the first key of all rows' windows: those before it, the sinks apart, are not read
         const int first = WIN ? window_start(a, PAGED ? p.Lk + a.has_new : p.Lk - p.Lq + p.first_tok + 1) : 0;

@@ -388,11 +388,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_ok = __any_sync(0xffffffffu, row_ok);
             float m = -INFINITY, l = 0.f;
             unsigned long long bits = 0;
+            int fresh = 1;  // WIN: the new tokens that it sees, itself counted in any case
             if (PAGED && row_ok) {
                 const int t = d->first_tok + (DUAL ? 0 : s * a.tile_tokens) + tok;
                 bits = a.mask != nullptr ? a.mask[(size_t)d->n * a.T + t]
                                          : (t >= 63 ? ~0ull : (2ull << t) - 1);
-                if (WIN && a.T < 64) bits &= (1ull << a.T) - 1;
+                if (WIN) {
+                    if (a.T < 64) bits &= (1ull << a.T) - 1;
+                    fresh = __popcll(bits | 1ull << t);
+                }
             }
             // keys that the row tile's first row and this row see
             const int seen0 = d->seen + (PAGED ? 0 : s * a.tile_tokens);
@@ -401,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // WIN: where this row's window starts, and where the last one of the row tile does (decode: at
             // most), among the item's keys; so are `seen` and `seen0` from there on
             const int shift = WIN ? d->span.shift : 0;
-            const int from = WIN ? window_start(a, PAGED && a.has_new ? seen + max(1, __popcll(bits)) : seen) - shift : 0;
+            const int from = WIN ? window_start(a, PAGED && a.has_new ? seen + fresh : seen) - shift : 0;
             const int from_last = WIN ? window_start(a, seen0 + (PAGED ? a.has_new * a.T : d->tokens[s] - 1)) - shift : 0;
             int t = d->start[s];
             for (int j = 0; j < steps; ++j, t += DUAL ? 2 : 1) {

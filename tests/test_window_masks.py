@@ -1,0 +1,54 @@
+"""kda_attn_decode_window under draft masks that are no plain chain or tree of their own bits: tokens whose
+masks lack their own bit, and drafts that all see one another."""
+import pytest
+import torch
+
+import kimi_delta_attention_rule_gb300 as kda
+from tests import attn_ref
+from tests.test_attn_decode import BF, DEV, F32, SCALE, make, tree_masks
+
+
+def without_own_bits(mask):
+    own = torch.tensor([(1 << t) - (2**64 if t == 63 else 0) for t in range(mask.shape[1])], dtype=torch.int64, device=mask.device)
+    return mask & ~own
+
+
+def reference(x, b, mask, window, sinks):
+    """Keys that the tokens of sequence b look at, [T, cached + T]: of the new ones those of the mask, of the cache the
+    positions from seq_len - (window - n) on and the sinks; n new tokens are seen, the token itself counted."""
+    T, L = x["q"].shape[1], x["ks"][b].shape[0]
+    seen = torch.zeros(T, L + T, dtype=torch.bool)
+    for t in range(T):
+        visible = {s for s in range(T) if (int(mask[b, t]) & (2**64 - 1)) >> s & 1}
+        n = len(visible | {t})
+        for j in range(L):
+            seen[t, j] = j >= L - (window - n) or j < sinks
+        for s in visible:
+            seen[t, L + s] = True
+    return seen.to(DEV)
+
+
+def check(x, mask, window, sinks):
+    ws = kda.attn_decode_workspace(x["q"], x["kp"], x["table"])
+    out, lse = kda.kda_attn_decode_window(x["q"], x["kp"], x["vp"], x["table"], x["lens"], SCALE, window, sinks, k_new=x["kn"],
+                                          v_new=x["vn"], tree_mask=mask, output_lse=True, workspace=ws)
+    assert kda.kda_workspace_status(ws) == kda.KDA_OK
+    G = x["q"].shape[2] // x["kn"].shape[2]
+    for b in range(x["q"].shape[0]):
+        seen = reference(x, b, mask, window, sinks)
+        k, v = torch.cat([x["ks"][b], x["kn"][b]]), torch.cat([x["vs"][b], x["vn"][b]])
+        for h in range(x["q"].shape[2]):
+            attn_ref.check(out[b, :, h], lse[b, :, h], attn_ref.attend(x["q"][b, :, h], k[:, h // G], v[:, h // G], seen, SCALE))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T,hq,hkv,window", [(2, 4, 2, 2), (6, 4, 2, 9), (24, 8, 2, 30), (64, 4, 2, 64), (64, 8, 1, 90)])
+def test_ancestors_without_the_token_itself(T, hq, hkv, window, dt):
+    x = make([0, 7, 100, 230], T, hq, hkv, 32, dt, seed=70)
+    mask = tree_masks(4, T, T)
+    mask[1] = torch.tensor([(2 << t) - 1 - (2**64 if t == 63 else 0) for t in range(T)], device=DEV)  # a chain: T - 1 ancestors
+    mask = without_own_bits(mask)
+    seen = torch.tensor([[bin(int(m) & (2**64 - 1)).count("1") for m in r] for r in mask.tolist()])
+    assert (seen[:, 0] == 0).all() and int(seen.max()) == T - 1
+    check(x, mask, window, 2)
