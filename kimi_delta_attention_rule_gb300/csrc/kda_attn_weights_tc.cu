@@ -81,6 +81,7 @@ struct Shared {
     Desc desc[kDescs];
     int4 least[kDescs];  // keys that all rows of each of the four warps see (0: some give nothing)
     uint64_t qfull[2], qempty[2];  // of a Q tile; PARTS = 4: of the first copy's rows, of the others
+    uint64_t landed[2];  // its tensor copies: a phase ends with them alone, whichever warp has given up
     uint64_t sfull[kGroups], sempty[kGroups];  // of a group's S, or of two groups'
     uint64_t kfull[kMaxRing], kempty[kMaxRing];
     uint64_t dfull[kDescs], rfull[kDescs], dempty[kDescs];
@@ -174,8 +175,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     auto bar = [](const uint64_t &x) { return smem_u32(&x); };
     if (warp == kWarpTma && lane == 0) {
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(bar(sh.qfull[i]), kRowWarps + (shape.box > 0));  // the rows' warps, and the copies
+            tc::mbar_init(bar(sh.qfull[i]), kRowWarps);
             tc::mbar_init(bar(sh.qempty[i]), 1);
+            tc::mbar_init(bar(sh.landed[i]), 1);
         }
         for (int i = 0; i < kMaxRing; ++i) {
             tc::mbar_init(bar(sh.kfull[i]), 1);
@@ -327,6 +329,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const __nv_bfloat16 *const q = static_cast<const __nv_bfloat16 *>(a.q);
         const uint32_t inv_g = (65536u + a.G - 1) / a.G;  // r / G = r inv_g >> 16 for r < 1024
         const int Hq = a.Hkv * a.G;
+        uint32_t sent[2] = {0, 0};  // copies into each Q tile, or of each half
         while (true) {
             const uint32_t slot = nd % kDescs, tile = nd % kQTiles;
             if (wr == 0) {
@@ -372,11 +375,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (nd >= kQTiles) alive = long_wait(bar(sh.qempty[half]), (nd / kQTiles - 1) & 1);
                 if (!alive || !copies || wr != 0) continue;
                 // (tokens past the part's own come along, whose columns nobody looks at)
-                const uint32_t lead = tc::elect_one(), full = bar(sh.qfull[half]), bytes = (uint32_t)(shape.box * a.G) * 128u;
+                const uint32_t lead = tc::elect_one(), full = bar(sh.landed[half]), bytes = (uint32_t)(shape.box * a.G) * 128u;
                 const int token = b * a.T + a.t0 + (int)i * shape.box;
                 attn::expect_tx(lead, full, 2 * bytes);
                 attn::tma_3d(lead, dst + i * bytes, &q_map, 0, head, token, full);
                 attn::tma_3d(lead, dst + (uint32_t)shape.nq * 128 + i * bytes, &q_map, 64, head, token, full);
+                sent[0] += half == 0;
+                sent[1] += half == 1;
                 __syncwarp();
             }
             if (!alive) break;
@@ -431,10 +436,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             ++nd;
         }
-        // (as the ring's copies below)
-        if (wr == 0 && shape.box > 0)
-            for (uint32_t i = 0; i < 2; ++i)
-                alive = wait_warp<kLimit>(bar(sh.qfull[i]), (PARTS == 4 ? nd - 1 : (nd + 1 - i) / 2 - 1) & 1) && alive;
+        // (as the ring's copies below; none: the parity of the phase before the first)
+        if (wr == 0)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) alive = wait_warp<kLimit>(bar(sh.landed[i]), (sent[i] - 1) & 1) && alive;
     } else if (warp == kWarpTma) {
         // ---- K tiles -------------------------------------------------------------------------
         // A copy is at most a page's rows of a tile; a lane each looks up the pages of the next 32
@@ -488,11 +493,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         while (const Desc *d = next_desc()) {
             const int n = d->tb - d->ta;
             const uint32_t tile = nd % kQTiles;
-            if (!(alive = warp_wait(bar(sh.qfull[tile]), (nd / kQTiles) & 1))) break;
+            auto rows_there = [&](uint32_t half) -> bool {
+                const uint32_t parity = (nd / kQTiles) & 1;
+                return warp_wait(bar(sh.qfull[half]), parity) && (shape.box == 0 || warp_wait(bar(sh.landed[half]), parity));
+            };
+            if (!(alive = rows_there(tile))) break;
             // PARTS = 4: the first products may need the second copy's rows too
             bool all = PARTS < 4;
             auto need_all = [&]() {
-                if (alive && !all) alive = warp_wait(bar(sh.qfull[1]), nd & 1);
+                if (alive && !all) alive = rows_there(1);
                 all = true;
             };
             if (PARTS == 4 && shape.box * a.G < 2 * shape.ns) need_all();
