@@ -1109,11 +1109,16 @@ namespace {
 // no second pass, 4). Direct and split, us: one token, 64 items of 9 tiles 14.7, 16.7, of 17
 // 21.5, 20.0; 64 drafts, 64 items of 17 tiles 31.2, 35.3, of 33 52.0, 44.5; prompts, 128
 // items of 18 tiles 32.9, 38.4, of 34 53.3, 50.5.
+// The host knows how long an item may be, not whether they are. One sequence of 65,000 tokens and many of 100
+// leave most SMs idle for as long as its items take, so items of more than kLongest tiles are always shared: up to there
+// even batches gain as much as uneven ones lose. Direct and split, us, even and uneven: 152 items of one token, 17 tiles 31.2,
+// 34.1 and 20.6, 17.2, of 33 53.3, 56.6 and 33.9, 18.1, of 510 222, 225 and 426, 51.4; 128 items of 24 tiles 36.5, 43.3
+// and 27.2, 18.1; 64 drafts, 144 items of 17 tiles 25.2, 38.1 and 24.6, 19.6, of 24 33.1, 43.1 and 32.3, 19.8.
 template <bool PAGED, bool DUAL>
 bool window_direct(const Args &a, long long slots, long long keys) {
-    constexpr int kTiles = PAGED ? (DUAL ? 7 : 11) : 4;
+    constexpr int kTiles = PAGED ? (DUAL ? 7 : 11) : 4, kLongest = 20;
     const long long own = (long long)a.window + a.sinks + (PAGED ? kTile : a.block), longest = keys < own ? keys : own;
-    return slots <= a.sms && longest * (a.sms - slots) <= (long long)kTiles * kTile * a.sms;
+    return slots <= a.sms && longest <= kLongest * kTile && longest * (a.sms - slots) <= (long long)kTiles * kTile * a.sms;
 }
 template <bool PAGED, bool DUAL, int RT, bool WIN, bool TEST>
 cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
