@@ -2,7 +2,7 @@
 and gives back the pages behind it, and one that keeps the tokens which get the most attention.
 
   windowed   kda_attn_prefill_window, then kda_attn_decode_window token by token; a page that has left
-             the window is dropped from the block table
+             the window is given back (KDA_PAGE_GONE in the block table keeps its place)
   evicting   kda_attn_prefill, its weights from the prompt's last tokens (kda_attn_weights), the cut to a
              budget (kda_cache_evict, kda_cache_trim); then per token kda_attn_decode,
              kda_cache_append, kda_attn_weights, and a cut whenever a sequence has grown past it
@@ -40,6 +40,16 @@ class Cache:
         kda.kda_cache_append(k, v, self.k, self.v, self.table, self.lens, workspace=self.ws)
         self.lens += 1
 
+    def give_back(self, out):
+        """Pages out (bool, as the table) leave their rows; those behind them keep their places."""
+        out = out & (self.table >= 0)
+        self.refs.index_add_(0, self.table.clamp(min=0).flatten().long(), -out.flatten().int())
+        self.table.masked_fill_(out, kda.KDA_PAGE_GONE)
+
+    def free(self):
+        kda.kda_cache_free(self.table, self.lens, self.refs, torch.arange(len(self.lens), dtype=torch.int32, device=self.lens.device),
+                           workspace=self.ws)
+
     def check(self):
         status = kda.kda_workspace_status(self.ws)
         assert status == kda.KDA_OK, kda.status_string(status)
@@ -51,16 +61,12 @@ def windowed(prompt, steps, window=64, sinks=4):
     kda.kda_attn_prefill_window(q, k, v, SCALE, window, sinks, cu_seqlens=cu)
     c = Cache(k, v, lens, cu, (max(lens) + len(steps)) // PAGE + 1)
     cols, kept_sinks = torch.arange(c.table.shape[1], device=k.device), (sinks + PAGE - 1) // PAGE
-    gone = torch.zeros_like(c.table, dtype=torch.bool)
     outs = []
     for q, k, v in steps:
         outs.append(kda.kda_attn_decode_window(q, c.k, c.v, c.table, c.lens, SCALE, window, sinks, k_new=k, v_new=v)[0][:, 0])
         c.append(k, v)
-        # the next token's window starts at lens + 1 - window: pages that end before it go back (their
-        # entries stay, which nobody looks at any more, so that later pages keep their places)
-        out = (cols >= kept_sinks) & ((cols + 1) * PAGE <= (c.lens + 1 - window)[:, None]) & (c.table >= 0)
-        c.refs[c.table[out & ~gone].long()] -= 1
-        gone |= out
+        # the next token's window starts at lens + 1 - window: pages that end before it go back
+        c.give_back((cols >= kept_sinks) & ((cols + 1) * PAGE <= (c.lens + 1 - window)[:, None]))
     c.check()
     return torch.stack(outs), c
 

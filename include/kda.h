@@ -518,6 +518,12 @@ int kda_attn_decode_window(const void *q, int64_t ldq, const void *k_new, const 
  * malformed rows, lengths or page numbers are skipped and flagged
  * (KDA_ERR_DEVICE); a call that needs more pages than are free changes nothing
  * and is flagged (KDA_ERR_NO_SPACE).
+ *   An entry KDA_PAGE_GONE stands for a page that its row has given back while those behind it keep their
+ * places (one behind a window, see kda_attn_decode_window): the caller takes one from its refs
+ * and writes the entry, both ahead of the next call that looks at the row. alloc takes it for a page in
+ * use, fork passes it on, free and trim drop it without a reference, compact leaves it. Calls that would read or
+ * write its tokens take it for a page number outside the pool (kda_cache_append, kda_cache_evict,
+ * kda_attn_decode, kda_attn_weights, a fork whose source ends inside it).
  *
  * kda_cache_alloc: gives every row the pages it lacks for want[row] tokens (DEVICE
  *   int32 [rows]; a row never loses pages). seq_lens is not touched.
@@ -551,6 +557,7 @@ int kda_attn_decode_window(const void *q, int64_t ldq, const void *k_new, const 
  *   Rows without a valid page are skipped and flagged (workspace may be NULL: then
  *   not flagged). Positions must be distinct.
  */
+#define KDA_PAGE_GONE (-2)
 size_t kda_cache_workspace_size(int32_t num_pages, int32_t rows);
 int kda_cache_alloc(int32_t *block_table, int64_t table_ld, int32_t rows, int32_t table_cols,
                     const int32_t *want, int32_t *refs, int32_t num_pages, int32_t page_size,

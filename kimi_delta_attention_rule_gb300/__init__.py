@@ -32,6 +32,7 @@ KDA_F32 = 1
 KDA_SCHEDULE_SPLIT = 0
 KDA_SCHEDULE_FUSED = 1
 KDA_SCHEDULE_DIRECT = 2
+KDA_PAGE_GONE = -2  # in a block table: a page given back, those behind it in their places
 
 EXPORTED = ("kda_status_string", "kda_abi_version", "kda_prefill_workspace_size", "kda_prefill",
             "kda_decode_step", "kda_workspace_status", "kda_check_cu_seqlens",

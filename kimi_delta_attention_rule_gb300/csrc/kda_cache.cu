@@ -173,9 +173,9 @@ __global__ void __launch_bounds__(256)
     int32_t *row = table.row(r);
     for (int j = blockIdx.y * blockDim.x + threadIdx.x; j < table.cols; j += gridDim.y * blockDim.x) {
         const int pg = row[j];
-        if (pg < 0) continue;
-        if (pg < pages) atomicSub(refs + pg, 1);
-        else if (status) atomicOr(status, kStatusBadSeqlens);
+        if (!in_use(pg)) continue;
+        if (pg >= 0 && pg < pages) atomicSub(refs + pg, 1);
+        else if (pg >= 0 && status) atomicOr(status, kStatusBadSeqlens);
         row[j] = -1;
     }
     if (blockIdx.y == 0 && threadIdx.x == 0) lens[r] = 0;
@@ -320,7 +320,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
                 if (ok) {
                     const int taken = table.row(z)[0];
                     len = lens[a];
-                    ok = len >= 0 && (long long)len <= (long long)table.cols * page && taken < 0;
+                    ok = len >= 0 && (long long)len <= (long long)table.cols * page && !in_use(taken);
                     state = len % page != 0;
                 }
                 if (ok && state == 1) {  // a page to copy from
@@ -375,7 +375,7 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
             auto share = [&](int j, int pg) {
                 to[j] = pg;
                 if (pg >= 0 && pg < pages) atomicAdd(refs + pg, 1);
-                else if (status) atomicOr(status, kStatusBadSeqlens);
+                else if (pg != kPageGone && status) atomicOr(status, kStatusBadSeqlens);
             };
             if (read) {
 #pragma unroll
@@ -398,13 +398,13 @@ __global__ void __cluster_dims__(kCtas, 1, 1) __launch_bounds__(kThreads)
 }
 
 // ---- alloc ------------------------------------------------------------------------
-// The entries in use of a row: the first -1, by a 32-way search of one warp.
+// The entries in use of a row: up to the first -1, by a 32-way search of one warp.
 __device__ __forceinline__ int row_used(const int32_t *row, int cols) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = cols;  // the answer lies in [lo, hi]
     while (hi > lo) {
         const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool used = at < hi && row[at] >= 0;
+        const bool used = at < hi && in_use(row[at]);
         const unsigned b = __ballot_sync(0xffffffffu, used);
         const int k = b == 0xffffffffu ? 32 : __ffs(~b) - 1;  // probes in use
         if (k == 0) return lo;

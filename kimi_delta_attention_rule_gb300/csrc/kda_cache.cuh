@@ -3,10 +3,16 @@
 
 #include <stdint.h>
 
+#include "kda.h"
+
 namespace kda {
 namespace cache {
 
 constexpr int kThreads = 1024;  // of a block of the calls that choose pages
+
+// An entry of a block table whose page the row has given back; the entries behind it keep their places.
+constexpr int kPageGone = KDA_PAGE_GONE;
+__device__ __forceinline__ bool in_use(int entry) { return entry >= 0 || entry == kPageGone; }
 
 struct Table {
     int32_t *entries;

@@ -443,9 +443,9 @@ __global__ void __launch_bounds__(256)
         const int first = (int)(((unsigned)n + page - 1) / (unsigned)page);
         for (int j = first + blockIdx.y * blockDim.x + threadIdx.x; j < table.cols; j += gridDim.y * blockDim.x) {
             const int pg = row[j];
-            if (pg < 0) continue;
-            if (pg < pages) atomicSub(refs + pg, 1);
-            else if (status) atomicOr(status, kStatusBadSeqlens);
+            if (!in_use(pg)) continue;
+            if (pg >= 0 && pg < pages) atomicSub(refs + pg, 1);
+            else if (pg >= 0 && status) atomicOr(status, kStatusBadSeqlens);
             row[j] = -1;
         }
         if (blockIdx.y == 0 && threadIdx.x == 0 && lens[r] > n) lens[r] = n;
