@@ -485,10 +485,14 @@ int kda_attn_decode(const void *q, int64_t ldq, const void *k_new, const void *v
  *   decode:  a token that sees n >= 1 of the new ones (itself counted, whether or not its mask has
  *            its own bit) looks at those and, of the cache, at the positions >= seq_lens[b] - (window - n) and
  *            < sinks. With k_new, window >= T (a window never ends among the drafts, else
- *            KDA_ERR_INVALID_ARG); without it n = 0. Pages of which no token of the call sees a key are not read, and
- *            their table entries may hold anything: they can have been given back.
- * Other keys between the two stretches are not used, but as in the plain calls a NaN or an infinity in v
- * reaches rows whose own keys share its key tile. All else (arguments, workspace, its size,
+ *            KDA_ERR_INVALID_ARG); without it n = 0. Pages without a sink that end at or before position
+ *            seq_lens[b] + 1 - window (without k_new: seq_lens[b] - window) are not read, whatever the mask: they
+ *            can have been given back (KDA_PAGE_GONE below; their entries may hold anything). All others of the
+ *            sequence must be there, also where a mask lets every token see so many new ones that none looks that far.
+ * Other keys between the two stretches are not used, but as in the plain calls a NaN or an infinity in v also
+ * reaches, in its channel, rows of its sequence that do not look at it: in decode from every page that is read, in
+ * prefill where one of the 256 / G tokens of a block (counted from a sequence's first one; fp32 64 / G)
+ * looks at it or at a key of its tile. All else (arguments, workspace, its size,
  * alignment, errors) is as in the plain calls; with a window past the longest sequence the
  * result is theirs, up to rounding. Work and reads grow with the window, not with the context.
  */

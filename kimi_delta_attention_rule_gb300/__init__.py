@@ -606,8 +606,9 @@ def kda_attn_decode_window(q, k_pages, v_pages, block_table, seq_lens, scale, wi
                            workspace=None, stream=None):
     """kda_attn_decode through a sliding window (C entry point
     ``kda_attn_decode_window``): a token that sees n of the new ones looks at those, at
-    the last window - n cached tokens and at the first `sinks`; window >= T. Pages that
-    no token looks at are not read. All else as kda_attn_decode (its workspace too)."""
+    the last window - n cached tokens and at the first `sinks`; window >= T. Pages without a
+    sink that end at or before seq_lens + 1 - window (without k_new: seq_lens - window) are not read
+    and can have been given back (KDA_PAGE_GONE). All else as kda_attn_decode (its workspace too)."""
     return (_bind or _native()).attn_decode_window(q, k_pages, v_pages, block_table, seq_lens, scale, k_new,
                                                    v_new, tree_mask, out, lse, output_lse, workspace,
                                                    stream, window, sinks)

@@ -1,9 +1,12 @@
 """kda_attn_decode_window under draft masks that are no plain chain or tree of their own bits: tokens whose
 masks lack their own bit, and drafts that all see one another."""
+import os
+
 import pytest
 import torch
 
 import kimi_delta_attention_rule_gb300 as kda
+from kimi_delta_attention_rule_gb300 import build as kbuild
 from tests import attn_ref
 from tests.test_attn_decode import BF, DEV, F32, SCALE, make, tree_masks
 
@@ -52,3 +55,29 @@ def test_ancestors_without_the_token_itself(T, hq, hkv, window, dt):
     seen = torch.tensor([[bin(int(m) & (2**64 - 1)).count("1") for m in r] for r in mask.tolist()])
     assert (seen[:, 0] == 0).all() and int(seen.max()) == T - 1
     check(x, mask, window, 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("T,hq,hkv,window", [(2, 4, 2, 40), (20, 8, 2, 20), (64, 4, 2, 300), (64, 8, 1, 64)])
+def test_drafts_that_all_see_one_another(T, hq, hkv, window, page, dt):
+    """Every window starts T before the end. Pages that end at or before the length + 1 - window can be gone; those
+    behind them, which no token looks at either, are there."""
+    x = make([0, 30, 200, 700, 1100], T, hq, hkv, page, dt, seed=71)
+    mask = torch.full((5, T), (1 << T) - 1 if T < 63 else -1, dtype=torch.int64, device=DEV)
+    sinks = 3
+    for b, n in enumerate(x["lens"].tolist()):
+        for j in range((n + page - 1) // page):
+            if j * page >= sinks and (j + 1) * page <= n + 1 - window:
+                p = int(x["table"][b, j])
+                x["kp"][p] = x["vp"][p] = float("nan")
+                x["table"][b, j] = (kda.KDA_PAGE_GONE, -1, 2**31 - 1)[j % 3]
+    check(x, mask, window, sinks)
+
+
+def test_the_contract_names_the_pages():
+    """A page may go by its place and the length alone, not by what a step's mask lets its tokens see."""
+    text = " ".join(open(os.path.join(kbuild.INCLUDE, "kda.h")).read().replace(" *", " ").split())
+    assert "Pages of which no token of the call sees a key" not in text
+    assert "Pages without a sink that end at or before position seq_lens[b] + 1 - window (without k_new: seq_lens[b] - window) are not read" in text
