@@ -598,9 +598,14 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv,
  *   The tokens are those of which the last count[b] (DEVICE int32 [B], NULL: T) cached ones are
  *   the keys, q and lse rows index[b][0 .. count[b] - 1] (DEVICE int32 [B, T], NULL: 0, 1, ..): the
  *   step's tokens once kda_cache_append has taken the accepted ones (the same index and
- *   count), or a prompt's last T.
- *   q : io dtype [B, T, Hq, D] as in kda_attn_decode, T <= 64   lse : fp32 [B, T, Hq], from the
- *       attention call of these rows; a row of lse = -inf gives nothing
+ *   count), or a prompt's last T. All queries of a prompt take a call for each 64 of them, with seq_lens
+ *   up to the last of these; each call reads the keys up to there again.
+ *   q : io dtype [B, T, Hq, D] as in kda_attn_decode, T <= 64   lse : fp32 [B, T, Hq]; a row of lse = -inf gives
+ *       nothing. The terms are the rows' probabilities if lse is over these very keys: from
+ *       kda_attn_prefill, or from kda_attn_decode where each of the tokens saw those of them up to itself (a chain, the
+ *       accepted path of a tree). The sum has no window: with the lse of kda_attn_prefill_window or
+ *       kda_attn_decode_window keys that a row does not look at get terms all the same, which may exceed 1,
+ *       and every page of the sequence must be there.
  *   weights : fp32 [B, Hkv, cap], cap >= every seq_lens[b]; past seq_lens[b] not touched
  *   k_pages, block_table, seq_lens, scale (at least 1e-30) and alignment as in kda_attn_decode. Logits, exponentials
  *   and sums are fp32. No two rows may share weights; pages may be shared. A malformed length or

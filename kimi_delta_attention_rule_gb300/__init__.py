@@ -667,7 +667,8 @@ def kda_attn_weights(q, k_pages, block_table, seq_lens, lse, scale, weights=None
     """Adds up the attention weight that cached tokens get from their sequence's last ones
     (C entry point ``kda_attn_weights``).
 
-    q: [B, T, Hq, D], T <= 64, and lse fp32 [B, T, Hq], of an attention call; k_pages: [P, Hkv,
+    q: [B, T, Hq, D], T <= 64, and lse fp32 [B, T, Hq], of kda_attn_prefill or kda_attn_decode (with the lse of
+    a windowed call the terms are no probabilities: this sum has no window); k_pages: [P, Hkv,
     page, D], in which the keys of these tokens are already the last ones; of sequence b's
     rows those of index[b, :count[b]] count (device int32; None: all, in order), as in
     kda_cache_append; weights: fp32 [B, Hkv, cap], added to (None: zeros, cap = cols * page).

@@ -4,8 +4,8 @@
 //   w[b, h, j] += sum_i sum_g exp(scale q_ig . k_j - lse_ig),   j <= L - count + i,
 //
 // over the accepted tokens i of sequence b (the last `count` of its L cached ones) and
-// the G query heads g of kv head h. With the lse of the attention call these are its
-// probabilities, so nothing is normalised here and every key is on its own.
+// the G query heads g of kv head h. With the lse of an attention call over these very keys (none
+// through a window) the terms are its probabilities, so nothing is normalised here and every key is on its own.
 //
 // Work. All sequences' (kv head, key tile) pairs form one line, of which CTA c takes
 // the part [U c / C, U (c + 1) / C): every CTA has as many tiles whatever the lengths
