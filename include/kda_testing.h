@@ -80,6 +80,28 @@ int kda_testing_attn_decode_timeout(const void *q, int64_t ldq, const void *k_ne
                                     float *lse, void *workspace, size_t workspace_bytes,
                                     int32_t warp, int32_t at, void *stream);
 
+/* kda_attn_prefill_window and kda_attn_decode_window likewise. */
+int kda_testing_attn_prefill_window_timeout(const void *q, const void *k, const void *v,
+                                            int64_t ldq, int64_t ldk, int64_t ldv, float scale,
+                                            int32_t window, int32_t sinks,
+                                            const int32_t *cu_seqlens_q,
+                                            const int32_t *cu_seqlens_k, int32_t N, int32_t Tq,
+                                            int32_t Tk, int32_t Hq, int32_t Hkv, int32_t D,
+                                            int32_t io, void *out, float *lse, void *workspace,
+                                            size_t workspace_bytes, int32_t warp, int32_t at,
+                                            void *stream);
+int kda_testing_attn_decode_window_timeout(const void *q, int64_t ldq, const void *k_new,
+                                           const void *v_new, int64_t ldk, int64_t ldv,
+                                           const void *k_pages, const void *v_pages,
+                                           int32_t num_pages, int32_t page_size,
+                                           const int32_t *block_table, int64_t table_ld,
+                                           int32_t table_cols, const int32_t *seq_lens,
+                                           const uint64_t *tree_mask, float scale, int32_t window,
+                                           int32_t sinks, int32_t B, int32_t T, int32_t Hq,
+                                           int32_t Hkv, int32_t D, int32_t io, void *out,
+                                           float *lse, void *workspace, size_t workspace_bytes,
+                                           int32_t warp, int32_t at, void *stream);
+
 /*
  * kda_attn_weights likewise (bf16 I/O only, arguments as there): warp 0..15 of the
  * exponentials, 16 products, 17 copies of keys, 18..21 rows, of which 18 walks the parts. The weights

@@ -166,6 +166,10 @@ def load() -> ctypes.CDLL:
         lib.kda_testing_attn_decode_timeout.argtypes = (lib.kda_attn_decode.argtypes[:-1] +
                                                         [I32, I32, P])
         lib.kda_testing_attn_decode_timeout.restype = ctypes.c_int
+        for name in ("kda_attn_prefill_window", "kda_attn_decode_window"):
+            f = getattr(lib, name.replace("kda_", "kda_testing_") + "_timeout")
+            f.argtypes = getattr(lib, name).argtypes[:-1] + [I32, I32, P]
+            f.restype = ctypes.c_int
         lib.kda_testing_attn_weights_timeout.argtypes = lib.kda_attn_weights.argtypes[:-1] + [I32, I32, P]
         lib.kda_testing_attn_weights_timeout.restype = ctypes.c_int
         lib.kda_testing_prefill_chain_timeout.argtypes = [P, P, P, P, P, F32, P, P, I32, I32, I32,

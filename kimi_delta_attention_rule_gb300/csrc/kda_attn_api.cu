@@ -291,6 +291,18 @@ int kda_testing_attn_prefill_timeout(const void *q, const void *k, const void *v
                         workspace_bytes, Window(), lose, stream);
 }
 
+int kda_testing_attn_prefill_window_timeout(const void *q, const void *k, const void *v, int64_t ldq, int64_t ldk, int64_t ldv,
+                                            float scale, int32_t window, int32_t sinks, const int32_t *cu_q,
+                                            const int32_t *cu_k, int32_t N, int32_t Tq, int32_t Tk, int32_t Hq, int32_t Hkv,
+                                            int32_t D, int32_t io, void *out, float *lse, void *workspace,
+                                            size_t workspace_bytes, int32_t warp, int32_t at, void *stream) {
+    const Window w = {window, sinks};
+    const Lose lose = {warp, at};
+    if (!w.ok() || !lose.ok(io)) return KDA_ERR_INVALID_ARG;
+    return prefill_impl(q, k, v, ldq, ldk, ldv, scale, cu_q, cu_k, N, Tq, Tk, Hq, Hkv, D, io, out, lse, workspace,
+                        workspace_bytes, w, lose, stream);
+}
+
 size_t kda_attn_decode_workspace_size(int32_t B, int32_t T, int32_t Hq, int32_t Hkv, int32_t D, int32_t page_size,
                                       int32_t table_cols, int32_t io) {
     if (B < 0 || T < 0 || T > kMaxTokens || table_cols < 0 || !page_ok(page_size) || check_heads(Hq, Hkv, D, io) != KDA_OK)
@@ -333,6 +345,21 @@ int kda_testing_attn_decode_timeout(const void *q, int64_t ldq, const void *k_ne
     return decode_impl(q, ldq, k_new, v_new, ldk, ldv, k_pages, v_pages, num_pages, page_size, block_table, table_ld,
                        table_cols, seq_lens, tree_mask, scale, B, T, Hq, Hkv, D, io, out, lse, workspace,
                        workspace_bytes, Window(), lose, stream);
+}
+
+int kda_testing_attn_decode_window_timeout(const void *q, int64_t ldq, const void *k_new, const void *v_new, int64_t ldk,
+                                           int64_t ldv, const void *k_pages, const void *v_pages, int32_t num_pages,
+                                           int32_t page_size, const int32_t *block_table, int64_t table_ld,
+                                           int32_t table_cols, const int32_t *seq_lens, const uint64_t *tree_mask,
+                                           float scale, int32_t window, int32_t sinks, int32_t B, int32_t T, int32_t Hq,
+                                           int32_t Hkv, int32_t D, int32_t io, void *out, float *lse, void *workspace,
+                                           size_t workspace_bytes, int32_t warp, int32_t at, void *stream) {
+    const Window w = {window, sinks};
+    const Lose lose = {warp, at};
+    if (!w.ok() || (k_new != nullptr && window < T) || !lose.ok(io)) return KDA_ERR_INVALID_ARG;
+    return decode_impl(q, ldq, k_new, v_new, ldk, ldv, k_pages, v_pages, num_pages, page_size, block_table, table_ld,
+                       table_cols, seq_lens, tree_mask, scale, B, T, Hq, Hkv, D, io, out, lse, workspace,
+                       workspace_bytes, w, lose, stream);
 }
 
 // Scratch of the calls that choose pages: the free pages' list and a state per

@@ -1158,7 +1158,9 @@ cudaError_t launch_form(Args &a, const Maps &maps, long long slots, long long ke
 }
 template <bool PAGED, bool DUAL, int RT>
 cudaError_t launch(Args &a, const Maps &maps, long long slots, long long keys, cudaStream_t stream) {
-    if (a.window > 0) return launch_form<PAGED, DUAL, RT, true, false>(a, maps, slots, keys, stream);
+    if (a.window > 0)
+        return a.lose > 0 ? launch_form<PAGED, DUAL, RT, true, true>(a, maps, slots, keys, stream)
+                          : launch_form<PAGED, DUAL, RT, true, false>(a, maps, slots, keys, stream);
     return a.lose > 0 ? launch_form<PAGED, DUAL, RT, false, true>(a, maps, slots, keys, stream)
                       : launch_form<PAGED, DUAL, RT, false, false>(a, maps, slots, keys, stream);
 }
