@@ -81,3 +81,30 @@ def test_the_contract_names_the_pages():
     text = " ".join(open(os.path.join(kbuild.INCLUDE, "kda.h")).read().replace(" *", " ").split())
     assert "Pages of which no token of the call sees a key" not in text
     assert "Pages without a sink that end at or before position seq_lens[b] + 1 - window (without k_new: seq_lens[b] - window) are not read" in text
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("B,T,hq,hkv,window", [(4, 64, 6, 2, 70), (3, 64, 5, 1, 64), (3, 40, 13, 1, 50), (2, 64, 64, 1, 100), (3, 9, 33, 1, 20),
+                                               (4, 43, 12, 2, 600), (2, 50, 27, 1, 3000)])
+def test_row_tiles_that_heads_do_not_divide(B, T, hq, hkv, window, dt):
+    """More than 128 rows per kv head, in row tiles of whole tokens: each with a CTA of its own, or shared."""
+    x = make([0, 37, 400, 1000][:B], T, hq, hkv, 16, dt, seed=72)
+    check(x, tree_masks(B, T, T + hq), window, 3)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("T", [3, 64])
+def test_several_tokens_over_the_cache_alone(T, dt):
+    """Without keys of their own all look at the last `window` cached ones, which may be fewer than the tokens."""
+    x = make([0, 1, 17, 300, 999], T, 8, 2, 32, dt, seed=73)
+    for window, sinks in ((2, 0), (40, 5), (500, 129)):
+        ws = kda.attn_decode_workspace(x["q"], x["kp"], x["table"])
+        out, lse = kda.kda_attn_decode_window(x["q"], x["kp"], x["vp"], x["table"], x["lens"], SCALE, window, sinks, output_lse=True, workspace=ws)
+        assert kda.kda_workspace_status(ws) == kda.KDA_OK
+        for b, n in enumerate(x["lens"].tolist()):
+            j = torch.arange(n, device=DEV)
+            seen = ((j >= n - window) | (j < sinks)).expand(T, n)
+            for h in range(8):
+                attn_ref.check(out[b, :, h], lse[b, :, h], attn_ref.attend(x["q"][b, :, h], x["ks"][b][:, h // 4], x["vs"][b][:, h // 4], seen, SCALE))
