@@ -407,7 +407,8 @@ int kda_noalloc_status(void *stream);
  * ever touch its own rows: whatever lies past a sequence's end (another
  * sequence, the rest of a page, NaN) is not used. Inside a sequence a NaN or an infinity
  * in v also reaches, in its channel, rows that do not see it but share its key tile (128 keys,
- * fp32 64; a call's drafts are a tile), as 0 * NaN and 0 * infinity do.
+ * fp32 64; a call's drafts are a tile) or have a row that does among the 128 / G tokens of their
+ * row tile (fp32 64 / G), as 0 * NaN and 0 * infinity do.
  * scale: finite and > 0. D = 128.
  *
  * Workspace: device buffer, 256-byte aligned, of the size that the query gives
@@ -611,7 +612,7 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv,
  *   and sums are fp32. No two rows may share weights; pages may be shared. A malformed length or
  *   count is flagged and its sequence skipped, a malformed index flagged and its row skipped, a
  *   page number outside the pool flagged and its keys read as zeros (workspace: 256-byte aligned, its
- *   first 256 bytes zero before its first use; NULL: not flagged).
+ *   first 256 bytes zero before its first use; NULL: not flagged). B, T, num_pages, table_cols or cap = 0 is a no-op.
  *
  * kda_cache_evict: of the seq_lens[b] tokens of row b, keep[b] (DEVICE int32 [rows]; < 0 skips the
  *   row) stay, or all if there are no more: per kv head the first `sinks`, the last `recent`
@@ -629,7 +630,9 @@ int kda_cache_append(const void *k, const void *v, int64_t ldk, int64_t ldv,
  *       that it writes to has not exactly one reference (in place, rows that shared pages
  *       with a fork would overwrite its tokens)
  *   seq_lens and the tables are not changed, for any number of layers to be cut alike:
- *   afterwards kda_cache_trim. Malformed lengths or page numbers are flagged, their rows skipped.
+ *   afterwards kda_cache_trim. Malformed lengths or page numbers are flagged, their rows skipped: such a row is as
+ *   it was, and kda_cache_trim would cut it to its first tokens, so where rows may be shared or malformed the
+ *   status is read before the trim. rows, num_pages, table_cols or cap = 0 is a no-op.
  *   rows * Hkv is at most 2^25, cap 2^31 - 2^13. workspace: kda_cache_evict_workspace_size bytes, as for the other calls.
  *
  * kda_cache_trim: each row keeps the pages of its first want[row] tokens (DEVICE int32 [rows]; < 0
