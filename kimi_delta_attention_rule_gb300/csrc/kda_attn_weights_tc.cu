@@ -23,7 +23,7 @@
 //
 // Measured (GB300; copy 6,790 GB/s): one token of 32 heads on 8 over 65,531 cached ones 26.8 us (5.1 TB/s with 5 us
 // of start), four drafts of 128 sequences on 400,003 134 us (6.3 TB/s): bound by HBM. 64 tokens of 8
-// prompts, 512 rows per kv head, 40,009 cached: 24 us, 1.62 us a tile and SM where its products alone take
+// prompts, 512 rows per kv head, 40,009 cached: 27.5 us, 24 with all inputs in L2, 1.62 us a tile and SM where its products alone take
 // 1.24 and its exponentials with one of nine products 1.49 (1.0 of the exponentials' pipe). Tried on those 512 rows: two groups of
 // warps that take 128 columns into registers at once 2.2 us, four that take their 64 at once 1.7, the next 16
 // columns while these are summed 1.83, products of 128 rows instead of 256 2.0 (their own

@@ -6,8 +6,8 @@
 // `heavy` by three passes over 11, 11 and 10 bits of the weights' ordered patterns, counted in one
 // histogram in shared memory, then goes once through the slots, four in a row to a thread, and writes
 // the staying ones by their rank, a prefix sum over the block. The first kCache patterns stay in shared
-// memory. The longest row bounds it, 22 us for 30,515 tokens of which 4,096 stay (3 to load, 8 for the passes, 9
-// for the last one): so 1,024 threads a block, patterns formed once and counted four at a time. (The last pass with
+// memory. The longest row bounds it, 24 us for 30,515 tokens of which 4,096 stay (3 to load, 10 to count and search, 9
+// to place, 2 for the zeros behind), 47 us for 65,531: so 1,024 threads a block, patterns formed once and counted four at a time. (The last pass with
 // a range of the slots per warp, twice, and one sum over the block: the same.)
 // The moves' launch comes when all blocks have chosen: blocks that wait for it on SMs with room made a
 // call 27 us longer.
