@@ -255,6 +255,19 @@ __device__ __forceinline__ void describe(const Args &a, const Part &p, int cta, 
     }
 }
 
+// The rows of an item that see no key: zeros, and -inf. A converged warp.
+__device__ __forceinline__ void write_nothing(const Args &a, const Part &p) {
+#pragma unroll 1
+    for (int t = 0; t < p.tokens; ++t) {
+        const size_t row = (size_t)(p.q0 + t) * a.Hq + p.h * a.G;
+#pragma unroll 1
+        for (int x = threadIdx.x & 31; x < a.G * 16; x += 32) {  // 16 pieces of a row
+            static_cast<uint4 *>(a.out)[row * 16 + x] = make_uint4(0, 0, 0, 0);
+            if (a.lse != nullptr && x < a.G) a.lse[row + x] = -INFINITY;
+        }
+    }
+}
+
 // Every wait has a limit. A role whose wait runs out goes to the kernel's end, the others
 // follow as theirs run out or they see kDead, and the status tells; the copies and products
 // in flight are waited for first. TEST (kda_testing_attn_*): waits of 20 ms, and warp
@@ -718,20 +731,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kWarpSched) {
             // ---- scheduler warp: walks the CTA's parts ahead of the others ------------
             Part p;
-            bool more = a.direct ? direct_part<PAGED, kTile, WIN>(a, cta, p) : any;
             Walk<PAGED, kTile, WIN> walk;
-            if (more && !a.direct) {
-                walk.init(p0, *reinterpret_cast<const Point *>(sm + L::kBars + Bars::kEnd), s0);
-                more = walk.next(a, p);
-            }
+            if (any && !a.direct) walk.init(p0, *reinterpret_cast<const Point *>(sm + L::kBars + Bars::kEnd), s0);
             Run run = {0, 0};
-            const bool tells = !DUAL && more && p.ta > 0 && p.tb == p.nt;  // the CTA before may take the first part
+            bool todo = a.direct ? direct_part<PAGED, kTile, WIN>(a, cta, p) : any;
+            bool tells = false;  // the CTA before may take the first part
             auto tell = [&]() {  // (its descriptor is back: all of it is written)
                 if (tells && lane == 0)
                     asm volatile("red.release.gpu.global.or.b32 [%0], %1;\n" ::"l"(early_flag(a, cta)), "r"(1u << (cta & 31))
                                  : "memory");
             };
             while (true) {
+                const bool more = todo && (a.direct || walk.next(a, p));
+                todo = more && !a.direct;
+                // Items that see nothing get their rows here. As descriptors they would stop all: a part's
+                // last P V runs with the next part's first Q K^T, which would lie behind more of them than
+                // there are descriptors, and these come back in order.
+                if (more && p.nt == 0) {
+                    write_nothing(a, p);
+                    continue;
+                }
+                if (nd == 0) tells = !DUAL && more && p.ta > 0 && p.tb == p.nt;
                 if (nd >= kDescs && !(alive = long_wait(bars.dempty(nd % kDescs), (nd / kDescs - 1) & 1))) break;
                 if (nd == kDescs) tell();
                 if (lane == 0) {
@@ -757,7 +777,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ++nd;
                 if (!more) break;
-                more = !a.direct && walk.next(a, p);
             }
             if (tells && alive && nd <= kDescs) {
                 alive = long_wait(bars.dempty(0), 0);
@@ -865,13 +884,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     more = d != nullptr;
                     if (!more) break;
                     const int n0 = d->count[0], n1 = d->count[1];
-                    left = DUAL ? n0 + n1 : (n0 > n1 ? n0 : n1);
-                    if (left == 0) {
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
-                        ++nd;
-                        continue;
-                    }
+                    left = DUAL ? n0 + n1 : (n0 > n1 ? n0 : n1);  // (one at least)
                     x.n = d->n;
                     x.h = d->h;
                     x.k0 = d->k0;
@@ -1019,7 +1032,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __syncwarp();
                         if (lane == 0) mbar_arrive(bars.dempty(nd % kDescs));
                         ++nd;
-                        if (c0 + c1 == 0) continue;
                     }
                     const int n = d == nullptr ? 1 : (c0 > c1 ? c0 : c1);
                     for (int j = 0; j < n && alive; ++j) {
